@@ -24,6 +24,8 @@
  *
  * Around the step: ssd_gate_retrieve (gate and retrieval in one launch),
  * ssd_commit_kv (append the accepted candidates' keys and values to the cache),
+ * the 8-bit cache (ssd_append_kv_quant, ssd_commit_kv_quant write it,
+ * ssd_verify_attn_quant attends over it) and its pages (ssd_page_tables),
  * ssd_copy_stats (copy attempts and speculation tax), ssd_lowrank_head (the
  * SlimSpec low-rank draft LM head), ssd_accept_static (ssd_accept without a
  * caller workspace) with ssd_read_static_error, and the diagnostics
@@ -79,7 +81,7 @@ enum {
   SSD_ERR_DEVICE = -6        /* a device-side check failed (device error word) */
 };
 
-/* element types */
+/* element types (codes of an 8-bit cache are always OCP e4m3, one byte each) */
 enum { SSD_F32 = 0, SSD_BF16 = 1 };
 /* what the vocabulary rows hold */
 enum { SSD_LOGITS_F32 = 0, SSD_LOGITS_BF16 = 1, SSD_PROBS_F32 = 2 };
@@ -381,6 +383,191 @@ typedef struct {
 } ssd_commit_args;
 
 int ssd_commit_kv(const ssd_commit_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ssd_page_tables — block tables and slot maps from request lengths.
+ *
+ * Speculative Decoding 해부 page, §6: the cache is a pool of pages that sequences take
+ * and give back as their lengths move. Pages hold 128 tokens. For each sequence b,
+ * want = ceil((cur_len[b] + add_len[b]) / 128) and the call makes its table hold
+ * exactly that many pages:
+ *   trim   pages block_table[b][want .. n_pages[b]-1] go back to the stack
+ *          free_pages[0 .. n_free-1], pushed in the order of b, then of the page's
+ *          place in the table; their table entries become -1;
+ *   grow   missing pages are then popped from the top of the stack in the same order
+ *          (trimmed pages among them). Sequence b is served when it lacks no page or
+ *          the pages that sequences 0 .. b lack together are at most those on the
+ *          stack; a sequence that is not served is left unchanged.
+ * So a step that adds tokens passes their number (prompt lengths, or the candidate
+ * slots of a verification), and one that gives back what was not kept passes
+ * add_len = 0 with the new lengths; a finished sequence has cur_len = add_len = 0.
+ *   row_start[b] = sum of add_len[0 .. b-1] (served or not), row_start[B] the total:
+ *          the first row of sequence b in a ragged list of the added tokens;
+ *   slot_map[row_start[b] + i] = 128 * (page of position cur_len[b] + i) + its place in
+ *          the page, -1 for the rows of a sequence that was not served and for every
+ *          entry from row_start[B] to slot_cap - 1.
+ * Arguments
+ *   cur_len, add_len [B] int32 (>= 0); n_pages [B], block_table [B][pages_per_seq],
+ *   free_pages [num_pages], n_free [1]: int32, updated in place; row_start [B+1],
+ *   slot_map [slot_cap] (NULL iff slot_cap == 0), served [B] (1 or 0; optional): int32
+ *   outputs. Every page belongs to one sequence or to the stack: pages shared by
+ *   sequences are not counted. Buffers must not overlap.
+ * Device-side errors (SSD_ERR_DEVICE in the workspace header): a negative length, a
+ * sequence that wants more than pages_per_seq pages or whose n_pages is outside
+ * [0, pages_per_seq] (it is not served and left unchanged; a negative add_len counts as
+ * 0 rows), n_free outside [0, num_pages] (read as the nearest bound), a page id outside
+ * [0, num_pages) (its slots are -1), a stack that would pass num_pages (the page is
+ * dropped), more than slot_cap rows (those beyond are not written), more than 2^31 - 1
+ * rows (row_start saturates).
+ * Limits: num_pages * 128 < 2^31, slot_cap < 2^31, else SSD_ERR_UNSUPPORTED. B == 0
+ * writes row_start[0] = 0 and the slots.
+ * Workspace: at least 256 bytes, 256-byte aligned (the status header).
+ */
+typedef struct {
+  const int32_t* cur_len;
+  const int32_t* add_len;
+  int32_t* n_pages;
+  int32_t* block_table;
+  int32_t* free_pages;
+  int32_t* n_free;
+  int32_t* row_start;
+  int32_t* slot_map;
+  int32_t* served;
+  int B, pages_per_seq;
+  int64_t num_pages, slot_cap;
+} ssd_pages_args;
+
+int ssd_page_tables(const ssd_pages_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ssd_append_kv_quant — quantise new keys and values into the 8-bit cache.
+ *
+ * The cache holds e4m3 codes k_cache, v_cache [num_pages][Hkv][page_tokens][dh] and one
+ * fp32 scale for each block of scale_block tokens and head, k_scale, v_scale
+ * [num_pages][Hkv][ceil(page_tokens / scale_block)]; a code c of a block with scale s
+ * stands for the value c * s. A paged cache has page_tokens = 128; a contiguous one
+ * [B][Hkv][P_max][dh] is num_pages = B pages of page_tokens = P_max tokens.
+ * Row t of k_new, v_new ([T] rows of [Hkv][dh], k_stride / v_stride elements apart) goes
+ * to slot slot_map[t] = page * page_tokens + place; rows with a negative slot are
+ * skipped. For each block and head that rows go to, with o the first place written:
+ *   a     = max |x| over the finite values of the rows written to the block
+ *   need  = the least power of two with a <= 448 * need, at least 2^-100
+ *   scale = need if o is the block's first place (what the block held is over), else
+ *           max(old scale, need); when it grows, the codes of the places before o
+ *           become round(code * old / new) (the later places keep their bytes)
+ *   code  = e4m3(x / scale), the quotient in fp32, round to nearest even; an infinity
+ *           becomes +-448, NaN the NaN code (also where the old code was NaN)
+ * The rows of one block have to be adjacent in the list with slots ascending by one, as
+ * ssd_page_tables lists them; a block named by two separate runs of the list, or a page
+ * held by two sequences, gets values of either run (nothing else is touched). Rows
+ * outside the pool (slot >= num_pages * page_tokens) are skipped and SSD_ERR_DEVICE is
+ * recorded.
+ * Arguments: dtype of the rows SSD_BF16 or SSD_F32; dh 64 or 128; scale_block 16, 32, 64
+ * or 128; row bases and strides multiples of 16 bytes, cache bases of 16 bytes
+ * (SSD_ERR_UNSUPPORTED otherwise); strides >= Hkv * dh; num_pages * page_tokens < 2^31.
+ * T == 0 launches nothing. The buffers must not overlap.
+ * Workspace: at least 256 bytes, 256-byte aligned (the status header).
+ */
+typedef struct {
+  const void* k_new;
+  const void* v_new;
+  const int32_t* slot_map;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int dtype;
+  int Hkv, dh, scale_block;
+  int64_t T, k_stride, v_stride;
+  int64_t num_pages, page_tokens;
+} ssd_append_quant_args;
+
+int ssd_append_kv_quant(const ssd_append_quant_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ssd_commit_kv_quant — ssd_commit_kv into the 8-bit cache.
+ *
+ * The a = n_out[b] - 1 accepted candidates of block best_blk[b] (as for ssd_commit_kv)
+ * are quantised, by the rules of ssd_append_kv_quant, into cache positions
+ * prefix_len[b] .. prefix_len[b] + a - 1, and new_len[b] = prefix_len[b] + a. The
+ * lengths are not updated in place: new_len must not overlap prefix_len, so the call
+ * may be repeated and the caller swaps the two.
+ *   k_cache, v_cache, k_scale, v_scale: with block_table NULL [B][Hkv][P_max][dh] and
+ *   [B][Hkv][ceil(P_max / scale_block)]; else pages of 128 tokens as above, and position
+ *   p of sequence b lies in page block_table[b][p / 128] (block_table
+ *   [B][pages_per_seq]; P_max is then unused).
+ *   k_cand, v_cand [B][NB*Dmax][Hkv][dh] of dtype (SSD_BF16 or SSD_F32).
+ * A sequence without room (prefix_len + a > P_max or 128 * pages_per_seq), with a page
+ * outside the pool, or with best_blk / n_out / prefix_len that do not fit the shape is
+ * left unchanged (new_len = prefix_len) and SSD_ERR_DEVICE is recorded. Two sequences
+ * must not hold the page that one of them writes.
+ * Limits and workspace: as for ssd_append_kv_quant; Dmax <= 256.
+ */
+typedef struct {
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  const void* k_cand;
+  const void* v_cand;
+  const int32_t* prefix_len;
+  const int32_t* best_blk;
+  const int32_t* n_out;
+  int32_t* new_len;
+  const int32_t* block_table;
+  int dtype;
+  int B, NB, Dmax, Hkv, dh, scale_block, pages_per_seq;
+  int64_t P_max, num_pages;
+} ssd_commit_quant_args;
+
+int ssd_commit_kv_quant(const ssd_commit_quant_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ssd_verify_attn_quant — ssd_verify_attn over the 8-bit cache.
+ *
+ * For each present token (slot t of block k, as for ssd_verify_attn) and q-head:
+ *   out = sum_j softmax_j(scale * q.k_j) v_j over the prefix keys, whose values are
+ *         code * (scale of their block), and the slots k*Dmax .. t of its own block
+ * One block of one token (NB = Dmax = 1) is the decoding of a single token, whose own
+ * key and value are the candidate's. Rows of absent tokens are not written.
+ * Layouts: q [B][NT][Hq][dh], k_cand, v_cand [B][NT][Hkv][dh] bf16; out the same in
+ * bf16 or fp32 (out_dtype); k_cache, v_cache, k_scale, v_scale: as for
+ * ssd_commit_kv_quant, contiguous or (block_table != NULL) pages of 128 tokens, which
+ * sequences may share. prefix_len [B], blk_len [B][NB] int32.
+ * Scales are finite and in [0, 2^20]; a v_scale below 2^-100 counts as 2^-100. Codes and
+ * scales past prefix_len are never used (they may hold anything); blocks need no scale
+ * before their first token.
+ * Scores, maxima and sums are fp32, products exact in fp32; the probabilities are rounded
+ * to 11 bits (fp16) or to a sum of two e4m3 numbers (about 8 bits) before they weight the
+ * values, the candidates' to bf16 or better.
+ * Supported: dh 64 or 128; Hq % Hkv == 0, Hq / Hkv <= 64; 1 <= Dmax <= 256,
+ * NB * Dmax <= 8192; scale_block 16, 32, 64 or 128; 16-byte aligned tensors;
+ * num_pages * 128 * Hkv < 2^31 (B * Hkv * P_max < 2^31); else SSD_ERR_UNSUPPORTED.
+ * scale == 0 selects 1/sqrt(dh). A prefix_len outside the cache or a page outside the
+ * pool records SSD_ERR_DEVICE (the prefix counts as empty, the page as page 0).
+ * Workspace: ssd_verify_attn_quant_workspace_size(a) bytes (256: the status header),
+ * 256-byte aligned.
+ */
+typedef struct {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const void* k_cand;
+  const void* v_cand;
+  void* out;
+  const int32_t* prefix_len;
+  const int32_t* blk_len;
+  const int32_t* block_table;
+  int out_dtype;
+  int B, NB, Dmax, Hq, Hkv, dh, scale_block, pages_per_seq;
+  float scale;
+  int64_t P_max, num_pages;
+} ssd_attn_quant_args;
+
+size_t ssd_verify_attn_quant_workspace_size(const ssd_attn_quant_args* a);
+int ssd_verify_attn_quant(const ssd_attn_quant_args* a, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * ssd_copy_stats — count copy attempts and the speculation tax over a batch.

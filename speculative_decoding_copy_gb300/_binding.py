@@ -29,7 +29,9 @@ EXPORTED = ["ssd_status_string", "ssd_version", "ssd_launch_count", "ssd_gate_ma
             "ssd_read_device_error", "ssd_profile_kernel", "ssd_accept_static", "ssd_gate_retrieve",
             "ssd_selftest_wait", "ssd_commit_kv",
             "ssd_copy_stats", "ssd_lowrank_head_workspace_size", "ssd_lowrank_head", "ssd_read_static_error",
-            "ssd_read_probe", "ssd_checked_build", "ssd_read_check_error"]
+            "ssd_read_probe", "ssd_checked_build", "ssd_read_check_error",
+            "ssd_page_tables", "ssd_append_kv_quant", "ssd_commit_kv_quant",
+            "ssd_verify_attn_quant_workspace_size", "ssd_verify_attn_quant"]
 SSD_KERNEL = dict(vocab_stats=1, verify_attn=2, attn_combine=3, accept_finish=4, gate_match=6,
                   retrieve=7, head_down=8, head_up=9, head_combine=10)
 
@@ -67,6 +69,37 @@ class AcceptArgs(ctypes.Structure):
                 ("K", c_int), ("chain_blk", c_int), ("u_acc", c_void_p), ("u_fin", c_void_p),
                 ("acc_len", c_void_p), ("best_blk", c_void_p), ("n_out", c_void_p), ("out_tok", c_void_p),
                 ("probs_out", c_void_p), ("early_rows", c_int), ("max_ctas", c_int)]
+
+
+class PagesArgs(ctypes.Structure):
+    _fields_ = [("cur_len", c_void_p), ("add_len", c_void_p), ("n_pages", c_void_p), ("block_table", c_void_p),
+                ("free_pages", c_void_p), ("n_free", c_void_p), ("row_start", c_void_p), ("slot_map", c_void_p),
+                ("served", c_void_p), ("B", c_int), ("pages_per_seq", c_int), ("num_pages", c_int64),
+                ("slot_cap", c_int64)]
+
+
+class AppendQuantArgs(ctypes.Structure):
+    _fields_ = [("k_new", c_void_p), ("v_new", c_void_p), ("slot_map", c_void_p), ("k_cache", c_void_p),
+                ("v_cache", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p), ("dtype", c_int),
+                ("Hkv", c_int), ("dh", c_int), ("scale_block", c_int), ("T", c_int64), ("k_stride", c_int64),
+                ("v_stride", c_int64), ("num_pages", c_int64), ("page_tokens", c_int64)]
+
+
+class CommitQuantArgs(ctypes.Structure):
+    _fields_ = [("k_cache", c_void_p), ("v_cache", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("k_cand", c_void_p), ("v_cand", c_void_p), ("prefix_len", c_void_p), ("best_blk", c_void_p),
+                ("n_out", c_void_p), ("new_len", c_void_p), ("block_table", c_void_p), ("dtype", c_int),
+                ("B", c_int), ("NB", c_int), ("Dmax", c_int), ("Hkv", c_int), ("dh", c_int), ("scale_block", c_int),
+                ("pages_per_seq", c_int), ("P_max", c_int64), ("num_pages", c_int64)]
+
+
+class AttnQuantArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k_cache", c_void_p), ("v_cache", c_void_p), ("k_scale", c_void_p),
+                ("v_scale", c_void_p), ("k_cand", c_void_p), ("v_cand", c_void_p), ("out", c_void_p),
+                ("prefix_len", c_void_p), ("blk_len", c_void_p), ("block_table", c_void_p), ("out_dtype", c_int),
+                ("B", c_int), ("NB", c_int), ("Dmax", c_int), ("Hq", c_int), ("Hkv", c_int), ("dh", c_int),
+                ("scale_block", c_int), ("pages_per_seq", c_int), ("scale", c_float), ("P_max", c_int64),
+                ("num_pages", c_int64)]
 
 
 _lib = None
@@ -148,6 +181,16 @@ def load(path) -> ctypes.CDLL:
         L.ssd_read_static_error.argtypes = [c_void_p, POINTER(c_int32)]
         L.ssd_profile_kernel.restype = c_int
         L.ssd_profile_kernel.argtypes = [c_int, c_void_p, c_void_p]
+        L.ssd_page_tables.restype = c_int
+        L.ssd_page_tables.argtypes = [POINTER(PagesArgs), c_void_p, c_size_t, c_void_p]
+        L.ssd_append_kv_quant.restype = c_int
+        L.ssd_append_kv_quant.argtypes = [POINTER(AppendQuantArgs), c_void_p, c_size_t, c_void_p]
+        L.ssd_commit_kv_quant.restype = c_int
+        L.ssd_commit_kv_quant.argtypes = [POINTER(CommitQuantArgs), c_void_p, c_size_t, c_void_p]
+        L.ssd_verify_attn_quant_workspace_size.restype = c_size_t
+        L.ssd_verify_attn_quant_workspace_size.argtypes = [POINTER(AttnQuantArgs)]
+        L.ssd_verify_attn_quant.restype = c_int
+        L.ssd_verify_attn_quant.argtypes = [POINTER(AttnQuantArgs), c_void_p, c_size_t, c_void_p]
         L.ssd_checked_build.restype = c_int
         L.ssd_read_check_error.restype = c_int
         L.ssd_read_check_error.argtypes = [c_void_p, POINTER(c_int32)]
@@ -380,6 +423,224 @@ def ssd_commit_kv(k_cache, v_cache, k_cand, v_cand, prefix_len, best_blk, n_out,
         ws = torch.zeros(256, dtype=torch.uint8, device=k_cache.device)
     _check("ssd_commit_kv", lib().ssd_commit_kv(ctypes.byref(args), _ptr(ws), ws.numel(), _stream(stream)))
     return ws
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit cache
+QUANT_PAGE = 128
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _need_shape(t, name, dtypes, shape, device):
+    """_need, with the exact shape and device (None: any size)."""
+    _need(t, name, dtypes, len(shape))
+    if any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _need_apart(**tensors):
+    """Raise where two of the named tensors share memory."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), n) for n, t in tensors.items()
+                   if t is not None and t.numel())
+    for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError(f"{a} and {b} overlap")
+
+
+def _quant_cache(k_cache, v_cache, k_scale, v_scale, scale_block, device, pages=None, tokens=None):
+    """Check a cache of codes [pages][Hkv][tokens][dh] and its scales; returns its four sizes."""
+    if scale_block not in (16, 32, 64, 128):
+        raise ValueError("scale_block must be 16, 32, 64 or 128")
+    _need_shape(k_cache, "k_cache", _CODES, (pages, None, tokens, None), device)
+    _need_shape(v_cache, "v_cache", _CODES, tuple(k_cache.shape), device)
+    n, Hkv, P, dh = k_cache.shape
+    shape = (n, Hkv, -(-P // scale_block))
+    _need_shape(k_scale, "k_scale", (torch.float32,), shape, device)
+    _need_shape(v_scale, "v_scale", (torch.float32,), shape, device)
+    return n, Hkv, P, dh
+
+
+def _new_on(stream, make):
+    """make() with `stream` current, so that a fresh tensor's memory belongs to the stream it is used on."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _quant_ws(ws, device, stream):
+    """The caller's workspace, or a fresh one whose header is clear."""
+    if ws is None:
+        return _new_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=device))
+    _need(ws, "ws", (torch.uint8,), 1)
+    if ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, not on {device}")
+    return ws
+
+
+def _on_device(device, stream):
+    """Handle of the stream a call on `device`'s tensors runs on: its current one where none is given."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return ctypes.c_void_p((stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
+
+
+def ssd_page_tables(cur_len, add_len, n_pages, block_table, free_pages, n_free, slot_cap, *, out=None, ws=None,
+                    stream=None):
+    """Block tables that hold exactly ceil((cur_len + add_len) / 128) pages a sequence (grown from
+    or trimmed to the stack of free pages, all updated in place) and the slots of the added
+    tokens; returns dict(row_start [B+1], slot_map [slot_cap], served [B])."""
+    _need(cur_len, "cur_len", (torch.int32,), 1)
+    dev, B, i32 = cur_len.device, cur_len.shape[0], (torch.int32,)
+    _need_shape(add_len, "add_len", i32, (B,), dev)
+    _need_shape(n_pages, "n_pages", i32, (B,), dev)
+    _need_shape(block_table, "block_table", i32, (B, None), dev)
+    _need_shape(free_pages, "free_pages", i32, (None,), dev)
+    _need_shape(n_free, "n_free", i32, (1,), dev)
+    cap = int(slot_cap)
+    if cap < 0:
+        raise ValueError("slot_cap must not be negative")
+    o = dict(out or {})
+    for k, n in (("row_start", B + 1), ("slot_map", cap), ("served", B)):
+        if o.get(k) is None:
+            o[k] = _new_on(stream, lambda: torch.empty(n, dtype=torch.int32, device=dev))
+        else:
+            _need_shape(o[k], k, i32, (n,), dev)
+    _need_apart(cur_len=cur_len, n_pages=n_pages, block_table=block_table, free_pages=free_pages, n_free=n_free, **o)
+    _need_apart(add_len=add_len, n_pages=n_pages, block_table=block_table, free_pages=free_pages, n_free=n_free, **o)
+    ws = _quant_ws(ws, dev, stream)
+    args = PagesArgs(_ptr(cur_len), _ptr(add_len), _ptr(n_pages), _ptr(block_table), _ptr(free_pages), _ptr(n_free),
+                     _ptr(o["row_start"]), _ptr(o["slot_map"]) if cap else None, _ptr(o["served"]), B,
+                     block_table.shape[1], free_pages.shape[0], cap)
+    with torch.cuda.device(dev):
+        _check("ssd_page_tables", lib().ssd_page_tables(ctypes.byref(args), _ptr(ws), ws.numel(), _on_device(dev, stream)))
+    return o
+
+
+def _rows(t, name, Hkv, dh, dtypes, device):
+    """Check new rows [T][Hkv][dh], dense but for the stride between rows; returns that stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.dim() != 3 or tuple(t.shape[1:]) != (Hkv, dh):
+        raise ValueError(f"{name} must be [T][{Hkv}][{dh}], got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.numel() and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != dh)):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    return t.stride(0) if t.shape[0] > 1 else Hkv * dh
+
+
+def ssd_append_kv_quant(k_new, v_new, slot_map, k_cache, v_cache, k_scale, v_scale, scale_block=128, *, ws=None,
+                        stream=None):
+    """Quantise the rows k_new, v_new [T][Hkv][dh] (bf16 or fp32, any row stride) into the 8-bit
+    cache at slot_map [T] (page * tokens of a page + place; negative: skipped), in place. A
+    contiguous cache [B][Hkv][P_max][dh] is B pages of P_max tokens. Returns the workspace."""
+    _need(slot_map, "slot_map", (torch.int32,), 1)
+    dev, T = slot_map.device, slot_map.shape[0]
+    pages, Hkv, tokens, dh = _quant_cache(k_cache, v_cache, k_scale, v_scale, int(scale_block), dev)
+    types = (torch.float32,) + _HALF
+    ks = _rows(k_new, "k_new", Hkv, dh, types, dev)
+    vs = _rows(v_new, "v_new", Hkv, dh, (k_new.dtype,), dev)
+    if k_new.shape[0] != T or v_new.shape[0] != T:
+        raise ValueError(f"k_new and v_new must hold the {T} rows of slot_map")
+    _need_apart(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, slot_map=slot_map)
+    ws = _quant_ws(ws, dev, stream)
+    args = AppendQuantArgs(_ptr(k_new), _ptr(v_new), _ptr(slot_map), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                           _ptr(v_scale), _elem_type(k_new), Hkv, dh, int(scale_block), T, ks, vs, pages, tokens)
+    with torch.cuda.device(dev):
+        _check("ssd_append_kv_quant", lib().ssd_append_kv_quant(ctypes.byref(args), _ptr(ws), ws.numel(),
+                                                                _on_device(dev, stream)))
+    return ws
+
+
+def ssd_commit_kv_quant(k_cache, v_cache, k_scale, v_scale, k_cand, v_cand, prefix_len, best_blk, n_out, Dmax,
+                        scale_block=128, *, new_len=None, block_table=None, ws=None, stream=None):
+    """Quantise the accepted tokens' K/V rows (ssd_accept's best_blk, n_out) into the 8-bit cache
+    at the end of each sequence's prefix; returns (new_len, workspace)."""
+    _need(prefix_len, "prefix_len", (torch.int32,), 1)
+    dev, B = prefix_len.device, prefix_len.shape[0]
+    paged = block_table is not None
+    pages, Hkv, P, dh = _quant_cache(k_cache, v_cache, k_scale, v_scale, int(scale_block), dev, None if paged else B,
+                                     QUANT_PAGE if paged else None)
+    _need_shape(k_cand, "k_cand", (torch.float32,) + _HALF, (B, None, Hkv, dh), dev)
+    _need_shape(v_cand, "v_cand", (k_cand.dtype,), tuple(k_cand.shape), dev)
+    _need_shape(best_blk, "best_blk", (torch.int32,), (B,), dev)
+    _need_shape(n_out, "n_out", (torch.int32,), (B,), dev)
+    NT = k_cand.shape[1]
+    if int(Dmax) < 1 or NT % int(Dmax):
+        raise ValueError(f"{NT} candidate slots are no whole blocks of {Dmax}")
+    if paged:
+        _need_shape(block_table, "block_table", (torch.int32,), (B, None), dev)
+    if new_len is None:
+        new_len = _new_on(stream, lambda: torch.empty_like(prefix_len))
+    else:
+        _need_shape(new_len, "new_len", (torch.int32,), (B,), dev)
+    _need_apart(new_len=new_len, prefix_len=prefix_len, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale,
+                v_scale=v_scale)
+    ws = _quant_ws(ws, dev, stream)
+    args = CommitQuantArgs(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(k_cand), _ptr(v_cand),
+                           _ptr(prefix_len), _ptr(best_blk), _ptr(n_out), _ptr(new_len), _ptr(block_table),
+                           _elem_type(k_cand), B, NT // int(Dmax), int(Dmax), Hkv, dh, int(scale_block),
+                           block_table.shape[1] if paged else 0, P, pages)
+    with torch.cuda.device(dev):
+        _check("ssd_commit_kv_quant", lib().ssd_commit_kv_quant(ctypes.byref(args), _ptr(ws), ws.numel(),
+                                                                _on_device(dev, stream)))
+    return new_len, ws
+
+
+def attn_quant_args(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand, prefix_len, blk_len, Dmax, scale_block,
+                    out, scale=0.0, block_table=None) -> AttnQuantArgs:
+    """Marshal the 8-bit attention's arguments (layouts as ssd_verify_attn_quant)."""
+    B, _, Hq, dh = q.shape
+    pages, Hkv, P, _ = k_cache.shape
+    return AttnQuantArgs(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(k_cand),
+                         _ptr(v_cand), _ptr(out), _ptr(prefix_len), _ptr(blk_len), _ptr(block_table),
+                         _elem_type(out), B, blk_len.shape[1], int(Dmax), Hq, Hkv, dh, int(scale_block),
+                         block_table.shape[1] if block_table is not None else 0, float(scale), P, pages)
+
+
+def ssd_verify_attn_quant_workspace_size(args: AttnQuantArgs) -> int:
+    return int(lib().ssd_verify_attn_quant_workspace_size(ctypes.byref(args)))
+
+
+def ssd_verify_attn_quant(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand, prefix_len, blk_len, Dmax,
+                          scale_block=128, *, out=None, ws=None, scale=0.0, stream=None, out_f32=False,
+                          block_table=None):
+    """Block-triangular verification attention over the 8-bit cache (one block of one token:
+    decoding); returns the output [B][NT][Hq][dh], bf16 or with out_f32 fp32. The cache is
+    contiguous [B][Hkv][P_max][dh], or with block_table [B][pages_per_seq] pages of 128 tokens."""
+    _need(q, "q", _HALF, 4)
+    dev = q.device
+    B, NT, Hq, dh = q.shape
+    paged = block_table is not None
+    _, Hkv, _, _ = _quant_cache(k_cache, v_cache, k_scale, v_scale, int(scale_block), dev, None if paged else B,
+                                QUANT_PAGE if paged else None)
+    if k_cache.shape[3] != dh:
+        raise ValueError(f"k_cache holds rows of {k_cache.shape[3]} elements, q of {dh}")
+    _need_shape(k_cand, "k_cand", _HALF, (B, NT, Hkv, dh), dev)
+    _need_shape(v_cand, "v_cand", _HALF, (B, NT, Hkv, dh), dev)
+    _need_shape(prefix_len, "prefix_len", (torch.int32,), (B,), dev)
+    _need_shape(blk_len, "blk_len", (torch.int32,), (B, None), dev)
+    if blk_len.shape[1] * int(Dmax) != NT:
+        raise ValueError(f"{NT} slots are not {blk_len.shape[1]} blocks of {Dmax}")
+    if paged:
+        _need_shape(block_table, "block_table", (torch.int32,), (B, None), dev)
+    if out is None:
+        out = _new_on(stream, lambda: torch.empty(q.shape, dtype=torch.float32 if out_f32 else q.dtype, device=dev))
+    else:
+        _need_shape(out, "out", (torch.float32,) + _HALF, tuple(q.shape), dev)
+    _need_apart(out=out, q=q)
+    ws = _quant_ws(ws, dev, stream)
+    args = attn_quant_args(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand, prefix_len, blk_len, Dmax,
+                           scale_block, out, scale, block_table)
+    with torch.cuda.device(dev):
+        _check("ssd_verify_attn_quant", lib().ssd_verify_attn_quant(ctypes.byref(args), _ptr(ws), ws.numel(),
+                                                                    _on_device(dev, stream)))
+    return out
 
 
 def ssd_copy_stats(gate, n_cand, acc_len, W, counts, stream=None):

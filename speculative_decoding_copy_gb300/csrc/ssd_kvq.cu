@@ -1,0 +1,341 @@
+// Writers of the 8-bit key/value cache: rows quantised into e4m3 codes with a power-of-two
+// scale for each block of tokens and head.
+//
+// A power of two costs an e4m3 number nothing (its precision is relative) and makes a
+// grown scale exact on the codes already there: only those that fall below the smallest
+// normal code round a second time.
+//
+// One CTA quantises one run (the rows that go to one block) of one head, of the keys or
+// of the values: the rows are read once into registers (up to eight 16-byte words a
+// thread cover the 128 rows x 128 elements of a block), their largest magnitude is reduced
+// over the CTA, and the codes leave as 8 bytes a word, contiguous over the run. Bound by
+// the bytes of the rows (and by launch latency for a few tokens).
+#include "ssd_kvq.cuh"
+
+namespace ssd {
+
+constexpr int kQuantThreads = 256;
+constexpr int kMaxScaleBlock = 128;
+
+struct QuantDst {
+  uint8_t* codes;       // place 0 of the block, [scale_block][dh]
+  float* scale;
+  int row;              // first place written
+};
+
+// |x| of 8 elements, the largest finite one as fp32 bits (infinities and NaN do not count)
+__device__ __forceinline__ uint32_t amax8(const float (&x)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t u = __float_as_uint(x[e]) & 0x7fffffffu;
+    m = max(m, u < 0x7f800000u ? u : 0u);
+  }
+  return m;
+}
+
+// the least power of two s with a <= 448 s (448 = 1.75 * 2^8), at least 2^-100; a as bits
+__device__ __forceinline__ float pow2_scale(uint32_t a) {
+  const int e = static_cast<int>(a >> 23) - 127;
+  const int k = max((a & 0x7fffffu) <= 0x600000u ? e - 8 : e - 7, -100);
+  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+
+// x / s, by the exact reciprocal where s is a power of two (|exponent| <= 126)
+struct Divider {
+  float s, inv;
+  bool pow2;
+  __device__ __forceinline__ explicit Divider(float sc) : s(sc) {
+    const uint32_t u = __float_as_uint(sc);
+    const int e = static_cast<int>(u >> 23);
+    pow2 = (u & 0x7fffffu) == 0 && e >= 1 && e <= 253;
+    inv = pow2 ? __uint_as_float(static_cast<uint32_t>(254 - e) << 23) : 0.f;
+  }
+  __device__ __forceinline__ float operator()(float x) const { return pow2 ? x * inv : __fdiv_rn(x, s); }
+};
+
+template <typename T>
+struct Word;             // 8 elements of a row
+template <>
+struct Word<uint16_t> {
+  uint4 a;
+  __device__ __forceinline__ void load(const uint16_t* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Word<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+
+// Quantise n <= 128 rows of dh elements, `stride` elements apart at src, into places
+// d.row .. d.row + n - 1 of one block. Every thread of the CTA calls it; `red` holds one
+// word a warp.
+template <typename T>
+__device__ __forceinline__ void quant_run(const T* __restrict__ src, int64_t stride, int n, int dh, QuantDst d,
+                                          uint32_t* red) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int sh = dh == 128 ? 4 : 3;           // 8-element words per row
+  const int words = n << sh;
+  constexpr int kWords = kMaxScaleBlock * 16 / kQuantThreads;
+  const float old = *d.scale;
+  Word<T> w[kWords];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    const int c = i * kQuantThreads + tid;
+    if (c < words) w[i].load(src + (c >> sh) * stride + ((c & ((1 << sh) - 1)) << 3));
+  }
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    if (i * kQuantThreads + tid < words) {
+      float x[8];
+      w[i].get(x);
+      m = max(m, amax8(x));
+    }
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  __syncthreads();                            // `red` and the block's scale of an earlier run
+  if (lane == 0) red[wid] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kQuantThreads / 32; ++i) m = max(m, red[i]);
+  const float need = pow2_scale(m);
+  const float now = d.row == 0 ? need : fmaxf(old, need);
+  if (d.row > 0 && now > old) {
+    // the rows before the run, under the grown scale
+    const float ratio = __fdiv_rn(old, now);
+    const int held = d.row << sh;
+    for (int c = tid; c < held; c += kQuantThreads) {
+      uint2* p = reinterpret_cast<uint2*>(d.codes) + c;
+      const uint2 v = *p;
+      const uint32_t h[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
+      uint32_t q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t f = e4m3x2_to_f16x2(h[i]);
+        float lo, hi;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+            : "=f"(lo), "=f"(hi) : "r"(f));
+        q[i] = e4m3x2(lo * ratio, hi * ratio);
+      }
+      *p = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+    }
+  }
+  const Divider by(now);
+  uint2* out = reinterpret_cast<uint2*>(d.codes) + (d.row << sh);
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    const int c = i * kQuantThreads + tid;
+    if (c < words) {
+      float x[8];
+      w[i].get(x);
+      out[c] = make_uint2(e4m3x2(by(x[0]), by(x[1])) | e4m3x2(by(x[2]), by(x[3])) << 16,
+                          e4m3x2(by(x[4]), by(x[5])) | e4m3x2(by(x[6]), by(x[7])) << 16);
+    }
+  }
+  __syncthreads();                            // every thread has read the old scale
+  if (tid == 0) *d.scale = now;
+}
+
+// grid (row ranges of `range` rows, heads, keys / values): the runs that start in the range
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads)
+k_append_quant(ssd_append_quant_args a, int range, int sb_log2, WsHeader* hdr) {
+  __shared__ int32_t slot[2 * kMaxScaleBlock];
+  __shared__ uint32_t brk[2 * kMaxScaleBlock / 32];     // rows that do not continue the row before
+  __shared__ uint32_t red[kQuantThreads / 32];
+  static_assert(kQuantThreads == 2 * kMaxScaleBlock, "one thread a row of the window");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x;
+  const int h = blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * range;
+  const int sb = 1 << sb_log2;
+  const int window = range + sb;                        // a run that starts in the range ends here
+  // one thread a row: its slot, and whether it continues the run of the row before
+  const int64_t t = t0 + tid;
+  const int64_t pool = a.num_pages * a.page_tokens;
+  int32_t s = -1, before = -2;
+  if (tid < window && t < a.T) {
+    s = a.slot_map[t];
+    if (t > 0) before = a.slot_map[t - 1];
+    if (s >= pool) {
+      if (h == 0 && !is_v && tid < range) record_error(hdr, SSD_ERR_DEVICE, 420);
+      s = -1;
+    }
+  }
+  const int32_t place = s >= 0 ? static_cast<int32_t>(s % a.page_tokens) : 0;
+  const bool cont = s >= 0 && before == s - 1 && (place & (sb - 1)) != 0;
+  slot[tid] = s;
+  const uint32_t word = __ballot_sync(0xffffffffu, !cont);
+  if ((tid & 31) == 0) brk[tid >> 5] = word;
+  __syncthreads();
+  const T* src = static_cast<const T*>(is_v ? a.v_new : a.k_new) + static_cast<int64_t>(h) * a.dh;
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  const int64_t blocks = (a.page_tokens + sb - 1) >> sb_log2;
+  for (int i = 0; i < range;) {
+    // next break at or after i
+    uint32_t bits = brk[i >> 5] & (0xffffffffu << (i & 31));
+    int wd = i >> 5;
+    while (bits == 0 && wd + 1 < 2 * kMaxScaleBlock / 32) bits = brk[++wd];
+    if (bits == 0) break;
+    const int first = wd * 32 + __ffs(static_cast<int>(bits)) - 1;
+    if (first >= range) break;
+    // the break after it ends the run (rows outside the list count as breaks)
+    bits &= bits - 1;
+    while (bits == 0 && wd + 1 < 2 * kMaxScaleBlock / 32) bits = brk[++wd];
+    const int last = bits != 0 ? wd * 32 + __ffs(static_cast<int>(bits)) - 1 : 2 * kMaxScaleBlock;
+    i = last;
+    const int32_t s0 = slot[first];
+    if (s0 < 0) continue;
+    const int64_t page = s0 / a.page_tokens;
+    const int off = static_cast<int>(s0 - page * a.page_tokens);
+    const int blk = off >> sb_log2;
+    const int64_t ph = page * a.Hkv + h;
+    QuantDst d;
+    d.codes = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) +
+              (ph * a.page_tokens + (static_cast<int64_t>(blk) << sb_log2)) * a.dh;
+    d.scale = (is_v ? a.v_scale : a.k_scale) + ph * blocks + blk;
+    d.row = off & (sb - 1);
+    quant_run<T>(src + (t0 + first) * stride, stride, last - first, a.dh, d, red);
+  }
+}
+
+// grid (sequences, heads, (keys / values) x blocks a run of Dmax rows can touch)
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads)
+k_commit_quant(ssd_commit_quant_args a, int64_t page_tokens, int sb_log2, int segs, WsHeader* hdr) {
+  __shared__ uint32_t red[kQuantThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x;
+  const int b = blockIdx.x, h = blockIdx.y;
+  const bool is_v = static_cast<int>(blockIdx.z) >= segs;
+  const int seg = static_cast<int>(blockIdx.z) - (is_v ? segs : 0);
+  const bool teller = h == 0 && blockIdx.z == 0 && tid == 0;
+  const int k = a.best_blk[b];
+  const int64_t n = k >= 0 ? static_cast<int64_t>(a.n_out[b]) - 1 : 0;
+  const int64_t P = a.prefix_len[b];
+  const int64_t room = a.block_table != nullptr ? static_cast<int64_t>(a.pages_per_seq) * kPageTokens : a.P_max;
+  bool ok = k < a.NB && n <= a.Dmax && P >= 0 && (n <= 0 || P + n <= room);
+  if (ok && n > 0 && a.block_table != nullptr) {
+    for (int64_t j = P / kPageTokens; j <= (P + n - 1) / kPageTokens; ++j) {
+      const int32_t pg = a.block_table[static_cast<int64_t>(b) * a.pages_per_seq + j];
+      ok = ok && pg >= 0 && pg < a.num_pages;
+    }
+  }
+  if (teller) {
+    if (!ok) record_error(hdr, SSD_ERR_DEVICE, 430);
+    a.new_len[b] = static_cast<int32_t>(ok && n > 0 ? P + n : P);
+  }
+  if (!ok || n <= 0) return;
+  // the seg-th block that the run touches: positions [p0, p1)
+  const int64_t blk = (P >> sb_log2) + seg;
+  const int64_t p0 = max(P, blk << sb_log2), p1 = min(P + n, (blk + 1) << sb_log2);
+  if (p0 >= p1) return;
+  int64_t page = b, place = p0;
+  if (a.block_table != nullptr) {
+    page = a.block_table[static_cast<int64_t>(b) * a.pages_per_seq + p0 / kPageTokens];
+    place = p0 % kPageTokens;
+  }
+  const int64_t ph = page * a.Hkv + h;
+  const int64_t blocks = (page_tokens + (1 << sb_log2) - 1) >> sb_log2;
+  const int64_t pblk = place >> sb_log2;
+  QuantDst d;
+  d.codes = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (ph * page_tokens + (pblk << sb_log2)) * a.dh;
+  d.scale = (is_v ? a.v_scale : a.k_scale) + ph * blocks + pblk;
+  d.row = static_cast<int>(place) & ((1 << sb_log2) - 1);
+  const int64_t src_row = static_cast<int64_t>(b) * a.NB * a.Dmax + static_cast<int64_t>(k) * a.Dmax + (p0 - P);
+  const int64_t stride = static_cast<int64_t>(a.Hkv) * a.dh;
+  quant_run<T>(static_cast<const T*>(is_v ? a.v_cand : a.k_cand) + src_row * stride + static_cast<int64_t>(h) * a.dh,
+               stride, static_cast<int>(p1 - p0), a.dh, d, red);
+}
+
+}  // namespace ssd
+
+extern "C" int ssd_append_kv_quant(const ssd_append_quant_args* a, void* ws, size_t ws_bytes, void* stream) {
+  using namespace ssd;
+  if (a == nullptr) return SSD_ERR_INVALID;
+  if (a->dtype != SSD_F32 && a->dtype != SSD_BF16) return SSD_ERR_INVALID;
+  if (a->T < 0 || a->Hkv < 1 || a->num_pages < 0 || a->page_tokens < 1) return SSD_ERR_INVALID;
+  if ((a->dh != 64 && a->dh != 128) || !scale_block_ok(a->scale_block) || a->Hkv > 65535) return SSD_ERR_UNSUPPORTED;
+  if (a->page_tokens >= (1LL << 31) || a->num_pages >= (1LL << 31) || a->num_pages * a->page_tokens >= (1LL << 31))
+    return SSD_ERR_UNSUPPORTED;
+  if (a->T >= (1LL << 31)) return SSD_ERR_UNSUPPORTED;
+  const int64_t row = static_cast<int64_t>(a->Hkv) * a->dh;
+  if (a->k_stride < row || a->v_stride < row) return SSD_ERR_INVALID;
+  if (a->T == 0) return SSD_OK;
+  if (!a->k_new || !a->v_new || !a->slot_map || !a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale)
+    return SSD_ERR_INVALID;
+  const int es = a->dtype == SSD_BF16 ? 2 : 4;
+  if (!aligned(a->k_new, 16) || !aligned(a->v_new, 16) || !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) ||
+      a->k_stride * es % 16 != 0 || a->v_stride * es % 16 != 0)
+    return SSD_ERR_UNSUPPORTED;
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < sizeof(WsHeader)) return SSD_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  WsHeader* hdr = static_cast<WsHeader*>(ws);
+  // rows a CTA looks at: one while there are few, so that single tokens run side by side;
+  // up to a whole block's where most rows continue a run and their CTAs would find nothing
+  int range = 1;
+  while (range < a->scale_block && a->T * a->Hkv * 2 / range > 4096) range *= 2;
+  const dim3 grid(static_cast<unsigned>((a->T + range - 1) / range), static_cast<unsigned>(a->Hkv), 2);
+  const int lg = log2_of(a->scale_block);
+  const cudaError_t e = a->dtype == SSD_BF16
+      ? launch_pdl(k_append_quant<uint16_t>, grid, dim3(kQuantThreads), 0, s, *a, range, lg, hdr)
+      : launch_pdl(k_append_quant<float>, grid, dim3(kQuantThreads), 0, s, *a, range, lg, hdr);
+  if (e != cudaSuccess) return SSD_ERR_CUDA;
+  count_launch();
+  return check_launch();
+}
+
+extern "C" int ssd_commit_kv_quant(const ssd_commit_quant_args* a, void* ws, size_t ws_bytes, void* stream) {
+  using namespace ssd;
+  if (a == nullptr) return SSD_ERR_INVALID;
+  if (a->dtype != SSD_F32 && a->dtype != SSD_BF16) return SSD_ERR_INVALID;
+  if (a->B < 0 || a->NB < 1 || a->Dmax < 1 || a->Hkv < 1) return SSD_ERR_INVALID;
+  if ((a->dh != 64 && a->dh != 128) || !scale_block_ok(a->scale_block) || a->Hkv > 65535 || a->Dmax > 256)
+    return SSD_ERR_UNSUPPORTED;
+  int64_t page_tokens = kPageTokens;
+  if (a->block_table != nullptr) {
+    if (a->pages_per_seq < 1 || a->num_pages < 1) return SSD_ERR_INVALID;
+    if (a->num_pages > 0x7fffffffLL / kPageTokens || a->pages_per_seq > 0x7fffffff / kPageTokens) return SSD_ERR_UNSUPPORTED;
+  } else {
+    if (a->P_max < 0) return SSD_ERR_INVALID;
+    if (a->P_max >= (1LL << 31) || a->P_max * a->B >= (1LL << 31)) return SSD_ERR_UNSUPPORTED;
+    page_tokens = a->P_max > 0 ? a->P_max : 1;
+  }
+  if (a->B == 0) return SSD_OK;
+  if (!a->k_cand || !a->v_cand || !a->prefix_len || !a->best_blk || !a->n_out || !a->new_len) return SSD_ERR_INVALID;
+  if ((a->block_table != nullptr || a->P_max > 0) && (!a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale))
+    return SSD_ERR_INVALID;
+  if (a->new_len == a->prefix_len) return SSD_ERR_INVALID;
+  if (!aligned(a->k_cand, 16) || !aligned(a->v_cand, 16) || !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16))
+    return SSD_ERR_UNSUPPORTED;
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < sizeof(WsHeader)) return SSD_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  WsHeader* hdr = static_cast<WsHeader*>(ws);
+  // blocks that Dmax rows can touch
+  const int segs = (a->Dmax + a->scale_block - 2) / a->scale_block + 1;
+  const dim3 grid(static_cast<unsigned>(a->B), static_cast<unsigned>(a->Hkv), static_cast<unsigned>(2 * segs));
+  const int lg = log2_of(a->scale_block);
+  const cudaError_t e = a->dtype == SSD_BF16
+      ? launch_pdl(k_commit_quant<uint16_t>, grid, dim3(kQuantThreads), 0, s, *a, page_tokens, lg, segs, hdr)
+      : launch_pdl(k_commit_quant<float>, grid, dim3(kQuantThreads), 0, s, *a, page_tokens, lg, segs, hdr);
+  if (e != cudaSuccess) return SSD_ERR_CUDA;
+  count_launch();
+  return check_launch();
+}

@@ -1,0 +1,122 @@
+"""Inputs and comparisons of the 8-bit cache's GPU tests."""
+import numpy as np
+import torch
+
+from oracle import kv_quant_oracle as K
+from oracle import ssd_oracle as O
+from speculative_decoding_copy_gb300 import _binding as S
+from speculative_decoding_copy_gb300 import workloads as WL
+
+DEV = "cuda"
+
+
+def dev(a):
+    a = np.ascontiguousarray(a)
+    return torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a).to(DEV)
+
+
+def bf16(rng, *shape, scale=1.0):
+    """Random bf16 rows: (bit patterns, their fp64 values)."""
+    bits = WL.f32_to_bf16_bits((rng.standard_normal(shape) * scale).astype(np.float32))
+    return bits, O.bf16_to_f64(bits)
+
+
+def cache(rng, pages, Hkv, tokens, dh, sb, pow2=True):
+    """A filled cache: codes and scales (powers of two, or any)."""
+    table = K.encode(rng.standard_normal(1 << 16) * 100)
+    codes = table[rng.integers(0, len(table), (pages, Hkv, tokens, dh))]
+    scale = 2.0 ** rng.integers(-8, -5, (pages, Hkv, -(-tokens // sb)))
+    if not pow2:
+        scale = scale * (1 + rng.random(scale.shape))
+    return codes, scale.astype(np.float32)
+
+
+class AttnCase:
+    """One attention call over a random cache, and its oracle."""
+
+    def __init__(self, seed, prefix, NB, Dmax, G, Hkv, dh, sb, paged, q_scale=1.5, blk_len=None, spare=2, pow2=False,
+                 order=None):
+        rng = self.rng = np.random.default_rng(seed)
+        B = len(prefix)
+        self.prefix, self.Dmax, self.sb, self.dh = np.asarray(prefix, np.int32), Dmax, sb, dh
+        NT, most = NB * Dmax, max(1, max(prefix))
+        if paged:
+            pps = -(-most // 128)
+            pages, tokens = B * pps + spare, 128
+            ids = rng.permutation(pages) if order is None else order(pages)
+            self.table = ids[:B * pps].reshape(B, pps).astype(np.int32)
+        else:
+            pages, tokens, self.table = B, most, None
+        self.k_codes, self.k_scale = cache(rng, pages, Hkv, tokens, dh, sb, pow2)
+        self.v_codes, self.v_scale = cache(rng, pages, Hkv, tokens, dh, sb, pow2)
+        self.q, self.q64 = bf16(rng, B, NT, Hkv * G, dh, scale=q_scale)
+        self.kc, self.kc64 = bf16(rng, B, NT, Hkv, dh)
+        self.vc, self.vc64 = bf16(rng, B, NT, Hkv, dh)
+        self.blk_len = np.asarray(blk_len if blk_len is not None else rng.integers(0, Dmax + 1, (B, NB)), np.int32)
+        if blk_len is None:
+            self.blk_len[0, 0] = Dmax
+
+    def poison(self):
+        """NaN codes and scales wherever the call must not look."""
+        for b, P in enumerate(self.prefix):
+            for codes, scale in ((self.k_codes, self.k_scale), (self.v_codes, self.v_scale)):
+                if self.table is None:
+                    codes[b, :, P:] = 0x7f
+                    scale[b, :, -(-P // self.sb):] = np.nan
+                else:
+                    for j, pg in enumerate(self.table[b]):
+                        left = max(0, P - 128 * j)
+                        codes[pg, :, left:] = 0x7f
+                        scale[pg, :, -(-left // self.sb):] = np.nan
+        NB = self.blk_len.shape[1]
+        absent = np.arange(self.Dmax)[None, None, :] >= self.blk_len[:, :, None]
+        absent = absent.reshape(len(self.prefix), NB * self.Dmax)
+        for x in (self.q, self.kc, self.vc):
+            x[absent] = 0x7fc0
+
+    def args(self):
+        t = [dev(x) for x in (self.q, self.k_codes, self.v_codes, self.k_scale, self.v_scale, self.kc, self.vc,
+                              self.prefix, self.blk_len)]
+        return t + [self.Dmax, self.sb]
+
+    def kw(self):
+        return dict(block_table=None if self.table is None else dev(self.table))
+
+    def oracle(self, slots=None):
+        k = K.values(self.k_codes, self.k_scale, self.sb, self.prefix, self.table)
+        v = K.values(self.v_codes, self.v_scale, self.sb, self.prefix, self.table)
+        return K.attention(self.q64, k, v, self.kc64, self.vc64, self.blk_len, self.Dmax, slots)
+
+    def check(self, out, slots=None, wide=1.0):
+        """Every present row within tolerance, absent rows as they were.
+
+        Tolerance, per element, with size = sum_j p_j |v_j|. The probabilities' rounding to 11
+        bits and the scores' errors (fp32 sums over dh <= 128 products of total magnitude
+        <= 32 in log2 units, 2^-23 each: < 2^-11) act on size: 2 * 2^-11. Weights below the
+        fp16 range round by at most 2^-25 each while the largest weight is at least 1:
+        N 2^-25 448 max v_scale. A bf16 output adds half a step of its own, 2^-8 |out|."""
+        f32 = out.dtype == torch.float32
+        got = out.cpu().numpy().astype(np.float64) if f32 else O.bf16_to_f64(out.view(torch.int16).cpu().numpy().view(np.uint16))
+        ref = self.oracle(slots)
+        assert ref
+        for (b, t), (o, size) in ref.items():
+            vs = self.v_scale[b] if self.table is None else self.v_scale[self.table[b]]
+            floor = self.prefix[b] * 2.0 ** -25 * 448 * float(np.nanmax(np.where(np.isfinite(vs), vs, 0), initial=0))
+            tol = wide * size * 2.0 ** -10 + floor + (0 if f32 else np.abs(o) * 2.0 ** -8) + 1e-30
+            err = np.abs(got[b, t] - o)
+            assert (err <= tol).all(), (b, t, float((err / tol).max()))
+        return ref
+
+
+def run(case, fill=7.0, f32=True, **kw):
+    """Call the attention into a buffer of `fill`; absent rows must keep it."""
+    B, NT, Hq, dh = case.q.shape
+    out = torch.full((B, NT, Hq, dh), fill, dtype=torch.float32 if f32 else torch.bfloat16, device=DEV)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    S.ssd_verify_attn_quant(*case.args(), out=out, ws=ws, **case.kw(), **kw)
+    torch.cuda.synchronize()
+    assert S.ssd_read_device_error(ws) == S.SSD_OK
+    keep = np.arange(case.Dmax)[None, None, :] >= case.blk_len[:, :, None]
+    keep = torch.from_numpy(keep.reshape(B, NT)).to(DEV)
+    assert bool((out[keep] == fill).all()), "a row of an absent token was written"
+    return out
