@@ -411,7 +411,8 @@ int ssd_commit_kv(const ssd_commit_args* a, void* ws, size_t ws_bytes, void* str
  *   free_pages [num_pages], n_free [1]: int32, updated in place; row_start [B+1],
  *   slot_map [slot_cap] (NULL iff slot_cap == 0), served [B] (1 or 0; optional): int32
  *   outputs. Every page belongs to one sequence or to the stack: pages shared by
- *   sequences are not counted. Buffers must not overlap.
+ *   sequences are not counted. Buffers that are written must not overlap others
+ *   (SSD_ERR_INVALID, as for the calls below).
  * Device-side errors (SSD_ERR_DEVICE in the workspace header): a negative length, a
  * sequence that wants more than pages_per_seq pages or whose n_pages is outside
  * [0, pages_per_seq] (it is not served and left unchanged; a negative add_len counts as
@@ -543,7 +544,7 @@ int ssd_commit_kv_quant(const ssd_commit_quant_args* a, void* ws, size_t ws_byte
  * Supported: dh 64 or 128; Hq % Hkv == 0, Hq / Hkv <= 64; 1 <= Dmax <= 256,
  * NB * Dmax <= 8192; scale_block 16, 32, 64 or 128; 16-byte aligned tensors;
  * num_pages * 128 * Hkv < 2^31 (B * Hkv * P_max < 2^31); else SSD_ERR_UNSUPPORTED.
- * scale == 0 selects 1/sqrt(dh). A prefix_len outside the cache or a page outside the
+ * scale == 0 selects 1/sqrt(dh). out must not overlap an input. A prefix_len outside the cache or a page outside the
  * pool records SSD_ERR_DEVICE (the prefix counts as empty, the page as page 0).
  * Workspace: ssd_verify_attn_quant_workspace_size(a) bytes (256: the status header),
  * 256-byte aligned.

@@ -426,40 +426,66 @@ def ssd_commit_kv(k_cache, v_cache, k_cand, v_cand, prefix_len, best_blk, n_out,
 
 
 # ---------------------------------------------------------------------------
-# the 8-bit cache
+# the 8-bit cache. A step makes several of these calls for a few microseconds of GPU work
+# each, so a call's checks cost one comparison of each property a tensor has to have; which
+# one failed is worked out only then. Pointers go to ctypes as plain integers.
 QUANT_PAGE = 128
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+_ROWS = (torch.float32,) + _HALF
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
 
 
 def _need_shape(t, name, dtypes, shape, device):
-    """_need, with the exact shape and device (None: any size)."""
+    """_need, with the exact shape and device."""
+    if (type(t) is torch.Tensor and t.shape == shape and t.dtype in dtypes and t.device == device
+            and t.is_contiguous()):
+        return
     _need(t, name, dtypes, len(shape))
-    if any(want is not None and have != want for have, want in zip(t.shape, shape)):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
-def _need_apart(**tensors):
-    """Raise where two of the named tensors share memory."""
-    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), n) for n, t in tensors.items()
-                   if t is not None and t.numel())
-    for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
+def _need_apart(*named):
+    """Raise where two of the (name, tensor) pairs share memory."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes, n) for n, t in named if t.nbytes)
+    end, a = 0, ""
+    for start, stop, b in spans:
         if start < end:
             raise ValueError(f"{a} and {b} overlap")
+        end, a = stop, b
 
 
-def _quant_cache(k_cache, v_cache, k_scale, v_scale, scale_block, device, pages=None, tokens=None):
-    """Check a cache of codes [pages][Hkv][tokens][dh] and its scales; returns its four sizes."""
+def _quant_cache(k_cache, v_cache, k_scale, v_scale, scale_block, device):
+    """Check a cache of codes [pages][Hkv][tokens][dh] and its scales; returns its shape."""
     if scale_block not in (16, 32, 64, 128):
         raise ValueError("scale_block must be 16, 32, 64 or 128")
-    _need_shape(k_cache, "k_cache", _CODES, (pages, None, tokens, None), device)
-    _need_shape(v_cache, "v_cache", _CODES, tuple(k_cache.shape), device)
-    n, Hkv, P, dh = k_cache.shape
-    shape = (n, Hkv, -(-P // scale_block))
-    _need_shape(k_scale, "k_scale", (torch.float32,), shape, device)
-    _need_shape(v_scale, "v_scale", (torch.float32,), shape, device)
-    return n, Hkv, P, dh
+    _need(k_cache, "k_cache", _CODES, 4)
+    shape = k_cache.shape
+    if k_cache.device != device:
+        raise ValueError(f"k_cache is on {k_cache.device}, not on {device}")
+    _need_shape(v_cache, "v_cache", _CODES, shape, device)
+    scales = (shape[0], shape[1], -(-shape[2] // scale_block))
+    _need_shape(k_scale, "k_scale", _F32, scales, device)
+    _need_shape(v_scale, "v_scale", _F32, scales, device)
+    return shape
+
+
+def _cache_fits(shape, B, block_table, device):
+    """A paged cache has pages of 128 tokens and a table row a sequence, a contiguous one a place
+    for every sequence; returns (pointer to the table, pages of a sequence)."""
+    if block_table is None:
+        if shape[0] != B:
+            raise ValueError(f"k_cache holds {shape[0]} sequences, not {B}")
+        return None, 0
+    if shape[2] != QUANT_PAGE:
+        raise ValueError(f"k_cache holds pages of {shape[2]} tokens, not {QUANT_PAGE}")
+    _need(block_table, "block_table", _I32, 2)
+    pps = block_table.shape[1]
+    _need_shape(block_table, "block_table", _I32, (B, pps), device)
+    return block_table.data_ptr(), pps
 
 
 def _new_on(stream, make):
@@ -470,21 +496,32 @@ def _new_on(stream, make):
         return make()
 
 
-def _quant_ws(ws, device, stream):
-    """The caller's workspace, or a fresh one whose header is clear."""
+def _quant_call(fn, args, ws, device, stream, *named):
+    """Call entry point `fn` on `stream` (the device's current one where none is given) with the
+    device current; a workspace whose header is clear is made where none is given. `named`:
+    the (name, tensor) pairs that must not overlap, to name those for which the call was
+    refused."""
     if ws is None:
-        return _new_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=device))
-    _need(ws, "ws", (torch.uint8,), 1)
-    if ws.device != device:
-        raise ValueError(f"ws is on {ws.device}, not on {device}")
-    return ws
-
-
-def _on_device(device, stream):
-    """Handle of the stream a call on `device`'s tensors runs on: its current one where none is given."""
-    if stream is not None and stream.device != device:
+        ws = _new_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=device))
+    elif ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    return ctypes.c_void_p((stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
+    else:
+        handle = stream.cuda_stream
+    call = getattr(lib(), fn)
+    if torch._C._cuda_getDevice() == device.index:
+        rc = call(ctypes.byref(args), ws.data_ptr(), ws.numel(), handle)
+    else:
+        with torch.cuda.device(device):
+            rc = call(ctypes.byref(args), ws.data_ptr(), ws.numel(), handle)
+    if rc != SSD_OK:
+        if rc == SSD_ERR_INVALID:
+            _need_apart(*named)
+        raise SsdError(fn, rc)
+    return ws
 
 
 def ssd_page_tables(cur_len, add_len, n_pages, block_table, free_pages, n_free, slot_cap, *, out=None, ws=None,
@@ -492,46 +529,54 @@ def ssd_page_tables(cur_len, add_len, n_pages, block_table, free_pages, n_free, 
     """Block tables that hold exactly ceil((cur_len + add_len) / 128) pages a sequence (grown from
     or trimmed to the stack of free pages, all updated in place) and the slots of the added
     tokens; returns dict(row_start [B+1], slot_map [slot_cap], served [B])."""
-    _need(cur_len, "cur_len", (torch.int32,), 1)
-    dev, B, i32 = cur_len.device, cur_len.shape[0], (torch.int32,)
-    _need_shape(add_len, "add_len", i32, (B,), dev)
-    _need_shape(n_pages, "n_pages", i32, (B,), dev)
-    _need_shape(block_table, "block_table", i32, (B, None), dev)
-    _need_shape(free_pages, "free_pages", i32, (None,), dev)
-    _need_shape(n_free, "n_free", i32, (1,), dev)
-    cap = int(slot_cap)
+    _need(cur_len, "cur_len", _I32, 1)
+    dev, B, cap = cur_len.device, cur_len.shape[0], int(slot_cap)
+    _need_shape(add_len, "add_len", _I32, (B,), dev)
+    _need_shape(n_pages, "n_pages", _I32, (B,), dev)
+    _need(block_table, "block_table", _I32, 2)
+    pps = block_table.shape[1]
+    _need_shape(block_table, "block_table", _I32, (B, pps), dev)
+    _need(free_pages, "free_pages", _I32, 1)
+    pool = free_pages.shape[0]
+    _need_shape(free_pages, "free_pages", _I32, (pool,), dev)
+    _need_shape(n_free, "n_free", _I32, (1,), dev)
     if cap < 0:
         raise ValueError("slot_cap must not be negative")
-    o = dict(out or {})
-    for k, n in (("row_start", B + 1), ("slot_map", cap), ("served", B)):
-        if o.get(k) is None:
-            o[k] = _new_on(stream, lambda: torch.empty(n, dtype=torch.int32, device=dev))
-        else:
-            _need_shape(o[k], k, i32, (n,), dev)
-    _need_apart(cur_len=cur_len, n_pages=n_pages, block_table=block_table, free_pages=free_pages, n_free=n_free, **o)
-    _need_apart(add_len=add_len, n_pages=n_pages, block_table=block_table, free_pages=free_pages, n_free=n_free, **o)
-    ws = _quant_ws(ws, dev, stream)
-    args = PagesArgs(_ptr(cur_len), _ptr(add_len), _ptr(n_pages), _ptr(block_table), _ptr(free_pages), _ptr(n_free),
-                     _ptr(o["row_start"]), _ptr(o["slot_map"]) if cap else None, _ptr(o["served"]), B,
-                     block_table.shape[1], free_pages.shape[0], cap)
-    with torch.cuda.device(dev):
-        _check("ssd_page_tables", lib().ssd_page_tables(ctypes.byref(args), _ptr(ws), ws.numel(), _on_device(dev, stream)))
-    return o
+    o = {} if out is None else out
+    start, slots, served = o.get("row_start"), o.get("slot_map"), o.get("served")
+    if start is None and slots is None and served is None:
+        buf = _new_on(stream, lambda: torch.empty(cap + 2 * B + 1, dtype=torch.int32, device=dev))
+        slots, start, served = buf.split((cap, B + 1, B))
+    else:
+        make = lambda n: _new_on(stream, lambda: torch.empty(n, dtype=torch.int32, device=dev))
+        start, slots, served = (make(n) if t is None else t for t, n in ((start, B + 1), (slots, cap), (served, B)))
+        _need_shape(start, "row_start", _I32, (B + 1,), dev)
+        _need_shape(slots, "slot_map", _I32, (cap,), dev)
+        _need_shape(served, "served", _I32, (B,), dev)
+    args = PagesArgs(cur_len.data_ptr(), add_len.data_ptr(), n_pages.data_ptr(), block_table.data_ptr(),
+                     free_pages.data_ptr(), n_free.data_ptr(), start.data_ptr(), slots.data_ptr() if cap else None,
+                     served.data_ptr(), B, pps, pool, cap)
+    _quant_call("ssd_page_tables", args, ws, dev, stream, ("n_pages", n_pages), ("block_table", block_table),
+                ("free_pages", free_pages), ("n_free", n_free), ("row_start", start), ("slot_map", slots),
+                ("served", served), ("cur_len", cur_len))
+    return {"row_start": start, "slot_map": slots, "served": served}
 
 
-def _rows(t, name, Hkv, dh, dtypes, device):
+def _rows(t, name, shape, dtypes, device):
     """Check new rows [T][Hkv][dh], dense but for the stride between rows; returns that stride."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if t.dim() != 3 or tuple(t.shape[1:]) != (Hkv, dh):
-        raise ValueError(f"{name} must be [T][{Hkv}][{dh}], got {list(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.numel() and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != dh)):
+    T, Hkv, dh = shape
+    row, head, one = t.stride()
+    if T and (one != 1 or (Hkv > 1 and head != dh)):
         raise ValueError(f"{name}: the heads of a row must be dense")
-    return t.stride(0) if t.shape[0] > 1 else Hkv * dh
+    return row if T > 1 else Hkv * dh
 
 
 def ssd_append_kv_quant(k_new, v_new, slot_map, k_cache, v_cache, k_scale, v_scale, scale_block=128, *, ws=None,
@@ -539,57 +584,45 @@ def ssd_append_kv_quant(k_new, v_new, slot_map, k_cache, v_cache, k_scale, v_sca
     """Quantise the rows k_new, v_new [T][Hkv][dh] (bf16 or fp32, any row stride) into the 8-bit
     cache at slot_map [T] (page * tokens of a page + place; negative: skipped), in place. A
     contiguous cache [B][Hkv][P_max][dh] is B pages of P_max tokens. Returns the workspace."""
-    _need(slot_map, "slot_map", (torch.int32,), 1)
+    _need(slot_map, "slot_map", _I32, 1)
     dev, T = slot_map.device, slot_map.shape[0]
-    pages, Hkv, tokens, dh = _quant_cache(k_cache, v_cache, k_scale, v_scale, int(scale_block), dev)
-    types = (torch.float32,) + _HALF
-    ks = _rows(k_new, "k_new", Hkv, dh, types, dev)
-    vs = _rows(v_new, "v_new", Hkv, dh, (k_new.dtype,), dev)
-    if k_new.shape[0] != T or v_new.shape[0] != T:
-        raise ValueError(f"k_new and v_new must hold the {T} rows of slot_map")
-    _need_apart(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, slot_map=slot_map)
-    ws = _quant_ws(ws, dev, stream)
-    args = AppendQuantArgs(_ptr(k_new), _ptr(v_new), _ptr(slot_map), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                           _ptr(v_scale), _elem_type(k_new), Hkv, dh, int(scale_block), T, ks, vs, pages, tokens)
-    with torch.cuda.device(dev):
-        _check("ssd_append_kv_quant", lib().ssd_append_kv_quant(ctypes.byref(args), _ptr(ws), ws.numel(),
-                                                                _on_device(dev, stream)))
-    return ws
+    pages, Hkv, tokens, dh = _quant_cache(k_cache, v_cache, k_scale, v_scale, scale_block, dev)
+    ks = _rows(k_new, "k_new", (T, Hkv, dh), _ROWS, dev)
+    vs = _rows(v_new, "v_new", (T, Hkv, dh), (k_new.dtype,), dev)
+    args = AppendQuantArgs(k_new.data_ptr(), v_new.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(),
+                           v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _elem_type(k_new), Hkv, dh,
+                           scale_block, T, ks, vs, pages, tokens)
+    return _quant_call("ssd_append_kv_quant", args, ws, dev, stream, ("k_cache", k_cache), ("v_cache", v_cache),
+                       ("k_scale", k_scale), ("v_scale", v_scale), ("slot_map", slot_map))
 
 
 def ssd_commit_kv_quant(k_cache, v_cache, k_scale, v_scale, k_cand, v_cand, prefix_len, best_blk, n_out, Dmax,
                         scale_block=128, *, new_len=None, block_table=None, ws=None, stream=None):
     """Quantise the accepted tokens' K/V rows (ssd_accept's best_blk, n_out) into the 8-bit cache
     at the end of each sequence's prefix; returns (new_len, workspace)."""
-    _need(prefix_len, "prefix_len", (torch.int32,), 1)
+    _need(prefix_len, "prefix_len", _I32, 1)
     dev, B = prefix_len.device, prefix_len.shape[0]
-    paged = block_table is not None
-    pages, Hkv, P, dh = _quant_cache(k_cache, v_cache, k_scale, v_scale, int(scale_block), dev, None if paged else B,
-                                     QUANT_PAGE if paged else None)
-    _need_shape(k_cand, "k_cand", (torch.float32,) + _HALF, (B, None, Hkv, dh), dev)
-    _need_shape(v_cand, "v_cand", (k_cand.dtype,), tuple(k_cand.shape), dev)
-    _need_shape(best_blk, "best_blk", (torch.int32,), (B,), dev)
-    _need_shape(n_out, "n_out", (torch.int32,), (B,), dev)
+    shape = pages, Hkv, P, dh = _quant_cache(k_cache, v_cache, k_scale, v_scale, scale_block, dev)
+    table, pps = _cache_fits(shape, B, block_table, dev)
+    _need(k_cand, "k_cand", _ROWS, 4)
     NT = k_cand.shape[1]
-    if int(Dmax) < 1 or NT % int(Dmax):
+    _need_shape(k_cand, "k_cand", _ROWS, (B, NT, Hkv, dh), dev)
+    _need_shape(v_cand, "v_cand", (k_cand.dtype,), (B, NT, Hkv, dh), dev)
+    _need_shape(best_blk, "best_blk", _I32, (B,), dev)
+    _need_shape(n_out, "n_out", _I32, (B,), dev)
+    if Dmax < 1 or NT % Dmax:
         raise ValueError(f"{NT} candidate slots are no whole blocks of {Dmax}")
-    if paged:
-        _need_shape(block_table, "block_table", (torch.int32,), (B, None), dev)
     if new_len is None:
         new_len = _new_on(stream, lambda: torch.empty_like(prefix_len))
     else:
-        _need_shape(new_len, "new_len", (torch.int32,), (B,), dev)
-    _need_apart(new_len=new_len, prefix_len=prefix_len, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale,
-                v_scale=v_scale)
-    ws = _quant_ws(ws, dev, stream)
-    args = CommitQuantArgs(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(k_cand), _ptr(v_cand),
-                           _ptr(prefix_len), _ptr(best_blk), _ptr(n_out), _ptr(new_len), _ptr(block_table),
-                           _elem_type(k_cand), B, NT // int(Dmax), int(Dmax), Hkv, dh, int(scale_block),
-                           block_table.shape[1] if paged else 0, P, pages)
-    with torch.cuda.device(dev):
-        _check("ssd_commit_kv_quant", lib().ssd_commit_kv_quant(ctypes.byref(args), _ptr(ws), ws.numel(),
-                                                                _on_device(dev, stream)))
-    return new_len, ws
+        _need_shape(new_len, "new_len", _I32, (B,), dev)
+    args = CommitQuantArgs(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                           k_cand.data_ptr(), v_cand.data_ptr(), prefix_len.data_ptr(), best_blk.data_ptr(),
+                           n_out.data_ptr(), new_len.data_ptr(), table, _elem_type(k_cand), B, NT // Dmax, Dmax, Hkv,
+                           dh, scale_block, pps, P, pages)
+    return new_len, _quant_call("ssd_commit_kv_quant", args, ws, dev, stream, ("new_len", new_len),
+                                ("prefix_len", prefix_len), ("k_cache", k_cache), ("v_cache", v_cache),
+                                ("k_scale", k_scale), ("v_scale", v_scale))
 
 
 def attn_quant_args(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand, prefix_len, blk_len, Dmax, scale_block,
@@ -597,10 +630,11 @@ def attn_quant_args(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand, prefi
     """Marshal the 8-bit attention's arguments (layouts as ssd_verify_attn_quant)."""
     B, _, Hq, dh = q.shape
     pages, Hkv, P, _ = k_cache.shape
-    return AttnQuantArgs(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(k_cand),
-                         _ptr(v_cand), _ptr(out), _ptr(prefix_len), _ptr(blk_len), _ptr(block_table),
-                         _elem_type(out), B, blk_len.shape[1], int(Dmax), Hq, Hkv, dh, int(scale_block),
-                         block_table.shape[1] if block_table is not None else 0, float(scale), P, pages)
+    table, pps = (None, 0) if block_table is None else (block_table.data_ptr(), block_table.shape[1])
+    return AttnQuantArgs(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                         k_cand.data_ptr(), v_cand.data_ptr(), out.data_ptr(), prefix_len.data_ptr(),
+                         blk_len.data_ptr(), table, _elem_type(out), B, blk_len.shape[1], Dmax, Hq, Hkv, dh,
+                         scale_block, pps, scale, P, pages)
 
 
 def ssd_verify_attn_quant_workspace_size(args: AttnQuantArgs) -> int:
@@ -616,30 +650,23 @@ def ssd_verify_attn_quant(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand,
     _need(q, "q", _HALF, 4)
     dev = q.device
     B, NT, Hq, dh = q.shape
-    paged = block_table is not None
-    _, Hkv, _, _ = _quant_cache(k_cache, v_cache, k_scale, v_scale, int(scale_block), dev, None if paged else B,
-                                QUANT_PAGE if paged else None)
-    if k_cache.shape[3] != dh:
-        raise ValueError(f"k_cache holds rows of {k_cache.shape[3]} elements, q of {dh}")
-    _need_shape(k_cand, "k_cand", _HALF, (B, NT, Hkv, dh), dev)
-    _need_shape(v_cand, "v_cand", _HALF, (B, NT, Hkv, dh), dev)
-    _need_shape(prefix_len, "prefix_len", (torch.int32,), (B,), dev)
-    _need_shape(blk_len, "blk_len", (torch.int32,), (B, None), dev)
-    if blk_len.shape[1] * int(Dmax) != NT:
-        raise ValueError(f"{NT} slots are not {blk_len.shape[1]} blocks of {Dmax}")
-    if paged:
-        _need_shape(block_table, "block_table", (torch.int32,), (B, None), dev)
+    shape = _quant_cache(k_cache, v_cache, k_scale, v_scale, scale_block, dev)
+    _cache_fits(shape, B, block_table, dev)
+    _need_shape(k_cand, "k_cand", _HALF, (B, NT, shape[1], dh), dev)
+    _need_shape(v_cand, "v_cand", _HALF, (B, NT, shape[1], dh), dev)
+    _need_shape(prefix_len, "prefix_len", _I32, (B,), dev)
+    if Dmax < 1 or NT % Dmax:
+        raise ValueError(f"{NT} candidate slots are no whole blocks of {Dmax}")
+    _need_shape(blk_len, "blk_len", _I32, (B, NT // Dmax), dev)
+    if shape[3] != dh:
+        raise ValueError(f"k_cache holds rows of {shape[3]} elements, q of {dh}")
     if out is None:
         out = _new_on(stream, lambda: torch.empty(q.shape, dtype=torch.float32 if out_f32 else q.dtype, device=dev))
     else:
-        _need_shape(out, "out", (torch.float32,) + _HALF, tuple(q.shape), dev)
-    _need_apart(out=out, q=q)
-    ws = _quant_ws(ws, dev, stream)
+        _need_shape(out, "out", _ROWS, q.shape, dev)
     args = attn_quant_args(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand, prefix_len, blk_len, Dmax,
                            scale_block, out, scale, block_table)
-    with torch.cuda.device(dev):
-        _check("ssd_verify_attn_quant", lib().ssd_verify_attn_quant(ctypes.byref(args), _ptr(ws), ws.numel(),
-                                                                    _on_device(dev, stream)))
+    _quant_call("ssd_verify_attn_quant", args, ws, dev, stream, ("out", out), ("q", q))
     return out
 
 

@@ -563,6 +563,11 @@ static int validate(const ssd_attn_quant_args* a) {
   if (!aligned(a->q, 16) || !aligned(a->k_cand, 16) || !aligned(a->v_cand, 16) || !aligned(a->out, 16) ||
       !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16))
     return SSD_ERR_UNSUPPORTED;
+  const int64_t slots = static_cast<int64_t>(a->B) * a->NB * a->Dmax, rows = slots * a->Hq * a->dh, cand = 2 * slots * a->Hkv * a->dh;
+  const int64_t tokens = a->block_table != nullptr ? a->num_pages * kPageTokens : a->B * a->P_max;
+  const Span spans[] = {{a->out, rows * (a->out_dtype == SSD_F32 ? 4 : 2)}, {a->q, 2 * rows}, {a->k_cand, cand},
+                        {a->v_cand, cand}, {a->k_cache, tokens * a->Hkv * a->dh}, {a->v_cache, tokens * a->Hkv * a->dh}};
+  if (overlap(spans, 1, 6)) return SSD_ERR_INVALID;
   return SSD_OK;
 }
 

@@ -279,12 +279,19 @@ extern "C" int ssd_append_kv_quant(const ssd_append_quant_args* a, void* ws, siz
   const int64_t row = static_cast<int64_t>(a->Hkv) * a->dh;
   if (a->k_stride < row || a->v_stride < row) return SSD_ERR_INVALID;
   if (a->T == 0) return SSD_OK;
+  if (a->k_stride > (1LL << 59) / a->T || a->v_stride > (1LL << 59) / a->T) return SSD_ERR_UNSUPPORTED;
   if (!a->k_new || !a->v_new || !a->slot_map || !a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale)
     return SSD_ERR_INVALID;
   const int es = a->dtype == SSD_BF16 ? 2 : 4;
   if (!aligned(a->k_new, 16) || !aligned(a->v_new, 16) || !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) ||
       a->k_stride * es % 16 != 0 || a->v_stride * es % 16 != 0)
     return SSD_ERR_UNSUPPORTED;
+  const int64_t codes = a->num_pages * a->page_tokens * row;
+  const int64_t scales = 4 * a->num_pages * a->Hkv * ((a->page_tokens + a->scale_block - 1) / a->scale_block);
+  const Span spans[] = {{a->k_cache, codes}, {a->v_cache, codes}, {a->k_scale, scales}, {a->v_scale, scales},
+                        {a->k_new, ((a->T - 1) * a->k_stride + row) * es}, {a->v_new, ((a->T - 1) * a->v_stride + row) * es},
+                        {a->slot_map, 4 * a->T}};
+  if (overlap(spans, 4, 7)) return SSD_ERR_INVALID;
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < sizeof(WsHeader)) return SSD_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   WsHeader* hdr = static_cast<WsHeader*>(ws);
@@ -309,6 +316,7 @@ extern "C" int ssd_commit_kv_quant(const ssd_commit_quant_args* a, void* ws, siz
   if (a->B < 0 || a->NB < 1 || a->Dmax < 1 || a->Hkv < 1) return SSD_ERR_INVALID;
   if ((a->dh != 64 && a->dh != 128) || !scale_block_ok(a->scale_block) || a->Hkv > 65535 || a->Dmax > 256)
     return SSD_ERR_UNSUPPORTED;
+  if (static_cast<double>(a->B) * a->NB * a->Dmax * a->Hkv >= 0x1p40) return SSD_ERR_UNSUPPORTED;
   int64_t page_tokens = kPageTokens;
   if (a->block_table != nullptr) {
     if (a->pages_per_seq < 1 || a->num_pages < 1) return SSD_ERR_INVALID;
@@ -322,9 +330,17 @@ extern "C" int ssd_commit_kv_quant(const ssd_commit_quant_args* a, void* ws, siz
   if (!a->k_cand || !a->v_cand || !a->prefix_len || !a->best_blk || !a->n_out || !a->new_len) return SSD_ERR_INVALID;
   if ((a->block_table != nullptr || a->P_max > 0) && (!a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale))
     return SSD_ERR_INVALID;
-  if (a->new_len == a->prefix_len) return SSD_ERR_INVALID;
   if (!aligned(a->k_cand, 16) || !aligned(a->v_cand, 16) || !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16))
     return SSD_ERR_UNSUPPORTED;
+  const int64_t pages = a->block_table != nullptr ? a->num_pages : a->B;
+  const int64_t cand = static_cast<int64_t>(a->B) * a->NB * a->Dmax * a->Hkv * a->dh * (a->dtype == SSD_BF16 ? 2 : 4);
+  const int64_t codes = pages * page_tokens * a->Hkv * a->dh;
+  const int64_t scales = 4 * pages * a->Hkv * ((page_tokens + a->scale_block - 1) / a->scale_block);
+  const Span spans[] = {{a->k_cache, codes}, {a->v_cache, codes}, {a->k_scale, scales}, {a->v_scale, scales},
+                        {a->new_len, 4LL * a->B}, {a->prefix_len, 4LL * a->B}, {a->k_cand, cand}, {a->v_cand, cand},
+                        {a->best_blk, 4LL * a->B}, {a->n_out, 4LL * a->B},
+                        {a->block_table, 4LL * a->B * a->pages_per_seq}};
+  if (overlap(spans, 5, 11)) return SSD_ERR_INVALID;
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < sizeof(WsHeader)) return SSD_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   WsHeader* hdr = static_cast<WsHeader*>(ws);

@@ -22,6 +22,22 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
   return r;
 }
 
+// bytes [p, p + n) that a call reads or writes
+struct Span {
+  const void* p;
+  int64_t n;
+};
+
+// whether one of the first `writes` spans shares a byte with any other
+inline bool overlap(const Span* s, int writes, int count) {
+  for (int i = 0; i < writes; ++i)
+    for (int j = i + 1; j < count; ++j) {
+      const char *a = static_cast<const char*>(s[i].p), *b = static_cast<const char*>(s[j].p);
+      if (a != nullptr && b != nullptr && s[i].n > 0 && s[j].n > 0 && a < b + s[j].n && b < a + s[i].n) return true;
+    }
+  return false;
+}
+
 inline bool scale_block_ok(int sb) { return sb == 16 || sb == 32 || sb == 64 || sb == 128; }
 inline int log2_of(int sb) { return sb == 16 ? 4 : sb == 32 ? 5 : sb == 64 ? 6 : 7; }
 

@@ -204,6 +204,11 @@ extern "C" int ssd_page_tables(const ssd_pages_args* a, void* ws, size_t ws_byte
   if (a->num_pages > (0x7fffffffLL / kPageTokens) || a->slot_cap > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
   // the pages of 1024 sequences are counted in 32 bits
   if (a->pages_per_seq > (1 << 20)) return SSD_ERR_UNSUPPORTED;
+  const Span spans[] = {{a->n_pages, 4LL * a->B}, {a->block_table, 4LL * a->B * a->pages_per_seq},
+                        {a->free_pages, 4 * a->num_pages}, {a->n_free, 4}, {a->row_start, 4LL * a->B + 4},
+                        {a->slot_map, 4 * a->slot_cap}, {a->served, 4LL * a->B}, {a->cur_len, 4LL * a->B},
+                        {a->add_len, 4LL * a->B}};
+  if (overlap(spans, 7, 9)) return SSD_ERR_INVALID;
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < sizeof(WsHeader)) return SSD_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   WsHeader* hdr = static_cast<WsHeader*>(ws);
