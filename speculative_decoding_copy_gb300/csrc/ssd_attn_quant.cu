@@ -8,21 +8,22 @@
 // the running maximum of y, moved only when it grows by more than 2^8.
 //
 // What bounds it: the cache's bytes, read once (2 dh bytes a key and kv head). A warp
-// takes 16 keys a step and keeps its own running maximum, sum and output (online
+// takes two tiles of 16 keys a step and keeps its own running maximum, sum and output (online
 // softmax), so warps share nothing until the end. Both products have the cache as their
 // 16-row operand and the packed query rows as the 8-column one (S^T = K Q^T and
-// O^T = V^T P^T, mma.sync m16n8k16), so eight rows, one token of most group sizes, waste
+// O^T = V^T P^T, mma.sync), so eight rows, one token of most group sizes, waste
 // nothing; a second column tile serves up to 16 rows. P^T turns from accumulator to operand
 // by one movmatrix for 8 keys. Each lane copies exactly the bytes that its own matrix
 // fragments need (cp.async, 16 bytes, whole 32-byte sectors) into a private ring in shared
 // memory several steps ahead and reads them back itself: no barrier, no transpose. That
 // works because both products may permute an index: for K Q^T lane (g, t) holds elements
 // 16t .. 16t+15 of each 64-element half of keys g and g + 8, and Q is laid out alike; for
-// V^T P^T it holds, for its four keys, the dh/8 output elements from dh/8 g on. Codes become
-// fp16 exactly by one conversion for two; q is scaled by a power of two per row to fit
-// fp16, probabilities are rounded to fp16 (at most 2^8). mma.sync is enough here: the matrix
-// work is under a third of the time the bytes take, and eight rows are a sixteenth of the
-// smallest tcgen05 tile.
+// V^T P^T it holds, for its four keys, the dh/8 output elements from dh/8 g on. K Q^T takes the
+// codes as they are (e4m3 products, fp32 sums) against q as a sum of two e4m3 numbers; for
+// V^T P^T they become fp16 exactly, by one conversion for two, against probabilities rounded
+// to fp16 (at most 2^8): 11 bits where two e4m3 numbers would hold 8, for few instructions
+// more. mma.sync is enough here: the matrix work is a fifth of the time the bytes take, and
+// eight rows are a sixteenth of the smallest tcgen05 tile.
 //
 // The CTAs of a cluster split the steps of a (sequence, kv head) evenly by its own length;
 // rank 0 adds the own-block keys (bf16 products, probabilities as a sum of two bf16). Warps
@@ -38,15 +39,17 @@
 
 namespace ssd {
 
-constexpr int kRowsWarps = 8;
+constexpr int kRowsWarps = 4;
 constexpr int kRowsThreads = kRowsWarps * 32;
-constexpr int kStepKeys = 16;
-constexpr int kRowsStages = 3;
+constexpr int kRowsPerSm = 3;             // CTAs
+constexpr int kTileKeys = 16;             // rows of one product
+constexpr int kStepKeys = 2 * kTileKeys;
+constexpr int kRowsStages = 2;
 
 template <int DH, int N8>
 struct RowsSmem {
   static constexpr int kTile = 8 * N8;                       // packed rows of a CTA
-  static constexpr int kStep = 2 * kStepKeys * DH + 16;      // K and V bytes of a step, then two scales
+  static constexpr int kStep = 2 * kStepKeys * DH + 16;      // K and V bytes of a step, then four scales
   static constexpr int kRing = kRowsWarps * kRowsStages * kStep;
   static constexpr int kPart = kRowsWarps * kTile * DH * 4;  // warps' outputs, over the ring
   static constexpr int kMain = kRing > kPart ? kRing : kPart;
@@ -59,6 +62,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
                                         uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -107,18 +118,21 @@ __device__ __forceinline__ float column_max(float v) {
   return v;
 }
 
-// Scores y (log2 units; -inf where masked) of keys g, g + 8 and rows 2t, 2t + 1 of every
-// column tile: moves the running maxima m, returns the factors on what was summed before and
+// Scores y (log2 units; -inf where masked) of keys g, g + 8 of U key tiles and rows 2t, 2t + 1
+// of every column tile: moves the running maxima m, returns the factors on what was summed before and
 // the references, and whether any lane of the warp needs the factors.
-template <int N8>
-__device__ __forceinline__ bool move_max(float (&m)[N8][2], const float (&y)[N8][4], float (&ref)[N8][2],
+template <int N8, int U>
+__device__ __forceinline__ bool move_max(float (&m)[N8][2], const float (&y)[U][N8][4], float (&ref)[N8][2],
                                          float (&alpha)[N8][2]) {
   bool moved = false;
 #pragma unroll
   for (int n = 0; n < N8; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float top = column_max(fmaxf(y[n][i], y[n][2 + i]));
+      float top = fmaxf(y[0][n][i], y[0][n][2 + i]);
+#pragma unroll
+      for (int u = 1; u < U; ++u) top = fmaxf(top, fmaxf(y[u][n][i], y[u][n][2 + i]));
+      top = column_max(top);
       alpha[n][i] = 1.f;
       if (top > m[n][i] + 8.f) {            // also the first keys: m is -inf
         alpha[n][i] = ex2_approx(m[n][i] - top);
@@ -131,7 +145,7 @@ __device__ __forceinline__ bool move_max(float (&m)[N8][2], const float (&y)[N8]
 }
 
 template <int DH, int N8>
-__global__ void __launch_bounds__(kRowsThreads, 2)
+__global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
 k_attn_quant_rows(AttnQuantParams p) {
   using SM = RowsSmem<DH, N8>;
   constexpr int TILE = SM::kTile;
@@ -175,10 +189,10 @@ k_attn_quant_rows(AttnQuantParams p) {
   // ---- the ring: copies of step s into a stage (an empty group past the end)
   auto page_of = [&](int s) -> int32_t {                // page of a step
     if (p.block_table == nullptr || s >= step1) return b;
-    return p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + (s >> 3)];
+    return p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + s / (kPageTokens / kStepKeys)];
   };
-  static_assert(kPageTokens == 8 * kStepKeys, "steps of a page");
   const uint32_t my = tc::smem_u32(smem) + warp * kRowsStages * SM::kStep;
+  // a lane's keys: g, g + 8 of a tile for K Q^T, 2t, 2t + 1, 2t + 8, 2t + 9 for V^T P^T
   const int k_lane = g * DH + t4 * 16, v_lane = 2 * t4 * DH + g * EV;
   auto issue = [&](int s, uint32_t st, int32_t page) {
     if (s < step1) {
@@ -191,76 +205,96 @@ k_attn_quant_rows(AttnQuantParams p) {
       const int64_t ph = static_cast<int64_t>(page) * p.Hkv + kvh;
       const int64_t at = (ph * p.page_tokens + place) * DH;
       const int left = static_cast<int>(P - key0);         // keys of the step that exist
-      const uint32_t dk = st + lane * 16, dv = st + kStepKeys * DH + lane * EV;
+      const uint32_t dk = st + lane * 16, dv = st + kTileKeys * DH + lane * EV;
       const uint8_t *ks = p.k_cache + at + k_lane, *vs = p.v_cache + at + v_lane;
       if (left >= kStepKeys) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 4; ++n) {                      // (tile, keys + 0 or + 8)
+          const uint32_t tile = (n >> 1) * 2 * kTileKeys * DH;
 #pragma unroll
-          for (int c = 0; c < KC; ++c) copy_async<16>(dk + (n * KC + c) * 512, ks + n * 8 * DH + c * 64);
+          for (int c = 0; c < KC; ++c) copy_async<16>(dk + tile + ((n & 1) * KC + c) * 512, ks + n * 8 * DH + c * 64);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) copy_async<EV>(dv + j * 32 * EV, vs + ((j & 1) + (j >> 1) * 8) * DH);
+          for (int j = 0; j < 2; ++j) copy_async<EV>(dv + tile + ((n & 1) * 2 + j) * 32 * EV, vs + (n * 8 + j) * DH);
+        }
       } else {                                             // places past the prefix are zeros
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t tile = (n >> 1) * 2 * kTileKeys * DH;
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             const bool ok = n * 8 + g < left;
-            copy_async<16>(dk + (n * KC + c) * 512, ok ? ks + n * 8 * DH + c * 64 : p.k_cache, ok);
+            copy_async<16>(dk + tile + ((n & 1) * KC + c) * 512, ok ? ks + n * 8 * DH + c * 64 : p.k_cache, ok);
           }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool ok = 2 * t4 + (j & 1) + (j >> 1) * 8 < left;
-          copy_async<EV>(dv + j * 32 * EV, ok ? vs + ((j & 1) + (j >> 1) * 8) * DH : p.v_cache, ok);
+          for (int j = 0; j < 2; ++j) {
+            const bool ok = n * 8 + 2 * t4 + j < left;
+            copy_async<EV>(dv + tile + ((n & 1) * 2 + j) * 32 * EV, ok ? vs + (n * 8 + j) * DH : p.v_cache, ok);
+          }
         }
       }
-      if (lane < 2)
-        copy_async<4>(st + 2 * kStepKeys * DH + lane * 4,
-                      (lane == 0 ? p.k_scale : p.v_scale) + ph * p.blocks + (place >> p.sb_log2));
+      if (lane < 4) {                                      // K scales of both tiles, V scales of both
+        const int64_t blk = (place + (lane & 1) * kTileKeys) >> p.sb_log2;
+        copy_async<4>(st + 2 * kStepKeys * DH + lane * 4, (lane < 2 ? p.k_scale : p.v_scale) + ph * p.blocks + min(blk, p.blocks - 1));
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int32_t next_page = page_of(step0);
 #pragma unroll
-  for (int i = 0; i < kRowsStages - 1; ++i) {
+  for (int i = 0; i < kRowsStages; ++i) {
     issue(step0 + i * kRowsWarps, my + i * SM::kStep, next_page);
     next_page = page_of(step0 + (i + 1) * kRowsWarps);
   }
 
-  // ---- Q: lane (g, t) holds row g of every column tile; a power of two per row brings its
-  // largest magnitude into [1, 2). Inner step 4c + i: elements 64c + 16t + 4i .. + 3.
-  uint32_t q[N8][KS][2];
+  // ---- Q: lane (g, t) holds row g of every column tile. A power of two per row brings its
+  // largest magnitude into [128, 256), and each element becomes the sum of two e4m3 numbers:
+  // four significant bits and the four that a bf16 number has left, so exact down to 2^-13
+  // of the row's largest and within 2^-18 of it below.
+  uint32_t q[N8][KS / 4 * 2][4];                     // [8-byte group][words: first part, second part]
   float q_mul[N8][2];
 #pragma unroll
   for (int n = 0; n < N8; ++n) {
     const int row = n * 8 + g, rr = r0 + row;
     const bool ok = row < rows;
     const uint16_t* src = p.q + ((static_cast<int64_t>(b) * NT + (ok ? rr / G : 0)) * p.Hq + kvh * G + (ok ? rr % G : 0)) * DH + t4 * 16;
-    uint32_t raw[KS][2];
-    uint32_t m = 0;
+    uint32_t raw[KC * 2][4];
+    uint32_t top = 0;
 #pragma unroll
     for (int c = 0; c < KC; ++c)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const uint4 x = ok ? *reinterpret_cast<const uint4*>(src + c * 64 + u * 8) : make_uint4(0u, 0u, 0u, 0u);
-        raw[c * 4 + 2 * u][0] = x.x; raw[c * 4 + 2 * u][1] = x.y;
-        raw[c * 4 + 2 * u + 1][0] = x.z; raw[c * 4 + 2 * u + 1][1] = x.w;
+        raw[c * 2 + u][0] = x.x; raw[c * 2 + u][1] = x.y; raw[c * 2 + u][2] = x.z; raw[c * 2 + u][3] = x.w;
       }
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
+    for (int k = 0; k < KC * 2; ++k)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) m = max(m, max((raw[k][h] << 16) & 0x7fff0000u, raw[k][h] & 0x7fff0000u));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t ex = m >> 23;                             // biased exponent; 0, 254 and 255 stay unscaled
-    const bool sc = ex > 0 && ex < 254;
-    const float mul = sc ? __uint_as_float((254 - ex) << 23) : 1.f;
+      for (int h = 0; h < 4; ++h) top = max(top, max((raw[k][h] << 16) & 0x7fff0000u, raw[k][h] & 0x7fff0000u));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // biased exponent of the factor 2^7 / 2^floor(log2 top); rows of zeros and subnormals, whose
+    // factor would pass the largest exponent, take that, and infinities or NaN come out as NaN
+    const int ex = static_cast<int>(top >> 23);
+    const int up = min(254 + 7 - ex, 253);
+    const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
+    for (int k = 0; k < KC * 2; ++k)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        q[n][k][h] = pack_f16(__uint_as_float(raw[k][h] << 16) * mul, __uint_as_float(raw[k][h] & 0xffff0000u) * mul);
-    const float back = (sc ? __uint_as_float(ex << 23) : 1.f) * p.scale_log2;
+      for (int h = 0; h < 2; ++h) {                  // four elements
+        float x[4], y[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[2 * e] = __uint_as_float(raw[k][2 * h + e] << 16) * mul;
+          x[2 * e + 1] = __uint_as_float(raw[k][2 * h + e] & 0xffff0000u) * mul;
+        }
+        if (ex == 255) x[0] = x[1] = x[2] = x[3] = __uint_as_float(0x7fffffffu);
+        const uint32_t a = e4m3x2(x[0], x[1]), c = e4m3x2(x[2], x[3]);
+        e4m3x2_to_f32(a, y[0], y[1]);
+        e4m3x2_to_f32(c, y[2], y[3]);
+        q[n][k][h] = a | c << 16;
+        q[n][k][2 + h] = e4m3x2(x[0] - y[0], x[1] - y[1]) | e4m3x2(x[2] - y[2], x[3] - y[3]) << 16;
+      }
+    const float back = ex == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * p.scale_log2;
     // the accumulator's columns 2t, 2t + 1 are rows held by lanes (2t, .) and (2t + 1, .)
     q_mul[n][0] = __shfl_sync(0xffffffffu, back, t4 * 8);
     q_mul[n][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
@@ -290,7 +324,7 @@ k_attn_quant_rows(AttnQuantParams p) {
       }
   };
 
-  // ---- own-block keys (rank 0), 16 slots a step from the block of the tile's first row
+  // ---- own-block keys (rank 0), one tile of 16 slots a step from the block of the tile's first row
   if (rank == 0) {
     const int t_first = r0 / G, t_last = (r0 + rows - 1) / G;
     const int s_base = t_first / p.Dmax * p.Dmax;
@@ -304,8 +338,8 @@ k_attn_quant_rows(AttnQuantParams p) {
         tr[n][i] = r < rows ? (r0 + r) / G : -1;       // rows past the end see nothing
         lo[n][i] = r < rows ? tr[n][i] / p.Dmax * p.Dmax : 0;
       }
-    for (int s = warp; s * kStepKeys < lim; s += kRowsWarps) {
-      const int slot0 = s_base + s * kStepKeys;
+    for (int s = warp; s * kTileKeys < lim; s += kRowsWarps) {
+      const int slot0 = s_base + s * kTileKeys;
       float c[N8][4] = {};
       // inner step k: elements 16 k + 4 t .. + 3 of a row
 #pragma unroll
@@ -330,7 +364,8 @@ k_attn_quant_rows(AttnQuantParams p) {
           mma_b16(c[n], a[0].x, a[1].x, a[0].y, a[1].y, v.x, v.y);
         }
       }
-      float y[N8][4], ref[N8][2], alpha[N8][2];
+      float yy[1][N8][4], ref[N8][2], alpha[N8][2];
+      float (&y)[N8][4] = yy[0];
 #pragma unroll
       for (int n = 0; n < N8; ++n)
 #pragma unroll
@@ -338,7 +373,7 @@ k_attn_quant_rows(AttnQuantParams p) {
           const int slot = slot0 + (e >> 1) * 8 + g;
           y[n][e] = slot >= lo[n][e & 1] && slot <= tr[n][e & 1] ? c[n][e] * p.scale_log2 : -INFINITY;
         }
-      if (move_max<N8>(m, y, ref, alpha)) rescale(alpha);
+      if (move_max<N8, 1>(m, yy, ref, alpha)) rescale(alpha);
       // values: lane's keys 2t, 2t + 1, 2t + 8, 2t + 9; elements g EV + ..
       uint32_t v[4][EV / 2];
       bool odd_value = false;                          // an infinity or NaN
@@ -382,7 +417,7 @@ k_attn_quant_rows(AttnQuantParams p) {
           // slots of other blocks and of absent tokens may hold anything, and 0 * inf is not
           // 0: key by key, for the rows that see it
 #pragma unroll 1
-          for (int k = 0; k < kStepKeys && slot0 + k <= t_last; ++k) {
+          for (int k = 0; k < kTileKeys && slot0 + k <= t_last; ++k) {
             const uint16_t* src = p.v_cand + ((static_cast<int64_t>(b) * NT + slot0 + k) * p.Hkv + kvh) * DH + g * EV;
             const int from = (k & 7) * 4 + t4;
 #pragma unroll
@@ -402,87 +437,97 @@ k_attn_quant_rows(AttnQuantParams p) {
     }
   }
 
-  // ---- prefix keys
+  // ---- prefix keys, two tiles a step
   int stage = 0;
   for (int s = step0; s < step1; s += kRowsWarps) {
-    {
-      const int ahead = s + (kRowsStages - 1) * kRowsWarps;
-      const int into = stage == 0 ? kRowsStages - 1 : stage - 1;
-      __syncwarp();                                  // the scales in that stage have been read
-      issue(ahead, my + into * SM::kStep, next_page);
-      next_page = page_of(ahead + kRowsWarps);
-    }
     asm volatile("cp.async.wait_group %0;" ::"n"(kRowsStages - 1) : "memory");
-    __syncwarp();                                    // the scales are another lane's copies
+    __syncwarp();                                    // the scales are other lanes' copies
     const uint8_t* st = smem + (warp * kRowsStages + stage) * SM::kStep;
-    stage = stage + 1 == kRowsStages ? 0 : stage + 1;
-    const float2 sc = *reinterpret_cast<const float2*>(st + 2 * kStepKeys * DH);
-    float c[N8][4] = {};
+    const float4 sc = *reinterpret_cast<const float4*>(st + 2 * kStepKeys * DH);
+    float c[2][N8][4];
 #pragma unroll
-    for (int ch = 0; ch < KC; ++ch) {
-      const uint4 k0 = *reinterpret_cast<const uint4*>(st + ch * 512 + lane * 16);
-      const uint4 k1 = *reinterpret_cast<const uint4*>(st + (KC + ch) * 512 + lane * 16);
-      const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a0 = e4m3x2_to_f16x2(w0[i]), a1 = e4m3x2_to_f16x2(w1[i]), a2 = e4m3x2_to_f16x2(w0[i] >> 16),
-                       a3 = e4m3x2_to_f16x2(w1[i] >> 16);
-#pragma unroll
-        for (int n = 0; n < N8; ++n) mma_f16(c[n], a0, a1, a2, a3, q[n][ch * 4 + i][0], q[n][ch * 4 + i][1]);
-      }
-    }
-    const int left = static_cast<int>(P - static_cast<int64_t>(s) * kStepKeys);
-    const float lv = fmaxf(__log2f(sc.y), kLeastVScaleLog2);
-    float y[N8][4], ref[N8][2], alpha[N8][2];
-#pragma unroll
-    for (int n = 0; n < N8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[n][e] = fmaf(c[n][e], q_mul[n][e & 1] * sc.x, lv);
-    if (left < kStepKeys) {
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int n = 0; n < N8; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if ((e >> 1) * 8 + g >= left) y[n][e] = -INFINITY;
-    }
-    if (move_max<N8>(m, y, ref, alpha)) rescale(alpha);
-    const float inv_sv = ex2_approx(-lv);
-    uint32_t pb[N8][2];
+        for (int e = 0; e < 4; ++e) c[u][n][e] = 0.f;
 #pragma unroll
-    for (int n = 0; n < N8; ++n) {
-      float sum[2] = {0.f, 0.f};
+      for (int ch = 0; ch < KC; ++ch) {
+        const uint8_t* kt = st + u * 2 * kTileKeys * DH + lane * 16;
+        const uint4 k0 = *reinterpret_cast<const uint4*>(kt + ch * 512), k1 = *reinterpret_cast<const uint4*>(kt + (KC + ch) * 512);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float w0 = ex2_approx(y[n][2 * h] - ref[n][0]), w1 = ex2_approx(y[n][2 * h + 1] - ref[n][1]);
-        sum[0] += w0;
-        sum[1] += w1;
-        pb[n][h] = transpose8(pack_f16(w0, w1));
-      }
-      l[n][0] = fmaf(sum[0], inv_sv, l[n][0]);
-      l[n][1] = fmaf(sum[1], inv_sv, l[n][1]);
-    }
-    uint32_t v[4][EV / 4];
+        for (int n = 0; n < N8; ++n)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint8_t* src = st + kStepKeys * DH + k * 32 * EV + lane * EV;
-      if constexpr (EV == 16) {
-        const uint4 x = *reinterpret_cast<const uint4*>(src);
-        v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(src);
-        v[k][0] = x.x; v[k][1] = x.y;
+          for (int part = 0; part < 2; ++part) {
+            mma_e4m3(c[u][n], k0.x, k1.x, k0.y, k1.y, q[n][ch * 2][2 * part], q[n][ch * 2][2 * part + 1]);
+            mma_e4m3(c[u][n], k0.z, k1.z, k0.w, k1.w, q[n][ch * 2 + 1][2 * part], q[n][ch * 2 + 1][2 * part + 1]);
+          }
       }
     }
+    const int left = static_cast<int>(P - static_cast<int64_t>(s) * kStepKeys);
+    const float sk[2] = {sc.x, sc.y};
+    const float lv[2] = {fmaxf(__log2f(sc.z), kLeastVScaleLog2), fmaxf(__log2f(sc.w), kLeastVScaleLog2)};
+    float y[2][N8][4], ref[N8][2], alpha[N8][2];
 #pragma unroll
-    for (int j = 0; j < KS; ++j) {
-      // bytes 2j, 2j + 1 of two keys side by side: one pair of codes for each of two elements
-      const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-      const uint32_t c0 = __byte_perm(v[0][j / 2], v[1][j / 2], sel), c1 = __byte_perm(v[2][j / 2], v[3][j / 2], sel);
-      const uint32_t a0 = e4m3x2_to_f16x2(c0), a1 = e4m3x2_to_f16x2(c0 >> 16), a2 = e4m3x2_to_f16x2(c1),
-                     a3 = e4m3x2_to_f16x2(c1 >> 16);
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int n = 0; n < N8; ++n) mma_f16(o[n][j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+      for (int n = 0; n < N8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[u][n][e] = fmaf(c[u][n][e], q_mul[n][e & 1] * sk[u], lv[u]);
+    if (left < kStepKeys) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int n = 0; n < N8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (u * kTileKeys + (e >> 1) * 8 + g >= left) y[u][n][e] = -INFINITY;
     }
+    if (move_max<N8, 2>(m, y, ref, alpha)) rescale(alpha);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float inv_sv = ex2_approx(-lv[u]);
+      uint32_t pb[N8][2];
+#pragma unroll
+      for (int n = 0; n < N8; ++n) {
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float w0 = ex2_approx(y[u][n][2 * h] - ref[n][0]), w1 = ex2_approx(y[u][n][2 * h + 1] - ref[n][1]);
+          sum[0] += w0;
+          sum[1] += w1;
+          pb[n][h] = transpose8(pack_f16(w0, w1));
+        }
+        l[n][0] = fmaf(sum[0], inv_sv, l[n][0]);
+        l[n][1] = fmaf(sum[1], inv_sv, l[n][1]);
+      }
+      uint32_t v[4][EV / 4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint8_t* src = st + (2 * u + 1) * kTileKeys * DH + k * 32 * EV + lane * EV;
+        if constexpr (EV == 16) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src);
+          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(src);
+          v[k][0] = x.x; v[k][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        // bytes 2j, 2j + 1 of two keys side by side: one pair of codes for each of two elements
+        const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+        const uint32_t c0 = __byte_perm(v[0][j / 2], v[1][j / 2], sel), c1 = __byte_perm(v[2][j / 2], v[3][j / 2], sel);
+        const uint32_t a0 = e4m3x2_to_f16x2(c0), a1 = e4m3x2_to_f16x2(c0 >> 16), a2 = e4m3x2_to_f16x2(c1),
+                       a3 = e4m3x2_to_f16x2(c1 >> 16);
+#pragma unroll
+        for (int n = 0; n < N8; ++n) mma_f16(o[n][j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+      }
+    }
+    __syncwarp();                                    // the scales of this stage have been read
+    issue(s + kRowsStages * kRowsWarps, my + stage * SM::kStep, next_page);
+    next_page = page_of(s + (kRowsStages + 1) * kRowsWarps);
+    stage = stage + 1 == kRowsStages ? 0 : stage + 1;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 

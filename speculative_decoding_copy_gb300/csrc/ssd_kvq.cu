@@ -127,10 +127,8 @@ __device__ __forceinline__ void quant_run(const T* __restrict__ src, int64_t str
       uint32_t q[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t f = e4m3x2_to_f16x2(h[i]);
         float lo, hi;
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-            : "=f"(lo), "=f"(hi) : "r"(f));
+        e4m3x2_to_f32(h[i], lo, hi);
         q[i] = e4m3x2(lo * ratio, hi * ratio);
       }
       *p = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);

@@ -22,6 +22,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
   return r;
 }
 
+__device__ __forceinline__ void e4m3x2_to_f32(uint32_t codes, float& lo, float& hi) {
+  const uint32_t f = e4m3x2_to_f16x2(codes);
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(lo), "=f"(hi) : "r"(f));
+}
+
 // bytes [p, p + n) that a call reads or writes
 struct Span {
   const void* p;
