@@ -13,11 +13,12 @@
 // 16-row operand and the packed query rows as the 8-column one (S^T = K Q^T and
 // O^T = V^T P^T, mma.sync), so eight rows, one token of most group sizes, waste
 // nothing; a second column tile serves up to 16 rows. P^T turns from accumulator to operand
-// by one movmatrix for 8 keys. Each lane copies exactly the bytes that its own matrix
-// fragments need (cp.async, 16 bytes, whole 32-byte sectors) into a private ring in shared
-// memory several steps ahead and reads them back itself: no barrier, no transpose. That
-// works because both products may permute an index: for K Q^T lane (g, t) holds elements
-// 16t .. 16t+15 of each 64-element half of keys g and g + 8, and Q is laid out alike; for
+// by one movmatrix for 8 keys. Each warp has a
+// ring of its own in shared memory, filled by one lane's tensor copies of 32 keys ahead of
+// use, and no barrier with other warps. (The same loop with only its copies reads 6.8 TB/s;
+// with 16-byte cp.async of each lane's own fragments 4.8.) Both products may permute an
+// index, so fragments need no transpose: for K Q^T lane (g, t) holds elements
+// 16t .. 16t+15 of each 64-element half of two keys, and Q is laid out alike; for
 // V^T P^T it holds, for its four keys, the dh/8 output elements from dh/8 g on. K Q^T takes the
 // codes as they are (e4m3 products, fp32 sums) against q as a sum of two e4m3 numbers; for
 // V^T P^T they become fp16 exactly, by one conversion for two, against probabilities rounded
@@ -49,14 +50,18 @@ constexpr int kRowsStages = 2;
 template <int DH, int N8>
 struct RowsSmem {
   static constexpr int kTile = 8 * N8;                       // packed rows of a CTA
-  static constexpr int kStep = 2 * kStepKeys * DH + 16;      // K and V bytes of a step, then four scales
+  static constexpr int kStep = 2 * kStepKeys * DH;           // K and V bytes of a step
   static constexpr int kRing = kRowsWarps * kRowsStages * kStep;
   static constexpr int kPart = kRowsWarps * kTile * DH * 4;  // warps' outputs, over the ring
   static constexpr int kMain = kRing > kPart ? kRing : kPart;
+  static constexpr int kScales = kRowsWarps * kRowsStages * 16;    // K scales of a step's tiles, V scales
+  static constexpr int kBars = kRowsWarps * kRowsStages * 8 + 8;   // mbarriers and the failure flag
   static constexpr int kOut = kTile * DH * 4;                // the CTA's merged output
   static constexpr int kStat = (kRowsWarps + 1) * kTile * 2 * 4;   // maxima and sums
-  static constexpr int kBytes = kMain + kOut + kStat;
+  static constexpr int kBytes = kMain + kScales + kBars + kOut + kStat + 1024;   // the base is aligned to 1024
+  static_assert(kStep % 1024 == 0 && kScales % 16 == 0 && kBars % 8 == 0, "alignment");
 };
+constexpr unsigned long long kRowsWaitClocks = 1ull << 32;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -95,14 +100,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
-// N bytes (16, 8 or 4) of global memory to shared memory, zeros when !take
-template <int N>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool take = true) {
-  const int n = take ? N : 0;
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
+// 4 bytes of global memory to shared memory
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ float ld_peer(uint32_t addr) {
@@ -146,14 +146,19 @@ __device__ __forceinline__ bool move_max(float (&m)[N8][2], const float (&y)[U][
 
 template <int DH, int N8>
 __global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
-k_attn_quant_rows(AttnQuantParams p) {
+k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                  AttnQuantParams p) {
   using SM = RowsSmem<DH, N8>;
   constexpr int TILE = SM::kTile;
   constexpr int KS = DH / 16;             // inner steps of K Q^T, and 16-element tiles of the output
   constexpr int EV = DH / 8;              // code bytes of a value row that a lane takes
   constexpr int KC = DH / 64;             // 16-byte chunks of a key row that a lane takes
-  extern __shared__ __align__(16) uint8_t smem[];
-  float* merged = reinterpret_cast<float*>(smem + SM::kMain);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float4* scales = reinterpret_cast<float4*>(smem + SM::kMain);      // [warp][stage]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kMain + SM::kScales);
+  volatile int* failed = reinterpret_cast<volatile int*>(bars + kRowsWarps * kRowsStages);
+  float* merged = reinterpret_cast<float*>(smem + SM::kMain + SM::kScales + SM::kBars);
   float* stat_m = merged + TILE * DH;                        // [warps + 1][rows]
   float* stat_l = stat_m + (kRowsWarps + 1) * TILE;
 
@@ -167,6 +172,13 @@ k_attn_quant_rows(AttnQuantParams p) {
   const int G = p.Hq / p.Hkv, NT = p.NB * p.Dmax;
   const int r0 = blockIdx.y * TILE, rows = min(TILE, NT * G - r0);
 
+  if (tid == 0) {
+    tc::prefetch_tmap(&map_k);
+    tc::prefetch_tmap(&map_v);
+    for (int i = 0; i < kRowsWarps * kRowsStages; ++i) tc::mbar_init(bars + i, 1);
+    *failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -186,63 +198,41 @@ k_attn_quant_rows(AttnQuantParams p) {
   const int step0 = static_cast<int>(static_cast<int64_t>(steps) * rank / S) + warp;
   const int step1 = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / S);
 
-  // ---- the ring: copies of step s into a stage (an empty group past the end)
+  // ---- the ring: step s into a stage, by one lane's tensor copies (K and V of 32 keys; rows
+  // land swizzled) and four lanes' scales (an empty group past the end)
   auto page_of = [&](int s) -> int32_t {                // page of a step
     if (p.block_table == nullptr || s >= step1) return b;
     return p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + s / (kPageTokens / kStepKeys)];
   };
-  const uint32_t my = tc::smem_u32(smem) + warp * kRowsStages * SM::kStep;
-  // a lane's keys: g, g + 8 of a tile for K Q^T, 2t, 2t + 1, 2t + 8, 2t + 9 for V^T P^T
-  const int k_lane = g * DH + t4 * 16, v_lane = 2 * t4 * DH + g * EV;
-  auto issue = [&](int s, uint32_t st, int32_t page) {
-    if (s < step1) {
+  uint8_t* my = smem + warp * kRowsStages * SM::kStep;
+  uint64_t* my_bar = bars + warp * kRowsStages;
+  auto issue = [&](int s, int stage, int32_t page) {
+    if (s < step1 && lane < 4) {
       if (page < 0 || page >= p.num_pages) {
         if (lane == 0) record_error(p.hdr, SSD_ERR_DEVICE, 441);
         page = 0;
       }
-      const int64_t key0 = static_cast<int64_t>(s) * kStepKeys;
-      const int64_t place = p.block_table == nullptr ? key0 : key0 & (kPageTokens - 1);
-      const int64_t ph = static_cast<int64_t>(page) * p.Hkv + kvh;
-      const int64_t at = (ph * p.page_tokens + place) * DH;
-      const int left = static_cast<int>(P - key0);         // keys of the step that exist
-      const uint32_t dk = st + lane * 16, dv = st + kTileKeys * DH + lane * EV;
-      const uint8_t *ks = p.k_cache + at + k_lane, *vs = p.v_cache + at + v_lane;
-      if (left >= kStepKeys) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {                      // (tile, keys + 0 or + 8)
-          const uint32_t tile = (n >> 1) * 2 * kTileKeys * DH;
-#pragma unroll
-          for (int c = 0; c < KC; ++c) copy_async<16>(dk + tile + ((n & 1) * KC + c) * 512, ks + n * 8 * DH + c * 64);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) copy_async<EV>(dv + tile + ((n & 1) * 2 + j) * 32 * EV, vs + (n * 8 + j) * DH);
-        }
-      } else {                                             // places past the prefix are zeros
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint32_t tile = (n >> 1) * 2 * kTileKeys * DH;
-#pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            const bool ok = n * 8 + g < left;
-            copy_async<16>(dk + tile + ((n & 1) * KC + c) * 512, ok ? ks + n * 8 * DH + c * 64 : p.k_cache, ok);
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const bool ok = n * 8 + 2 * t4 + j < left;
-            copy_async<EV>(dv + tile + ((n & 1) * 2 + j) * 32 * EV, ok ? vs + (n * 8 + j) * DH : p.v_cache, ok);
-          }
-        }
+      // rows and blocks of the whole cache are counted in 31 bits
+      const int place = p.block_table == nullptr ? s * kStepKeys : (s * kStepKeys) & (kPageTokens - 1);
+      const int ph = page * p.Hkv + kvh;
+      if (lane == 0) {
+        const int row = ph * static_cast<int>(p.page_tokens) + place;
+        const uint32_t dst = tc::smem_u32(my + stage * SM::kStep);
+        tc::mbar_expect_tx(my_bar + stage, SM::kStep);
+        tc::tma_load_2d(dst, &map_k, 0, row, my_bar + stage);
+        tc::tma_load_2d(dst + kStepKeys * DH, &map_v, 0, row, my_bar + stage);
       }
-      if (lane < 4) {                                      // K scales of both tiles, V scales of both
-        const int64_t blk = (place + (lane & 1) * kTileKeys) >> p.sb_log2;
-        copy_async<4>(st + 2 * kStepKeys * DH + lane * 4, (lane < 2 ? p.k_scale : p.v_scale) + ph * p.blocks + min(blk, p.blocks - 1));
-      }
+      const int blocks = static_cast<int>(p.blocks);
+      const int blk = min((place + (lane & 1) * kTileKeys) >> p.sb_log2, blocks - 1);
+      copy_async4(tc::smem_u32(scales + warp * kRowsStages + stage) + lane * 4,
+                  (lane < 2 ? p.k_scale : p.v_scale) + static_cast<int64_t>(ph) * blocks + blk);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int32_t next_page = page_of(step0);
 #pragma unroll
   for (int i = 0; i < kRowsStages; ++i) {
-    issue(step0 + i * kRowsWarps, my + i * SM::kStep, next_page);
+    issue(step0 + i * kRowsWarps, i, next_page);
     next_page = page_of(step0 + (i + 1) * kRowsWarps);
   }
 
@@ -437,13 +427,34 @@ k_attn_quant_rows(AttnQuantParams p) {
     }
   }
 
-  // ---- prefix keys, two tiles a step
+  // ---- prefix keys, two tiles a step. Which key of eight lane row g takes, and the order in
+  // which lanes read their four value rows, keep the reads of the swizzled rows (16-byte chunk
+  // c of row r lies at chunk c ^ (r & 7) for 128-byte rows, c ^ (r >> 1 & 3) for 64) free of
+  // bank conflicts.
+  const int kap = DH == 128 ? (g >> 1) | ((g & 1) << 2) : g;
+  const int k_at = kap * DH + ((t4 ^ (DH == 128 ? kap : (kap >> 1) & 3)) << 4);
+  const int swap = DH == 128 ? g & 1 : (g >> 1) & 1;
+  int v_at[2];                                       // first and second key of four, as this lane reads them
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = DH == 128 ? t4 + 4 * (k ^ swap) : 2 * t4 + (k ^ swap);
+    v_at[k] = r * DH + (DH == 128 ? (g ^ r) << 4 : (((g >> 1) ^ t4) << 4) + (g & 1) * 8);
+  }
+  const uint32_t sel[2] = {swap ? 0x1504u : 0x5140u, swap ? 0x3726u : 0x7362u};
   int stage = 0;
+  uint32_t parity = 0;
   for (int s = step0; s < step1; s += kRowsWarps) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kRowsStages - 1) : "memory");
+    if (!mbar_wait_bounded(my_bar + stage, parity, failed, p.hdr, 442, kRowsWaitClocks)) break;
     __syncwarp();                                    // the scales are other lanes' copies
-    const uint8_t* st = smem + (warp * kRowsStages + stage) * SM::kStep;
-    const float4 sc = *reinterpret_cast<const float4*>(st + 2 * kStepKeys * DH);
+    uint8_t* st = my + stage * SM::kStep;
+    const float4 sc = scales[warp * kRowsStages + stage];
+    const int left = static_cast<int>(P - static_cast<int64_t>(s) * kStepKeys);
+    if (left < kStepKeys) {                          // codes past the prefix may be NaN: 0 * NaN is not 0
+      for (int i = left * (DH / 16) + lane; i < kStepKeys * (DH / 16); i += 32)
+        reinterpret_cast<uint4*>(st + kStepKeys * DH)[i] = make_uint4(0u, 0u, 0u, 0u);
+      __syncwarp();
+    }
     float c[2][N8][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -453,8 +464,8 @@ k_attn_quant_rows(AttnQuantParams p) {
         for (int e = 0; e < 4; ++e) c[u][n][e] = 0.f;
 #pragma unroll
       for (int ch = 0; ch < KC; ++ch) {
-        const uint8_t* kt = st + u * 2 * kTileKeys * DH + lane * 16;
-        const uint4 k0 = *reinterpret_cast<const uint4*>(kt + ch * 512), k1 = *reinterpret_cast<const uint4*>(kt + (KC + ch) * 512);
+        const uint8_t* kt = st + u * kTileKeys * DH + (k_at ^ (ch * 64));
+        const uint4 k0 = *reinterpret_cast<const uint4*>(kt), k1 = *reinterpret_cast<const uint4*>(kt + 8 * DH);
 #pragma unroll
         for (int n = 0; n < N8; ++n)
 #pragma unroll
@@ -464,7 +475,6 @@ k_attn_quant_rows(AttnQuantParams p) {
           }
       }
     }
-    const int left = static_cast<int>(P - static_cast<int64_t>(s) * kStepKeys);
     const float sk[2] = {sc.x, sc.y};
     const float lv[2] = {fmaxf(__log2f(sc.z), kLeastVScaleLog2), fmaxf(__log2f(sc.w), kLeastVScaleLog2)};
     float y[2][N8][4], ref[N8][2], alpha[N8][2];
@@ -481,7 +491,7 @@ k_attn_quant_rows(AttnQuantParams p) {
         for (int n = 0; n < N8; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (u * kTileKeys + (e >> 1) * 8 + g >= left) y[u][n][e] = -INFINITY;
+            if (u * kTileKeys + (e >> 1) * 8 + kap >= left) y[u][n][e] = -INFINITY;
     }
     if (move_max<N8, 2>(m, y, ref, alpha)) rescale(alpha);
 #pragma unroll
@@ -504,7 +514,7 @@ k_attn_quant_rows(AttnQuantParams p) {
       uint32_t v[4][EV / 4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint8_t* src = st + (2 * u + 1) * kTileKeys * DH + k * 32 * EV + lane * EV;
+        const uint8_t* src = st + (kStepKeys + u * kTileKeys + (k >> 1) * 8) * DH + v_at[k & 1];
         if constexpr (EV == 16) {
           const uint4 x = *reinterpret_cast<const uint4*>(src);
           v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
@@ -516,20 +526,28 @@ k_attn_quant_rows(AttnQuantParams p) {
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
         // bytes 2j, 2j + 1 of two keys side by side: one pair of codes for each of two elements
-        const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-        const uint32_t c0 = __byte_perm(v[0][j / 2], v[1][j / 2], sel), c1 = __byte_perm(v[2][j / 2], v[3][j / 2], sel);
+        const uint32_t c0 = __byte_perm(v[0][j / 2], v[1][j / 2], sel[j & 1]), c1 = __byte_perm(v[2][j / 2], v[3][j / 2], sel[j & 1]);
         const uint32_t a0 = e4m3x2_to_f16x2(c0), a1 = e4m3x2_to_f16x2(c0 >> 16), a2 = e4m3x2_to_f16x2(c1),
                        a3 = e4m3x2_to_f16x2(c1 >> 16);
 #pragma unroll
         for (int n = 0; n < N8; ++n) mma_f16(o[n][j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
       }
     }
-    __syncwarp();                                    // the scales of this stage have been read
-    issue(s + kRowsStages * kRowsWarps, my + stage * SM::kStep, next_page);
+    __syncwarp();                                    // this stage has been read
+    issue(s + kRowsStages * kRowsWarps, stage, next_page);
     next_page = page_of(s + (kRowsStages + 1) * kRowsWarps);
-    stage = stage + 1 == kRowsStages ? 0 : stage + 1;
+    if (++stage == kRowsStages) {
+      stage = 0;
+      parity ^= 1;
+    }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  if (*failed) {
+    // a wait gave up: the copies still in flight write this CTA's shared memory, so give them
+    // as long again before anything else does
+    int one_more = 0;
+    for (int i = 0; i < kRowsStages; ++i) mbar_wait_bounded(my_bar + i, i >= stage ? parity : parity ^ 1, &one_more, p.hdr, 443, kRowsWaitClocks);
+  }
 
   // ---- merge the warps
 #pragma unroll
@@ -604,7 +622,7 @@ k_attn_quant_rows(AttnQuantParams p) {
         v = fmaf(ld_peer(tc::map_peer(so + e * 4, c)), f, v);
       }
     }
-    if (tt % p.Dmax < p.blk_len[b * p.NB + tt / p.Dmax]) {
+    if (!*failed && tt % p.Dmax < p.blk_len[b * p.NB + tt / p.Dmax]) {
       const int64_t at = ((static_cast<int64_t>(b) * NT + tt) * p.Hq + kvh * G + rr % G) * DH + e % DH;
       const float out = v / L;
       if (p.out_f32) static_cast<float*>(p.out)[at] = out;
@@ -651,6 +669,19 @@ static int validate(const ssd_attn_quant_args* a) {
   return SSD_OK;
 }
 
+// rows of dh codes, `box` of them a copy, swizzled over their whole length
+static bool codes_map(CUtensorMap* map, const void* base, uint64_t rows, int dh, int box_rows) {
+  tc::EncodeTiledFn enc = tc::encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(dh), rows > 0 ? rows : 1};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(dh)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(dh), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, dh == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DH, int N8>
 static int rows_launch(const AttnQuantParams& p, int rows, cudaStream_t s) {
   using SM = RowsSmem<DH, N8>;
@@ -670,6 +701,12 @@ static int rows_launch(const AttnQuantParams& p, int rows, cudaStream_t s) {
   int S = 1;
   const char* env = getenv("SSD_S"); const int cap = env ? atoi(env) : 4 * 304;
   while (S < 8 && S * 2 <= most && groups * S < cap) S *= 2;
+  const uint64_t cache_rows = static_cast<uint64_t>(p.num_pages) * p.Hkv * p.page_tokens;
+  CUtensorMap map_k, map_v;
+  // an empty cache is never read, but a map needs an address and a row
+  const void *kb = cache_rows > 0 ? p.k_cache : static_cast<const void*>(p.q), *vb = cache_rows > 0 ? p.v_cache : kb;
+  if (!codes_map(&map_k, kb, cache_rows, DH, kStepKeys) || !codes_map(&map_v, vb, cache_rows, DH, kStepKeys))
+    return SSD_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.Hkv * S), static_cast<unsigned>(mtiles), 1);
   cfg.blockDim = dim3(kRowsThreads);
@@ -684,7 +721,7 @@ static int rows_launch(const AttnQuantParams& p, int rows, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, k_attn_quant_rows<DH, N8>, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, k_attn_quant_rows<DH, N8>, map_k, map_v, p) != cudaSuccess) {
     cudaGetLastError();
     return SSD_ERR_CUDA;
   }
