@@ -30,7 +30,6 @@
 // rank 0 adds the own-block keys (bf16 products, probabilities as a sum of two bf16). Warps
 // and then CTAs merge maxima, sums and outputs in a fixed order through shared memory.
 #include <math.h>
-#include <stdlib.h>
 
 #include <algorithm>
 #include <mutex>
@@ -40,26 +39,31 @@
 
 namespace ssd {
 
-constexpr int kRowsWarps = 4;
-constexpr int kRowsThreads = kRowsWarps * 32;
-constexpr int kRowsPerSm = 3;             // CTAs
 constexpr int kTileKeys = 16;             // rows of one product
-constexpr int kStepKeys = 2 * kTileKeys;
-constexpr int kRowsStages = 2;
+constexpr int kStepKeys = 2 * kTileKeys;  // keys of a warp's step
+constexpr int kMaxRanks = 16;             // CTAs of a cluster
 
-template <int DH, int N8>
-struct RowsSmem {
+// DH: head dim; N8: column tiles of eight packed rows; W: warps of a CTA; ST: steps in its
+// rings; PER_SM: CTAs of an SM
+template <int DH_, int N8_, int W_, int ST_, int PER_SM_>
+struct RowsConfig {
+  static constexpr int DH = DH_, N8 = N8_, W = W_, ST = ST_, PER_SM = PER_SM_;
+  static constexpr int kThreads = W * 32;
   static constexpr int kTile = 8 * N8;                       // packed rows of a CTA
   static constexpr int kStep = 2 * kStepKeys * DH;           // K and V bytes of a step
-  static constexpr int kRing = kRowsWarps * kRowsStages * kStep;
-  static constexpr int kPart = kRowsWarps * kTile * DH * 4;  // warps' outputs, over the ring
-  static constexpr int kMain = kRing > kPart ? kRing : kPart;
-  static constexpr int kScales = kRowsWarps * kRowsStages * 16;    // K scales of a step's tiles, V scales
-  static constexpr int kBars = kRowsWarps * kRowsStages * 8 + 8;   // mbarriers and the failure flag
-  static constexpr int kOut = kTile * DH * 4;                // the CTA's merged output
-  static constexpr int kStat = (kRowsWarps + 1) * kTile * 2 * 4;   // maxima and sums
-  static constexpr int kBytes = kMain + kScales + kBars + kOut + kStat + 1024;   // the base is aligned to 1024
-  static_assert(kStep % 1024 == 0 && kScales % 16 == 0 && kBars % 8 == 0, "alignment");
+  static constexpr int kWarpRing = ST * kStep;               // later the warp's output [row][DH] fp32
+  static constexpr int kRing = W * kWarpRing;
+  static constexpr int kScales = W * ST * 16;                // K scales of a step's tiles, V scales
+  static constexpr int kBars = W * ST * 8 + 16;              // mbarriers, the failure flag, the sequence
+  static constexpr int kStat = W * kTile * 8;                // maxima and sums of the warps
+  static constexpr int kPeerStat = kMaxRanks * kTile * 8;    // ... of the cluster's CTAs
+  static constexpr int kPeerOut = (kTile * DH + 4 * kMaxRanks) * 4;   // this CTA's share of their outputs
+  static constexpr int OFF_SCALES = kRing, OFF_BARS = OFF_SCALES + kScales, OFF_STAT = OFF_BARS + kBars,
+                       OFF_PEER_STAT = OFF_STAT + kStat, OFF_PEER_OUT = OFF_PEER_STAT + kPeerStat,
+                       OFF_HERE = OFF_PEER_OUT + kPeerOut;
+  static constexpr int kBytes = OFF_HERE + 16 + 1024;        // the base is aligned to 1024
+  static_assert(kStep % 1024 == 0 && kTile * DH * 4 <= kWarpRing, "ring");
+  static_assert(OFF_BARS % 16 == 0 && OFF_STAT % 16 == 0 && OFF_PEER_OUT % 16 == 0, "alignment");
 };
 constexpr unsigned long long kRowsWaitClocks = 1ull << 32;
 
@@ -105,12 +109,6 @@ __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ float ld_peer(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 // over the eight lanes that hold one column of an accumulator
 __device__ __forceinline__ float column_max(float v) {
 #pragma unroll
@@ -144,23 +142,24 @@ __device__ __forceinline__ bool move_max(float (&m)[N8][2], const float (&y)[U][
   return __any_sync(0xffffffffu, moved);
 }
 
-template <int DH, int N8>
-__global__ void __launch_bounds__(kRowsThreads, kRowsPerSm)
+template <typename C>
+__global__ void __launch_bounds__(C::kThreads, C::PER_SM)
 k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                   AttnQuantParams p) {
-  using SM = RowsSmem<DH, N8>;
-  constexpr int TILE = SM::kTile;
+  constexpr int DH = C::DH, N8 = C::N8, W = C::W, ST = C::ST, TILE = C::kTile;
   constexpr int KS = DH / 16;             // inner steps of K Q^T, and 16-element tiles of the output
   constexpr int EV = DH / 8;              // code bytes of a value row that a lane takes
   constexpr int KC = DH / 64;             // 16-byte chunks of a key row that a lane takes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float4* scales = reinterpret_cast<float4*>(smem + SM::kMain);      // [warp][stage]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kMain + SM::kScales);
-  volatile int* failed = reinterpret_cast<volatile int*>(bars + kRowsWarps * kRowsStages);
-  float* merged = reinterpret_cast<float*>(smem + SM::kMain + SM::kScales + SM::kBars);
-  float* stat_m = merged + TILE * DH;                        // [warps + 1][rows]
-  float* stat_l = stat_m + (kRowsWarps + 1) * TILE;
+  float4* scales = reinterpret_cast<float4*>(smem + C::OFF_SCALES);  // [warp][stage]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+  volatile int* failed = reinterpret_cast<volatile int*>(bars + W * ST);
+  volatile int* chosen = failed + 1;
+  float2* stat = reinterpret_cast<float2*>(smem + C::OFF_STAT);            // [warp][row]: maximum, sum
+  float2* peer_stat = reinterpret_cast<float2*>(smem + C::OFF_PEER_STAT);  // [rank][row]
+  float4* peer_out = reinterpret_cast<float4*>(smem + C::OFF_PEER_OUT);    // [rank][share]
+  uint8_t* present = smem + C::OFF_HERE;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
@@ -168,28 +167,66 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(S));
   const int bk = blockIdx.x / S;
-  const int b = bk / p.Hkv, kvh = bk % p.Hkv;
+  int b = bk / p.Hkv;
+  const int kvh = bk % p.Hkv;
   const int G = p.Hq / p.Hkv, NT = p.NB * p.Dmax;
   const int r0 = blockIdx.y * TILE, rows = min(TILE, NT * G - r0);
 
   if (tid == 0) {
     tc::prefetch_tmap(&map_k);
     tc::prefetch_tmap(&map_v);
-    for (int i = 0; i < kRowsWarps * kRowsStages; ++i) tc::mbar_init(bars + i, 1);
+    for (int i = 0; i < W * ST; ++i) tc::mbar_init(bars + i, 1);
     *failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // every CTA of the cluster runs before one writes to another's shared memory (waited for
+  // before the merge)
+  if (S > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  if (p.longest_first) {
+    // the CTAs of the longest prefixes start first, so that none of them is left for the end
+    int* lens = reinterpret_cast<int*>(smem);
+    const int mine = tid < p.B ? p.prefix_len[tid] : -1;
+    lens[tid] = mine;
+    __syncthreads();
+    int before = 0;
+    for (int i = 0; i < p.B; ++i) before += lens[i] > mine || (lens[i] == mine && i < tid) ? 1 : 0;
+    if (tid < p.B && before == b) *chosen = tid;
+    __syncthreads();
+    b = *chosen;
+  }
   int64_t P = p.prefix_len[b];
   // present rows of the tile; the CTAs of a cluster hold the same rows and leave together
   bool here = false;
   if (tid < rows) {
     const int tt = (r0 + tid) / G;
     here = tt % p.Dmax < p.blk_len[b * p.NB + tt / p.Dmax];
+    present[tid] = here ? 1 : 0;
   }
-  if (!__syncthreads_or(here)) return;
+  // rows of Q, and on rank 0 the first tile of own-block slots: loads that wait for nothing
+  const int t_first = r0 / G, t_last = (r0 + rows - 1) / G;
+  const int s_base = t_first / p.Dmax * p.Dmax;
+  uint32_t raw[N8][KC * 2][4];
+#pragma unroll
+  for (int n = 0; n < N8; ++n) {
+    const int row = n * 8 + g, rr = r0 + row;
+    const bool ok = row < rows;
+    const uint16_t* src = p.q + ((static_cast<int64_t>(b) * NT + (ok ? rr / G : 0)) * p.Hq + kvh * G + (ok ? rr % G : 0)) * DH + t4 * 16;
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint4 x = ok ? *reinterpret_cast<const uint4*>(src + c * 64 + u * 8) : make_uint4(0u, 0u, 0u, 0u);
+        raw[n][c * 2 + u][0] = x.x; raw[n][c * 2 + u][1] = x.y; raw[n][c * 2 + u][2] = x.z; raw[n][c * 2 + u][3] = x.w;
+      }
+  }
+  const bool any_here = __syncthreads_or(here);
+  if (!any_here) {
+    if (S > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
+    return;
+  }
   if (P < 0 || P > p.capacity) {
     if (tid == 0) record_error(p.hdr, SSD_ERR_DEVICE, 440);
     P = 0;
@@ -204,8 +241,8 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     if (p.block_table == nullptr || s >= step1) return b;
     return p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + s / (kPageTokens / kStepKeys)];
   };
-  uint8_t* my = smem + warp * kRowsStages * SM::kStep;
-  uint64_t* my_bar = bars + warp * kRowsStages;
+  uint8_t* my = smem + warp * C::kWarpRing;
+  uint64_t* my_bar = bars + warp * ST;
   auto issue = [&](int s, int stage, int32_t page) {
     if (s < step1 && lane < 4) {
       if (page < 0 || page >= p.num_pages) {
@@ -217,23 +254,23 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       const int ph = page * p.Hkv + kvh;
       if (lane == 0) {
         const int row = ph * static_cast<int>(p.page_tokens) + place;
-        const uint32_t dst = tc::smem_u32(my + stage * SM::kStep);
-        tc::mbar_expect_tx(my_bar + stage, SM::kStep);
+        const uint32_t dst = tc::smem_u32(my + stage * C::kStep);
+        tc::mbar_expect_tx(my_bar + stage, C::kStep);
         tc::tma_load_2d(dst, &map_k, 0, row, my_bar + stage);
         tc::tma_load_2d(dst + kStepKeys * DH, &map_v, 0, row, my_bar + stage);
       }
       const int blocks = static_cast<int>(p.blocks);
       const int blk = min((place + (lane & 1) * kTileKeys) >> p.sb_log2, blocks - 1);
-      copy_async4(tc::smem_u32(scales + warp * kRowsStages + stage) + lane * 4,
+      copy_async4(tc::smem_u32(scales + warp * ST + stage) + lane * 4,
                   (lane < 2 ? p.k_scale : p.v_scale) + static_cast<int64_t>(ph) * blocks + blk);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int32_t next_page = page_of(step0);
 #pragma unroll
-  for (int i = 0; i < kRowsStages; ++i) {
-    issue(step0 + i * kRowsWarps, i, next_page);
-    next_page = page_of(step0 + (i + 1) * kRowsWarps);
+  for (int i = 0; i < ST; ++i) {
+    issue(step0 + i * W, i, next_page);
+    next_page = page_of(step0 + (i + 1) * W);
   }
 
   // ---- Q: lane (g, t) holds row g of every column tile. A power of two per row brings its
@@ -244,22 +281,11 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   float q_mul[N8][2];
 #pragma unroll
   for (int n = 0; n < N8; ++n) {
-    const int row = n * 8 + g, rr = r0 + row;
-    const bool ok = row < rows;
-    const uint16_t* src = p.q + ((static_cast<int64_t>(b) * NT + (ok ? rr / G : 0)) * p.Hq + kvh * G + (ok ? rr % G : 0)) * DH + t4 * 16;
-    uint32_t raw[KC * 2][4];
     uint32_t top = 0;
-#pragma unroll
-    for (int c = 0; c < KC; ++c)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint4 x = ok ? *reinterpret_cast<const uint4*>(src + c * 64 + u * 8) : make_uint4(0u, 0u, 0u, 0u);
-        raw[c * 2 + u][0] = x.x; raw[c * 2 + u][1] = x.y; raw[c * 2 + u][2] = x.z; raw[c * 2 + u][3] = x.w;
-      }
 #pragma unroll
     for (int k = 0; k < KC * 2; ++k)
 #pragma unroll
-      for (int h = 0; h < 4; ++h) top = max(top, max((raw[k][h] << 16) & 0x7fff0000u, raw[k][h] & 0x7fff0000u));
+      for (int h = 0; h < 4; ++h) top = max(top, max((raw[n][k][h] << 16) & 0x7fff0000u, raw[n][k][h] & 0x7fff0000u));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     // biased exponent of the factor 2^7 / 2^floor(log2 top); rows of zeros and subnormals, whose
@@ -274,8 +300,8 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         float x[4], y[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          x[2 * e] = __uint_as_float(raw[k][2 * h + e] << 16) * mul;
-          x[2 * e + 1] = __uint_as_float(raw[k][2 * h + e] & 0xffff0000u) * mul;
+          x[2 * e] = __uint_as_float(raw[n][k][2 * h + e] << 16) * mul;
+          x[2 * e + 1] = __uint_as_float(raw[n][k][2 * h + e] & 0xffff0000u) * mul;
         }
         if (ex == 255) x[0] = x[1] = x[2] = x[3] = __uint_as_float(0x7fffffffu);
         const uint32_t a = e4m3x2(x[0], x[1]), c = e4m3x2(x[2], x[3]);
@@ -316,8 +342,6 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 
   // ---- own-block keys (rank 0), one tile of 16 slots a step from the block of the tile's first row
   if (rank == 0) {
-    const int t_first = r0 / G, t_last = (r0 + rows - 1) / G;
-    const int s_base = t_first / p.Dmax * p.Dmax;
     const int lim = t_last + 1 - s_base;
     int tr[N8][2], lo[N8][2];                          // slot of a row and first slot of its block
 #pragma unroll
@@ -328,8 +352,23 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         tr[n][i] = r < rows ? (r0 + r) / G : -1;       // rows past the end see nothing
         lo[n][i] = r < rows ? tr[n][i] / p.Dmax * p.Dmax : 0;
       }
-    for (int s = warp; s * kTileKeys < lim; s += kRowsWarps) {
+    for (int s = warp; s * kTileKeys < lim; s += W) {
       const int slot0 = s_base + s * kTileKeys;
+      // values: lane's keys 2t, 2t + 1, 2t + 8, 2t + 9; elements g EV + ..
+      uint32_t v[4][EV / 2];
+      bool odd_value = false;                          // an infinity or NaN
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int slot = slot0 + 2 * t4 + (k & 1) + (k >> 1) * 8;
+        const bool ok = slot <= t_last;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.v_cand + ((static_cast<int64_t>(b) * NT + (ok ? slot : t_last)) * p.Hkv + kvh) * DH + g * EV);
+#pragma unroll
+        for (int u = 0; u < EV / 8; ++u) {
+          const uint4 x = ok ? src[u] : make_uint4(0u, 0u, 0u, 0u);
+          v[k][4 * u] = x.x; v[k][4 * u + 1] = x.y; v[k][4 * u + 2] = x.z; v[k][4 * u + 3] = x.w;
+        }
+      }
       float c[N8][4] = {};
       // inner step k: elements 16 k + 4 t .. + 3 of a row
 #pragma unroll
@@ -364,24 +403,11 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           y[n][e] = slot >= lo[n][e & 1] && slot <= tr[n][e & 1] ? c[n][e] * p.scale_log2 : -INFINITY;
         }
       if (move_max<N8, 1>(m, yy, ref, alpha)) rescale(alpha);
-      // values: lane's keys 2t, 2t + 1, 2t + 8, 2t + 9; elements g EV + ..
-      uint32_t v[4][EV / 2];
-      bool odd_value = false;                          // an infinity or NaN
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int slot = slot0 + 2 * t4 + (k & 1) + (k >> 1) * 8;
-        const bool ok = slot <= t_last;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.v_cand + ((static_cast<int64_t>(b) * NT + (ok ? slot : t_last)) * p.Hkv + kvh) * DH + g * EV);
-#pragma unroll
-        for (int u = 0; u < EV / 8; ++u) {
-          const uint4 x = ok ? src[u] : make_uint4(0u, 0u, 0u, 0u);
-          v[k][4 * u] = x.x; v[k][4 * u + 1] = x.y; v[k][4 * u + 2] = x.z; v[k][4 * u + 3] = x.w;
-        }
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int u = 0; u < EV / 2; ++u)
           odd_value |= (v[k][u] & 0x7f800000u) == 0x7f800000u || (v[k][u] & 0x7f80u) == 0x7f80u;
-      }
       odd_value = __any_sync(0xffffffffu, odd_value);
 #pragma unroll
       for (int n = 0; n < N8; ++n) {
@@ -443,12 +469,12 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   const uint32_t sel[2] = {swap ? 0x1504u : 0x5140u, swap ? 0x3726u : 0x7362u};
   int stage = 0;
   uint32_t parity = 0;
-  for (int s = step0; s < step1; s += kRowsWarps) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRowsStages - 1) : "memory");
+  for (int s = step0; s < step1; s += W) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
     if (!mbar_wait_bounded(my_bar + stage, parity, failed, p.hdr, 442, kRowsWaitClocks)) break;
     __syncwarp();                                    // the scales are other lanes' copies
-    uint8_t* st = my + stage * SM::kStep;
-    const float4 sc = scales[warp * kRowsStages + stage];
+    uint8_t* st = my + stage * C::kStep;
+    const float4 sc = scales[warp * ST + stage];
     const int left = static_cast<int>(P - static_cast<int64_t>(s) * kStepKeys);
     if (left < kStepKeys) {                          // codes past the prefix may be NaN: 0 * NaN is not 0
       for (int i = left * (DH / 16) + lane; i < kStepKeys * (DH / 16); i += 32)
@@ -534,9 +560,9 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       }
     }
     __syncwarp();                                    // this stage has been read
-    issue(s + kRowsStages * kRowsWarps, stage, next_page);
-    next_page = page_of(s + (kRowsStages + 1) * kRowsWarps);
-    if (++stage == kRowsStages) {
+    issue(s + ST * W, stage, next_page);
+    next_page = page_of(s + (ST + 1) * W);
+    if (++stage == ST) {
       stage = 0;
       parity ^= 1;
     }
@@ -546,94 +572,91 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     // a wait gave up: the copies still in flight write this CTA's shared memory, so give them
     // as long again before anything else does
     int one_more = 0;
-    for (int i = 0; i < kRowsStages; ++i) mbar_wait_bounded(my_bar + i, i >= stage ? parity : parity ^ 1, &one_more, p.hdr, 443, kRowsWaitClocks);
+    for (int i = 0; i < ST; ++i) mbar_wait_bounded(my_bar + i, i >= stage ? parity : parity ^ 1, &one_more, p.hdr, 443, kRowsWaitClocks);
   }
 
-  // ---- merge the warps
-#pragma unroll
-  for (int n = 0; n < N8; ++n)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float x = l[n][i];
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      l[n][i] = x;
-      if (g == 0) {
-        stat_m[warp * TILE + n * 8 + 2 * t4 + i] = m[n][i];
-        stat_l[warp * TILE + n * 8 + 2 * t4 + i] = x;
-      }
-    }
-  __syncthreads();                                   // also: every ring is idle
-  float* part = reinterpret_cast<float*>(smem);      // [warp][row][DH]
+  // ---- merge the warps: each leaves its output in its own ring
 #pragma unroll
   for (int n = 0; n < N8; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = n * 8 + 2 * t4 + i;
-      if (r >= rows) continue;
-      float M = -INFINITY;
+      float x = l[n][i];
 #pragma unroll
-      for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, stat_m[w * TILE + r]);
-      // a warp without keys has l = 0 and o = 0; a NaN score leaves m and makes l NaN
-      const float f = m[n][i] == -INFINITY ? 1.f : ex2_approx(m[n][i] - M);
-      float* dst = part + (warp * TILE + r) * DH + g * EV;
+      for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+      if (g == 0) stat[warp * TILE + r] = make_float2(m[n][i], x);
+      if (r < rows) {
+        float* dst = reinterpret_cast<float*>(my) + r * DH + g * EV;
 #pragma unroll
-      for (int j = 0; j < KS; j += 2)
-        *reinterpret_cast<float4*>(dst + 2 * j) =
-            make_float4(o[n][j][i] * f, o[n][j][2 + i] * f, o[n][j + 1][i] * f, o[n][j + 1][2 + i] * f);
+        for (int j = 0; j < KS; j += 2)
+          *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[n][j][i], o[n][j][2 + i], o[n][j + 1][i], o[n][j + 1][2 + i]);
+      }
     }
-  if (tid < rows) {
-    float M = -INFINITY, L = 0.f;
-    for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, stat_m[w * TILE + tid]);
-    for (int w = 0; w < kRowsWarps; ++w) {
-      const float mw = stat_m[w * TILE + tid], lw = stat_l[w * TILE + tid];
-      L += mw == -INFINITY ? lw : lw * ex2_approx(mw - M);
-    }
-    stat_m[kRowsWarps * TILE + tid] = M;
-    stat_l[kRowsWarps * TILE + tid] = L;
-  }
   __syncthreads();
-  for (int e = tid; e < rows * DH; e += kRowsThreads) {
-    float v = 0.f;
+  // parts of a row are summed under their common maximum. A part without keys has maximum -inf, sum 0 and output 0; a NaN
+  // score leaves the maximum and makes the sum NaN.
+  const int quads = rows * (DH / 4), share = (quads + static_cast<int>(S) - 1) / static_cast<int>(S);
+  auto store = [&](int e, float4 v, float L) {
+    const int row = e / (DH / 4), rr = r0 + row, tt = rr / G;
+    if (*failed || !present[row]) return;
+    const int64_t at = ((static_cast<int64_t>(b) * NT + tt) * p.Hq + kvh * G + rr % G) * DH + e % (DH / 4) * 4;
+    const float inv = __frcp_rn(L);
+    v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;
+    else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(tc::pack_bf16(v.x, v.y), tc::pack_bf16(v.z, v.w));
+  };
+  auto add = [&](float4& v, float f, const float4& x) {
+    v = make_float4(fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w));
+  };
+  if (S > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
+  for (int e = tid; e < quads; e += C::kThreads) {
+    const int row = e / (DH / 4);
+    float2 st[W];
+    float M = -INFINITY, L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRowsWarps; ++w) v += part[w * TILE * DH + e];
-    merged[e] = v;
-  }
-  // ---- merge the CTAs of the cluster: each takes a share of the elements
-  if (S > 1) tc::cluster_sync(); else __syncthreads();
-  const uint32_t sm = tc::smem_u32(stat_m + kRowsWarps * TILE), sl = tc::smem_u32(stat_l + kRowsWarps * TILE),
-                 so = tc::smem_u32(merged);
-  for (int e = static_cast<int>(rank) * kRowsThreads + tid; e < rows * DH; e += static_cast<int>(S) * kRowsThreads) {
-    const int row = e / DH;
-    const int rr = r0 + row, tt = rr / G;
-    float v, L;
+    for (int w = 0; w < W; ++w) {
+      st[w] = stat[w * TILE + row];
+      M = fmaxf(M, st[w].x);
+    }
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = st[w].x == -INFINITY ? 1.f : ex2_approx(st[w].x - M);
+      L = fmaf(f, st[w].y, L);
+      add(v, f, reinterpret_cast<const float4*>(smem + w * C::kWarpRing)[e]);
+    }
     if (S == 1) {
-      v = merged[e];
-      L = stat_l[kRowsWarps * TILE + row];
+      store(e, v, L);
     } else {
-      float M = -INFINITY;
-      for (uint32_t c = 0; c < S; ++c) M = fmaxf(M, ld_peer(tc::map_peer(sm + row * 4, c)));
-      v = 0.f;
-      L = 0.f;
-      for (uint32_t c = 0; c < S; ++c) {
-        const float mc = ld_peer(tc::map_peer(sm + row * 4, c));
-        const float f = mc == -INFINITY ? 1.f : ex2_approx(mc - M);
-        L = fmaf(ld_peer(tc::map_peer(sl + row * 4, c)), f, L);
-        v = fmaf(ld_peer(tc::map_peer(so + e * 4, c)), f, v);
-      }
-    }
-    if (!*failed && tt % p.Dmax < p.blk_len[b * p.NB + tt / p.Dmax]) {
-      const int64_t at = ((static_cast<int64_t>(b) * NT + tt) * p.Hq + kvh * G + rr % G) * DH + e % DH;
-      const float out = v / L;
-      if (p.out_f32) static_cast<float*>(p.out)[at] = out;
-      else {
-        uint16_t h;
-        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(out));
-        static_cast<uint16_t*>(p.out)[at] = h;
+      // to the CTA that owns this element, and the row's maximum and sum to every CTA
+      const int to = e / share;
+      const uint32_t dst = tc::map_peer(tc::smem_u32(peer_out + rank * share + (e - to * share)), to);
+      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                   : "memory");
+      const int c = e % (DH / 4);
+      if (c < static_cast<int>(S)) {
+        const uint32_t ds = tc::map_peer(tc::smem_u32(peer_stat + rank * TILE + row), c);
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(ds), "f"(M), "f"(L) : "memory");
       }
     }
   }
-  if (S > 1) tc::cluster_sync();                     // a CTA's shared memory outlives its readers
+  if (S == 1) return;
+  tc::cluster_sync();                                // from here on only this CTA's own memory is read
+  for (int i = tid; i < share; i += C::kThreads) {
+    const int e = static_cast<int>(rank) * share + i;
+    if (e >= quads) break;
+    const int row = e / (DH / 4);
+    float M = -INFINITY, L = 0.f;
+    for (uint32_t c = 0; c < S; ++c) M = fmaxf(M, peer_stat[c * TILE + row].x);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t c = 0; c < S; ++c) {
+      const float2 st = peer_stat[c * TILE + row];
+      const float f = st.x == -INFINITY ? 1.f : ex2_approx(st.x - M);
+      L = fmaf(f, st.y, L);
+      add(v, f, peer_out[c * share + i]);
+    }
+    store(e, v, L);
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -682,35 +705,84 @@ static bool codes_map(CUtensorMap* map, const void* base, uint64_t rows, int dh,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DH, int N8>
-static int rows_launch(const AttnQuantParams& p, int rows, cudaStream_t s) {
-  using SM = RowsSmem<DH, N8>;
-  const int mtiles = (rows + SM::kTile - 1) / SM::kTile;
-  static std::once_flag once[kMaxDevices];
-  static cudaError_t err[kMaxDevices];
+// Kernel attributes, once a device, and how many clusters of S CTAs are resident at once.
+template <typename C>
+static int rows_resident(int S) {
+  static std::mutex mu;
+  static bool ready[kMaxDevices];
+  static int found[kMaxDevices][kMaxRanks + 1];
   const int dev = current_device();
-  if (dev < 0) return SSD_ERR_CUDA;
-  std::call_once(once[dev], [dev] {
-    err[dev] = cudaFuncSetAttribute(k_attn_quant_rows<DH, N8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes);
-  });
-  if (err[dev] != cudaSuccess) return SSD_ERR_CUDA;
-  // CTAs that split a sequence: enough to fill the GPU several times over (their lengths
-  // differ), no more than one for each 128 keys of the longest sequence the cache can hold
-  const long long groups = static_cast<long long>(p.B) * p.Hkv * mtiles;
-  const long long most = std::max<long long>(1, (p.capacity + 127) / 128);
-  int S = 1;
-  const char* env = getenv("SSD_S"); const int cap = env ? atoi(env) : 4 * 304;
-  while (S < 8 && S * 2 <= most && groups * S < cap) S *= 2;
+  if (dev < 0) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!ready[dev]) {
+    if (cudaFuncSetAttribute(k_attn_quant_rows<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(k_attn_quant_rows<C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    for (int n = 1; n <= kMaxRanks; ++n) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(n), 1, 1);
+      cfg.blockDim = dim3(C::kThreads);
+      cfg.dynamicSmemBytes = C::kBytes;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = static_cast<unsigned>(n);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int count = 0;
+      if (cudaOccupancyMaxActiveClusters(&count, k_attn_quant_rows<C>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        count = 0;
+      }
+      found[dev][n] = count;
+    }
+    ready[dev] = true;
+  }
+  return found[dev][S];
+}
+
+// CTAs that split a sequence, at most `most`. A CTA takes its share of the longest sequence's
+// steps and 6 beside them; the waves of resident clusters, at least one, and half of one for
+// the end, where CTAs run out (the longest started first), are to cost least. Over 2k-8k prefixes
+// of 8 kv heads it takes 4, 3 and 2 for 16, 32 and 64 sequences, the fastest of 1 .. 8 each
+// time (36.8, 60.6 and 117.3 us; with 1: 69.1, 90.1 and 119.4, with 8: 44.7, 85.0 and 163.4).
+template <typename C>
+static int rows_split(long long groups, long long keys, int most) {
+  const double iters = static_cast<double>(std::max<long long>(1, (keys + C::W * kStepKeys - 1) / (C::W * kStepKeys)));
+  int best = 0;
+  double cost = 0;
+  for (int S = 1; S <= most && S <= iters; ++S) {
+    const int clusters = rows_resident<C>(S);
+    if (clusters <= 0) continue;
+    const double waves = static_cast<double>(groups) / clusters, cta = iters / S + 6.;
+    const double c = cta * (std::max(waves, 1.) + 0.5 * std::min(waves, 1.));
+    if (best == 0 || c < cost) {
+      cost = c;
+      best = S;
+    }
+  }
+  return best;
+}
+
+template <typename C>
+static int rows_launch(const AttnQuantParams& p, int rows, int S, cudaStream_t s) {
+  if (S < 1 || rows_resident<C>(S) <= 0) return SSD_ERR_CUDA;
   const uint64_t cache_rows = static_cast<uint64_t>(p.num_pages) * p.Hkv * p.page_tokens;
   CUtensorMap map_k, map_v;
   // an empty cache is never read, but a map needs an address and a row
   const void *kb = cache_rows > 0 ? p.k_cache : static_cast<const void*>(p.q), *vb = cache_rows > 0 ? p.v_cache : kb;
-  if (!codes_map(&map_k, kb, cache_rows, DH, kStepKeys) || !codes_map(&map_v, vb, cache_rows, DH, kStepKeys))
+  if (!codes_map(&map_k, kb, cache_rows, C::DH, kStepKeys) || !codes_map(&map_v, vb, cache_rows, C::DH, kStepKeys))
     return SSD_ERR_CUDA;
+  AttnQuantParams q = p;
+  q.longest_first = p.B > 1 && p.B <= C::kThreads ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.Hkv * S), static_cast<unsigned>(mtiles), 1);
-  cfg.blockDim = dim3(kRowsThreads);
-  cfg.dynamicSmemBytes = SM::kBytes;
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.Hkv * S),
+                     static_cast<unsigned>((rows + C::kTile - 1) / C::kTile), 1);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -721,12 +793,24 @@ static int rows_launch(const AttnQuantParams& p, int rows, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, k_attn_quant_rows<DH, N8>, map_k, map_v, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, k_attn_quant_rows<C>, map_k, map_v, q) != cudaSuccess) {
     cudaGetLastError();
     return SSD_ERR_CUDA;
   }
   count_launch();
   return check_launch();
+}
+
+template <int DH, int N8>
+static int rows_choose(const AttnQuantParams& p, int rows, cudaStream_t s) {
+  // Few sequences: latency counts, so eight warps and up to 16 CTAs share each (a token over
+  // 4096 keys of 8 kv heads: 8.6 us, with the other shape 11.0). Many: three CTAs of an SM
+  // keep it reading while one starts or ends; sixteen rows need the registers of two.
+  using Few = RowsConfig<DH, N8, 8, 3, 1>;
+  using Many = RowsConfig<DH, N8, 4, N8 == 1 ? 2 : 3, N8 == 1 ? 3 : 2>;
+  const long long groups = static_cast<long long>(p.B) * p.Hkv * ((rows + 8 * N8 - 1) / (8 * N8));
+  if (groups * 8 <= 152) return rows_launch<Few>(p, rows, rows_split<Few>(groups, p.capacity, kMaxRanks), s);
+  return rows_launch<Many>(p, rows, rows_split<Many>(groups, p.capacity, 8), s);
 }
 
 }  // namespace ssd
@@ -769,6 +853,6 @@ extern "C" int ssd_verify_attn_quant(const ssd_attn_quant_args* a, void* ws, siz
   const int rows = a->NB * a->Dmax * (a->Hq / a->Hkv);
   KernelTimer timer(SSD_KERNEL_VERIFY_ATTN, s);
   // eight rows or sixteen in a CTA
-  if (a->dh == 128) return rows <= 8 ? rows_launch<128, 1>(p, rows, s) : rows_launch<128, 2>(p, rows, s);
-  return rows <= 8 ? rows_launch<64, 1>(p, rows, s) : rows_launch<64, 2>(p, rows, s);
+  if (a->dh == 128) return rows <= 8 ? rows_choose<128, 1>(p, rows, s) : rows_choose<128, 2>(p, rows, s);
+  return rows <= 8 ? rows_choose<64, 1>(p, rows, s) : rows_choose<64, 2>(p, rows, s);
 }

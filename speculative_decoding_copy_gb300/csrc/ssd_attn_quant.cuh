@@ -22,6 +22,7 @@ struct AttnQuantParams {
   int sb_log2;                  // tokens of a scale block, log2
   int out_f32;
   float scale_log2;             // softmax scale times log2(e)
+  int longest_first;            // CTAs in the order of the prefix lengths
   int64_t capacity;             // most prefix tokens
   int64_t page_tokens;          // tokens of one page, P_max of a contiguous cache
   int64_t num_pages;            // B of a contiguous cache
