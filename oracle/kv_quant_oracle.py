@@ -146,10 +146,11 @@ def values(codes, scale, sb, prefix, table=None):
     return out
 
 
-def attention(q, k, v, k_cand, v_cand, blk_len, Dmax, slots=None, scale=None):
+def attention(q, k, v, k_cand, v_cand, blk_len, Dmax, slots=None, scale=None, probs=None):
     """Verification attention of the present tokens over cached rows k, v (from values()), all
     fp64. Returns {(b, t): (out [Hq][dh], spread [Hq][dh])}, where spread is
-    sum_j p_j |v_j|, the size that relative errors of the probabilities act on."""
+    sum_j p_j |v_j|, the size that relative errors of the probabilities act on. A dict `probs`
+    receives {(b, t): [(p [G][keys], v [keys][dh]) for each kv head]}."""
     B, NT, Hq, dh = q.shape
     Hkv = k_cand.shape[2]
     G = Hq // Hkv
@@ -170,5 +171,7 @@ def attention(q, k, v, k_cand, v_cand, blk_len, Dmax, slots=None, scale=None):
                 p = e / e.sum(1, keepdims=True)
                 out[h * G:(h + 1) * G] = p @ vv
                 size[h * G:(h + 1) * G] = p @ np.abs(vv)
+                if probs is not None:
+                    probs.setdefault((b, t), []).append((p, vv))
             res[b, t] = (out, size)
     return res

@@ -32,6 +32,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "ssd_attn_quant.cuh"
@@ -746,11 +747,14 @@ static int rows_resident(int S) {
 
 // CTAs that split a sequence, at most `most`. A CTA takes its share of the longest sequence's
 // steps and 6 beside them; the waves of resident clusters, at least one, and half of one for
-// the end, where CTAs run out (the longest started first), are to cost least. Over 2k-8k prefixes
+// the end, where CTAs run out (the longest started first), are to cost least. A sequence or
+// two (`even`) leave nothing short for a second wave, which then costs as much as the first
+// (one sequence of 32768 keys: 20.1 us by 12 CTAs, 31.3 by 16, of which one cluster of eight
+// waits). Over 2k-8k prefixes
 // of 8 kv heads it takes 4, 3 and 2 for 16, 32 and 64 sequences, the fastest of 1 .. 8 each
 // time (36.8, 60.6 and 117.3 us; with 1: 69.1, 90.1 and 119.4, with 8: 44.7, 85.0 and 163.4).
 template <typename C>
-static int rows_split(long long groups, long long keys, int most) {
+static int rows_split(long long groups, long long keys, int most, bool even) {
   const double iters = static_cast<double>(std::max<long long>(1, (keys + C::W * kStepKeys - 1) / (C::W * kStepKeys)));
   int best = 0;
   double cost = 0;
@@ -758,7 +762,7 @@ static int rows_split(long long groups, long long keys, int most) {
     const int clusters = rows_resident<C>(S);
     if (clusters <= 0) continue;
     const double waves = static_cast<double>(groups) / clusters, cta = iters / S + 6.;
-    const double c = cta * (std::max(waves, 1.) + 0.5 * std::min(waves, 1.));
+    const double c = cta * (even ? std::ceil(waves) : std::max(waves, 1.) + 0.5 * std::min(waves, 1.));
     if (best == 0 || c < cost) {
       cost = c;
       best = S;
@@ -809,8 +813,8 @@ static int rows_choose(const AttnQuantParams& p, int rows, cudaStream_t s) {
   using Few = RowsConfig<DH, N8, 8, 3, 1>;
   using Many = RowsConfig<DH, N8, 4, N8 == 1 ? 2 : 3, N8 == 1 ? 3 : 2>;
   const long long groups = static_cast<long long>(p.B) * p.Hkv * ((rows + 8 * N8 - 1) / (8 * N8));
-  if (groups * 8 <= 152) return rows_launch<Few>(p, rows, rows_split<Few>(groups, p.capacity, kMaxRanks), s);
-  return rows_launch<Many>(p, rows, rows_split<Many>(groups, p.capacity, 8), s);
+  if (groups * 8 <= 152) return rows_launch<Few>(p, rows, rows_split<Few>(groups, p.capacity, kMaxRanks, true), s);
+  return rows_launch<Many>(p, rows, rows_split<Many>(groups, p.capacity, 8, false), s);
 }
 
 }  // namespace ssd
@@ -852,6 +856,7 @@ extern "C" int ssd_verify_attn_quant(const ssd_attn_quant_args* a, void* ws, siz
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int rows = a->NB * a->Dmax * (a->Hq / a->Hkv);
   KernelTimer timer(SSD_KERNEL_VERIFY_ATTN, s);
+  if (rows > 32 && attn_quant_tc_applies(p, a->dh)) return attn_quant_tc_launch(p, s);
   // eight rows or sixteen in a CTA
   if (a->dh == 128) return rows <= 8 ? rows_choose<128, 1>(p, rows, s) : rows_choose<128, 2>(p, rows, s);
   return rows <= 8 ? rows_choose<64, 1>(p, rows, s) : rows_choose<64, 2>(p, rows, s);

@@ -32,4 +32,8 @@ struct AttnQuantParams {
 
 constexpr float kLeastVScaleLog2 = -100.f;     // a smaller v scale counts as this
 
+// tensor-core path for many rows (ssd_attn_quant_tc.cu)
+bool attn_quant_tc_applies(const AttnQuantParams& p, int dh);
+int attn_quant_tc_launch(const AttnQuantParams& p, cudaStream_t s);
+
 }  // namespace ssd

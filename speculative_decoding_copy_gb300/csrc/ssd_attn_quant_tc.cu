@@ -1,0 +1,976 @@
+// Attention over the 8-bit cache for many packed rows, head dim 128, on the tensor cores
+// (tcgen05): a verification of many candidate tokens. The mathematics is that of
+// ssd_attn_quant.cu; what differs is who does the products.
+//
+// Precision on e4m3 operands. The codes go into the products as they lie in the cache
+// (kind::f8f6f4, fp32 sums). Q and P, which have more bits, are sums of two e4m3 numbers, one
+// product each into the same accumulator: q (8 significant bits) splits exactly, down to 2^-17
+// of its row's largest; a probability keeps 8 bits (as bf16 would), with an absolute floor of
+// 2^-14 of the largest. Two e4m3 products cost what one bf16 product costs, and no code is
+// converted. (Converting each tile to fp16 in shared memory would move 64 KB more per tile
+// through shared memory, which the products already keep three quarters busy.)
+//
+// Rows. The G query heads of the present tokens pack into rows (absent tokens take none, so a
+// batch with few present candidates runs few row tiles); a CTA owns 128 of them and one share
+// of the prefix, the S CTAs of a row tile form a cluster, rank 0 also takes the own-block keys
+// (bf16, masked), and the shares are merged on chip.
+//
+// Per CTA (384 threads, one CTA per SM, all 512 TMEM columns):
+//   warps 0-3  one thread per row: its Q into shared memory (two e4m3 parts, swizzled; rank 0
+//              also bf16), then the online softmax of each 128-key tile read from TMEM: per 16
+//              keys one K factor, one log2 of the V factor and one weight 1/sv of the sum. P
+//              goes back to TMEM over the first half of the tile's S buffer (two parts of 32
+//              columns, four keys a word; bf16 pairs for own-block tiles). In fp16 with the
+//              exponent offset of the two formats taken into the exponential, the first part is
+//              the upper byte of a probability's bits and the second the rounded upper byte of
+//              what is left, so no format conversion is needed;
+//   warp 4     TMEM allocation, then the producer of the K tiles;
+//   warp 6     the producer of the V tiles; it clears the value rows past the prefix (codes
+//              there may be NaN, and 0 * NaN is not 0);
+//   warp 5     the MMA-issuing thread, S three tiles ahead of the softmax;
+//   warps 6-11 add threads to the merge.
+// Shared memory: Q (64 KB), then four 16 KB slots each for K and V. A prefix tile takes one
+// slot of each, an own-block tile (bf16) two.
+// TMEM columns: S buffers 0-127, 128-255, 256-383, O 384-511.
+// The merge is that of ssd_attn_tc.cu: rows as 16-bit integers with a power-of-two scale per
+// 64 columns, one bulk copy to each CTA that owns rows.
+// Waits are bounded; on expiry the CTA records SSD_ERR_TIMEOUT, skips what is left and exits
+// through the cluster barriers.
+#include <cuda.h>
+#include <math.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "ssd_attn_quant.cuh"
+#include "ssd_tc.cuh"
+
+namespace ssd {
+namespace qtc {
+
+using namespace tc;
+
+constexpr int DH = 128;
+constexpr int BM = 128;                   // packed rows per CTA
+constexpr int BN = 128;                   // keys per tile
+constexpr int SLOTS = 4;                  // ring slots of K, and of V
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr int SBUF = 3;
+constexpr uint32_t TM_S = 0, TM_O = SBUF * BN;
+constexpr uint32_t P2 = BN / 4;           // columns from a probability's first part to its second
+constexpr uint32_t kSlot = 16384;         // 128 rows of 128 bytes, 128-byte swizzle
+constexpr uint32_t OFF_Q8 = 0;            // two parts
+constexpr uint32_t OFF_QB = 2 * kSlot;    // bf16, two 64-column halves
+constexpr uint32_t OFF_K = 4 * kSlot;
+constexpr uint32_t OFF_V = OFF_K + SLOTS * kSlot;
+constexpr uint32_t OFF_BAR = OFF_V + SLOTS * kSlot;
+constexpr uint32_t kBarBytes = 1024;
+constexpr uint32_t kSmemBytes = OFF_BAR + kBarBytes + 1024;   // + slack to align the base to 1024
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+constexpr unsigned long long kWaitClocks = 1ull << 32;
+constexpr int kMaxSplit = 8;
+constexpr int kCleaners = 5;              // warps 7-11
+constexpr int kRowB = 2 * DH + 16;        // one share's partial row as sent to its owner
+constexpr int kMaxBlocks = 8192;          // NB: the block ends are kept in the ring at first
+static_assert((2 * BM + kMaxSplit) * kRowB <= static_cast<int>(2 * SLOTS * kSlot), "merge buffers fit in the ring");
+static_assert(kMaxBlocks * 4 <= static_cast<int>(2 * SLOTS * kSlot), "block ends fit in the ring");
+
+struct Bars {
+  uint64_t full_k[SLOTS], full_v[SLOTS], empty_k[SLOTS], empty_v[SLOTS];
+  uint64_t q_full;
+  uint64_t s_full[SBUF], p_full[SBUF], pv_done[2];
+  uint64_t v_clean;                       // the value rows past the prefix are zeros
+  uint64_t own_clean[2];                  // an own-block tile's values are finite
+  uint64_t recv_full;
+  uint32_t tmem_base;
+  int failed;
+  int odd_own;                            // an own-block value was not finite
+  int seq, rows;                          // the sequence; its present rows
+  int row_slot[BM];                       // candidate slot of a row of this tile
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
+
+__device__ __forceinline__ bool mbar_wait(Bars& bars, uint64_t* bar, uint32_t parity, WsHeader* hdr, int where) {
+  return mbar_wait_bounded(bar, parity, &bars.failed, hdr, where, kWaitClocks);
+}
+
+// instruction descriptor, kind::f8f6f4: e4m3 A and B, fp32 D, M = 128, N = n
+__host__ __device__ constexpr uint32_t idesc_e4m3(bool b_mn_major, uint32_t n) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// A in TMEM: M rows on the lanes, four K elements a column
+__device__ __forceinline__ void mma_e4m3_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// merged rows travel as 16-bit integers, two a word
+__device__ __forceinline__ uint32_t pack_i16(float x0, float x1, float s) {
+  const uint32_t a = __float_as_uint(fmaf(x0, s, 12582912.f)), b = __float_as_uint(fmaf(x1, s, 12582912.f));
+  return __byte_perm(a, b, 0x5410);
+}
+__device__ __forceinline__ float2 unpack_i16(uint32_t w) {
+  const uint32_t f = w ^ 0x80008000u;
+  return make_float2(__uint_as_float(__byte_perm(f, 0x4B000000u, 0x7610)) - 8421376.f,
+                     __uint_as_float(__byte_perm(f, 0x4B000000u, 0x7632)) - 8421376.f);
+}
+
+// ------------------------------------------------------------------ softmax pieces
+// Probabilities carry a factor 16 against their reference and may grow by another 16 before
+// the reference moves: at most 2^8, under e4m3's 448.
+constexpr float kLift = 4.f, kLag = 4.f;
+
+// the factors of four groups of 16 keys (64 columns)
+struct Groups {
+  float k[4];      // score to log2 units
+  float lv[4];     // log2 of the V factor
+  float w[4];      // weight of the group's sum: 1 / V factor
+};
+
+__device__ __forceinline__ void load64(uint32_t taddr, uint32_t* v) {
+  tmem_ld32(taddr, v);
+  tmem_ld32(taddr + 32, v + 32);
+  tmem_wait_ld();
+}
+
+// largest y of the columns [lo, hi) of 64 (MASK), or of all
+template <bool MASK>
+__device__ __forceinline__ float chunk_max(uint32_t taddr, const Groups& f, int lo, int hi) {
+  uint32_t v[64];
+  load64(taddr, v);
+  float top = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int c = 16 * q; c < 16 * q + 16; c += 2) {
+      const float x = __uint_as_float(v[c]), y = __uint_as_float(v[c + 1]);
+      if (!MASK || (c >= lo && c < hi)) a = fmaxf(a, x);
+      if (!MASK || (c + 1 >= lo && c + 1 < hi)) b = fmaxf(b, y);
+    }
+    a = fmaxf(a, b);
+    if (!MASK || a > -INFINITY) top = fmaxf(top, fmaf(a, f.k[q], f.lv[q]));   // an empty group's factors may be anything
+  }
+  return top;
+}
+
+// prefix tile: 2^(y - ref + lift) as two e4m3 parts, four keys a word, at paddr and paddr + P2;
+// returns the sum weighted by 1 / V factor
+template <bool MASK>
+__device__ __forceinline__ float chunk_parts(uint32_t saddr, uint32_t paddr, const Groups& f, int hi, float ref) {
+  uint32_t v[64];
+  load64(saddr, v);
+  uint32_t p1[16], p2[16];
+  float total = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    // fp16 bits of p * 2^-8 are, from bit 7 up, the bits of p's e4m3 number
+    const float off = f.lv[q] - ref + (kLift - 8.f);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int c = 16 * q; c < 16 * q + 16; c += 4) {
+      uint32_t t1[2], t2[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = ex2_approx(fmaf(__uint_as_float(v[c + 2 * h]), f.k[q], off));
+        float y = ex2_approx(fmaf(__uint_as_float(v[c + 2 * h + 1]), f.k[q], off));
+        if (MASK) {
+          if (c + 2 * h >= hi) x = 0.f;
+          if (c + 2 * h + 1 >= hi) y = 0.f;
+        }
+        s0 += x;
+        s1 += y;
+        uint32_t w, left;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(left) : "r"(w), "r"(w & 0xff80ff80u));
+        t1[h] = w + w;                              // the first part in each upper byte
+        t2[h] = left + left + 0x00800080u;          // the rest, rounded
+      }
+      p1[c / 4] = __byte_perm(t1[0], t1[1], 0x7531);
+      p2[c / 4] = __byte_perm(t2[0], t2[1], 0x7531);
+    }
+    const float s = s0 + s1;
+    if (!MASK || 16 * q < hi) total = fmaf(s, f.w[q], total);
+  }
+  tmem_st16(paddr, p1);
+  tmem_st16(paddr + P2, p2);
+  return total * 256.f;
+}
+
+// own-block tile: 2^(y - ref + lift) as bf16 pairs over the columns [lo, hi); returns the sum
+// of the rounded values
+__device__ __forceinline__ float chunk_pairs(uint32_t saddr, uint32_t paddr, float k, int lo, int hi, float ref) {
+  uint32_t v[64];
+  load64(saddr, v);
+  uint32_t pk[32];
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+  for (int c = 0; c < 64; c += 2) {
+    float x = ex2_approx(fmaf(__uint_as_float(v[c]), k, kLift - ref)), y = ex2_approx(fmaf(__uint_as_float(v[c + 1]), k, kLift - ref));
+    if (c < lo || c >= hi) x = 0.f;
+    if (c + 1 < lo || c + 1 >= hi) y = 0.f;
+    const uint32_t w = pack_bf16(x, y);
+    pk[c / 2] = w;
+    s0 += __uint_as_float(w << 16);
+    s1 += __uint_as_float(w & 0xffff0000u);
+  }
+  tmem_st32(paddr, pk);
+  return s0 + s1;
+}
+
+// ------------------------------------------------------------------ kernel
+// grid (S, row tiles, B*Hkv), cluster (S, 1, 1)
+__global__ void __launch_bounds__(kThreads, 1)
+k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                const __grid_constant__ CUtensorMap tmap_kc, const __grid_constant__ CUtensorMap tmap_vc,
+                AttnQuantParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  Bars& bars = *reinterpret_cast<Bars*>(smem + OFF_BAR);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int S = static_cast<int>(gridDim.x);
+  const int r0 = blockIdx.y * BM;
+  const int kvh = blockIdx.z % p.Hkv;
+  const int G = p.Hq / p.Hkv;
+  const int NT = p.NB * p.Dmax;
+  int b = blockIdx.z / p.Hkv;
+
+  if (warp == 4 && lane == 0) {
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+  }
+  if (tid == 32) {
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(&bars.full_k[s], 1);
+      mbar_init(&bars.full_v[s], 1);
+      mbar_init(&bars.empty_k[s], 1);
+      mbar_init(&bars.empty_v[s], 1);
+    }
+    mbar_init(&bars.q_full, BM);
+    mbar_init(&bars.recv_full, 1);
+    mbar_init(&bars.v_clean, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.own_clean[i], kCleaners);
+    for (int i = 0; i < SBUF; ++i) {
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_full[i], BM);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.pv_done[i], 1);
+    bars.failed = 0;
+    bars.odd_own = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (p.longest_first) {
+    // the CTAs of the longest prefixes start first
+    int* lens = reinterpret_cast<int*>(smem);
+    const int mine = tid < p.B ? p.prefix_len[tid] : -1;
+    lens[tid] = mine;
+    __syncthreads();
+    int before = 0;
+    for (int i = 0; i < p.B; ++i) before += lens[i] > mine || (lens[i] == mine && i < tid) ? 1 : 0;
+    if (tid < p.B && before == b) bars.seq = tid;
+    __syncthreads();
+    b = bars.seq;
+  }
+  // ends of the blocks in the list of present tokens, by one warp
+  int* ends = reinterpret_cast<int*>(smem + OFF_K);
+  if (warp == 0) {
+    int sum = 0;
+    for (int k0 = 0; k0 < p.NB; k0 += 32) {
+      const int k = k0 + lane;
+      int n = k < p.NB ? min(max(p.blk_len[static_cast<int64_t>(b) * p.NB + k], 0), p.Dmax) : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) n += up;
+      }
+      if (k < p.NB) ends[k] = sum + n;
+      sum += __shfl_sync(0xffffffffu, n, 31);
+    }
+    if (lane == 0) bars.rows = sum * G;
+  }
+  int P = p.prefix_len[b];
+  if (P < 0 || P > p.capacity) {
+    if (tid == 0) record_error(p.hdr, SSD_ERR_DEVICE, 450);
+    P = 0;
+  }
+  __syncthreads();
+  const int rows_total = bars.rows;
+  if (r0 >= rows_total) return;            // every CTA of the cluster
+  const int rv = min(BM, rows_total - r0);
+  if (tid < BM) {
+    // slot of this row's token: the block whose end is the first above its number
+    const int i = (r0 + min(tid, rv - 1)) / G;
+    int lo = 0, hi = p.NB - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (ends[mid] > i) hi = mid; else lo = mid + 1;
+    }
+    bars.row_slot[tid] = lo * p.Dmax + i - (lo > 0 ? ends[lo - 1] : 0);
+  }
+  if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();                         // the block ends have been read: the ring may be filled
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+
+  // candidate slots of this row tile: from its first token's block on
+  const int s_base = bars.row_slot[0] / p.Dmax * p.Dmax;
+  const int s_end = bars.row_slot[rv - 1] + 1;
+  const int own_tiles = (s_end - s_base + BN - 1) / BN;
+  const int nC = rank == 0 ? own_tiles : 0;
+  // prefix tiles of this rank; rank 0 takes two fewer for each own-block tile (masked: about
+  // twice the work of a prefix tile)
+  const int T = (P + BN - 1) / BN;
+  int j0 = 0, j1 = T;
+  if (S > 1) {
+    const int first = min(T, max(0, (T + 2 * own_tiles + S - 1) / S - 2 * own_tiles)), rest = T - first;
+    j0 = rank == 0 ? 0 : first + rest * (rank - 1) / (S - 1);
+    j1 = rank == 0 ? first : first + rest * rank / (S - 1);
+  }
+  const int nP = j1 - j0, nT = nC + nP;
+  const bool ragged = nP > 0 && j1 * BN > P;             // the last tile ends past the prefix
+  // rows merged by this CTA: [rb, rb + nr)
+  const int rpc = (rv + S - 1) / S;
+  const int rb = rank * rpc, nr = max(0, min(rv, rb + rpc) - rb);
+  float m = -INFINITY, l = 0.f;            // reference maximum (log2 units) and sum of a softmax row
+
+  if (warp < 4) {
+    // ---------------------------------------------------------- rows
+    const bool row_ok = tid < rv;
+    const int slot = bars.row_slot[tid];
+    const int c_lo = slot / p.Dmax * p.Dmax;
+    // Q: a power of two brings the row's largest magnitude into [128, 256); two e4m3 parts
+    float q_mul;
+    {
+      uint4 raw[16];
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + ((static_cast<int64_t>(b) * NT + slot) * p.Hq + kvh * G + (r0 + tid) % G) * DH);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) raw[i] = row_ok ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+      }
+      const int ex = static_cast<int>(top >> 23);
+      const int up = min(254 + 7 - ex, 253);
+      const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
+      q_mul = ex == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * p.scale_log2;
+      const uint32_t row_at = tid * 128, sw = tid & 7;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {                      // 16 elements
+        uint32_t part[2][4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {                    // four of them
+          const uint4& r = raw[2 * i + (h >> 1)];
+          const uint32_t w[2] = {(h & 1) ? r.z : r.x, (h & 1) ? r.w : r.y};
+          float x[4], y[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x[2 * e] = __uint_as_float(w[e] << 16) * mul;
+            x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u) * mul;
+          }
+          if (ex == 255) x[0] = x[1] = x[2] = x[3] = __uint_as_float(0x7fffffffu);
+          const uint32_t lo = e4m3x2(x[0], x[1]), hi = e4m3x2(x[2], x[3]);
+          e4m3x2_to_f32(lo, y[0], y[1]);
+          e4m3x2_to_f32(hi, y[2], y[3]);
+          part[0][h] = lo | hi << 16;
+          part[1][h] = e4m3x2(x[0] - y[0], x[1] - y[1]) | e4m3x2(x[2] - y[2], x[3] - y[3]) << 16;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          *reinterpret_cast<uint4*>(smem + OFF_Q8 + u * kSlot + row_at + ((i ^ sw) << 4)) =
+              make_uint4(part[u][0], part[u][1], part[u][2], part[u][3]);
+      }
+      if (nC > 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          *reinterpret_cast<uint4*>(smem + OFF_QB + (i >> 3) * kSlot + row_at + (((i & 7) ^ sw) << 4)) = raw[i];
+      }
+      fence_async_smem();
+      mbar_arrive(&bars.q_full);
+    }
+    // scales of a prefix tile: lane i < 8 holds the K scale of the tile's group i, lane 8 + i the
+    // V scale; loaded a tile ahead
+    auto load_scale = [&](int j) -> float {
+      if (j >= nT || j < nC || lane >= 16) return 0.f;
+      const int tile = j0 + (j - nC);
+      int ph, place;
+      if (p.block_table != nullptr) {
+        int pg = p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + tile];
+        if (pg < 0 || pg >= p.num_pages) pg = 0;
+        ph = pg * p.Hkv + kvh;
+        place = (lane & 7) * 16;
+      } else {
+        ph = b * p.Hkv + kvh;
+        place = tile * BN + (lane & 7) * 16;
+      }
+      const int blocks = static_cast<int>(p.blocks);
+      const int blk = min(place >> p.sb_log2, blocks - 1);
+      return (lane < 8 ? p.k_scale : p.v_scale)[static_cast<int64_t>(ph) * blocks + blk];
+    };
+    float next_scale = load_scale(0);
+    for (int j = 0; j < nT; ++j) {
+      const int sb = j % SBUF;
+      const bool own = j < nC;
+      // lanes 0-7: K factor; 8-15: log2 of the V factor
+      const float sc = next_scale;
+      const float lane_f = lane < 8 ? sc : fmaxf(__log2f(sc), kLeastVScaleLog2);
+      const float lane_w = ex2_approx(-lane_f);          // lanes 8-15: 1 / V factor
+      next_scale = load_scale(j + 1);
+      mbar_wait(bars, &bars.s_full[sb], (j / SBUF) & 1, p.hdr, 460);
+      tc_fence_after();
+      int v_lo = 0, v_hi;
+      if (own) {
+        const int s0 = s_base + j * BN;
+        v_lo = row_ok ? c_lo - s0 : BN;
+        v_hi = row_ok ? slot + 1 - s0 : 0;
+      } else {
+        v_hi = P - (j0 + (j - nC)) * BN;
+      }
+      const bool full = !own && v_hi >= BN;
+      const uint32_t sp = tmem + TM_S + sb * BN + lane_off;
+      Groups f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float k = __shfl_sync(0xffffffffu, lane_f, 4 * h + q), lv = __shfl_sync(0xffffffffu, lane_f, 8 + 4 * h + q),
+                      w = __shfl_sync(0xffffffffu, lane_w, 8 + 4 * h + q);
+          f[h].k[q] = own ? p.scale_log2 : k * q_mul;
+          f[h].lv[q] = own ? 0.f : lv;
+          f[h].w[q] = own ? 1.f : w;
+        }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        mx = fmaxf(mx, full ? chunk_max<false>(sp + h * 64, f[h], 0, 0)
+                            : chunk_max<true>(sp + h * 64, f[h], v_lo - h * 64, v_hi - h * 64));
+      const float m_new = fmaxf(m, mx);
+      const bool need = m_new > m + kLag;
+      const float alpha = need ? ex2_approx(m - m_new) : 1.f;
+      if (need) m = m_new;
+      const float ref = m == -INFINITY ? 0.f : m;
+      float rs = 0.f;
+      if (own) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          rs += chunk_pairs(sp + h * 64, sp + h * 32, p.scale_log2, v_lo - h * 64, v_hi - h * 64, ref);
+      } else if (full) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) rs += chunk_parts<false>(sp + h * 64, sp + h * 16, f[h], 0, ref);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) rs += chunk_parts<true>(sp + h * 64, sp + h * 16, f[h], v_hi - h * 64, ref);
+      }
+      if (j > 0 && __any_sync(0xffffffffu, need)) {
+        // O holds the sum up to tile j - 1: wait for its last product, then rescale
+        mbar_wait(bars, &bars.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.hdr, 461);
+        tc_fence_after();
+#pragma unroll 1
+        for (int q = 0; q < DH / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld32(tmem + TM_O + lane_off + q * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st32(tmem + TM_O + lane_off + q * 32, o);
+        }
+      }
+      l = l * alpha + rs;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bars.p_full[sb]);
+    }
+    if (nT > 0) {
+      mbar_wait(bars, &bars.pv_done[(nT - 1) & 1], ((nT - 1) >> 1) & 1, p.hdr, 462);
+      tc_fence_after();
+    }
+  } else if (warp == 4 || warp == 6) {
+    // ---------------------------------------------------------- producers (4: K, 6: V)
+    const bool kside = warp == 4;
+    uint64_t* full = kside ? bars.full_k : bars.full_v;
+    uint64_t* empty = kside ? bars.empty_k : bars.empty_v;
+    const uint32_t ring = sbase + (kside ? OFF_K : OFF_V);
+    if (lane == 0) {
+      // unit u goes to slot u % SLOTS: the two halves of an own-block tile, or a prefix tile
+      auto slot_for = [&](int u) -> bool {
+        if (u >= SLOTS) mbar_wait(bars, &empty[u % SLOTS], ((u / SLOTS) - 1) & 1, p.hdr, kside ? 470 : 471);
+        if (bars.failed) return false;
+        mbar_expect_tx(&full[u % SLOTS], kSlot);
+        return true;
+      };
+      int u = 0;
+      for (int j = 0; j < nC; ++j) {
+        for (int h = 0; h < 2; ++h, ++u) {
+          if (!slot_for(u)) break;
+          tma_load_3d(ring + (u % SLOTS) * kSlot, kside ? &tmap_kc : &tmap_vc, 64 * h, kvh, b * NT + s_base + j * BN,
+                      &full[u % SLOTS]);
+        }
+      }
+      for (int j = j0; j < j1; ++j, ++u) {
+        int pg = b, place = j * BN;
+        if (p.block_table != nullptr) {
+          pg = __ldg(p.block_table + static_cast<int64_t>(b) * p.pages_per_seq + j);
+          place = 0;
+          if (pg < 0 || pg >= p.num_pages) {
+            record_error(p.hdr, SSD_ERR_DEVICE, 451);
+            pg = 0;
+          }
+        }
+        if (!slot_for(u)) break;
+        tma_load_2d(ring + (u % SLOTS) * kSlot, kside ? &tmap_k : &tmap_v, 0,
+                    (pg * p.Hkv + kvh) * static_cast<int>(p.page_tokens) + place, &full[u % SLOTS]);
+      }
+    }
+    __syncwarp();
+    if (!kside && ragged) {
+      const int u = 2 * nC + nP - 1;
+      if (mbar_wait(bars, &full[u % SLOTS], (u / SLOTS) & 1, p.hdr, 472)) {
+        uint4* v = reinterpret_cast<uint4*>(smem + OFF_V + (u % SLOTS) * kSlot);
+        for (int i = (P - (j1 - 1) * BN) * 8 + lane; i < BN * 8; i += 32) v[i] = make_uint4(0u, 0u, 0u, 0u);
+        fence_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.v_clean);
+    }
+  } else if (warp == 5) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0 && nT > 0) {
+      constexpr uint32_t idS = idesc_e4m3(false, BN), idPV = idesc_e4m3(true, DH);
+      constexpr uint32_t idSb = idesc_bf16(false, BN), idPVb = idesc_bf16(true, DH);
+      auto unit = [&](int j) -> int { return j < nC ? 2 * j : nC + j; };
+      auto issue_S = [&](int j) {
+        const int u = unit(j);
+        const uint32_t d = tmem + TM_S + (j % SBUF) * BN;
+        mbar_wait(bars, &bars.full_k[u % SLOTS], (u / SLOTS) & 1, p.hdr, 481);
+        if (j < nC) mbar_wait(bars, &bars.full_k[(u + 1) % SLOTS], ((u + 1) / SLOTS) & 1, p.hdr, 482);
+        tc_fence_after();
+        const uint32_t kb = sbase + OFF_K + (u % SLOTS) * kSlot;
+        if (j < nC) {
+#pragma unroll
+          for (int ks = 0; ks < DH / 16; ++ks)
+            mma_bf16(d, sw128_desc(sbase + OFF_QB + (ks >> 2) * kSlot + (ks & 3) * 32, 16, 1024),
+                     sw128_desc(kb + (ks >> 2) * kSlot + (ks & 3) * 32, 16, 1024), idSb, ks > 0 ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < DH / 32; ++ks) {
+            const uint64_t bd = sw128_desc(kb + ks * 32, 16, 1024);
+            mma_e4m3(d, sw128_desc(sbase + OFF_Q8 + ks * 32, 16, 1024), bd, idS, ks > 0 ? 1u : 0u);
+            mma_e4m3(d, sw128_desc(sbase + OFF_Q8 + kSlot + ks * 32, 16, 1024), bd, idS, 1u);
+          }
+        }
+        mma_commit(&bars.s_full[j % SBUF]);
+        mma_commit(&bars.empty_k[u % SLOTS]);
+        if (j < nC) mma_commit(&bars.empty_k[(u + 1) % SLOTS]);
+      };
+      mbar_wait(bars, &bars.q_full, 0, p.hdr, 480);
+      for (int j = 0; j < SBUF && j < nT; ++j) issue_S(j);
+      for (int j = 0; j < nT; ++j) {
+        const int u = unit(j);
+        mbar_wait(bars, &bars.p_full[j % SBUF], (j / SBUF) & 1, p.hdr, 483);
+        mbar_wait(bars, &bars.full_v[u % SLOTS], (u / SLOTS) & 1, p.hdr, 484);
+        if (j < nC) mbar_wait(bars, &bars.full_v[(u + 1) % SLOTS], ((u + 1) / SLOTS) & 1, p.hdr, 485);
+        if (j < nC) mbar_wait(bars, &bars.own_clean[j & 1], (j >> 1) & 1, p.hdr, 487);
+        if (ragged && j == nT - 1) mbar_wait(bars, &bars.v_clean, 0, p.hdr, 486);
+        tc_fence_after();
+        const uint32_t vb = sbase + OFF_V + (u % SLOTS) * kSlot;
+        const uint32_t pa = tmem + TM_S + (j % SBUF) * BN;
+        if (j < nC) {
+#pragma unroll
+          for (int ks = 0; ks < BN / 16; ++ks)
+            mma_bf16_ts(tmem + TM_O, pa + ks * 8, sw128_desc(vb + ks * 16 * 128, kSlot, 1024), idPVb,
+                        (j > 0 || ks > 0) ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < BN / 32; ++ks) {
+            const uint64_t bd = sw128_desc(vb + ks * 32 * 128, kSlot, 1024);
+            mma_e4m3_ts(tmem + TM_O, pa + ks * 8, bd, idPV, (j > 0 || ks > 0) ? 1u : 0u);
+            mma_e4m3_ts(tmem + TM_O, pa + P2 + ks * 8, bd, idPV, 1u);
+          }
+        }
+        mma_commit(&bars.pv_done[j & 1]);
+        mma_commit(&bars.empty_v[u % SLOTS]);
+        if (j < nC) mma_commit(&bars.empty_v[(u + 1) % SLOTS]);
+        // products of one kind run in the order issued: P V above reads P_j before S of tile
+        // j + SBUF overwrites it. Between the kinds the order is made.
+        if (j < nC) {
+          mbar_wait(bars, &bars.pv_done[j & 1], (j >> 1) & 1, p.hdr, 488);
+          tc_fence_after();
+        }
+        if (j + SBUF < nT) issue_S(j + SBUF);
+      }
+    }
+  }
+
+  else if (nC > 0) {
+    // ---------------------------------------------------------- cleaners (warps 7-11)
+    // Slots of other blocks and of absent tokens may hold anything, and 0 * inf is not 0: values
+    // that are not finite leave the tile, and the rows that see one get it at the end.
+    bool odd = false;
+    for (int j = 0; j < nC; ++j) {
+      for (int h = 0; h < 2; ++h) {
+        const int u = 2 * j + h;
+        if (!mbar_wait(bars, &bars.full_v[u % SLOTS], (u / SLOTS) & 1, p.hdr, 473)) break;
+        uint4* v = reinterpret_cast<uint4*>(smem + OFF_V + (u % SLOTS) * kSlot);
+        for (int i = (warp - 7) * 32 + lane; i < BN * 8; i += kCleaners * 32) {
+          uint4 x = v[i];
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+          bool bad = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if ((w[e] & 0x7f80u) == 0x7f80u) {
+              w[e] &= 0xffff0000u;
+              bad = true;
+            }
+            if ((w[e] & 0x7f800000u) == 0x7f800000u) {
+              w[e] &= 0xffffu;
+              bad = true;
+            }
+          }
+          if (bad) {
+            v[i] = x;
+            odd = true;
+          }
+        }
+      }
+      if (odd) *reinterpret_cast<volatile int*>(&bars.odd_own) = 1;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.own_clean[j & 1]);
+    }
+    __syncwarp();
+  }
+
+  // ---- merge the S shares of every row in the CTA that owns it. Ring layout (bytes): staged
+  // rows [BM][kRowB], received rows [sender][rpc][kRowB].
+  uint8_t* stage = smem + OFF_K;
+  uint8_t* recv = stage + BM * kRowB;
+  auto part = [&](int c, int i) -> const uint8_t* {
+    return c == rank ? stage + (rb + i) * kRowB : recv + (c * rpc + i) * kRowB;
+  };
+  if (warp < 4 || (warp >= 6 && warp < 10)) {
+    const int half = warp < 4 ? 0 : 1;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t oa = tmem + TM_O + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * 64;
+    // warps 6-9 read O once warps 0-3 have seen the last P V product complete
+    __syncwarp();
+    tc_fence_before();
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    tc_fence_after();
+    uint32_t o[64];
+    if (nT > 0) {
+      load64(oa, o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 64; ++e) o[e] = 0u;
+    }
+    float amax = 0.f;
+    bool odd = false;                                    // an element is not finite
+#pragma unroll
+    for (int e = 0; e < 64; ++e) {
+      odd |= (o[e] & 0x7f800000u) == 0x7f800000u;
+      amax = fmaxf(amax, fabsf(__uint_as_float(o[e])));
+    }
+    if (odd) {
+      amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < 64; ++e)
+        if ((o[e] & 0x7f800000u) != 0x7f800000u) amax = fmaxf(amax, fabsf(__uint_as_float(o[e])));
+    }
+    const int k = (amax >= 0x1p-100f) ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127 : -1;
+    const int ex = min(k, 125) + 1;
+    const float scale = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
+    const float inv_scale = __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
+    uint4* dst = reinterpret_cast<uint4*>(stage + row * kRowB + half * DH);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      uint32_t pk[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t x = o[8 * u + 2 * e], y = o[8 * u + 2 * e + 1];
+        pk[e] = pack_i16(__uint_as_float(x), __uint_as_float(y), scale);
+        if (odd) {                                       // -2^15 stands for what is not finite
+          if ((x & 0x7f800000u) == 0x7f800000u) pk[e] = (pk[e] & 0xffff0000u) | 0x8000u;
+          if ((y & 0x7f800000u) == 0x7f800000u) pk[e] = (pk[e] & 0xffffu) | 0x80000000u;
+        }
+      }
+      dst[u] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    }
+    float* tail = reinterpret_cast<float*>(stage + row * kRowB + 2 * DH);
+    if (half == 0) {
+      tail[0] = m;
+      tail[1] = l;
+    }
+    // the sign tells the owner of the row to look closer
+    const bool look = odd || (nC > 0 && *reinterpret_cast<volatile int*>(&bars.odd_own));
+    tail[2 + half] = look ? -inv_scale : inv_scale;
+    fence_async_smem();
+  }
+  if (tid == 0) mbar_expect_tx(&bars.recv_full, static_cast<uint32_t>((S - 1) * nr * kRowB));
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();                                        // every ring of the cluster is idle
+  tc_fence_after();
+  if (tid < S - 1) {
+    const int c = (rank + 1 + tid) % S;
+    const int n_c = min(rv, (c + 1) * rpc) - c * rpc;
+    if (n_c > 0) {
+      const uint32_t dst = map_peer(smem_u32(recv + rank * rpc * kRowB), static_cast<uint32_t>(c));
+      const uint32_t bar = map_peer(smem_u32(&bars.recv_full), static_cast<uint32_t>(c));
+      bulk_copy_to_peer(dst, smem_u32(stage + c * rpc * kRowB), static_cast<uint32_t>(n_c * kRowB), bar);
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+  __syncthreads();
+  for (int it = tid; it < nr * (DH / 16); it += kThreads) {
+    const int i = it / (DH / 16), cg = it % (DH / 16);
+    if (!mbar_wait(bars, &bars.recv_full, 0, p.hdr, 490)) continue;
+    float4 tl[kMaxSplit];
+    uint4 h[kMaxSplit][2];
+#pragma unroll
+    for (int c = 0; c < kMaxSplit; ++c) {
+      tl[c] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      if (c < S) {
+        const uint8_t* pr = part(c, i);
+        tl[c] = *reinterpret_cast<const float4*>(pr + 2 * DH);
+        const uint4* src = reinterpret_cast<const uint4*>(pr + cg * 32);
+        h[c][0] = src[0];
+        h[c][1] = src[1];
+      }
+    }
+    float M = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kMaxSplit; ++c) M = fmaxf(M, tl[c].x);
+    // a share without keys has sum 0 and zeros; a NaN score leaves the maximum and is in the sum
+    float fw[kMaxSplit], L = 0.f;
+#pragma unroll
+    for (int c = 0; c < kMaxSplit; ++c) {
+      fw[c] = tl[c].x > -INFINITY ? ex2_approx(tl[c].x - M) : 1.f;
+      L = fmaf(tl[c].y, fw[c], L);
+    }
+    if (bars.failed) continue;
+    const float inv = __frcp_rn(L);
+    float acc[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int c = 0; c < kMaxSplit; ++c) {
+      if (c < S) {
+        const float g = fw[c] * inv * fabsf(cg < 4 ? tl[c].z : tl[c].w);
+        const uint32_t w[8] = {h[c][0].x, h[c][0].y, h[c][0].z, h[c][0].w, h[c][1].x, h[c][1].y, h[c][1].z, h[c][1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 v = unpack_i16(w[e]);
+          acc[2 * e] = fmaf(g, v.x, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(g, v.y, acc[2 * e + 1]);
+        }
+      }
+    }
+    const int slot = bars.row_slot[rb + i];
+    bool look = false;
+#pragma unroll
+    for (int c = 0; c < kMaxSplit; ++c) look |= c < S && (cg < 4 ? tl[c].z : tl[c].w) < 0.f;
+    if (look) {
+#pragma unroll
+      for (int c = 0; c < kMaxSplit; ++c) {
+        if (c < S) {
+          const uint32_t w[8] = {h[c][0].x, h[c][0].y, h[c][0].z, h[c][0].w, h[c][1].x, h[c][1].y, h[c][1].z, h[c][1].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if ((w[e] & 0xffffu) == 0x8000u) acc[2 * e] = NAN;
+            if ((w[e] >> 16) == 0x8000u) acc[2 * e + 1] = NAN;
+          }
+        }
+      }
+      // the own-block values that left the tile: an infinity or NaN, whatever its weight
+      for (int t = slot / p.Dmax * p.Dmax; t <= slot; ++t) {
+        const uint16_t* v = p.v_cand + ((static_cast<int64_t>(b) * NT + t) * p.Hkv + kvh) * DH + cg * 16;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if ((v[e] & 0x7f80u) == 0x7f80u) acc[e] += bf16_to_f32(v[e]);
+      }
+    }
+    const int hh = kvh * G + (r0 + rb + i) % G;
+    const int64_t at = ((static_cast<int64_t>(b) * NT + slot) * p.Hq + hh) * DH + cg * 16;
+    if (p.out_f32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) o[u] = make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
+    } else {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
+      o[0] = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]), pack_bf16(acc[4], acc[5]),
+                        pack_bf16(acc[6], acc[7]));
+      o[1] = make_uint4(pack_bf16(acc[8], acc[9]), pack_bf16(acc[10], acc[11]), pack_bf16(acc[12], acc[13]),
+                        pack_bf16(acc[14], acc[15]));
+    }
+  }
+  // this CTA's outgoing copies have finished reading its staged rows before it exits
+  if (tid < S - 1) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ host
+static bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
+                     const cuuint64_t* strides, const cuuint32_t* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Kernel attributes, once a device, and how many clusters of S CTAs are resident at once.
+static int resident(int S) {
+  static std::mutex mu;
+  static bool ready[kMaxDevices];
+  static int found[kMaxDevices][kMaxSplit + 1];
+  const int dev = current_device();
+  if (dev < 0) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!ready[dev]) {
+    if (cudaFuncSetAttribute(k_attn_quant_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    for (int n = 1; n <= kMaxSplit; ++n) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(n), 1, 1);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kSmemBytes;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = static_cast<unsigned>(n);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int count = 0;
+      if (cudaOccupancyMaxActiveClusters(&count, k_attn_quant_tc, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        count = 0;
+      }
+      found[dev][n] = count;
+    }
+    ready[dev] = true;
+  }
+  return found[dev][S];
+}
+
+// CTAs that share a row tile's prefix: whole waves of resident clusters times the tiles of a CTA
+// and 4 for its start and merge.
+static int choose_split(long long groups, long long tiles) {
+  int best = 0;
+  double cost = 0;
+  for (int S = 1; S <= kMaxSplit && S <= std::max<long long>(tiles, 1); ++S) {
+    const int clusters = resident(S);
+    if (clusters <= 0) continue;
+    const double c = std::ceil(static_cast<double>(groups) / clusters) * (std::ceil(static_cast<double>(tiles) / S) + 4.);
+    if (best == 0 || c < cost) {
+      cost = c;
+      best = S;
+    }
+  }
+  return best;
+}
+
+}  // namespace qtc
+
+bool attn_quant_tc_applies(const AttnQuantParams& p, int dh) {
+  if (dh != qtc::DH || p.NB > qtc::kMaxBlocks) return false;
+  if (static_cast<long long>(p.B) * p.Hkv > 65535 || static_cast<long long>(p.B) * p.NB * p.Dmax >= (1LL << 31)) return false;
+  return tc::encode_fn() != nullptr;
+}
+
+int attn_quant_tc_launch(const AttnQuantParams& p, cudaStream_t s) {
+  using namespace qtc;
+  const int NT = p.NB * p.Dmax;
+  const int G = p.Hq / p.Hkv;
+  const int mtiles = (NT * G + BM - 1) / BM;
+  const int S = choose_split(static_cast<long long>(p.B) * p.Hkv * mtiles, (p.capacity + BN - 1) / BN + 2);
+  if (S < 1) return SSD_ERR_CUDA;
+  // an empty cache is never read, but a map needs an address and a row
+  const uint64_t rows = static_cast<uint64_t>(p.num_pages) * p.Hkv * p.page_tokens;
+  const void *kb = rows > 0 ? p.k_cache : static_cast<const void*>(p.q), *vb = rows > 0 ? p.v_cache : kb;
+  const cuuint64_t dims2[2] = {DH, rows > 0 ? rows : 1}, strides2[1] = {DH};
+  const cuuint32_t box2[2] = {DH, BN};
+  const cuuint64_t dims3[3] = {DH, static_cast<cuuint64_t>(p.Hkv), static_cast<cuuint64_t>(p.B) * NT};
+  const cuuint64_t strides3[2] = {DH * 2, static_cast<cuuint64_t>(p.Hkv) * DH * 2};
+  const cuuint32_t box3[3] = {64, 1, BN};
+  CUtensorMap mk, mv, mkc, mvc;
+  if (!make_map(&mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, kb, 2, dims2, strides2, box2) ||
+      !make_map(&mv, CU_TENSOR_MAP_DATA_TYPE_UINT8, vb, 2, dims2, strides2, box2) ||
+      !make_map(&mkc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.k_cand, 3, dims3, strides3, box3) ||
+      !make_map(&mvc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.v_cand, 3, dims3, strides3, box3))
+    return SSD_ERR_CUDA;
+  AttnQuantParams q = p;
+  q.longest_first = p.B > 1 && p.B <= kThreads ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(S), static_cast<unsigned>(mtiles), static_cast<unsigned>(p.B * p.Hkv));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, k_attn_quant_tc, mk, mv, mkc, mvc, q) != cudaSuccess) {
+    cudaGetLastError();
+    return SSD_ERR_CUDA;
+  }
+  count_launch();
+  return check_launch();
+}
+
+}  // namespace ssd

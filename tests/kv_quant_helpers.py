@@ -82,27 +82,62 @@ class AttnCase:
     def kw(self):
         return dict(block_table=None if self.table is None else dev(self.table))
 
-    def oracle(self, slots=None):
+    def oracle(self, slots=None, probs=None):
         k = K.values(self.k_codes, self.k_scale, self.sb, self.prefix, self.table)
         v = K.values(self.v_codes, self.v_scale, self.sb, self.prefix, self.table)
-        return K.attention(self.q64, k, v, self.kc64, self.vc64, self.blk_len, self.Dmax, slots)
+        return K.attention(self.q64, k, v, self.kc64, self.vc64, self.blk_len, self.Dmax, slots, probs=probs)
+
+    def v_scales(self, b):
+        """The value scale of every prefix key of sequence b: [Hkv][prefix]."""
+        pages = [b] if self.table is None else self.table[b, :-(-int(self.prefix[b]) // 128)]
+        s = [np.repeat(self.v_scale[p].astype(np.float64), self.sb, 1)[:, :self.v_codes.shape[2]] for p in pages]
+        s = np.concatenate(s, 1) if s else np.zeros((self.kc.shape[2], 0))
+        return np.maximum(s[:, :self.prefix[b]], 2.0 ** -100)
+
+    def tolerance(self, b, o, size, heads, f32, wide):
+        """Per element [Hq][dh]; heads = [(p, v)] of the kv heads, size = sum_j p_j |v_j|.
+
+        Both paths: scores are off by less than 2^-11 in log2 units (fp32 sums over at most 128
+        products of total magnitude <= 32, 2^-23 each; q as two e4m3 numbers is off by 2^-18 of
+        its largest per element) and exponentials by 2^-21, which acts on size; a bf16 output
+        adds half a step of its own, 2^-8 |out|.
+
+        Few rows: probabilities are rounded to 11 bits, 2^-11 size, and below the fp16 range by
+        2^-25 each while the largest weight is at least 1: N 2^-25 448 max v_scale.
+
+        Many rows (over 32 packed ones at head dim 128): a probability is rounded to 8 bits (half
+        a step 2^-8), or by half of 2^-9 where that is more, while the key with the largest
+        weight p_j s_j (s the value scale) has at least 2^4. With sum_j p_j = 1 the second is
+        (max_i p_i s_i / 2^4) 2^-9 / 2 for a code. Both are independent from key to key and
+        uniform, so six standard deviations (half-width / sqrt 3) of the sums are allowed. The
+        merge rounds a share's row to 2^-14 of its largest element: 2^-14 sum_j p_j max_d |v_jd|."""
+        tol = np.zeros_like(o)
+        G = o.shape[0] // len(heads)
+        many = self.dh == 128 and self.q.shape[1] * G > 32
+        P = int(self.prefix[b])
+        sv = self.v_scales(b)
+        for h, (p, v) in enumerate(heads):
+            rows = slice(h * G, (h + 1) * G)
+            if not many:
+                tol[rows] = size[rows] * 2.0 ** -10 * wide + P * 2.0 ** -25 * 448 * float(sv.max(initial=0))
+                continue
+            rel = (p ** 2) @ (v ** 2) * (2.0 ** -8) ** 2 / 3
+            top = (p[:, :P] * sv[h]).max(1, initial=0.0)
+            codes2 = ((v[:P] / sv[h][:, None]) ** 2).sum(0)
+            floor = (top[:, None] * 2.0 ** -4 * 2.0 ** -10) ** 2 / 3 * codes2[None, :]
+            most = p @ np.abs(v).max(1)
+            tol[rows] = 6 * np.sqrt(rel + floor) + size[rows] * 2.0 ** -11 * wide + most[:, None] * 2.0 ** -14
+        return tol + (0 if f32 else np.abs(o) * 2.0 ** -8) + 1e-30
 
     def check(self, out, slots=None, wide=1.0):
-        """Every present row within tolerance, absent rows as they were.
-
-        Tolerance, per element, with size = sum_j p_j |v_j|. The probabilities' rounding to 11
-        bits and the scores' errors (fp32 sums over dh <= 128 products of total magnitude
-        <= 32 in log2 units, 2^-23 each: < 2^-11) act on size: 2 * 2^-11. Weights below the
-        fp16 range round by at most 2^-25 each while the largest weight is at least 1:
-        N 2^-25 448 max v_scale. A bf16 output adds half a step of its own, 2^-8 |out|."""
+        """Every present row within tolerance of the oracle."""
         f32 = out.dtype == torch.float32
         got = out.cpu().numpy().astype(np.float64) if f32 else O.bf16_to_f64(out.view(torch.int16).cpu().numpy().view(np.uint16))
-        ref = self.oracle(slots)
+        probs = {}
+        ref = self.oracle(slots, probs)
         assert ref
         for (b, t), (o, size) in ref.items():
-            vs = self.v_scale[b] if self.table is None else self.v_scale[self.table[b]]
-            floor = self.prefix[b] * 2.0 ** -25 * 448 * float(np.nanmax(np.where(np.isfinite(vs), vs, 0), initial=0))
-            tol = wide * size * 2.0 ** -10 + floor + (0 if f32 else np.abs(o) * 2.0 ** -8) + 1e-30
+            tol = self.tolerance(b, o, size, probs[b, t], f32, wide)
             err = np.abs(got[b, t] - o)
             assert (err <= tol).all(), (b, t, float((err / tol).max()))
         return ref
