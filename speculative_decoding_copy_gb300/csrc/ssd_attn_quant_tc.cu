@@ -158,6 +158,24 @@ __device__ __forceinline__ void load64(uint32_t taddr, uint32_t* v) {
   tmem_wait_ld();
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ void fma2(float& x, float& y, float a0, float a1, float b, float c) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(x), "=f"(y) : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a0, float a1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y) : "f"(a0), "f"(a1));
+}
+
 // largest y of the columns [lo, hi) of 64 (MASK), or of all
 template <bool MASK>
 __device__ __forceinline__ float chunk_max(uint32_t taddr, const Groups& f, int lo, int hi) {
@@ -168,10 +186,13 @@ __device__ __forceinline__ float chunk_max(uint32_t taddr, const Groups& f, int 
   for (int q = 0; q < 4; ++q) {
     float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-    for (int c = 16 * q; c < 16 * q + 16; c += 2) {
-      const float x = __uint_as_float(v[c]), y = __uint_as_float(v[c + 1]);
-      if (!MASK || (c >= lo && c < hi)) a = fmaxf(a, x);
-      if (!MASK || (c + 1 >= lo && c + 1 < hi)) b = fmaxf(b, y);
+    for (int c = 16 * q; c < 16 * q + 16; c += 4) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[e] = !MASK || (c + e >= lo && c + e < hi) ? __uint_as_float(v[c + e]) : -INFINITY;
+      a = max3(a, x[0], x[1]);
+      b = max3(b, x[2], x[3]);
     }
     a = fmaxf(a, b);
     if (!MASK || a > -INFINITY) top = fmaxf(top, fmaf(a, f.k[q], f.lv[q]));   // an empty group's factors may be anything
@@ -197,14 +218,15 @@ __device__ __forceinline__ float chunk_parts(uint32_t saddr, uint32_t paddr, con
       uint32_t t1[2], t2[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float x = ex2_approx(fmaf(__uint_as_float(v[c + 2 * h]), f.k[q], off));
-        float y = ex2_approx(fmaf(__uint_as_float(v[c + 2 * h + 1]), f.k[q], off));
+        float x, y;
+        fma2(x, y, __uint_as_float(v[c + 2 * h]), __uint_as_float(v[c + 2 * h + 1]), f.k[q], off);
+        x = ex2_approx(x);
+        y = ex2_approx(y);
         if (MASK) {
           if (c + 2 * h >= hi) x = 0.f;
           if (c + 2 * h + 1 >= hi) y = 0.f;
         }
-        s0 += x;
-        s1 += y;
+        add2(s0, s1, x, y);
         uint32_t w, left;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(left) : "r"(w), "r"(w & 0xff80ff80u));
@@ -431,12 +453,15 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     }
     // scales of a prefix tile: lane i < 8 holds the K scale of the tile's group i, lane 8 + i the
     // V scale; loaded a tile ahead
-    auto load_scale = [&](int j) -> float {
+    auto load_page = [&](int j) -> int {
+      if (j >= nT || j < nC || p.block_table == nullptr) return b;
+      return p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + j0 + (j - nC)];
+    };
+    auto load_scale = [&](int j, int pg) -> float {
       if (j >= nT || j < nC || lane >= 16) return 0.f;
       const int tile = j0 + (j - nC);
       int ph, place;
       if (p.block_table != nullptr) {
-        int pg = p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + tile];
         if (pg < 0 || pg >= p.num_pages) pg = 0;
         ph = pg * p.Hkv + kvh;
         place = (lane & 7) * 16;
@@ -448,7 +473,8 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       const int blk = min(place >> p.sb_log2, blocks - 1);
       return (lane < 8 ? p.k_scale : p.v_scale)[static_cast<int64_t>(ph) * blocks + blk];
     };
-    float next_scale = load_scale(0);
+    float next_scale = load_scale(0, load_page(0));
+    int next_page = load_page(1);                        // a page ahead of its scales
     for (int j = 0; j < nT; ++j) {
       const int sb = j % SBUF;
       const bool own = j < nC;
@@ -456,7 +482,8 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       const float sc = next_scale;
       const float lane_f = lane < 8 ? sc : fmaxf(__log2f(sc), kLeastVScaleLog2);
       const float lane_w = ex2_approx(-lane_f);          // lanes 8-15: 1 / V factor
-      next_scale = load_scale(j + 1);
+      next_scale = load_scale(j + 1, next_page);
+      next_page = load_page(j + 2);
       mbar_wait(bars, &bars.s_full[sb], (j / SBUF) & 1, p.hdr, 460);
       tc_fence_after();
       int v_lo = 0, v_hi;
@@ -469,38 +496,38 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       }
       const bool full = !own && v_hi >= BN;
       const uint32_t sp = tmem + TM_S + sb * BN + lane_off;
-      Groups f[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
+      auto groups = [&](int h) -> Groups {
+        Groups f;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float k = __shfl_sync(0xffffffffu, lane_f, 4 * h + q), lv = __shfl_sync(0xffffffffu, lane_f, 8 + 4 * h + q),
-                      w = __shfl_sync(0xffffffffu, lane_w, 8 + 4 * h + q);
-          f[h].k[q] = own ? p.scale_log2 : k * q_mul;
-          f[h].lv[q] = own ? 0.f : lv;
-          f[h].w[q] = own ? 1.f : w;
+          const float k = __shfl_sync(0xffffffffu, lane_f, 4 * h + q), lv = __shfl_sync(0xffffffffu, lane_f, 8 + 4 * h + q);
+          f.k[q] = own ? p.scale_log2 : k * q_mul;
+          f.lv[q] = own ? 0.f : lv;
+          f.w[q] = __shfl_sync(0xffffffffu, lane_w, 8 + 4 * h + q);
         }
+        return f;
+      };
       float mx = -INFINITY;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        mx = fmaxf(mx, full ? chunk_max<false>(sp + h * 64, f[h], 0, 0)
-                            : chunk_max<true>(sp + h * 64, f[h], v_lo - h * 64, v_hi - h * 64));
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const Groups f = groups(h);
+        mx = fmaxf(mx, full ? chunk_max<false>(sp + h * 64, f, 0, 0) : chunk_max<true>(sp + h * 64, f, v_lo - h * 64, v_hi - h * 64));
+      }
       const float m_new = fmaxf(m, mx);
       const bool need = m_new > m + kLag;
       const float alpha = need ? ex2_approx(m - m_new) : 1.f;
       if (need) m = m_new;
       const float ref = m == -INFINITY ? 0.f : m;
       float rs = 0.f;
-      if (own) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        if (own) {
           rs += chunk_pairs(sp + h * 64, sp + h * 32, p.scale_log2, v_lo - h * 64, v_hi - h * 64, ref);
-      } else if (full) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) rs += chunk_parts<false>(sp + h * 64, sp + h * 16, f[h], 0, ref);
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) rs += chunk_parts<true>(sp + h * 64, sp + h * 16, f[h], v_hi - h * 64, ref);
+        } else {
+          const Groups f = groups(h);
+          rs += full ? chunk_parts<false>(sp + h * 64, sp + h * 16, f, 0, ref)
+                     : chunk_parts<true>(sp + h * 64, sp + h * 16, f, v_hi - h * 64, ref);
+        }
       }
       if (j > 0 && __any_sync(0xffffffffu, need)) {
         // O holds the sum up to tile j - 1: wait for its last product, then rescale
