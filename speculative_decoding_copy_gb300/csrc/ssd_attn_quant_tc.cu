@@ -16,19 +16,22 @@
 // (bf16, masked), and the shares are merged on chip.
 //
 // Per CTA (384 threads, one CTA per SM, all 512 TMEM columns):
-//   warps 0-3  one thread per row: its Q into shared memory (two e4m3 parts, swizzled; rank 0
-//              also bf16), then the online softmax of each 128-key tile read from TMEM: per 16
-//              keys one K factor, one log2 of the V factor and one weight 1/sv of the sum. P
-//              goes back to TMEM over the first half of the tile's S buffer (two parts of 32
-//              columns, four keys a word; bf16 pairs for own-block tiles). In fp16 with the
-//              exponent offset of the two formats taken into the exponential, the first part is
-//              the upper byte of a probability's bits and the second the rounded upper byte of
-//              what is left, so no format conversion is needed;
+//   warps 0-3, 8-11  two threads per row, 64 columns of a tile each (one warp a scheduler left
+//              it waiting on its own latencies: 1.7 us a tile): Q into shared memory (two e4m3
+//              parts, swizzled; rank 0 also bf16), then the online softmax of each 128-key tile,
+//              read from TMEM once: per 16 keys one K factor, one log2 of the V factor and one
+//              weight 1/sv of the sum. A barrier tells all rows whether any reference has to
+//              move, which is rare. P goes back to TMEM over the first half of the tile's S
+//              buffer (two parts of 32 columns, four keys a word; bf16 pairs for own-block
+//              tiles). In fp16 with the exponent offset of the two formats taken into the
+//              exponential, the first part is the upper byte of a probability's bits and the
+//              second the rounded upper byte of what is left, so no format conversion is
+//              needed. On rank 0 they also take infinities and NaN out of own-block values;
 //   warp 4     TMEM allocation, then the producer of the K tiles;
 //   warp 6     the producer of the V tiles; it clears the value rows past the prefix (codes
 //              there may be NaN, and 0 * NaN is not 0);
 //   warp 5     the MMA-issuing thread, S three tiles ahead of the softmax;
-//   warps 6-11 add threads to the merge.
+//   warp 7     joins the merge.
 // Shared memory: Q (64 KB), then four 16 KB slots each for K and V. A prefix tile takes one
 // slot of each, an own-block tile (bf16) two.
 // TMEM columns: S buffers 0-127, 128-255, 256-383, O 384-511.
@@ -66,12 +69,12 @@ constexpr uint32_t OFF_QB = 2 * kSlot;    // bf16, two 64-column halves
 constexpr uint32_t OFF_K = 4 * kSlot;
 constexpr uint32_t OFF_V = OFF_K + SLOTS * kSlot;
 constexpr uint32_t OFF_BAR = OFF_V + SLOTS * kSlot;
-constexpr uint32_t kBarBytes = 1024;
+constexpr uint32_t kBarBytes = 2048;
 constexpr uint32_t kSmemBytes = OFF_BAR + kBarBytes + 1024;   // + slack to align the base to 1024
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr unsigned long long kWaitClocks = 1ull << 32;
 constexpr int kMaxSplit = 8;
-constexpr int kCleaners = 5;              // warps 7-11
+constexpr int kSoftmax = 256;             // softmax threads
 constexpr int kRowB = 2 * DH + 16;        // one share's partial row as sent to its owner
 constexpr int kMaxBlocks = 8192;          // NB: the block ends are kept in the ring at first
 static_assert((2 * BM + kMaxSplit) * kRowB <= static_cast<int>(2 * SLOTS * kSlot), "merge buffers fit in the ring");
@@ -81,6 +84,7 @@ struct Bars {
   uint64_t full_k[SLOTS], full_v[SLOTS], empty_k[SLOTS], empty_v[SLOTS];
   uint64_t q_full;
   uint64_t s_full[SBUF], p_full[SBUF], pv_done[2];
+  uint64_t o_done;                        // every product into O is done
   uint64_t v_clean;                       // the value rows past the prefix are zeros
   uint64_t own_clean[2];                  // an own-block tile's values are finite
   uint64_t recv_full;
@@ -89,6 +93,7 @@ struct Bars {
   int odd_own;                            // an own-block value was not finite
   int seq, rows;                          // the sequence; its present rows
   int row_slot[BM];                       // candidate slot of a row of this tile
+  float pair[2][BM];                      // a value of each half of a row
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
@@ -178,9 +183,7 @@ __device__ __forceinline__ void add2(float& x, float& y, float a0, float a1) {
 
 // largest y of the columns [lo, hi) of 64 (MASK), or of all
 template <bool MASK>
-__device__ __forceinline__ float chunk_max(uint32_t taddr, const Groups& f, int lo, int hi) {
-  uint32_t v[64];
-  load64(taddr, v);
+__device__ __forceinline__ float chunk_max(const uint32_t (&v)[64], const Groups& f, int lo, int hi) {
   float top = -INFINITY;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -203,9 +206,7 @@ __device__ __forceinline__ float chunk_max(uint32_t taddr, const Groups& f, int 
 // prefix tile: 2^(y - ref + lift) as two e4m3 parts, four keys a word, at paddr and paddr + P2;
 // returns the sum weighted by 1 / V factor
 template <bool MASK>
-__device__ __forceinline__ float chunk_parts(uint32_t saddr, uint32_t paddr, const Groups& f, int hi, float ref) {
-  uint32_t v[64];
-  load64(saddr, v);
+__device__ __forceinline__ float chunk_parts(const uint32_t (&v)[64], uint32_t paddr, const Groups& f, int hi, float ref) {
   uint32_t p1[16], p2[16];
   float total = 0.f;
 #pragma unroll
@@ -246,9 +247,7 @@ __device__ __forceinline__ float chunk_parts(uint32_t saddr, uint32_t paddr, con
 
 // own-block tile: 2^(y - ref + lift) as bf16 pairs over the columns [lo, hi); returns the sum
 // of the rounded values
-__device__ __forceinline__ float chunk_pairs(uint32_t saddr, uint32_t paddr, float k, int lo, int hi, float ref) {
-  uint32_t v[64];
-  load64(saddr, v);
+__device__ __forceinline__ float chunk_pairs(const uint32_t (&v)[64], uint32_t paddr, float k, int lo, int hi, float ref) {
   uint32_t pk[32];
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -263,6 +262,23 @@ __device__ __forceinline__ float chunk_pairs(uint32_t saddr, uint32_t paddr, flo
   }
   tmem_st32(paddr, pk);
   return s0 + s1;
+}
+
+// whether `x` holds in any softmax thread, once all of them have come here (and read S)
+__device__ __forceinline__ bool any_row(bool x) {
+  uint32_t r;
+  tc_fence_before();
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"(x ? 1u : 0u) : "memory");
+  tc_fence_after();
+  return r != 0;
+}
+__device__ __forceinline__ void softmax_sync() {
+  __syncwarp();
+  asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ kernel
@@ -296,13 +312,14 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       mbar_init(&bars.empty_k[s], 1);
       mbar_init(&bars.empty_v[s], 1);
     }
-    mbar_init(&bars.q_full, BM);
+    mbar_init(&bars.q_full, kSoftmax);
     mbar_init(&bars.recv_full, 1);
     mbar_init(&bars.v_clean, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&bars.own_clean[i], kCleaners);
+    mbar_init(&bars.o_done, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.own_clean[i], kSoftmax);
     for (int i = 0; i < SBUF; ++i) {
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i], BM);
+      mbar_init(&bars.p_full[i], kSoftmax);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&bars.pv_done[i], 1);
     bars.failed = 0;
@@ -393,33 +410,40 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
   const int rb = rank * rpc, nr = max(0, min(rv, rb + rpc) - rb);
   float m = -INFINITY, l = 0.f;            // reference maximum (log2 units) and sum of a softmax row
 
-  if (warp < 4) {
+  const bool softmax = warp < 4 || warp >= 8;
+  const int half = warp < 4 ? 0 : 1;                       // columns 64 half .. of every tile
+  const int row = (warp & 3) * 32 + lane;                  // TMEM lane
+  if (softmax) {
     // ---------------------------------------------------------- rows
-    const bool row_ok = tid < rv;
-    const int slot = bars.row_slot[tid];
+    const bool row_ok = row < rv;
+    const int slot = bars.row_slot[row];
     const int c_lo = slot / p.Dmax * p.Dmax;
-    // Q: a power of two brings the row's largest magnitude into [128, 256); two e4m3 parts
+    // Q: a power of two brings the row's largest magnitude into [128, 256); two e4m3 parts. Each
+    // thread converts 64 elements.
     float q_mul;
     {
-      uint4 raw[16];
+      uint4 raw[8];
       const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + ((static_cast<int64_t>(b) * NT + slot) * p.Hq + kvh * G + (r0 + tid) % G) * DH);
+          p.q + ((static_cast<int64_t>(b) * NT + slot) * p.Hq + kvh * G + (r0 + row) % G) * DH + half * 64);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) raw[i] = row_ok ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 8; ++i) raw[i] = row_ok ? src[i] : make_uint4(0u, 0u, 0u, 0u);
       uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
       }
+      bars.pair[half][row] = __uint_as_float(top);
+      softmax_sync();
+      top = max(top, __float_as_uint(bars.pair[half ^ 1][row]));
       const int ex = static_cast<int>(top >> 23);
       const int up = min(254 + 7 - ex, 253);
       const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
       q_mul = ex == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * p.scale_log2;
-      const uint32_t row_at = tid * 128, sw = tid & 7;
+      const uint32_t row_at = row * 128, sw = row & 7;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {                      // 16 elements
+      for (int i = 0; i < 4; ++i) {                      // 16 elements
         uint32_t part[2][4];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {                    // four of them
@@ -440,101 +464,35 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          *reinterpret_cast<uint4*>(smem + OFF_Q8 + u * kSlot + row_at + ((i ^ sw) << 4)) =
+          *reinterpret_cast<uint4*>(smem + OFF_Q8 + u * kSlot + row_at + (((4 * half + i) ^ sw) << 4)) =
               make_uint4(part[u][0], part[u][1], part[u][2], part[u][3]);
       }
       if (nC > 0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          *reinterpret_cast<uint4*>(smem + OFF_QB + (i >> 3) * kSlot + row_at + (((i & 7) ^ sw) << 4)) = raw[i];
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(smem + OFF_QB + half * kSlot + row_at + ((i ^ sw) << 4)) = raw[i];
       }
       fence_async_smem();
       mbar_arrive(&bars.q_full);
     }
-    // scales of a prefix tile: lane i < 8 holds the K scale of the tile's group i, lane 8 + i the
-    // V scale; loaded a tile ahead
-    auto load_page = [&](int j) -> int {
-      if (j >= nT || j < nC || p.block_table == nullptr) return b;
-      return p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + j0 + (j - nC)];
-    };
-    auto load_scale = [&](int j, int pg) -> float {
-      if (j >= nT || j < nC || lane >= 16) return 0.f;
-      const int tile = j0 + (j - nC);
-      int ph, place;
-      if (p.block_table != nullptr) {
-        if (pg < 0 || pg >= p.num_pages) pg = 0;
-        ph = pg * p.Hkv + kvh;
-        place = (lane & 7) * 16;
-      } else {
-        ph = b * p.Hkv + kvh;
-        place = tile * BN + (lane & 7) * 16;
-      }
-      const int blocks = static_cast<int>(p.blocks);
-      const int blk = min(place >> p.sb_log2, blocks - 1);
-      return (lane < 8 ? p.k_scale : p.v_scale)[static_cast<int64_t>(ph) * blocks + blk];
-    };
-    float next_scale = load_scale(0, load_page(0));
-    int next_page = load_page(1);                        // a page ahead of its scales
-    for (int j = 0; j < nT; ++j) {
-      const int sb = j % SBUF;
-      const bool own = j < nC;
-      // lanes 0-7: K factor; 8-15: log2 of the V factor
-      const float sc = next_scale;
-      const float lane_f = lane < 8 ? sc : fmaxf(__log2f(sc), kLeastVScaleLog2);
-      const float lane_w = ex2_approx(-lane_f);          // lanes 8-15: 1 / V factor
-      next_scale = load_scale(j + 1, next_page);
-      next_page = load_page(j + 2);
-      mbar_wait(bars, &bars.s_full[sb], (j / SBUF) & 1, p.hdr, 460);
-      tc_fence_after();
-      int v_lo = 0, v_hi;
-      if (own) {
-        const int s0 = s_base + j * BN;
-        v_lo = row_ok ? c_lo - s0 : BN;
-        v_hi = row_ok ? slot + 1 - s0 : 0;
-      } else {
-        v_hi = P - (j0 + (j - nC)) * BN;
-      }
-      const bool full = !own && v_hi >= BN;
-      const uint32_t sp = tmem + TM_S + sb * BN + lane_off;
-      auto groups = [&](int h) -> Groups {
-        Groups f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float k = __shfl_sync(0xffffffffu, lane_f, 4 * h + q), lv = __shfl_sync(0xffffffffu, lane_f, 8 + 4 * h + q);
-          f.k[q] = own ? p.scale_log2 : k * q_mul;
-          f.lv[q] = own ? 0.f : lv;
-          f.w[q] = __shfl_sync(0xffffffffu, lane_w, 8 + 4 * h + q);
-        }
-        return f;
-      };
-      float mx = -INFINITY;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        const Groups f = groups(h);
-        mx = fmaxf(mx, full ? chunk_max<false>(sp + h * 64, f, 0, 0) : chunk_max<true>(sp + h * 64, f, v_lo - h * 64, v_hi - h * 64));
-      }
-      const float m_new = fmaxf(m, mx);
+    // Where a reference has to move: the row's new one, from both halves, and O and the sum
+    // under it (each half rescales its 64 columns of O).
+    auto move_refs = [&](int j, float mx) {
+      bars.pair[half][row] = mx;
+      softmax_sync();
+      const float m_new = fmaxf(m, fmaxf(mx, bars.pair[half ^ 1][row]));
       const bool need = m_new > m + kLag;
       const float alpha = need ? ex2_approx(m - m_new) : 1.f;
       if (need) m = m_new;
-      const float ref = m == -INFINITY ? 0.f : m;
-      float rs = 0.f;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        if (own) {
-          rs += chunk_pairs(sp + h * 64, sp + h * 32, p.scale_log2, v_lo - h * 64, v_hi - h * 64, ref);
-        } else {
-          const Groups f = groups(h);
-          rs += full ? chunk_parts<false>(sp + h * 64, sp + h * 16, f, 0, ref)
-                     : chunk_parts<true>(sp + h * 64, sp + h * 16, f, v_hi - h * 64, ref);
-        }
-      }
+      l *= alpha;
+      softmax_sync();                                    // the pairs may be written again
       if (j > 0 && __any_sync(0xffffffffu, need)) {
         // O holds the sum up to tile j - 1: wait for its last product, then rescale
         mbar_wait(bars, &bars.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.hdr, 461);
+        __syncwarp();
         tc_fence_after();
 #pragma unroll 1
-        for (int q = 0; q < DH / 32; ++q) {
+        for (int q = 2 * half; q < 2 * half + 2; ++q) {
           uint32_t o[32];
           tmem_ld32(tmem + TM_O + lane_off + q * 32, o);
           tmem_wait_ld();
@@ -543,15 +501,114 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           tmem_st32(tmem + TM_O + lane_off + q * 32, o);
         }
       }
-      l = l * alpha + rs;
+    };
+    uint32_t v[64];
+    // ---- own-block tiles
+    bool odd = false;
+    for (int j = 0; j < nC; ++j) {
+      // slots of other blocks and of absent tokens may hold anything, and 0 * inf is not 0:
+      // values that are not finite leave the tile, and the rows that see one get it at the end
+      for (int h = 0; h < 2; ++h) {
+        const int u = 2 * j + h;
+        if (!mbar_wait(bars, &bars.full_v[u % SLOTS], (u / SLOTS) & 1, p.hdr, 473)) break;
+        uint4* vt = reinterpret_cast<uint4*>(smem + OFF_V + (u % SLOTS) * kSlot);
+        for (int i = half * BM + row; i < BN * 8; i += kSoftmax) {
+          uint4 x = vt[i];
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+          bool bad = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if ((w[e] & 0x7f80u) == 0x7f80u) {
+              w[e] &= 0xffff0000u;
+              bad = true;
+            }
+            if ((w[e] & 0x7f800000u) == 0x7f800000u) {
+              w[e] &= 0xffffu;
+              bad = true;
+            }
+          }
+          if (bad) {
+            vt[i] = x;
+            odd = true;
+          }
+        }
+      }
+      if (odd) *reinterpret_cast<volatile int*>(&bars.odd_own) = 1;
+      fence_async_smem();
+      mbar_arrive(&bars.own_clean[j & 1]);
+      const int sb = j % SBUF;
+      mbar_wait(bars, &bars.s_full[sb], (j / SBUF) & 1, p.hdr, 460);
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t sp = tmem + TM_S + sb * BN + lane_off;
+      load64(sp + half * 64, v);
+      const int s0 = s_base + j * BN + half * 64;
+      const int lo = row_ok ? c_lo - s0 : BN, hi = row_ok ? slot + 1 - s0 : 0;
+      Groups f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f.k[q] = p.scale_log2;
+        f.lv[q] = 0.f;
+      }
+      const float mx = chunk_max<true>(v, f, lo, hi);
+      if (any_row(mx > m + kLag)) move_refs(j, mx);
+      l += chunk_pairs(v, sp + half * 32, p.scale_log2, lo, hi, m == -INFINITY ? 0.f : m);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bars.p_full[sb]);
     }
-    if (nT > 0) {
-      mbar_wait(bars, &bars.pv_done[(nT - 1) & 1], ((nT - 1) >> 1) & 1, p.hdr, 462);
+    // ---- prefix tiles. Lane i < 4 holds the K scale of this half's group i, lane 4 + i the V
+    // scale: loaded a tile ahead, and the page a tile ahead of them.
+    auto load_page = [&](int t) -> int {
+      if (t >= j1 || p.block_table == nullptr) return b;
+      return p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + t];
+    };
+    auto load_scale = [&](int t, int pg) -> float {
+      if (t >= j1 || lane >= 8) return 0.f;
+      int place = half * 64 + (lane & 3) * 16;
+      if (p.block_table == nullptr) place += t * BN;
+      if (pg < 0 || pg >= p.num_pages) pg = 0;
+      const int blocks = static_cast<int>(p.blocks);
+      const int blk = min(place >> p.sb_log2, blocks - 1);
+      return (lane < 4 ? p.k_scale : p.v_scale)[static_cast<int64_t>(pg * p.Hkv + kvh) * blocks + blk];
+    };
+    float next_scale = load_scale(j0, load_page(j0));
+    int next_page = load_page(j0 + 1);
+    for (int t = j0; t < j1; ++t) {
+      const int j = nC + t - j0, sb = j % SBUF;
+      // lanes 0-3: K factor; 4-7: log2 of the V factor
+      const float lane_f = lane < 4 ? next_scale : fmaxf(__log2f(next_scale), kLeastVScaleLog2);
+      const float lane_w = ex2_approx(-lane_f);            // lanes 4-7: 1 / V factor
+      next_scale = load_scale(t + 1, next_page);
+      next_page = load_page(t + 2);
+      Groups f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f.k[q] = __shfl_sync(0xffffffffu, lane_f, q) * q_mul;
+        f.lv[q] = __shfl_sync(0xffffffffu, lane_f, 4 + q);
+        f.w[q] = __shfl_sync(0xffffffffu, lane_w, 4 + q);
+      }
+      mbar_wait(bars, &bars.s_full[sb], (j / SBUF) & 1, p.hdr, 460);
+      __syncwarp();
       tc_fence_after();
+      const uint32_t sp = tmem + TM_S + sb * BN + lane_off;
+      load64(sp + half * 64, v);
+      const int hi = P - t * BN - half * 64;
+      const bool full = P - t * BN >= BN;
+      const float mx = full ? chunk_max<false>(v, f, 0, 0) : chunk_max<true>(v, f, 0, hi);
+      if (any_row(mx > m + kLag)) move_refs(j, mx);
+      const float ref = m == -INFINITY ? 0.f : m;
+      l += full ? chunk_parts<false>(v, sp + half * 16, f, 0, ref) : chunk_parts<true>(v, sp + half * 16, f, hi, ref);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bars.p_full[sb]);
     }
+    bars.pair[half][row] = l;                              // read after the barrier before the merge
+    // (a wait on pv_done would not do: the last three products may be open, and a wait for a
+    // parity returns at once while the phase two before is the last one completed)
+    if (nT > 0) mbar_wait(bars, &bars.o_done, 0, p.hdr, 462);
+    __syncwarp();
+    tc_fence_after();
   } else if (warp == 4 || warp == 6) {
     // ---------------------------------------------------------- producers (4: K, 6: V)
     const bool kside = warp == 4;
@@ -666,47 +723,10 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         }
         if (j + SBUF < nT) issue_S(j + SBUF);
       }
+      mma_commit(&bars.o_done);
     }
   }
 
-  else if (nC > 0) {
-    // ---------------------------------------------------------- cleaners (warps 7-11)
-    // Slots of other blocks and of absent tokens may hold anything, and 0 * inf is not 0: values
-    // that are not finite leave the tile, and the rows that see one get it at the end.
-    bool odd = false;
-    for (int j = 0; j < nC; ++j) {
-      for (int h = 0; h < 2; ++h) {
-        const int u = 2 * j + h;
-        if (!mbar_wait(bars, &bars.full_v[u % SLOTS], (u / SLOTS) & 1, p.hdr, 473)) break;
-        uint4* v = reinterpret_cast<uint4*>(smem + OFF_V + (u % SLOTS) * kSlot);
-        for (int i = (warp - 7) * 32 + lane; i < BN * 8; i += kCleaners * 32) {
-          uint4 x = v[i];
-          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-          bool bad = false;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if ((w[e] & 0x7f80u) == 0x7f80u) {
-              w[e] &= 0xffff0000u;
-              bad = true;
-            }
-            if ((w[e] & 0x7f800000u) == 0x7f800000u) {
-              w[e] &= 0xffffu;
-              bad = true;
-            }
-          }
-          if (bad) {
-            v[i] = x;
-            odd = true;
-          }
-        }
-      }
-      if (odd) *reinterpret_cast<volatile int*>(&bars.odd_own) = 1;
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.own_clean[j & 1]);
-    }
-    __syncwarp();
-  }
 
   // ---- merge the S shares of every row in the CTA that owns it. Ring layout (bytes): staged
   // rows [BM][kRowB], received rows [sender][rpc][kRowB].
@@ -715,15 +735,9 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
   auto part = [&](int c, int i) -> const uint8_t* {
     return c == rank ? stage + (rb + i) * kRowB : recv + (c * rpc + i) * kRowB;
   };
-  if (warp < 4 || (warp >= 6 && warp < 10)) {
-    const int half = warp < 4 ? 0 : 1;
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t oa = tmem + TM_O + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * 64;
-    // warps 6-9 read O once warps 0-3 have seen the last P V product complete
-    __syncwarp();
-    tc_fence_before();
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    tc_fence_after();
+  if (softmax) {
+    const uint32_t oa = tmem + TM_O + lane_off + half * 64;
+    softmax_sync();                                        // both halves' sums are there
     uint32_t o[64];
     if (nT > 0) {
       load64(oa, o);
@@ -766,7 +780,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     float* tail = reinterpret_cast<float*>(stage + row * kRowB + 2 * DH);
     if (half == 0) {
       tail[0] = m;
-      tail[1] = l;
+      tail[1] = l + bars.pair[1][row];
     }
     // the sign tells the owner of the row to look closer
     const bool look = odd || (nC > 0 && *reinterpret_cast<volatile int*>(&bars.odd_own));
