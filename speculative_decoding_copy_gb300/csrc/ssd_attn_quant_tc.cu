@@ -30,8 +30,8 @@
 //   warp 4     TMEM allocation, then the producer of the K tiles;
 //   warp 6     the producer of the V tiles; it clears the value rows past the prefix (codes
 //              there may be NaN, and 0 * NaN is not 0);
-//   warp 5     the MMA-issuing thread, S three tiles ahead of the softmax;
-//   warp 7     joins the merge.
+//   warp 5     issues S = Q K^T, up to three tiles ahead of the softmax;
+//   warp 7     issues O += P V (two issuing threads, so that neither's waits hold the other back).
 // Shared memory: Q (64 KB), then four 16 KB slots each for K and V. A prefix tile takes one
 // slot of each, an own-block tile (bf16) two.
 // TMEM columns: S buffers 0-127, 128-255, 256-383, O 384-511.
@@ -83,7 +83,7 @@ static_assert(kMaxBlocks * 4 <= static_cast<int>(2 * SLOTS * kSlot), "block ends
 struct Bars {
   uint64_t full_k[SLOTS], full_v[SLOTS], empty_k[SLOTS], empty_v[SLOTS];
   uint64_t q_full;
-  uint64_t s_full[SBUF], p_full[SBUF], pv_done[2];
+  uint64_t s_full[SBUF], p_full[SBUF], s_free[SBUF], pv_done[2];
   uint64_t o_done;                        // every product into O is done
   uint64_t v_clean;                       // the value rows past the prefix are zeros
   uint64_t own_clean[2];                  // an own-block tile's values are finite
@@ -319,6 +319,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     for (int i = 0; i < 2; ++i) mbar_init(&bars.own_clean[i], kSoftmax);
     for (int i = 0; i < SBUF; ++i) {
       mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.s_free[i], 1);
       mbar_init(&bars.p_full[i], kSoftmax);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&bars.pv_done[i], 1);
@@ -658,75 +659,91 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       if (lane == 0) mbar_arrive(&bars.v_clean);
     }
   } else if (warp == 5) {
-    // ---------------------------------------------------------- MMA issuer
+    // ---------------------------------------------------------- S = Q K^T
+    // Descriptors of one operand differ in the address field alone (16-byte units, no carry out
+    // of it): one base and small sums keep the issue ahead of the tensor pipe's 64 clocks a product.
     if (lane == 0 && nT > 0) {
-      constexpr uint32_t idS = idesc_e4m3(false, BN), idPV = idesc_e4m3(true, DH);
-      constexpr uint32_t idSb = idesc_bf16(false, BN), idPVb = idesc_bf16(true, DH);
-      auto unit = [&](int j) -> int { return j < nC ? 2 * j : nC + j; };
-      auto issue_S = [&](int j) {
-        const int u = unit(j);
-        const uint32_t d = tmem + TM_S + (j % SBUF) * BN;
-        mbar_wait(bars, &bars.full_k[u % SLOTS], (u / SLOTS) & 1, p.hdr, 481);
-        if (j < nC) mbar_wait(bars, &bars.full_k[(u + 1) % SLOTS], ((u + 1) / SLOTS) & 1, p.hdr, 482);
+      constexpr uint32_t idS = idesc_e4m3(false, BN), idSb = idesc_bf16(false, BN);
+      const uint64_t q8 = sw128_desc(sbase + OFF_Q8, 16, 1024), qb = sw128_desc(sbase + OFF_QB, 16, 1024),
+                     k0 = sw128_desc(sbase + OFF_K, 16, 1024);
+      mbar_wait(bars, &bars.q_full, 0, p.hdr, 480);
+      int u = 0;
+      for (int j = 0; j < nT; ++j) {
+        const int sb = j % SBUF;
+        const uint32_t d = tmem + TM_S + sb * BN;
+        const bool own = j < nC;
+        const int s0 = u % SLOTS, s1 = (u + 1) % SLOTS;
+        // the buffer still holds P of tile j - SBUF until its product is done
+        if (j >= SBUF) mbar_wait(bars, &bars.s_free[sb], (j / SBUF - 1) & 1, p.hdr, 483);
+        mbar_wait(bars, &bars.full_k[s0], (u / SLOTS) & 1, p.hdr, 481);
+        if (own) mbar_wait(bars, &bars.full_k[s1], ((u + 1) / SLOTS) & 1, p.hdr, 482);
         tc_fence_after();
-        const uint32_t kb = sbase + OFF_K + (u % SLOTS) * kSlot;
-        if (j < nC) {
+        const uint64_t kd = k0 + static_cast<uint32_t>(s0) * (kSlot / 16);
+        if (own) {
 #pragma unroll
           for (int ks = 0; ks < DH / 16; ++ks)
-            mma_bf16(d, sw128_desc(sbase + OFF_QB + (ks >> 2) * kSlot + (ks & 3) * 32, 16, 1024),
-                     sw128_desc(kb + (ks >> 2) * kSlot + (ks & 3) * 32, 16, 1024), idSb, ks > 0 ? 1u : 0u);
+            mma_bf16(d, qb + (ks >> 2) * (kSlot / 16) + (ks & 3) * 2, kd + (ks >> 2) * (kSlot / 16) + (ks & 3) * 2, idSb,
+                     ks > 0 ? 1u : 0u);
         } else {
 #pragma unroll
           for (int ks = 0; ks < DH / 32; ++ks) {
-            const uint64_t bd = sw128_desc(kb + ks * 32, 16, 1024);
-            mma_e4m3(d, sw128_desc(sbase + OFF_Q8 + ks * 32, 16, 1024), bd, idS, ks > 0 ? 1u : 0u);
-            mma_e4m3(d, sw128_desc(sbase + OFF_Q8 + kSlot + ks * 32, 16, 1024), bd, idS, 1u);
+            mma_e4m3(d, q8 + ks * 2, kd + ks * 2, idS, ks > 0 ? 1u : 0u);
+            mma_e4m3(d, q8 + kSlot / 16 + ks * 2, kd + ks * 2, idS, 1u);
           }
         }
-        mma_commit(&bars.s_full[j % SBUF]);
-        mma_commit(&bars.empty_k[u % SLOTS]);
-        if (j < nC) mma_commit(&bars.empty_k[(u + 1) % SLOTS]);
-      };
-      mbar_wait(bars, &bars.q_full, 0, p.hdr, 480);
-      for (int j = 0; j < SBUF && j < nT; ++j) issue_S(j);
+        mma_commit(&bars.s_full[sb]);
+        mma_commit(&bars.empty_k[s0]);
+        if (own) mma_commit(&bars.empty_k[s1]);
+        u += own ? 2 : 1;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- O += P V (warp 7)
+    if (lane == 0 && nT > 0) {
+      constexpr uint32_t idPV = idesc_e4m3(true, DH), idPVb = idesc_bf16(true, DH);
+      const uint64_t v0 = sw128_desc(sbase + OFF_V, kSlot, 1024);
+      int u = 0;
       for (int j = 0; j < nT; ++j) {
-        const int u = unit(j);
-        mbar_wait(bars, &bars.p_full[j % SBUF], (j / SBUF) & 1, p.hdr, 483);
-        mbar_wait(bars, &bars.full_v[u % SLOTS], (u / SLOTS) & 1, p.hdr, 484);
-        if (j < nC) mbar_wait(bars, &bars.full_v[(u + 1) % SLOTS], ((u + 1) / SLOTS) & 1, p.hdr, 485);
-        if (j < nC) mbar_wait(bars, &bars.own_clean[j & 1], (j >> 1) & 1, p.hdr, 487);
+        const int sb = j % SBUF;
+        const bool own = j < nC;
+        const int s0 = u % SLOTS, s1 = (u + 1) % SLOTS;
+        mbar_wait(bars, &bars.full_v[s0], (u / SLOTS) & 1, p.hdr, 484);
+        if (own) {
+          mbar_wait(bars, &bars.full_v[s1], ((u + 1) / SLOTS) & 1, p.hdr, 485);
+          mbar_wait(bars, &bars.own_clean[j & 1], (j >> 1) & 1, p.hdr, 487);
+        }
         if (ragged && j == nT - 1) mbar_wait(bars, &bars.v_clean, 0, p.hdr, 486);
+        mbar_wait(bars, &bars.p_full[sb], (j / SBUF) & 1, p.hdr, 488);
         tc_fence_after();
-        const uint32_t vb = sbase + OFF_V + (u % SLOTS) * kSlot;
-        const uint32_t pa = tmem + TM_S + (j % SBUF) * BN;
-        if (j < nC) {
+        const uint64_t vd = v0 + static_cast<uint32_t>(s0) * (kSlot / 16);
+        const uint32_t pa = tmem + TM_S + sb * BN;
+        if (own) {
 #pragma unroll
           for (int ks = 0; ks < BN / 16; ++ks)
-            mma_bf16_ts(tmem + TM_O, pa + ks * 8, sw128_desc(vb + ks * 16 * 128, kSlot, 1024), idPVb,
-                        (j > 0 || ks > 0) ? 1u : 0u);
+            mma_bf16_ts(tmem + TM_O, pa + ks * 8, vd + ks * (16 * 128 / 16), idPVb, (j > 0 || ks > 0) ? 1u : 0u);
         } else {
 #pragma unroll
           for (int ks = 0; ks < BN / 32; ++ks) {
-            const uint64_t bd = sw128_desc(vb + ks * 32 * 128, kSlot, 1024);
-            mma_e4m3_ts(tmem + TM_O, pa + ks * 8, bd, idPV, (j > 0 || ks > 0) ? 1u : 0u);
-            mma_e4m3_ts(tmem + TM_O, pa + P2 + ks * 8, bd, idPV, 1u);
+            mma_e4m3_ts(tmem + TM_O, pa + ks * 8, vd + ks * (32 * 128 / 16), idPV, (j > 0 || ks > 0) ? 1u : 0u);
+            mma_e4m3_ts(tmem + TM_O, pa + P2 + ks * 8, vd + ks * (32 * 128 / 16), idPV, 1u);
           }
         }
+        mma_commit(&bars.s_free[sb]);
         mma_commit(&bars.pv_done[j & 1]);
-        mma_commit(&bars.empty_v[u % SLOTS]);
-        if (j < nC) mma_commit(&bars.empty_v[(u + 1) % SLOTS]);
-        // products of one kind run in the order issued: P V above reads P_j before S of tile
-        // j + SBUF overwrites it. Between the kinds the order is made.
-        if (j < nC) {
-          mbar_wait(bars, &bars.pv_done[j & 1], (j >> 1) & 1, p.hdr, 488);
+        mma_commit(&bars.empty_v[s0]);
+        if (own) mma_commit(&bars.empty_v[s1]);
+        u += own ? 2 : 1;
+        // the two kinds of products into O: the order between them is made
+        if (own) {
+          mbar_wait(bars, &bars.s_free[sb], (j / SBUF) & 1, p.hdr, 489);
           tc_fence_after();
         }
-        if (j + SBUF < nT) issue_S(j + SBUF);
       }
       mma_commit(&bars.o_done);
     }
+    __syncwarp();
   }
-
 
   // ---- merge the S shares of every row in the CTA that owns it. Ring layout (bytes): staged
   // rows [BM][kRowB], received rows [sender][rpc][kRowB].
