@@ -69,12 +69,13 @@ constexpr uint32_t OFF_QB = 2 * kSlot;    // bf16, two 64-column halves
 constexpr uint32_t OFF_K = 4 * kSlot;
 constexpr uint32_t OFF_V = OFF_K + SLOTS * kSlot;
 constexpr uint32_t OFF_BAR = OFF_V + SLOTS * kSlot;
-constexpr uint32_t kBarBytes = 2048;
+constexpr uint32_t kBarBytes = 3072;
 constexpr uint32_t kSmemBytes = OFF_BAR + kBarBytes + 1024;   // + slack to align the base to 1024
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr unsigned long long kWaitClocks = 1ull << 32;
 constexpr int kMaxSplit = 8;
 constexpr int kSoftmax = 256;             // softmax threads
+constexpr int FACTORS = 8;                // prefix tiles whose factors are kept
 constexpr int kRowB = 2 * DH + 16;        // one share's partial row as sent to its owner
 constexpr int kMaxBlocks = 8192;          // NB: the block ends are kept in the ring at first
 static_assert((2 * BM + kMaxSplit) * kRowB <= static_cast<int>(2 * SLOTS * kSlot), "merge buffers fit in the ring");
@@ -94,6 +95,8 @@ struct Bars {
   int seq, rows;                          // the sequence; its present rows
   int row_slot[BM];                       // candidate slot of a row of this tile
   float pair[2][BM];                      // a value of each half of a row
+  // of a prefix tile's eight groups of 16 keys: K factor, log2 of the V factor, 1 / V factor
+  float4 factors[FACTORS][3][2];
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
@@ -264,21 +267,22 @@ __device__ __forceinline__ float chunk_pairs(const uint32_t (&v)[64], uint32_t p
   return s0 + s1;
 }
 
-// whether `x` holds in any softmax thread, once all of them have come here (and read S)
-__device__ __forceinline__ bool any_row(bool x) {
+// the two warps of a lane quarter share its rows: barriers 1-4, 64 threads
+__device__ __forceinline__ void pair_sync(int quarter) {
+  __syncwarp();
+  asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(quarter + 1) : "memory");
+}
+// whether `x` holds in any thread of the pair, once both warps have come here (and read S)
+__device__ __forceinline__ bool any_row(bool x, int quarter) {
   uint32_t r;
   tc_fence_before();
   __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r) : "r"(x ? 1u : 0u) : "memory");
+      "barrier.cta.red.or.aligned.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"(x ? 1u : 0u), "r"(quarter + 1) : "memory");
   tc_fence_after();
   return r != 0;
-}
-__device__ __forceinline__ void softmax_sync() {
-  __syncwarp();
-  asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ kernel
@@ -307,7 +311,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
   }
   if (tid == 32) {
     for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(&bars.full_k[s], 1);
+      mbar_init(&bars.full_k[s], 2);                      // the copy, and the tile's factors
       mbar_init(&bars.full_v[s], 1);
       mbar_init(&bars.empty_k[s], 1);
       mbar_init(&bars.empty_v[s], 1);
@@ -436,7 +440,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
       }
       bars.pair[half][row] = __uint_as_float(top);
-      softmax_sync();
+      pair_sync(warp & 3);
       top = max(top, __float_as_uint(bars.pair[half ^ 1][row]));
       const int ex = static_cast<int>(top >> 23);
       const int up = min(254 + 7 - ex, 253);
@@ -480,13 +484,13 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     // under it (each half rescales its 64 columns of O).
     auto move_refs = [&](int j, float mx) {
       bars.pair[half][row] = mx;
-      softmax_sync();
+      pair_sync(warp & 3);
       const float m_new = fmaxf(m, fmaxf(mx, bars.pair[half ^ 1][row]));
       const bool need = m_new > m + kLag;
       const float alpha = need ? ex2_approx(m - m_new) : 1.f;
       if (need) m = m_new;
       l *= alpha;
-      softmax_sync();                                    // the pairs may be written again
+      pair_sync(warp & 3);                                    // the pairs may be written again
       if (j > 0 && __any_sync(0xffffffffu, need)) {
         // O holds the sum up to tile j - 1: wait for its last product, then rescale
         mbar_wait(bars, &bars.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.hdr, 461);
@@ -552,52 +556,28 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         f.lv[q] = 0.f;
       }
       const float mx = chunk_max<true>(v, f, lo, hi);
-      if (any_row(mx > m + kLag)) move_refs(j, mx);
+      if (any_row(mx > m + kLag, warp & 3)) move_refs(j, mx);
       l += chunk_pairs(v, sp + half * 32, p.scale_log2, lo, hi, m == -INFINITY ? 0.f : m);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bars.p_full[sb]);
     }
-    // ---- prefix tiles. Lane i < 4 holds the K scale of this half's group i, lane 4 + i the V
-    // scale: loaded a tile ahead, and the page a tile ahead of them.
-    auto load_page = [&](int t) -> int {
-      if (t >= j1 || p.block_table == nullptr) return b;
-      return p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + t];
-    };
-    auto load_scale = [&](int t, int pg) -> float {
-      if (t >= j1 || lane >= 8) return 0.f;
-      int place = half * 64 + (lane & 3) * 16;
-      if (p.block_table == nullptr) place += t * BN;
-      if (pg < 0 || pg >= p.num_pages) pg = 0;
-      const int blocks = static_cast<int>(p.blocks);
-      const int blk = min(place >> p.sb_log2, blocks - 1);
-      return (lane < 4 ? p.k_scale : p.v_scale)[static_cast<int64_t>(pg * p.Hkv + kvh) * blocks + blk];
-    };
-    float next_scale = load_scale(j0, load_page(j0));
-    int next_page = load_page(j0 + 1);
+    // ---- prefix tiles
     for (int t = j0; t < j1; ++t) {
       const int j = nC + t - j0, sb = j % SBUF;
-      // lanes 0-3: K factor; 4-7: log2 of the V factor
-      const float lane_f = lane < 4 ? next_scale : fmaxf(__log2f(next_scale), kLeastVScaleLog2);
-      const float lane_w = ex2_approx(-lane_f);            // lanes 4-7: 1 / V factor
-      next_scale = load_scale(t + 1, next_page);
-      next_page = load_page(t + 2);
-      Groups f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f.k[q] = __shfl_sync(0xffffffffu, lane_f, q) * q_mul;
-        f.lv[q] = __shfl_sync(0xffffffffu, lane_f, 4 + q);
-        f.w[q] = __shfl_sync(0xffffffffu, lane_w, 4 + q);
-      }
       mbar_wait(bars, &bars.s_full[sb], (j / SBUF) & 1, p.hdr, 460);
       __syncwarp();
       tc_fence_after();
       const uint32_t sp = tmem + TM_S + sb * BN + lane_off;
+      // the factors were written before the tile's products were issued
+      const float4(&ft)[3][2] = bars.factors[(t - j0) % FACTORS];
+      const float4 fk = ft[0][half], fl = ft[1][half], fw = ft[2][half];
+      const Groups f = {{fk.x * q_mul, fk.y * q_mul, fk.z * q_mul, fk.w * q_mul}, {fl.x, fl.y, fl.z, fl.w}, {fw.x, fw.y, fw.z, fw.w}};
       load64(sp + half * 64, v);
       const int hi = P - t * BN - half * 64;
       const bool full = P - t * BN >= BN;
       const float mx = full ? chunk_max<false>(v, f, 0, 0) : chunk_max<true>(v, f, 0, hi);
-      if (any_row(mx > m + kLag)) move_refs(j, mx);
+      if (any_row(mx > m + kLag, warp & 3)) move_refs(j, mx);
       const float ref = m == -INFINITY ? 0.f : m;
       l += full ? chunk_parts<false>(v, sp + half * 16, f, 0, ref) : chunk_parts<true>(v, sp + half * 16, f, hi, ref);
       tmem_wait_st();
@@ -612,40 +592,73 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     tc_fence_after();
   } else if (warp == 4 || warp == 6) {
     // ---------------------------------------------------------- producers (4: K, 6: V)
+    // Unit u goes to slot u % SLOTS: the two halves of an own-block tile, or a prefix tile. Lanes
+    // 0-15 of the K side also fetch a prefix tile's K and V scales, two tiles ahead of the copy
+    // (and the page a tile ahead of them), and leave the factors made of them in shared memory:
+    // a tile's products, whose end the softmax waits for, start only after them. Their place is
+    // free by then: this copy's slot was left by the products of the tile four before, which
+    // waited for the softmax of the tile seven before.
     const bool kside = warp == 4;
     uint64_t* full = kside ? bars.full_k : bars.full_v;
     uint64_t* empty = kside ? bars.empty_k : bars.empty_v;
     const uint32_t ring = sbase + (kside ? OFF_K : OFF_V);
-    if (lane == 0) {
-      // unit u goes to slot u % SLOTS: the two halves of an own-block tile, or a prefix tile
-      auto slot_for = [&](int u) -> bool {
-        if (u >= SLOTS) mbar_wait(bars, &empty[u % SLOTS], ((u / SLOTS) - 1) & 1, p.hdr, kside ? 470 : 471);
-        if (bars.failed) return false;
-        mbar_expect_tx(&full[u % SLOTS], kSlot);
-        return true;
-      };
-      int u = 0;
-      for (int j = 0; j < nC; ++j) {
-        for (int h = 0; h < 2; ++h, ++u) {
-          if (!slot_for(u)) break;
+    auto slot_for = [&](int u) {
+      if (u >= SLOTS) mbar_wait(bars, &empty[u % SLOTS], ((u / SLOTS) - 1) & 1, p.hdr, kside ? 470 : 471);
+      __syncwarp();
+    };
+    int u = 0;
+    for (int j = 0; j < nC; ++j) {
+      for (int h = 0; h < 2; ++h, ++u) {
+        slot_for(u);
+        if (lane == 0 && !bars.failed) {
+          if (kside) mbar_arrive(&full[u % SLOTS]);        // no factors
+          mbar_expect_tx(&full[u % SLOTS], kSlot);
           tma_load_3d(ring + (u % SLOTS) * kSlot, kside ? &tmap_kc : &tmap_vc, 64 * h, kvh, b * NT + s_base + j * BN,
                       &full[u % SLOTS]);
         }
       }
-      for (int j = j0; j < j1; ++j, ++u) {
-        int pg = b, place = j * BN;
-        if (p.block_table != nullptr) {
-          pg = __ldg(p.block_table + static_cast<int64_t>(b) * p.pages_per_seq + j);
-          place = 0;
-          if (pg < 0 || pg >= p.num_pages) {
-            record_error(p.hdr, SSD_ERR_DEVICE, 451);
-            pg = 0;
-          }
-        }
-        if (!slot_for(u)) break;
+    }
+    auto load_page = [&](int t) -> int {
+      if (t >= j1 || p.block_table == nullptr) return b;
+      const int pg = __ldg(p.block_table + static_cast<int64_t>(b) * p.pages_per_seq + t);
+      if (pg >= 0 && pg < p.num_pages) return pg;
+      if (lane == 0) record_error(p.hdr, SSD_ERR_DEVICE, 451);
+      return 0;
+    };
+    const int blocks = static_cast<int>(p.blocks);
+    auto load_scale = [&](int t, int pg) -> float {
+      if (!kside || t >= j1 || lane >= 16) return 0.f;
+      const int place = (p.block_table == nullptr ? t * BN : 0) + (lane & 7) * 16;
+      const int blk = min(place >> p.sb_log2, blocks - 1);
+      return __ldg((lane < 8 ? p.k_scale : p.v_scale) + static_cast<int64_t>(pg * p.Hkv + kvh) * blocks + blk);
+    };
+    int page = load_page(j0), page1 = load_page(j0 + 1), page2 = load_page(j0 + 2);
+    float scale = load_scale(j0, page), scale1 = load_scale(j0 + 1, page1);
+    for (int t = j0; t < j1; ++t, ++u) {
+      slot_for(u);
+      if (lane == 0 && !bars.failed) {
+        mbar_expect_tx(&full[u % SLOTS], kSlot);
         tma_load_2d(ring + (u % SLOTS) * kSlot, kside ? &tmap_k : &tmap_v, 0,
-                    (pg * p.Hkv + kvh) * static_cast<int>(p.page_tokens) + place, &full[u % SLOTS]);
+                    (page * p.Hkv + kvh) * static_cast<int>(p.page_tokens) + (p.block_table == nullptr ? t * BN : 0),
+                    &full[u % SLOTS]);
       }
+      if (kside) {
+        float* at = reinterpret_cast<float*>(bars.factors[(t - j0) % FACTORS]);
+        if (lane < 8) {
+          at[lane] = scale;
+        } else if (lane < 16) {
+          const float lv = fmaxf(__log2f(scale), kLeastVScaleLog2);
+          at[lane] = lv;
+          at[lane + 8] = ex2_approx(-lv);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[u % SLOTS]);
+      }
+      scale = scale1;
+      scale1 = load_scale(t + 2, page2);
+      page = page1;
+      page1 = page2;
+      page2 = load_page(t + 3);
     }
     __syncwarp();
     if (!kside && ragged) {
@@ -754,7 +767,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
   };
   if (softmax) {
     const uint32_t oa = tmem + TM_O + lane_off + half * 64;
-    softmax_sync();                                        // both halves' sums are there
+    pair_sync(warp & 3);                                        // both halves' sums are there
     uint32_t o[64];
     if (nT > 0) {
       load64(oa, o);
