@@ -488,12 +488,12 @@ def _cache_fits(shape, B, block_table, device):
     return block_table.data_ptr(), pps
 
 
-def _new_on(stream, make):
-    """make() with `stream` current, so that a fresh tensor's memory belongs to the stream it is used on."""
+def _new(stream, shape, dtype, device, make=torch.empty):
+    """A fresh tensor whose memory belongs to the stream it is used on."""
     if stream is None:
-        return make()
+        return make(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return make()
+        return make(shape, dtype=dtype, device=device)
 
 
 def _quant_call(fn, args, ws, device, stream, *named):
@@ -502,7 +502,7 @@ def _quant_call(fn, args, ws, device, stream, *named):
     the (name, tensor) pairs that must not overlap, to name those for which the call was
     refused."""
     if ws is None:
-        ws = _new_on(stream, lambda: torch.zeros(256, dtype=torch.uint8, device=device))
+        ws = _new(stream, 256, torch.uint8, device, torch.zeros)
     elif ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
     if stream is None:
@@ -544,14 +544,17 @@ def ssd_page_tables(cur_len, add_len, n_pages, block_table, free_pages, n_free, 
         raise ValueError("slot_cap must not be negative")
     o = {} if out is None else out
     start, slots, served = o.get("row_start"), o.get("slot_map"), o.get("served")
-    if start is None and slots is None and served is None:
-        buf = _new_on(stream, lambda: torch.empty(cap + 2 * B + 1, dtype=torch.int32, device=dev))
-        slots, start, served = buf.split((cap, B + 1, B))
+    if start is None:
+        start = _new(stream, B + 1, torch.int32, dev)
     else:
-        make = lambda n: _new_on(stream, lambda: torch.empty(n, dtype=torch.int32, device=dev))
-        start, slots, served = (make(n) if t is None else t for t, n in ((start, B + 1), (slots, cap), (served, B)))
         _need_shape(start, "row_start", _I32, (B + 1,), dev)
+    if slots is None:
+        slots = _new(stream, cap, torch.int32, dev)
+    else:
         _need_shape(slots, "slot_map", _I32, (cap,), dev)
+    if served is None:
+        served = _new(stream, B, torch.int32, dev)
+    else:
         _need_shape(served, "served", _I32, (B,), dev)
     args = PagesArgs(cur_len.data_ptr(), add_len.data_ptr(), n_pages.data_ptr(), block_table.data_ptr(),
                      free_pages.data_ptr(), n_free.data_ptr(), start.data_ptr(), slots.data_ptr() if cap else None,
@@ -613,7 +616,7 @@ def ssd_commit_kv_quant(k_cache, v_cache, k_scale, v_scale, k_cand, v_cand, pref
     if Dmax < 1 or NT % Dmax:
         raise ValueError(f"{NT} candidate slots are no whole blocks of {Dmax}")
     if new_len is None:
-        new_len = _new_on(stream, lambda: torch.empty_like(prefix_len))
+        new_len = _new(stream, B, torch.int32, dev)
     else:
         _need_shape(new_len, "new_len", _I32, (B,), dev)
     args = CommitQuantArgs(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
@@ -661,7 +664,7 @@ def ssd_verify_attn_quant(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand,
     if shape[3] != dh:
         raise ValueError(f"k_cache holds rows of {shape[3]} elements, q of {dh}")
     if out is None:
-        out = _new_on(stream, lambda: torch.empty(q.shape, dtype=torch.float32 if out_f32 else q.dtype, device=dev))
+        out = _new(stream, q.shape, torch.float32 if out_f32 else q.dtype, dev)
     else:
         _need_shape(out, "out", _ROWS, q.shape, dev)
     args = attn_quant_args(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand, prefix_len, blk_len, Dmax,

@@ -23,17 +23,6 @@ struct QuantDst {
   int row;              // first place written
 };
 
-// |x| of 8 elements, the largest finite one as fp32 bits (infinities and NaN do not count)
-__device__ __forceinline__ uint32_t amax8(const float (&x)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t u = __float_as_uint(x[e]) & 0x7fffffffu;
-    m = max(m, u < 0x7f800000u ? u : 0u);
-  }
-  return m;
-}
-
 // the least power of two s with a <= 448 s (448 = 1.75 * 2^8), at least 2^-100; a as bits
 __device__ __forceinline__ float pow2_scale(uint32_t a) {
   const int e = static_cast<int>(a >> 23) - 127;
@@ -41,21 +30,26 @@ __device__ __forceinline__ float pow2_scale(uint32_t a) {
   return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
-// x / s, by the exact reciprocal where s is a power of two (|exponent| <= 126)
-struct Divider {
-  float s, inv;
-  bool pow2;
-  __device__ __forceinline__ explicit Divider(float sc) : s(sc) {
-    const uint32_t u = __float_as_uint(sc);
-    const int e = static_cast<int>(u >> 23);
-    pow2 = (u & 0x7fffffu) == 0 && e >= 1 && e <= 253;
-    inv = pow2 ? __uint_as_float(static_cast<uint32_t>(254 - e) << 23) : 0.f;
-  }
-  __device__ __forceinline__ float operator()(float x) const { return pow2 ? x * inv : __fdiv_rn(x, s); }
-};
+// 1 / s where s is a power of two whose reciprocal is normal, else 0
+__device__ __forceinline__ float exact_reciprocal(float s) {
+  const uint32_t u = __float_as_uint(s);
+  const uint32_t e = u >> 23;
+  return (u & 0x7fffffu) == 0 && e >= 1 && e <= 253 ? __uint_as_float((254 - e) << 23) : 0.f;
+}
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// off the common path: its code is kept out of the loops
+__device__ __noinline__ float divide(float x, float s) { return __fdiv_rn(x, s); }
+
+// 8 elements of a row. top: an upper bound of their magnitudes, as fp32 bits, that is exact unless
+// one is not finite (then >= 0x7f800000); finite_top: the largest finite one.
 template <typename T>
-struct Word;             // 8 elements of a row
+struct Word;
 template <>
 struct Word<uint16_t> {
   uint4 a;
@@ -67,6 +61,10 @@ struct Word<uint16_t> {
       x[2 * i] = __uint_as_float(w[i] << 16);
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = max_u16x2(max_u16x2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu), max_u16x2(a.z & 0x7fff7fffu, a.w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
   }
 };
 template <>
@@ -80,7 +78,28 @@ struct Word<float> {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
+  __device__ __forceinline__ uint32_t top() const {
+    float x[8];
+    get(x);
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+    return m;
+  }
 };
+
+template <typename T>
+__device__ __forceinline__ uint32_t finite_top(const Word<T>& w) {
+  float x[8];
+  w.get(x);
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t u = __float_as_uint(x[e]) & 0x7fffffffu;
+    m = max(m, u < 0x7f800000u ? u : 0u);
+  }
+  return m;
+}
 
 // Quantise n <= 128 rows of dh elements, `stride` elements apart at src, into places
 // d.row .. d.row + n - 1 of one block. Every thread of the CTA calls it; `red` holds one
@@ -90,23 +109,28 @@ __device__ __forceinline__ void quant_run(const T* __restrict__ src, int64_t str
                                           uint32_t* red) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int sh = dh == 128 ? 4 : 3;           // 8-element words per row
-  const int words = n << sh;
   constexpr int kWords = kMaxScaleBlock * 16 / kQuantThreads;
+  // word i of a thread: row row0 + i * rows_step, the same place in each
+  const int row0 = tid >> sh, rows_step = kQuantThreads >> sh;
+  const T* p = src + row0 * stride + ((tid & ((1 << sh) - 1)) << 3);
+  const int64_t step = rows_step * stride;
+  const int mine = row0 < n ? min(kWords, (n - 1 - row0) / rows_step + 1) : 0;
   const float old = *d.scale;
   Word<T> w[kWords];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < kWords; ++i) {
-    const int c = i * kQuantThreads + tid;
-    if (c < words) w[i].load(src + (c >> sh) * stride + ((c & ((1 << sh) - 1)) << 3));
+    if (i < mine) w[i].load(p);
+    p += step;
   }
 #pragma unroll
-  for (int i = 0; i < kWords; ++i) {
-    if (i * kQuantThreads + tid < words) {
-      float x[8];
-      w[i].get(x);
-      m = max(m, amax8(x));
-    }
+  for (int i = 0; i < kWords; ++i)
+    if (i < mine) m = max(m, w[i].top());
+  if (m >= 0x7f800000u) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      if (i < mine) m = max(m, finite_top<T>(w[i]));
   }
   m = __reduce_max_sync(0xffffffffu, m);
   __syncthreads();                            // `red` and the block's scale of an earlier run
@@ -134,35 +158,53 @@ __device__ __forceinline__ void quant_run(const T* __restrict__ src, int64_t str
       *p = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
     }
   }
-  const Divider by(now);
-  uint2* out = reinterpret_cast<uint2*>(d.codes) + (d.row << sh);
+  uint2* out = reinterpret_cast<uint2*>(d.codes) + (d.row << sh) + tid;
+  const float inv = exact_reciprocal(now);
+  if (inv != 0.f) {
 #pragma unroll
-  for (int i = 0; i < kWords; ++i) {
-    const int c = i * kQuantThreads + tid;
-    if (c < words) {
-      float x[8];
-      w[i].get(x);
-      out[c] = make_uint2(e4m3x2(by(x[0]), by(x[1])) | e4m3x2(by(x[2]), by(x[3])) << 16,
-                          e4m3x2(by(x[4]), by(x[5])) | e4m3x2(by(x[6]), by(x[7])) << 16);
+    for (int i = 0; i < kWords; ++i) {
+      if (i < mine) {
+        float x[8];
+        w[i].get(x);
+        out[i * kQuantThreads] = make_uint2(e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                                            e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+      }
+    }
+  } else {
+    // a scale that is no power of two: the caller's own, which this run left as it was
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if (i < mine) {
+        float x[8];
+        w[i].get(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = divide(x[e], now);
+        out[i * kQuantThreads] = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+      }
     }
   }
   __syncthreads();                            // every thread has read the old scale
   if (tid == 0) *d.scale = now;
 }
 
-// grid (row ranges of `range` rows, heads, keys / values): the runs that start in the range
+// grid (row ranges of `range` rows) x (heads, keys / values), the latter fastest, so that the CTAs
+// that share rows (and DRAM pages of a projection's output) run together: the runs that start
+// in the range
 template <typename T>
-__global__ void __launch_bounds__(kQuantThreads)
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2)
 k_append_quant(ssd_append_quant_args a, int range, int sb_log2, WsHeader* hdr) {
   __shared__ int32_t slot[2 * kMaxScaleBlock];
-  __shared__ uint32_t brk[2 * kMaxScaleBlock / 32];     // rows that do not continue the row before
+  constexpr int kMasks = 2 * kMaxScaleBlock / 32;
+  __shared__ uint32_t brk[kMasks];                      // rows that do not continue the row before
+  __shared__ uint32_t start[kMasks];                    // ... and have a slot
   __shared__ uint32_t red[kQuantThreads / 32];
   static_assert(kQuantThreads == 2 * kMaxScaleBlock, "one thread a row of the window");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x;
-  const int h = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * range;
+  const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(2 * a.Hkv));
+  const bool is_v = part >= a.Hkv;
+  const int h = is_v ? part - a.Hkv : part;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(2 * a.Hkv)) * range;
   const int sb = 1 << sb_log2;
   const int window = range + sb;                        // a run that starts in the range ends here
   // one thread a row: its slot, and whether it continues the run of the row before
@@ -177,40 +219,40 @@ k_append_quant(ssd_append_quant_args a, int range, int sb_log2, WsHeader* hdr) {
       s = -1;
     }
   }
-  const int32_t place = s >= 0 ? static_cast<int32_t>(s % a.page_tokens) : 0;
+  const uint32_t page_tokens = static_cast<uint32_t>(a.page_tokens);      // under 2^31, as every slot
+  const uint32_t place = s >= 0 ? static_cast<uint32_t>(s) % page_tokens : 0;
   const bool cont = s >= 0 && before == s - 1 && (place & (sb - 1)) != 0;
   slot[tid] = s;
   const uint32_t word = __ballot_sync(0xffffffffu, !cont);
-  if ((tid & 31) == 0) brk[tid >> 5] = word;
+  const uint32_t begins = __ballot_sync(0xffffffffu, !cont && s >= 0 && tid < range);
+  if ((tid & 31) == 0) {
+    brk[tid >> 5] = word;
+    start[tid >> 5] = begins;
+  }
   __syncthreads();
   const T* src = static_cast<const T*>(is_v ? a.v_new : a.k_new) + static_cast<int64_t>(h) * a.dh;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
   const int64_t blocks = (a.page_tokens + sb - 1) >> sb_log2;
-  for (int i = 0; i < range;) {
-    // next break at or after i
-    uint32_t bits = brk[i >> 5] & (0xffffffffu << (i & 31));
-    int wd = i >> 5;
-    while (bits == 0 && wd + 1 < 2 * kMaxScaleBlock / 32) bits = brk[++wd];
-    if (bits == 0) break;
-    const int first = wd * 32 + __ffs(static_cast<int>(bits)) - 1;
-    if (first >= range) break;
-    // the break after it ends the run (rows outside the list count as breaks)
-    bits &= bits - 1;
-    while (bits == 0 && wd + 1 < 2 * kMaxScaleBlock / 32) bits = brk[++wd];
-    const int last = bits != 0 ? wd * 32 + __ffs(static_cast<int>(bits)) - 1 : 2 * kMaxScaleBlock;
-    i = last;
-    const int32_t s0 = slot[first];
-    if (s0 < 0) continue;
-    const int64_t page = s0 / a.page_tokens;
-    const int off = static_cast<int>(s0 - page * a.page_tokens);
-    const int blk = off >> sb_log2;
-    const int64_t ph = page * a.Hkv + h;
-    QuantDst d;
-    d.codes = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) +
-              (ph * a.page_tokens + (static_cast<int64_t>(blk) << sb_log2)) * a.dh;
-    d.scale = (is_v ? a.v_scale : a.k_scale) + ph * blocks + blk;
-    d.row = off & (sb - 1);
-    quant_run<T>(src + (t0 + first) * stride, stride, last - first, a.dh, d, red);
+  for (int q = 0; q < kMasks; ++q) {
+    for (uint32_t left = start[q]; left != 0; left &= left - 1) {
+      const int first = q * 32 + __ffs(static_cast<int>(left)) - 1;
+      // the next break ends the run (rows outside the list or the window are breaks)
+      int wd = q;
+      uint32_t bits = brk[wd] & ~(0xffffffffu >> (31 - (first & 31)));
+      while (bits == 0 && wd + 1 < kMasks) bits = brk[++wd];
+      const int last = bits != 0 ? wd * 32 + __ffs(static_cast<int>(bits)) - 1 : 2 * kMaxScaleBlock;
+      const int32_t s0 = slot[first];
+      const uint32_t page = static_cast<uint32_t>(s0) / page_tokens;
+      const int off = static_cast<int>(static_cast<uint32_t>(s0) - page * page_tokens);
+      const int blk = off >> sb_log2;
+      const int64_t ph = static_cast<int64_t>(page) * a.Hkv + h;
+      QuantDst d;
+      d.codes = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) +
+                (ph * a.page_tokens + (static_cast<int64_t>(blk) << sb_log2)) * a.dh;
+      d.scale = (is_v ? a.v_scale : a.k_scale) + ph * blocks + blk;
+      d.row = off & (sb - 1);
+      quant_run<T>(src + (t0 + first) * stride, stride, last - first, a.dh, d, red);
+    }
   }
 }
 
@@ -297,7 +339,9 @@ extern "C" int ssd_append_kv_quant(const ssd_append_quant_args* a, void* ws, siz
   // up to a whole block's where most rows continue a run and their CTAs would find nothing
   int range = 1;
   while (range < a->scale_block && a->T * a->Hkv * 2 / range > 4096) range *= 2;
-  const dim3 grid(static_cast<unsigned>((a->T + range - 1) / range), static_cast<unsigned>(a->Hkv), 2);
+  const int64_t ctas = (a->T + range - 1) / range * 2 * a->Hkv;
+  if (ctas > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(ctas));
   const int lg = log2_of(a->scale_block);
   const cudaError_t e = a->dtype == SSD_BF16
       ? launch_pdl(k_append_quant<uint16_t>, grid, dim3(kQuantThreads), 0, s, *a, range, lg, hdr)
