@@ -8,13 +8,14 @@
 // search in the scan. Two passes over the batch, because the trimmed pages of all
 // sequences are on the stack before the first one is taken. The call is bound by latency:
 // it reads 12 bytes a sequence.
-// k_slot_map: one thread for four slots, the row's sequence by a binary search in
+// k_slot_map: one thread for four slots, the first one's sequence by a binary search in
 // row_start. Short maps are written by the plan kernel itself.
 #include "ssd_kvq.cuh"
 
 namespace ssd {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kMoves = 4;         // pages a thread has on the way at once
 
 struct SeqNeed {
   int64_t want;     // pages for cur + add tokens
@@ -68,19 +69,40 @@ __device__ __forceinline__ int last_not_above(const T* off, int n, T q) {
   return lo;
 }
 
-// slot of row t; `start` = row_start
-__device__ __forceinline__ int32_t slot_of(const ssd_pages_args& a, const int32_t* start, int64_t t, WsHeader* hdr) {
-  if (a.B == 0 || t >= start[a.B]) return -1;
-  const int b = last_not_above(start, a.B, static_cast<int32_t>(t));
-  const SeqNeed n = seq_need(a, b, a.n_pages[b]);
-  if (!n.ok || n.held < n.want) return -1;              // not served
-  const int64_t pos = static_cast<int64_t>(a.cur_len[b]) + (t - start[b]);
-  const int32_t page = a.block_table[static_cast<int64_t>(b) * a.pages_per_seq + pos / kPageTokens];
-  if (page < 0 || page >= a.num_pages) {
-    record_error(hdr, SSD_ERR_DEVICE, 410);
-    return -1;
+// slots of rows t .. t + 3, of which those below slot_cap are written; `start` = row_start
+__device__ __forceinline__ void fill_four(const ssd_pages_args& a, const int32_t* start, int64_t t, WsHeader* hdr) {
+  int32_t out[4] = {-1, -1, -1, -1};
+  const int64_t total = a.B > 0 ? start[a.B] : 0;
+  if (t < total) {
+    int b = last_not_above(start, a.B, static_cast<int32_t>(t));
+    int64_t begin = -1, end = -1;
+    const int32_t* table = nullptr;
+    bool served = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (t + e >= total) break;
+      if (t + e >= end) {                        // the first row, or the first one of another sequence
+        while (t + e >= start[b + 1]) ++b;
+        end = start[b + 1];
+        begin = static_cast<int64_t>(a.cur_len[b]) - start[b];
+        table = a.block_table + static_cast<int64_t>(b) * a.pages_per_seq;
+        const SeqNeed n = seq_need(a, b, a.n_pages[b]);
+        served = n.ok && n.held >= n.want;
+      }
+      if (!served) continue;
+      const int64_t pos = begin + t + e;
+      const int32_t page = table[pos / kPageTokens];
+      if (page < 0 || page >= a.num_pages) record_error(hdr, SSD_ERR_DEVICE, 410);
+      else out[e] = page * kPageTokens + static_cast<int32_t>(pos % kPageTokens);
+    }
   }
-  return page * kPageTokens + static_cast<int32_t>(pos % kPageTokens);
+  if (t + 4 <= a.slot_cap && (reinterpret_cast<uintptr_t>(a.slot_map) & 15) == 0) {
+    *reinterpret_cast<int4*>(a.slot_map + t) = make_int4(out[0], out[1], out[2], out[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (t + e < a.slot_cap) a.slot_map[t + e] = out[e];
+  }
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
@@ -114,12 +136,27 @@ k_page_plan(ssd_pages_args a, int fill_slots, WsHeader* hdr) {
       off[tid] = static_cast<int32_t>(at);
       base[tid] = want;
       __syncthreads();
-      for (int64_t q = tid; q < total; q += kPlanThreads) {
-        const int i = last_not_above(off, kPlanThreads, static_cast<int32_t>(q));
-        int32_t* entry = a.block_table + static_cast<int64_t>(b0 + i) * a.pages_per_seq + base[i] + (q - off[i]);
-        if (avail + q < a.num_pages) a.free_pages[avail + q] = *entry;
-        else record_error(hdr, SSD_ERR_DEVICE, 402);
-        *entry = -1;
+      for (int64_t q0 = tid; q0 < total; q0 += kMoves * kPlanThreads) {
+        int32_t* entry[kMoves];
+        int32_t page[kMoves];
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u) {
+          const int64_t q = q0 + u * kPlanThreads;
+          if (q < total) {
+            const int i = last_not_above(off, kPlanThreads, static_cast<int32_t>(q));
+            entry[u] = a.block_table + static_cast<int64_t>(b0 + i) * a.pages_per_seq + base[i] + (q - off[i]);
+            page[u] = *entry[u];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u) {
+          const int64_t q = q0 + u * kPlanThreads;
+          if (q < total) {
+            if (avail + q < a.num_pages) a.free_pages[avail + q] = page[u];
+            else record_error(hdr, SSD_ERR_DEVICE, 402);
+            *entry[u] = -1;
+          }
+        }
       }
       if (trim > 0) a.n_pages[b] = want;
     }
@@ -158,11 +195,25 @@ k_page_plan(ssd_pages_args a, int fill_slots, WsHeader* hdr) {
       off[tid] = static_cast<int32_t>(at);
       base[tid] = held;
       __syncthreads();
-      for (int64_t q = tid; q < take; q += kPlanThreads) {
-        const int i = last_not_above(off, kPlanThreads, static_cast<int32_t>(q));
-        const int32_t page = a.free_pages[avail - 1 - (lacked + q)];
-        if (page < 0 || page >= a.num_pages) record_error(hdr, SSD_ERR_DEVICE, 403);
-        a.block_table[static_cast<int64_t>(b0 + i) * a.pages_per_seq + base[i] + (q - off[i])] = page;
+      for (int64_t q0 = tid; q0 < take; q0 += kMoves * kPlanThreads) {
+        int32_t* entry[kMoves];
+        int32_t page[kMoves];
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u) {
+          const int64_t q = q0 + u * kPlanThreads;
+          if (q < take) {
+            page[u] = a.free_pages[avail - 1 - (lacked + q)];
+            const int i = last_not_above(off, kPlanThreads, static_cast<int32_t>(q));
+            entry[u] = a.block_table + static_cast<int64_t>(b0 + i) * a.pages_per_seq + base[i] + (q - off[i]);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u) {
+          if (q0 + u * kPlanThreads < take) {
+            if (page[u] < 0 || page[u] >= a.num_pages) record_error(hdr, SSD_ERR_DEVICE, 403);
+            *entry[u] = page[u];
+          }
+        }
       }
       if (serve && grow > 0) a.n_pages[b] = static_cast<int32_t>(held + grow);
     }
@@ -177,7 +228,7 @@ k_page_plan(ssd_pages_args a, int fill_slots, WsHeader* hdr) {
   }
   if (fill_slots) {
     __syncthreads();                          // tables and row_start are written
-    for (int64_t t = tid; t < a.slot_cap; t += kPlanThreads) a.slot_map[t] = slot_of(a, a.row_start, t, hdr);
+    for (int64_t t = 4 * tid; t < a.slot_cap; t += 4 * kPlanThreads) fill_four(a, a.row_start, t, hdr);
   }
 }
 
@@ -186,8 +237,8 @@ constexpr int kSlotThreads = 256;
 __global__ void __launch_bounds__(kSlotThreads)
 k_slot_map(ssd_pages_args a, WsHeader* hdr) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kSlotThreads + threadIdx.x;
-  if (t < a.slot_cap) a.slot_map[t] = slot_of(a, a.row_start, t, hdr);
+  const int64_t t = 4 * (static_cast<int64_t>(blockIdx.x) * kSlotThreads + threadIdx.x);
+  if (t < a.slot_cap) fill_four(a, a.row_start, t, hdr);
 }
 
 }  // namespace ssd
@@ -216,7 +267,7 @@ extern "C" int ssd_page_tables(const ssd_pages_args* a, void* ws, size_t ws_byte
   if (launch_pdl(k_page_plan, dim3(1), dim3(kPlanThreads), 0, s, *a, fill, hdr) != cudaSuccess) return SSD_ERR_CUDA;
   count_launch();
   if (!fill) {
-    const unsigned g = static_cast<unsigned>((a->slot_cap + kSlotThreads - 1) / kSlotThreads);
+    const unsigned g = static_cast<unsigned>((a->slot_cap + 4 * kSlotThreads - 1) / (4 * kSlotThreads));
     if (launch_pdl(k_slot_map, dim3(g), dim3(kSlotThreads), 0, s, *a, hdr) != cudaSuccess) return SSD_ERR_CUDA;
     count_launch();
   }
