@@ -77,6 +77,7 @@ struct Bars {
   uint64_t full_k[STAGES], full_v[STAGES], empty_k[STAGES], empty_v[STAGES];
   uint64_t q_full;
   uint64_t s_full[SBUF], p_full[SBUF], pv_done[2];
+  uint64_t o_done;                        // every product into O has completed
   uint64_t recv_full;                     // every other split's copy of the owned rows has arrived
   uint32_t tmem_base;
   int failed;
@@ -242,6 +243,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CU
       mbar_init(&bars.empty_v[s], 1);
     }
     mbar_init(&bars.q_full, 1);
+    mbar_init(&bars.o_done, 1);
     mbar_init(&bars.recv_full, 1);
     for (int i = 0; i < SBUF; ++i) {
       mbar_init(&bars.s_full[i], 1);
@@ -327,7 +329,9 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CU
       mbar_arrive(&bars.p_full[sb]);
     }
     if (nT > 0) {
-      mbar_wait(bars, &bars.pv_done[(nT - 1) & 1], ((nT - 1) >> 1) & 1, p.hdr, 13);
+      // S runs three tiles ahead, so the last three P V products may still be open here: a wait on
+      // pv_done, two phases back, could take an earlier phase of the same parity for the last one
+      mbar_wait(bars, &bars.o_done, 0, p.hdr, 13);
       tc_fence_after();
     }
   } else if (warp == 4 || warp == 6) {
@@ -416,6 +420,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CU
         // the order issued, so the P V product above has read P_j before it is overwritten
         if (j + SBUF < nT) issue_S(j + SBUF);
       }
+      mma_commit(&bars.o_done);
     }
   }
 
@@ -439,8 +444,7 @@ k_attn_tc(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CU
     const int half = warp < 4 ? 0 : 1;
     const int row = (warp & 3) * 32 + lane;          // this warp's TMEM lane quarter
     const uint32_t oa = tmem + TM_O + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * 64;
-    // warps 6-9 read O once warps 0-3 have seen the last P V product complete (a parity
-    // wait on pv_done is only valid for a waiter at most one phase behind, as those are)
+    // warps 6-9 read O once warps 0-3 have seen the last P V product complete
     tc_fence_before();
     asm volatile("bar.sync 1, 256;" ::: "memory");
     tc_fence_after();
