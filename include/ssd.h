@@ -539,8 +539,8 @@ int ssd_commit_kv_quant(const ssd_commit_quant_args* a, void* ws, size_t ws_byte
  * scales past prefix_len are never used (they may hold anything); blocks need no scale
  * before their first token.
  * Scores, maxima and sums are fp32, products exact in fp32; the probabilities are rounded
- * to 11 bits (fp16) or to a sum of two e4m3 numbers (about 8 bits) before they weight the
- * values, the candidates' to bf16 or better.
+ * to 11 bits (fp16), or over many rows to the sum of an e4m3 and an e5m2 number (about 8
+ * bits), before they weight the values, the candidates' to bf16 or better.
  * Supported: dh 64 or 128; Hq % Hkv == 0, Hq / Hkv <= 64; 1 <= Dmax <= 256,
  * NB * Dmax <= 8192; scale_block 16, 32, 64 or 128; 16-byte aligned tensors;
  * num_pages * 128 * Hkv < 2^31 (B * Hkv * P_max < 2^31); else SSD_ERR_UNSUPPORTED.

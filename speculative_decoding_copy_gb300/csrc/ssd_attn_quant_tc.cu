@@ -2,13 +2,16 @@
 // (tcgen05): a verification of many candidate tokens. The mathematics is that of
 // ssd_attn_quant.cu; what differs is who does the products.
 //
-// Precision on e4m3 operands. The codes go into the products as they lie in the cache
-// (kind::f8f6f4, fp32 sums). Q and P, which have more bits, are sums of two e4m3 numbers, one
-// product each into the same accumulator: q (8 significant bits) splits exactly, down to 2^-17
-// of its row's largest; a probability keeps 8 bits (as bf16 would), with an absolute floor of
-// 2^-14 of the largest. Two e4m3 products cost what one bf16 product costs, and no code is
-// converted. (Converting each tile to fp16 in shared memory would move 64 KB more per tile
-// through shared memory, which the products already keep three quarters busy.)
+// Precision on 8-bit operands. The codes go into the products as they lie in the cache
+// (kind::f8f6f4, fp32 sums). Q and P, which have more bits, are sums of two 8-bit numbers, one
+// product each into the same accumulator. q (8 significant bits) is two e4m3 numbers, exact but
+// for what lies under 2^-17 of its row's largest element. A probability is an e4m3 number and,
+// for what is left, an e5m2 number: its relative error is about that of one bf16 number, and
+// e5m2's range carries small probabilities (the long tail of a long prefix) down to 2^-21 of
+// the largest. Two 8-bit products cost what one bf16 product costs, and no code is converted.
+// (Converting each tile to fp16 in shared memory would move 64 KB more per tile through it,
+// which the products already keep three quarters busy; with e4m3 for what is left, 2^-14 of
+// the largest, the output of 32768 keys was 0.0018 off beside its own rounding's 0.0017.)
 //
 // Rows. The G query heads of the present tokens pack into rows (absent tokens take none, so a
 // batch with few present candidates runs few row tiles); a CTA owns 128 of them and one share
@@ -23,10 +26,10 @@
 //              weight 1/sv of the sum. A barrier tells all rows whether any reference has to
 //              move, which is rare. P goes back to TMEM over the first half of the tile's S
 //              buffer (two parts of 32 columns, four keys a word; bf16 pairs for own-block
-//              tiles). In fp16 with the exponent offset of the two formats taken into the
-//              exponential, the first part is the upper byte of a probability's bits and the
-//              second the rounded upper byte of what is left, so no format conversion is
-//              needed. On rank 0 they also take infinities and NaN out of own-block values;
+//              tiles). In fp16 with the exponent offset of the formats taken into the
+//              exponential, the parts are bytes of a probability's bits and of what is left,
+//              so no format conversion is needed. On rank 0 they also take infinities and NaN
+//              out of own-block values;
 //   warp 4     TMEM allocation, then the producer of the K tiles;
 //   warp 6     the producer of the V tiles; it clears the value rows past the prefix (codes
 //              there may be NaN, and 0 * NaN is not 0);
@@ -104,12 +107,12 @@ __device__ __forceinline__ bool mbar_wait(Bars& bars, uint64_t* bar, uint32_t pa
   return mbar_wait_bounded(bar, parity, &bars.failed, hdr, where, kWaitClocks);
 }
 
-// instruction descriptor, kind::f8f6f4: e4m3 A and B, fp32 D, M = 128, N = n
-__host__ __device__ constexpr uint32_t idesc_e4m3(bool b_mn_major, uint32_t n) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+// instruction descriptor, kind::f8f6f4: A e4m3 (or e5m2), B e4m3, fp32 D, M = 128, N = n
+__host__ __device__ constexpr uint32_t idesc_f8(bool a_e5m2, bool b_mn_major, uint32_t n) {
+  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_mn_major ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -119,7 +122,7 @@ __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b
 }
 
 // A in TMEM: M rows on the lanes, four K elements a column
-__device__ __forceinline__ void mma_e4m3_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_f8_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -206,7 +209,7 @@ __device__ __forceinline__ float chunk_max(const uint32_t (&v)[64], const Groups
   return top;
 }
 
-// prefix tile: 2^(y - ref + lift) as two e4m3 parts, four keys a word, at paddr and paddr + P2;
+// prefix tile: 2^(y - ref + lift) as an e4m3 and an e5m2 part, four keys a word, at paddr and paddr + P2;
 // returns the sum weighted by 1 / V factor
 template <bool MASK>
 __device__ __forceinline__ float chunk_parts(const uint32_t (&v)[64], uint32_t paddr, const Groups& f, int hi, float ref) {
@@ -214,7 +217,8 @@ __device__ __forceinline__ float chunk_parts(const uint32_t (&v)[64], uint32_t p
   float total = 0.f;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    // fp16 bits of p * 2^-8 are, from bit 7 up, the bits of p's e4m3 number
+    // fp16 bits of p * 2^-8 are, from bit 7 up, the bits of p's e4m3 number; those of a number
+    // itself are, from bit 8 up, its e5m2 number's
     const float off = f.lv[q] - ref + (kLift - 8.f);
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -233,9 +237,11 @@ __device__ __forceinline__ float chunk_parts(const uint32_t (&v)[64], uint32_t p
         add2(s0, s1, x, y);
         uint32_t w, left;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(left) : "r"(w), "r"(w & 0xff80ff80u));
-        t1[h] = w + w;                              // the first part in each upper byte
-        t2[h] = left + left + 0x00800080u;          // the rest, rounded
+        const uint32_t near = w + 0x00400040u;      // rounded to e4m3 above bit 7
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(left) : "r"(w), "r"(near & 0xff80ff80u));
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(left) : "r"(left), "r"(0x5c005c00u));    // 2^8
+        t1[h] = near + near;                        // the first part in each upper byte
+        t2[h] = left + 0x00800080u;                 // the rest, rounded to e5m2 in each upper byte
       }
       p1[c / 4] = __byte_perm(t1[0], t1[1], 0x7531);
       p2[c / 4] = __byte_perm(t2[0], t2[1], 0x7531);
@@ -676,7 +682,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     // Descriptors of one operand differ in the address field alone (16-byte units, no carry out
     // of it): one base and small sums keep the issue ahead of the tensor pipe's 64 clocks a product.
     if (lane == 0 && nT > 0) {
-      constexpr uint32_t idS = idesc_e4m3(false, BN), idSb = idesc_bf16(false, BN);
+      constexpr uint32_t idS = idesc_f8(false, false, BN), idSb = idesc_bf16(false, BN);
       const uint64_t q8 = sw128_desc(sbase + OFF_Q8, 16, 1024), qb = sw128_desc(sbase + OFF_QB, 16, 1024),
                      k0 = sw128_desc(sbase + OFF_K, 16, 1024);
       mbar_wait(bars, &bars.q_full, 0, p.hdr, 480);
@@ -700,8 +706,8 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         } else {
 #pragma unroll
           for (int ks = 0; ks < DH / 32; ++ks) {
-            mma_e4m3(d, q8 + ks * 2, kd + ks * 2, idS, ks > 0 ? 1u : 0u);
-            mma_e4m3(d, q8 + kSlot / 16 + ks * 2, kd + ks * 2, idS, 1u);
+            mma_f8(d, q8 + ks * 2, kd + ks * 2, idS, ks > 0 ? 1u : 0u);
+            mma_f8(d, q8 + kSlot / 16 + ks * 2, kd + ks * 2, idS, 1u);
           }
         }
         mma_commit(&bars.s_full[sb]);
@@ -714,7 +720,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
   } else {
     // ---------------------------------------------------------- O += P V (warp 7)
     if (lane == 0 && nT > 0) {
-      constexpr uint32_t idPV = idesc_e4m3(true, DH), idPVb = idesc_bf16(true, DH);
+      constexpr uint32_t idPV = idesc_f8(false, true, DH), idPV2 = idesc_f8(true, true, DH), idPVb = idesc_bf16(true, DH);
       const uint64_t v0 = sw128_desc(sbase + OFF_V, kSlot, 1024);
       int u = 0;
       for (int j = 0; j < nT; ++j) {
@@ -738,8 +744,8 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         } else {
 #pragma unroll
           for (int ks = 0; ks < BN / 32; ++ks) {
-            mma_e4m3_ts(tmem + TM_O, pa + ks * 8, vd + ks * (32 * 128 / 16), idPV, (j > 0 || ks > 0) ? 1u : 0u);
-            mma_e4m3_ts(tmem + TM_O, pa + P2 + ks * 8, vd + ks * (32 * 128 / 16), idPV, 1u);
+            mma_f8_ts(tmem + TM_O, pa + ks * 8, vd + ks * (32 * 128 / 16), idPV, (j > 0 || ks > 0) ? 1u : 0u);
+            mma_f8_ts(tmem + TM_O, pa + P2 + ks * 8, vd + ks * (32 * 128 / 16), idPV2, 1u);
           }
         }
         mma_commit(&bars.s_free[sb]);

@@ -105,12 +105,16 @@ class AttnCase:
         Few rows: probabilities are rounded to 11 bits, 2^-11 size, and below the fp16 range by
         2^-25 each while the largest weight is at least 1: N 2^-25 448 max v_scale.
 
-        Many rows (over 32 packed ones at head dim 128): a probability is rounded to 8 bits (half
-        a step 2^-8), or by half of 2^-9 where that is more, while the key with the largest
-        weight p_j s_j (s the value scale) has at least 2^4. With sum_j p_j = 1 the second is
-        (max_i p_i s_i / 2^4) 2^-9 / 2 for a code. Both are independent from key to key and
-        uniform, so six standard deviations (half-width / sqrt 3) of the sums are allowed. The
-        merge rounds a share's row to 2^-14 of its largest element: 2^-14 sum_j p_j max_d |v_jd|."""
+        Many rows (over 32 packed ones at head dim 128): a probability is rounded to an e4m3
+        number and what is left (at most 2^-4 of it) to an e5m2 number (half a step 2^-3), or
+        by half of 2^-16, e5m2's least step, where that is more, while the key with the largest
+        weight p_j s_j (s the value scale) has at least 2^4. Over a binade of the first and of
+        the second number the product of the two uniform errors has a standard deviation under
+        (2^-4 / sqrt 3)(2^-3 / sqrt 3) = 2^-7 / 3 < 2^-8 / sqrt 3; with sum_j p_j = 1 the least
+        step is (max_i p_i s_i / 2^4) 2^-17 for a code, over sqrt 3. Both are independent from
+        key to key: six standard deviations of their sums are allowed (for a single key 2^-5.4,
+        over the 2^-7 it can be off by). The merge rounds a share's row to 2^-14 of its largest
+        element: 2^-14 sum_j p_j max_d |v_jd|."""
         tol = np.zeros_like(o)
         G = o.shape[0] // len(heads)
         many = self.dh == 128 and self.q.shape[1] * G > 32
@@ -124,7 +128,7 @@ class AttnCase:
             rel = (p ** 2) @ (v ** 2) * (2.0 ** -8) ** 2 / 3
             top = (p[:, :P] * sv[h]).max(1, initial=0.0)
             codes2 = ((v[:P] / sv[h][:, None]) ** 2).sum(0)
-            floor = (top[:, None] * 2.0 ** -4 * 2.0 ** -10) ** 2 / 3 * codes2[None, :]
+            floor = (top[:, None] * 2.0 ** -4 * 2.0 ** -17) ** 2 / 3 * codes2[None, :]
             most = p @ np.abs(v).max(1)
             tol[rows] = 6 * np.sqrt(rel + floor) + size[rows] * 2.0 ** -11 * wide + most[:, None] * 2.0 ** -14
         return tol + (0 if f32 else np.abs(o) * 2.0 ** -8) + 1e-30
