@@ -314,6 +314,8 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
   if (warp == 4 && lane == 0) {
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
+    prefetch_tmap(&tmap_kc);
+    prefetch_tmap(&tmap_vc);
   }
   if (tid == 32) {
     for (int s = 0; s < SLOTS; ++s) {
@@ -980,15 +982,19 @@ static int resident(int S) {
   return found[dev][S];
 }
 
-// CTAs that share a row tile's prefix: whole waves of resident clusters times the tiles of a CTA
-// and 4 for its start and merge.
+// CTAs that share a row tile's prefix. A CTA takes its share of the longest prefix's tiles and 6
+// for its start and merge; the waves of resident clusters are to cost least, with half a CTA for
+// the end where there is more than one (the longest started first). Over 32 sequences of 1k-16k
+// it takes one CTA (279 us; two 309), over 4 of 32768 two (462; one 572, three 531), for one of
+// 4096 five (19.7; four 21.5, six, of which one cluster waits, 31.7).
 static int choose_split(long long groups, long long tiles) {
   int best = 0;
   double cost = 0;
   for (int S = 1; S <= kMaxSplit && S <= std::max<long long>(tiles, 1); ++S) {
     const int clusters = resident(S);
     if (clusters <= 0) continue;
-    const double c = std::ceil(static_cast<double>(groups) / clusters) * (std::ceil(static_cast<double>(tiles) / S) + 4.);
+    const double waves = static_cast<double>(groups) / clusters, cta = static_cast<double>(tiles) / S + 6.;
+    const double c = waves <= 1. ? cta : (waves + 0.5) * cta;
     if (best == 0 || c < cost) {
       cost = c;
       best = S;
