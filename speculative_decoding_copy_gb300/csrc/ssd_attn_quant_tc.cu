@@ -72,7 +72,7 @@ constexpr uint32_t OFF_QB = 2 * kSlot;    // bf16, two 64-column halves
 constexpr uint32_t OFF_K = 4 * kSlot;
 constexpr uint32_t OFF_V = OFF_K + SLOTS * kSlot;
 constexpr uint32_t OFF_BAR = OFF_V + SLOTS * kSlot;
-constexpr uint32_t kBarBytes = 3072;
+constexpr uint32_t kBarBytes = 4096;
 constexpr uint32_t kSmemBytes = OFF_BAR + kBarBytes + 1024;   // + slack to align the base to 1024
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr unsigned long long kWaitClocks = 1ull << 32;
@@ -97,6 +97,7 @@ struct Bars {
   int odd_own;                            // an own-block value was not finite
   int seq, rows;                          // the sequence; its present rows
   int row_slot[BM];                       // candidate slot of a row of this tile
+  int row_at[BM];                         // its place in the sequence's Q and output, in rows of DH
   float pair[2][BM];                      // a value of each half of a row
   // of a prefix tile's eight groups of 16 keys: K factor, log2 of the V factor, 1 / V factor
   float4 factors[FACTORS][3][2];
@@ -388,7 +389,9 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       const int mid = (lo + hi) >> 1;
       if (ends[mid] > i) hi = mid; else lo = mid + 1;
     }
-    bars.row_slot[tid] = lo * p.Dmax + i - (lo > 0 ? ends[lo - 1] : 0);
+    const int slot = lo * p.Dmax + i - (lo > 0 ? ends[lo - 1] : 0);
+    bars.row_slot[tid] = slot;
+    bars.row_at[tid] = slot * p.Hq + kvh * G + (r0 + min(tid, rv - 1)) % G;
   }
   if (warp == 4) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem_base)),
@@ -431,63 +434,60 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     const bool row_ok = row < rv;
     const int slot = bars.row_slot[row];
     const int c_lo = slot / p.Dmax * p.Dmax;
-    // Q: a power of two brings the row's largest magnitude into [128, 256); two e4m3 parts. Each
-    // thread converts 64 elements.
-    float q_mul;
-    {
-      uint4 raw[8];
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + ((static_cast<int64_t>(b) * NT + slot) * p.Hq + kvh * G + (r0 + row) % G) * DH + half * 64);
+    // Q: a power of two brings a row's largest magnitude into [128, 256); two e4m3 parts. Sixteen
+    // lanes take a row, a warp 16 rows in two rounds (a loop: this code runs once a CTA, and
+    // unrolled it cost more in instruction fetches than in work).
+    const int q_row = ((warp & 3) + 4 * half) * 16 + (lane >> 4), chunk = lane & 15;
+    const uint16_t* q_seq = p.q + static_cast<int64_t>(b) * NT * p.Hq * DH + chunk * 8;
+    uint4 raw[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) raw[i] = row_ok ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-      uint32_t top = 0;
+    for (int i = 0; i < 8; ++i) {
+      const int r = q_row + 2 * i;
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rv) raw[i] = *reinterpret_cast<const uint4*>(q_seq + static_cast<int64_t>(bars.row_at[r]) * DH);
+    }
+#pragma unroll 1
+    for (int first = q_row; first < q_row + 16; first += 8) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
+        const int r = first + 2 * i;
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
-      }
-      bars.pair[half][row] = __uint_as_float(top);
-      pair_sync(warp & 3);
-      top = max(top, __float_as_uint(bars.pair[half ^ 1][row]));
-      const int ex = static_cast<int>(top >> 23);
-      const int up = min(254 + 7 - ex, 253);
-      const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
-      q_mul = ex == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * p.scale_log2;
-      const uint32_t row_at = row * 128, sw = row & 7;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {                      // 16 elements
-        uint32_t part[2][4];
+        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int ex = static_cast<int>(top >> 23);
+        const int up = min(254 + 7 - ex, 253);
+        const float mul = ex == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(static_cast<uint32_t>(up) << 23);
+        float x[8], y[8];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {                    // four of them
-          const uint4& r = raw[2 * i + (h >> 1)];
-          const uint32_t w[2] = {(h & 1) ? r.z : r.x, (h & 1) ? r.w : r.y};
-          float x[4], y[4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            x[2 * e] = __uint_as_float(w[e] << 16) * mul;
-            x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u) * mul;
-          }
-          if (ex == 255) x[0] = x[1] = x[2] = x[3] = __uint_as_float(0x7fffffffu);
-          const uint32_t lo = e4m3x2(x[0], x[1]), hi = e4m3x2(x[2], x[3]);
-          e4m3x2_to_f32(lo, y[0], y[1]);
-          e4m3x2_to_f32(hi, y[2], y[3]);
-          part[0][h] = lo | hi << 16;
-          part[1][h] = e4m3x2(x[0] - y[0], x[1] - y[1]) | e4m3x2(x[2] - y[2], x[3] - y[3]) << 16;
+        for (int e = 0; e < 4; ++e) {
+          x[2 * e] = __uint_as_float(w[e] << 16) * mul;            // a row that is not finite becomes NaN
+          x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u) * mul;
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          *reinterpret_cast<uint4*>(smem + OFF_Q8 + u * kSlot + row_at + (((4 * half + i) ^ sw) << 4)) =
-              make_uint4(part[u][0], part[u][1], part[u][2], part[u][3]);
+        const uint32_t lo = e4m3x4(x[0], x[1], x[2], x[3]), hi = e4m3x4(x[4], x[5], x[6], x[7]);
+        e4m3x2_to_f32(lo, y[0], y[1]);
+        e4m3x2_to_f32(lo >> 16, y[2], y[3]);
+        e4m3x2_to_f32(hi, y[4], y[5]);
+        e4m3x2_to_f32(hi >> 16, y[6], y[7]);
+        uint8_t* at = smem + OFF_Q8 + r * 128 + (((chunk >> 1) ^ (r & 7)) << 4) + (chunk & 1) * 8;
+        *reinterpret_cast<uint2*>(at) = make_uint2(lo, hi);
+        *reinterpret_cast<uint2*>(at + kSlot) = make_uint2(e4m3x4(x[0] - y[0], x[1] - y[1], x[2] - y[2], x[3] - y[3]),
+                                                           e4m3x4(x[4] - y[4], x[5] - y[5], x[6] - y[6], x[7] - y[7]));
+        if (nC > 0)
+          *reinterpret_cast<uint4*>(smem + OFF_QB + (chunk >> 3) * kSlot + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)) = raw[i];
+        if (chunk == 0)
+          bars.pair[0][r] = ex == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * p.scale_log2;
       }
-      if (nC > 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(smem + OFF_QB + half * kSlot + row_at + ((i ^ sw) << 4)) = raw[i];
-      }
-      fence_async_smem();
-      mbar_arrive(&bars.q_full);
+      for (int i = 0; i < 4; ++i) raw[i] = raw[4 + i];
     }
+    fence_async_smem();
+    mbar_arrive(&bars.q_full);
+    mbar_wait(bars, &bars.q_full, 0, p.hdr, 464);            // the factors of all rows are there
+    const float q_mul = bars.pair[0][row];
+    pair_sync(warp & 3);                                     // the pairs may be written again
     // Where a reference has to move: the row's new one, from both halves, and O and the sum
     // under it (each half rescales its 64 columns of O).
     auto move_refs = [&](int j, float mx) {
@@ -766,6 +766,57 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     __syncwarp();
   }
 
+  // ---- one share: the rows leave from TMEM
+  if (S == 1) {
+    if (softmax) {
+      pair_sync(warp & 3);                                   // both halves' sums are there
+      const int slot = bars.row_slot[row];
+      const float inv = __frcp_rn(bars.pair[0][row] + bars.pair[1][row]);
+      const bool look = nC > 0 && *reinterpret_cast<volatile int*>(&bars.odd_own);
+      const int64_t at = (static_cast<int64_t>(b) * NT * p.Hq + bars.row_at[row]) * DH + half * 64;
+#pragma unroll 1
+      for (int q = 0; q < 2; ++q) {
+        uint32_t o[32];
+        tmem_ld32(tmem + TM_O + lane_off + half * 64 + q * 32, o);
+        tmem_wait_ld();
+        if (row >= rv || bars.failed) continue;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+        if (look) {
+          // the own-block values that left the tile: an infinity or NaN, whatever its weight
+          for (int t = slot / p.Dmax * p.Dmax; t <= slot; ++t) {
+            const uint16_t* v = p.v_cand + ((static_cast<int64_t>(b) * NT + t) * p.Hkv + kvh) * DH + half * 64 + q * 32;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((v[e] & 0x7f80u) == 0x7f80u) o[e] = __float_as_uint(__uint_as_float(o[e]) + bf16_to_f32(v[e]));
+          }
+        }
+        if (p.out_f32) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + at + q * 32);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) dst[u] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at + q * 32);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16(__uint_as_float(o[8 * u + 2 * e]), __uint_as_float(o[8 * u + 2 * e + 1]));
+            dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 4) {
+      tc_fence_after();
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+    return;
+  }
+
   // ---- merge the S shares of every row in the CTA that owns it. Ring layout (bytes): staged
   // rows [BM][kRowB], received rows [sender][rpc][kRowB].
   uint8_t* stage = smem + OFF_K;
@@ -909,8 +960,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           if ((v[e] & 0x7f80u) == 0x7f80u) acc[e] += bf16_to_f32(v[e]);
       }
     }
-    const int hh = kvh * G + (r0 + rb + i) % G;
-    const int64_t at = ((static_cast<int64_t>(b) * NT + slot) * p.Hq + hh) * DH + cg * 16;
+    const int64_t at = (static_cast<int64_t>(b) * NT * p.Hq + bars.row_at[rb + i]) * DH + cg * 16;
     if (p.out_f32) {
       float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
 #pragma unroll
@@ -1007,6 +1057,7 @@ static int choose_split(long long groups, long long tiles) {
 
 bool attn_quant_tc_applies(const AttnQuantParams& p, int dh) {
   if (dh != qtc::DH || p.NB > qtc::kMaxBlocks) return false;
+  if (static_cast<long long>(p.NB) * p.Dmax * p.Hq >= (1LL << 31)) return false;
   if (static_cast<long long>(p.B) * p.Hkv > 65535 || static_cast<long long>(p.B) * p.NB * p.Dmax >= (1LL << 31)) return false;
   return tc::encode_fn() != nullptr;
 }
