@@ -856,7 +856,10 @@ extern "C" int ssd_verify_attn_quant(const ssd_attn_quant_args* a, void* ws, siz
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int rows = a->NB * a->Dmax * (a->Hq / a->Hkv);
   KernelTimer timer(SSD_KERNEL_VERIFY_ATTN, s);
-  if (rows > 32 && attn_quant_tc_applies(p, a->dh)) return attn_quant_tc_launch(p, s);
+  // 4096 keys, 8 kv heads, us by the tensor-core kernel (any row count costs it the same) and by
+  // this one: one sequence 15.3 and 13.0 at 16 rows, 15.4 and 15.1 at 20; four 21.1 and 18.9,
+  // 21.4 and 28.3; 64 of 2k-8k 200 and 173, 200 and 281 (beyond 16 rows it reads the cache twice)
+  if (rows > 16 && attn_quant_tc_applies(p, a->dh)) return attn_quant_tc_launch(p, s);
   // eight rows or sixteen in a CTA
   if (a->dh == 128) return rows <= 8 ? rows_choose<128, 1>(p, rows, s) : rows_choose<128, 2>(p, rows, s);
   return rows <= 8 ? rows_choose<64, 1>(p, rows, s) : rows_choose<64, 2>(p, rows, s);

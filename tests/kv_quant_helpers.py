@@ -105,7 +105,7 @@ class AttnCase:
         Few rows: probabilities are rounded to 11 bits, 2^-11 size, and below the fp16 range by
         2^-25 each while the largest weight is at least 1: N 2^-25 448 max v_scale.
 
-        Many rows (over 32 packed ones at head dim 128): a probability is rounded to an e4m3
+        Many rows (over 16 packed ones at head dim 128): a probability is rounded to an e4m3
         number and what is left (at most 2^-4 of it) to an e5m2 number (half a step 2^-3), or
         by half of 2^-16, e5m2's least step, where that is more, while the key with the largest
         weight p_j s_j (s the value scale) has at least 2^4. Over a binade of the first and of
@@ -117,7 +117,7 @@ class AttnCase:
         element: 2^-14 sum_j p_j max_d |v_jd|."""
         tol = np.zeros_like(o)
         G = o.shape[0] // len(heads)
-        many = self.dh == 128 and self.q.shape[1] * G > 32
+        many = self.dh == 128 and self.q.shape[1] * G > 16
         P = int(self.prefix[b])
         sv = self.v_scales(b)
         for h, (p, v) in enumerate(heads):
