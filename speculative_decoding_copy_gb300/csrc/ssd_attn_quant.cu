@@ -34,6 +34,7 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "ssd_attn_quant.cuh"
 #include "ssd_tc.cuh"
@@ -751,8 +752,8 @@ static int rows_resident(int S) {
 // two (`even`) leave nothing short for a second wave, which then costs as much as the first
 // (one sequence of 32768 keys: 20.1 us by 12 CTAs, 31.3 by 16, of which one cluster of eight
 // waits). Over 2k-8k prefixes
-// of 8 kv heads it takes 4, 3 and 2 for 16, 32 and 64 sequences, the fastest of 1 .. 8 each
-// time (36.8, 60.6 and 117.3 us; with 1: 69.1, 90.1 and 119.4, with 8: 44.7, 85.0 and 163.4).
+// of 8 kv heads it takes 5, 4 and 2 for 16, 32 and 64 sequences, the fastest of 1 .. 8 each
+// time (38.5, 61.8 and 107.4 us; with 1: 91.6, 103.2 and 131.2, with 8: 39.5, 73.9 and 142.1).
 template <typename C>
 static int rows_split(long long groups, long long keys, int most, bool even) {
   const double iters = static_cast<double>(std::max<long long>(1, (keys + C::W * kStepKeys - 1) / (C::W * kStepKeys)));
@@ -808,13 +809,15 @@ static int rows_launch(const AttnQuantParams& p, int rows, int S, cudaStream_t s
 template <int DH, int N8>
 static int rows_choose(const AttnQuantParams& p, int rows, cudaStream_t s) {
   // Few sequences: latency counts, so eight warps and up to 16 CTAs share each (a token over
-  // 4096 keys of 8 kv heads: 8.6 us, with the other shape 11.0). Many: three CTAs of an SM
-  // keep it reading while one starts or ends; sixteen rows need the registers of two.
+  // 4096 keys of 8 kv heads: 8.6 us, with the other shape 11.0). Many: four small CTAs of an SM
+  // keep it reading while one starts or ends (64 sequences of 2k-8k: 107 us; three of four
+  // warps 119, six of two 120, one of eight 123). Sixteen rows need the registers of eight
+  // warps, in either case.
   using Few = RowsConfig<DH, N8, 8, 3, 1>;
-  using Many = RowsConfig<DH, N8, 4, N8 == 1 ? 2 : 3, N8 == 1 ? 3 : 2>;
+  using Many = std::conditional_t<N8 == 1, RowsConfig<DH, N8, 3, 2, 4>, Few>;
   const long long groups = static_cast<long long>(p.B) * p.Hkv * ((rows + 8 * N8 - 1) / (8 * N8));
   if (groups * 8 <= 152) return rows_launch<Few>(p, rows, rows_split<Few>(groups, p.capacity, kMaxRanks, true), s);
-  return rows_launch<Many>(p, rows, rows_split<Many>(groups, p.capacity, 8, false), s);
+  return rows_launch<Many>(p, rows, rows_split<Many>(groups, p.capacity, kMaxRanks, false), s);
 }
 
 }  // namespace ssd
