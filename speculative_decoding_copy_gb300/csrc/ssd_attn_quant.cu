@@ -192,6 +192,7 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     int* lens = reinterpret_cast<int*>(smem);
     const int mine = tid < p.B ? p.prefix_len[tid] : -1;
     lens[tid] = mine;
+    tc::fence_async_smem();                          // tensor copies write the same place later
     __syncthreads();
     int before = 0;
     for (int i = 0; i < p.B; ++i) before += lens[i] > mine || (lens[i] == mine && i < tid) ? 1 : 0;
@@ -204,7 +205,7 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   bool here = false;
   if (tid < rows) {
     const int tt = (r0 + tid) / G;
-    here = tt % p.Dmax < p.blk_len[b * p.NB + tt / p.Dmax];
+    here = tt % p.Dmax < p.blk_len[static_cast<int64_t>(b) * p.NB + tt / p.Dmax];
     present[tid] = here ? 1 : 0;
   }
   // rows of Q, and on rank 0 the first tile of own-block slots: loads that wait for nothing
@@ -402,9 +403,14 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int slot = slot0 + (e >> 1) * 8 + g;
-          y[n][e] = slot >= lo[n][e & 1] && slot <= tr[n][e & 1] ? c[n][e] * p.scale_log2 : -INFINITY;
+          y[n][e] = slot >= lo[n][e & 1] && slot <= tr[n][e & 1] ? fmaf(c[n][e], p.scale_log2, -kOwnLowered) : -INFINITY;
         }
       if (move_max<N8, 1>(m, yy, ref, alpha)) rescale(alpha);
+#pragma unroll
+      for (int n = 0; n < N8; ++n) {
+        ref[n][0] -= kOwnLowered;
+        ref[n][1] -= kOwnLowered;
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -473,7 +479,8 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   uint32_t parity = 0;
   for (int s = step0; s < step1; s += W) {
     asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
-    if (!mbar_wait_bounded(my_bar + stage, parity, failed, p.hdr, 442, kRowsWaitClocks)) break;
+    const bool arrived = mbar_wait_bounded(my_bar + stage, parity, failed, p.hdr, 442, kRowsWaitClocks);
+    if (!__all_sync(0xffffffffu, arrived)) break;    // the warp leaves together
     __syncwarp();                                    // the scales are other lanes' copies
     uint8_t* st = my + stage * C::kStep;
     const float4 sc = scales[warp * ST + stage];
@@ -687,10 +694,15 @@ static int validate(const ssd_attn_quant_args* a) {
       !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16))
     return SSD_ERR_UNSUPPORTED;
   const int64_t slots = static_cast<int64_t>(a->B) * a->NB * a->Dmax, rows = slots * a->Hq * a->dh, cand = 2 * slots * a->Hkv * a->dh;
-  const int64_t tokens = a->block_table != nullptr ? a->num_pages * kPageTokens : a->B * a->P_max;
+  const bool paged = a->block_table != nullptr;
+  const int64_t pages = paged ? a->num_pages : a->B, tokens = paged ? kPageTokens : a->P_max;
+  const int64_t codes = pages * a->Hkv * tokens * a->dh;
+  const int64_t scales = 4 * pages * a->Hkv * ((tokens + a->scale_block - 1) / a->scale_block);
   const Span spans[] = {{a->out, rows * (a->out_dtype == SSD_F32 ? 4 : 2)}, {a->q, 2 * rows}, {a->k_cand, cand},
-                        {a->v_cand, cand}, {a->k_cache, tokens * a->Hkv * a->dh}, {a->v_cache, tokens * a->Hkv * a->dh}};
-  if (overlap(spans, 1, 6)) return SSD_ERR_INVALID;
+                        {a->v_cand, cand}, {a->k_cache, codes}, {a->v_cache, codes}, {a->k_scale, scales},
+                        {a->v_scale, scales}, {a->prefix_len, 4LL * a->B},
+                        {a->blk_len, 4LL * a->B * a->NB}, {a->block_table, 4LL * a->B * a->pages_per_seq}};
+  if (overlap(spans, 1, 11)) return SSD_ERR_INVALID;
   return SSD_OK;
 }
 

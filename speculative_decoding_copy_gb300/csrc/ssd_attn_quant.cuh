@@ -32,6 +32,12 @@ struct AttnQuantParams {
 
 constexpr float kLeastVScaleLog2 = -100.f;     // a smaller v scale counts as this
 
+// Own-block keys have no value scale in the exponent, so beside prefix keys of the same score
+// they look 1 / sv times as heavy, and a reference maximum set by one would push the prefix's
+// probabilities, which have 8 or 16 bits, to the low end of their range. They enter the maximum
+// lowered by this (log2); their own probabilities, bf16 numbers, may then pass the reference.
+constexpr float kOwnLowered = 16.f;
+
 // tensor-core path for many rows (ssd_attn_quant_tc.cu)
 bool attn_quant_tc_applies(const AttnQuantParams& p, int dh);
 int attn_quant_tc_launch(const AttnQuantParams& p, cudaStream_t s);

@@ -23,8 +23,8 @@
 //              it waiting on its own latencies: 1.7 us a tile): Q into shared memory (two e4m3
 //              parts, swizzled; rank 0 also bf16), then the online softmax of each 128-key tile,
 //              read from TMEM once: per 16 keys one K factor, one log2 of the V factor and one
-//              weight 1/sv of the sum. A barrier tells all rows whether any reference has to
-//              move, which is rare. P goes back to TMEM over the first half of the tile's S
+//              weight 1/sv of the sum. A barrier of the two warps that share rows tells whether one of their
+//              references has to move, which is rare. P goes back to TMEM over the first half of the tile's S
 //              buffer (two parts of 32 columns, four keys a word; bf16 pairs for own-block
 //              tiles). In fp16 with the exponent offset of the formats taken into the
 //              exponential, the parts are bytes of a probability's bits and of what is left,
@@ -371,6 +371,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       sum += __shfl_sync(0xffffffffu, n, 31);
     }
     if (lane == 0) bars.rows = sum * G;
+    fence_async_smem();                    // tensor copies write the same place later
   }
   int P = p.prefix_len[b];
   if (P < 0 || P > p.capacity) {
@@ -561,7 +562,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         f.k[q] = p.scale_log2;
-        f.lv[q] = 0.f;
+        f.lv[q] = -kOwnLowered;
       }
       const float mx = chunk_max<true>(v, f, lo, hi);
       if (any_row(mx > m + kLag, warp & 3)) move_refs(j, mx);
@@ -628,7 +629,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     }
     auto load_page = [&](int t) -> int {
       if (t >= j1 || p.block_table == nullptr) return b;
-      const int pg = __ldg(p.block_table + static_cast<int64_t>(b) * p.pages_per_seq + t);
+      const int pg = p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + t];
       if (pg >= 0 && pg < p.num_pages) return pg;
       if (lane == 0) record_error(p.hdr, SSD_ERR_DEVICE, 451);
       return 0;
@@ -638,7 +639,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       if (!kside || t >= j1 || lane >= 16) return 0.f;
       const int place = (p.block_table == nullptr ? t * BN : 0) + (lane & 7) * 16;
       const int blk = min(place >> p.sb_log2, blocks - 1);
-      return __ldg((lane < 8 ? p.k_scale : p.v_scale) + static_cast<int64_t>(pg * p.Hkv + kvh) * blocks + blk);
+      return (lane < 8 ? p.k_scale : p.v_scale)[static_cast<int64_t>(pg * p.Hkv + kvh) * blocks + blk];
     };
     int page = load_page(j0), page1 = load_page(j0 + 1), page2 = load_page(j0 + 2);
     float scale = load_scale(j0, page), scale1 = load_scale(j0 + 1, page1);
@@ -777,6 +778,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 #pragma unroll 1
       for (int q = 0; q < 2; ++q) {
         uint32_t o[32];
+        __syncwarp();
         tmem_ld32(tmem + TM_O + lane_off + half * 64 + q * 32, o);
         tmem_wait_ld();
         if (row >= rv || bars.failed) continue;

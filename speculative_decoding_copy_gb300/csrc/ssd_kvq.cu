@@ -374,7 +374,7 @@ extern "C" int ssd_commit_kv_quant(const ssd_commit_quant_args* a, void* ws, siz
     return SSD_ERR_INVALID;
   if (!aligned(a->k_cand, 16) || !aligned(a->v_cand, 16) || !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16))
     return SSD_ERR_UNSUPPORTED;
-  const int64_t pages = a->block_table != nullptr ? a->num_pages : a->B;
+  const int64_t pages = a->block_table != nullptr ? a->num_pages : a->P_max > 0 ? a->B : 0;
   const int64_t cand = static_cast<int64_t>(a->B) * a->NB * a->Dmax * a->Hkv * a->dh * (a->dtype == SSD_BF16 ? 2 : 4);
   const int64_t codes = pages * page_tokens * a->Hkv * a->dh;
   const int64_t scales = 4 * pages * a->Hkv * ((page_tokens + a->scale_block - 1) / a->scale_block);

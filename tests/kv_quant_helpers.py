@@ -111,10 +111,11 @@ class AttnCase:
         weight p_j s_j (s the value scale) has at least 2^4. Over a binade of the first and of
         the second number the product of the two uniform errors has a standard deviation under
         (2^-4 / sqrt 3)(2^-3 / sqrt 3) = 2^-7 / 3 < 2^-8 / sqrt 3; with sum_j p_j = 1 the least
-        step is (max_i p_i s_i / 2^4) 2^-17 for a code, over sqrt 3. Both are independent from
-        key to key: six standard deviations of their sums are allowed (for a single key 2^-5.4,
-        over the 2^-7 it can be off by). The merge rounds a share's row to 2^-14 of its largest
-        element: 2^-14 sum_j p_j max_d |v_jd|."""
+        step is (max_i p_i s_i / 2^4) 2^-17 for a code, over sqrt 3 (the maximum runs over the
+        own-block keys too, which enter it with s = 2^-16). Both are independent from key to key:
+        six standard deviations of their sums are allowed (for a single key 2^-5.4, over the 2^-7
+        it can be off by). The merge rounds a share's row to 2^-14 of its largest element:
+        2^-14 sum_j p_j max_d |v_jd|."""
         tol = np.zeros_like(o)
         G = o.shape[0] // len(heads)
         many = self.dh == 128 and self.q.shape[1] * G > 16
@@ -126,7 +127,7 @@ class AttnCase:
                 tol[rows] = size[rows] * 2.0 ** -10 * wide + P * 2.0 ** -25 * 448 * float(sv.max(initial=0))
                 continue
             rel = (p ** 2) @ (v ** 2) * (2.0 ** -8) ** 2 / 3
-            top = (p[:, :P] * sv[h]).max(1, initial=0.0)
+            top = np.maximum((p[:, :P] * sv[h]).max(1, initial=0.0), p[:, P:].max(1, initial=0.0) * 2.0 ** -16)
             codes2 = ((v[:P] / sv[h][:, None]) ** 2).sum(0)
             floor = (top[:, None] * 2.0 ** -4 * 2.0 ** -17) ** 2 / 3 * codes2[None, :]
             most = p @ np.abs(v).max(1)

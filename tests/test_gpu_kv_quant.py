@@ -297,6 +297,17 @@ def test_attention_with_block_scales_far_apart(dh, Dmax):
     case.check(H.run(case))
 
 
+@pytest.mark.parametrize("v_scale", [2.0 ** -16, 2.0 ** -8, 2.0 ** 6])
+@pytest.mark.parametrize("dh,Dmax", [(64, 1), (128, 1), (128, 20)])
+def test_attention_of_a_flat_prefix_beside_heavy_own_keys(dh, Dmax, v_scale):
+    """Thousands of keys of equal small weight, which the own-block keys, without a value scale,
+    must not push to the low end of the probabilities' range."""
+    case = H.AttnCase(73, [5000, 333], 1, Dmax, 4, 2, dh, 64, True, blk_len=np.full((2, 1), Dmax))
+    case.k_scale[:] = 2.0 ** -30
+    case.v_scale[:] = v_scale
+    case.check(H.run(case))
+
+
 @pytest.mark.parametrize("dh,Dmax", [(128, 1), (128, 20)])
 def test_attention_with_sharp_and_growing_scores(dh, Dmax):
     """Scores of +-60 whose maximum keeps growing along the prefix, far past every threshold."""
@@ -345,6 +356,83 @@ def test_attention_repeats_bit_for_bit():
             assert torch.equal(a, H.run(case))
 
 
+@pytest.mark.parametrize("prefix,Dmax", [([4096] * 8, 9), ([20000], 9), ([4096, 100], 5), ([900] * 20, 1)])
+def test_attention_is_stable_over_many_calls(prefix, Dmax):
+    """The end of a CTA's products, the merge and the ring's reuse are ordered by waits: every
+    one of many calls gives the first one's bits, and those are right."""
+    case = H.AttnCase(43, prefix, 1, Dmax, 4, 2, 128, 64, True, blk_len=np.full((len(prefix), 1), Dmax))
+    a, kw = case.args(), case.kw()
+    first = S.ssd_verify_attn_quant(*a, **kw, out_f32=True)
+    out = [torch.empty_like(first) for _ in range(200)]
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for o in out:
+        S.ssd_verify_attn_quant(*a, **kw, out=o, ws=ws)
+    assert all(torch.equal(o, first) for o in out)
+    assert S.ssd_read_device_error(ws) == S.SSD_OK
+    case.check(first)
+
+
+@pytest.mark.parametrize("dh,NB,Dmax", [(64, 2, 3), (128, 1, 1), (128, 3, 20)])
+def test_attention_without_a_prefix(dh, NB, Dmax):
+    """Empty prefixes, and a contiguous cache of no tokens."""
+    case = H.AttnCase(47, [0, 0, 0], NB, Dmax, 4, 2, dh, 16, False)
+    case.check(H.run(case))
+    case.k_codes, case.v_codes, case.k_scale, case.v_scale = (
+        x[:, :, :0] for x in (case.k_codes, case.v_codes, case.k_scale, case.v_scale))
+    case.check(H.run(case))
+
+
+@pytest.mark.parametrize("B,NB,Dmax", [(400, 1, 1), (400, 2, 4), (97, 1, 2), (257, 1, 6)])
+def test_attention_of_many_sequences(B, NB, Dmax):
+    """More sequences than threads of a CTA: they run in their own order; fewer: by length."""
+    case = H.AttnCase(53, list(np.random.default_rng(B).integers(0, 300, B)), NB, Dmax, 4, 1, 128, 32, True)
+    case.check(H.run(case))
+
+
+@pytest.mark.parametrize("NB,Dmax,G", [(300, 16, 2), (1024, 8, 1), (8192, 1, 1), (32, 256, 1)])
+def test_attention_of_many_sparse_blocks(NB, Dmax, G):
+    """One present token in each of many blocks: rows of one tile far apart in the slots."""
+    blk_len = np.zeros((1, NB), np.int32)
+    blk_len[:, ::max(1, NB // 300)] = 1
+    blk_len[0, NB - 1] = Dmax
+    case = H.AttnCase(59, [200], NB, Dmax, G, 1, 128, 128, True, blk_len=blk_len)
+    case.poison()
+    case.check(H.run(case))
+
+
+@pytest.mark.parametrize("Dmax", [1, 20])
+def test_pages_past_four_billion_bytes(Dmax):
+    """A pool of 5 GB each of keys and values, of which the last pages are used."""
+    pages, Hkv, dh, sb = 40000, 8, 128, 64
+    case = H.AttnCase(61, [700, 130], 1, Dmax, 4, Hkv, dh, sb, True, blk_len=np.full((2, 1), Dmax))
+    t = [torch.zeros((pages, Hkv, 128, dh), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    t += [torch.zeros((pages, Hkv, 128 // sb), dtype=torch.float32, device="cuda") for _ in range(2)]
+    assert t[0].nbytes > 1 << 32
+    held = len(case.k_codes)
+    for x, part in zip(t, (case.k_codes, case.v_codes, case.k_scale, case.v_scale)):
+        x[pages - held:] = dev(part)
+    a = case.args()
+    a[1:5] = t
+    table = dev(case.table + pages - held)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    case.check(S.ssd_verify_attn_quant(*a, out_f32=True, block_table=table, ws=ws))
+    # rows appended and committed behind the prefixes, in pages as far out
+    c = [case.k_codes, case.k_scale, case.v_codes, case.v_scale]
+    place = np.array([case.table[b, P // 128] * 128 + P % 128 for b, P in enumerate(case.prefix)], np.int32)
+    K.append(case.kc64[:, 0], place, c[0], c[1], sb)
+    K.append(case.vc64[:, 0], place, c[2], c[3], sb)
+    S.ssd_append_kv_quant(a[5][:, 0], a[6][:, 0], dev(place + (pages - held) * 128), *t, sb, ws=ws)
+    best, n_out = np.zeros(2, np.int32), np.full(2, Dmax + 1, np.int32)
+    new, ok = K.commit(case.kc64, case.prefix + 1, best, n_out, Dmax, c[0], c[1], sb, case.table)
+    K.commit(case.vc64, case.prefix + 1, best, n_out, Dmax, c[2], c[3], sb, case.table)
+    assert ok.all()
+    got, _ = S.ssd_commit_kv_quant(*t, a[5], a[6], dev(case.prefix + 1), dev(best), dev(n_out), Dmax, sb, block_table=table, ws=ws)
+    np.testing.assert_array_equal(got.cpu().numpy(), new)
+    _same_cache(c, [t[0][pages - held:], t[2][pages - held:], t[1][pages - held:], t[3][pages - held:]])
+    assert not t[0][:pages - held].any() and not t[1][:pages - held].any()
+    assert S.ssd_read_device_error(ws) == S.SSD_OK
+
+
 # ---------------------------------------------------------------------------- streams, graphs
 @pytest.mark.parametrize("Dmax", [1, 20])
 def test_on_another_stream_and_in_two_graphs(Dmax):
@@ -376,6 +464,65 @@ def test_on_another_stream_and_in_two_graphs(Dmax):
             g.replay()
             torch.cuda.synchronize()
             assert torch.equal(o, r)
+    assert S.ssd_read_device_error(ws) == S.SSD_OK
+
+
+def test_two_streams_at_once():
+    """Calls that run side by side, with a workspace each."""
+    cases = [H.AttnCase(67 + i, [3000, 700], 1, (1, 20)[i], 4, 2, 128, 64, True) for i in range(2)]
+    args = [c.args() for c in cases]
+    tables = [c.kw()["block_table"] for c in cases]
+    refs = [torch.zeros(c.q.shape, dtype=torch.float32, device="cuda") for c in cases]      # absent rows are not written
+    for a, t, r in zip(args, tables, refs):
+        S.ssd_verify_attn_quant(*a, block_table=t, out=r)
+    outs = [[torch.zeros_like(r) for _ in range(20)] for r in refs]
+    ws = [torch.zeros(256, dtype=torch.uint8, device="cuda") for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for i, s in enumerate(streams):
+            S.ssd_verify_attn_quant(*args[i], block_table=tables[i], out=outs[i][k], ws=ws[i], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, r) for os, r in zip(outs, refs) for o in os)
+
+
+def test_a_captured_step_is_replayed():
+    """Pages, rows, attention and the commit of a decoding step in one graph: three replays give
+    what three steps of the oracle give."""
+    rng = np.random.default_rng(71)
+    B, Hkv, G, dh, sb, pps = 3, 2, 4, 128, 32, 4
+    length = np.array([127, 5, 254], np.int32)
+    held, table = np.array([1, 1, 2], np.int32), np.full((B, pps), -1, np.int32)
+    table[0, 0], table[1, 0], table[2, :2] = 3, 0, (7, 5)
+    stack, n = np.array([1, 2, 4, 6, 8, 9, 10, 11, 0, 0, 0, 0], np.int32), 8
+    c = [x for w in range(2) for x in H.cache(rng, len(stack), Hkv, 128, dh, sb)]
+    t = [dev(x) for x in c]
+    d = [dev(x) for x in (held, table, stack, np.array([n], np.int32))]
+    len_d, one, zero = dev(length), dev(np.ones(B, np.int32)), dev(np.zeros(B, np.int32))
+    bits, x64 = H.bf16(rng, B, 1, 2, Hkv, dh)
+    kd, vd = (dev(np.ascontiguousarray(bits[:, :, w])) for w in range(2))
+    n_out, new_len = dev(np.full(B, 2, np.int32)), dev(length)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = S.ssd_page_tables(len_d, one, *d, B, ws=ws)
+        S.ssd_append_kv_quant(kd[:, 0], vd[:, 0], got["slot_map"], t[0], t[2], t[1], t[3], sb, ws=ws)
+        S.ssd_commit_kv_quant(t[0], t[2], t[1], t[3], kd, vd, len_d, zero, n_out, 1, sb, new_len=new_len, block_table=d[1], ws=ws)
+        len_d.copy_(new_len)
+    for _ in range(3):
+        graph.replay()
+        n, start, slots, served, err = K.page_tables(length, np.ones(B, np.int32), held, table, stack, n, B)
+        assert served.all() and not err
+        for w in range(2):
+            K.append(x64[:, 0, w], slots, c[2 * w], c[2 * w + 1], sb)
+            new, ok = K.commit(x64[:, :, w], length, np.zeros(B, np.int32), np.full(B, 2, np.int32), 1, c[2 * w], c[2 * w + 1], sb, table)
+            assert ok.all()
+        length = new
+        np.testing.assert_array_equal(len_d.cpu().numpy(), length)
+        np.testing.assert_array_equal(got["slot_map"].cpu().numpy(), slots)
+        for x, ref in zip(d, (held, table, stack, [n])):
+            np.testing.assert_array_equal(x.cpu().numpy(), ref)
+        _same_cache(c, t)
     assert S.ssd_read_device_error(ws) == S.SSD_OK
 
 
@@ -460,6 +607,11 @@ def test_refusals():
     for bad in (-1.0, float("nan"), float("inf")):
         with pytest.raises(S.SsdError):
             call(-1, None, scale=bad)
+    words = torch.zeros(2 * 6 * 4 * 64, dtype=torch.float32, device="cuda")
+    with pytest.raises(S.SsdError, match="invalid"):       # the result over a scale
+        call(3, words[:a[3].numel()].view(a[3].shape), out=words.view(2, 6, 4, 64))
+    with pytest.raises(S.SsdError):                        # a workspace off its alignment
+        call(-1, None, ws=torch.zeros(512, dtype=torch.uint8, device="cuda")[16:272])
     with pytest.raises(S.SsdError):
         call(-1, None, ws=torch.zeros(128, dtype=torch.uint8, device="cuda"))
     k = a[5].view(12, 2, 64)
