@@ -540,12 +540,15 @@ int ssd_commit_kv_quant(const ssd_commit_quant_args* a, void* ws, size_t ws_byte
  * before their first token.
  * Scores, maxima and sums are fp32, products exact in fp32; the probabilities are rounded
  * to 11 bits (fp16), or over many rows to the sum of an e4m3 and an e5m2 number (about 8
- * bits), before they weight the values, the candidates' to bf16 or better.
+ * bits), before they weight the values, the candidates' to bf16 or better. Over many rows
+ * the CTAs that share a row merge its output as 16-bit integers, 2^-14 of the largest of 64
+ * elements. Results do not depend on the order of execution: a call repeats bit for bit.
  * Supported: dh 64 or 128; Hq % Hkv == 0, Hq / Hkv <= 64; 1 <= Dmax <= 256,
  * NB * Dmax <= 8192; scale_block 16, 32, 64 or 128; 16-byte aligned tensors;
  * num_pages * 128 * Hkv < 2^31 (B * Hkv * P_max < 2^31); else SSD_ERR_UNSUPPORTED.
- * scale == 0 selects 1/sqrt(dh). out must not overlap an input. A prefix_len outside the cache or a page outside the
- * pool records SSD_ERR_DEVICE (the prefix counts as empty, the page as page 0).
+ * scale == 0 selects 1/sqrt(dh). out must not overlap an input (SSD_ERR_INVALID). A
+ * prefix_len outside the cache or a page outside the pool records SSD_ERR_DEVICE (the
+ * prefix counts as empty, the page as page 0).
  * Workspace: ssd_verify_attn_quant_workspace_size(a) bytes (256: the status header),
  * 256-byte aligned.
  */
@@ -720,7 +723,8 @@ int ssd_read_device_error(void* ws, void* stream, int32_t* out);
 enum {
   SSD_KERNEL_NONE = 0,
   SSD_KERNEL_VOCAB_STATS = 1,
-  SSD_KERNEL_VERIFY_ATTN = 2,        /* the tensor-core attention kernel, or the SIMT prefix pass */
+  SSD_KERNEL_VERIFY_ATTN = 2,        /* the tensor-core attention kernel, or the SIMT prefix pass;
+                                        ssd_verify_attn_quant's kernel */
   SSD_KERNEL_ATTN_COMBINE = 3,
   SSD_KERNEL_ACCEPT_FINISH = 4,      /* merge, acceptance, choice and final draw */
   SSD_KERNEL_RESERVED_5 = 5,         /* unused */

@@ -26,6 +26,10 @@
 // more. mma.sync is enough here: the matrix work is a fifth of the time the bytes take, and
 // eight rows are a sixteenth of the smallest tcgen05 tile.
 //
+// Measured: 64 sequences of 2k-8k keys, 8 kv heads, one token each (672 MB): 106.5 us, 6.3 TB/s,
+// 0.93 of a plain copy. One sequence of 4096 keys (8.4 MB): 8.7 us replayed from a graph, of which
+// 1.2 are its bytes; launch, first loads, the own-block key and two merges are the rest.
+//
 // The CTAs of a cluster split the steps of a (sequence, kv head) evenly by its own length;
 // rank 0 adds the own-block keys (bf16 products, probabilities as a sum of two bf16). Warps
 // and then CTAs merge maxima, sums and outputs in a fixed order through shared memory.

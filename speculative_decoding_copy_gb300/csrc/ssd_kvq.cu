@@ -8,8 +8,13 @@
 // One CTA quantises one run (the rows that go to one block) of one head, of the keys or
 // of the values: the rows are read once into registers (up to eight 16-byte words a
 // thread cover the 128 rows x 128 elements of a block), their largest magnitude is reduced
-// over the CTA, and the codes leave as 8 bytes a word, contiguous over the run. Bound by
-// the bytes of the rows (and by launch latency for a few tokens).
+// over the CTA, and the codes leave as 8 bytes a word, contiguous over the run.
+//
+// What bounds them: the bytes of the rows, and for a few tokens the launch. 21 384 prompt rows
+// of 8 kv heads (131 MB) take 26.4 us, 5.0 TB/s of the 6.8 that a plain copy reaches: a CTA reads
+// its 32 KB, waits for the maximum of all of it, and writes; four CTAs an SM fill each other's
+// waits only in part. Replayed from a graph 64 single tokens take 5.9 us, the accepted tokens of
+// one sequence 3.1 and of 32 sequences 4.6: little more than an empty kernel.
 #include "ssd_kvq.cuh"
 
 namespace ssd {

@@ -7,7 +7,10 @@
 // one now and then) are then moved by all threads, each finding its sequence by a binary
 // search in the scan. Two passes over the batch, because the trimmed pages of all
 // sequences are on the stack before the first one is taken. The call is bound by latency:
-// it reads 12 bytes a sequence.
+// it reads 12 bytes a sequence. Taking the pages of a step of 64 sequences and trimming them
+// behind it are two launches, 9.9 us replayed from a graph; admitting 512 prompts (a million
+// slots, 8 400 pages) and ending them 26 us, most of it the chain of two loads a page that one
+// CTA's threads keep four of on the way.
 // k_slot_map: one thread for four slots, the first one's sequence by a binary search in
 // row_start. Short maps are written by the plan kernel itself.
 #include "ssd_kvq.cuh"
