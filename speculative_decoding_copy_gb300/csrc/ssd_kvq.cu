@@ -11,9 +11,10 @@
 // over the CTA, and the codes leave as 8 bytes a word, contiguous over the run.
 //
 // What bounds them: the bytes of the rows, and for a few tokens the launch. 21 384 prompt rows
-// of 8 kv heads (131 MB) take 26.4 us, 5.0 TB/s of the 6.8 that a plain copy reaches: a CTA reads
-// its 32 KB, waits for the maximum of all of it, and writes; four CTAs an SM fill each other's
-// waits only in part. Replayed from a graph 64 single tokens take 5.9 us, the accepted tokens of
+// of 8 kv heads (131 MB) take 24 us, 5.5 TB/s of the 6.8 that a plain copy reaches: a CTA reads
+// its 32 KB, waits for the maximum of all of it, and writes; five CTAs an SM, a few registers of
+// theirs spilled, fill each other's waits better than four without (29.1 against 26.7 us replayed
+// from a graph), six worse. Replayed from a graph 64 single tokens take 5.9 us, the accepted tokens of
 // one sequence 3.1 and of 32 sequences 4.6: little more than an empty kernel.
 #include "ssd_kvq.cuh"
 
@@ -120,7 +121,7 @@ __device__ __forceinline__ void quant_run(const T* __restrict__ src, int64_t str
   const T* p = src + row0 * stride + ((tid & ((1 << sh) - 1)) << 3);
   const int64_t step = rows_step * stride;
   const int mine = row0 < n ? min(kWords, (n - 1 - row0) / rows_step + 1) : 0;
-  const float old = *d.scale;
+  const float old = d.row == 0 ? 0.f : *d.scale;
   Word<T> w[kWords];
   uint32_t m = 0;
 #pragma unroll
@@ -196,7 +197,7 @@ __device__ __forceinline__ void quant_run(const T* __restrict__ src, int64_t str
 // that share rows (and DRAM pages of a projection's output) run together: the runs that start
 // in the range
 template <typename T>
-__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2)
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 5 : 2)
 k_append_quant(ssd_append_quant_args a, int range, int sb_log2, WsHeader* hdr) {
   __shared__ int32_t slot[2 * kMaxScaleBlock];
   constexpr int kMasks = 2 * kMaxScaleBlock / 32;
