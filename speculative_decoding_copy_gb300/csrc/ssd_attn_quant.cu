@@ -875,10 +875,15 @@ extern "C" int ssd_verify_attn_quant(const ssd_attn_quant_args* a, void* ws, siz
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int rows = a->NB * a->Dmax * (a->Hq / a->Hkv);
   KernelTimer timer(SSD_KERNEL_VERIFY_ATTN, s);
-  // 4096 keys, 8 kv heads, us by the tensor-core kernel (any row count costs it the same) and by
-  // this one: one sequence 15.3 and 13.0 at 16 rows, 15.4 and 15.1 at 20; four 21.1 and 18.9,
-  // 21.4 and 28.3; 64 of 2k-8k 200 and 173, 200 and 281 (beyond 16 rows it reads the cache twice)
-  if (rows > 16 && attn_quant_tc_applies(p, a->dh)) return attn_quant_tc_launch(p, s);
+  // Beyond 16 rows this kernel reads the cache once for each 16; the tensor-core kernel costs the
+  // same up to 128 but starts and merges more slowly. So this one up to 48 rows while its CTAs run
+  // at once and have little to read. Replayed from a graph, us by this and by the other: 20 rows of
+  // 4 sequences of 1024 keys, 8 kv heads, 19.7 and 21.6 (head dim 64: 17.2 and 18.3), one of 4096
+  // with 2 kv heads 17.6 and 21.4 (15.2 and 19.5); past the limits, 16 sequences of 500 30.2
+  // and 21.6 (23.7 and 19.6), 4 of 16384 83 and 55 (60 and 51), 48 rows of 8192 46 and 26 (35 and 24).
+  const long long groups = static_cast<long long>(p.B) * p.Hkv * ((rows + 15) / 16);
+  const bool small = rows <= 16 || (rows <= 48 && groups <= 152 && groups * p.capacity <= (1 << 17));
+  if (!small && attn_quant_tc_applies(p)) return attn_quant_tc_launch(p, a->dh, s);
   // eight rows or sixteen in a CTA
   if (a->dh == 128) return rows <= 8 ? rows_choose<128, 1>(p, rows, s) : rows_choose<128, 2>(p, rows, s);
   return rows <= 8 ? rows_choose<64, 1>(p, rows, s) : rows_choose<64, 2>(p, rows, s);

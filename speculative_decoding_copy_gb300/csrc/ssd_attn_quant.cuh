@@ -39,7 +39,7 @@ constexpr float kLeastVScaleLog2 = -100.f;     // a smaller v scale counts as th
 constexpr float kOwnLowered = 16.f;
 
 // tensor-core path for many rows (ssd_attn_quant_tc.cu)
-bool attn_quant_tc_applies(const AttnQuantParams& p, int dh);
-int attn_quant_tc_launch(const AttnQuantParams& p, cudaStream_t s);
+bool attn_quant_tc_applies(const AttnQuantParams& p);
+int attn_quant_tc_launch(const AttnQuantParams& p, int dh, cudaStream_t s);
 
 }  // namespace ssd

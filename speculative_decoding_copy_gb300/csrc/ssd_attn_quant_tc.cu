@@ -1,5 +1,4 @@
-// Attention over the 8-bit cache for many packed rows, head dim 128, on the tensor cores
-// (tcgen05): a verification of many candidate tokens. The mathematics is that of
+// Attention over the 8-bit cache for many packed rows on the tensor cores (tcgen05): a verification of many candidate tokens. The mathematics is that of
 // ssd_attn_quant.cu; what differs is who does the products.
 //
 // Precision on 8-bit operands. The codes go into the products as they lie in the cache
@@ -35,6 +34,9 @@
 //              there may be NaN, and 0 * NaN is not 0);
 //   warp 5     issues S = Q K^T, up to three tiles ahead of the softmax;
 //   warp 7     issues O += P V (two issuing threads, so that neither's waits hold the other back).
+// Head dim 64: the same layouts, with zeros behind a row's 64 codes (filled in by the tensor copies),
+// half the products of S and half of O's columns kept: 320 rows of one sequence of 4096 keys 23.7 us
+// where the kernel for few rows takes 56.4, of 32 of 2048 157 and 552.
 // Shared memory: Q (64 KB), then four 16 KB slots each for K and V. A prefix tile takes one
 // slot of each, an own-block tile (bf16) two.
 // TMEM columns: S buffers 0-127, 128-255, 256-383, O 384-511.
@@ -66,7 +68,6 @@ namespace qtc {
 
 using namespace tc;
 
-constexpr int DH = 128;
 constexpr int BM = 128;                   // packed rows per CTA
 constexpr int BN = 128;                   // keys per tile
 constexpr int SLOTS = 4;                  // ring slots of K, and of V
@@ -85,12 +86,11 @@ constexpr uint32_t kBarBytes = 4096;
 constexpr uint32_t kSmemBytes = OFF_BAR + kBarBytes + 1024;   // + slack to align the base to 1024
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr unsigned long long kWaitClocks = 1ull << 32;
-constexpr int kMaxSplit = 8;
+constexpr int kMaxSplit = 16;
 constexpr int kSoftmax = 256;             // softmax threads
 constexpr int FACTORS = 8;                // prefix tiles whose factors are kept
-constexpr int kRowB = 2 * DH + 16;        // one share's partial row as sent to its owner
 constexpr int kMaxBlocks = 8192;          // NB: the block ends are kept in the ring at first
-static_assert((2 * BM + kMaxSplit) * kRowB <= static_cast<int>(2 * SLOTS * kSlot), "merge buffers fit in the ring");
+static_assert((2 * BM + kMaxSplit) * (2 * 128 + 16) <= static_cast<int>(2 * SLOTS * kSlot), "merge buffers fit in the ring");
 static_assert(kMaxBlocks * 4 <= static_cast<int>(2 * SLOTS * kSlot), "block ends fit in the ring");
 
 struct Bars {
@@ -303,10 +303,15 @@ __device__ __forceinline__ bool any_row(bool x, int quarter) {
 
 // ------------------------------------------------------------------ kernel
 // grid (S, row tiles, B*Hkv), cluster (S, 1, 1)
+template <int DH>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                 const __grid_constant__ CUtensorMap tmap_kc, const __grid_constant__ CUtensorMap tmap_vc,
                 AttnQuantParams p) {
+  constexpr int UO = DH / 64;              // ring slots of K, and of V, of an own-block tile
+  constexpr int LR = DH / 8;               // lanes of a row of Q
+  constexpr int OC = DH / 2;               // output columns of a row's thread
+  constexpr int kRowB = 2 * DH + 16;       // one share's partial row as sent to its owner
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -444,29 +449,30 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     const bool row_ok = row < rv;
     const int slot = bars.row_slot[row];
     const int c_lo = slot / p.Dmax * p.Dmax;
-    // Q: a power of two brings a row's largest magnitude into [128, 256); two e4m3 parts. Sixteen
-    // lanes take a row, a warp 16 rows in two rounds (a loop: this code runs once a CTA, and
-    // unrolled it cost more in instruction fetches than in work).
-    const int q_row = ((warp & 3) + 4 * half) * 16 + (lane >> 4), chunk = lane & 15;
+    // Q: a power of two brings a row's largest magnitude into [128, 256); two e4m3 parts. DH / 8
+    // lanes take a row, a warp 16 rows four passes a round (a loop: this code runs once a CTA,
+    // and unrolled it cost more in instruction fetches than in work).
+    constexpr int kStep = 32 / LR, kPasses = 16 / kStep;
+    const int q_row = ((warp & 3) + 4 * half) * 16 + lane / LR, chunk = lane % LR;
     const uint16_t* q_seq = p.q + static_cast<int64_t>(b) * NT * p.Hq * DH + chunk * 8;
-    uint4 raw[8];
+    uint4 raw[kPasses];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = q_row + 2 * i;
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = q_row + kStep * i;
       raw[i] = make_uint4(0u, 0u, 0u, 0u);
       if (r < rv) raw[i] = *reinterpret_cast<const uint4*>(q_seq + static_cast<int64_t>(bars.row_at[r]) * DH);
     }
 #pragma unroll 1
-    for (int first = q_row; first < q_row + 16; first += 8) {
+    for (int first = q_row; first < q_row + 16; first += 4 * kStep) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = first + 2 * i;
+        const int r = first + kStep * i;
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int o = 1; o < LR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         const int ex = static_cast<int>(top >> 23);
         const int up = min(254 + 7 - ex, 253);
         const float mul = ex == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(static_cast<uint32_t>(up) << 23);
@@ -491,7 +497,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           bars.pair[0][r] = ex == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * p.scale_log2;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) raw[i] = raw[4 + i];
+      for (int i = 0; i + 4 < kPasses; ++i) raw[i] = raw[4 + i];
     }
     fence_async_smem();
     mbar_arrive(&bars.q_full);
@@ -499,7 +505,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     const float q_mul = bars.pair[0][row];
     pair_sync(warp & 3);                                     // the pairs may be written again
     // Where a reference has to move: the row's new one, from both halves, and O and the sum
-    // under it (each half rescales its 64 columns of O).
+    // under it (each half rescales its columns of O).
     auto move_refs = [&](int j, float mx) {
       bars.pair[half][row] = mx;
       pair_sync(warp & 3);
@@ -515,7 +521,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         __syncwarp();
         tc_fence_after();
 #pragma unroll 1
-        for (int q = 2 * half; q < 2 * half + 2; ++q) {
+        for (int q = UO * half; q < UO * half + UO; ++q) {
           uint32_t o[32];
           tmem_ld32(tmem + TM_O + lane_off + q * 32, o);
           tmem_wait_ld();
@@ -531,8 +537,8 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     for (int j = 0; j < nC; ++j) {
       // slots of other blocks and of absent tokens may hold anything, and 0 * inf is not 0:
       // values that are not finite leave the tile, and the rows that see one get it at the end
-      for (int h = 0; h < 2; ++h) {
-        const int u = 2 * j + h;
+      for (int h = 0; h < UO; ++h) {
+        const int u = UO * j + h;
         if (!mbar_wait(bars, &bars.full_v[u % SLOTS], (u / SLOTS) & 1, p.hdr, 473)) break;
         uint4* vt = reinterpret_cast<uint4*>(smem + OFF_V + (u % SLOTS) * kSlot);
         for (int i = half * BM + row; i < BN * 8; i += kSoftmax) {
@@ -626,7 +632,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     };
     int u = 0;
     for (int j = 0; j < nC; ++j) {
-      for (int h = 0; h < 2; ++h, ++u) {
+      for (int h = 0; h < UO; ++h, ++u) {
         slot_for(u);
         if (lane == 0 && !bars.failed) {
           if (kside) mbar_arrive(&full[u % SLOTS]);        // no factors
@@ -680,7 +686,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     }
     __syncwarp();
     if (!kside && ragged) {
-      const int u = 2 * nC + nP - 1;
+      const int u = UO * nC + nP - 1;
       if (mbar_wait(bars, &full[u % SLOTS], (u / SLOTS) & 1, p.hdr, 472)) {
         uint4* v = reinterpret_cast<uint4*>(smem + OFF_V + (u % SLOTS) * kSlot);
         for (int i = (P - (j1 - 1) * BN) * 8 + lane; i < BN * 8; i += 32) v[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -703,11 +709,11 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         const int sb = j % SBUF;
         const uint32_t d = tmem + TM_S + sb * BN;
         const bool own = j < nC;
-        const int s0 = u % SLOTS, s1 = (u + 1) % SLOTS;
+        const int s0 = u % SLOTS, s1 = (u + UO - 1) % SLOTS;
         // the buffer still holds P of tile j - SBUF until its product is done
         if (j >= SBUF) mbar_wait(bars, &bars.s_free[sb], (j / SBUF - 1) & 1, p.hdr, 483);
         mbar_wait(bars, &bars.full_k[s0], (u / SLOTS) & 1, p.hdr, 481);
-        if (own) mbar_wait(bars, &bars.full_k[s1], ((u + 1) / SLOTS) & 1, p.hdr, 482);
+        if (own) mbar_wait(bars, &bars.full_k[s1], ((u + UO - 1) / SLOTS) & 1, p.hdr, 482);
         tc_fence_after();
         const uint64_t kd = k0 + static_cast<uint32_t>(s0) * (kSlot / 16);
         if (own) {
@@ -724,24 +730,25 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         }
         mma_commit(&bars.s_full[sb]);
         mma_commit(&bars.empty_k[s0]);
-        if (own) mma_commit(&bars.empty_k[s1]);
-        u += own ? 2 : 1;
+        if (own && UO > 1) mma_commit(&bars.empty_k[s1]);
+        u += own ? UO : 1;
       }
     }
     __syncwarp();
   } else {
     // ---------------------------------------------------------- O += P V (warp 7)
     if (lane == 0 && nT > 0) {
-      constexpr uint32_t idPV = idesc_f8(false, true, DH), idPV2 = idesc_f8(true, true, DH), idPVb = idesc_bf16(true, DH);
+      // rows of codes are 128 bytes in the ring, zeros behind a shorter head's
+      constexpr uint32_t idPV = idesc_f8(false, true, 128), idPV2 = idesc_f8(true, true, 128), idPVb = idesc_bf16(true, DH);
       const uint64_t v0 = sw128_desc(sbase + OFF_V, kSlot, 1024);
       int u = 0;
       for (int j = 0; j < nT; ++j) {
         const int sb = j % SBUF;
         const bool own = j < nC;
-        const int s0 = u % SLOTS, s1 = (u + 1) % SLOTS;
+        const int s0 = u % SLOTS, s1 = (u + UO - 1) % SLOTS;
         mbar_wait(bars, &bars.full_v[s0], (u / SLOTS) & 1, p.hdr, 484);
         if (own) {
-          mbar_wait(bars, &bars.full_v[s1], ((u + 1) / SLOTS) & 1, p.hdr, 485);
+          mbar_wait(bars, &bars.full_v[s1], ((u + UO - 1) / SLOTS) & 1, p.hdr, 485);
           mbar_wait(bars, &bars.own_clean[j & 1], (j >> 1) & 1, p.hdr, 487);
         }
         if (ragged && j == nT - 1) mbar_wait(bars, &bars.v_clean, 0, p.hdr, 486);
@@ -763,8 +770,8 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         mma_commit(&bars.s_free[sb]);
         mma_commit(&bars.pv_done[j & 1]);
         mma_commit(&bars.empty_v[s0]);
-        if (own) mma_commit(&bars.empty_v[s1]);
-        u += own ? 2 : 1;
+        if (own && UO > 1) mma_commit(&bars.empty_v[s1]);
+        u += own ? UO : 1;
         // the two kinds of products into O: the order between them is made
         if (own) {
           mbar_wait(bars, &bars.s_free[sb], (j / SBUF) & 1, p.hdr, 489);
@@ -783,12 +790,12 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       const int slot = bars.row_slot[row];
       const float inv = __frcp_rn(bars.pair[0][row] + bars.pair[1][row]);
       const bool look = nC > 0 && *reinterpret_cast<volatile int*>(&bars.odd_own);
-      const int64_t at = (static_cast<int64_t>(b) * NT * p.Hq + bars.row_at[row]) * DH + half * 64;
+      const int64_t at = (static_cast<int64_t>(b) * NT * p.Hq + bars.row_at[row]) * DH + half * OC;
 #pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < UO; ++q) {
         uint32_t o[32];
         __syncwarp();
-        tmem_ld32(tmem + TM_O + lane_off + half * 64 + q * 32, o);
+        tmem_ld32(tmem + TM_O + lane_off + half * OC + q * 32, o);
         tmem_wait_ld();
         if (row >= rv || bars.failed) continue;
 #pragma unroll
@@ -796,7 +803,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         if (look) {
           // the own-block values that left the tile: an infinity or NaN, whatever its weight
           for (int t = slot / p.Dmax * p.Dmax; t <= slot; ++t) {
-            const uint16_t* v = p.v_cand + ((static_cast<int64_t>(b) * NT + t) * p.Hkv + kvh) * DH + half * 64 + q * 32;
+            const uint16_t* v = p.v_cand + ((static_cast<int64_t>(b) * NT + t) * p.Hkv + kvh) * DH + half * OC + q * 32;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if ((v[e] & 0x7f80u) == 0x7f80u) o[e] = __float_as_uint(__uint_as_float(o[e]) + bf16_to_f32(v[e]));
@@ -836,26 +843,28 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     return c == rank ? stage + (rb + i) * kRowB : recv + (c * rpc + i) * kRowB;
   };
   if (softmax) {
-    const uint32_t oa = tmem + TM_O + lane_off + half * 64;
+    const uint32_t oa = tmem + TM_O + lane_off + half * OC;
     pair_sync(warp & 3);                                        // both halves' sums are there
-    uint32_t o[64];
+    uint32_t o[OC];
     if (nT > 0) {
-      load64(oa, o);
+#pragma unroll
+      for (int c = 0; c < OC; c += 32) tmem_ld32(oa + c, o + c);
+      tmem_wait_ld();
     } else {
 #pragma unroll
-      for (int e = 0; e < 64; ++e) o[e] = 0u;
+      for (int e = 0; e < OC; ++e) o[e] = 0u;
     }
     float amax = 0.f;
     bool odd = false;                                    // an element is not finite
 #pragma unroll
-    for (int e = 0; e < 64; ++e) {
+    for (int e = 0; e < OC; ++e) {
       odd |= (o[e] & 0x7f800000u) == 0x7f800000u;
       amax = fmaxf(amax, fabsf(__uint_as_float(o[e])));
     }
     if (odd) {
       amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < 64; ++e)
+      for (int e = 0; e < OC; ++e)
         if ((o[e] & 0x7f800000u) != 0x7f800000u) amax = fmaxf(amax, fabsf(__uint_as_float(o[e])));
     }
     const int k = (amax >= 0x1p-100f) ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127 : -1;
@@ -864,7 +873,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     const float inv_scale = __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
     uint4* dst = reinterpret_cast<uint4*>(stage + row * kRowB + half * DH);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < OC / 8; ++u) {
       uint32_t pk[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -906,61 +915,44 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
   for (int it = tid; it < nr * (DH / 16); it += kThreads) {
     const int i = it / (DH / 16), cg = it % (DH / 16);
     if (!mbar_wait(bars, &bars.recv_full, 0, p.hdr, 490)) continue;
-    float4 tl[kMaxSplit];
-    uint4 h[kMaxSplit][2];
-#pragma unroll
-    for (int c = 0; c < kMaxSplit; ++c) {
-      tl[c] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      if (c < S) {
-        const uint8_t* pr = part(c, i);
-        tl[c] = *reinterpret_cast<const float4*>(pr + 2 * DH);
-        const uint4* src = reinterpret_cast<const uint4*>(pr + cg * 32);
-        h[c][0] = src[0];
-        h[c][1] = src[1];
-      }
-    }
-    float M = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < kMaxSplit; ++c) M = fmaxf(M, tl[c].x);
-    // a share without keys has sum 0 and zeros; a NaN score leaves the maximum and is in the sum
-    float fw[kMaxSplit], L = 0.f;
-#pragma unroll
-    for (int c = 0; c < kMaxSplit; ++c) {
-      fw[c] = tl[c].x > -INFINITY ? ex2_approx(tl[c].x - M) : 1.f;
-      L = fmaf(tl[c].y, fw[c], L);
-    }
-    if (bars.failed) continue;
-    const float inv = __frcp_rn(L);
+    // the shares under their common maximum; one without keys has sum 0 and zeros, and a NaN score
+    // leaves the maximum and is in the sum
+    float M = -INFINITY, L = 0.f;
+    for (int c = 0; c < S; ++c) M = fmaxf(M, *reinterpret_cast<const float*>(part(c, i) + 2 * DH));
+    bool look = false;
     float acc[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < S; ++c) {
+      const uint8_t* pr = part(c, i);
+      const float4 tl = *reinterpret_cast<const float4*>(pr + 2 * DH);
+      const uint4* src = reinterpret_cast<const uint4*>(pr + cg * 32);
+      const uint4 h0 = src[0], h1 = src[1];
+      const float f = tl.x > -INFINITY ? ex2_approx(tl.x - M) : 1.f, unit = cg < DH / 32 ? tl.z : tl.w;
+      L = fmaf(tl.y, f, L);
+      look |= unit < 0.f;
+      const float g = f * fabsf(unit);
+      const uint32_t w[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
 #pragma unroll
-    for (int c = 0; c < kMaxSplit; ++c) {
-      if (c < S) {
-        const float g = fw[c] * inv * fabsf(cg < 4 ? tl[c].z : tl[c].w);
-        const uint32_t w[8] = {h[c][0].x, h[c][0].y, h[c][0].z, h[c][0].w, h[c][1].x, h[c][1].y, h[c][1].z, h[c][1].w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 v = unpack_i16(w[e]);
-          acc[2 * e] = fmaf(g, v.x, acc[2 * e]);
-          acc[2 * e + 1] = fmaf(g, v.y, acc[2 * e + 1]);
-        }
+      for (int e = 0; e < 8; ++e) {
+        const float2 v = unpack_i16(w[e]);
+        acc[2 * e] = fmaf(g, v.x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(g, v.y, acc[2 * e + 1]);
       }
     }
+    if (bars.failed) continue;
+    const float inv = __frcp_rn(L);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] *= inv;
     const int slot = bars.row_slot[rb + i];
-    bool look = false;
-#pragma unroll
-    for (int c = 0; c < kMaxSplit; ++c) look |= c < S && (cg < 4 ? tl[c].z : tl[c].w) < 0.f;
     if (look) {
+      for (int c = 0; c < S; ++c) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(part(c, i) + cg * 32);
 #pragma unroll
-      for (int c = 0; c < kMaxSplit; ++c) {
-        if (c < S) {
-          const uint32_t w[8] = {h[c][0].x, h[c][0].y, h[c][0].z, h[c][0].w, h[c][1].x, h[c][1].y, h[c][1].z, h[c][1].w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if ((w[e] & 0xffffu) == 0x8000u) acc[2 * e] = NAN;
-            if ((w[e] >> 16) == 0x8000u) acc[2 * e + 1] = NAN;
-          }
+        for (int e = 0; e < 8; ++e) {
+          if ((w[e] & 0xffffu) == 0x8000u) acc[2 * e] = NAN;
+          if ((w[e] >> 16) == 0x8000u) acc[2 * e + 1] = NAN;
         }
       }
       // the own-block values that left the tile: an infinity or NaN, whatever its weight
@@ -1006,6 +998,7 @@ static bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* bas
 }
 
 // Kernel attributes, once a device, and how many clusters of S CTAs are resident at once.
+template <int DH>
 static int resident(int S) {
   static std::mutex mu;
   static bool ready[kMaxDevices];
@@ -1014,8 +1007,9 @@ static int resident(int S) {
   if (dev < 0) return 0;
   std::lock_guard<std::mutex> lock(mu);
   if (!ready[dev]) {
-    if (cudaFuncSetAttribute(k_attn_quant_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
-        cudaSuccess) {
+    if (cudaFuncSetAttribute(k_attn_quant_tc<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(k_attn_quant_tc<DH>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
       cudaGetLastError();
       return 0;
     }
@@ -1032,7 +1026,7 @@ static int resident(int S) {
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int count = 0;
-      if (cudaOccupancyMaxActiveClusters(&count, k_attn_quant_tc, &cfg) != cudaSuccess) {
+      if (cudaOccupancyMaxActiveClusters(&count, k_attn_quant_tc<DH>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         count = 0;
       }
@@ -1047,12 +1041,14 @@ static int resident(int S) {
 // for its start and merge; the waves of resident clusters are to cost least, with half a CTA for
 // the end where there is more than one (the longest started first). Over 32 sequences of 1k-16k
 // it takes one CTA (279 us; two 309), over 4 of 32768 two (462; one 572, three 531), for one of
-// 4096 five (19.7; four 21.5, six, of which one cluster waits, 31.7).
+// 4096 five (19.7; four 21.5, six, of which one cluster waits, 31.7). Few row tiles over a long
+// prefix take up to 16 (one sequence of 32768, 2 kv heads, 320 rows: 38 us; with 8, 55).
+template <int DH>
 static int choose_split(long long groups, long long tiles) {
   int best = 0;
   double cost = 0;
   for (int S = 1; S <= kMaxSplit && S <= std::max<long long>(tiles, 1); ++S) {
-    const int clusters = resident(S);
+    const int clusters = resident<DH>(S);
     if (clusters <= 0) continue;
     const double waves = static_cast<double>(groups) / clusters, cta = static_cast<double>(tiles) / S + 6.;
     const double c = waves <= 1. ? cta : (waves + 0.5) * cta;
@@ -1066,25 +1062,26 @@ static int choose_split(long long groups, long long tiles) {
 
 }  // namespace qtc
 
-bool attn_quant_tc_applies(const AttnQuantParams& p, int dh) {
-  if (dh != qtc::DH || p.NB > qtc::kMaxBlocks) return false;
+bool attn_quant_tc_applies(const AttnQuantParams& p) {
+  if (p.NB > qtc::kMaxBlocks) return false;
   if (static_cast<long long>(p.NB) * p.Dmax * p.Hq >= (1LL << 31)) return false;
   if (static_cast<long long>(p.B) * p.Hkv > 65535 || static_cast<long long>(p.B) * p.NB * p.Dmax >= (1LL << 31)) return false;
   return tc::encode_fn() != nullptr;
 }
 
-int attn_quant_tc_launch(const AttnQuantParams& p, cudaStream_t s) {
+template <int DH>
+static int tc_launch(const AttnQuantParams& p, cudaStream_t s) {
   using namespace qtc;
   const int NT = p.NB * p.Dmax;
   const int G = p.Hq / p.Hkv;
   const int mtiles = (NT * G + BM - 1) / BM;
-  const int S = choose_split(static_cast<long long>(p.B) * p.Hkv * mtiles, (p.capacity + BN - 1) / BN + 2);
+  const int S = choose_split<DH>(static_cast<long long>(p.B) * p.Hkv * mtiles, (p.capacity + BN - 1) / BN + 2);
   if (S < 1) return SSD_ERR_CUDA;
   // an empty cache is never read, but a map needs an address and a row
   const uint64_t rows = static_cast<uint64_t>(p.num_pages) * p.Hkv * p.page_tokens;
   const void *kb = rows > 0 ? p.k_cache : static_cast<const void*>(p.q), *vb = rows > 0 ? p.v_cache : kb;
   const cuuint64_t dims2[2] = {DH, rows > 0 ? rows : 1}, strides2[1] = {DH};
-  const cuuint32_t box2[2] = {DH, BN};
+  const cuuint32_t box2[2] = {128, BN};             // what lies past a shorter row is filled with zeros
   const cuuint64_t dims3[3] = {DH, static_cast<cuuint64_t>(p.Hkv), static_cast<cuuint64_t>(p.B) * NT};
   const cuuint64_t strides3[2] = {DH * 2, static_cast<cuuint64_t>(p.Hkv) * DH * 2};
   const cuuint32_t box3[3] = {64, 1, BN};
@@ -1110,12 +1107,16 @@ int attn_quant_tc_launch(const AttnQuantParams& p, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, k_attn_quant_tc, mk, mv, mkc, mvc, q) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, k_attn_quant_tc<DH>, mk, mv, mkc, mvc, q) != cudaSuccess) {
     cudaGetLastError();
     return SSD_ERR_CUDA;
   }
   count_launch();
   return check_launch();
+}
+
+int attn_quant_tc_launch(const AttnQuantParams& p, int dh, cudaStream_t s) {
+  return dh == 128 ? tc_launch<128>(p, s) : tc_launch<64>(p, s);
 }
 
 }  // namespace ssd

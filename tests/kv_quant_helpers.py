@@ -94,6 +94,13 @@ class AttnCase:
         s = np.concatenate(s, 1) if s else np.zeros((self.kc.shape[2], 0))
         return np.maximum(s[:, :self.prefix[b]], 2.0 ** -100)
 
+    def many(self, G):
+        """Whether the call takes the kernel for many rows."""
+        rows, (pages, Hkv) = self.q.shape[1] * G, self.k_codes.shape[:2]
+        capacity = self.k_codes.shape[2] if self.table is None else self.table.shape[1] * 128
+        groups = len(self.prefix) * Hkv * -(-rows // 16)
+        return not (rows <= 16 or (rows <= 48 and groups <= 152 and groups * capacity <= 1 << 17))
+
     def tolerance(self, b, o, size, heads, f32, wide):
         """Per element [Hq][dh]; heads = [(p, v)] of the kv heads, size = sum_j p_j |v_j|.
 
@@ -105,9 +112,8 @@ class AttnCase:
         Few rows: probabilities are rounded to 11 bits, 2^-11 size, and below the fp16 range by
         2^-25 each while the largest weight is at least 1: N 2^-25 448 max v_scale.
 
-        Many rows (over 16 packed ones at head dim 128): a probability is rounded to an e4m3
-        number and what is left (at most 2^-4 of it) to an e5m2 number (half a step 2^-3), or
-        by half of 2^-16, e5m2's least step, where that is more, while the key with the largest
+        Many rows: a probability is rounded to an e4m3 number and what is left (at most 2^-4 of
+        it) to an e5m2 number (half a step 2^-3), or by half of 2^-16, e5m2's least step, where that is more, while the key with the largest
         weight p_j s_j (s the value scale) has at least 2^4. Over a binade of the first and of
         the second number the product of the two uniform errors has a standard deviation under
         (2^-4 / sqrt 3)(2^-3 / sqrt 3) = 2^-7 / 3 < 2^-8 / sqrt 3; with sum_j p_j = 1 the least
@@ -118,7 +124,7 @@ class AttnCase:
         2^-14 sum_j p_j max_d |v_jd|."""
         tol = np.zeros_like(o)
         G = o.shape[0] // len(heads)
-        many = self.dh == 128 and self.q.shape[1] * G > 16
+        many = self.many(G)
         P = int(self.prefix[b])
         sv = self.v_scales(b)
         for h, (p, v) in enumerate(heads):

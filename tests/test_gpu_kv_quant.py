@@ -246,6 +246,17 @@ def test_attention_matches_the_oracle(paged, dh, G, NB, Dmax, sb):
     case.check(H.run(case, f32=False))
 
 
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("G,NB,Dmax,sb", [(4, 1, 13, 128), (7, 3, 5, 16), (8, 2, 9, 64), (1, 9, 16, 32), (64, 1, 1, 128), (13, 1, 10, 64),
+                                          (3, 1, 130, 16)])
+def test_attention_of_many_rows_matches_the_oracle(paged, dh, G, NB, Dmax, sb):
+    case = H.AttnCase(7 * G + NB + Dmax, LENGTHS, NB, Dmax, G, 2, dh, sb, paged)
+    assert case.many(G)
+    case.poison()
+    case.check(H.run(case))
+
+
 @pytest.mark.parametrize("dh,G,NB,Dmax", [(128, 4, 1, 1), (64, 4, 4, 20), (128, 4, 4, 20), (128, 8, 5, 20), (128, 1, 9, 16),
                                           (128, 2, 1, 256), (128, 7, 3, 40), (64, 2, 1, 200), (128, 32, 2, 9)])
 @pytest.mark.parametrize("sb", [16, 128])
@@ -356,7 +367,7 @@ def test_attention_repeats_bit_for_bit():
             assert torch.equal(a, H.run(case))
 
 
-@pytest.mark.parametrize("prefix,Dmax", [([4096] * 8, 9), ([20000], 9), ([4096, 100], 5), ([900] * 20, 1)])
+@pytest.mark.parametrize("prefix,Dmax", [([4096] * 8, 9), ([20000], 9), ([30000], 13), ([4096, 100], 5), ([900] * 20, 1)])
 def test_attention_is_stable_over_many_calls(prefix, Dmax):
     """The end of a CTA's products, the merge and the ring's reuse are ordered by waits: every
     one of many calls gives the first one's bits, and those are right."""
