@@ -762,25 +762,29 @@ static int rows_resident(int S) {
   return found[dev][S];
 }
 
-// CTAs that split a sequence, at most `most`. A CTA takes its share of the longest sequence's
-// steps and 6 beside them; the waves of resident clusters, at least one, and half of one for
-// the end, where CTAs run out (the longest started first), are to cost least. A sequence or
-// two (`even`) leave nothing short for a second wave, which then costs as much as the first
-// (one sequence of 32768 keys: 20.1 us by 12 CTAs, 31.3 by 16, of which one cluster of eight
-// waits). Over 2k-8k prefixes
-// of 8 kv heads it takes 5, 4 and 2 for 16, 32 and 64 sequences, the fastest of 1 .. 8 each
-// time (38.5, 61.8 and 107.4 us; with 1: 91.6, 103.2 and 131.2, with 8: 39.5, 73.9 and 142.1).
+// CTAs that split a sequence, at most `most`: those whose waves of resident clusters cost least. A CTA
+// takes its share of the longest sequence's steps and a few beside them. A sequence or two (`even`)
+// leave nothing short for a second wave, which then costs as much as the first (one sequence
+// of 32768 keys: 20.1 us by 12 CTAs, 31.3 by 16, of which one cluster of eight waits). Of many the
+// host knows only the capacity: where the lengths are equal waves count in full, where they vary
+// (the longest started first) they run into each other, so the mean of both is taken; a fuller GPU
+// makes each CTA slower, the more the less it computes a byte. Replayed from a graph, flushed, one
+// token and 8 kv heads, us by 1 .. 6 CTAs: 16 sequences of 4096 56.7 43.5 39.9 *41.3 52.5 50.3, 32 68.7
+// *66.7 77.3 70.0 78.9 74.1, of 2k-8k 111.6 85.8 82.7 *79.0 86.6 85.1, 64 152.2 *130.6 135.8 137.1
+// 141.9 149.3 (* the one taken); 32 rows of 4 sequences of 4096 58.5 38.1 35.9 *30.9 49.7 46.6.
 template <typename C>
 static int rows_split(long long groups, long long keys, int most, bool even) {
   const double iters = static_cast<double>(std::max<long long>(1, (keys + C::W * kStepKeys - 1) / (C::W * kStepKeys)));
+  const double slower = C::N8 == 1 ? 0.75 : 0.25;
   int best = 0;
   double cost = 0;
   for (int S = 1; S <= most && S <= iters; ++S) {
     const int clusters = rows_resident<C>(S);
     if (clusters <= 0) continue;
-    const double waves = static_cast<double>(groups) / clusters, cta = iters / S + 6.;
-    const double c = cta * (even ? std::ceil(waves) : std::max(waves, 1.) + 0.5 * std::min(waves, 1.));
-    if (best == 0 || c < cost) {
+    const double waves = static_cast<double>(groups) / clusters;
+    const double c = even ? (iters / S + 6.) * std::ceil(waves)
+                          : (iters / S + 8.) * ((std::ceil(waves) + std::max(waves, 1.)) / 2 + slower * std::min(waves, 1.));
+    if (best == 0 || c < (even ? 1. : 0.98) * cost) {
       cost = c;
       best = S;
     }
@@ -828,9 +832,10 @@ static int rows_choose(const AttnQuantParams& p, int rows, cudaStream_t s) {
   // 4096 keys of 8 kv heads: 8.6 us, with the other shape 11.0). Many: four small CTAs of an SM
   // keep it reading while one starts or ends (64 sequences of 2k-8k: 107 us; three of four
   // warps 119, six of two 120, one of eight 123). Sixteen rows need the registers of eight
-  // warps, in either case.
+  // warps an SM: two CTAs of four (32 sequences of 1000 keys 31.9 us, one of eight 44.6; 64 of
+  // 2k-8k 181 by both).
   using Few = RowsConfig<DH, N8, 8, 3, 1>;
-  using Many = std::conditional_t<N8 == 1, RowsConfig<DH, N8, 3, 2, 4>, Few>;
+  using Many = std::conditional_t<N8 == 1, RowsConfig<DH, N8, 3, 2, 4>, RowsConfig<DH, N8, 4, 2, 2>>;
   const long long groups = static_cast<long long>(p.B) * p.Hkv * ((rows + 8 * N8 - 1) / (8 * N8));
   if (groups * 8 <= 152) return rows_launch<Few>(p, rows, rows_split<Few>(groups, p.capacity, kMaxRanks, true), s);
   return rows_launch<Many>(p, rows, rows_split<Many>(groups, p.capacity, kMaxRanks, false), s);
