@@ -1037,12 +1037,14 @@ static int resident(int S) {
   return found[dev][S];
 }
 
-// CTAs that share a row tile's prefix. A CTA takes its share of the longest prefix's tiles and 6
-// for its start and merge; the waves of resident clusters are to cost least, with half a CTA for
-// the end where there is more than one (the longest started first). Over 32 sequences of 1k-16k
-// it takes one CTA (279 us; two 309), over 4 of 32768 two (462; one 572, three 531), for one of
-// 4096 five (19.7; four 21.5, six, of which one cluster waits, 31.7). Few row tiles over a long
-// prefix take up to 16 (one sequence of 32768, 2 kv heads, 320 rows: 38 us; with 8, 55).
+// CTAs that share a row tile's prefix: those whose waves of resident clusters cost least. A CTA takes its
+// share of the longest prefix's tiles and the time of 14 for its start and merge. The host knows
+// only the capacity: where prefixes are equal waves count in full, where they vary (the longest
+// started first) by the work, so the mean of both is taken. us by 1 .. 6 CTAs, 8 kv heads, replayed
+// from a graph: 320 rows of one sequence of 4096 keys 54.4 38.0 31.4 27.8 *25.8 42.1, of 4 *56.5 68.8
+// 78.9 70.8 83.1 95.4; 120 rows of 16 sequences of 1k-16k 158.9 *101.8 124.1 128.2 142.2 154.0, of
+// 4096 *56.4 72.8 83.8 95.4 106.5 119.6 (* the one taken); 800 rows of 4 of 32768 572 *462 531. Few
+// row tiles over a long prefix take up to 16 (one of 32768, 2 kv heads, 320 rows: 38 us; with 8, 55).
 template <int DH>
 static int choose_split(long long groups, long long tiles) {
   int best = 0;
@@ -1050,9 +1052,9 @@ static int choose_split(long long groups, long long tiles) {
   for (int S = 1; S <= kMaxSplit && S <= std::max<long long>(tiles, 1); ++S) {
     const int clusters = resident<DH>(S);
     if (clusters <= 0) continue;
-    const double waves = static_cast<double>(groups) / clusters, cta = static_cast<double>(tiles) / S + 6.;
-    const double c = waves <= 1. ? cta : (waves + 0.5) * cta;
-    if (best == 0 || c < cost) {
+    const double waves = static_cast<double>(groups) / clusters;
+    const double c = (static_cast<double>(tiles) / S + 14.) * (std::ceil(waves) + std::max(1., 0.8 * waves)) / 2;
+    if (best == 0 || c < 0.95 * cost) {
       cost = c;
       best = S;
     }
