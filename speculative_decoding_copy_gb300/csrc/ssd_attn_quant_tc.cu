@@ -43,7 +43,7 @@
 // The merge is that of ssd_attn_tc.cu: rows as 16-bit integers with a power-of-two scale per
 // 64 columns, one bulk copy to each CTA that owns rows.
 //
-// What bounds it, and what it measured: per 128 x 128 tile the products take 1024 clocks and the
+// What bounds it, and what it measured: per 128 x 128 tile the products take 1340 clocks and the
 // whole loop 2050 (2300 with every SM busy): issue slots are 54% used, the tensor pipe 57%, and no
 // more warps (four threads a row: 470 us where this takes 464), no turns of two softmax groups
 // on alternate tiles (509), no second accumulator for them (570) and no single thread a row (624)
