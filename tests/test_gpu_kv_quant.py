@@ -268,7 +268,7 @@ def test_attention_of_many_rows_and_long_prefixes(dh, G, NB, Dmax, sb):
     case.check(H.run(case), pick)
 
 
-@pytest.mark.parametrize("dh,NB,Dmax", [(64, 2, 3), (128, 2, 3), (128, 4, 20)])
+@pytest.mark.parametrize("dh,NB,Dmax", [(64, 2, 3), (128, 2, 3), (64, 4, 20), (128, 4, 20)])
 @pytest.mark.parametrize("paged", [False, True])
 def test_attention_never_looks_at_masked_places(dh, NB, Dmax, paged):
     """NaN in every code, scale, query and candidate that no present token may see."""
@@ -277,10 +277,10 @@ def test_attention_never_looks_at_masked_places(dh, NB, Dmax, paged):
     case.check(H.run(case))
 
 
-@pytest.mark.parametrize("NB,Dmax", [(2, 3), (4, 20)])
-def test_attention_keeps_a_spoiled_candidate_to_its_block(NB, Dmax):
+@pytest.mark.parametrize("dh,NB,Dmax", [(128, 2, 3), (128, 4, 20), (64, 2, 3), (64, 4, 20)])
+def test_attention_keeps_a_spoiled_candidate_to_its_block(dh, NB, Dmax):
     """An infinite key or value of one present token reaches the rows that see it, no others."""
-    case = H.AttnCase(11, [70, 200], NB, Dmax, 2, 2, 128, 64, True, blk_len=np.full((2, NB), Dmax))
+    case = H.AttnCase(11, [70, 200], NB, Dmax, 2, 2, dh, 64, True, blk_len=np.full((2, NB), Dmax))
     clean = H.run(case)
     case.vc[0, 1, 0, 5], case.kc[1, Dmax + 1, 1, :] = 0x7f80, 0x7fc0
     out = H.run(case).cpu().numpy()
@@ -292,7 +292,7 @@ def test_attention_keeps_a_spoiled_candidate_to_its_block(NB, Dmax):
     np.testing.assert_allclose(out[~bad], ref[~bad], rtol=2e-3, atol=2e-3)
 
 
-@pytest.mark.parametrize("dh,Dmax", [(128, 1), (128, 20), (64, 3)])
+@pytest.mark.parametrize("dh,Dmax", [(128, 1), (128, 20), (64, 3), (64, 20)])
 def test_attention_with_block_scales_far_apart(dh, Dmax):
     """Blocks of zero values (the least scale), of scale zero, and of scales 2^12 apart: the
     probabilities of their keys still count, and the small blocks lose nothing to the large."""
@@ -309,7 +309,7 @@ def test_attention_with_block_scales_far_apart(dh, Dmax):
 
 
 @pytest.mark.parametrize("v_scale", [2.0 ** -16, 2.0 ** -8, 2.0 ** 6])
-@pytest.mark.parametrize("dh,Dmax", [(64, 1), (128, 1), (128, 20)])
+@pytest.mark.parametrize("dh,Dmax", [(64, 1), (64, 20), (128, 1), (128, 20)])
 def test_attention_of_a_flat_prefix_beside_heavy_own_keys(dh, Dmax, v_scale):
     """Thousands of keys of equal small weight, which the own-block keys, without a value scale,
     must not push to the low end of the probabilities' range."""
@@ -319,7 +319,7 @@ def test_attention_of_a_flat_prefix_beside_heavy_own_keys(dh, Dmax, v_scale):
     case.check(H.run(case))
 
 
-@pytest.mark.parametrize("dh,Dmax", [(128, 1), (128, 20)])
+@pytest.mark.parametrize("dh,Dmax", [(128, 1), (128, 20), (64, 20)])
 def test_attention_with_sharp_and_growing_scores(dh, Dmax):
     """Scores of +-60 whose maximum keeps growing along the prefix, far past every threshold."""
     case = H.AttnCase(17, [2000], 2, Dmax, 4, 1, dh, 16, True, q_scale=6.0, pow2=True, blk_len=np.full((1, 2), Dmax))
@@ -368,10 +368,11 @@ def test_attention_repeats_bit_for_bit():
 
 
 @pytest.mark.parametrize("prefix,Dmax", [([4096] * 8, 9), ([20000], 9), ([30000], 13), ([4096, 100], 5), ([900] * 20, 1)])
-def test_attention_is_stable_over_many_calls(prefix, Dmax):
+@pytest.mark.parametrize("dh", [64, 128])
+def test_attention_is_stable_over_many_calls(dh, prefix, Dmax):
     """The end of a CTA's products, the merge and the ring's reuse are ordered by waits: every
     one of many calls gives the first one's bits, and those are right."""
-    case = H.AttnCase(43, prefix, 1, Dmax, 4, 2, 128, 64, True, blk_len=np.full((len(prefix), 1), Dmax))
+    case = H.AttnCase(43, prefix, 1, Dmax, 4, 2, dh, 64, True, blk_len=np.full((len(prefix), 1), Dmax))
     a, kw = case.args(), case.kw()
     first = S.ssd_verify_attn_quant(*a, **kw, out_f32=True)
     out = [torch.empty_like(first) for _ in range(200)]
@@ -400,13 +401,14 @@ def test_attention_of_many_sequences(B, NB, Dmax):
     case.check(H.run(case))
 
 
+@pytest.mark.parametrize("dh", [64, 128])
 @pytest.mark.parametrize("NB,Dmax,G", [(300, 16, 2), (1024, 8, 1), (8192, 1, 1), (32, 256, 1)])
-def test_attention_of_many_sparse_blocks(NB, Dmax, G):
+def test_attention_of_many_sparse_blocks(dh, NB, Dmax, G):
     """One present token in each of many blocks: rows of one tile far apart in the slots."""
     blk_len = np.zeros((1, NB), np.int32)
     blk_len[:, ::max(1, NB // 300)] = 1
     blk_len[0, NB - 1] = Dmax
-    case = H.AttnCase(59, [200], NB, Dmax, G, 1, 128, 128, True, blk_len=blk_len)
+    case = H.AttnCase(59, [200], NB, Dmax, G, 1, dh, 128, True, blk_len=blk_len)
     case.poison()
     case.check(H.run(case))
 
