@@ -5,23 +5,29 @@
 // grown scale exact on the codes already there: only those that fall below the smallest
 // normal code round a second time.
 //
-// One CTA quantises one run (the rows that go to one block) of one head, of the keys or
-// of the values: the rows are read once into registers (up to eight 16-byte words a
-// thread cover the 128 rows x 128 elements of a block), their largest magnitude is reduced
-// over the CTA, and the codes leave as 8 bytes a word, contiguous over the run.
+// A group of warps, one for each 16 tokens of a scale block, quantises one run (the rows that go to
+// one block) of one head, of the keys or of the values: the rows are read once into registers
+// (up to eight 16-byte words a thread cover the block's rows x 128 elements), their largest
+// magnitude is reduced over the group, and the codes leave as 8 bytes a word, contiguous over
+// the run.
 //
 // What bounds them: the bytes of the rows, and for a few tokens the launch. 21 384 prompt rows
 // of 8 kv heads (131 MB) take 24 us, 5.5 TB/s of the 6.8 that a plain copy reaches: a CTA reads
 // its 32 KB, waits for the maximum of all of it, and writes; five CTAs an SM, a few registers of
-// theirs spilled, fill each other's waits better than four without (29.1 against 26.7 us replayed
-// from a graph), six worse. Replayed from a graph 64 single tokens take 5.9 us, the accepted tokens of
+// theirs spilled, fill each other's waits better than four without (31.3 us from cold caches, 34.5),
+// six worse; with smaller blocks, whose groups are not tied to each other, four do (33.9, five 42).
+// Blocks of 16 tokens take 33.9 us by a warp each, where one run after another by all of a CTA took
+// 101, fp32 rows 54 and 205. Replayed from a graph 64 single tokens take 5.9 us, the accepted tokens of
 // one sequence 3.1 and of 32 sequences 4.6: little more than an empty kernel.
+#include <type_traits>
+
 #include "ssd_kvq.cuh"
 
 namespace ssd {
 
 constexpr int kQuantThreads = 256;
 constexpr int kMaxScaleBlock = 128;
+constexpr int kGroupRows = 16;          // rows of a run that a warp takes
 
 struct QuantDst {
   uint8_t* codes;       // place 0 of the block, [scale_block][dh]
@@ -107,17 +113,29 @@ __device__ __forceinline__ uint32_t finite_top(const Word<T>& w) {
   return m;
 }
 
-// Quantise n <= 128 rows of dh elements, `stride` elements apart at src, into places
-// d.row .. d.row + n - 1 of one block. Every thread of the CTA calls it; `red` holds one
-// word a warp.
-template <typename T>
+// the W warps that work on one run
+template <int W>
+struct Group {
+  static constexpr int kThreads = 32 * W;
+  int tid;                                // this thread's number among them
+  int barrier;                            // of their own
+  uint32_t* red;                          // one word a warp
+  __device__ __forceinline__ void sync() const {
+    __syncwarp();
+    if (W > 1) asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(barrier), "n"(kThreads) : "memory");
+  }
+};
+
+// Quantise n rows (at most 16 a warp of the group) of dh elements, `stride` elements apart at src, into
+// places d.row .. d.row + n - 1 of one block. Every thread of the group calls it.
+template <typename T, int W>
 __device__ __forceinline__ void quant_run(const T* __restrict__ src, int64_t stride, int n, int dh, QuantDst d,
-                                          uint32_t* red) {
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+                                          const Group<W>& grp) {
+  const int tid = grp.tid, lane = tid & 31, wid = tid >> 5;
   const int sh = dh == 128 ? 4 : 3;           // 8-element words per row
-  constexpr int kWords = kMaxScaleBlock * 16 / kQuantThreads;
+  constexpr int kWords = kGroupRows * 16 / 32;
   // word i of a thread: row row0 + i * rows_step, the same place in each
-  const int row0 = tid >> sh, rows_step = kQuantThreads >> sh;
+  const int row0 = tid >> sh, rows_step = grp.kThreads >> sh;
   const T* p = src + row0 * stride + ((tid & ((1 << sh) - 1)) << 3);
   const int64_t step = rows_step * stride;
   const int mine = row0 < n ? min(kWords, (n - 1 - row0) / rows_step + 1) : 0;
@@ -139,18 +157,18 @@ __device__ __forceinline__ void quant_run(const T* __restrict__ src, int64_t str
       if (i < mine) m = max(m, finite_top<T>(w[i]));
   }
   m = __reduce_max_sync(0xffffffffu, m);
-  __syncthreads();                            // `red` and the block's scale of an earlier run
-  if (lane == 0) red[wid] = m;
-  __syncthreads();
+  grp.sync();                                 // `red` and the block's scale of an earlier run
+  if (lane == 0) grp.red[wid] = m;
+  grp.sync();
 #pragma unroll
-  for (int i = 0; i < kQuantThreads / 32; ++i) m = max(m, red[i]);
+  for (int i = 0; i < W; ++i) m = max(m, grp.red[i]);
   const float need = pow2_scale(m);
   const float now = d.row == 0 ? need : fmaxf(old, need);
   if (d.row > 0 && now > old) {
     // the rows before the run, under the grown scale
     const float ratio = __fdiv_rn(old, now);
     const int held = d.row << sh;
-    for (int c = tid; c < held; c += kQuantThreads) {
+    for (int c = tid; c < held; c += grp.kThreads) {
       uint2* p = reinterpret_cast<uint2*>(d.codes) + c;
       const uint2 v = *p;
       const uint32_t h[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
@@ -172,7 +190,7 @@ __device__ __forceinline__ void quant_run(const T* __restrict__ src, int64_t str
       if (i < mine) {
         float x[8];
         w[i].get(x);
-        out[i * kQuantThreads] = make_uint2(e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+        out[i * grp.kThreads] = make_uint2(e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
                                             e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
       }
     }
@@ -185,25 +203,29 @@ __device__ __forceinline__ void quant_run(const T* __restrict__ src, int64_t str
         w[i].get(x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = divide(x[e], now);
-        out[i * kQuantThreads] = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+        out[i * grp.kThreads] = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
       }
     }
   }
-  __syncthreads();                            // every thread has read the old scale
+  grp.sync();                                 // every thread has read the old scale
   if (tid == 0) *d.scale = now;
 }
 
 // grid (row ranges of `range` rows) x (heads, keys / values), the latter fastest, so that the CTAs
 // that share rows (and DRAM pages of a projection's output) run together: the runs that start
-// in the range
-template <typename T>
-__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 5 : 2)
-k_append_quant(ssd_append_quant_args a, int range, int sb_log2, WsHeader* hdr) {
+// in the range, dealt to the groups in turn
+template <typename T, int W>
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? (W == 8 ? 5 : 4) : 2)
+k_append_quant(ssd_append_quant_args a, int range, WsHeader* hdr) {
+  constexpr int sb_log2 = W == 1 ? 4 : W == 2 ? 5 : W == 4 ? 6 : 7;     // 16 tokens a warp
   __shared__ int32_t slot[2 * kMaxScaleBlock];
   constexpr int kMasks = 2 * kMaxScaleBlock / 32;
   __shared__ uint32_t brk[kMasks];                      // rows that do not continue the row before
   __shared__ uint32_t start[kMasks];                    // ... and have a slot
   __shared__ uint32_t red[kQuantThreads / 32];
+  constexpr int kGroups = kQuantThreads / Group<W>::kThreads;
+  const int mine = static_cast<int>(threadIdx.x) / Group<W>::kThreads;
+  const Group<W> grp = {static_cast<int>(threadIdx.x) % Group<W>::kThreads, 1 + mine, red + mine * W};
   static_assert(kQuantThreads == 2 * kMaxScaleBlock, "one thread a row of the window");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x;
@@ -211,7 +233,7 @@ k_append_quant(ssd_append_quant_args a, int range, int sb_log2, WsHeader* hdr) {
   const bool is_v = part >= a.Hkv;
   const int h = is_v ? part - a.Hkv : part;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(2 * a.Hkv)) * range;
-  const int sb = 1 << sb_log2;
+  constexpr int sb = 1 << sb_log2;
   const int window = range + sb;                        // a run that starts in the range ends here
   // one thread a row: its slot, and whether it continues the run of the row before
   const int64_t t = t0 + tid;
@@ -239,8 +261,10 @@ k_append_quant(ssd_append_quant_args a, int range, int sb_log2, WsHeader* hdr) {
   const T* src = static_cast<const T*>(is_v ? a.v_new : a.k_new) + static_cast<int64_t>(h) * a.dh;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
   const int64_t blocks = (a.page_tokens + sb - 1) >> sb_log2;
+  int run = 0;
   for (int q = 0; q < kMasks; ++q) {
     for (uint32_t left = start[q]; left != 0; left &= left - 1) {
+      if (run++ % kGroups != mine) continue;
       const int first = q * 32 + __ffs(static_cast<int>(left)) - 1;
       // the next break ends the run (rows outside the list or the window are breaks)
       int wd = q;
@@ -257,18 +281,20 @@ k_append_quant(ssd_append_quant_args a, int range, int sb_log2, WsHeader* hdr) {
                 (ph * a.page_tokens + (static_cast<int64_t>(blk) << sb_log2)) * a.dh;
       d.scale = (is_v ? a.v_scale : a.k_scale) + ph * blocks + blk;
       d.row = off & (sb - 1);
-      quant_run<T>(src + (t0 + first) * stride, stride, last - first, a.dh, d, red);
+      quant_run<T, W>(src + (t0 + first) * stride, stride, last - first, a.dh, d, grp);
     }
   }
 }
 
 // grid (sequences, heads, (keys / values) x blocks a run of Dmax rows can touch)
-template <typename T>
-__global__ void __launch_bounds__(kQuantThreads)
-k_commit_quant(ssd_commit_quant_args a, int64_t page_tokens, int sb_log2, int segs, WsHeader* hdr) {
-  __shared__ uint32_t red[kQuantThreads / 32];
+template <typename T, int W>
+__global__ void __launch_bounds__(32 * W)
+k_commit_quant(ssd_commit_quant_args a, int64_t page_tokens, int segs, WsHeader* hdr) {
+  constexpr int sb_log2 = W == 1 ? 4 : W == 2 ? 5 : W == 4 ? 6 : 7;     // 16 tokens a warp
+  __shared__ uint32_t red[W];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x;
+  const Group<W> grp = {tid, 0, red};
   const int b = blockIdx.x, h = blockIdx.y;
   const bool is_v = static_cast<int>(blockIdx.z) >= segs;
   const int seg = static_cast<int>(blockIdx.z) - (is_v ? segs : 0);
@@ -307,8 +333,19 @@ k_commit_quant(ssd_commit_quant_args a, int64_t page_tokens, int sb_log2, int se
   d.row = static_cast<int>(place) & ((1 << sb_log2) - 1);
   const int64_t src_row = static_cast<int64_t>(b) * a.NB * a.Dmax + static_cast<int64_t>(k) * a.Dmax + (p0 - P);
   const int64_t stride = static_cast<int64_t>(a.Hkv) * a.dh;
-  quant_run<T>(static_cast<const T*>(is_v ? a.v_cand : a.k_cand) + src_row * stride + static_cast<int64_t>(h) * a.dh,
-               stride, static_cast<int>(p1 - p0), a.dh, d, red);
+  quant_run<T, W>(static_cast<const T*>(is_v ? a.v_cand : a.k_cand) + src_row * stride + static_cast<int64_t>(h) * a.dh,
+               stride, static_cast<int>(p1 - p0), a.dh, d, grp);
+}
+
+// `launch` with the warps of a group as a constant
+template <typename F>
+static cudaError_t by_warps(int scale_block, F launch) {
+  switch (scale_block) {
+    case 16: return launch(std::integral_constant<int, 1>());
+    case 32: return launch(std::integral_constant<int, 2>());
+    case 64: return launch(std::integral_constant<int, 4>());
+    default: return launch(std::integral_constant<int, 8>());
+  }
 }
 
 }  // namespace ssd
@@ -342,16 +379,17 @@ extern "C" int ssd_append_kv_quant(const ssd_append_quant_args* a, void* ws, siz
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   WsHeader* hdr = static_cast<WsHeader*>(ws);
   // rows a CTA looks at: one while there are few, so that single tokens run side by side;
-  // up to a whole block's where most rows continue a run and their CTAs would find nothing
+  // up to 128, a run for each of its groups, where most rows continue a run
   int range = 1;
-  while (range < a->scale_block && a->T * a->Hkv * 2 / range > 4096) range *= 2;
+  while (range < kMaxScaleBlock && a->T * a->Hkv * 2 / range > 4096) range *= 2;
   const int64_t ctas = (a->T + range - 1) / range * 2 * a->Hkv;
   if (ctas > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(ctas));
-  const int lg = log2_of(a->scale_block);
-  const cudaError_t e = a->dtype == SSD_BF16
-      ? launch_pdl(k_append_quant<uint16_t>, grid, dim3(kQuantThreads), 0, s, *a, range, lg, hdr)
-      : launch_pdl(k_append_quant<float>, grid, dim3(kQuantThreads), 0, s, *a, range, lg, hdr);
+  const cudaError_t e = by_warps(a->scale_block, [&](auto w) {
+    return a->dtype == SSD_BF16
+        ? launch_pdl(k_append_quant<uint16_t, w()>, grid, dim3(kQuantThreads), 0, s, *a, range, hdr)
+        : launch_pdl(k_append_quant<float, w()>, grid, dim3(kQuantThreads), 0, s, *a, range, hdr);
+  });
   if (e != cudaSuccess) return SSD_ERR_CUDA;
   count_launch();
   return check_launch();
@@ -395,10 +433,11 @@ extern "C" int ssd_commit_kv_quant(const ssd_commit_quant_args* a, void* ws, siz
   // blocks that Dmax rows can touch
   const int segs = (a->Dmax + a->scale_block - 2) / a->scale_block + 1;
   const dim3 grid(static_cast<unsigned>(a->B), static_cast<unsigned>(a->Hkv), static_cast<unsigned>(2 * segs));
-  const int lg = log2_of(a->scale_block);
-  const cudaError_t e = a->dtype == SSD_BF16
-      ? launch_pdl(k_commit_quant<uint16_t>, grid, dim3(kQuantThreads), 0, s, *a, page_tokens, lg, segs, hdr)
-      : launch_pdl(k_commit_quant<float>, grid, dim3(kQuantThreads), 0, s, *a, page_tokens, lg, segs, hdr);
+  const cudaError_t e = by_warps(a->scale_block, [&](auto w) {
+    return a->dtype == SSD_BF16
+        ? launch_pdl(k_commit_quant<uint16_t, w()>, grid, dim3(32 * w()), 0, s, *a, page_tokens, segs, hdr)
+        : launch_pdl(k_commit_quant<float, w()>, grid, dim3(32 * w()), 0, s, *a, page_tokens, segs, hdr);
+  });
   if (e != cudaSuccess) return SSD_ERR_CUDA;
   count_launch();
   return check_launch();

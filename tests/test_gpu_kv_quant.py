@@ -145,7 +145,7 @@ def test_append_of_many_rows():
     """Long prompts: ranges of rows a CTA walks, runs across their borders."""
     rng = np.random.default_rng(8)
     Hkv, dh, pages = 2, 64, 64
-    for sb in (16, 128):
+    for sb in (16, 32, 64, 128):
         c = [x for w in range(2) for x in H.cache(rng, pages, Hkv, 128, dh, sb)]
         t = [dev(x) for x in c]
         parts, at = [], 0
@@ -162,6 +162,30 @@ def test_append_of_many_rows():
         full = dev(bits)
         S.ssd_append_kv_quant(full[:, 0], full[:, 1], dev(slots), t[0], t[2], t[1], t[3], sb)
         _same_cache(c, t)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("sb", [16, 32, 64, 128])
+def test_append_of_a_large_prompt(sb, f32):
+    """Enough rows that a CTA walks 128 of them, all its groups at work."""
+    rng = np.random.default_rng(sb)
+    T, Hkv, dh, pages = 16500, 16, 64, 135
+    c = [x for w in range(2) for x in H.cache(rng, pages, Hkv, 128, dh, sb)]
+    t = [dev(x) for x in c]
+    order = rng.permutation(pages)
+    pos = 5 + np.arange(T)
+    slots = (order[pos // 128] * 128 + pos % 128).astype(np.int32)
+    slots[7040 - 5:7168 - 5] = -1        # whole blocks: a hole inside one would leave it two runs, whose order is open
+    if f32:
+        x = rng.standard_normal((T, 2, Hkv, dh)).astype(np.float32)
+        rows, x64 = dev(x), x.astype(np.float64)
+    else:
+        bits, x64 = H.bf16(rng, T, 2, Hkv, dh)
+        rows = dev(bits)
+    K.append(x64[:, 0], slots, c[0], c[1], sb)
+    K.append(x64[:, 1], slots, c[2], c[3], sb)
+    S.ssd_append_kv_quant(rows[:, 0], rows[:, 1], dev(slots), t[0], t[2], t[1], t[3], sb)
+    _same_cache(c, t)
 
 
 def test_append_edges():
