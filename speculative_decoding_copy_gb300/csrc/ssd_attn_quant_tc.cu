@@ -99,7 +99,10 @@ struct Bars {
   uint64_t s_full[SBUF], p_full[SBUF], s_free[SBUF], pv_done[2];
   uint64_t o_done;                        // every product into O is done
   uint64_t v_clean;                       // the value rows past the prefix are zeros
-  uint64_t own_clean[2];                  // an own-block tile's values are finite
+  // an own-block tile's values are finite. One barrier a ring slot: an arrival for tile j + 4
+  // follows the copy into the slots that P V of tile j left, whose issue waited for tile j's phase,
+  // so no phase passes the wait for the one before.
+  uint64_t own_clean[SLOTS];
   uint64_t recv_full;
   uint32_t tmem_base;
   int failed;
@@ -343,7 +346,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     mbar_init(&bars.recv_full, 1);
     mbar_init(&bars.v_clean, 1);
     mbar_init(&bars.o_done, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&bars.own_clean[i], kSoftmax);
+    for (int i = 0; i < SLOTS; ++i) mbar_init(&bars.own_clean[i], kSoftmax);
     for (int i = 0; i < SBUF; ++i) {
       mbar_init(&bars.s_full[i], 1);
       mbar_init(&bars.s_free[i], 1);
@@ -564,7 +567,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       }
       if (odd) *reinterpret_cast<volatile int*>(&bars.odd_own) = 1;
       fence_async_smem();
-      mbar_arrive(&bars.own_clean[j & 1]);
+      mbar_arrive(&bars.own_clean[j % SLOTS]);
       const int sb = j % SBUF;
       mbar_wait(bars, &bars.s_full[sb], (j / SBUF) & 1, p.hdr, 460);
       __syncwarp();
@@ -749,7 +752,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         mbar_wait(bars, &bars.full_v[s0], (u / SLOTS) & 1, p.hdr, 484);
         if (own) {
           mbar_wait(bars, &bars.full_v[s1], ((u + UO - 1) / SLOTS) & 1, p.hdr, 485);
-          mbar_wait(bars, &bars.own_clean[j & 1], (j >> 1) & 1, p.hdr, 487);
+          mbar_wait(bars, &bars.own_clean[j % SLOTS], (j / SLOTS) & 1, p.hdr, 487);
         }
         if (ragged && j == nT - 1) mbar_wait(bars, &bars.v_clean, 0, p.hdr, 486);
         mbar_wait(bars, &bars.p_full[sb], (j / SBUF) & 1, p.hdr, 488);
