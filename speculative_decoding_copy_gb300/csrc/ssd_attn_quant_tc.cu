@@ -96,7 +96,9 @@ static_assert(kMaxBlocks * 4 <= static_cast<int>(2 * SLOTS * kSlot), "block ends
 struct Bars {
   uint64_t full_k[SLOTS], full_v[SLOTS], empty_k[SLOTS], empty_v[SLOTS];
   uint64_t q_full;
-  uint64_t s_full[SBUF], p_full[SBUF], s_free[SBUF], pv_done[2];
+  // s_free: P V of the tile in the buffer is done. Also what a rescaling of O waits for: S of tile j - 1
+  // was issued behind the phase of tile j - 4, so a wait for tile j - 1's cannot take an earlier one.
+  uint64_t s_full[SBUF], p_full[SBUF], s_free[SBUF];
   uint64_t o_done;                        // every product into O is done
   uint64_t v_clean;                       // the value rows past the prefix are zeros
   // an own-block tile's values are finite. One barrier a ring slot: an arrival for tile j + 4
@@ -352,7 +354,6 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       mbar_init(&bars.s_free[i], 1);
       mbar_init(&bars.p_full[i], kSoftmax);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&bars.pv_done[i], 1);
     bars.failed = 0;
     bars.odd_own = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -520,7 +521,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       pair_sync(warp & 3);                                    // the pairs may be written again
       if (j > 0 && __any_sync(0xffffffffu, need)) {
         // O holds the sum up to tile j - 1: wait for its last product, then rescale
-        mbar_wait(bars, &bars.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.hdr, 461);
+        mbar_wait(bars, &bars.s_free[(j - 1) % SBUF], ((j - 1) / SBUF) & 1, p.hdr, 461);
         __syncwarp();
         tc_fence_after();
 #pragma unroll 1
@@ -612,8 +613,6 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       mbar_arrive(&bars.p_full[sb]);
     }
     bars.pair[half][row] = l;                              // read after the barrier before the merge
-    // (a wait on pv_done would not do: the last three products may be open, and a wait for a
-    // parity returns at once while the phase two before is the last one completed)
     if (nT > 0) mbar_wait(bars, &bars.o_done, 0, p.hdr, 462);
     __syncwarp();
     tc_fence_after();
@@ -771,7 +770,6 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           }
         }
         mma_commit(&bars.s_free[sb]);
-        mma_commit(&bars.pv_done[j & 1]);
         mma_commit(&bars.empty_v[s0]);
         if (own && UO > 1) mma_commit(&bars.empty_v[s1]);
         u += own ? UO : 1;
