@@ -51,8 +51,8 @@
 // bf16, at 1375 of the GPU's 1400 W: there even the loop without its maximum takes as long. 32
 // sequences of 1k-16k: 263 us. One of 4096 keys, 320 rows: 19 us, of which the loop is 8.5; Q's
 // conversion, the own-block tile and the merge are the rest.
-// Waits are bounded; on expiry the CTA records SSD_ERR_TIMEOUT, skips what is left and exits
-// through the cluster barriers.
+// Waits are bounded; on expiry the CTA records SSD_ERR_TIMEOUT, skips what is left, gives its own
+// copies and products in flight as long again, and exits through the cluster barriers.
 #include <cuda.h>
 #include <math.h>
 
@@ -106,8 +106,10 @@ struct Bars {
   // so no phase passes the wait for the one before.
   uint64_t own_clean[SLOTS];
   uint64_t recv_full;
+  uint64_t drained[2];                    // after a wait gave up: the products issued so far are done
   uint32_t tmem_base;
   int failed;
+  int sent[2];                            // ring units that the K and V producers have copied
   int odd_own;                            // an own-block value was not finite
   int seq, rows;                          // the sequence; its present rows
   int row_slot[BM];                       // candidate slot of a row of this tile
@@ -348,6 +350,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     mbar_init(&bars.recv_full, 1);
     mbar_init(&bars.v_clean, 1);
     mbar_init(&bars.o_done, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.drained[i], 1);
     for (int i = 0; i < SLOTS; ++i) mbar_init(&bars.own_clean[i], kSoftmax);
     for (int i = 0; i < SBUF; ++i) {
       mbar_init(&bars.s_full[i], 1);
@@ -628,15 +631,17 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     uint64_t* full = kside ? bars.full_k : bars.full_v;
     uint64_t* empty = kside ? bars.empty_k : bars.empty_v;
     const uint32_t ring = sbase + (kside ? OFF_K : OFF_V);
-    auto slot_for = [&](int u) {
+    // whether the slot of unit u may be filled: no more copies once a wait gave up
+    auto slot_for = [&](int u) -> bool {
       if (u >= SLOTS) mbar_wait(bars, &empty[u % SLOTS], ((u / SLOTS) - 1) & 1, p.hdr, kside ? 470 : 471);
-      __syncwarp();
+      return __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&bars.failed), 0) == 0;
     };
     int u = 0;
-    for (int j = 0; j < nC; ++j) {
+    bool go = true;
+    for (int j = 0; go && j < nC; ++j) {
       for (int h = 0; h < UO; ++h, ++u) {
-        slot_for(u);
-        if (lane == 0 && !bars.failed) {
+        if (!(go = slot_for(u))) break;
+        if (lane == 0) {
           if (kside) mbar_arrive(&full[u % SLOTS]);        // no factors
           mbar_expect_tx(&full[u % SLOTS], kSlot);
           tma_load_3d(ring + (u % SLOTS) * kSlot, kside ? &tmap_kc : &tmap_vc, 64 * h, kvh, b * NT + s_base + j * BN,
@@ -660,9 +665,9 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     };
     int page = load_page(j0), page1 = load_page(j0 + 1), page2 = load_page(j0 + 2);
     float scale = load_scale(j0, page), scale1 = load_scale(j0 + 1, page1);
-    for (int t = j0; t < j1; ++t, ++u) {
-      slot_for(u);
-      if (lane == 0 && !bars.failed) {
+    for (int t = j0; go && t < j1; ++t, ++u) {
+      if (!(go = slot_for(u))) break;
+      if (lane == 0) {
         mbar_expect_tx(&full[u % SLOTS], kSlot);
         tma_load_2d(ring + (u % SLOTS) * kSlot, kside ? &tmap_k : &tmap_v, 0,
                     (page * p.Hkv + kvh) * static_cast<int>(p.page_tokens) + (p.block_table == nullptr ? t * BN : 0),
@@ -686,6 +691,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       page1 = page2;
       page2 = load_page(t + 3);
     }
+    if (lane == 0) bars.sent[kside ? 0 : 1] = u;
     __syncwarp();
     if (!kside && ragged) {
       const int u = UO * nC + nP - 1;
@@ -784,6 +790,22 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     __syncwarp();
   }
 
+  // After a wait gave up (every role has ended): this CTA's copies and products still in flight are
+  // given as long again before shared memory serves another purpose, TMEM is freed and the CTA ends.
+  auto drain = [&] {
+    if (lane != 0 || !bars.failed) return;
+    int gave_up = 0;
+    if (warp == 4 || warp == 6) {
+      const int n = bars.sent[warp == 4 ? 0 : 1];
+      for (int i = max(0, n - SLOTS); i < n; ++i)
+        mbar_wait_bounded((warp == 4 ? bars.full_k : bars.full_v) + i % SLOTS, (i / SLOTS) & 1, &gave_up, p.hdr, 491, kWaitClocks);
+    } else if (warp == 5 || warp == 7) {
+      uint64_t* bar = &bars.drained[warp == 5 ? 0 : 1];
+      mma_commit(bar);
+      mbar_wait_bounded(bar, 0, &gave_up, p.hdr, 492, kWaitClocks);
+    }
+  };
+
   // ---- one share: the rows leave from TMEM
   if (S == 1) {
     if (softmax) {
@@ -829,6 +851,10 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       tc_fence_before();
     }
     __syncthreads();
+    if (bars.failed) {
+      drain();
+      __syncthreads();
+    }
     if (warp == 4) {
       tc_fence_after();
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -890,7 +916,8 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     float* tail = reinterpret_cast<float*>(stage + row * kRowB + 2 * DH);
     if (half == 0) {
       tail[0] = m;
-      tail[1] = l + bars.pair[1][row];
+      // a share that gave up makes the rows NaN
+      tail[1] = *reinterpret_cast<volatile int*>(&bars.failed) ? NAN : l + bars.pair[1][row];
     }
     // the sign tells the owner of the row to look closer
     const bool look = odd || (nC > 0 && *reinterpret_cast<volatile int*>(&bars.odd_own));
@@ -902,6 +929,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
   __syncwarp();
   cluster_sync();                                        // every ring of the cluster is idle
   tc_fence_after();
+  if (bars.failed) drain();
   if (tid < S - 1) {
     const int c = (rank + 1 + tid) % S;
     const int n_c = min(rv, (c + 1) * rpc) - c * rpc;
@@ -979,6 +1007,10 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
   }
   // this CTA's outgoing copies have finished reading its staged rows before it exits
   if (tid < S - 1) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  if (tid == 0 && nr > 0 && bars.failed) {               // ... and the incoming ones have arrived
+    int gave_up = 0;
+    mbar_wait_bounded(&bars.recv_full, 0, &gave_up, p.hdr, 493, kWaitClocks);
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 4) {
