@@ -2,15 +2,17 @@
 // ssd_attn_quant.cu; what differs is who does the products.
 //
 // Precision on 8-bit operands. The codes go into the products as they lie in the cache
-// (kind::f8f6f4, fp32 sums). Q and P, which have more bits, are sums of two 8-bit numbers, one
+// (kind::f8f6f4, fp32 sums). Q and P, which have more bits, are sums of two and three 8-bit numbers, one
 // product each into the same accumulator. q (8 significant bits) is two e4m3 numbers, exact but
-// for what lies under 2^-17 of its row's largest element. A probability is an e4m3 number and,
-// for what is left, an e5m2 number: its relative error is about that of one bf16 number, and
-// e5m2's range carries small probabilities (the long tail of a long prefix) down to 2^-21 of
-// the largest. Two 8-bit products cost what one bf16 product costs, and no code is converted.
+// for what lies under 2^-17 of its row's largest element. A probability is the sum of three e5m2
+// numbers, each the rest of the ones before (2^-9 together, a bf16 number's rounding), for which
+// e5m2's range lets the largest lie at 2^11 to 2^15: a probability of 2^-19 of the largest still has
+// its 9 bits, and smaller ones are off by at most 2^-28 of it. A long prefix needs that: beside one key
+// of a large weight (or a block of a large value scale) its tail is 2^-15 each and most of the mass
+// together. With an e4m3 and an e5m2 number, 8 bits down to 2^-10 and three at 2^-15, such a
+// tail of 32768 keys was 1.3% off. The third product costs 256 of a tile's 1600 clocks of products; no code is converted.
 // (Converting each tile to fp16 in shared memory would move 64 KB more per tile through it,
-// which the products already keep three quarters busy; with e4m3 for what is left, 2^-14 of
-// the largest, the output of 32768 keys was 0.0018 off beside its own rounding's 0.0017.)
+// which the products already keep three quarters busy.)
 //
 // Rows. The G query heads of the present tokens pack into rows (absent tokens take none, so a
 // batch with few present candidates runs few row tiles); a CTA owns 128 of them and one share
@@ -23,11 +25,10 @@
 //              parts, swizzled; rank 0 also bf16), then the online softmax of each 128-key tile,
 //              read from TMEM once: per 16 keys one K factor, one log2 of the V factor and one
 //              weight 1/sv of the sum. A barrier of the two warps that share rows tells whether one of their
-//              references has to move, which is rare. P goes back to TMEM over the first half of the tile's S
-//              buffer (two parts of 32 columns, four keys a word; bf16 pairs for own-block
-//              tiles). In fp16 with the exponent offset of the formats taken into the
-//              exponential, the parts are bytes of a probability's bits and of what is left,
-//              so no format conversion is needed. On rank 0 they also take infinities and NaN
+//              references has to move, which is rare. P goes back to TMEM over the tile's S
+//              buffer (three parts of 32 columns, four keys a word; bf16 pairs for own-block
+//              tiles). In fp16 the parts are the upper bytes of a probability's bits and of what
+//              is left, so no format conversion is needed. On rank 0 they also take infinities and NaN
 //              out of own-block values;
 //   warp 4     TMEM allocation, then the producer of the K tiles;
 //   warp 6     the producer of the V tiles; it clears the value rows past the prefix (codes
@@ -75,7 +76,7 @@ constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int SBUF = 3;
 constexpr uint32_t TM_S = 0, TM_O = SBUF * BN;
-constexpr uint32_t P2 = BN / 4;           // columns from a probability's first part to its second
+constexpr uint32_t PART = BN / 4;         // columns of one part of the probabilities
 constexpr uint32_t kSlot = 16384;         // 128 rows of 128 bytes, 128-byte swizzle
 constexpr uint32_t OFF_Q8 = 0;            // two parts
 constexpr uint32_t OFF_QB = 2 * kSlot;    // bf16, two 64-column halves
@@ -169,9 +170,9 @@ __device__ __forceinline__ float2 unpack_i16(uint32_t w) {
 }
 
 // ------------------------------------------------------------------ softmax pieces
-// Probabilities carry a factor 16 against their reference and may grow by another 16 before
-// the reference moves: at most 2^8, under e4m3's 448.
-constexpr float kLift = 4.f, kLag = 4.f;
+// Probabilities carry a factor 2^11 against their reference and may grow by another 2^4 before
+// the reference moves: at most 2^15, under e5m2's 57344. Sums carry no factor.
+constexpr float kLift = 11.f, kLag = 4.f, kUnlift = 1.f / 2048.f;
 
 // the factors of four groups of 16 keys (64 columns)
 struct Groups {
@@ -226,21 +227,21 @@ __device__ __forceinline__ float chunk_max(const uint32_t (&v)[64], const Groups
   return top;
 }
 
-// prefix tile: 2^(y - ref + lift) as an e4m3 and an e5m2 part, four keys a word, at paddr and paddr + P2;
-// returns the sum weighted by 1 / V factor
+// prefix tile: 2^(y - ref + lift) as three e5m2 parts, four keys a word, at paddr, paddr + PART and
+// paddr + 2 PART; returns the sum weighted by 1 / V factor
 template <bool MASK>
 __device__ __forceinline__ float chunk_parts(const uint32_t (&v)[64], uint32_t paddr, const Groups& f, int hi, float ref) {
-  uint32_t p1[16], p2[16];
+  uint32_t p1[16], p2[16], p3[16];
   float total = 0.f;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    // fp16 bits of p * 2^-8 are, from bit 7 up, the bits of p's e4m3 number; those of a number
-    // itself are, from bit 8 up, its e5m2 number's
-    const float off = f.lv[q] - ref + (kLift - 8.f);
+    // fp16 bits are, from bit 8 up, those of the e5m2 number: half of bit 8 rounds, and what a part
+    // leaves is exact in fp16
+    const float off = f.lv[q] - ref + kLift;
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int c = 16 * q; c < 16 * q + 16; c += 4) {
-      uint32_t t1[2], t2[2];
+      uint32_t t1[2], t2[2], t3[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float x, y;
@@ -254,21 +255,23 @@ __device__ __forceinline__ float chunk_parts(const uint32_t (&v)[64], uint32_t p
         add2(s0, s1, x, y);
         uint32_t w, left;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
-        const uint32_t near = w + 0x00400040u;      // rounded to e4m3 above bit 7
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(left) : "r"(w), "r"(near & 0xff80ff80u));
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(left) : "r"(left), "r"(0x5c005c00u));    // 2^8
-        t1[h] = near + near;                        // the first part in each upper byte
-        t2[h] = left + 0x00800080u;                 // the rest, rounded to e5m2 in each upper byte
+        t1[h] = w + 0x00800080u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(left) : "r"(w), "r"(t1[h] & 0xff00ff00u));
+        t2[h] = left + 0x00800080u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(left) : "r"(left), "r"(t2[h] & 0xff00ff00u));
+        t3[h] = left + 0x00800080u;
       }
       p1[c / 4] = __byte_perm(t1[0], t1[1], 0x7531);
       p2[c / 4] = __byte_perm(t2[0], t2[1], 0x7531);
+      p3[c / 4] = __byte_perm(t3[0], t3[1], 0x7531);
     }
     const float s = s0 + s1;
     if (!MASK || 16 * q < hi) total = fmaf(s, f.w[q], total);
   }
   tmem_st16(paddr, p1);
-  tmem_st16(paddr + P2, p2);
-  return total * 256.f;
+  tmem_st16(paddr + PART, p2);
+  tmem_st16(paddr + 2 * PART, p3);
+  return total * kUnlift;
 }
 
 // own-block tile: 2^(y - ref + lift) as bf16 pairs over the columns [lo, hi); returns the sum
@@ -287,7 +290,7 @@ __device__ __forceinline__ float chunk_pairs(const uint32_t (&v)[64], uint32_t p
     s1 += __uint_as_float(w & 0xffff0000u);
   }
   tmem_st32(paddr, pk);
-  return s0 + s1;
+  return (s0 + s1) * kUnlift;
 }
 
 // the two warps of a lane quarter share its rows: barriers 1-4, 64 threads
@@ -747,7 +750,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     // ---------------------------------------------------------- O += P V (warp 7)
     if (lane == 0 && nT > 0) {
       // rows of codes are 128 bytes in the ring, zeros behind a shorter head's
-      constexpr uint32_t idPV = idesc_f8(false, true, 128), idPV2 = idesc_f8(true, true, 128), idPVb = idesc_bf16(true, DH);
+      constexpr uint32_t idPV = idesc_f8(true, true, 128), idPVb = idesc_bf16(true, DH);
       const uint64_t v0 = sw128_desc(sbase + OFF_V, kSlot, 1024);
       int u = 0;
       for (int j = 0; j < nT; ++j) {
@@ -772,7 +775,8 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 #pragma unroll
           for (int ks = 0; ks < BN / 32; ++ks) {
             mma_f8_ts(tmem + TM_O, pa + ks * 8, vd + ks * (32 * 128 / 16), idPV, (j > 0 || ks > 0) ? 1u : 0u);
-            mma_f8_ts(tmem + TM_O, pa + P2 + ks * 8, vd + ks * (32 * 128 / 16), idPV2, 1u);
+            mma_f8_ts(tmem + TM_O, pa + PART + ks * 8, vd + ks * (32 * 128 / 16), idPV, 1u);
+            mma_f8_ts(tmem + TM_O, pa + 2 * PART + ks * 8, vd + ks * (32 * 128 / 16), idPV, 1u);
           }
         }
         mma_commit(&bars.s_free[sb]);
@@ -822,7 +826,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         tmem_wait_ld();
         if (row >= rv || bars.failed) continue;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * kUnlift * inv);
         if (look) {
           // the own-block values that left the tile: an infinity or NaN, whatever its weight
           for (int t = slot / p.Dmax * p.Dmax; t <= slot; ++t) {
@@ -897,7 +901,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     const int k = (amax >= 0x1p-100f) ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127 : -1;
     const int ex = min(k, 125) + 1;
     const float scale = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
-    const float inv_scale = __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
+    const float inv_scale = __uint_as_float(static_cast<uint32_t>(127 - 14 - static_cast<int>(kLift) + ex) << 23);
     uint4* dst = reinterpret_cast<uint4*>(stage + row * kRowB + half * DH);
 #pragma unroll
     for (int u = 0; u < OC / 8; ++u) {
