@@ -5,7 +5,9 @@
 // log2 sv_j, the output is  sum_j 2^(y_j - M) c_j / sum_j 2^(y_j - M) / sv_j  for any M:
 // the values' scale rides in the exponent, so no element is multiplied by it, and the
 // denominator gets one multiplication by 1/sv for each group of keys of one block. M is
-// the running maximum of y, moved only when it grows by more than 2^8.
+// the running maximum of y, moved only when it grows by more than 2^8; the weights of the
+// output carry a factor 2^7 (at most 2^15 then), so that fp16 keeps the 11 bits of those down
+// to 2^-21 of the largest: the tail of a long prefix beside one large key.
 //
 // What bounds it: the cache's bytes, read once (2 dh bytes a key and kv head). A warp
 // takes two tiles of 16 keys a step and keeps its own running maximum, sum and output (online
@@ -22,7 +24,7 @@
 // V^T P^T it holds, for its four keys, the dh/8 output elements from dh/8 g on. K Q^T takes the
 // codes as they are (e4m3 products, fp32 sums) against q as a sum of two e4m3 numbers; for
 // V^T P^T they become fp16 exactly, by one conversion for two, against probabilities rounded
-// to fp16 (at most 2^8): 11 bits where two e4m3 numbers would hold 8, for few instructions
+// to fp16 (at most 2^15): 11 bits where two e4m3 numbers would hold 8, for few instructions
 // more. mma.sync is enough here: the matrix work is a fifth of the time the bytes take, and
 // eight rows are a sixteenth of the smallest tcgen05 tile.
 //
@@ -72,6 +74,7 @@ struct RowsConfig {
   static_assert(OFF_BARS % 16 == 0 && OFF_STAT % 16 == 0 && OFF_PEER_OUT % 16 == 0, "alignment");
 };
 constexpr unsigned long long kRowsWaitClocks = 1ull << 32;
+constexpr float kRowsLag = 8.f, kRowsLift = 7.f, kRowsUnlift = 1.f / 128.f;   // log2, log2; sums carry no factor
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -124,7 +127,8 @@ __device__ __forceinline__ float column_max(float v) {
 
 // Scores y (log2 units; -inf where masked) of keys g, g + 8 of U key tiles and rows 2t, 2t + 1
 // of every column tile: moves the running maxima m, returns the factors on what was summed before and
-// the references, and whether any lane of the warp needs the factors.
+// the references (with the factor 2^kRowsLift of the weights), and whether any lane of the warp needs
+// the factors.
 template <int N8, int U>
 __device__ __forceinline__ bool move_max(float (&m)[N8][2], const float (&y)[U][N8][4], float (&ref)[N8][2],
                                          float (&alpha)[N8][2]) {
@@ -138,12 +142,12 @@ __device__ __forceinline__ bool move_max(float (&m)[N8][2], const float (&y)[U][
       for (int u = 1; u < U; ++u) top = fmaxf(top, fmaxf(y[u][n][i], y[u][n][2 + i]));
       top = column_max(top);
       alpha[n][i] = 1.f;
-      if (top > m[n][i] + 8.f) {            // also the first keys: m is -inf
+      if (top > m[n][i] + kRowsLag) {            // also the first keys: m is -inf
         alpha[n][i] = ex2_approx(m[n][i] - top);
         m[n][i] = top;
         moved = true;
       }
-      ref[n][i] = m[n][i] == -INFINITY ? 0.f : m[n][i];
+      ref[n][i] = m[n][i] == -INFINITY ? 0.f : m[n][i] - kRowsLift;
     }
   return __any_sync(0xffffffffu, moved);
 }
@@ -427,8 +431,8 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float w0 = ex2_approx(y[n][2 * h] - ref[n][0]), w1 = ex2_approx(y[n][2 * h + 1] - ref[n][1]);
-          l[n][0] += w0;
-          l[n][1] += w1;
+          l[n][0] = fmaf(w0, kRowsUnlift, l[n][0]);
+          l[n][1] = fmaf(w1, kRowsUnlift, l[n][1]);
           const uint32_t x = tc::pack_bf16(w0, w1);
           hi[h] = transpose8(x);
           low[h] = transpose8(tc::pack_bf16(w0 - __uint_as_float(x << 16), w1 - __uint_as_float(x & 0xffff0000u)));
@@ -535,7 +539,7 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     if (move_max<N8, 2>(m, y, ref, alpha)) rescale(alpha);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const float inv_sv = ex2_approx(-lv[u]);
+      const float inv_sv = ex2_approx(-lv[u] - kRowsLift);     // and off with the factor
       uint32_t pb[N8][2];
 #pragma unroll
       for (int n = 0; n < N8; ++n) {
@@ -614,7 +618,7 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     if (*failed || !present[row]) return;
     const int64_t at = ((static_cast<int64_t>(b) * NT + tt) * p.Hq + kvh * G + rr % G) * DH + e % (DH / 4) * 4;
     const float inv = __frcp_rn(L);
-    v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    v = make_float4(v.x * kRowsUnlift * inv, v.y * kRowsUnlift * inv, v.z * kRowsUnlift * inv, v.w * kRowsUnlift * inv);
     if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;
     else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(tc::pack_bf16(v.x, v.y), tc::pack_bf16(v.z, v.w));
   };

@@ -98,3 +98,15 @@ def test_a_value_block_of_a_large_scale_of_many_rows(dh):
         v[64:, :, 0] = 2.0 ** (11 + b % 6)
         case.write(b, k, v)
     case.compare(H.run(case), {(b, (7 * b) % 20) for b in range(B)})
+
+
+def test_a_long_tail_beside_one_large_key_of_few_rows():
+    """So many sequences, most of them empty, that one CTA of three warps takes a whole prefix."""
+    P, B, more = 65536, 12, 60000
+    case = Tail(P, 1, 1, 64, 128, 15 + 3.5 * np.arange(B) / B, 0.0)
+    empty = lambda x: np.concatenate([x, np.zeros((more,) + x.shape[1:], x.dtype)])
+    case.q, case.kc, case.vc, case.table, case.prefix = map(empty, (case.q, case.kc, case.vc, case.table, case.prefix))
+    case.q64, case.kc64, case.vc64 = map(empty, (case.q64, case.kc64, case.vc64))
+    case.blk_len = np.ones((B + more, 1), np.int32)
+    assert not case.many(1)
+    case.compare(H.run(case), {(b, 0) for b in range(B)})
