@@ -538,11 +538,16 @@ int ssd_commit_kv_quant(const ssd_commit_quant_args* a, void* ws, size_t ws_byte
  * Scales are finite and in [0, 2^20]; a v_scale below 2^-100 counts as 2^-100. Codes and
  * scales past prefix_len are never used (they may hold anything); blocks need no scale
  * before their first token.
- * Scores, maxima and sums are fp32, products exact in fp32; the probabilities are rounded
- * to 11 bits (fp16), or over many rows to the sum of an e4m3 and an e5m2 number (about 8
- * bits), before they weight the values, the candidates' to bf16 or better. Over many rows
- * the CTAs that share a row merge its output as 16-bit integers, 2^-14 of the largest of 64
- * elements. Results do not depend on the order of execution: a call repeats bit for bit.
+ * Scores, maxima and sums are fp32, products of the rounded operands exact in fp32. An element
+ * of q is off by at most 2^-17 of its row's largest (q is split into two e4m3 numbers). The
+ * probabilities are rounded before they weight the values: over few rows to 11 bits (fp16) down
+ * to 2^-21 of the largest p_j * v_scale_j, over many to the sum of three e5m2 numbers (2^-9
+ * relative) down to 2^-19; smaller ones are off by up to 2^-32 or 2^-28 of the largest. The
+ * candidates' probabilities are bf16 numbers or better; a candidate's v_scale is the one that
+ * its value row alone would have, so values of any size may meet (the largest finite ones do not
+ * overflow). Over many rows the CTAs that share a row merge its output as 16-bit integers,
+ * 2^-14 of the largest of dh / 2 elements, so an fp32 output, too, holds about three digits.
+ * Results do not depend on the order of execution: a call repeats bit for bit.
  * Supported: dh 64 or 128; Hq % Hkv == 0, Hq / Hkv <= 64; 1 <= Dmax <= 256,
  * NB * Dmax <= 8192; scale_block 16, 32, 64 or 128; 16-byte aligned tensors;
  * num_pages * 128 * Hkv < 2^31 (B * Hkv * P_max < 2^31); else SSD_ERR_UNSUPPORTED.

@@ -404,6 +404,37 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           mma_b16(c[n], a[0].x, a[1].x, a[0].y, a[1].y, v.x, v.y);
         }
       }
+      // scales of keys g and g + 8, from the largest finite magnitudes of their rows: each lane's own
+      // 16 bits a key, two keys a word, then over the eight lanes of a key
+      uint32_t top[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t most[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t x = 0;
+#pragma unroll
+          for (int u = 0; u < EV / 2; ++u) x = max_u16x2(x, v[2 * h + k][u] & 0x7fff7fffu);
+          most[k] = max(x & 0xffffu, x >> 16);
+          if (most[k] >= 0x7f80u) {
+            odd_value = true;
+            most[k] = 0;
+#pragma unroll
+            for (int u = 0; u < EV / 2; ++u) {
+              const uint32_t a = v[2 * h + k][u] & 0x7fffu, b = v[2 * h + k][u] >> 16 & 0x7fffu;
+              most[k] = max(most[k], max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+            }
+          }
+        }
+        top[h] = most[0] | most[1] << 16;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) top[h] = max_u16x2(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
+      }
+      odd_value = __any_sync(0xffffffffu, odd_value);
+      float own_lv[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        own_lv[h] = own_scale_log2(__shfl_sync(0xffffffffu, top[h], g >> 1) >> ((g & 1) * 16) & 0xffffu);
       float yy[1][N8][4], ref[N8][2], alpha[N8][2];
       float (&y)[N8][4] = yy[0];
 #pragma unroll
@@ -411,26 +442,16 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int slot = slot0 + (e >> 1) * 8 + g;
-          y[n][e] = slot >= lo[n][e & 1] && slot <= tr[n][e & 1] ? fmaf(c[n][e], p.scale_log2, -kOwnLowered) : -INFINITY;
+          c[n][e] = slot >= lo[n][e & 1] && slot <= tr[n][e & 1] ? c[n][e] * p.scale_log2 : -INFINITY;
+          y[n][e] = c[n][e] + own_lv[e >> 1];
         }
       if (move_max<N8, 1>(m, yy, ref, alpha)) rescale(alpha);
-#pragma unroll
-      for (int n = 0; n < N8; ++n) {
-        ref[n][0] -= kOwnLowered;
-        ref[n][1] -= kOwnLowered;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int u = 0; u < EV / 2; ++u)
-          odd_value |= (v[k][u] & 0x7f800000u) == 0x7f800000u || (v[k][u] & 0x7f80u) == 0x7f80u;
-      odd_value = __any_sync(0xffffffffu, odd_value);
 #pragma unroll
       for (int n = 0; n < N8; ++n) {
         uint32_t hi[2], low[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float w0 = ex2_approx(y[n][2 * h] - ref[n][0]), w1 = ex2_approx(y[n][2 * h + 1] - ref[n][1]);
+          const float w0 = ex2_approx(c[n][2 * h] - ref[n][0]), w1 = ex2_approx(c[n][2 * h + 1] - ref[n][1]);
           l[n][0] = fmaf(w0, kRowsUnlift, l[n][0]);
           l[n][1] = fmaf(w1, kRowsUnlift, l[n][1]);
           const uint32_t x = tc::pack_bf16(w0, w1);
@@ -454,9 +475,9 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             const int from = (k & 7) * 4 + t4;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float yk = __shfl_sync(0xffffffffu, k < 8 ? y[n][i] : y[n][2 + i], from);
+              const float ck = __shfl_sync(0xffffffffu, k < 8 ? c[n][i] : c[n][2 + i], from);
               if (slot0 + k < lo[n][i] || slot0 + k > tr[n][i]) continue;
-              const float w = ex2_approx(yk - ref[n][i]);
+              const float w = ex2_approx(ck - ref[n][i]);
 #pragma unroll
               for (int j = 0; j < KS; ++j)
 #pragma unroll

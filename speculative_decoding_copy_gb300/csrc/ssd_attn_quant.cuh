@@ -33,10 +33,15 @@ struct AttnQuantParams {
 constexpr float kLeastVScaleLog2 = -100.f;     // a smaller v scale counts as this
 
 // Own-block keys have no value scale in the exponent, so beside prefix keys of the same score
-// they look 1 / sv times as heavy, and a reference maximum set by one would push the prefix's
-// probabilities, which have 8 or 16 bits, to the low end of their range. They enter the maximum
-// lowered by this (log2); their own probabilities, bf16 numbers, may then pass the reference.
-constexpr float kOwnLowered = 16.f;
+// they would look 1 / sv times as heavy, and a reference maximum set by one would push the prefix's
+// probabilities, which have 8 or 16 bits, to the low end of their range. Each enters the maximum with
+// the scale that a cache block of its value row alone would have, so that the reference is the
+// largest contribution to the output whatever the values' size; its own probability, a bf16
+// number or two, has the range for the rest. The log2 of that scale, from the largest finite
+// magnitude of the row as bf16 bits; the bounds keep weights, sums and outputs in fp32's range.
+__device__ __forceinline__ float own_scale_log2(uint32_t top) {
+  return static_cast<float>(min(max(static_cast<int>(top >> 7) - 127 - 8, -100), 60));
+}
 
 // tensor-core path for many rows (ssd_attn_quant_tc.cu)
 bool attn_quant_tc_applies(const AttnQuantParams& p);

@@ -83,7 +83,7 @@ constexpr uint32_t OFF_QB = 2 * kSlot;    // bf16, two 64-column halves
 constexpr uint32_t OFF_K = 4 * kSlot;
 constexpr uint32_t OFF_V = OFF_K + SLOTS * kSlot;
 constexpr uint32_t OFF_BAR = OFF_V + SLOTS * kSlot;
-constexpr uint32_t kBarBytes = 4096;
+constexpr uint32_t kBarBytes = 5120;
 constexpr uint32_t kSmemBytes = OFF_BAR + kBarBytes + 1024;   // + slack to align the base to 1024
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr unsigned long long kWaitClocks = 1ull << 32;
@@ -116,6 +116,7 @@ struct Bars {
   int row_slot[BM];                       // candidate slot of a row of this tile
   int row_at[BM];                         // its place in the sequence's Q and output, in rows of DH
   float pair[2][BM];                      // a value of each half of a row
+  alignas(16) float own_lv[2][BN];                    // log2 of the scales of an own-block tile's value rows, in turns
   // of a prefix tile's eight groups of 16 keys: K factor, log2 of the V factor, 1 / V factor
   float4 factors[FACTORS][3][2];
 };
@@ -205,9 +206,23 @@ __device__ __forceinline__ void add2(float& x, float& y, float a0, float a1) {
       : "+f"(x), "+f"(y) : "f"(a0), "f"(a1));
 }
 
-// largest y of the columns [lo, hi) of 64 (MASK), or of all
+// own-block tile: largest y of the columns [lo, hi) of 64, whose keys have a scale each
+__device__ __forceinline__ float own_max(const uint32_t (&v)[64], float k, const float* lv, int lo, int hi) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 64; c += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(lv + c);
+    const float l[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e >= lo && c + e < hi) top = fmaxf(top, fmaf(__uint_as_float(v[c + e]), k, l[e]));
+  }
+  return top;
+}
+
+// largest y of the columns below hi of 64 (MASK), or of all
 template <bool MASK>
-__device__ __forceinline__ float chunk_max(const uint32_t (&v)[64], const Groups& f, int lo, int hi) {
+__device__ __forceinline__ float chunk_max(const uint32_t (&v)[64], const Groups& f, int hi) {
   float top = -INFINITY;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -217,7 +232,7 @@ __device__ __forceinline__ float chunk_max(const uint32_t (&v)[64], const Groups
       float x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        x[e] = !MASK || (c + e >= lo && c + e < hi) ? __uint_as_float(v[c + e]) : -INFINITY;
+        x[e] = !MASK || c + e < hi ? __uint_as_float(v[c + e]) : -INFINITY;
       a = max3(a, x[0], x[1]);
       b = max3(b, x[2], x[3]);
     }
@@ -546,12 +561,17 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     bool odd = false;
     for (int j = 0; j < nC; ++j) {
       // slots of other blocks and of absent tokens may hold anything, and 0 * inf is not 0:
-      // values that are not finite leave the tile, and the rows that see one get it at the end
+      // values that are not finite leave the tile, and the rows that see one get it at the end. Eight
+      // lanes read a value row; their largest magnitude is its scale.
+      constexpr int kReads = BN * 8 / kSoftmax;
+      uint32_t tops[kReads] = {};
       for (int h = 0; h < UO; ++h) {
         const int u = UO * j + h;
-        if (!mbar_wait(bars, &bars.full_v[u % SLOTS], (u / SLOTS) & 1, p.hdr, 473)) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(bars, &bars.full_v[u % SLOTS], (u / SLOTS) & 1, p.hdr, 473))) break;
         uint4* vt = reinterpret_cast<uint4*>(smem + OFF_V + (u % SLOTS) * kSlot);
-        for (int i = half * BM + row; i < BN * 8; i += kSoftmax) {
+#pragma unroll
+        for (int n = 0; n < kReads; ++n) {
+          const int i = half * BM + row + n * kSoftmax;
           uint4 x = vt[i];
           uint32_t* w = reinterpret_cast<uint32_t*>(&x);
           bool bad = false;
@@ -570,7 +590,16 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
             vt[i] = x;
             odd = true;
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) tops[n] = max_u16x2(tops[n], w[e] & 0x7fff7fffu);
         }
+      }
+#pragma unroll
+      for (int n = 0; n < kReads; ++n) {
+        uint32_t top = max(tops[n] & 0xffffu, tops[n] >> 16);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if ((lane & 7) == 0) bars.own_lv[j & 1][(half * BM + row + n * kSoftmax) >> 3] = own_scale_log2(top);
       }
       if (odd) *reinterpret_cast<volatile int*>(&bars.odd_own) = 1;
       fence_async_smem();
@@ -583,13 +612,11 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       load64(sp + half * 64, v);
       const int s0 = s_base + j * BN + half * 64;
       const int lo = row_ok ? c_lo - s0 : BN, hi = row_ok ? slot + 1 - s0 : 0;
-      Groups f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f.k[q] = p.scale_log2;
-        f.lv[q] = -kOwnLowered;
-      }
-      const float mx = chunk_max<true>(v, f, lo, hi);
+      // every softmax thread's scales are there (they are written again two tiles on, behind the next
+      // tile's barrier)
+      __syncwarp();
+      asm volatile("barrier.cta.sync.aligned 5, %0;" ::"n"(kSoftmax) : "memory");
+      const float mx = own_max(v, p.scale_log2, bars.own_lv[j & 1] + half * 64, lo, hi);
       if (any_row(mx > m + kLag, warp & 3)) move_refs(j, mx);
       l += chunk_pairs(v, sp + half * 32, p.scale_log2, lo, hi, m == -INFINITY ? 0.f : m);
       tmem_wait_st();
@@ -610,7 +637,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       load64(sp + half * 64, v);
       const int hi = P - t * BN - half * 64;
       const bool full = P - t * BN >= BN;
-      const float mx = full ? chunk_max<false>(v, f, 0, 0) : chunk_max<true>(v, f, 0, hi);
+      const float mx = full ? chunk_max<false>(v, f, 0) : chunk_max<true>(v, f, hi);
       if (any_row(mx > m + kLag, warp & 3)) move_refs(j, mx);
       const float ref = m == -INFINITY ? 0.f : m;
       l += full ? chunk_parts<false>(v, sp + half * 16, f, 0, ref) : chunk_parts<true>(v, sp + half * 16, f, hi, ref);

@@ -49,12 +49,6 @@ __device__ __forceinline__ float exact_reciprocal(float s) {
   return (u & 0x7fffffu) == 0 && e >= 1 && e <= 253 ? __uint_as_float((254 - e) << 23) : 0.f;
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // off the common path: its code is kept out of the loops
 __device__ __noinline__ float divide(float x, float s) { return __fdiv_rn(x, s); }
 

@@ -37,6 +37,12 @@ __device__ __forceinline__ void e4m3x2_to_f32(uint32_t codes, float& lo, float& 
       : "=f"(lo), "=f"(hi) : "r"(f));
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // bytes [p, p + n) that a call reads or writes
 struct Span {
   const void* p;
