@@ -250,6 +250,7 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   // land swizzled) and four lanes' scales (an empty group past the end)
   auto page_of = [&](int s) -> int32_t {                // page of a step
     if (p.block_table == nullptr || s >= step1) return b;
+    if (!in_range(s / (kPageTokens / kStepKeys), p.pages_per_seq, p.hdr, 445)) return 0;
     return p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + s / (kPageTokens / kStepKeys)];
   };
   uint8_t* my = smem + warp * C::kWarpRing;
@@ -272,7 +273,8 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       }
       const int blocks = static_cast<int>(p.blocks);
       const int blk = min((place + (lane & 1) * kTileKeys) >> p.sb_log2, blocks - 1);
-      copy_async4(tc::smem_u32(scales + warp * ST + stage) + lane * 4,
+      if (in_range(static_cast<int64_t>(ph) * blocks + blk, p.num_pages * p.Hkv * blocks, p.hdr, 446))
+        copy_async4(tc::smem_u32(scales + warp * ST + stage) + lane * 4,
                   (lane < 2 ? p.k_scale : p.v_scale) + static_cast<int64_t>(ph) * blocks + blk);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -638,6 +640,7 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     const int row = e / (DH / 4), rr = r0 + row, tt = rr / G;
     if (*failed || !present[row]) return;
     const int64_t at = ((static_cast<int64_t>(b) * NT + tt) * p.Hq + kvh * G + rr % G) * DH + e % (DH / 4) * 4;
+    if (!in_range(at + 3, static_cast<int64_t>(p.B) * NT * p.Hq * DH, p.hdr, 447)) return;
     const float inv = __frcp_rn(L);
     v = make_float4(v.x * kRowsUnlift * inv, v.y * kRowsUnlift * inv, v.z * kRowsUnlift * inv, v.w * kRowsUnlift * inv);
     if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;

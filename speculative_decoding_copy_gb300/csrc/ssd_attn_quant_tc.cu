@@ -429,7 +429,8 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       const int mid = (lo + hi) >> 1;
       if (ends[mid] > i) hi = mid; else lo = mid + 1;
     }
-    const int slot = lo * p.Dmax + i - (lo > 0 ? ends[lo - 1] : 0);
+    const int found = lo * p.Dmax + i - (lo > 0 ? ends[lo - 1] : 0);
+    const int slot = in_range(found, NT, p.hdr, 454) ? found : 0;
     bars.row_slot[tid] = slot;
     bars.row_at[tid] = slot * p.Hq + kvh * G + (r0 + min(tid, rv - 1)) % G;
   }
@@ -681,6 +682,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     }
     auto load_page = [&](int t) -> int {
       if (t >= j1 || p.block_table == nullptr) return b;
+      if (!in_range(t, p.pages_per_seq, p.hdr, 452)) return 0;
       const int pg = p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + t];
       if (pg >= 0 && pg < p.num_pages) return pg;
       if (lane == 0) record_error(p.hdr, SSD_ERR_DEVICE, 451);
@@ -691,6 +693,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       if (!kside || t >= j1 || lane >= 16) return 0.f;
       const int place = (p.block_table == nullptr ? t * BN : 0) + (lane & 7) * 16;
       const int blk = min(place >> p.sb_log2, blocks - 1);
+      if (!in_range(static_cast<int64_t>(pg * p.Hkv + kvh) * blocks + blk, p.num_pages * p.Hkv * blocks, p.hdr, 453)) return 0.f;
       return (lane < 8 ? p.k_scale : p.v_scale)[static_cast<int64_t>(pg * p.Hkv + kvh) * blocks + blk];
     };
     int page = load_page(j0), page1 = load_page(j0 + 1), page2 = load_page(j0 + 2);
@@ -852,6 +855,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         tmem_ld32(tmem + TM_O + lane_off + half * OC + q * 32, o);
         tmem_wait_ld();
         if (row >= rv || bars.failed) continue;
+        if (!in_range(at + q * 32 + 31, static_cast<int64_t>(p.B) * NT * p.Hq * DH, p.hdr, 455)) continue;
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * kUnlift * inv);
         if (look) {
@@ -1024,6 +1028,7 @@ k_attn_quant_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       }
     }
     const int64_t at = (static_cast<int64_t>(b) * NT * p.Hq + bars.row_at[rb + i]) * DH + cg * 16;
+    if (!in_range(at + 15, static_cast<int64_t>(p.B) * NT * p.Hq * DH, p.hdr, 456)) continue;
     if (p.out_f32) {
       float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
 #pragma unroll

@@ -275,6 +275,9 @@ k_append_quant(ssd_append_quant_args a, int range, WsHeader* hdr) {
                 (ph * a.page_tokens + (static_cast<int64_t>(blk) << sb_log2)) * a.dh;
       d.scale = (is_v ? a.v_scale : a.k_scale) + ph * blocks + blk;
       d.row = off & (sb - 1);
+      if (!in_range(page, a.num_pages, hdr, 421) || !in_range(off + last - first - 1, a.page_tokens, hdr, 422) ||
+          !in_range(d.row + last - first - 1, sb, hdr, 423) || !in_range(t0 + last - 1, a.T, hdr, 424))
+        continue;
       quant_run<T, W>(src + (t0 + first) * stride, stride, last - first, a.dh, d, grp);
     }
   }
@@ -327,6 +330,10 @@ k_commit_quant(ssd_commit_quant_args a, int64_t page_tokens, int segs, WsHeader*
   d.row = static_cast<int>(place) & ((1 << sb_log2) - 1);
   const int64_t src_row = static_cast<int64_t>(b) * a.NB * a.Dmax + static_cast<int64_t>(k) * a.Dmax + (p0 - P);
   const int64_t stride = static_cast<int64_t>(a.Hkv) * a.dh;
+  if (!in_range(page, a.block_table != nullptr ? a.num_pages : a.B, hdr, 431) ||
+      !in_range(place + p1 - p0 - 1, page_tokens, hdr, 432) || !in_range(d.row + p1 - p0 - 1, 1 << sb_log2, hdr, 433) ||
+      !in_range(src_row + p1 - p0 - 1, static_cast<int64_t>(a.B) * a.NB * a.Dmax, hdr, 434))
+    return;
   quant_run<T, W>(static_cast<const T*>(is_v ? a.v_cand : a.k_cand) + src_row * stride + static_cast<int64_t>(h) * a.dh,
                stride, static_cast<int>(p1 - p0), a.dh, d, grp);
 }

@@ -94,6 +94,7 @@ __device__ __forceinline__ void fill_four(const ssd_pages_args& a, const int32_t
       }
       if (!served) continue;
       const int64_t pos = begin + t + e;
+      if (!in_range(pos / kPageTokens, a.pages_per_seq, hdr, 411)) continue;
       const int32_t page = table[pos / kPageTokens];
       if (page < 0 || page >= a.num_pages) record_error(hdr, SSD_ERR_DEVICE, 410);
       else out[e] = page * kPageTokens + static_cast<int32_t>(pos % kPageTokens);
@@ -147,6 +148,8 @@ k_page_plan(ssd_pages_args a, int fill_slots, WsHeader* hdr) {
           const int64_t q = q0 + u * kPlanThreads;
           if (q < total) {
             const int i = last_not_above(off, kPlanThreads, static_cast<int32_t>(q));
+            entry[u] = nullptr;
+            if (!in_range(b0 + i, a.B, hdr, 405) || !in_range(base[i] + (q - off[i]), a.pages_per_seq, hdr, 405)) continue;
             entry[u] = a.block_table + static_cast<int64_t>(b0 + i) * a.pages_per_seq + base[i] + (q - off[i]);
             page[u] = *entry[u];
           }
@@ -154,7 +157,7 @@ k_page_plan(ssd_pages_args a, int fill_slots, WsHeader* hdr) {
 #pragma unroll
         for (int u = 0; u < kMoves; ++u) {
           const int64_t q = q0 + u * kPlanThreads;
-          if (q < total) {
+          if (q < total && (!SSD_CHECKS || entry[u] != nullptr)) {
             if (avail + q < a.num_pages) a.free_pages[avail + q] = page[u];
             else record_error(hdr, SSD_ERR_DEVICE, 402);
             *entry[u] = -1;
@@ -205,14 +208,17 @@ k_page_plan(ssd_pages_args a, int fill_slots, WsHeader* hdr) {
         for (int u = 0; u < kMoves; ++u) {
           const int64_t q = q0 + u * kPlanThreads;
           if (q < take) {
+            entry[u] = nullptr;
+            if (!in_range(avail - 1 - (lacked + q), a.num_pages, hdr, 406)) continue;
             page[u] = a.free_pages[avail - 1 - (lacked + q)];
             const int i = last_not_above(off, kPlanThreads, static_cast<int32_t>(q));
+            if (!in_range(b0 + i, a.B, hdr, 407) || !in_range(base[i] + (q - off[i]), a.pages_per_seq, hdr, 407)) continue;
             entry[u] = a.block_table + static_cast<int64_t>(b0 + i) * a.pages_per_seq + base[i] + (q - off[i]);
           }
         }
 #pragma unroll
         for (int u = 0; u < kMoves; ++u) {
-          if (q0 + u * kPlanThreads < take) {
+          if (q0 + u * kPlanThreads < take && (!SSD_CHECKS || entry[u] != nullptr)) {
             if (page[u] < 0 || page[u] >= a.num_pages) record_error(hdr, SSD_ERR_DEVICE, 403);
             *entry[u] = page[u];
           }
