@@ -540,9 +540,9 @@ int ssd_commit_kv_quant(const ssd_commit_quant_args* a, void* ws, size_t ws_byte
  * before their first token.
  * Scores, maxima and sums are fp32, products of the rounded operands exact in fp32. An element
  * of q is off by at most 2^-17 of its row's largest (q is split into two e4m3 numbers). The
- * probabilities are rounded before they weight the values: over few rows to 11 bits (fp16) down
- * to 2^-21 of the largest p_j * v_scale_j, over many to the sum of three e5m2 numbers (2^-9
- * relative) down to 2^-19; smaller ones are off by up to 2^-32 or 2^-28 of the largest. The
+ * probabilities are rounded to 11 bits (fp16) before they weight the values, down to 2^-21 of the
+ * largest p_j * v_scale_j over few rows and to 2^-17 over many (where three e5m2 numbers hold
+ * them); smaller ones are off by up to 2^-32 or 2^-28 of the largest. The
  * candidates' probabilities are bf16 numbers or better; a candidate's v_scale is the one that
  * its value row alone would have, so values of any size may meet (the largest finite ones do not
  * overflow). Over many rows the CTAs that share a row merge its output as 16-bit integers,

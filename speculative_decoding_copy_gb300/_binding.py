@@ -648,7 +648,8 @@ def ssd_verify_attn_quant(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand,
                           scale_block=128, *, out=None, ws=None, scale=0.0, stream=None, out_f32=False,
                           block_table=None):
     """Block-triangular verification attention over the 8-bit cache (one block of one token:
-    decoding); returns the output [B][NT][Hq][dh], bf16 or with out_f32 fp32. The cache is
+    decoding); returns the output [B][NT][Hq][dh], bf16 or with out_f32 fp32 (of which about three
+    digits hold: weights of 11 bits, and over many rows a merge of 16-bit integers). The cache is
     contiguous [B][Hkv][P_max][dh], or with block_table [B][pages_per_seq] pages of 128 tokens."""
     _need(q, "q", _HALF, 4)
     dev = q.device

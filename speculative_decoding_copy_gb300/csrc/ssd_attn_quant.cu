@@ -28,8 +28,8 @@
 // more. mma.sync is enough here: the matrix work is a fifth of the time the bytes take, and
 // eight rows are a sixteenth of the smallest tcgen05 tile.
 //
-// Measured: 64 sequences of 2k-8k keys, 8 kv heads, one token each (672 MB): 106.5 us, 6.3 TB/s,
-// 0.93 of a plain copy. One sequence of 4096 keys (8.4 MB): 8.7 us replayed from a graph, of which
+// Measured: 64 sequences of 2k-8k keys, 8 kv heads, one token each (672 MB): 105.4 us, 6.4 TB/s,
+// 0.94 of a plain copy. One sequence of 4096 keys (8.4 MB): 8.7 us replayed from a graph, of which
 // 1.2 are its bytes; launch, first loads, the own-block key and two merges are the rest.
 //
 // The CTAs of a cluster split the steps of a (sequence, kv head) evenly by its own length;
@@ -288,8 +288,8 @@ k_attn_quant_rows(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 
   // ---- Q: lane (g, t) holds row g of every column tile. A power of two per row brings its
   // largest magnitude into [128, 256), and each element becomes the sum of two e4m3 numbers:
-  // four significant bits and the four that a bf16 number has left, so exact down to 2^-13
-  // of the row's largest and within 2^-18 of it below.
+  // four significant bits and the four that a bf16 number has left, so exact down to 2^-9
+  // of the row's largest and within 2^-17 of it below (half of e4m3's least step, 2^-10 of 128).
   uint32_t q[N8][KS / 4 * 2][4];                     // [8-byte group][words: first part, second part]
   float q_mul[N8][2];
 #pragma unroll
@@ -861,7 +861,7 @@ static int rows_choose(const AttnQuantParams& p, int rows, cudaStream_t s) {
   // keep it reading while one starts or ends (64 sequences of 2k-8k: 107 us; three of four
   // warps 119, six of two 120, one of eight 123). Sixteen rows need the registers of eight
   // warps an SM: two CTAs of four (32 sequences of 1000 keys 31.9 us, one of eight 44.6; 64 of
-  // 2k-8k 181 by both).
+  // 2k-8k now 163).
   using Few = RowsConfig<DH, N8, 8, 3, 1>;
   using Many = std::conditional_t<N8 == 1, RowsConfig<DH, N8, 3, 2, 4>, RowsConfig<DH, N8, 4, 2, 2>>;
   const long long groups = static_cast<long long>(p.B) * p.Hkv * ((rows + 8 * N8 - 1) / (8 * N8));
@@ -910,10 +910,10 @@ extern "C" int ssd_verify_attn_quant(const ssd_attn_quant_args* a, void* ws, siz
   KernelTimer timer(SSD_KERNEL_VERIFY_ATTN, s);
   // Beyond 16 rows this kernel reads the cache once for each 16; the tensor-core kernel costs the
   // same up to 128 but starts and merges more slowly. So this one up to 48 rows while its CTAs run
-  // at once and have little to read. Replayed from a graph, us by this and by the other: 20 rows of
-  // 4 sequences of 1024 keys, 8 kv heads, 19.7 and 21.6 (head dim 64: 17.2 and 18.3), one of 4096
-  // with 2 kv heads 17.6 and 21.4 (15.2 and 19.5); past the limits, 16 sequences of 500 30.2
-  // and 21.6 (23.7 and 19.6), 4 of 16384 83 and 55 (60 and 51), 48 rows of 8192 46 and 26 (35 and 24).
+  // at once and have little to read. Replayed from a graph, cold, us by this and by the other: 20 rows of
+  // 4 sequences of 1024 keys, 8 kv heads, 19.6 and 21.6 (head dim 64: 15.5 and 19.6), one of 4096
+  // with 2 kv heads 17.5 and 23.7 (15.5 and 19.6); at or past the limits, 16 sequences of 500 21.6
+  // and 21.6 (17.5 and 19.6), 4 of 16384 71 and 54 (52 and 50), 48 rows of 8192 28 and 26 (22 and 24).
   const long long groups = static_cast<long long>(p.B) * p.Hkv * ((rows + 15) / 16);
   const bool small = rows <= 16 || (rows <= 48 && groups <= 152 && groups * p.capacity <= (1 << 17));
   if (!small && attn_quant_tc_applies(p)) return attn_quant_tc_launch(p, a->dh, s);

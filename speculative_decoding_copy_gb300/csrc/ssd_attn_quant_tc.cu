@@ -4,15 +4,15 @@
 // Precision on 8-bit operands. The codes go into the products as they lie in the cache
 // (kind::f8f6f4, fp32 sums). Q and P, which have more bits, are sums of two and three 8-bit numbers, one
 // product each into the same accumulator. q (8 significant bits) is two e4m3 numbers, exact but
-// for what lies under 2^-17 of its row's largest element. A probability is the sum of three e5m2
-// numbers, each the rest of the ones before (2^-9 together, a bf16 number's rounding), for which
-// e5m2's range lets the largest lie at 2^11 to 2^15: a probability of 2^-19 of the largest still has
-// its 9 bits, and smaller ones are off by at most 2^-28 of it. A long prefix needs that: beside one key
-// of a large weight (or a block of a large value scale) its tail is 2^-15 each and most of the mass
-// together. With an e4m3 and an e5m2 number, 8 bits down to 2^-10 and three at 2^-15, such a
-// tail of 32768 keys was 1.3% off. The third product costs 256 of a tile's 1600 clocks of products; no code is converted.
-// (Converting each tile to fp16 in shared memory would move 64 KB more per tile through it,
-// which the products already keep three quarters busy.)
+// for what lies under 2^-17 of its row's largest element. A probability, rounded to fp16, is the sum
+// of three e5m2 numbers, each the rest of the ones before: three times three bits and two signs,
+// exact. e5m2's range lets the largest lie at 2^11 to 2^15, so that all 11 bits are there down to 2^-17
+// of the largest, nine at 2^-19, and smaller ones are off by at most 2^-28 of it. A long prefix needs
+// that: beside one key of a large weight (or a block of a large value scale) its tail is 2^-15 each and
+// most of the mass together. With an e4m3 and an e5m2 number, 8 bits down to 2^-10 and three at 2^-15,
+// such a tail of 32768 keys was 1.3% off; the third product takes 2% more time in a single call, 8% in
+// a loop that the GPU's power limits (4 sequences of 32768 keys), 6% in the serving batch. No code is converted.
+// (Converting each tile to fp16 in shared memory would move 64 KB more per tile through it.)
 //
 // Rows. The G query heads of the present tokens pack into rows (absent tokens take none, so a
 // batch with few present candidates runs few row tiles); a CTA owns 128 of them and one share
@@ -37,21 +37,23 @@
 //   warp 7     issues O += P V (two issuing threads, so that neither's waits hold the other back).
 // Head dim 64: the same layouts, with zeros behind a row's 64 codes (filled in by the tensor copies),
 // half the products of S and half of O's columns kept: 320 rows of one sequence of 4096 keys 23.7 us
-// where the kernel for few rows takes 56.4, of 32 of 2048 157 and 552.
+// where the kernel for few rows takes 48.3, of 32 of 2048 161 and 446.
 // Shared memory: Q (64 KB), then four 16 KB slots each for K and V. A prefix tile takes one
 // slot of each, an own-block tile (bf16) two.
 // TMEM columns: S buffers 0-127, 128-255, 256-383, O 384-511.
 // The merge is that of ssd_attn_tc.cu: rows as 16-bit integers with a power-of-two scale per
-// 64 columns, one bulk copy to each CTA that owns rows.
+// DH / 2 columns, one bulk copy to each CTA that owns rows.
 //
-// What bounds it, and what it measured: per 128 x 128 tile the products take 1340 clocks and the
-// whole loop 2050 (2300 with every SM busy): issue slots are 54% used, the tensor pipe 57%, and no
-// more warps (four threads a row: 470 us where this takes 464), no turns of two softmax groups
-// on alternate tiles (509), no second accumulator for them (570) and no single thread a row (624)
-// makes it shorter. Four sequences of 32768 keys and 800 rows: 458 us, 0.94 PFLOP/s counted as
-// bf16, at 1375 of the GPU's 1400 W: there even the loop without its maximum takes as long. 32
-// sequences of 1k-16k: 263 us. One of 4096 keys, 320 rows: 19 us, of which the loop is 8.5; Q's
-// conversion, the own-block tile and the merge are the rest.
+// What bounds it, and what it measured: a 128 x 128 tile takes 2020 to 2270 clocks on 8 to 64 SMs and
+// 2300 on all, where its 20 instructions of products need 1280 at the tensor pipe's best: the
+// softmax beside them. (With two products of P V, 16 instructions, it was 2050 and 2300. Measured
+// then, four sequences of 32768 keys, us: four threads a row 470 where this took 464, turns of
+// two softmax groups on alternate tiles 509, a second accumulator for them 570, a single thread a
+// row 624.) Four sequences of 32768 keys and 800 rows: 468 us for a single call, 490-500 in a loop
+// (0.87 PFLOP/s counted as bf16), where all SMs busy for long take the GPU to its power limit: a loop of
+// 152 CTAs drew 1355 W with the power cap active and the clock at 1762 of 2070 MHz, on 64 SMs 805 W at
+// 2070. 32 sequences of 1k-16k, nine blocks of 16, some absent: 285-329 us between draws. One of 4096
+// keys, 320 rows: 21 us, Q's conversion, an own-block tile, seven tiles and the merge in a row.
 // Waits are bounded; on expiry the CTA records SSD_ERR_TIMEOUT, skips what is left, gives its own
 // copies and products in flight as long again, and exits through the cluster barriers.
 #include <cuda.h>
@@ -1110,10 +1112,11 @@ static int resident(int S) {
 // share of the longest prefix's tiles and the time of 14 for its start and merge. The host knows
 // only the capacity: where prefixes are equal waves count in full, where they vary (the longest
 // started first) by the work, so the mean of both is taken. us by 1 .. 6 CTAs, 8 kv heads, replayed
-// from a graph: 320 rows of one sequence of 4096 keys 54.4 38.0 31.4 27.8 *25.8 42.1, of 4 *56.5 68.8
-// 78.9 70.8 83.1 95.4; 120 rows of 16 sequences of 1k-16k 158.9 *101.8 124.1 128.2 142.2 154.0, of
-// 4096 *56.4 72.8 83.8 95.4 106.5 119.6 (* the one taken); 800 rows of 4 of 32768 572 *462 531. Few
-// row tiles over a long prefix take up to 16 (one of 32768, 2 kv heads, 320 rows: 38 us; with 8, 55).
+// from a graph, cold: 320 rows of one sequence of 4096 keys 54.4 38.0 31.9 29.8 *27.8 42.1, of 4 *56.4 68.7
+// 81.0 74.9 87.2 97.4; 120 rows of 16 sequences of 1k-16k 146.6 *115.8 126.1 138.4 154.8 169.1, of
+// 4096 *57.5 75.0 89.2 101.5 111.7 124.0 (* the one taken); 800 rows of 4 of 32768 571 *468 532, of 2 of
+// 8192 93 *106 118 (one wave would do, but equal lengths are not known here). Few row tiles over a
+// long prefix take up to 16 (one of 32768, 2 kv heads, 320 rows: 40 us; with 8, 54).
 template <int DH>
 static int choose_split(long long groups, long long tiles) {
   int best = 0;

@@ -12,13 +12,14 @@
 // the run.
 //
 // What bounds them: the bytes of the rows, and for a few tokens the launch. 21 384 prompt rows
-// of 8 kv heads (131 MB) take 24 us, 5.5 TB/s of the 6.8 that a plain copy reaches: a CTA reads
+// of 8 kv heads (131 MB) take 24 us where L2 still holds part of them, as behind a projection, and
+// 31.3 from cold caches, 4.2 TB/s of the 6.8 that a plain copy reaches: a CTA reads
 // its 32 KB, waits for the maximum of all of it, and writes; five CTAs an SM, a few registers of
 // theirs spilled, fill each other's waits better than four without (31.3 us from cold caches, 34.5),
 // six worse; with smaller blocks, whose groups are not tied to each other, four do (33.9, five 42).
 // Blocks of 16 tokens take 33.9 us by a warp each, where one run after another by all of a CTA took
-// 101, fp32 rows 54 and 205. Replayed from a graph 64 single tokens take 5.9 us, the accepted tokens of
-// one sequence 3.1 and of 32 sequences 4.6: little more than an empty kernel.
+// 101, fp32 rows 54 and 205. Replayed from a graph 64 single tokens take 5.4 us, the accepted tokens of
+// one sequence and of 32 sequences 2.5: little more than an empty kernel.
 #include <type_traits>
 
 #include "ssd_kvq.cuh"
