@@ -640,6 +640,67 @@ size_t ssd_lowrank_head_workspace_size(const ssd_head_args* a);
 int ssd_lowrank_head(const ssd_head_args* a, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * ssd_filter_probs — the distributions that sampling settings leave of logit rows.
+ *
+ * Speculative Decoding 해부 page, §3: the acceptance compares p(x) and q(x), so where tokens are
+ * drawn from a distribution changed by a temperature or cut to its best tokens, both sides of
+ * the comparison have to be that distribution. This call makes it: its rows are ssd_accept's
+ * SSD_PROBS_F32 rows. For a row z with settings T, top_k, top_p, min_p:
+ *   w_i = exp((z_i - max z) / T); the tokens in the order (z descending, index ascending);
+ *   a token at place j (from 0) of that order stays iff
+ *     j < top_k                                          (top_k <= 0 or >= V: all)
+ *     sum of w before it < top_p * sum of w of the first top_k   (top_p >= 1 or NaN: all)
+ *     w >= min_p                                         (min_p <= 0 or NaN: all)
+ *   or j = 0; p_i = w_i / sum of w of those that stay, 0 for the others.
+ * T == 0 is greedy: the first of the largest stays alone. A T that is negative or NaN
+ * records SSD_ERR_DEVICE and counts as 0. A NaN logit counts as -inf and never stays, +inf as the
+ * largest finite number; a row without a logit above -inf becomes all zeros.
+ * Weights have a relative error under 2^-29 and sums are exact sums of round(w 2^43), so results
+ * do not depend on the order of execution, and a token is cut otherwise than in exact
+ * arithmetic only where the sum before it is within about 2^-29 of the border (relative).
+ * Rows and settings (ssd_rows_args): logits R rows of V elements of dtype (SSD_F32 or SSD_BF16),
+ * row_stride elements apart (any alignment of the element); row r takes its setting from entry
+ * r / rows_per of temperature, top_k, top_p, min_p (each may be NULL: 1, all, all, all).
+ *   probs [R][V] fp32 output.
+ *   blk_len [B][NB] (optional): with it R = B * (1 + NB * Dmax) rows as ssd_accept takes them, and
+ *   the rows of absent tokens (row 1 + k*Dmax + d-1 with d > blk_len[b][k]) are not read and stay
+ *   as they were.
+ * probs must not overlap an input (SSD_ERR_INVALID). 1 <= V <= 2^20, R < 2^28, else
+ * SSD_ERR_UNSUPPORTED; R == 0 launches nothing. The kernel starts only after the one before it
+ * on the stream has completed and lets the next one start when it has completed itself, so
+ * ssd_accept may take its rows in either row mode.
+ * Workspace: at least 256 bytes, 256-byte aligned (the status header).
+ */
+typedef struct {
+  const void* logits;
+  int dtype;
+  int64_t R, V, row_stride, rows_per;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+} ssd_rows_args;
+
+int ssd_filter_probs(const ssd_rows_args* a, const int32_t* blk_len, int NB, int Dmax, float* probs,
+                     void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ssd_sample — one token of each row, drawn from the distribution of ssd_filter_probs.
+ *
+ * Speculative Decoding 해부 page, §2 Phase 1: the drafter draws x_i from q_i, and the acceptance
+ * needs q_i(x). For row r with the uniform u[r] in [0, 1) (values outside: the nearest inside,
+ * NaN 0):
+ *   token[r] = the first i, in index order, with w_0 + .. + w_i > u * (sum of w), over the tokens
+ *              that stay; -1 for a row without a logit above -inf
+ *   prob[r]  = p of that token (optional, may be NULL; 0 where token is -1)
+ *   probs    = the whole row of p, as ssd_filter_probs writes it (optional, [R][V])
+ * The sums are those of round(w 2^43): a token whose weight is below 2^-44 of the largest is
+ * never drawn. Arguments, limits and workspace as for ssd_filter_probs.
+ */
+int ssd_sample(const ssd_rows_args* a, const float* u, int32_t* token, float* prob, float* probs,
+               void* ws, size_t ws_bytes, void* stream);
+
+/*
  * ssd_accept_static — ssd_accept without a caller-provided workspace.
  *
  * The pages have no counterpart for this call; it exists for callers that
@@ -737,7 +798,8 @@ enum {
   SSD_KERNEL_RETRIEVE = 7,
   SSD_KERNEL_HEAD_DOWN = 8,          /* ssd_lowrank_head: u = W_down h */
   SSD_KERNEL_HEAD_UP = 9,            /* ssd_lowrank_head: z = W_up u and its statistics */
-  SSD_KERNEL_HEAD_COMBINE = 10       /* ssd_lowrank_head: per-row merge */
+  SSD_KERNEL_HEAD_COMBINE = 10,      /* ssd_lowrank_head: per-row merge */
+  SSD_KERNEL_SAMPLE = 11             /* ssd_filter_probs, ssd_sample */
 };
 int ssd_profile_kernel(int kernel_id, void* start_event, void* end_event);
 

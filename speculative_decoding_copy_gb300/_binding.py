@@ -31,9 +31,10 @@ EXPORTED = ["ssd_status_string", "ssd_version", "ssd_launch_count", "ssd_gate_ma
             "ssd_copy_stats", "ssd_lowrank_head_workspace_size", "ssd_lowrank_head", "ssd_read_static_error",
             "ssd_read_probe", "ssd_checked_build", "ssd_read_check_error",
             "ssd_page_tables", "ssd_append_kv_quant", "ssd_commit_kv_quant",
-            "ssd_verify_attn_quant_workspace_size", "ssd_verify_attn_quant"]
+            "ssd_verify_attn_quant_workspace_size", "ssd_verify_attn_quant",
+            "ssd_filter_probs", "ssd_sample"]
 SSD_KERNEL = dict(vocab_stats=1, verify_attn=2, attn_combine=3, accept_finish=4, gate_match=6,
-                  retrieve=7, head_down=8, head_up=9, head_combine=10)
+                  retrieve=7, head_down=8, head_up=9, head_combine=10, sample=11)
 
 
 class SsdError(RuntimeError):
@@ -91,6 +92,12 @@ class CommitQuantArgs(ctypes.Structure):
                 ("n_out", c_void_p), ("new_len", c_void_p), ("block_table", c_void_p), ("dtype", c_int),
                 ("B", c_int), ("NB", c_int), ("Dmax", c_int), ("Hkv", c_int), ("dh", c_int), ("scale_block", c_int),
                 ("pages_per_seq", c_int), ("P_max", c_int64), ("num_pages", c_int64)]
+
+
+class RowsArgs(ctypes.Structure):
+    _fields_ = [("logits", c_void_p), ("dtype", c_int), ("R", c_int64), ("V", c_int64), ("row_stride", c_int64),
+                ("rows_per", c_int64), ("temperature", c_void_p), ("top_k", c_void_p), ("top_p", c_void_p),
+                ("min_p", c_void_p)]
 
 
 class AttnQuantArgs(ctypes.Structure):
@@ -191,6 +198,10 @@ def load(path) -> ctypes.CDLL:
         L.ssd_verify_attn_quant_workspace_size.argtypes = [POINTER(AttnQuantArgs)]
         L.ssd_verify_attn_quant.restype = c_int
         L.ssd_verify_attn_quant.argtypes = [POINTER(AttnQuantArgs), c_void_p, c_size_t, c_void_p]
+        L.ssd_filter_probs.restype = c_int
+        L.ssd_filter_probs.argtypes = [POINTER(RowsArgs), c_void_p, c_int, c_int, c_void_p, c_void_p, c_size_t, c_void_p]
+        L.ssd_sample.restype = c_int
+        L.ssd_sample.argtypes = [POINTER(RowsArgs), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
         L.ssd_checked_build.restype = c_int
         L.ssd_read_check_error.restype = c_int
         L.ssd_read_check_error.argtypes = [c_void_p, POINTER(c_int32)]
@@ -496,8 +507,8 @@ def _new(stream, shape, dtype, device, make=torch.empty):
         return make(shape, dtype=dtype, device=device)
 
 
-def _quant_call(fn, args, ws, device, stream, *named):
-    """Call entry point `fn` on `stream` (the device's current one where none is given) with the
+def _quant_call(fn, args, ws, device, stream, *named, more=()):
+    """Call entry point `fn` (`more`: what it takes between `args` and the workspace) on `stream` (the device's current one where none is given) with the
     device current; a workspace whose header is clear is made where none is given. `named`:
     the (name, tensor) pairs that must not overlap, to name those for which the call was
     refused."""
@@ -513,10 +524,10 @@ def _quant_call(fn, args, ws, device, stream, *named):
         handle = stream.cuda_stream
     call = getattr(lib(), fn)
     if torch._C._cuda_getDevice() == device.index:
-        rc = call(ctypes.byref(args), ws.data_ptr(), ws.numel(), handle)
+        rc = call(ctypes.byref(args), *more, ws.data_ptr(), ws.numel(), handle)
     else:
         with torch.cuda.device(device):
-            rc = call(ctypes.byref(args), ws.data_ptr(), ws.numel(), handle)
+            rc = call(ctypes.byref(args), *more, ws.data_ptr(), ws.numel(), handle)
     if rc != SSD_OK:
         if rc == SSD_ERR_INVALID:
             _need_apart(*named)
@@ -672,6 +683,100 @@ def ssd_verify_attn_quant(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand,
                            scale_block, out, scale, block_table)
     _quant_call("ssd_verify_attn_quant", args, ws, dev, stream, ("out", out), ("q", q))
     return out
+
+
+# ---------------------------------------------------------------------------
+# sampling distributions
+def _logit_rows(logits, temperature, top_k, top_p, min_p):
+    """Check logit rows [..][V] (dense but for the stride between rows) and their settings; returns
+    (RowsArgs, shape of the rows, the named tensors)."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.dtype not in _ROWS:
+        raise ValueError(f"logits: dtype {logits.dtype} not in {_ROWS}")
+    if logits.dim() not in (1, 2, 3):
+        raise ValueError(f"logits must be [V], [R][V] or [B][n][V], got {list(logits.shape)}")
+    *lead, V = logits.shape
+    R = 1
+    for n in lead:
+        R *= n
+    st = logits.stride()
+    if R and V > 1 and st[-1] != 1:
+        raise ValueError("logits: the elements of a row must be dense")
+    step = V
+    if R > 1:
+        step = st[-2] if lead[-1] > 1 else st[0]
+        if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * step:
+            raise ValueError("logits: rows must be evenly spaced")
+        if step < V:
+            raise ValueError("logits: rows must not overlap")
+    dev, named, ptrs, sets = logits.device, [("logits", logits)], [], None
+    for name, t, kinds in (("temperature", temperature, _F32), ("top_k", top_k, _I32), ("top_p", top_p, _F32), ("min_p", min_p, _F32)):
+        if t is None:
+            ptrs.append(None)
+            continue
+        if sets is None:
+            _need(t, name, kinds, 1)
+            sets = t.shape[0]
+            if R and (sets < 1 or R % sets):
+                raise ValueError(f"{R} rows do not divide among {sets} settings")
+        _need_shape(t, name, kinds, (sets,), dev)
+        named.append((name, t))
+        ptrs.append(t.data_ptr())
+    return RowsArgs(logits.data_ptr(), _elem_type(logits), R, V, max(step, V) if R <= 1 else step, max(1, R // (sets or 1)), *ptrs), lead, named
+
+
+def ssd_filter_probs(logits, temperature=None, top_k=None, top_p=None, min_p=None, *, blk_len=None, Dmax=0, out=None, ws=None,
+                     stream=None):
+    """The distributions that temperature, top-k, top-p and min-p leave of logit rows [R][V] or
+    [B][n][V] (fp32 or bf16, any row stride): fp32 probabilities of the same shape, as ssd_accept
+    takes them (SSD_PROBS_F32). The settings are vectors (top_k int32, the others fp32) of one
+    entry for each R / len(setting) rows in turn; None: 1, all, all, all. With blk_len [B][NB] and
+    Dmax the rows are ssd_accept's [B][1 + NB*Dmax][V] and those of absent tokens stay as they were."""
+    args, lead, named = _logit_rows(logits, temperature, top_k, top_p, min_p)
+    dev, NB = logits.device, 0
+    if blk_len is not None:
+        _need(blk_len, "blk_len", _I32, 2)
+        B, NB = blk_len.shape
+        if blk_len.device != dev:
+            raise ValueError(f"blk_len is on {blk_len.device}, not on {dev}")
+        if Dmax < 1 or args.R != B * (1 + NB * Dmax):
+            raise ValueError(f"{args.R} rows are not {B} x (1 + {NB} x {Dmax})")
+        named.append(("blk_len", blk_len))
+    if out is None:
+        out = _new(stream, logits.shape, torch.float32, dev)
+    else:
+        _need_shape(out, "out", _F32, logits.shape, dev)
+    _quant_call("ssd_filter_probs", args, ws, dev, stream, ("out", out), *named,
+                more=(None if blk_len is None else blk_len.data_ptr(), NB, int(Dmax), out.data_ptr()))
+    return out
+
+
+def ssd_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, *, out=None, probs_out=None, ws=None, stream=None):
+    """One token of each logit row, drawn from ssd_filter_probs's distribution with the uniforms u
+    [R] or [B][n]; returns dict(token, prob) of u's shape (int32, -1 for a row without a logit above
+    -inf; fp32 probability of the token). probs_out: fp32 tensor of the logits' shape that gets the
+    rows' distributions."""
+    args, lead, named = _logit_rows(logits, temperature, top_k, top_p, min_p)
+    dev, lead = logits.device, tuple(lead)
+    _need_shape(u, "u", _F32, lead, dev)
+    o = {} if out is None else out
+    token, prob = o.get("token"), o.get("prob")
+    if token is None:
+        token = _new(stream, lead, torch.int32, dev)
+    else:
+        _need_shape(token, "token", _I32, lead, dev)
+    if prob is None:
+        prob = _new(stream, lead, torch.float32, dev)
+    else:
+        _need_shape(prob, "prob", _F32, lead, dev)
+    named = [("token", token), ("prob", prob)] + named + [("u", u)]
+    if probs_out is not None:
+        _need_shape(probs_out, "probs_out", _F32, logits.shape, dev)
+        named.append(("probs_out", probs_out))
+    _quant_call("ssd_sample", args, ws, dev, stream, *named,
+                more=(u.data_ptr(), token.data_ptr(), prob.data_ptr(), None if probs_out is None else probs_out.data_ptr()))
+    return {"token": token, "prob": prob}
 
 
 def ssd_copy_stats(gate, n_cand, acc_len, W, counts, stream=None):
