@@ -653,7 +653,7 @@ int ssd_lowrank_head(const ssd_head_args* a, void* ws, size_t ws_bytes, void* st
  *     w >= min_p                                         (min_p <= 0 or NaN: all)
  *   or j = 0; p_i = w_i / sum of w of those that stay, 0 for the others.
  * T == 0 is greedy: the first of the largest stays alone. A T that is negative or NaN
- * records SSD_ERR_DEVICE and counts as 0. A NaN logit counts as -inf and never stays, +inf as the
+ * records SSD_ERR_DEVICE and counts as 0; one above 2^100 counts as 2^100. A NaN logit counts as -inf and never stays, +inf as the
  * largest finite number; a row without a logit above -inf becomes all zeros.
  * Weights have a relative error under 2^-29 and sums are exact sums of round(w 2^43), so results
  * do not depend on the order of execution, and a token is cut otherwise than in exact
