@@ -32,10 +32,12 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kBinBits = 10;
+constexpr int kLin = 256;                  // bins of a row's values, the first level of top-p
 constexpr int kMaxCluster = 8;
 constexpr int kIdxBits = 20;               // V <= 2^20: the weight sums then fit 64 bits
 constexpr int kTab = 64;
 constexpr uint64_t kAll = ~0ull;
+constexpr int kMaxShare = 4;                // top-k tokens a warp answers for, where its lanes' largest bound them
 constexpr int kList = 1024;                // tokens near a border that one CTA may hold,
 constexpr int kMerged = 2048;              // and all CTAs of the cluster together, to be sorted
 
@@ -59,7 +61,8 @@ struct Params {
 };
 
 struct Shared {
-  float2 tab[kTab];                        // 2^(i/64) as fp32, and what that lacks relative to it
+  float2 pow[kTab];                        // kPowers
+  int2 tab[kTab];                          // powers of two of the row (make_table)
   union {
     uint32_t hist[2][3][kBins];            // count, low and high word of the weight; two levels in turns
     uint64_t sort[kMerged];
@@ -71,6 +74,7 @@ struct Shared {
   uint64_t part[kWarps], part2[kWarps];
   uint64_t wsum[kWarps];
   float wmax[kWarps];
+  uint32_t wkey[kWarps];
   uint64_t sel_e, sel_incl;                // of the bin chosen: weight before it, and with it
   uint32_t sel_n, sel_cnt, sel_bin, list_n;
 };
@@ -114,45 +118,95 @@ constexpr float kFltMax = 3.402823466e38f;
 constexpr float kMagic = 12582912.f;       // 1.5 * 2^23: adding it rounds to an integer, held in the low bits
 constexpr int kMagicBits = 0x4B400000;
 
-// w = 2^((z - zmax) c), c = ch + cl = log2(e) / T, of z >= zmin (where w >= 2^-125.5). With d = z - zp
-// exact and zmax's own d c = M, rounded to n0 / 64 and a rest mu:
-//   round(64 d ch) - n0 = n,   (z - zmax) c = n / 64 + r,   r = (d ch - round(64 d ch) / 64) + (d cl - mu)
-// zp = 0 unless |M| >= 2^15 (the magic number would lose bits): zp = zmax then, and every z >= zmin
-// lies within a factor of two of it, so that d is exact again.
+// Weights w = 2^((z - zmax) c), c = ch + cl = log2(e) / T, of z >= zmin (where w >= 2^-125.5).
+// `plain` rows: with n = round(64 z ch), held in the low bits of m = 64 z ch + 1.5 2^23,
+//   64 z c = n + r,  r = (64 z ch - n) + 64 z cl,   w = 2^(n/64 - zmax c) 2^(r/64)
+// and the first factor is entry n mod 64 of a table of the row, 2^(i/64 - zmax c) with what its fp32
+// number lacks, plus n / 64 in the exponent (the entry's bits are less i 2^17, so that the bits of m
+// shifted by 17 are all there is to add). Values below zmin act as zmin, whose weight sums see as 0.
+// Other rows: 64 |zmax c| >= 2^21 (m would lose bits), an infinity, or a zmin that is not far
+// enough below zmax or not above -inf. They take differences to zmax first: where |zmax c| is
+// large, every z >= zmin lies within a factor of two of it, so that these are exact again.
 struct Scale {
-  float zmax, zmin, zp, c64, ch, cl, mu;
+  float zmax, zmin, c64, cl64, zp, mu;
   int nbias;
   uint32_t kmax;
+  bool plain;
 };
 
-// In pairs of fp32 numbers: a division in fp64 by every thread of a CTA takes microseconds here
-__device__ __forceinline__ Scale make_scale(float zmax, float temp) {
+// what depends on the temperature alone, in pairs of fp32 numbers: a division in fp64 by every thread
+// of a CTA takes microseconds here
+struct Rate {
+  float ch, cl, span;                      // log2(e) / T, and 125.49 of its inverse
+};
+__device__ __forceinline__ Rate make_rate(float temp) {
+  Rate t;
+  t.ch = fminf(__fdiv_rn(1.44269502f, temp), 0x1p120f);
+  t.cl = t.ch < 0x1p120f ? __fdiv_rn(fmaf(-t.ch, temp, 1.44269502f) + 1.92596299e-8f, temp) : 0.f;
+  t.span = __fdiv_rd(125.49f, t.ch);
+  return t;
+}
+
+__device__ __forceinline__ Scale make_scale(float zmax, const Rate& t, bool inf) {
   Scale s;
   s.zmax = zmax;
   s.kmax = okey(zmax + 0.f);
-  s.ch = fminf(__fdiv_rn(1.44269502f, temp), 0x1p120f);
-  s.cl = s.ch < 0x1p120f ? __fdiv_rn(fmaf(-s.ch, temp, 1.44269502f) + 1.92596299e-8f, temp) : 0.f;
-  s.c64 = s.ch * kTab;
-  s.zp = fabsf(zmax) * s.ch < 32768.f ? 0.f : zmax;
-  const float d = zmax - s.zp, ph = d * s.ch, n0 = rintf(ph * kTab);
-  s.mu = fmaf(n0, -1.f / kTab, ph) + fmaf(d, s.cl, fmaf(d, s.ch, -ph));
+  s.c64 = t.ch * kTab;
+  s.cl64 = t.cl * kTab;
+  const bool near = fabsf(zmax) * t.ch < 32768.f;
+  s.zp = near ? 0.f : zmax;
+  const float d = zmax - s.zp, ph = d * s.c64, n0 = rintf(ph);
+  s.mu = (ph - n0) + fmaf(d, s.cl64, fmaf(d, s.c64, -ph));
   s.nbias = kMagicBits + static_cast<int>(n0);
-  s.zmin = fmaxf(__fadd_ru(zmax, -__fdiv_rd(125.49f, s.ch)), -kFltMax);
+  s.zmin = fmaxf(__fadd_ru(zmax, -t.span), -kFltMax);
+  s.plain = near && !inf && s.zmin > -kFltMax && (zmax - s.zmin) * t.ch > 100.f;
   return s;
 }
 
-// w = wh + wl of a logit x: 0 below zmin and for NaN, +inf counts as the largest finite number.
-// Rounding: r 2^-31, its power series 2^-31, wl 2^-31 (|wl| <= wh / 128): relative error under 2^-29
-__device__ __forceinline__ void weight(float x, const Scale& s, const float2* tab, float& wh, float& wl) {
+// 2^(r/64) - 1 for |r| <= 1/2: powers of ln 2 / 64 over factorials, the next term is below 4e-11
+__device__ __forceinline__ float exp_rest(float r, float last) {
+  return fmaf(fmaf(fmaf(2.11731752e-7f, r, 5.86490495e-5f), r, 1.08304247e-2f), r, last);
+}
+
+// w = wh + wl of a logit: rounding of r 2^-31, of the series 2^-31, of wl 2^-31 (|wl| <= wh / 128): relative
+// error under 2^-29. The product is never fused with a later sum, so that a weight is the same wherever
+// it is asked for.
+__device__ __forceinline__ void weight_plain(float x, const Scale& s, const int2* tab, float& wh, float& wl) {
+  const float z = fmaxf(x, s.zmin);
+  const float m = fmaf(z, s.c64, kMagic);
+  const float r = fmaf(z, s.cl64, fmaf(z, s.c64, -(m - kMagic)));
+  const uint32_t n = __float_as_uint(m);
+  const int2 t = tab[n & (kTab - 1)];
+  wh = __uint_as_float(static_cast<uint32_t>(t.x) + (n << 17));
+  wl = __fmul_rn(wh, exp_rest(r, __int_as_float(t.y)));
+}
+
+// the same for any row: 0 below zmin and for NaN, +inf counts as the largest finite number
+__device__ __forceinline__ void weight_any(float x, const Scale& s, const float2* pow, float& wh, float& wl) {
   const float d = fminf(fmaxf(x, s.zmin), kFltMax) - s.zp;
   const float m = fmaf(d, s.c64, kMagic);
-  const float r = fmaf(d, s.ch, (m - kMagic) * (-1.f / kTab)) + fmaf(d, s.cl, -s.mu);
+  const float r = fmaf(d, s.c64, -(m - kMagic)) + fmaf(d, s.cl64, -s.mu);
   const int n = __float_as_int(m) - s.nbias;
-  const float2 t = tab[n & (kTab - 1)];
+  const float2 t = pow[n & (kTab - 1)];
   wh = x >= s.zmin ? __int_as_float(__float_as_int(t.x) + ((n >> 6) << 23)) : 0.f;
-  // 2^r - 1 for |r| <= 1/128: powers of ln 2 over factorials, the next term is below 4e-11
-  const float q = fmaf(fmaf(0.0555041087f, r, 0.2402265070f), r, 0.6931471806f);
-  wl = __fmul_rn(wh, fmaf(q, r, t.y));     // never fused with a later sum: a weight is the same wherever it is asked for
+  wl = __fmul_rn(wh, exp_rest(r, t.y));
+}
+
+__device__ __forceinline__ void weight(float x, const Scale& s, const int2* tab, const float2* pow, float& wh, float& wl) {
+  if (s.plain) weight_plain(x, s, tab, wh, wl);
+  else weight_any(x, s, pow, wh, wl);
+}
+
+// the row's table of weight_plain, by the first 64 threads: entry i is 2^((i - n0 - mu) / 64)
+__device__ __forceinline__ void make_table(const Scale& s, const float2* pow, int2* tab) {
+  const int i = threadIdx.x;
+  if (i >= kTab || !s.plain) return;
+  const int n = i - (s.nbias - kMagicBits);
+  const float2 t = pow[n & (kTab - 1)];
+  const float e = exp_rest(-s.mu, t.y);
+  const float h = fmaf(t.x, e, t.x);
+  const float rest = fmaf(t.x, e, t.x - h) / h;
+  tab[i] = make_int2(__float_as_int(h) + ((n >> 6) << 23) - (i << 17), __float_as_int(rest));
 }
 
 // round(w 2^43) = A 2^22 + B, |B| <= 2^21 + 1: both as the bits of the rounded fp32 numbers, biased
@@ -227,7 +281,7 @@ struct Row {
   __device__ __forceinline__ uint4 get(int w, int first, int k) const {
     return k < nres ? data[w * nres + k] : global(first + k);
   }
-  // f(value, index) for every element of this warp, as it stands in the row
+  // f(four neighbours as they stand in the row, the first one's index) for every four of this warp
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -235,7 +289,10 @@ struct Row {
       const uint4 q = get(w, v0, k);
       const int i = (v0 + k) * VE - off;
 #pragma unroll
-      for (int e = 0; e < VE; ++e) f(elem(q, e), i + e);
+      for (int g = 0; g < VE; g += 4) {
+        const float x[4] = {elem(q, g), elem(q, g + 1), elem(q, g + 2), elem(q, g + 3)};
+        f(x, i + g);
+      }
     }
   }
 };
@@ -287,9 +344,9 @@ __device__ __forceinline__ uint64_t cluster_sum(uint64_t v, Shared& sh, int ex, 
   return total;
 }
 
+template <int BINS>
 __device__ __forceinline__ void clear_bins(Shared& sh, int buf) {
-  uint32_t* h = &sh.hist[buf][0][0];
-  for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) h[i] = 0u;
+  for (int i = threadIdx.x; i < BINS; i += kThreads) sh.hist[buf][0][i] = sh.hist[buf][1][i] = sh.hist[buf][2][i] = 0u;
   if (threadIdx.x == 0) sh.sel_bin = 0;
   __syncthreads();
 }
@@ -307,11 +364,11 @@ __device__ __forceinline__ void add_to_bin(Shared& sh, int buf, int bin, uint64_
 // The last bin that is not empty and before which the target is not reached (n0, e0: what lies
 // before the first bin); every CTA finds the same. A bin of tokens without weight counts as
 // empty where weights are asked for: no target above the weight before them is left there.
-template <bool COUNT>
+template <bool COUNT, int BINS>
 __device__ int find_bin(Shared& sh, int buf, int C, uint64_t target, uint64_t& n0, uint64_t& e0, uint64_t* incl, uint64_t* count) {
   const int tid = threadIdx.x;
   uint64_t n[2] = {0, 0}, w[2] = {0, 0};
-  for (int c = 0; c < C; ++c) {
+  for (int c = 0; c < C && 2 * tid < BINS; ++c) {
     const uint2 b = reinterpret_cast<const uint2*>(peer(sh.hist[buf][1], c))[tid];
     const uint2 d = reinterpret_cast<const uint2*>(peer(sh.hist[buf][2], c))[tid];
     w[0] += (static_cast<uint64_t>(d.x) << 32) + b.x;
@@ -351,52 +408,54 @@ __device__ __forceinline__ uint64_t comp_of(float z, int i, uint32_t kmax) {
 }
 
 // The bound of comp below which the tokens stay, COUNT: the first `target` of them, else those before
-// which the weight is below `target` (> 0). Looked at: comp in [lo, lo + 2^width) with z >= z_cut,
-// before which lies the weight e0. *kept gets the weight of those that stay.
-template <bool COUNT, typename T>
-__device__ uint64_t select(const Row<T>& row, const Scale& sc, uint64_t target, uint64_t lo, int width, uint64_t e0, float z_cut,
-                           Shared& sh, int& buf, int C, uint64_t* kept) {
-  uint64_t n0 = 0, count;
+// which the weight is below `target` (> 0). Looked at: the tokens that f picks, before which lies the
+// weight e0. Returns the bound and the weight of those that stay. One level for each 10 bits of comp.
+// (Arguments by value: their addresses would keep the caller's in local memory.)
+template <bool COUNT, typename T, typename F>
+__device__ __noinline__ ulonglong2 select(Row<T> row, Scale sc, uint64_t target, uint64_t e0, Shared& sh, int C, F f) {
+  uint64_t n0 = 0, count, lo = 0, kept;
+  int buf = 0, width = 32 + kIdxBits;
+  cluster_sync();                          // another CTA may still read the bins or the list of before
   for (;;) {
     const int shift = max(0, width - kBinBits);
-    clear_bins(sh, buf);
-    row.each([&](float x, int i) {
-      const float z = fminf(x, kFltMax);
-      if (!(x >= z_cut) || z == -INFINITY) return;
-      const uint64_t at = comp_of(z, i, sc.kmax) - lo;       // wraps to a large number below lo
-      if (at >> width != 0) return;
-      float wh, wl;
-      weight(z, sc, sh.tab, wh, wl);
-      add_to_bin<true>(sh, buf, static_cast<int>(at >> shift), weight_int(wh, wl));
+    clear_bins<kBins>(sh, buf);
+    row.each([&](const float (&x)[4], int i) {
+      for (int e = 0; e < 4; ++e) {
+        if (!f(x[e])) continue;
+        const uint64_t at = comp_of(fminf(x[e], kFltMax), i + e, sc.kmax) - lo;       // wraps to a large number below lo
+        if (at >> width != 0) continue;
+        float wh, wl;
+        weight(x[e], sc, sh.tab, sh.pow, wh, wl);
+        add_to_bin<true>(sh, buf, static_cast<int>(at >> shift), weight_int(wh, wl));
+      }
     });
     cluster_sync();
-    const int bin = find_bin<COUNT>(sh, buf, C, target, n0, e0, kept, &count);
+    const int bin = find_bin<COUNT, kBins>(sh, buf, C, target, n0, e0, &kept, &count);
     buf ^= 1;
     lo += static_cast<uint64_t>(bin) << shift;
-    if (shift == 0 || (COUNT && n0 + count <= target)) return lo + (1ull << shift);
+    if (shift == 0 || (COUNT && n0 + count <= target)) return make_ulonglong2(lo + (1ull << shift), kept);
     width = shift;
   }
 }
 
 // sort the first P (a power of two, 32 <= P <= kMerged) of sh.sort ascending
+__device__ __forceinline__ uint64_t exchange(uint64_t v, int i, int k, int d) {
+  const uint64_t o = __shfl_xor_sync(0xffffffffu, v, d);
+  return (((i & k) == 0) == ((i & d) == 0)) == (o < v) ? o : v;
+}
 __device__ void sort_merged(Shared& sh, int P) {
   const int tid = threadIdx.x;
-  for (int k = 2; k <= P; k <<= 1) {
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      if (j < 32) {
-        // the rest of this merge stays within a warp's 32 neighbours
-        for (int i = tid; i < P; i += kThreads) {
-          uint64_t v = sh.sort[i];
-          for (int d = j; d > 0; d >>= 1) {
-            const uint64_t o = __shfl_xor_sync(0xffffffffu, v, d);
-            const bool up = (i & k) == 0, low = (i & d) == 0;
-            v = (up == low) == (o < v) ? o : v;
-          }
-          sh.sort[i] = v;
-        }
-        __syncthreads();
-        break;
-      }
+  for (int i = tid; i < P; i += kThreads) {
+    uint64_t v = sh.sort[i];
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+      for (int d = k >> 1; d > 0; d >>= 1) v = exchange(v, i, k, d);
+    sh.sort[i] = v;
+  }
+  __syncthreads();
+  for (int k = 64; k <= P; k <<= 1) {
+    for (int j = k >> 1; j >= 32; j >>= 1) {
       for (int t = tid; t < P / 2; t += kThreads) {
         const int i = ((t & ~(j - 1)) << 1) | (t & (j - 1));
         const uint64_t a = sh.sort[i], b = sh.sort[i + j];
@@ -407,6 +466,14 @@ __device__ void sort_merged(Shared& sh, int P) {
       }
       __syncthreads();
     }
+    // the rest of this merge stays within 32 neighbours
+    for (int i = tid; i < P; i += kThreads) {
+      uint64_t v = sh.sort[i];
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) v = exchange(v, i, k, d);
+      sh.sort[i] = v;
+    }
+    __syncthreads();
   }
 }
 
@@ -419,38 +486,39 @@ __device__ __forceinline__ int padded(int n) {
 // The tokens f picks, as comp, of all CTAs in sh.sort, sorted; returns their number, or -1 where they are
 // too many. Every CTA gets the same.
 template <typename T, typename F>
-__device__ int gather(const Row<T>& row, const Scale& sc, Shared& sh, int C, F f) {
-  const int tid = threadIdx.x;
-  if (tid == 0) sh.list_n = 0;
-  __syncthreads();
-  row.each([&](float x, int i) {
-    if (!f(x, i)) return;
-    const uint32_t at = atomicAdd(&sh.list_n, 1u);
-    if (at < kList) sh.list[at] = comp_of(fminf(x, kFltMax), i, sc.kmax);
+__device__ __forceinline__ int gather(const Row<T>& row, const Scale& sc, Shared& sh, int C, F f) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  row.each([&](const float (&x)[4], int i) {
+    const bool b[4] = {f(x[0]), f(x[1]), f(x[2]), f(x[3])};
+    if (!(b[0] || b[1] || b[2] || b[3])) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (b[e]) {
+        const uint32_t at = atomicAdd(&sh.list_n, 1u);
+        if (at < kList) sh.list[at] = comp_of(fminf(x[e], kFltMax), i + e, sc.kmax);
+      }
   });
   cluster_sync();
-  uint32_t n = 0;
-  bool fits = true;
+  // one warp a CTA of the cluster; every warp knows all counts
+  uint32_t k = lane < C ? *peer(&sh.list_n, lane) : 0;
+  const bool fits = __all_sync(0xffffffffu, k <= kList);
+  uint32_t before = 0, n = 0;
   for (int c = 0; c < C; ++c) {
-    const uint32_t k = *peer(&sh.list_n, c);
-    fits = fits && k <= kList;
-    n += k;
+    const uint32_t kc = __shfl_sync(0xffffffffu, k, c);
+    if (c < wid) before += kc;
+    n += kc;
   }
-  fits = fits && n <= kMerged;
-  if (fits) {
-    const int P = padded(static_cast<int>(n));
-    uint32_t at = 0;
-    for (int c = 0; c < C; ++c) {
-      const uint32_t k = *peer(&sh.list_n, c);
-      const uint64_t* from = peer(sh.list, c);
-      for (uint32_t i = tid; i < k; i += kThreads) sh.sort[at + i] = from[i];
-      at += k;
-    }
-    for (int i = static_cast<int>(n) + tid; i < P; i += kThreads) sh.sort[i] = kAll;
-    __syncthreads();
-    sort_merged(sh, P);
+  if (!fits || n > kMerged) return -1;
+  k = __shfl_sync(0xffffffffu, k, wid & (kMaxCluster - 1));
+  if (wid < C) {
+    const uint64_t* from = peer(sh.list, wid);
+    for (uint32_t i = lane; i < k; i += 32) sh.sort[before + i] = from[i];
+  } else if (wid == kWarps - 1) {
+    for (int i = static_cast<int>(n) + lane, P = padded(static_cast<int>(n)); i < P; i += 32) sh.sort[i] = kAll;
   }
-  return fits ? static_cast<int>(n) : -1;
+  __syncthreads();
+  sort_merged(sh, padded(static_cast<int>(n)));
+  return static_cast<int>(n);
 }
 
 // Of the n sorted tokens in sh.sort, before which lies the weight e0: those that stay, in their order,
@@ -470,7 +538,7 @@ __device__ int cut_sorted(Shared& sh, const Scale& sc, int n, uint64_t e0, int k
     if (e < per && j < n) {
       const float z = okey_value(sc.kmax - static_cast<uint32_t>(sh.sort[j] >> kIdxBits));
       float wh, wl;
-      weight(z, sc, sh.tab, wh, wl);
+      weight(z, sc, sh.tab, sh.pow, wh, wl);
       W[e] = weight_int(wh, wl);
       mp[e] = !(min_p > 0.f) || z >= sc.zmax || (wh - min_p) + wl >= 0.f;
     }
@@ -536,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
     else
       *dst = row.edge(v);
   }
-  if (tid < kTab) sh.tab[tid] = kPowers.v[tid];
+  if (tid < kTab) sh.pow[tid] = kPowers.v[tid];
   float temp = p.temperature != nullptr ? __ldg(p.temperature + set) : 1.f;
   int64_t k = p.top_k != nullptr ? __ldg(p.top_k + set) : 0;
   const float top_p = p.top_p != nullptr ? __ldg(p.top_p + set) : 1.f;
@@ -552,93 +620,160 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
   }
   min_p = fminf(min_p, 1.f);
   if (k < 0 || k >= p.V) k = 0;
+  const Rate rate = make_rate(temp);
+  // how far below the largest a token may lie whose weight is (1 - top_p) / V of it
+  const float depth = top_p < 1.f ? __fmul_ru(-logf((1.f - fmaxf(top_p, 0.f)) / static_cast<float>(p.V) * 0.999f), temp) : 0.f;
+  // with top-k: the tokens that each warp that holds any, or each CTA, answers for
+  const int warps = (nvec + p.nvw - 1) / p.nvw, ctas = (warps + kWarps - 1) / kWarps;
+  const int share_w = static_cast<int>((k + warps - 1) / warps), share = static_cast<int>((k + ctas - 1) / ctas);
+  if (tid == 0) sh.list_n = 0;
   asm volatile("cp.async.wait_all;" ::: "memory");
 
-  // ---- the row's largest value; with top-k also a value that k tokens at least reach: the smallest,
-  // over the CTAs, of the ceil(k / C)-th largest of the threads' own maxima
+  // ---- the row's largest value; with top-k also a value that k tokens at least reach
   float mx = -INFINITY;
-  row.each([&](float x, int) { mx = fmaxf(mx, x); });
-  mx = fminf(mx, kFltMax);
+  row.each([&](const float (&x)[4], int) { mx = fmaxf(fmaxf(mx, fmaxf(x[0], x[1])), fmaxf(x[2], x[3])); });
+  uint32_t reach = 0;                      // as okey; 0: none found
+  const uint32_t key = okey(fminf(mx, kFltMax) + 0.f);
+  if (k > 0 && share_w <= kMaxShare) {
+    // the least, over the warps, of the share_w-th largest of the lanes' largest
+    uint32_t left = key;
+    for (int j = 0; j < share_w; ++j) {
+      reach = __reduce_max_sync(0xffffffffu, left);
+      const uint32_t who = __ballot_sync(0xffffffffu, left == reach);
+      if (lane == __ffs(who) - 1) left = 0;
+    }
+    if (lane == 0) sh.wkey[wid] = row.nw > 0 ? reach : ~0u;
+  }
   {
     const float m = warp_max(mx);
     if (lane == 0) sh.wmax[wid] = m;
   }
   __syncthreads();
-  uint32_t reach = 0;
-  const int64_t share = (k + C - 1) / C;
-  if (k > 0 && share <= kThreads) {
-    const uint32_t key = okey(mx + 0.f);
-    for (int bit = 31; bit >= 10; --bit) {
-      const uint32_t t = reach | (1u << bit);
-      if (__syncthreads_count(key >= t) >= share) reach = t;
+  if (k > 0 && share_w > kMaxShare && share <= 2 * kThreads) {
+    // the least, over the CTAs, of the share-th largest of the threads' largest (with more tokens
+    // than threads: half the share by their second largest, which two tokens reach), to 16 bits
+    uint32_t own = key;
+    int want = share;
+    if (share > kThreads) {
+      float m1 = -INFINITY, m2 = -INFINITY;
+      row.each([&](const float (&x)[4], int) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          m2 = fmaxf(m2, fminf(m1, x[e] > -INFINITY ? x[e] : -INFINITY));
+          m1 = fmaxf(m1, x[e]);
+        }
+      });
+      own = okey(fminf(m2, kFltMax) + 0.f);
+      want = (share + 1) / 2;
     }
+    reach = 0;
+    for (int bit = 31; bit >= 16; --bit) {
+      const uint32_t t = reach | (1u << bit);
+      if (__syncthreads_count(own >= t) >= want) reach = t;
+    }
+    if (rank >= ctas) reach = ~0u;
   }
   if (tid < C) {
     float t = -INFINITY;
+    uint32_t least = share_w <= kMaxShare ? ~0u : reach;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) t = fmaxf(t, sh.wmax[w]);
+    for (int w = 0; w < kWarps; ++w) {
+      t = fmaxf(t, sh.wmax[w]);
+      if (share_w <= kMaxShare) least = min(least, sh.wkey[w]);
+    }
     *peer(&sh.ex_max[rank], tid) = t;
-    *peer(&sh.ex_key[rank], tid) = reach;
+    *peer(&sh.ex_key[rank], tid) = least;
   }
   cluster_sync();
   float zmax = -INFINITY;
+  reach = ~0u;
   for (int c = 0; c < C; ++c) {
     zmax = fmaxf(zmax, sh.ex_max[c]);
     reach = min(reach, sh.ex_key[c]);
   }
   const bool empty = !(zmax > -INFINITY);
-  const Scale sc = make_scale(zmax, temp);
+  const Scale sc = make_scale(fminf(zmax, kFltMax), rate, zmax == INFINITY);
+  make_table(sc, sh.pow, sh.tab);
+  __syncthreads();
 
   uint64_t bound = kAll, S = 0, before = 0, mine = 0;
+  int stays = 0;
   bool known = false, all_cut = false;       // S is that of the tokens that stay; min-p is in the bound
   if (!empty) {
-    int buf = 0;
     if (k > 0) {
-      const float low = reach > okey(-INFINITY) ? okey_value(reach) : -INFINITY;
-      const int n = gather(row, sc, sh, C, [&](float x, int) { return x >= low && x > -INFINITY; });
+      const float low = reach > okey(-INFINITY) ? okey_value(reach) : -kFltMax;
+      const int n = gather(row, sc, sh, C, [low](float x) { return x >= low; });
       if (n >= 0) {
         const int m = cut_sorted(sh, sc, n, 0, static_cast<int>(k), top_p, 0, min_p, &S);
         bound = sh.sort[m - 1] + 1;
+        stays = m;
         all_cut = true;
       } else {
-        bound = select<true>(row, sc, static_cast<uint64_t>(k), 0, 32 + kIdxBits, 0, low, sh, buf, C, &S);
+        const ulonglong2 got = select<true>(row, sc, static_cast<uint64_t>(k), 0, sh, C, [low](float x) { return x >= low; });
+        bound = got.x;
+        S = got.y;
       }
       known = true;
     }
     if (top_p < 1.f && !all_cut) {
       // tokens of a weight below (1 - top_p) / V, together, are not more than the tail that is cut
-      // (the sum is at least 1); binned are the others, and all are summed
-      const float low = __fadd_rd(zmax, __fmul_rd(logf((1.f - fmaxf(top_p, 0.f)) / static_cast<float>(p.V) * 0.999f), temp));
-      const float z_cut = fmaxf(low, sc.zmin);
-      const uint32_t kd_cut = sc.kmax - okey(z_cut + 0.f);
-      const int width = 32 - __clz(kd_cut | 1) + kIdxBits;
-      const int shift = width - kBinBits;
-      clear_bins(sh, buf);
-      int sa = 0, sb = 0;
-      row.each([&](float x, int i) {
-        float wh, wl;
-        int a, b;
-        weight(x, sc, sh.tab, wh, wl);
-        weight_parts(wh, wl, a, b);
-        sa += a - kMagicBits;
-        sb += b - kMagicBits;
-        if (x >= z_cut)
-          add_to_bin<false>(sh, buf, static_cast<int>(comp_of(fminf(x, kFltMax), i, sc.kmax) >> shift),
-                            static_cast<uint64_t>(static_cast<int64_t>(a - kMagicBits) * 4194304 + (b - kMagicBits)));
-      });
-      const uint64_t sum = cluster_sum(static_cast<uint64_t>(static_cast<int64_t>(sa) * 4194304 + sb), sh, 0, rank, C, &before, &mine);
+      // (the sum is at least 1); binned by their value are the others, and all are summed
+      const float z_cut = fmaxf(__fadd_rd(sc.zmax, -depth), sc.zmin), range = sc.zmax - z_cut;
+      const float per = range > 0.f ? __fdiv_rd(kLin - 2.f, range) : 0.f;
+      const float per_bin = per < kFltMax ? per : 0.f;
+      // rounded, but never falls as x does
+      const float top = sc.zmax;
+      auto bin_of = [top, per_bin](float x) { return __float_as_int(fmaf(top - fminf(x, kFltMax), per_bin, kMagic)) - kMagicBits; };
+      if (known) {                         // another CTA may still read the bins or the list of before
+        cluster_sync();
+        if (tid == 0) sh.list_n = 0;
+      }
+      clear_bins<kLin>(sh, 0);
+      uint32_t sa = 0, sb = 0, count = 0;
+      auto add = [&](const float (&x)[4], const float (&wh)[4], const float (&wl)[4]) {
+        int a[4], b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          weight_parts(wh[e], wl[e], a[e], b[e]);
+          sa += static_cast<uint32_t>(a[e]);
+          sb += static_cast<uint32_t>(b[e]);
+        }
+        count += 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (x[e] >= z_cut)
+            add_to_bin<false>(sh, 0, bin_of(x[e]), static_cast<uint64_t>(static_cast<int64_t>(a[e] - kMagicBits) * 4194304 + (b[e] - kMagicBits)));
+      };
+      if (sc.plain) {
+        row.each([&](const float (&x)[4], int) {
+          float wh[4], wl[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) weight_plain(x[e], sc, sh.tab, wh[e], wl[e]);
+          add(x, wh, wl);
+        });
+      } else {
+        row.each([&](const float (&x)[4], int) {
+          float wh[4], wl[4];
+          for (int e = 0; e < 4; ++e) weight_any(x[e], sc, sh.pow, wh[e], wl[e]);
+          add(x, wh, wl);
+        });
+      }
+      // the biases go out modulo 2^32: a thread holds at most 512 tokens, so the sums fit
+      sa -= count * kMagicBits;
+      sb -= count * kMagicBits;
+      const uint64_t sum = cluster_sum(static_cast<uint64_t>(static_cast<int64_t>(static_cast<int>(sa)) * 4194304 + static_cast<int>(sb)), sh, 0, rank, C, &before, &mine);
       const uint64_t target = max(mul_fraction(known ? S : sum, fmaxf(top_p, 0.f), true), uint64_t{1});
-      uint64_t n0 = 0, e0 = 0, incl, count;
-      const uint64_t lo = static_cast<uint64_t>(find_bin<false>(sh, buf, C, target, n0, e0, &incl, &count)) << shift;
-      buf ^= 1;
-      const int n = gather(row, sc, sh, C, [&](float x, int i) {
-        return x >= z_cut && (comp_of(fminf(x, kFltMax), i, sc.kmax) - lo) >> shift == 0;
-      });
+      uint64_t n0 = 0, e0 = 0, incl, cnt;
+      const int bin = find_bin<false, kLin>(sh, 0, C, target, n0, e0, &incl, &cnt);
+      auto border = [z_cut, bin, bin_of](float x) { return x >= z_cut && bin_of(x) == bin; };
+      const int n = gather(row, sc, sh, C, border);
       if (n >= 0) {
         const int m = cut_sorted(sh, sc, n, e0, n, 1.f, target, 0.f, &S);
         bound = sh.sort[m - 1] + 1;
       } else {
-        bound = select<false>(row, sc, target, lo, shift, e0, z_cut, sh, buf, C, &S);
+        const ulonglong2 got = select<false>(row, sc, target, e0, sh, C, border);
+        bound = got.x;
+        S = got.y;
       }
       known = true;
     }
@@ -657,25 +792,40 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
     }
   }
   const bool use_min_p = min_p > 0.f && !all_cut;
-  // the weight of a token that stays; false for the others (NaN among them)
-  auto kept_weight = [&](float x, int i, float& wh, float& wl) {
-    wh = wl = 0.f;
-    const float z = fminf(x, kFltMax);
-    if (!(z > zt || (z == zt && i < it)) || !(x >= sc.zmin)) return false;
-    weight(x, sc, sh.tab, wh, wl);
-    if (use_min_p && !(x >= sc.zmax || (wh - min_p) + wl >= 0.f)) {
-      wh = wl = 0.f;
-      return false;
+  // of four neighbours the weights of those that stay, 0 for the others (NaN among them); false where none does
+  auto kept_weights = [&](const float (&x)[4], int i, float (&wh)[4], float (&wl)[4]) {
+    bool stay[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float z = fminf(x[e], kFltMax);
+      stay[e] = (z > zt || (z == zt && i + e < it)) && x[e] >= sc.zmin;
+      wh[e] = wl[e] = 0.f;
+    }
+    if (!(stay[0] || stay[1] || stay[2] || stay[3])) return false;
+    if (sc.plain) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) weight_plain(x[e], sc, sh.tab, wh[e], wl[e]);
+    } else {
+      for (int e = 0; e < 4; ++e) weight_any(x[e], sc, sh.pow, wh[e], wl[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (use_min_p) stay[e] = stay[e] && (x[e] >= sc.zmax || (wh[e] - min_p) + wl[e] >= 0.f);
+      if (!stay[e]) wh[e] = wl[e] = 0.f;
     }
     return true;
   };
 
+  // a few tokens that stay, known in their order: drawn from there, by the first CTA
+  const bool from_list = all_cut && stays <= kThreads;
   const bool draw = p.token != nullptr && !empty;
-  if (!empty && (use_min_p || !known || draw)) {
+  if (!empty && (use_min_p || !known || (draw && !from_list))) {
     uint64_t t = 0;
-    row.each([&](float x, int i) {
-      float wh, wl;
-      if (kept_weight(x, i, wh, wl)) t += weight_int(wh, wl);
+    row.each([&](const float (&x)[4], int i) {
+      float wh[4], wl[4];
+      if (kept_weights(x, i, wh, wl))
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t += weight_int(wh[e], wl[e]);
     });
     S = cluster_sum(t, sh, 1, rank, C, &before, &mine);
   }
@@ -693,25 +843,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
     float* out = p.probs + r * p.V;
     const bool wide = ((reinterpret_cast<uintptr_t>(out) / 4 - row.off) & 3) == 0;
     if (wide) {
-      for (int kv = lane; kv < row.nw; kv += 32) {
-        const uint4 q = row.get(wid, row.v0, kv);
-        const int i = (row.v0 + kv) * VE - row.off;
-        float v[VE];
+      row.each([&](const float (&x)[4], int i) {
+        float wh[4], wl[4], v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (kept_weights(x, i, wh, wl))
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          float wh, wl;
-          kept_weight(Row<T>::elem(q, e), i + e, wh, wl);
-          v[e] = probability(wh, wl);
-        }
-        if (row.inside(row.v0 + kv) && in_range(i + VE - 1, p.V, p.hdr, 510)) {
-#pragma unroll
-          for (int e = 0; e < VE; e += 4) *reinterpret_cast<float4*>(out + i + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int e = 0; e < 4; ++e) v[e] = probability(wh[e], wl[e]);
+        if (i >= 0 && i + 4 <= p.V && in_range(i + 3, p.V, p.hdr, 510)) {
+          *reinterpret_cast<float4*>(out + i) = make_float4(v[0], v[1], v[2], v[3]);
         } else {
 #pragma unroll
-          for (int e = 0; e < VE; ++e)
+          for (int e = 0; e < 4; ++e)
             if (i + e >= 0 && i + e < p.V) out[i + e] = v[e];
         }
-      }
+      });
     } else {
       // rows whose elements lie otherwise in 16 bytes than the output's: four bytes a lane
       const int i0 = row.v0 * VE - row.off;
@@ -721,10 +865,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
         const int kv = j / VE;
         const T* src = kv < row.nres ? reinterpret_cast<const T*>(row.data + wid * row.nres) + j
                                      : reinterpret_cast<const T*>(row.base) + static_cast<int64_t>(row.v0) * VE + j;
-        float x, wh, wl;
+        float x;
         if constexpr (sizeof(T) == 4) x = *src; else x = bf16_to_f32(*src);
-        kept_weight(x, i, wh, wl);
-        out[i] = probability(wh, wl);
+        const float z = fminf(x, kFltMax);
+        float v = 0.f;
+        if ((z > zt || (z == zt && i < it)) && x >= sc.zmin) {
+          float wh, wl;
+          weight(x, sc, sh.tab, sh.pow, wh, wl);
+          if (!use_min_p || x >= sc.zmax || (wh - min_p) + wl >= 0.f) v = probability(wh, wl);
+        }
+        out[i] = v;
       }
     }
   }
@@ -737,41 +887,64 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
     float u = __ldg(p.u + r);
     u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
     const uint64_t thr = mul_fraction(S, u, false);         // the first token with C_i > thr
-    if (thr >= before && thr < before + mine) {
-      // this CTA holds it: the warp, then the vector, then the element
+    auto found = [&](int i, float wh, float wl) {
+      p.token[r] = i;
+      if (p.prob != nullptr) p.prob[r] = probability(wh, wl);
+    };
+    if (from_list) {
+      if (rank == 0) {
+        // the tokens again, by index: 20 bits of it above 44 of the weight
+        const int P = padded(stays);
+        uint64_t own = kAll;
+        if (tid < stays) {
+          const uint64_t comp = sh.sort[tid];
+          float wh, wl;
+          weight(okey_value(sc.kmax - static_cast<uint32_t>(comp >> kIdxBits)), sc, sh.tab, sh.pow, wh, wl);
+          own = (comp & ((1u << kIdxBits) - 1)) << 44 | weight_int(wh, wl);
+        }
+        const uint64_t comp = tid < stays ? sh.sort[tid] : 0;
+        __syncthreads();
+        if (tid < P) sh.sort[tid] = own;
+        __syncthreads();
+        sort_merged(sh, P);
+        const uint64_t at = tid < stays ? sh.sort[tid] : 0, W = at & ((1ull << 44) - 1);
+        uint64_t all;
+        const uint64_t pre = block_scan(W, sh.part, &all);
+        if (thr >= pre && thr < pre + W) sh.sel_bin = static_cast<uint32_t>(at >> 44);
+        __syncthreads();
+        if (tid < stays && (comp & ((1u << kIdxBits) - 1)) == sh.sel_bin) {
+          float wh, wl;
+          weight(okey_value(sc.kmax - static_cast<uint32_t>(comp >> kIdxBits)), sc, sh.tab, sh.pow, wh, wl);
+          found(static_cast<int>(sh.sel_bin), wh, wl);
+        }
+      }
+    } else if (thr >= before && thr < before + mine) {
+      // this CTA holds it: the warp, then the four neighbours, then the token
       uint64_t c0 = before;
       int w = 0;
       while (w < kWarps - 1 && thr >= c0 + sh.wsum[w]) c0 += sh.wsum[w++];
       const int first = (rank * kWarps + w) * p.nvw;
-      const int nw = max(0, min(p.nvw, nvec - first));
-      for (int k0 = 0; k0 < nw; k0 += kThreads) {
-        const int kk = k0 + tid;
-        uint4 q = make_uint4(0, 0, 0, 0);
-        uint64_t t = 0, all;
-        const int i = (first + kk) * VE - row.off;
-        if (kk < nw) {
-          q = row.get(w, first, kk);
+      const int groups = max(0, min(p.nvw, nvec - first)) * (VE / 4);
+      for (int k0 = 0; k0 < groups; k0 += kThreads) {
+        const int g = k0 + tid;
+        const int i = first * VE - row.off + 4 * g;
+        uint64_t W[4] = {0, 0, 0, 0}, all;
+        float wh[4], wl[4];
+        if (g < groups) {
+          const uint4 q = row.get(w, first, g / (VE / 4));
+          const int e0 = g % (VE / 4) * 4;
+          float x[4];
 #pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            float wh, wl;
-            if (kept_weight(Row<T>::elem(q, e), i + e, wh, wl)) t += weight_int(wh, wl);
-          }
+          for (int e = 0; e < 4; ++e) x[e] = e0 == 0 ? Row<T>::elem(q, e) : Row<T>::elem(q, (e + 4) % VE);
+          if (kept_weights(x, i, wh, wl))
+#pragma unroll
+            for (int e = 0; e < 4; ++e) W[e] = weight_int(wh[e], wl[e]);
         }
-        uint64_t pre = c0 + block_scan(t, sh.part, &all);
-        if (thr >= pre && thr < pre + t) {
-          bool done = false;
+        uint64_t pre = c0 + block_scan(W[0] + W[1] + W[2] + W[3], sh.part, &all);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            float wh, wl;
-            if (!done && kept_weight(Row<T>::elem(q, e), i + e, wh, wl)) {
-              pre += weight_int(wh, wl);
-              if (thr < pre) {
-                done = true;
-                p.token[r] = i + e;
-                if (p.prob != nullptr) p.prob[r] = probability(wh, wl);
-              }
-            }
-          }
+        for (int e = 0; e < 4; ++e) {
+          if (thr >= pre && thr < pre + W[e]) found(i + e, wh[e], wl[e]);
+          pre += W[e];
         }
         c0 += all;
         if (thr < c0) break;
@@ -798,10 +971,9 @@ static int launch(const Params& in, int64_t rows, cudaStream_t s) {
   Params p = in;
   const int nvec = (p.V + 2 * VE - 2) / VE;                  // at most, whatever the row's first element's place
   int C = 1;
-  while (C < kMaxCluster && (16LL * nvec / C > 72 * 1024 || (rows * C * 2 <= 2LL * sms[dev] && nvec / C > 4 * kThreads))) C *= 2;
+  while (C < kMaxCluster && (16LL * nvec / C > 78 * 1024 || (rows * C * 2 <= 2LL * sms[dev] && nvec / C > 4 * kThreads))) C *= 2;
   const int per = kWarps * C;
   p.nvw = (nvec + per - 1) / per;
-  p.nvw = (p.nvw + 31) / 32 * 32;
   p.nres = std::min(p.nvw, kMaxData / 16 / kWarps);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
