@@ -6,7 +6,7 @@
 // cut nor a token depends on the order in which threads add. The tokens that stay are the first
 // ones in the order (z descending, index ascending), so one composite number
 //   comp = (okey(z_max) - okey(z)) * 2^20 + index       (okey: the fp32 order as unsigned integers)
-// and one bound say which. A bound is found by histograms of 1024 bins of comp (count and weight
+// and one bound say which. A bound is found by histograms of 512 bins of comp (count and weight
 // of each), the next one over the bin in which the count passes top-k or the weight passes
 // top_p * sum, down to single tokens; ties at the border are thereby cut by their index.
 //
@@ -30,8 +30,8 @@ using tc::cluster_sync;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 1024;
-constexpr int kBinBits = 10;
+constexpr int kBins = 512;                 // of one level of `select`
+constexpr int kBinBits = 9;
 constexpr int kLin = 256;                  // bins of a row's values, the first level of top-p
 constexpr int kMaxCluster = 8;
 constexpr int kIdxBits = 20;               // V <= 2^20: the weight sums then fit 64 bits
@@ -39,7 +39,9 @@ constexpr int kTab = 64;
 constexpr uint64_t kAll = ~0ull;
 constexpr int kMaxShare = 4;                // top-k tokens a warp answers for, where its lanes' largest bound them
 constexpr int kList = 1024;                // tokens near a border that one CTA may hold,
-constexpr int kMerged = 2048;              // and all CTAs of the cluster together, to be sorted
+constexpr int kFew = 256;                   // tokens from which one is drawn by sorting them once more
+constexpr int kCrowd = 256;                // entries of a bucket up to which they are counted against each other
+constexpr int kMerged = 4 * kThreads;       // and all CTAs of the cluster together, to be ordered
 
 struct Params {
   const void* logits;
@@ -61,11 +63,17 @@ struct Params {
 };
 
 struct Shared {
+  uint4 ends[2];
   float2 pow[kTab];                        // kPowers
   int2 tab[kTab];                          // powers of two of the row (make_table)
   union {
-    uint32_t hist[2][3][kBins];            // count, low and high word of the weight; two levels in turns
-    uint64_t sort[kMerged];
+    uint32_t hist[2][4][kBins];            // count; bits 0-15, 16-31 and 32-43 of the weight; two levels in turns
+    struct {
+      uint64_t list[2048];                 // unsorted (kMerged of them at most), and
+      uint16_t order[kMerged];             // the places of its entries in ascending order
+      uint16_t slot[kMerged];
+      uint32_t bucket[kThreads + 1];
+    } m;
   };
   uint64_t list[kList];                    // this CTA's tokens near a border
   uint64_t ex_sum[2][kMaxCluster];         // from every CTA of the cluster
@@ -76,7 +84,7 @@ struct Shared {
   float wmax[kWarps];
   uint32_t wkey[kWarps];
   uint64_t sel_e, sel_incl;                // of the bin chosen: weight before it, and with it
-  uint32_t sel_n, sel_cnt, sel_bin, list_n;
+  uint32_t sel_n, sel_cnt, sel_bin, list_n, kd_min, kd_max, fullest;
 };
 
 // the same variable in the CTA of rank `r`
@@ -117,6 +125,30 @@ __device__ constexpr Powers kPowers;
 constexpr float kFltMax = 3.402823466e38f;
 constexpr float kMagic = 12582912.f;       // 1.5 * 2^23: adding it rounds to an integer, held in the low bits
 constexpr int kMagicBits = 0x4B400000;
+
+// two fp32 numbers in one register pair: one instruction for both, each rounded as alone
+typedef uint64_t f32x2;
+__device__ __forceinline__ f32x2 two(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void apart(f32x2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // Weights w = 2^((z - zmax) c), c = ch + cl = log2(e) / T, of z >= zmin (where w >= 2^-125.5).
 // `plain` rows: with n = round(64 z ch), held in the low bits of m = 64 z ch + 1.5 2^23,
@@ -181,6 +213,21 @@ __device__ __forceinline__ void weight_plain(float x, const Scale& s, const int2
   wl = __fmul_rn(wh, exp_rest(r, __int_as_float(t.y)));
 }
 
+// weight_plain of two logits
+__device__ __forceinline__ void weight_plain2(float x0, float x1, const Scale& s, const int2* tab, f32x2& wh, f32x2& wl) {
+  const f32x2 z = two(fmaxf(x0, s.zmin), fmaxf(x1, s.zmin)), c = two(s.c64, s.c64), magic = two(kMagic, kMagic);
+  const f32x2 m = fma2(z, c, magic);
+  const f32x2 r = fma2(z, two(s.cl64, s.cl64), fma2(z, c, fma2(m, two(-1.f, -1.f), magic)));
+  float m0, m1;
+  apart(m, m0, m1);
+  const uint32_t n0 = __float_as_uint(m0), n1 = __float_as_uint(m1);
+  const int2 t0 = tab[n0 & (kTab - 1)], t1 = tab[n1 & (kTab - 1)];
+  wh = two(__uint_as_float(static_cast<uint32_t>(t0.x) + (n0 << 17)), __uint_as_float(static_cast<uint32_t>(t1.x) + (n1 << 17)));
+  f32x2 q = fma2(two(2.11731752e-7f, 2.11731752e-7f), r, two(5.86490495e-5f, 5.86490495e-5f));
+  q = fma2(q, r, two(1.08304247e-2f, 1.08304247e-2f));
+  wl = mul2(wh, fma2(q, r, two(__int_as_float(t0.y), __int_as_float(t1.y))));
+}
+
 // the same for any row: 0 below zmin and for NaN, +inf counts as the largest finite number
 __device__ __forceinline__ void weight_any(float x, const Scale& s, const float2* pow, float& wh, float& wl) {
   const float d = fminf(fmaxf(x, s.zmin), kFltMax) - s.zp;
@@ -210,16 +257,48 @@ __device__ __forceinline__ void make_table(const Scale& s, const float2* pow, in
 }
 
 // round(w 2^43) = A 2^22 + B, |B| <= 2^21 + 1: both as the bits of the rounded fp32 numbers, biased
-__device__ __forceinline__ void weight_parts(float wh, float wl, int& a, int& b) {
+__device__ __forceinline__ void weight_parts(float wh, float wl, uint32_t& a, uint32_t& b) {
   const float fa = fmaf(wh + wl, 2097152.f, kMagic);
   const float lo = fmaf(fa - kMagic, -1.f / 2097152.f, wh) + wl;
-  a = __float_as_int(fa);
-  b = __float_as_int(fmaf(lo, 8796093022208.f, kMagic));
+  a = __float_as_uint(fa);
+  b = __float_as_uint(fmaf(lo, 8796093022208.f, kMagic));
+}
+__device__ __forceinline__ uint64_t weight_of(uint32_t a, uint32_t b) {
+  constexpr uint64_t bias = static_cast<uint64_t>(kMagicBits) * 4194305ull;
+  return static_cast<uint64_t>(a) * 4194304ull + b - bias;
 }
 __device__ __forceinline__ uint64_t weight_int(float wh, float wl) {
-  int a, b;
+  uint32_t a, b;
   weight_parts(wh, wl, a, b);
-  return static_cast<uint64_t>(static_cast<int64_t>(a - kMagicBits) * 4194304 + (b - kMagicBits));
+  return weight_of(a, b);
+}
+
+// weight_parts of two
+__device__ __forceinline__ void weight_parts2(f32x2 wh, f32x2 wl, uint32_t* a, uint32_t* b) {
+  const f32x2 magic = two(kMagic, kMagic);
+  const f32x2 fa = fma2(add2(wh, wl), two(2097152.f, 2097152.f), magic);
+  const f32x2 lo = add2(fma2(add2(fa, two(-kMagic, -kMagic)), two(-1.f / 2097152.f, -1.f / 2097152.f), wh), wl);
+  const f32x2 fb = fma2(lo, two(8796093022208.f, 8796093022208.f), magic);
+  a[0] = static_cast<uint32_t>(fa);
+  a[1] = static_cast<uint32_t>(fa >> 32);
+  b[0] = static_cast<uint32_t>(fb);
+  b[1] = static_cast<uint32_t>(fb >> 32);
+}
+
+// weights of four neighbours
+__device__ __forceinline__ void weights4(const float (&x)[4], const Scale& s, const int2* tab, const float2* pow, f32x2 (&wh)[2], f32x2 (&wl)[2]) {
+  if (s.plain) {
+    weight_plain2(x[0], x[1], s, tab, wh[0], wl[0]);
+    weight_plain2(x[2], x[3], s, tab, wh[1], wl[1]);
+  } else {
+    float h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) weight_any(x[e], s, pow, h[e], l[e]);
+    wh[0] = two(h[0], h[1]);
+    wh[1] = two(h[2], h[3]);
+    wl[0] = two(l[0], l[1]);
+    wl[1] = two(l[2], l[3]);
+  }
 }
 
 // S * f for f in [0, 1), rounded down or up
@@ -242,14 +321,37 @@ __device__ __forceinline__ uint32_t cluster_nctas() {
   return n;
 }
 
+// vector v of the row that starts `off` elements behind `base`: what reaches beyond its V elements is -inf
 template <typename T>
+__device__ __noinline__ uint4 edge(const uint8_t* base, int off, int V, int v) {
+  constexpr int VE = 16 / sizeof(T);
+  const T* p = reinterpret_cast<const T*>(base) + static_cast<int64_t>(v) * VE;
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < VE; ++e) {
+    const int i = v * VE + e - off;
+    const bool ok = i >= 0 && i < V;
+    if constexpr (sizeof(T) == 4) {
+      w[e] = ok ? __float_as_uint(p[e]) : 0xff800000u;
+    } else {
+      const uint32_t h = ok ? p[e] : 0xff80u;
+      w[e >> 1] |= (e & 1) ? h << 16 : h;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// RES: all of the row's vectors are in shared memory
+template <typename T, bool RES>
 struct Row {
   static constexpr int VE = 16 / sizeof(T);
   const uint8_t* base;                     // 16-byte aligned, at or before the row's first element
   int off;                                 // elements between the two
   int V;
   uint4* data;                             // this CTA's vectors, [warp][nres]
-  int nres, v0, nw;                        // this warp's first vector and their number
+  const uint4* ends;                       // in shared memory, where vectors are read from L2
+  int nres, nvw, nvec;                     // vectors of a warp in shared memory, of a warp, of the row
+  int v0, nw;                              // this warp's first vector and their number
 
   __device__ __forceinline__ static float elem(const uint4& q, int e) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -257,29 +359,11 @@ struct Row {
     else return __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
   }
   __device__ __forceinline__ bool inside(int v) const { return v * VE - off >= 0 && (v + 1) * VE - off <= V; }
-  // the row's first and last vector may reach beyond it: what does is -inf
-  __device__ uint4 edge(int v) const {
-    const T* p = reinterpret_cast<const T*>(base) + static_cast<int64_t>(v) * VE;
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const int i = v * VE + e - off;
-      const bool ok = i >= 0 && i < V;
-      if constexpr (sizeof(T) == 4) {
-        w[e] = ok ? __float_as_uint(p[e]) : 0xff800000u;
-      } else {
-        const uint32_t h = ok ? p[e] : 0xff80u;
-        if (e & 1) w[e >> 1] |= h << 16; else w[e >> 1] = h;
-      }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  __device__ __forceinline__ uint4 global(int v) const {
-    return inside(v) ? __ldg(reinterpret_cast<const uint4*>(base) + v) : edge(v);
-  }
-  // vector k of warp `w`, whose first vector is `first`
+  // vector k of warp `w`, whose first vector is `first`; ends: the row's first and last vector
   __device__ __forceinline__ uint4 get(int w, int first, int k) const {
-    return k < nres ? data[w * nres + k] : global(first + k);
+    if (RES || k < nres) return data[w * nres + k];
+    const int v = first + k;
+    return inside(v) ? __ldg(reinterpret_cast<const uint4*>(base) + v) : ends[v == 0 ? 0 : 1];
   }
   // f(four neighbours as they stand in the row, the first one's index) for every four of this warp
   template <typename F>
@@ -346,19 +430,20 @@ __device__ __forceinline__ uint64_t cluster_sum(uint64_t v, Shared& sh, int ex, 
 
 template <int BINS>
 __device__ __forceinline__ void clear_bins(Shared& sh, int buf) {
-  for (int i = threadIdx.x; i < BINS; i += kThreads) sh.hist[buf][0][i] = sh.hist[buf][1][i] = sh.hist[buf][2][i] = 0u;
+  for (int i = threadIdx.x; i < BINS; i += kThreads) sh.hist[buf][0][i] = sh.hist[buf][1][i] = sh.hist[buf][2][i] = sh.hist[buf][3][i] = 0u;
   if (threadIdx.x == 0) sh.sel_bin = 0;
   __syncthreads();
 }
 
-// add one token to a bin: the 64-bit weight as two words, the carry by the value before
+// add one token to a bin: its weight in three parts, whose sums over a CTA's tokens (fewer than 2^16)
+// fit a word each, so that no addition has to wait for a carry; the last one is rare
 template <bool COUNT>
 __device__ __forceinline__ void add_to_bin(Shared& sh, int buf, int bin, uint64_t W) {
   if (COUNT) atomicAdd(&sh.hist[buf][0][bin], 1u);
-  const uint32_t l = static_cast<uint32_t>(W);
-  const uint32_t old = atomicAdd(&sh.hist[buf][1][bin], l);
-  const uint32_t h = static_cast<uint32_t>(W >> 32) + (old + l < old ? 1u : 0u);
-  if (h != 0) atomicAdd(&sh.hist[buf][2][bin], h);
+  const uint32_t l = static_cast<uint32_t>(W), h = static_cast<uint32_t>(W >> 32);
+  atomicAdd(&sh.hist[buf][1][bin], l & 0xffffu);
+  atomicAdd(&sh.hist[buf][2][bin], l >> 16);
+  if (h != 0) atomicAdd(&sh.hist[buf][3][bin], h);
 }
 
 // The last bin that is not empty and before which the target is not reached (n0, e0: what lies
@@ -371,8 +456,9 @@ __device__ int find_bin(Shared& sh, int buf, int C, uint64_t target, uint64_t& n
   for (int c = 0; c < C && 2 * tid < BINS; ++c) {
     const uint2 b = reinterpret_cast<const uint2*>(peer(sh.hist[buf][1], c))[tid];
     const uint2 d = reinterpret_cast<const uint2*>(peer(sh.hist[buf][2], c))[tid];
-    w[0] += (static_cast<uint64_t>(d.x) << 32) + b.x;
-    w[1] += (static_cast<uint64_t>(d.y) << 32) + b.y;
+    const uint2 g = reinterpret_cast<const uint2*>(peer(sh.hist[buf][3], c))[tid];
+    w[0] += (static_cast<uint64_t>(g.x) << 32) + (static_cast<uint64_t>(d.x) << 16) + b.x;
+    w[1] += (static_cast<uint64_t>(g.y) << 32) + (static_cast<uint64_t>(d.y) << 16) + b.y;
     if (COUNT) {
       const uint2 a = reinterpret_cast<const uint2*>(peer(sh.hist[buf][0], c))[tid];
       n[0] += a.x;
@@ -389,11 +475,11 @@ __device__ int find_bin(Shared& sh, int buf, int C, uint64_t target, uint64_t& n
   __syncthreads();
   const int bin = static_cast<int>(sh.sel_bin);
   if (bin >> 1 == tid) {
-    const int j = bin & 1;
-    sh.sel_e = ee[j];
-    sh.sel_incl = ee[j] + w[j];
-    sh.sel_n = static_cast<uint32_t>(nn[j]);
-    sh.sel_cnt = static_cast<uint32_t>(n[j]);
+    const bool odd = bin & 1;
+    sh.sel_e = odd ? ee[1] : ee[0];
+    sh.sel_incl = odd ? ee[1] + w[1] : ee[1];
+    sh.sel_n = static_cast<uint32_t>(odd ? nn[1] : nn[0]);
+    sh.sel_cnt = static_cast<uint32_t>(odd ? n[1] : n[0]);
   }
   __syncthreads();
   n0 = sh.sel_n;
@@ -407,21 +493,40 @@ __device__ __forceinline__ uint64_t comp_of(float z, int i, uint32_t kmax) {
   return (static_cast<uint64_t>(kmax - okey(z + 0.f)) << kIdxBits) + static_cast<uint32_t>(i);
 }
 
+// Tokens near a border: those x >= cut (`per` == 0), or those of one bin of values of them. `maybe` is
+// true for all of them and few others, in two instructions.
+struct Pick {
+  float cut, top, per, mid, half;
+  int bin;
+  __device__ __forceinline__ int bin_of(float x) const { return __float_as_int(fmaf(top - fminf(x, kFltMax), per, kMagic)) - kMagicBits; }
+  __device__ __forceinline__ bool maybe(float x) const { return fabsf(x - mid) <= half; }
+  __device__ __forceinline__ bool operator()(float x) const { return x >= cut && (per == 0.f || bin_of(x) == bin); }
+};
+
 // The bound of comp below which the tokens stay, COUNT: the first `target` of them, else those before
-// which the weight is below `target` (> 0). Looked at: the tokens that f picks, before which lies the
-// weight e0. Returns the bound and the weight of those that stay. One level for each 10 bits of comp.
-// (Arguments by value: their addresses would keep the caller's in local memory.)
-template <bool COUNT, typename T, typename F>
-__device__ __noinline__ ulonglong2 select(Row<T> row, Scale sc, uint64_t target, uint64_t e0, Shared& sh, int C, F f) {
+// which the weight is below `target` (> 0). Looked at: the tokens of `pick`, before which lies the
+// weight e0. Returns the bound and the weight of those that stay. One level for each 9 bits of comp.
+// The way for rows whose border has more tokens than a list holds. (Out of line, what it needs of
+// the caller in shared memory: the caller's registers stay its own.)
+template <bool COUNT, typename T, bool RES>
+__device__ __noinline__ ulonglong2 select(const Row<T, RES>* shared_row, const Scale* shared_scale, const Pick* shared_pick, uint64_t target,
+                                          uint64_t e0, Shared& sh, int C) {
   uint64_t n0 = 0, count, lo = 0, kept;
   int buf = 0, width = 32 + kIdxBits;
   cluster_sync();                          // another CTA may still read the bins or the list of before
+  Row<T, RES> row = *shared_row;
+  const int wid = threadIdx.x >> 5;
+  row.v0 += wid * row.nvw;                 // the row there is that of the first warp
+  row.nw = max(0, min(row.nvw, row.nvec - row.v0));
+  const Scale sc = *shared_scale;
+  const Pick pick = *shared_pick;
   for (;;) {
     const int shift = max(0, width - kBinBits);
     clear_bins<kBins>(sh, buf);
     row.each([&](const float (&x)[4], int i) {
+#pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (!f(x[e])) continue;
+        if (!pick(x[e])) continue;
         const uint64_t at = comp_of(fminf(x[e], kFltMax), i + e, sc.kmax) - lo;       // wraps to a large number below lo
         if (at >> width != 0) continue;
         float wh, wl;
@@ -438,40 +543,40 @@ __device__ __noinline__ ulonglong2 select(Row<T> row, Scale sc, uint64_t target,
   }
 }
 
-// sort the first P (a power of two, 32 <= P <= kMerged) of sh.sort ascending
 __device__ __forceinline__ uint64_t exchange(uint64_t v, int i, int k, int d) {
   const uint64_t o = __shfl_xor_sync(0xffffffffu, v, d);
   return (((i & k) == 0) == ((i & d) == 0)) == (o < v) ? o : v;
 }
-__device__ void sort_merged(Shared& sh, int P) {
+// sort the first P (a power of two, 32 <= P <= kMerged) entries of `list` ascending, in place
+__device__ void sort_list(uint64_t* list, int P) {
   const int tid = threadIdx.x;
   for (int i = tid; i < P; i += kThreads) {
-    uint64_t v = sh.sort[i];
+    uint64_t v = list[i];
 #pragma unroll
     for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
       for (int d = k >> 1; d > 0; d >>= 1) v = exchange(v, i, k, d);
-    sh.sort[i] = v;
+    list[i] = v;
   }
   __syncthreads();
   for (int k = 64; k <= P; k <<= 1) {
     for (int j = k >> 1; j >= 32; j >>= 1) {
       for (int t = tid; t < P / 2; t += kThreads) {
         const int i = ((t & ~(j - 1)) << 1) | (t & (j - 1));
-        const uint64_t a = sh.sort[i], b = sh.sort[i + j];
+        const uint64_t a = list[i], b = list[i + j];
         if (((i & k) == 0) == (b < a)) {
-          sh.sort[i] = b;
-          sh.sort[i + j] = a;
+          list[i] = b;
+          list[i + j] = a;
         }
       }
       __syncthreads();
     }
     // the rest of this merge stays within 32 neighbours
     for (int i = tid; i < P; i += kThreads) {
-      uint64_t v = sh.sort[i];
+      uint64_t v = list[i];
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) v = exchange(v, i, k, d);
-      sh.sort[i] = v;
+      list[i] = v;
     }
     __syncthreads();
   }
@@ -483,17 +588,75 @@ __device__ __forceinline__ int padded(int n) {
   return P;
 }
 
-// The tokens f picks, as comp, of all CTAs in sh.sort, sorted; returns their number, or -1 where they are
-// too many. Every CTA gets the same.
-template <typename T, typename F>
-__device__ __forceinline__ int gather(const Row<T>& row, const Scale& sc, Shared& sh, int C, F f) {
+// sh.m.order from the n entries of sh.m.list: each goes to one of 512 buckets by its value, and in there
+// to the place that the number of smaller ones gives it. Rows whose values crowd into one bucket
+// (ties) are sorted instead. bucket, kd_min and kd_max are set, `fullest` is 0.
+__device__ __forceinline__ void order_list(Shared& sh, const Scale& sc, int n) {
+  const int tid = threadIdx.x;
+  const float top = okey_value(sc.kmax - sh.kd_min), range = top - okey_value(sc.kmax - sh.kd_max);
+  const float per = range > 0.f ? fminf(__fdividef(kThreads - 2.f, range), kFltMax) : 0.f;
+  uint32_t at[kMerged / kThreads];         // bucket, and place in it above 16 bits
+#pragma unroll
+  for (int e = 0; e < kMerged / kThreads; ++e) {
+    const int j = tid + e * kThreads;
+    if (j < n) {
+      const float z = okey_value(sc.kmax - static_cast<uint32_t>(sh.m.list[j] >> kIdxBits));
+      const int b = min(__float_as_int(fmaf(top - z, per, kMagic)) - kMagicBits, kThreads - 1);
+      at[e] = static_cast<uint32_t>(b) | atomicAdd(&sh.m.bucket[b], 1u) << 16;
+    }
+  }
+  __syncthreads();
+  const uint32_t own = sh.m.bucket[tid];
+  const uint32_t most = __reduce_max_sync(0xffffffffu, own);
+  if ((tid & 31) == 0) atomicMax(&sh.fullest, most);
+  uint64_t total;
+  const uint32_t first = static_cast<uint32_t>(block_scan(own, sh.part, &total));
+  if (sh.fullest > kCrowd) {
+    const int P = padded(n);
+    for (int j = n + tid; j < P; j += kThreads) sh.m.list[j] = kAll;
+    __syncthreads();
+    sort_list(sh.m.list, P);
+    for (int j = tid; j < n; j += kThreads) sh.m.order[j] = static_cast<uint16_t>(j);
+    __syncthreads();
+    return;
+  }
+  sh.m.bucket[tid] = first;
+  if (tid == 0) sh.m.bucket[kThreads] = static_cast<uint32_t>(n);
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kMerged / kThreads; ++e) {
+    const int j = tid + e * kThreads;
+    if (j < n) sh.m.slot[sh.m.bucket[at[e] & 0xffff] + (at[e] >> 16)] = static_cast<uint16_t>(j);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kMerged / kThreads; ++e) {
+    const int j = tid + e * kThreads;
+    if (j < n) {
+      const uint32_t b = at[e] & 0xffff, b0 = sh.m.bucket[b], b1 = sh.m.bucket[b + 1];
+      const uint64_t v = sh.m.list[j];
+      uint32_t place = b0;
+      for (uint32_t i = b0; i < b1; ++i) place += sh.m.list[sh.m.slot[i]] < v ? 1 : 0;
+      sh.m.order[place] = static_cast<uint16_t>(j);
+    }
+  }
+  __syncthreads();
+}
+
+// The tokens of `pick`, as comp, of all CTAs in sh.m.list, ordered; returns their number, or -1 where they
+// are too many. Every CTA gets the same.
+template <typename R>
+__device__ __forceinline__ int gather(const R& row, const Scale& sc, Shared& sh, int C, const Pick& pick) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  if (tid == 0) {
+    sh.kd_min = ~0u;
+    sh.kd_max = sh.fullest = 0;
+  }
   row.each([&](const float (&x)[4], int i) {
-    const bool b[4] = {f(x[0]), f(x[1]), f(x[2]), f(x[3])};
-    if (!(b[0] || b[1] || b[2] || b[3])) return;
+    if (!(pick.maybe(x[0]) || pick.maybe(x[1]) || pick.maybe(x[2]) || pick.maybe(x[3]))) return;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (b[e]) {
+      if (pick(x[e])) {
         const uint32_t at = atomicAdd(&sh.list_n, 1u);
         if (at < kList) sh.list[at] = comp_of(fminf(x[e], kFltMax), i + e, sc.kmax);
       }
@@ -510,18 +673,29 @@ __device__ __forceinline__ int gather(const Row<T>& row, const Scale& sc, Shared
   }
   if (!fits || n > kMerged) return -1;
   k = __shfl_sync(0xffffffffu, k, wid & (kMaxCluster - 1));
+  sh.m.bucket[tid] = 0;
   if (wid < C) {
     const uint64_t* from = peer(sh.list, wid);
-    for (uint32_t i = lane; i < k; i += 32) sh.sort[before + i] = from[i];
-  } else if (wid == kWarps - 1) {
-    for (int i = static_cast<int>(n) + lane, P = padded(static_cast<int>(n)); i < P; i += 32) sh.sort[i] = kAll;
+    uint32_t lo = ~0u, hi = 0;
+    for (uint32_t i = lane; i < k; i += 32) {
+      const uint64_t v = from[i];
+      sh.m.list[before + i] = v;
+      lo = min(lo, static_cast<uint32_t>(v >> kIdxBits));
+      hi = max(hi, static_cast<uint32_t>(v >> kIdxBits));
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      atomicMin(&sh.kd_min, lo);
+      atomicMax(&sh.kd_max, hi);
+    }
   }
   __syncthreads();
-  sort_merged(sh, padded(static_cast<int>(n)));
+  order_list(sh, sc, static_cast<int>(n));
   return static_cast<int>(n);
 }
 
-// Of the n sorted tokens in sh.sort, before which lies the weight e0: those that stay, in their order,
+// Of the n ordered tokens in sh.m, before which lies the weight e0: those that stay, in their order,
 // under `k` tokens, the sum before a token below ceil(top_p * sum of the first k) (or below
 // `target`, where that is > 0) and min-p. *kept: e0 and their weight. At least one stays.
 __device__ int cut_sorted(Shared& sh, const Scale& sc, int n, uint64_t e0, int k, float top_p, uint64_t target, float min_p, uint64_t* kept) {
@@ -536,7 +710,7 @@ __device__ int cut_sorted(Shared& sh, const Scale& sc, int n, uint64_t e0, int k
     W[e] = 0;
     mp[e] = true;
     if (e < per && j < n) {
-      const float z = okey_value(sc.kmax - static_cast<uint32_t>(sh.sort[j] >> kIdxBits));
+      const float z = okey_value(sc.kmax - static_cast<uint32_t>(sh.m.list[sh.m.order[j]] >> kIdxBits));
       float wh, wl;
       weight(z, sc, sh.tab, sh.pow, wh, wl);
       W[e] = weight_int(wh, wl);
@@ -557,19 +731,34 @@ __device__ int cut_sorted(Shared& sh, const Scale& sc, int n, uint64_t e0, int k
     }
     b += W[e];
   }
-  block_scan(static_cast<uint64_t>(stay), sh.part2, &total);
-  const int m = static_cast<int>(total);
-  block_scan(mine, sh.part, &total);
-  *kept = e0 + total;
+  mine = warp_sum(mine);
+  stay = __reduce_add_sync(0xffffffffu, stay);
+  if ((tid & 31) == 0) {
+    sh.part2[tid >> 5] = mine;
+    sh.wkey[tid >> 5] = static_cast<uint32_t>(stay);
+  }
+  __syncthreads();
+  uint64_t sum = 0;
+  int m = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    sum += sh.part2[w];
+    m += static_cast<int>(sh.wkey[w]);
+  }
+  *kept = e0 + sum;
   return m;
 }
 
 // grid (rows * C), clusters of C CTAs: one row each
-template <typename T>
+template <typename T, bool RES>
 __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
-  constexpr int VE = Row<T>::VE;
+  using R = Row<T, RES>;
+  constexpr int VE = R::VE;
+  __shared__ R shared_row;
+  __shared__ Scale shared_scale;
+  __shared__ Pick shared_pick;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int C = static_cast<int>(cluster_nctas());
   const int rank = static_cast<int>(cluster_rank());
@@ -583,15 +772,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
     if (t >= 0 && t % p.Dmax >= __ldg(p.blk_len + b * p.NB + t / p.Dmax)) return;
   }
   const uint8_t* start = static_cast<const uint8_t*>(p.logits) + r * p.row_bytes;
-  Row<T> row;
+  R row;
   row.off = static_cast<int>((reinterpret_cast<uintptr_t>(start) & 15) / sizeof(T));
   row.base = start - row.off * sizeof(T);
   row.V = p.V;
   row.nres = p.nres;
   row.data = reinterpret_cast<uint4*>(smem);
+  row.ends = sh.ends;
   const int nvec = (row.off + p.V + VE - 1) / VE;
   row.v0 = (rank * kWarps + wid) * p.nvw;
   row.nw = max(0, min(p.nvw, nvec - row.v0));
+  row.nvw = p.nvw;
+  row.nvec = nvec;
 
   // every vector of this thread is on its way at once
   for (int k = lane; k < min(row.nw, row.nres); k += 32) {
@@ -602,8 +794,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
                    "l"(reinterpret_cast<const uint4*>(row.base) + v)
                    : "memory");
     else
-      *dst = row.edge(v);
+      *dst = edge<T>(row.base, row.off, p.V, v);
   }
+  if (!RES && tid < 2) sh.ends[tid] = edge<T>(row.base, row.off, p.V, tid == 0 ? 0 : nvec - 1);
   if (tid < kTab) sh.pow[tid] = kPowers.v[tid];
   float temp = p.temperature != nullptr ? __ldg(p.temperature + set) : 1.f;
   int64_t k = p.top_k != nullptr ? __ldg(p.top_k + set) : 0;
@@ -628,6 +821,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
   const int share_w = static_cast<int>((k + warps - 1) / warps), share = static_cast<int>((k + ctas - 1) / ctas);
   if (tid == 0) sh.list_n = 0;
   asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!RES) __syncthreads();               // the ends
 
   // ---- the row's largest value; with top-k also a value that k tokens at least reach
   float mx = -INFINITY;
@@ -694,6 +888,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
   const bool empty = !(zmax > -INFINITY);
   const Scale sc = make_scale(fminf(zmax, kFltMax), rate, zmax == INFINITY);
   make_table(sc, sh.pow, sh.tab);
+  if (tid == 0) {
+    shared_row = row;
+    shared_scale = sc;
+  }
   __syncthreads();
 
   uint64_t bound = kAll, S = 0, before = 0, mine = 0;
@@ -702,14 +900,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
   if (!empty) {
     if (k > 0) {
       const float low = reach > okey(-INFINITY) ? okey_value(reach) : -kFltMax;
-      const int n = gather(row, sc, sh, C, [low](float x) { return x >= low; });
+      // from low to zmax, a little wider
+      const float span = 0.5f * (sc.zmax - low);
+      const Pick pick = {low, 0.f, 0.f, low + span, sc.plain ? fmaf(fabsf(sc.zmax) + fabsf(low), 1e-6f, span) + 1.17549435e-38f : INFINITY, 0};
+      const int n = gather(row, sc, sh, C, pick);
       if (n >= 0) {
         const int m = cut_sorted(sh, sc, n, 0, static_cast<int>(k), top_p, 0, min_p, &S);
-        bound = sh.sort[m - 1] + 1;
+        bound = sh.m.list[sh.m.order[m - 1]] + 1;
         stays = m;
         all_cut = true;
       } else {
-        const ulonglong2 got = select<true>(row, sc, static_cast<uint64_t>(k), 0, sh, C, [low](float x) { return x >= low; });
+        if (tid == 0) shared_pick = pick;
+        const ulonglong2 got = select<true>(&shared_row, &shared_scale, &shared_pick, static_cast<uint64_t>(k), 0, sh, C);
         bound = got.x;
         S = got.y;
       }
@@ -720,65 +922,53 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
       // (the sum is at least 1); binned by their value are the others, and all are summed
       const float z_cut = fmaxf(__fadd_rd(sc.zmax, -depth), sc.zmin), range = sc.zmax - z_cut;
       const float per = range > 0.f ? __fdiv_rd(kLin - 2.f, range) : 0.f;
-      const float per_bin = per < kFltMax ? per : 0.f;
-      // rounded, but never falls as x does
-      const float top = sc.zmax;
-      auto bin_of = [top, per_bin](float x) { return __float_as_int(fmaf(top - fminf(x, kFltMax), per_bin, kMagic)) - kMagicBits; };
+      // bins of values: rounded, but never falling as the value falls
+      Pick pick = {z_cut, sc.zmax, per < kFltMax ? per : 0.f, 0.f, INFINITY, 0};
       if (known) {                         // another CTA may still read the bins or the list of before
         cluster_sync();
         if (tid == 0) sh.list_n = 0;
       }
       clear_bins<kLin>(sh, 0);
       uint32_t sa = 0, sb = 0, count = 0;
-      auto add = [&](const float (&x)[4], const float (&wh)[4], const float (&wl)[4]) {
-        int a[4], b[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          weight_parts(wh[e], wl[e], a[e], b[e]);
-          sa += static_cast<uint32_t>(a[e]);
-          sb += static_cast<uint32_t>(b[e]);
-        }
+      row.each([&](const float (&x)[4], int) {
+        uint32_t a[4], b[4];
+        f32x2 wh[2], wl[2];
+        weights4(x, sc, sh.tab, sh.pow, wh, wl);
+        weight_parts2(wh[0], wl[0], a, b);
+        weight_parts2(wh[1], wl[1], a + 2, b + 2);
+        sa += (a[0] + a[1]) + (a[2] + a[3]);
+        sb += (b[0] + b[1]) + (b[2] + b[3]);
         count += 4;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (x[e] >= z_cut)
-            add_to_bin<false>(sh, 0, bin_of(x[e]), static_cast<uint64_t>(static_cast<int64_t>(a[e] - kMagicBits) * 4194304 + (b[e] - kMagicBits)));
-      };
-      if (sc.plain) {
-        row.each([&](const float (&x)[4], int) {
-          float wh[4], wl[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) weight_plain(x[e], sc, sh.tab, wh[e], wl[e]);
-          add(x, wh, wl);
-        });
-      } else {
-        row.each([&](const float (&x)[4], int) {
-          float wh[4], wl[4];
-          for (int e = 0; e < 4; ++e) weight_any(x[e], sc, sh.pow, wh[e], wl[e]);
-          add(x, wh, wl);
-        });
-      }
+          if (x[e] >= z_cut) add_to_bin<false>(sh, 0, pick.bin_of(x[e]), weight_of(a[e], b[e]));
+      });
       // the biases go out modulo 2^32: a thread holds at most 512 tokens, so the sums fit
       sa -= count * kMagicBits;
       sb -= count * kMagicBits;
       const uint64_t sum = cluster_sum(static_cast<uint64_t>(static_cast<int64_t>(static_cast<int>(sa)) * 4194304 + static_cast<int>(sb)), sh, 0, rank, C, &before, &mine);
       const uint64_t target = max(mul_fraction(known ? S : sum, fmaxf(top_p, 0.f), true), uint64_t{1});
       uint64_t n0 = 0, e0 = 0, incl, cnt;
-      const int bin = find_bin<false, kLin>(sh, 0, C, target, n0, e0, &incl, &cnt);
-      auto border = [z_cut, bin, bin_of](float x) { return x >= z_cut && bin_of(x) == bin; };
-      const int n = gather(row, sc, sh, C, border);
+      pick.bin = find_bin<false, kLin>(sh, 0, C, target, n0, e0, &incl, &cnt);
+      if (sc.plain) {
+        const float width = range * (1.f / (kLin - 2));
+        pick.mid = fmaf(-width, static_cast<float>(pick.bin), sc.zmax);
+        pick.half = fmaf(fabsf(sc.zmax) + range, 1e-6f, 0.501f * width) + 1.17549435e-38f;
+      }
+      const int n = gather(row, sc, sh, C, pick);
       if (n >= 0) {
         const int m = cut_sorted(sh, sc, n, e0, n, 1.f, target, 0.f, &S);
-        bound = sh.sort[m - 1] + 1;
+        bound = sh.m.list[sh.m.order[m - 1]] + 1;
       } else {
-        const ulonglong2 got = select<false>(row, sc, target, e0, sh, C, border);
+        if (tid == 0) shared_pick = pick;
+        const ulonglong2 got = select<false>(&shared_row, &shared_scale, &shared_pick, target, e0, sh, C);
         bound = got.x;
         S = got.y;
       }
       known = true;
     }
   }
-  // kept: z > zt, or z == zt and index < it
+  // kept: z > zt, or z == zt and index < it; none below zmin
   float zt = -INFINITY;
   int it = 0;
   if (bound != kAll) {
@@ -791,41 +981,55 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
       zt = okey_value(key) + 0.f;
     }
   }
+  if (zt < sc.zmin) {
+    zt = sc.zmin;
+    it = p.V;
+  }
   const bool use_min_p = min_p > 0.f && !all_cut;
-  // of four neighbours the weights of those that stay, 0 for the others (NaN among them); false where none does
-  auto kept_weights = [&](const float (&x)[4], int i, float (&wh)[4], float (&wl)[4]) {
-    bool stay[4];
+  // the weights of four neighbours and which of them stay; false where none does
+  auto kept_weights = [&](const float (&x)[4], int i, f32x2 (&wh)[2], f32x2 (&wl)[2], bool (&stay)[4]) {
+    if (!(x[0] >= zt || x[1] >= zt || x[2] >= zt || x[3] >= zt)) return false;
+    weights4(x, sc, sh.tab, sh.pow, wh, wl);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float z = fminf(x[e], kFltMax);
-      stay[e] = (z > zt || (z == zt && i + e < it)) && x[e] >= sc.zmin;
-      wh[e] = wl[e] = 0.f;
+    for (int e = 0; e < 4; ++e) stay[e] = x[e] > zt;
+    if (x[0] == zt || x[1] == zt || x[2] == zt || x[3] == zt || !sc.plain) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) stay[e] = x[e] >= zt && (fminf(x[e], kFltMax) > zt || i + e < it);
     }
-    if (!(stay[0] || stay[1] || stay[2] || stay[3])) return false;
-    if (sc.plain) {
+    if (use_min_p) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) weight_plain(x[e], sc, sh.tab, wh[e], wl[e]);
-    } else {
-      for (int e = 0; e < 4; ++e) weight_any(x[e], sc, sh.pow, wh[e], wl[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (use_min_p) stay[e] = stay[e] && (x[e] >= sc.zmax || (wh[e] - min_p) + wl[e] >= 0.f);
-      if (!stay[e]) wh[e] = wl[e] = 0.f;
+      for (int e = 0; e < 4; ++e) {
+        float h[2], l[2];
+        apart(wh[e >> 1], h[0], h[1]);
+        apart(wl[e >> 1], l[0], l[1]);
+        stay[e] = stay[e] && (x[e] >= sc.zmax || (h[e & 1] - min_p) + l[e & 1] >= 0.f);
+      }
     }
     return true;
   };
+  // as integers, 0 for those that do not stay
+  auto kept_ints = [&](const float (&x)[4], int i, uint64_t (&W)[4]) {
+    f32x2 wh[2], wl[2];
+    bool stay[4];
+    W[0] = W[1] = W[2] = W[3] = 0;
+    if (!kept_weights(x, i, wh, wl, stay)) return;
+    uint32_t a[4], b[4];
+    weight_parts2(wh[0], wl[0], a, b);
+    weight_parts2(wh[1], wl[1], a + 2, b + 2);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (stay[e]) W[e] = weight_of(a[e], b[e]);
+  };
 
   // a few tokens that stay, known in their order: drawn from there, by the first CTA
-  const bool from_list = all_cut && stays <= kThreads;
+  const bool from_list = all_cut && stays <= kFew;
   const bool draw = p.token != nullptr && !empty;
   if (!empty && (use_min_p || !known || (draw && !from_list))) {
     uint64_t t = 0;
     row.each([&](const float (&x)[4], int i) {
-      float wh[4], wl[4];
-      if (kept_weights(x, i, wh, wl))
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t += weight_int(wh[e], wl[e]);
+      uint64_t W[4];
+      kept_ints(x, i, W);
+      t += (W[0] + W[1]) + (W[2] + W[3]);
     });
     S = cluster_sum(t, sh, 1, rank, C, &before, &mine);
   }
@@ -837,17 +1041,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
     ih = __fdiv_rn(8796093022208.f, s_h);
     il = __fdiv_rn(fmaf(-ih, s_l, fmaf(-ih, s_h, 8796093022208.f)), s_h);
   }
-  auto probability = [&](float wh, float wl) { return fmaf(wh, ih, fmaf(wh, il, wl * ih)); };
+  auto probability = [&](float wh, float wl) { return fmaf(wh, ih, fmaf(wh, il, __fmul_rn(wl, ih))); };
 
   if (p.probs != nullptr) {
     float* out = p.probs + r * p.V;
     const bool wide = ((reinterpret_cast<uintptr_t>(out) / 4 - row.off) & 3) == 0;
     if (wide) {
       row.each([&](const float (&x)[4], int i) {
-        float wh[4], wl[4], v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (kept_weights(x, i, wh, wl))
+        f32x2 wh[2], wl[2];
+        bool stay[4];
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (kept_weights(x, i, wh, wl, stay)) {
+          const f32x2 h = two(ih, ih), l = two(il, il);
+          apart(fma2(wh[0], h, fma2(wh[0], l, mul2(wl[0], h))), v[0], v[1]);
+          apart(fma2(wh[1], h, fma2(wh[1], l, mul2(wl[1], h))), v[2], v[3]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = probability(wh[e], wl[e]);
+          for (int e = 0; e < 4; ++e) v[e] = stay[e] ? v[e] : 0.f;
+        }
         if (i >= 0 && i + 4 <= p.V && in_range(i + 3, p.V, p.hdr, 510)) {
           *reinterpret_cast<float4*>(out + i) = make_float4(v[0], v[1], v[2], v[3]);
         } else {
@@ -863,13 +1073,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
         const int i = i0 + j;
         if (i < 0 || i >= p.V || !in_range(i, p.V, p.hdr, 511)) continue;
         const int kv = j / VE;
-        const T* src = kv < row.nres ? reinterpret_cast<const T*>(row.data + wid * row.nres) + j
+        const T* src = RES || kv < row.nres ? reinterpret_cast<const T*>(row.data + wid * row.nres) + j
                                      : reinterpret_cast<const T*>(row.base) + static_cast<int64_t>(row.v0) * VE + j;
         float x;
         if constexpr (sizeof(T) == 4) x = *src; else x = bf16_to_f32(*src);
         const float z = fminf(x, kFltMax);
         float v = 0.f;
-        if ((z > zt || (z == zt && i < it)) && x >= sc.zmin) {
+        if (x >= zt && (z > zt || i < it)) {
           float wh, wl;
           weight(x, sc, sh.tab, sh.pow, wh, wl);
           if (!use_min_p || x >= sc.zmax || (wh - min_p) + wl >= 0.f) v = probability(wh, wl);
@@ -897,17 +1107,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
         const int P = padded(stays);
         uint64_t own = kAll;
         if (tid < stays) {
-          const uint64_t comp = sh.sort[tid];
+          const uint64_t comp = sh.m.list[sh.m.order[tid]];
           float wh, wl;
           weight(okey_value(sc.kmax - static_cast<uint32_t>(comp >> kIdxBits)), sc, sh.tab, sh.pow, wh, wl);
           own = (comp & ((1u << kIdxBits) - 1)) << 44 | weight_int(wh, wl);
         }
-        const uint64_t comp = tid < stays ? sh.sort[tid] : 0;
+        const uint64_t comp = tid < stays ? sh.m.list[sh.m.order[tid]] : 0;
         __syncthreads();
-        if (tid < P) sh.sort[tid] = own;
+        if (tid < P) sh.m.list[tid] = own;
         __syncthreads();
-        sort_merged(sh, P);
-        const uint64_t at = tid < stays ? sh.sort[tid] : 0, W = at & ((1ull << 44) - 1);
+        sort_list(sh.m.list, P);
+        const uint64_t at = tid < stays ? sh.m.list[tid] : 0, W = at & ((1ull << 44) - 1);
         uint64_t all;
         const uint64_t pre = block_scan(W, sh.part, &all);
         if (thr >= pre && thr < pre + W) sh.sel_bin = static_cast<uint32_t>(at >> 44);
@@ -929,21 +1139,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
         const int g = k0 + tid;
         const int i = first * VE - row.off + 4 * g;
         uint64_t W[4] = {0, 0, 0, 0}, all;
-        float wh[4], wl[4];
+        float x[4];
         if (g < groups) {
           const uint4 q = row.get(w, first, g / (VE / 4));
           const int e0 = g % (VE / 4) * 4;
-          float x[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = e0 == 0 ? Row<T>::elem(q, e) : Row<T>::elem(q, (e + 4) % VE);
-          if (kept_weights(x, i, wh, wl))
-#pragma unroll
-            for (int e = 0; e < 4; ++e) W[e] = weight_int(wh[e], wl[e]);
+          for (int e = 0; e < 4; ++e) x[e] = e0 == 0 ? R::elem(q, e) : R::elem(q, (e + 4) % VE);
+          kept_ints(x, i, W);
         }
         uint64_t pre = c0 + block_scan(W[0] + W[1] + W[2] + W[3], sh.part, &all);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (thr >= pre && thr < pre + W[e]) found(i + e, wh[e], wl[e]);
+          if (thr >= pre && thr < pre + W[e]) {
+            float wh, wl;
+            weight(x[e], sc, sh.tab, sh.pow, wh, wl);
+            found(i + e, wh, wl);
+          }
           pre += W[e];
         }
         c0 += all;
@@ -954,27 +1165,76 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
+constexpr int kMaxData = 160 * 1024;       // a CTA's part of a row in shared memory, at most
+
+template <typename T>
+static void shape(int nvec, int C, Params& p) {
+  p.nvw = (nvec + kWarps * C - 1) / (kWarps * C);
+  p.nres = std::min(p.nvw, kMaxData / 16 / kWarps);
+}
+
+// CTAs of a row and clusters that run at once, for a row of nvec vectors: asked once for each C and
+// 4 KB step of shared memory
+template <typename T>
+static int active_clusters(int dev, int C, size_t bytes) {
+  static std::mutex mu;
+  static int16_t known[kMaxDevices][kMaxCluster + 1][kMaxData / 4096 + 1];
+  const int step = static_cast<int>((bytes + 4095) / 4096);
+  std::lock_guard<std::mutex> lock(mu);
+  int16_t& n = known[dev][C][step];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(C));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(step) * 4096;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int got = 0;
+    if (cudaOccupancyMaxActiveClusters(&got, k_sample<T, true>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      got = 0;
+    }
+    n = static_cast<int16_t>(got > 0 ? std::min(got, 32000) : -1);
+  }
+  return n;
+}
+
 template <typename T>
 static int launch(const Params& in, int64_t rows, cudaStream_t s) {
-  constexpr int VE = Row<T>::VE;
+  constexpr int VE = Row<T, true>::VE;
   static std::once_flag once[kMaxDevices];
   static cudaError_t err[kMaxDevices];
-  static int sms[kMaxDevices];
-  constexpr int kMaxData = 160 * 1024;
   const int dev = current_device();
   if (dev < 0) return SSD_ERR_CUDA;
   std::call_once(once[dev], [dev] {
-    err[dev] = cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxData);
-    if (err[dev] == cudaSuccess) err[dev] = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
+    err[dev] = cudaFuncSetAttribute(k_sample<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxData);
+    if (err[dev] == cudaSuccess) err[dev] = cudaFuncSetAttribute(k_sample<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxData);
   });
   if (err[dev] != cudaSuccess) return SSD_ERR_CUDA;
   Params p = in;
   const int nvec = (p.V + 2 * VE - 2) / VE;                  // at most, whatever the row's first element's place
-  int C = 1;
-  while (C < kMaxCluster && (16LL * nvec / C > 78 * 1024 || (rows * C * 2 <= 2LL * sms[dev] && nvec / C > 4 * kThreads))) C *= 2;
-  const int per = kWarps * C;
-  p.nvw = (nvec + per - 1) / per;
-  p.nres = std::min(p.nvw, kMaxData / 16 / kWarps);
+  // CTAs a row: the least of (waves of clusters) x (a fixed part, the cluster's barriers, and the CTA's
+  // share of the row), both in tokens: 512 threads pass over 12500 of them in the fixed part's time
+  int C = 0;
+  double least = 0.;
+  for (int c = 1; c <= kMaxCluster; ++c) {
+    shape<T>(nvec, c, p);
+    const int active = active_clusters<T>(dev, c, static_cast<size_t>(p.nres) * kWarps * 16);
+    if (active < 1) continue;
+    double part = static_cast<double>(p.nvw) * kWarps * VE;
+    if (p.nvw > p.nres) part += 2. * (p.nvw - p.nres) * kWarps * VE;      // read again from L2 by every pass
+    const double cost = static_cast<double>((rows + active - 1) / active) * (12500. + part);
+    if (C == 0 || cost < least) {
+      C = c;
+      least = cost;
+    }
+  }
+  if (C == 0) return SSD_ERR_CUDA;
+  shape<T>(nvec, C, p);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
   cfg.blockDim = dim3(kThreads);
@@ -991,7 +1251,7 @@ static int launch(const Params& in, int64_t rows, cudaStream_t s) {
   cfg.numAttrs = 2;
   {
     KernelTimer timer(SSD_KERNEL_SAMPLE, s);
-    if (cudaLaunchKernelEx(&cfg, k_sample<T>, p) != cudaSuccess) return SSD_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, p.nvw <= p.nres ? k_sample<T, true> : k_sample<T, false>, p) != cudaSuccess) return SSD_ERR_CUDA;
   }
   count_launch();
   return check_launch();
