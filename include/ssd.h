@@ -640,6 +640,64 @@ size_t ssd_lowrank_head_workspace_size(const ssd_head_args* a);
 int ssd_lowrank_head(const ssd_head_args* a, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * ssd_verify_attn_shared — ssd_verify_attn for a batch whose sequences share a prompt.
+ *
+ * Sampled continuations of one prompt (or requests behind one system prompt) have their first
+ * keys in common. For each present token (slot t of block k of sequence b, as for
+ * ssd_verify_attn) and q-head:
+ *   out = sum_j softmax_j(scale * q.k_j) v_j over the shared keys 0 .. shared_len - 1, the
+ *         sequence's own keys 0 .. prefix_len[b] - 1 behind them, and the slots k*Dmax .. t
+ * The shared keys are read once for the whole batch (their products have the tokens of all
+ * sequences as rows) instead of once a sequence. Rows of absent tokens are not written.
+ * Layouts (elements of dtype, SSD_BF16 or SSD_F32; out of out_dtype: dtype or SSD_F32):
+ *   q, out [B][NT][Hq][dh]; k_cand, v_cand [B][NT][Hkv][dh];
+ *   k_shared, v_shared [Hkv][S_max][dh] (shared_len <= S_max);
+ *   k_cache, v_cache [B][Hkv][P_max][dh] (prefix_len[b] <= P_max);
+ *   shared_len [1], prefix_len [B], blk_len [B][NB] int32.
+ * In pages (block_table [B][pages_per_seq] int32 not NULL): k_cache, v_cache are pages of 128
+ * tokens [num_pages][Hkv][128][dh], key p of sequence b is row p % 128 of page
+ * block_table[b][p / 128]; with shared_table [shared_pages] int32 (only then) the shared keys lie
+ * in pages of the same pool and k_shared, v_shared, S_max are unused.
+ * What lies behind a length, in other blocks or in absent slots is never used: it may hold
+ * anything. Scores, maxima, sums and the joins of a row's parts are fp32; with bf16 inputs the
+ * probabilities of the shared and the own keys are rounded to bf16 before they weight the values
+ * (their sum is that of the rounded ones), those of the own block are not. Results do not
+ * depend on the order of execution: a call repeats bit for bit.
+ * Supported: dh 64 or 128; Hq % Hkv == 0, Hq / Hkv <= 64; Dmax <= 256, NB * Dmax <= 8192;
+ * B <= 4096; Hkv <= 1024; 16-byte aligned tensors; fewer than 2^31 rows of keys and rows of out,
+ * fewer than 2^30 units of work (128 keys x 256 rows of a kv head); else SSD_ERR_UNSUPPORTED.
+ * scale == 0 selects 1/sqrt(dh). out must not overlap an input (SSD_ERR_INVALID). A length
+ * outside its cache or a page outside the pool records SSD_ERR_DEVICE (the length counts as 0,
+ * the page as page 0); block lengths count as the nearest of 0 .. Dmax.
+ * Workspace: ssd_verify_attn_shared_workspace_size(a) bytes for the current device, 256-byte
+ * aligned; its contents need no initialisation but for the header (as for ssd_verify_attn). Calls
+ * one after another on a stream may share it; calls that overlap on the GPU may not.
+ */
+typedef struct {
+  const void* q;
+  const void* k_shared;
+  const void* v_shared;
+  const int32_t* shared_len;
+  const void* k_cache;
+  const void* v_cache;
+  const void* k_cand;
+  const void* v_cand;
+  void* out;
+  const int32_t* prefix_len;
+  const int32_t* blk_len;
+  const int32_t* shared_table;
+  const int32_t* block_table;
+  int dtype, out_dtype;
+  int B, NB, Dmax, Hq, Hkv, dh;
+  int shared_pages, pages_per_seq;
+  float scale;
+  int64_t S_max, P_max, num_pages;
+} ssd_attn_shared_args;
+
+size_t ssd_verify_attn_shared_workspace_size(const ssd_attn_shared_args* a);
+int ssd_verify_attn_shared(const ssd_attn_shared_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * ssd_filter_probs — the distributions that sampling settings leave of logit rows.
  *
  * Speculative Decoding 해부 page, §3: the acceptance compares p(x) and q(x), so where tokens are
@@ -799,7 +857,8 @@ enum {
   SSD_KERNEL_HEAD_DOWN = 8,          /* ssd_lowrank_head: u = W_down h */
   SSD_KERNEL_HEAD_UP = 9,            /* ssd_lowrank_head: z = W_up u and its statistics */
   SSD_KERNEL_HEAD_COMBINE = 10,      /* ssd_lowrank_head: per-row merge */
-  SSD_KERNEL_SAMPLE = 11             /* ssd_filter_probs, ssd_sample */
+  SSD_KERNEL_SAMPLE = 11,            /* ssd_filter_probs, ssd_sample */
+  SSD_KERNEL_ATTN_SHARED = 12        /* ssd_verify_attn_shared: the parts of shared and own keys */
 };
 int ssd_profile_kernel(int kernel_id, void* start_event, void* end_event);
 

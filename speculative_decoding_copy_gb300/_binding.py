@@ -32,9 +32,10 @@ EXPORTED = ["ssd_status_string", "ssd_version", "ssd_launch_count", "ssd_gate_ma
             "ssd_read_probe", "ssd_checked_build", "ssd_read_check_error",
             "ssd_page_tables", "ssd_append_kv_quant", "ssd_commit_kv_quant",
             "ssd_verify_attn_quant_workspace_size", "ssd_verify_attn_quant",
-            "ssd_filter_probs", "ssd_sample"]
+            "ssd_filter_probs", "ssd_sample",
+            "ssd_verify_attn_shared_workspace_size", "ssd_verify_attn_shared"]
 SSD_KERNEL = dict(vocab_stats=1, verify_attn=2, attn_combine=3, accept_finish=4, gate_match=6,
-                  retrieve=7, head_down=8, head_up=9, head_combine=10, sample=11)
+                  retrieve=7, head_down=8, head_up=9, head_combine=10, sample=11, attn_shared=12)
 
 
 class SsdError(RuntimeError):
@@ -92,6 +93,16 @@ class CommitQuantArgs(ctypes.Structure):
                 ("n_out", c_void_p), ("new_len", c_void_p), ("block_table", c_void_p), ("dtype", c_int),
                 ("B", c_int), ("NB", c_int), ("Dmax", c_int), ("Hkv", c_int), ("dh", c_int), ("scale_block", c_int),
                 ("pages_per_seq", c_int), ("P_max", c_int64), ("num_pages", c_int64)]
+
+
+class AttnSharedArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k_shared", c_void_p), ("v_shared", c_void_p), ("shared_len", c_void_p),
+                ("k_cache", c_void_p), ("v_cache", c_void_p), ("k_cand", c_void_p), ("v_cand", c_void_p),
+                ("out", c_void_p), ("prefix_len", c_void_p), ("blk_len", c_void_p), ("shared_table", c_void_p),
+                ("block_table", c_void_p), ("dtype", c_int), ("out_dtype", c_int), ("B", c_int), ("NB", c_int),
+                ("Dmax", c_int), ("Hq", c_int), ("Hkv", c_int), ("dh", c_int), ("shared_pages", c_int),
+                ("pages_per_seq", c_int), ("scale", c_float), ("S_max", c_int64), ("P_max", c_int64),
+                ("num_pages", c_int64)]
 
 
 class RowsArgs(ctypes.Structure):
@@ -198,6 +209,10 @@ def load(path) -> ctypes.CDLL:
         L.ssd_verify_attn_quant_workspace_size.argtypes = [POINTER(AttnQuantArgs)]
         L.ssd_verify_attn_quant.restype = c_int
         L.ssd_verify_attn_quant.argtypes = [POINTER(AttnQuantArgs), c_void_p, c_size_t, c_void_p]
+        L.ssd_verify_attn_shared_workspace_size.restype = c_size_t
+        L.ssd_verify_attn_shared_workspace_size.argtypes = [POINTER(AttnSharedArgs)]
+        L.ssd_verify_attn_shared.restype = c_int
+        L.ssd_verify_attn_shared.argtypes = [POINTER(AttnSharedArgs), c_void_p, c_size_t, c_void_p]
         L.ssd_filter_probs.restype = c_int
         L.ssd_filter_probs.argtypes = [POINTER(RowsArgs), c_void_p, c_int, c_int, c_void_p, c_void_p, c_size_t, c_void_p]
         L.ssd_sample.restype = c_int
@@ -683,6 +698,83 @@ def ssd_verify_attn_quant(q, k_cache, v_cache, k_scale, v_scale, k_cand, v_cand,
                            scale_block, out, scale, block_table)
     _quant_call("ssd_verify_attn_quant", args, ws, dev, stream, ("out", out), ("q", q))
     return out
+
+
+# ---------------------------------------------------------------------------
+# attention over a shared prompt
+def attn_shared_args(q, k_shared, v_shared, shared_len, k_cache, v_cache, k_cand, v_cand, prefix_len, blk_len, Dmax, out,
+                     scale=0.0, block_table=None, shared_table=None) -> AttnSharedArgs:
+    """Marshal the arguments of ssd_verify_attn_shared (its layouts)."""
+    B, _, Hq, dh = q.shape
+    pages, Hkv, P, _ = k_cache.shape
+    ptr = lambda t: None if t is None else t.data_ptr()
+    return AttnSharedArgs(q.data_ptr(), ptr(k_shared), ptr(v_shared), shared_len.data_ptr(), k_cache.data_ptr(),
+                          v_cache.data_ptr(), k_cand.data_ptr(), v_cand.data_ptr(), out.data_ptr(), prefix_len.data_ptr(),
+                          blk_len.data_ptr(), ptr(shared_table), ptr(block_table), _elem_type(q), _elem_type(out), B,
+                          blk_len.shape[1], Dmax, Hq, Hkv, dh, 0 if shared_table is None else shared_table.shape[0],
+                          0 if block_table is None else block_table.shape[1], scale,
+                          0 if k_shared is None else k_shared.shape[1], P, pages)
+
+
+def ssd_verify_attn_shared_workspace_size(args: AttnSharedArgs) -> int:
+    """Bytes of workspace on the current device (0: the arguments are not supported)."""
+    return int(lib().ssd_verify_attn_shared_workspace_size(ctypes.byref(args)))
+
+
+def ssd_verify_attn_shared(q, k_shared, v_shared, shared_len, k_cache, v_cache, k_cand, v_cand, prefix_len, blk_len, Dmax, *,
+                           out=None, ws=None, scale=0.0, stream=None, out_f32=False, block_table=None, shared_table=None):
+    """Block-triangular verification attention of a batch whose sequences share a prompt: keys
+    k_shared, v_shared [Hkv][S_max][dh] (the first shared_len [1] of them), read once for all, then
+    each sequence's own prefix and block. The own cache is contiguous [B][Hkv][P_max][dh], or with
+    block_table [B][pages_per_seq] pages of 128 tokens; with shared_table [pages] the prompt lies in
+    pages of the same pool (k_shared, v_shared None). Returns the output [B][NT][Hq][dh]."""
+    _need(q, "q", _ROWS, 4)
+    dev, kind = q.device, (q.dtype,) if q.dtype == torch.float32 else _HALF
+    B, NT, Hq, dh = q.shape
+    _need(k_cache, "k_cache", kind, 4)
+    shape = k_cache.shape
+    Hkv = shape[1]
+    if k_cache.device != dev:
+        raise ValueError(f"k_cache is on {k_cache.device}, not on {dev}")
+    if shape[3] != dh:
+        raise ValueError(f"k_cache holds rows of {shape[3]} elements, q of {dh}")
+    _need_shape(v_cache, "v_cache", kind, shape, dev)
+    _cache_fits(shape, B, block_table, dev)
+    if shared_table is not None:
+        if block_table is None or k_shared is not None or v_shared is not None:
+            raise ValueError("shared_table goes with a block_table and without k_shared, v_shared")
+        _need(shared_table, "shared_table", _I32, 1)
+        if shared_table.device != dev:
+            raise ValueError(f"shared_table is on {shared_table.device}, not on {dev}")
+    else:
+        _need(k_shared, "k_shared", kind, 3)
+        _need_shape(k_shared, "k_shared", kind, (Hkv, k_shared.shape[1], dh), dev)
+        _need_shape(v_shared, "v_shared", kind, k_shared.shape, dev)
+    _need_shape(shared_len, "shared_len", _I32, (1,), dev)
+    _need_shape(k_cand, "k_cand", kind, (B, NT, Hkv, dh), dev)
+    _need_shape(v_cand, "v_cand", kind, (B, NT, Hkv, dh), dev)
+    _need_shape(prefix_len, "prefix_len", _I32, (B,), dev)
+    if Dmax < 1 or NT % Dmax:
+        raise ValueError(f"{NT} candidate slots are no whole blocks of {Dmax}")
+    _need_shape(blk_len, "blk_len", _I32, (B, NT // Dmax), dev)
+    if out is None:
+        out = _new(stream, q.shape, torch.float32 if out_f32 else q.dtype, dev)
+    else:
+        _need_shape(out, "out", (torch.float32,) + kind, q.shape, dev)
+    args = attn_shared_args(q, k_shared, v_shared, shared_len, k_cache, v_cache, k_cand, v_cand, prefix_len, blk_len, Dmax, out,
+                            scale, block_table, shared_table)
+    if ws is None:
+        with torch.cuda.device(dev):
+            need = ssd_verify_attn_shared_workspace_size(args)
+        ws = _new(stream, max(need, 256), torch.uint8, dev)
+        ws[:256].zero_() if stream is None else _zero_on(stream, ws)
+    _quant_call("ssd_verify_attn_shared", args, ws, dev, stream, ("out", out), ("q", q))
+    return out
+
+
+def _zero_on(stream, ws):
+    with torch.cuda.stream(stream):
+        ws[:256].zero_()
 
 
 # ---------------------------------------------------------------------------

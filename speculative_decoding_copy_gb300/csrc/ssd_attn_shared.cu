@@ -1,0 +1,1026 @@
+// Verification attention of a batch whose sequences share a prompt: the prompt's keys once for all.
+//
+// For a present token t of sequence b and a q-head, with the row's softmax kept as (m, l, O) = (reference
+// maximum, sum of 2^(s - m), sum of 2^(s - m) v) over any part of its keys, two parts join by
+//   M = max(m1, m2),  l = l1 2^(m1 - M) + l2 2^(m2 - M),  O likewise,
+// so the parts may be computed wherever that is cheapest: the shared prompt with the present tokens of
+// all sequences as the rows of one product, a sequence's own prefix with its tokens, the own block
+// (at most 256 keys) row by row. Three kernels:
+//   k_plan    one CTA: list of the present tokens, offsets of the sequences, and the work in units of
+//             128 keys x 256 packed rows ("pairs" of two row tiles) x one kv head;
+//   k_parts   one CTA an SM: an equal run of units each, so that a long prompt, many short prefixes or
+//             both fill the GPU whatever their sizes. Where a run crosses from one pair (and head) to
+//             the next, a segment ends and its (m, l, O) go to the workspace;
+//   k_join    a warp a row: the segments of its shared and own keys, and its own block.
+// k_parts, 320 threads, all 512 columns of TMEM: warps 0-3 and 4-7 hold a row tile each (a thread a row):
+// scores of 128 keys from TMEM into registers, running maximum, P as bf16 pairs over the scores' own
+// columns, O rescaled in TMEM only when a maximum grew by more than 2^8; warp 8 fetches K and V tiles by
+// TMA into a ring of five; warp 9 issues the products, those of one tile while the other's softmax
+// runs, and before that zeroes the value rows behind a length (0 times NaN is NaN).
+// Every wait is bounded; after one that gave up the CTA records SSD_ERR_TIMEOUT, waits (bounded) for its
+// copies and products in flight and ends.
+#include <cuda.h>
+#include <math.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "ssd_kvq.cuh"
+#include "ssd_tc.cuh"
+
+namespace ssd {
+namespace shr {
+
+using namespace tc;
+
+constexpr int kTile = 128;                 // keys of a tile, packed rows of a row tile
+constexpr int kThreads = 320;
+constexpr int kSlots = 5;                  // ring of K and V tiles
+constexpr int kSegs = 40;                  // segments a CTA has described at once
+constexpr int kMaxBatch = 4096;            // sequences: their offsets fit the ring before it is used
+constexpr unsigned long long kWaitClocks = 1ull << 32;
+
+struct Params {
+  const void *q, *k_shared, *v_shared, *k_cache, *v_cache, *k_cand, *v_cand;
+  void* out;
+  const int32_t *shared_len, *prefix_len, *blk_len, *shared_table, *block_table;
+  int B, NB, Dmax, Hq, Hkv, G;
+  int tokens;                              // of a row tile: 128 / G
+  int64_t S_max, P_max, num_pages;
+  int shared_pages, pages_per_seq;
+  float scale_log2;
+  int out_f32, ctas;
+  WsHeader* hdr;
+  int32_t* plan;                           // kPlan numbers
+  int32_t* tok;                            // the present tokens b * NT + t
+  int32_t *tok_first, *unit0, *ph0, *own_len;      // [B + 1] (own_len [B])
+  float* ml;                               // [segments][256][2]
+  float* o;                                // [segments][256][dh]
+};
+enum { kTokens = 0, kShare = 1, kUnits = 2, kSharedLen = 3, kPlan = 16 };
+
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// ------------------------------------------------------------------ plan
+constexpr int kPlanThreads = 1024;
+
+__device__ __forceinline__ int plan_scan(int v, int* part, int* total) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) part[wid] = x;
+  __syncthreads();
+  int w = part[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, max(wid - 1, 0));
+  return x - v + (wid > 0 ? before : 0);
+}
+
+// Segment (of pair-and-head ph, cut by CTA c's run) has the number ph + c: from one segment to the next
+// one of the two grows or both do. Pairs of the shared prompt come first, then those of each sequence.
+__global__ void __launch_bounds__(kPlanThreads) k_plan(Params p) {
+  __shared__ int part[32];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int S = __ldg(p.shared_len);
+  const int64_t s_cap = p.shared_table != nullptr ? 128LL * p.shared_pages : p.S_max;
+  if (S < 0 || S > s_cap) {
+    if (tid == 0) record_error(p.hdr, SSD_ERR_DEVICE, 601);
+    S = 0;
+  }
+  const int64_t p_cap = p.block_table != nullptr ? 128LL * p.pages_per_seq : p.P_max;
+  int tokens = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < p.B)
+      for (int k = 0; k < p.NB; ++k) n += min(max(__ldg(p.blk_len + static_cast<int64_t>(b) * p.NB + k), 0), p.Dmax);
+    int total;
+    const int first = plan_scan(n, part, &total);
+    if (b < p.B) p.tok_first[b] = tokens + first;
+    tokens += total;
+  }
+  if (tid == 0) p.tok_first[p.B] = tokens;
+  const int pair = 2 * p.tokens;
+  int ph = S > 0 ? ceil_div(tokens, pair) * p.Hkv : 0;
+  int units = ph * ceil_div(S, kTile);
+  __syncthreads();                          // tok_first is written
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int u = 0, h = 0;
+    if (b < p.B) {
+      int P = __ldg(p.prefix_len + b);
+      if (P < 0 || P > p_cap) {
+        record_error(p.hdr, SSD_ERR_DEVICE, 602);
+        P = 0;
+      }
+      p.own_len[b] = P;
+      h = P > 0 ? ceil_div(p.tok_first[b + 1] - p.tok_first[b], pair) * p.Hkv : 0;
+      u = h * ceil_div(P, kTile);
+    }
+    int total_u, total_h;
+    const int fu = plan_scan(u, part, &total_u), fh = plan_scan(h, part, &total_h);
+    if (b < p.B) {
+      p.unit0[b] = units + fu;
+      p.ph0[b] = ph + fh;
+    }
+    units += total_u;
+    ph += total_h;
+  }
+  if (tid == 0) {
+    p.unit0[p.B] = units;
+    p.ph0[p.B] = ph;
+    p.plan[kTokens] = tokens;
+    p.plan[kShare] = max(1, ceil_div(units, p.ctas));
+    p.plan[kUnits] = units;
+    p.plan[kSharedLen] = S;
+  }
+  // the tokens: a warp a sequence
+  for (int b = wid; b < p.B; b += kPlanThreads / 32) {
+    int at = p.tok_first[b];
+    for (int k0 = 0; k0 < p.NB; k0 += 32) {
+      const int len = k0 + lane < p.NB ? min(max(__ldg(p.blk_len + static_cast<int64_t>(b) * p.NB + k0 + lane), 0), p.Dmax) : 0;
+      for (int k = k0; k < min(p.NB, k0 + 32); ++k) {
+        const int n = __shfl_sync(0xffffffffu, len, k - k0);
+        for (int d = lane; d < n; d += 32) p.tok[at + d] = (b * p.NB + k) * p.Dmax + d;
+        at += n;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ segments
+struct Seg {
+  int b;                                   // sequence, or -1: the shared prompt
+  int kvh, tok0, ntok;                     // first present token and their number (up to two tiles')
+  int j0, j1, len;                         // key tiles, and the length of all keys
+  int id;
+};
+
+// the sequence whose units hold u (unit0 ascending; the last one that starts at or before u and has any)
+__device__ __forceinline__ int find_seq(const int* unit0, int B, int u) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (unit0[mid] <= u) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Segments of units [u, u1) for CTA c, as many as fit; returns the unit behind them. `b` is the sequence
+// that u lies in, where it is not in the shared part (-1: not looked for yet).
+__device__ int describe(const Params& p, Seg* segs, int* count, int c, int u, int u1, const int* unit0, const int* ph0, const int* tok_first,
+                        const int* own_len, int tokens, int shared_len) {
+  const int pair = 2 * p.tokens, own0 = unit0[0];
+  int n = 0, b = -1;
+  while (u < u1 && n < kSegs) {
+    Seg s;
+    int base, first, all, ph;
+    if (u < own0) {
+      s.b = -1;
+      s.len = shared_len;
+      base = 0;
+      first = 0;
+      all = tokens;
+      ph = 0;
+    } else {
+      if (b < 0) b = find_seq(unit0, p.B, u);
+      while (unit0[b + 1] <= u) ++b;
+      s.b = b;
+      s.len = own_len[b];
+      base = unit0[b];
+      first = tok_first[b];
+      all = tok_first[b + 1] - first;
+      ph = ph0[b];
+    }
+    const int kt = ceil_div(s.len, kTile), at = (u - base) / kt;
+    s.kvh = at % p.Hkv;
+    const int pr = at / p.Hkv;
+    s.tok0 = first + pr * pair;
+    s.ntok = min(pair, all - pr * pair);
+    s.j0 = (u - base) - at * kt;
+    s.j1 = min(kt, s.j0 + (u1 - u));
+    s.id = ph + at + c;
+    segs[n++] = s;
+    u += s.j1 - s.j0;
+  }
+  *count = n;
+  return u;
+}
+
+// row of the K or V tensor (rows of dh elements) at which key tile j of a segment starts
+__device__ __forceinline__ int64_t tile_row(const Params& p, const Seg& s, int j) {
+  if (s.b < 0 && p.shared_table == nullptr) return static_cast<int64_t>(s.kvh) * p.S_max + j * kTile;
+  if (s.b >= 0 && p.block_table == nullptr) return (static_cast<int64_t>(s.b) * p.Hkv + s.kvh) * p.P_max + j * kTile;
+  int pg = s.b < 0 ? __ldg(p.shared_table + j) : __ldg(p.block_table + static_cast<int64_t>(s.b) * p.pages_per_seq + j);
+  if (pg < 0 || pg >= p.num_pages) {
+    record_error(p.hdr, SSD_ERR_DEVICE, 603);
+    pg = 0;
+  }
+  return (static_cast<int64_t>(pg) * p.Hkv + s.kvh) * kTile;
+}
+
+// ------------------------------------------------------------------ parts, tensor cores
+struct Bars {
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], o_free[2];
+  uint64_t last;
+  uint32_t tmem_base;
+  int failed, count, next;
+  Seg segs[kSegs];
+};
+static_assert(sizeof(Bars) <= 2048, "barriers and segments");
+
+template <int DH>
+struct Shape {
+  static constexpr uint32_t kHalves = DH / 64;
+  static constexpr uint32_t kHalf = kTile * 128;            // 128 rows x 64 bf16, 128-byte swizzle
+  static constexpr uint32_t kTileB = kHalves * kHalf;
+  static constexpr uint32_t OFF_Q = 0;                      // two row tiles
+  static constexpr uint32_t OFF_RING = 2 * kTileB;
+  static constexpr uint32_t OFF_BAR = OFF_RING + kSlots * kTileB;
+  static constexpr uint32_t kSmem = OFF_BAR + 2048 + 1024;  // + slack to align the base to 1024
+};
+static_assert(Shape<128>::kSmem <= 232448, "shared memory per CTA");
+static_assert(4 * (kMaxBatch + 1) * 4 <= kSlots * static_cast<int>(Shape<64>::kTileB), "offsets fit the ring");
+constexpr uint32_t TM_S = 0, TM_O = 256;   // scores of tile 0 and 1 (P over their first 64 columns), O of tile 0 and 1
+
+__device__ __forceinline__ bool wait(Bars& bars, uint64_t* bar, uint32_t parity, WsHeader* hdr, int where) {
+  return mbar_wait_bounded(bar, parity, &bars.failed, hdr, where, kWaitClocks);
+}
+// without a look at `failed`: for what is in flight after a wait gave up
+__device__ __forceinline__ void wait_anyway(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = clock64();
+  while (!mbar_probe(bar, parity) && clock64() - t0 < kWaitClocks) {
+  }
+}
+
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUtensorMap map_vs, const __grid_constant__ CUtensorMap map_k,
+        const __grid_constant__ CUtensorMap map_v, Params p) {
+  using Sh = Shape<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  Bars& bars = *reinterpret_cast<Bars*>(smem + Sh::OFF_BAR);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+
+  if (tid == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars.s_full[t], 1);
+      mbar_init(&bars.p_full[t], 128);
+      mbar_init(&bars.pv_done[t], 1);
+      mbar_init(&bars.q_full[t], 128);
+      mbar_init(&bars.o_free[t], 128);
+    }
+    mbar_init(&bars.last, 1);
+    bars.failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    if (lane == 0) {
+      prefetch_tmap(&map_ks);
+      prefetch_tmap(&map_vs);
+      prefetch_tmap(&map_k);
+      prefetch_tmap(&map_v);
+    }
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem_base)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the plan
+  const int share = __ldcg(p.plan + kShare), units = __ldcg(p.plan + kUnits), tokens = __ldcg(p.plan + kTokens);
+  const int shared_len = __ldcg(p.plan + kSharedLen);
+  const int64_t start = static_cast<int64_t>(cta) * share;
+  int u = static_cast<int>(start < units ? start : units);
+  const int u1 = static_cast<int>(start + share < units ? start + share : units);
+
+  // phases, each role its own: ring entries so far; of the softmax warps the tiles so far; of the
+  // products one bit a row tile
+  uint32_t it = 0, tiles = 0, ph_p = 0, ph_q = 0, ph_o = 0, used = 0;
+
+  bool more = u < u1;
+  while (more) {
+    // offsets of the sequences into the ring, then this CTA's segments from there
+    int* off = reinterpret_cast<int*>(smem + Sh::OFF_RING);
+    for (int i = tid; i <= p.B; i += kThreads) {
+      off[i] = __ldcg(p.unit0 + i);
+      off[(p.B + 1) + i] = __ldcg(p.ph0 + i);
+      off[2 * (p.B + 1) + i] = __ldcg(p.tok_first + i);
+      off[3 * (p.B + 1) + i] = i < p.B ? __ldcg(p.own_len + i) : 0;
+    }
+    __syncthreads();
+    if (tid == 0)
+      bars.next = describe(p, bars.segs, &bars.count, cta, u, u1, off, off + (p.B + 1), off + 2 * (p.B + 1), off + 3 * (p.B + 1), tokens, shared_len);
+    fence_async_smem();                                     // TMA writes over what was just read
+    __syncthreads();
+    u = bars.next;
+    const int nseg = bars.count;
+
+    if (warp < 8) {
+      // -------------------------------------------------------- softmax rows
+      const int t = warp >> 2;                              // row tile
+      const int wr = (warp & 3) * 32;                       // this warp's first row
+      const uint32_t lane_off = static_cast<uint32_t>(wr) << 16;
+      const uint32_t sc = tmem + TM_S + t * 128 + lane_off, oc = tmem + TM_O + t * 128 + lane_off;
+      // rows of tile t of a segment: G heads of each of its tokens
+      auto load_q = [&](const Seg& s) {
+        const int nrow = min(p.tokens, s.ntok - t * p.tokens) * p.G;
+        const int r = wr + lane;
+        const int token = r < nrow ? __ldcg(p.tok + s.tok0 + t * p.tokens + r / p.G) : -1;
+        constexpr int CH = DH / 8;                          // 16-byte pieces of a row
+        constexpr int RI = 32 / CH;                         // rows of one round
+        uint4 v[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int rr = i * RI + lane / CH;
+          const int tk = __shfl_sync(0xffffffffu, token, rr);
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (tk >= 0)
+            v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                        (static_cast<int64_t>(tk) * p.Hq + s.kvh * p.G + (wr + rr) % p.G) * DH) + lane % CH);
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int rr = wr + i * RI + lane / CH, ch = lane % CH;
+          *reinterpret_cast<uint4*>(smem + Sh::OFF_Q + t * Sh::kTileB + (ch >> 3) * Sh::kHalf + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v[i];
+        }
+        fence_async_smem();
+        mbar_arrive(&bars.q_full[t]);
+      };
+      auto active = [&](const Seg& s) { return s.ntok > t * p.tokens; };
+      int i = 0;
+      while (i < nseg && !active(bars.segs[i])) ++i;
+      if (i < nseg) load_q(bars.segs[i]);
+      while (i < nseg) {
+        const Seg s = bars.segs[i];
+        int next = i + 1;
+        while (next < nseg && !active(bars.segs[next])) ++next;
+        float m = -INFINITY, l = 0.f;
+        for (int j = s.j0; j < s.j1; ++j) {
+          wait(bars, &bars.s_full[t], tiles & 1, p.hdr, 610);
+          tc_fence_after();
+          uint32_t v[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(sc + 32 * c, v + 32 * c);
+          tmem_wait_ld();
+          const int hi = s.len - j * kTile;
+          if (hi < kTile) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c >= hi) v[c] = 0xff800000u;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 128; c += 2) mx[(c >> 1) & 3] = fmaxf(mx[(c >> 1) & 3], fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          // the reference moves only when the maximum grows by more than 2^8
+          const bool need = top > m + 8.f || m == -INFINITY;
+          const float ref = need ? fmaxf(m, top) : m;
+          const float alpha = need && m > -INFINITY ? ex2_approx(m - ref) : 1.f;     // nothing counted yet: O and l are 0
+          const float sub = ref > -INFINITY ? ref : 0.f;    // every key at -inf: all weights 0
+          float rs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 128; c += 2) {
+            const uint32_t w = pack_bf16(ex2_approx(fmaf(__uint_as_float(v[c]), p.scale_log2, -sub)),
+                                         ex2_approx(fmaf(__uint_as_float(v[c + 1]), p.scale_log2, -sub)));
+            rs[(c >> 1) & 1] += __uint_as_float(w << 16);
+            rs[2 + ((c >> 1) & 1)] += __uint_as_float(w & 0xffff0000u);
+            v[c >> 1] = w;
+          }
+          tmem_st32(sc, v);
+          tmem_st32(sc + 32, v + 32);
+          if (j > s.j0) {
+            if (__any_sync(0xffffffffu, need)) {
+              // O holds the sum up to the tile before: wait for that product, then rescale
+              wait(bars, &bars.pv_done[t], (tiles - 1) & 1, p.hdr, 611);
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < DH / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(oc + 32 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st32(oc + 32 * c, o);
+              }
+            }
+          }
+          l = l * alpha + ((rs[0] + rs[1]) + (rs[2] + rs[3]));
+          m = ref;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars.p_full[t]);
+          ++tiles;
+        }
+        // the last scores are read: Q is free for the next segment, whose first product may start
+        if (next < nseg) load_q(bars.segs[next]);
+        wait(bars, &bars.pv_done[t], (tiles - 1) & 1, p.hdr, 612);
+        tc_fence_after();
+        const int nrow = min(p.tokens, s.ntok - t * p.tokens) * p.G;
+        const int64_t row = static_cast<int64_t>(s.id) * 256 + t * 128 + wr + lane;
+        const bool keep = wr + lane < nrow && !bars.failed;
+#pragma unroll 1
+        for (int c = 0; c < DH / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(oc + 32 * c, o);
+          tmem_wait_ld();
+          if (keep) {
+            float4* dst = reinterpret_cast<float4*>(p.o + row * DH + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+          }
+        }
+        if (wr + lane < nrow) *reinterpret_cast<float2*>(p.ml + row * 2) = bars.failed ? make_float2(NAN, NAN) : make_float2(m, l);
+        tc_fence_before();
+        mbar_arrive(&bars.o_free[t]);
+        i = next;
+      }
+    } else if (warp == 8) {
+      // -------------------------------------------------------- TMA: K0 V0 K1 V1 ..
+      if (lane == 0) {
+        for (int i = 0; i < nseg && !bars.failed; ++i) {
+          const Seg s = bars.segs[i];
+          const CUtensorMap* mk = s.b < 0 ? &map_ks : &map_k;
+          const CUtensorMap* mv = s.b < 0 ? &map_vs : &map_v;
+          for (int j = s.j0; j < s.j1 && !bars.failed; ++j) {
+            const int y = static_cast<int>(tile_row(p, s, j));
+            for (int kv = 0; kv < 2; ++kv, ++it) {
+              const int slot = it % kSlots;
+              if (it >= kSlots && !wait(bars, &bars.empty[slot], ((it / kSlots) - 1) & 1, p.hdr, 620)) break;
+              const uint32_t dst = sbase + Sh::OFF_RING + slot * Sh::kTileB;
+              mbar_expect_tx(&bars.full[slot], Sh::kTileB);
+#pragma unroll
+              for (uint32_t h = 0; h < Sh::kHalves; ++h) tma_load_2d(dst + h * Sh::kHalf, kv == 0 ? mk : mv, 64 * h, y, &bars.full[slot]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // -------------------------------------------------------- products: the whole warp waits, one lane issues
+      constexpr uint32_t idS = idesc_bf16(false, kTile), idPV = idesc_bf16(true, DH);
+      for (int i = 0; i < nseg; ++i) {
+        const Seg s = bars.segs[i];
+        const int nt = s.ntok > p.tokens ? 2 : 1, nj = s.j1 - s.j0;
+        // K of tile j is ring entry it + 2 (j - j0), V the one behind it
+        auto scores = [&](int t, int jj) {
+          const uint32_t e = it + 2 * jj, slot = e % kSlots;
+          wait(bars, &bars.full[slot], (e / kSlots) & 1, p.hdr, 630);
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t kb = sbase + Sh::OFF_RING + slot * Sh::kTileB, qb = sbase + Sh::OFF_Q + t * Sh::kTileB;
+#pragma unroll
+            for (int ks = 0; ks < DH / 16; ++ks)
+              mma_bf16(tmem + TM_S + t * 128, sw128_desc(qb + (ks >> 2) * Sh::kHalf + (ks & 3) * 32, 16, 1024),
+                       sw128_desc(kb + (ks >> 2) * Sh::kHalf + (ks & 3) * 32, 16, 1024), idS, ks > 0 ? 1u : 0u);
+            mma_commit(&bars.s_full[t]);
+            if (t == nt - 1) mma_commit(&bars.empty[slot]);
+          }
+          __syncwarp();
+        };
+        for (int t = 0; t < nt; ++t) {
+          wait(bars, &bars.q_full[t], (ph_q >> t) & 1, p.hdr, 631);
+          ph_q ^= 1u << t;
+          scores(t, 0);
+        }
+        for (int jj = 0; jj < nj; ++jj) {
+          const uint32_t e = it + 2 * jj + 1, slot = e % kSlots;
+          for (int t = 0; t < nt; ++t) {
+            if (t == 0) {
+              wait(bars, &bars.full[slot], (e / kSlots) & 1, p.hdr, 634);
+              const int r0 = s.len - (s.j0 + jj) * kTile;
+              if (r0 < kTile) {
+                // value rows behind the length: their weights are 0, and 0 times NaN would be NaN
+                uint8_t* v = smem + Sh::OFF_RING + slot * Sh::kTileB;
+                for (int x = r0 * 8 + lane; x < kTile * 8; x += 32)
+#pragma unroll
+                  for (uint32_t h = 0; h < Sh::kHalves; ++h) *reinterpret_cast<uint4*>(v + h * Sh::kHalf + x * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+              }
+            }
+            wait(bars, &bars.p_full[t], (ph_p >> t) & 1, p.hdr, 632);
+            ph_p ^= 1u << t;
+            if (jj == 0) {
+              // O of the tile's last segment has been read
+              if ((used >> t) & 1) {
+                wait(bars, &bars.o_free[t], (ph_o >> t) & 1, p.hdr, 633);
+                ph_o ^= 1u << t;
+              }
+              used |= 1u << t;
+            }
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t vb = sbase + Sh::OFF_RING + slot * Sh::kTileB, pa = tmem + TM_S + t * 128;
+#pragma unroll
+              for (int ks = 0; ks < kTile / 16; ++ks)
+                mma_bf16_ts(tmem + TM_O + t * 128, pa + ks * 8, sw128_desc(vb + ks * 16 * 128, Sh::kHalf, 1024), idPV, (jj > 0 || ks > 0) ? 1u : 0u);
+              mma_commit(&bars.pv_done[t]);
+              if (t == nt - 1) mma_commit(&bars.empty[slot]);
+            }
+            __syncwarp();
+            // the scores of the next tile go over P: products of one thread run in the order issued
+            if (jj + 1 < nj) scores(t, jj + 1);
+          }
+        }
+        it += 2 * nj;
+        if (__any_sync(0xffffffffu, bars.failed)) break;
+      }
+    }
+    // segments and ring are free; the CTA goes on, or ends, as one
+    more = !__syncthreads_or(bars.failed) && u < u1;
+  }
+
+  // copies in flight end before the CTA does, also after a wait that gave up
+  if (warp == 8 && lane == 0)
+    for (uint32_t e = it > kSlots ? it - kSlots : 0; e < it; ++e) wait_anyway(&bars.full[e % kSlots], (e / kSlots) & 1);
+  if (warp == 9 && lane == 0 && used != 0) {
+    mma_commit(&bars.last);
+    wait_anyway(&bars.last, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ parts, fp32
+// The same runs and segments without tensor cores: 8 warps, four rows a warp at a time over tiles of 32
+// keys in shared memory. Bound by its fp32 products; fp32 inputs are for small models and tests.
+constexpr int kSimtThreads = 256;
+constexpr int kSimtRows = 4;               // of a warp
+constexpr int kSimtKeys = 32;
+
+template <int DH>
+__global__ void __launch_bounds__(kSimtThreads) k_parts_simt(Params p) {
+  constexpr int E = DH / 32;
+  __shared__ float q_s[8 * kSimtRows][DH];
+  __shared__ float kv_s[kSimtKeys][DH + 1];
+  __shared__ Seg segs[kSegs];
+  __shared__ int count, next;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t start = static_cast<int64_t>(blockIdx.x) * p.plan[kShare];
+  const int units = p.plan[kUnits];
+  int u = static_cast<int>(start < units ? start : units);
+  const int u1 = static_cast<int>(start + p.plan[kShare] < units ? start + p.plan[kShare] : units);
+  while (u < u1) {
+    __syncthreads();
+    if (tid == 0)
+      next = describe(p, segs, &count, blockIdx.x, u, u1, p.unit0, p.ph0, p.tok_first, p.own_len, p.plan[kTokens], p.plan[kSharedLen]);
+    __syncthreads();
+    u = next;
+    for (int i = 0; i < count; ++i) {
+      const Seg s = segs[i];
+      const float* kb = static_cast<const float*>(s.b < 0 ? p.k_shared : p.k_cache);
+      const float* vb = static_cast<const float*>(s.b < 0 ? p.v_shared : p.v_cache);
+      // the rows of both tiles one after another: row x is head x % G of token x / G
+      const int rows = s.ntok * p.G;
+      for (int x0 = 0; x0 < rows; x0 += 8 * kSimtRows) {
+        __syncthreads();
+        for (int e = tid; e < 8 * kSimtRows * DH; e += kSimtThreads) {
+          const int x = x0 + e / DH;
+          q_s[e / DH][e % DH] = x < rows ? static_cast<const float*>(p.q)[(static_cast<int64_t>(p.tok[s.tok0 + x / p.G]) * p.Hq + s.kvh * p.G + x % p.G) * DH + e % DH] *
+                                               p.scale_log2
+                                         : 0.f;
+        }
+        float m[kSimtRows], l[kSimtRows], o[kSimtRows][E], w[kSimtRows];
+#pragma unroll
+        for (int r = 0; r < kSimtRows; ++r) {
+          m[r] = -INFINITY;
+          l[r] = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[r][e] = 0.f;
+        }
+        for (int j = s.j0; j < s.j1; ++j) {
+          const int64_t y = tile_row(p, s, j);
+          const int keys = min(kTile, s.len - j * kTile);
+          for (int k0 = 0; k0 < keys; k0 += kSimtKeys) {
+            const int n = min(kSimtKeys, keys - k0);
+            __syncthreads();
+            for (int e = tid; e < kSimtKeys * DH; e += kSimtThreads) kv_s[e / DH][e % DH] = e / DH < n ? kb[(y + k0) * DH + e] : 0.f;
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < kSimtRows; ++r) {
+              const float* qr = q_s[warp * kSimtRows + r];
+              float sc = 0.f;
+#pragma unroll 8
+              for (int e = 0; e < DH; ++e) sc = fmaf(qr[e], kv_s[lane][e], sc);
+              sc = lane < n ? sc : -INFINITY;
+              const float top = fmaxf(m[r], warp_max(sc));
+              const float f = m[r] > -INFINITY ? exp2f(m[r] - top) : 0.f;
+              w[r] = top > -INFINITY ? exp2f(sc - top) : 0.f;
+              l[r] = l[r] * f + warp_sum(w[r]);
+#pragma unroll
+              for (int e = 0; e < E; ++e) o[r][e] *= f;
+              m[r] = top;
+            }
+            __syncthreads();
+            for (int e = tid; e < kSimtKeys * DH; e += kSimtThreads) kv_s[e / DH][e % DH] = e / DH < n ? vb[(y + k0) * DH + e] : 0.f;
+            __syncthreads();
+            for (int kk = 0; kk < n; ++kk) {
+              float v[E];
+#pragma unroll
+              for (int e = 0; e < E; ++e) v[e] = kv_s[kk][lane + 32 * e];
+#pragma unroll
+              for (int r = 0; r < kSimtRows; ++r) {
+                const float pk = __shfl_sync(0xffffffffu, w[r], kk);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[r][e] = fmaf(pk, v[e], o[r][e]);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kSimtRows; ++r) {
+          const int x = x0 + warp * kSimtRows + r;
+          if (x >= rows) continue;
+          const int tk = x / p.G, tile = tk / p.tokens;
+          const int64_t row = static_cast<int64_t>(s.id) * 256 + tile * 128 + (tk - tile * p.tokens) * p.G + x % p.G;
+          if (lane == 0) *reinterpret_cast<float2*>(p.ml + row * 2) = make_float2(m[r], l[r]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) p.o[row * DH + lane + 32 * e] = o[r][e];
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ join
+// four (dh 128) or two neighbours of a row
+template <typename T, int N>
+__device__ __forceinline__ void load_n(const T* p, float (&v)[N]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const float2 x = __ldg(reinterpret_cast<const float2*>(p + e));
+      v[e] = x.x;
+      v[e + 1] = x.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(p + e));
+      v[e] = __uint_as_float(x << 16);
+      v[e + 1] = __uint_as_float(x & 0xffff0000u);
+    }
+  }
+}
+
+// One warp a row: lane i holds dims i N .. i N + N - 1. Own-block keys are read here, one row after
+// another: a key of another block or of an absent token is never touched, whatever it holds.
+template <typename T, int DH>
+__global__ void __launch_bounds__(128) k_join(Params p) {
+  constexpr int N = DH / 32;
+  constexpr int KG = 8;                    // keys, or segments, whose loads are issued together
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t R = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int i = static_cast<int>(R / p.Hq), h = static_cast<int>(R % p.Hq);
+  if (i >= __ldcg(p.plan + kTokens)) return;
+  const int share = __ldcg(p.plan + kShare), pair = 2 * p.tokens;
+  const int token = __ldcg(p.tok + i), NT = p.NB * p.Dmax;
+  const int b = token / NT, t = token % NT, pos = t % p.Dmax;
+  const int kvh = h / p.G, g = h % p.G;
+  float q[N];
+  load_n<T, N>(static_cast<const T*>(p.q) + (static_cast<int64_t>(token) * p.Hq + h) * DH + lane * N, q);
+#pragma unroll
+  for (int e = 0; e < N; ++e) q[e] *= p.scale_log2;
+  float m = -INFINITY, l = 0.f, o[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] = 0.f;
+
+  // own block: slots k Dmax .. t
+  const int64_t kv0 = ((static_cast<int64_t>(token) - pos) * p.Hkv + kvh) * DH + lane * N;
+  const int64_t step = static_cast<int64_t>(p.Hkv) * DH;
+  for (int c0 = 0; c0 <= pos; c0 += KG) {
+    float k[KG][N], v[KG][N], s[KG];
+#pragma unroll
+    for (int c = 0; c < KG; ++c) {
+      const int64_t at = kv0 + min(c0 + c, pos) * step;      // behind the last one: that again
+      load_n<T, N>(static_cast<const T*>(p.k_cand) + at, k[c]);
+      load_n<T, N>(static_cast<const T*>(p.v_cand) + at, v[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < KG; ++c) {
+      s[c] = 0.f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) s[c] = fmaf(q[e], k[c][e], s[c]);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+      for (int c = 0; c < KG; ++c) s[c] += __shfl_xor_sync(0xffffffffu, s[c], d);
+    float top = m;
+#pragma unroll
+    for (int c = 0; c < KG; ++c) {
+      if (c0 + c > pos) s[c] = -INFINITY;
+      top = fmaxf(top, s[c]);
+    }
+    bool nan = false;                      // a score that is no number makes the row none
+#pragma unroll
+    for (int c = 0; c < KG; ++c) nan = nan || s[c] != s[c];
+    if (top == -INFINITY && !nan) continue;
+    const float f = m == -INFINITY ? 0.f : ex2_approx(m - top);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] *= f;
+#pragma unroll
+    for (int c = 0; c < KG; ++c) {
+      if (c0 + c > pos) break;
+      const float w = ex2_approx(s[c] - top);
+      l += w;
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] = fmaf(w, v[c][e], o[e]);
+    }
+    m = top;
+  }
+
+  // segments: first and last of the shared prompt's, then of the own prefix's
+  auto join = [&](int i0, int u_base, int ph_base, int len) {
+    if (len <= 0) return;
+    const int kt = ceil_div(len, kTile), at = (i0 / pair) * p.Hkv + kvh, in = i0 % pair;
+    const int row = (in / p.tokens) * 128 + (in % p.tokens) * p.G + g;
+    const int u = u_base + at * kt, c0 = u / share, n = (u + kt - 1) / share - c0 + 1;
+    const int64_t r0 = static_cast<int64_t>(ph_base + at + c0) * 256 + row;
+    for (int s0 = 0; s0 < n; s0 += 4) {
+      float2 ml[4];
+      float x[4][N];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int64_t r = r0 + static_cast<int64_t>(min(s0 + c, n - 1)) * 256;
+        ml[c] = __ldcg(reinterpret_cast<const float2*>(p.ml) + r);
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(p.o + r * DH + lane * N + e));
+          x[c][e] = y.x;
+          x[c][e + 1] = y.y;
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (s0 + c >= n) ml[c].x = -INFINITY;
+        top = fmaxf(top, ml[c].x);
+      }
+      if (top == -INFINITY) {
+        // no weight so far; a sum that is no number stays one
+#pragma unroll
+        for (int c = 0; c < 4; ++c) l += s0 + c < n ? ml[c].y : 0.f;
+        continue;
+      }
+      const float f = m == -INFINITY ? 0.f : ex2_approx(m - top);
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] *= f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (s0 + c >= n) continue;
+        const float w = ex2_approx(ml[c].x - top);          // 0 for a segment of scores at -inf, whose O is 0
+        l = fmaf(ml[c].y, w, l);
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] = fmaf(w, x[c][e], o[e]);
+      }
+      m = top;
+    }
+  };
+  join(i, 0, 0, __ldcg(p.plan + kSharedLen));
+  join(i - __ldcg(p.tok_first + b), __ldcg(p.unit0 + b), __ldcg(p.ph0 + b), __ldcg(p.own_len + b));
+
+  const float inv = 1.f / l;
+  const int64_t at = (static_cast<int64_t>(token) * p.Hq + h) * DH + lane * N;
+  if (sizeof(T) == 4 || p.out_f32) {
+    float* out = static_cast<float*>(p.out) + at;
+#pragma unroll
+    for (int e = 0; e < N; e += 2) *reinterpret_cast<float2*>(out + e) = make_float2(o[e] * inv, o[e + 1] * inv);
+  } else {
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at);
+#pragma unroll
+    for (int e = 0; e < N; e += 2) out[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
+  }
+}
+
+// ------------------------------------------------------------------ host
+static int validate(const ssd_attn_shared_args* a) {
+  if (a == nullptr) return SSD_ERR_INVALID;
+  if (a->B < 0 || a->NB < 1 || a->Dmax < 1 || a->Hq < 1 || a->Hkv < 1 || a->P_max < 0 || a->S_max < 0) return SSD_ERR_INVALID;
+  if (a->dtype != SSD_F32 && a->dtype != SSD_BF16) return SSD_ERR_INVALID;
+  if (a->out_dtype != a->dtype && a->out_dtype != SSD_F32) return SSD_ERR_INVALID;
+  if (a->Hq % a->Hkv != 0 || !(a->scale >= 0.f)) return SSD_ERR_INVALID;
+  if (a->dh != 64 && a->dh != 128) return SSD_ERR_UNSUPPORTED;
+  if (a->Dmax > 256 || static_cast<int64_t>(a->NB) * a->Dmax > 8192 || a->Hq / a->Hkv > 64) return SSD_ERR_UNSUPPORTED;
+  if (a->B > kMaxBatch || a->Hkv > 1024) return SSD_ERR_UNSUPPORTED;
+  if (a->block_table != nullptr || a->shared_table != nullptr) {
+    if (a->num_pages < 1) return SSD_ERR_INVALID;
+    if (a->num_pages >= (1LL << 31) / 128 / a->Hkv) return SSD_ERR_UNSUPPORTED;
+  }
+  if (a->block_table != nullptr && a->pages_per_seq < 1) return SSD_ERR_INVALID;
+  if (a->shared_table != nullptr && a->shared_pages < 1) return SSD_ERR_INVALID;
+  // a shared prompt in pages lies in the pool of the sequences' pages
+  if (a->shared_table != nullptr && a->block_table == nullptr) return SSD_ERR_INVALID;
+  if (a->pages_per_seq > (1 << 20) || a->shared_pages > (1 << 20) || a->P_max > (1LL << 27) || a->S_max > (1LL << 27)) return SSD_ERR_UNSUPPORTED;
+  if (a->block_table == nullptr && static_cast<double>(a->B) * a->Hkv * a->P_max >= 0x1p31) return SSD_ERR_UNSUPPORTED;
+  if (a->shared_table == nullptr && static_cast<double>(a->Hkv) * a->S_max >= 0x1p31) return SSD_ERR_UNSUPPORTED;
+  if (a->B == 0) return SSD_OK;
+  if (!a->q || !a->k_cand || !a->v_cand || !a->out || !a->shared_len || !a->prefix_len || !a->blk_len) return SSD_ERR_INVALID;
+  if ((a->block_table != nullptr || a->P_max > 0) && (!a->k_cache || !a->v_cache)) return SSD_ERR_INVALID;
+  if (a->shared_table == nullptr && a->S_max > 0 && (!a->k_shared || !a->v_shared)) return SSD_ERR_INVALID;
+  for (const void* x : {a->q, a->k_shared, a->v_shared, a->k_cache, a->v_cache, a->k_cand, a->v_cand, static_cast<const void*>(a->out)})
+    if (!aligned(x, 16)) return SSD_ERR_UNSUPPORTED;
+  return SSD_OK;
+}
+
+struct Layout {
+  size_t plan, tok, tok_first, unit0, ph0, own_len, ml, o, total;
+  int64_t units, segments;
+};
+
+static int sm_count(int dev) {
+  static std::once_flag once[kMaxDevices];
+  static int n[kMaxDevices];
+  std::call_once(once[dev], [dev] {
+    if (cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n[dev] = 0;
+  });
+  return n[dev];
+}
+
+static int grid_of(const ssd_attn_shared_args* a, int sms) { return a->dtype == SSD_BF16 ? sms : 4 * sms; }
+
+static Layout layout(const ssd_attn_shared_args* a, int ctas) {
+  Layout L{};
+  const int64_t NT = static_cast<int64_t>(a->NB) * a->Dmax, all = a->B * NT;
+  const int pair = 2 * (kTile / (a->Hq / a->Hkv));
+  const int64_t s_cap = a->shared_table != nullptr ? 128LL * a->shared_pages : a->S_max;
+  const int64_t p_cap = a->block_table != nullptr ? 128LL * a->pages_per_seq : a->P_max;
+  const int64_t ph_s = (all + pair - 1) / pair * a->Hkv, ph_o = (NT + pair - 1) / pair * a->Hkv * a->B;
+  L.units = ph_s * ((s_cap + kTile - 1) / kTile) + ph_o * ((p_cap + kTile - 1) / kTile);
+  L.segments = (s_cap > 0 ? ph_s : 0) + (p_cap > 0 ? ph_o : 0) + ctas;
+  size_t at = sizeof(WsHeader);
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = round_up(at + bytes, 256);
+    return here;
+  };
+  L.plan = take(4 * kPlan);
+  L.tok = take(4 * static_cast<size_t>(all));
+  L.tok_first = take(4 * (static_cast<size_t>(a->B) + 1));
+  L.unit0 = take(4 * (static_cast<size_t>(a->B) + 1));
+  L.ph0 = take(4 * (static_cast<size_t>(a->B) + 1));
+  L.own_len = take(4 * static_cast<size_t>(a->B));
+  L.ml = take(static_cast<size_t>(L.segments) * 256 * 8);
+  L.o = take(static_cast<size_t>(L.segments) * 256 * a->dh * 4);
+  L.total = at;
+  return L;
+}
+
+static bool kv_map(CUtensorMap* map, const void* base, uint64_t rows, int dh) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(dh), rows};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(dh) * 2};
+  const cuuint32_t box[2] = {64, kTile};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DH>
+static int launch_parts(const Params& p, const ssd_attn_shared_args* a, cudaStream_t s) {
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t err[kMaxDevices];
+  const int dev = current_device();
+  std::call_once(once[dev], [dev] {
+    err[dev] = cudaFuncSetAttribute(k_parts<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Shape<DH>::kSmem));
+  });
+  if (err[dev] != cudaSuccess) return SSD_ERR_CUDA;
+  const uint64_t pool = static_cast<uint64_t>(a->num_pages) * a->Hkv * kTile;
+  const uint64_t rs = a->shared_table != nullptr ? pool : static_cast<uint64_t>(a->Hkv) * a->S_max;
+  const uint64_t ro = a->block_table != nullptr ? pool : static_cast<uint64_t>(a->B) * a->Hkv * a->P_max;
+  const void* ks = a->shared_table != nullptr ? a->k_cache : a->k_shared;
+  const void* vs = a->shared_table != nullptr ? a->v_cache : a->v_shared;
+  // a part without keys gets no unit: its map only has to be a valid one
+  CUtensorMap m[4];
+  if (!kv_map(&m[0], rs > 0 ? ks : a->q, rs > 0 ? rs : 1, DH) || !kv_map(&m[1], rs > 0 ? vs : a->q, rs > 0 ? rs : 1, DH) ||
+      !kv_map(&m[2], ro > 0 ? a->k_cache : a->q, ro > 0 ? ro : 1, DH) || !kv_map(&m[3], ro > 0 ? a->v_cache : a->q, ro > 0 ? ro : 1, DH))
+    return SSD_ERR_CUDA;
+  KernelTimer timer(SSD_KERNEL_ATTN_SHARED, s);
+  if (launch_pdl(k_parts<DH>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads), Shape<DH>::kSmem, s, m[0], m[1], m[2], m[3], p) != cudaSuccess)
+    return SSD_ERR_CUDA;
+  return SSD_OK;
+}
+
+template <typename T, int DH>
+static cudaError_t launch_join(const Params& p, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(p.B) * p.NB * p.Dmax * p.Hq;
+  return launch_pdl(k_join<T, DH>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, p);
+}
+
+}  // namespace shr
+}  // namespace ssd
+
+extern "C" size_t ssd_verify_attn_shared_workspace_size(const ssd_attn_shared_args* a) {
+  using namespace ssd;
+  if (shr::validate(a) != SSD_OK) return 0;
+  const int dev = current_device();
+  if (a->B == 0 || dev < 0) return sizeof(WsHeader);
+  return shr::layout(a, shr::grid_of(a, shr::sm_count(dev))).total;
+}
+
+extern "C" int ssd_verify_attn_shared(const ssd_attn_shared_args* a, void* ws, size_t ws_bytes, void* stream) {
+  using namespace ssd;
+  const int rc = shr::validate(a);
+  if (rc != SSD_OK) return rc;
+  if (a->B == 0) return SSD_OK;
+  const int64_t es = a->dtype == SSD_BF16 ? 2 : 4, NT = static_cast<int64_t>(a->NB) * a->Dmax;
+  const int64_t rows = a->B * NT * a->Hq * a->dh, cand = a->B * NT * a->Hkv * a->dh * es, row = static_cast<int64_t>(a->Hkv) * a->dh * es;
+  const int64_t own = a->block_table != nullptr ? a->num_pages * 128 * row : a->B * a->P_max * row;
+  const Span spans[] = {{a->out, rows * (a->out_dtype == SSD_F32 ? 4 : 2)}, {a->q, rows * es}, {a->k_shared, a->S_max * row}, {a->v_shared, a->S_max * row},
+                        {a->k_cache, own}, {a->v_cache, own}, {a->k_cand, cand}, {a->v_cand, cand}, {a->shared_len, 4}, {a->prefix_len, 4LL * a->B},
+                        {a->blk_len, 4LL * a->B * a->NB}, {a->shared_table, 4LL * a->shared_pages}, {a->block_table, 4LL * a->B * a->pages_per_seq}};
+  if (overlap(spans, 1, 13)) return SSD_ERR_INVALID;
+  const int dev = current_device();
+  if (dev < 0) return SSD_ERR_CUDA;
+  const int ctas = shr::grid_of(a, shr::sm_count(dev));
+  if (ctas < 1) return SSD_ERR_CUDA;
+  const shr::Layout L = shr::layout(a, ctas);
+  if (L.units >= (1LL << 30) || rows / a->dh >= (1LL << 31)) return SSD_ERR_UNSUPPORTED;
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < L.total) return SSD_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* w = static_cast<char*>(ws);
+  shr::Params p = {};
+  p.q = a->q;
+  p.k_shared = a->k_shared;
+  p.v_shared = a->v_shared;
+  p.k_cache = a->k_cache;
+  p.v_cache = a->v_cache;
+  p.k_cand = a->k_cand;
+  p.v_cand = a->v_cand;
+  p.out = a->out;
+  p.shared_len = a->shared_len;
+  p.prefix_len = a->prefix_len;
+  p.blk_len = a->blk_len;
+  p.shared_table = a->shared_table;
+  p.block_table = a->block_table;
+  p.B = a->B;
+  p.NB = a->NB;
+  p.Dmax = a->Dmax;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.G = a->Hq / a->Hkv;
+  p.tokens = shr::kTile / p.G;
+  p.S_max = a->S_max;
+  p.P_max = a->P_max;
+  p.num_pages = a->num_pages;
+  p.shared_pages = a->shared_pages;
+  p.pages_per_seq = a->pages_per_seq;
+  p.scale_log2 = (a->scale != 0.f ? a->scale : 1.f / sqrtf(static_cast<float>(a->dh))) * kLog2e;
+  p.out_f32 = a->out_dtype == SSD_F32;
+  p.ctas = ctas;
+  p.hdr = static_cast<WsHeader*>(ws);
+  p.plan = reinterpret_cast<int32_t*>(w + L.plan);
+  p.tok = reinterpret_cast<int32_t*>(w + L.tok);
+  p.tok_first = reinterpret_cast<int32_t*>(w + L.tok_first);
+  p.unit0 = reinterpret_cast<int32_t*>(w + L.unit0);
+  p.ph0 = reinterpret_cast<int32_t*>(w + L.ph0);
+  p.own_len = reinterpret_cast<int32_t*>(w + L.own_len);
+  p.ml = reinterpret_cast<float*>(w + L.ml);
+  p.o = reinterpret_cast<float*>(w + L.o);
+  if (launch_pdl(shr::k_plan, dim3(1), dim3(shr::kPlanThreads), 0, s, p) != cudaSuccess) return SSD_ERR_CUDA;
+  if (a->dtype == SSD_BF16) {
+    const int e = a->dh == 64 ? shr::launch_parts<64>(p, a, s) : shr::launch_parts<128>(p, a, s);
+    if (e != SSD_OK) return e;
+  } else {
+    KernelTimer timer(SSD_KERNEL_ATTN_SHARED, s);
+    const cudaError_t e = a->dh == 64 ? launch_pdl(shr::k_parts_simt<64>, dim3(ctas), dim3(shr::kSimtThreads), 0, s, p)
+                                      : launch_pdl(shr::k_parts_simt<128>, dim3(ctas), dim3(shr::kSimtThreads), 0, s, p);
+    if (e != cudaSuccess) return SSD_ERR_CUDA;
+  }
+  cudaError_t e;
+  if (a->dtype == SSD_BF16) e = a->dh == 64 ? shr::launch_join<uint16_t, 64>(p, s) : shr::launch_join<uint16_t, 128>(p, s);
+  else e = a->dh == 64 ? shr::launch_join<float, 64>(p, s) : shr::launch_join<float, 128>(p, s);
+  if (e != cudaSuccess) return SSD_ERR_CUDA;
+  count_launch(3);
+  return check_launch();
+}
