@@ -12,7 +12,7 @@
 //             both fill the GPU whatever their sizes. Where a run crosses from one pair (and head) to
 //             the next, a segment ends and its (m, l, O) go to the workspace;
 //   k_join    a warp a row: the segments of its shared and own keys, and its own block.
-// k_parts, 320 threads, all 512 columns of TMEM: warps 0-3 and 4-7 hold a row tile each (a thread a row):
+// k_parts, 384 threads, all 512 columns of TMEM: warps 0-3 and 4-7 hold a row tile each (a thread a row):
 // scores of 128 keys from TMEM into registers, running maximum, P as bf16 pairs over the scores' own
 // columns, O rescaled in TMEM only when a maximum grew by more than 2^8; warp 8 fetches K and V tiles by
 // TMA into a ring of five; warp 9 issues the products, those of one tile while the other's softmax
@@ -34,7 +34,7 @@ namespace shr {
 using namespace tc;
 
 constexpr int kTile = 128;                 // keys of a tile, packed rows of a row tile
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kSlots = 5;                  // ring of K and V tiles
 constexpr int kSegs = 40;                  // segments a CTA has described at once
 constexpr int kMaxBatch = 4096;            // sequences: their offsets fit the ring before it is used
@@ -265,6 +265,52 @@ __device__ __forceinline__ void wait_anyway(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// two fp32 numbers in one register pair, one instruction for both
+typedef uint64_t f32x2;
+__device__ __forceinline__ f32x2 two(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void apart(f32x2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 2^x of a pair with x <= 2^6, on the FMA pipes: x = n + r, |r| <= 1/2, and a cubic for 2^r with a relative
+// error of 7.5e-5 (2^-13.7; the result is rounded to 8 bits). Below 2^-125: that. NaN becomes infinity or NaN.
+// The exponential unit makes 4 results a clock and scheduler, 1024 clocks for a row tile of 128 keys: as
+// long as one of its two products takes, twice a unit of work. With 3 of 8 pairs computed here neither waits
+// for the other.
+constexpr int kPolyOf8 = 3;
+__device__ __forceinline__ void exp2_pair(f32x2 x, float& e0, float& e1) {
+  constexpr float kMagic = 12582912.f;
+  float x0, x1, m0, m1, p0, p1;
+  apart(x, x0, x1);
+  x = two(max_nan(x0, -125.f), max_nan(x1, -125.f));
+  const f32x2 magic = two(kMagic, kMagic), m = add2(x, magic);
+  const f32x2 r = add2(x, fma2(m, two(-1.f, -1.f), magic));
+  f32x2 q = fma2(two(0.05517167f, 0.05517167f), r, two(0.24261113f, 0.24261113f));
+  q = fma2(q, r, two(0.69326099f, 0.69326099f));
+  q = fma2(q, r, two(0.99992807f, 0.99992807f));
+  apart(m, m0, m1);
+  apart(q, p0, p1);
+  e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(m0) << 23));
+  e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(m1) << 23));
+}
+
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1)
 k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUtensorMap map_vs, const __grid_constant__ CUtensorMap map_k,
@@ -378,36 +424,64 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
         for (int j = s.j0; j < s.j1; ++j) {
           wait(bars, &bars.s_full[t], tiles & 1, p.hdr, 610);
           tc_fence_after();
-          uint32_t v[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(sc + 32 * c, v + 32 * c);
-          tmem_wait_ld();
+          // the scores are read twice, 64 at a time: all 128 at once leave the thread without registers
           const int hi = s.len - j * kTile;
-          if (hi < kTile) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c >= hi) v[c] = 0xff800000u;
-          }
+          uint32_t v[64];
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto read = [&](int h) {
+            tmem_ld32(sc + 64 * h, v);
+            tmem_ld32(sc + 64 * h + 32, v + 32);
+            tmem_wait_ld();
+            if (hi < 64 * h + 64) {
 #pragma unroll
-          for (int c = 0; c < 128; c += 2) mx[(c >> 1) & 3] = fmaxf(mx[(c >> 1) & 3], fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+              for (int c = 0; c < 64; ++c)
+                if (64 * h + c >= hi) v[c] = 0xff800000u;
+            }
+          };
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            read(h);
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) mx[(c >> 1) & 3] = fmaxf(mx[(c >> 1) & 3], fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+          }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
           // the reference moves only when the maximum grows by more than 2^8
           const bool need = top > m + 8.f || m == -INFINITY;
           const float ref = need ? fmaxf(m, top) : m;
           const float alpha = need && m > -INFINITY ? ex2_approx(m - ref) : 1.f;     // nothing counted yet: O and l are 0
           const float sub = ref > -INFINITY ? ref : 0.f;    // every key at -inf: all weights 0
-          float rs[4] = {0.f, 0.f, 0.f, 0.f};
+          f32x2 rs[2] = {two(0.f, 0.f), two(0.f, 0.f)};
+          const f32x2 slope = two(p.scale_log2, p.scale_log2), shift = two(-sub, -sub);
+          // P of keys 64 h .. goes over the scores 32 h .., which have been read for the last time
 #pragma unroll
-          for (int c = 0; c < 128; c += 2) {
-            const uint32_t w = pack_bf16(ex2_approx(fmaf(__uint_as_float(v[c]), p.scale_log2, -sub)),
-                                         ex2_approx(fmaf(__uint_as_float(v[c + 1]), p.scale_log2, -sub)));
-            rs[(c >> 1) & 1] += __uint_as_float(w << 16);
-            rs[2 + ((c >> 1) & 1)] += __uint_as_float(w & 0xffff0000u);
-            v[c >> 1] = w;
+          for (int h = 0; h < 2; ++h) {
+            read(h);
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              const f32x2 x = fma2(two(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), slope, shift);
+              float e0, e1;
+              if ((c >> 1) % 8 < kPolyOf8) {
+                exp2_pair(x, e0, e1);
+              } else {
+                apart(x, e0, e1);
+                e0 = ex2_approx(e0);
+                e1 = ex2_approx(e1);
+              }
+              const uint32_t w = pack_bf16(e0, e1);
+              rs[(c >> 1) & 1] = add2(rs[(c >> 1) & 1], two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
+              v[c >> 1] = w;
+            }
+            if (ref == -INFINITY) {
+              // no key above -inf yet: weights 0, which the polynomial does not reach
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = 0;
+            }
+            tmem_st32(sc + 32 * h, v);
           }
-          tmem_st32(sc, v);
-          tmem_st32(sc + 32, v + 32);
+          float sum0, sum1;
+          apart(add2(rs[0], rs[1]), sum0, sum1);
+          float sum = sum0 + sum1;
+          if (ref == -INFINITY) sum = sum < 1.f ? 0.f : NAN;           // scores that are no number stay so
           if (j > s.j0) {
             if (__any_sync(0xffffffffu, need)) {
               // O holds the sum up to the tile before: wait for that product, then rescale
@@ -424,7 +498,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
               }
             }
           }
-          l = l * alpha + ((rs[0] + rs[1]) + (rs[2] + rs[3]));
+          l = l * alpha + sum;
           m = ref;
           tmem_wait_st();
           tc_fence_before();
@@ -478,6 +552,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
       __syncwarp();
     } else if (warp == 9) {
       // -------------------------------------------------------- products: the whole warp waits, one lane issues
+      const uint32_t lead = elect_one();
       constexpr uint32_t idS = idesc_bf16(false, kTile), idPV = idesc_bf16(true, DH);
       for (int i = 0; i < nseg; ++i) {
         const Seg s = bars.segs[i];
@@ -487,16 +562,15 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
           const uint32_t e = it + 2 * jj, slot = e % kSlots;
           wait(bars, &bars.full[slot], (e / kSlots) & 1, p.hdr, 630);
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t kb = sbase + Sh::OFF_RING + slot * Sh::kTileB, qb = sbase + Sh::OFF_Q + t * Sh::kTileB;
+          const uint64_t kd = sw128_desc(sbase + Sh::OFF_RING + slot * Sh::kTileB, 16, 1024);
+          const uint64_t qd = sw128_desc(sbase + Sh::OFF_Q + t * Sh::kTileB, 16, 1024);
 #pragma unroll
-            for (int ks = 0; ks < DH / 16; ++ks)
-              mma_bf16(tmem + TM_S + t * 128, sw128_desc(qb + (ks >> 2) * Sh::kHalf + (ks & 3) * 32, 16, 1024),
-                       sw128_desc(kb + (ks >> 2) * Sh::kHalf + (ks & 3) * 32, 16, 1024), idS, ks > 0 ? 1u : 0u);
-            mma_commit(&bars.s_full[t]);
-            if (t == nt - 1) mma_commit(&bars.empty[slot]);
+          for (int ks = 0; ks < DH / 16; ++ks) {
+            const uint32_t step = ((ks >> 2) * Sh::kHalf + (ks & 3) * 32) >> 4;      // addresses in 16 bytes; no carry: all below 2^18
+            mma_bf16_warp(tmem + TM_S + t * 128, qd + step, kd + step, idS, ks > 0 ? 1u : 0u, lead);
           }
-          __syncwarp();
+          mma_commit_warp(&bars.s_full[t], lead);
+          if (t == nt - 1) mma_commit_warp(&bars.empty[slot], lead);
         };
         for (int t = 0; t < nt; ++t) {
           wait(bars, &bars.q_full[t], (ph_q >> t) & 1, p.hdr, 631);
@@ -530,15 +604,13 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
               used |= 1u << t;
             }
             tc_fence_after();
-            if (lane == 0) {
-              const uint32_t vb = sbase + Sh::OFF_RING + slot * Sh::kTileB, pa = tmem + TM_S + t * 128;
+            const uint64_t vd = sw128_desc(sbase + Sh::OFF_RING + slot * Sh::kTileB, Sh::kHalf, 1024);
+            const uint32_t pa = tmem + TM_S + t * 128;
 #pragma unroll
-              for (int ks = 0; ks < kTile / 16; ++ks)
-                mma_bf16_ts(tmem + TM_O + t * 128, pa + ks * 8, sw128_desc(vb + ks * 16 * 128, Sh::kHalf, 1024), idPV, (jj > 0 || ks > 0) ? 1u : 0u);
-              mma_commit(&bars.pv_done[t]);
-              if (t == nt - 1) mma_commit(&bars.empty[slot]);
-            }
-            __syncwarp();
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              mma_bf16_ts_warp(tmem + TM_O + t * 128, pa + ks * 8, vd + ks * (16 * 128 >> 4), idPV, (jj > 0 || ks > 0) ? 1u : 0u, lead);
+            mma_commit_warp(&bars.pv_done[t], lead);
+            if (t == nt - 1) mma_commit_warp(&bars.empty[slot], lead);
             // the scores of the next tile go over P: products of one thread run in the order issued
             if (jj + 1 < nj) scores(t, jj + 1);
           }
@@ -554,8 +626,8 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
   // copies in flight end before the CTA does, also after a wait that gave up
   if (warp == 8 && lane == 0)
     for (uint32_t e = it > kSlots ? it - kSlots : 0; e < it; ++e) wait_anyway(&bars.full[e % kSlots], (e / kSlots) & 1);
-  if (warp == 9 && lane == 0 && used != 0) {
-    mma_commit(&bars.last);
+  if (warp == 9 && used != 0) {
+    mma_commit_warp(&bars.last, elect_one());
     wait_anyway(&bars.last, 0);
   }
   tc_fence_before();
