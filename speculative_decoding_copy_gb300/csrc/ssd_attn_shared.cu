@@ -12,10 +12,10 @@
 //             both fill the GPU whatever their sizes. Where a run crosses from one pair (and head) to
 //             the next, a segment ends and its (m, l, O) go to the workspace;
 //   k_join    a warp a row: the segments of its shared and own keys, and its own block.
-// k_parts, 384 threads, all 512 columns of TMEM: warps 0-3 and 4-7 hold a row tile each (a thread a row):
-// scores of 128 keys from TMEM into registers, running maximum, P as bf16 pairs over the scores' own
-// columns, O rescaled in TMEM only when a maximum grew by more than 2^8; warp 8 fetches K and V tiles by
-// TMA into a ring of five; warp 9 issues the products, those of one tile while the other's softmax
+// k_parts, 576 threads, all 512 columns of TMEM: warps 0-7 and 8-15 hold a row tile each (two threads a row,
+// 64 of a tile's 128 keys each): scores from TMEM into registers, the row's maximum between the two
+// threads, P as bf16 pairs over the scores' own columns, O rescaled in TMEM only when a maximum grew by
+// more than 2^8; warp 16 fetches K and V tiles by TMA into a ring of five; warp 17 issues the products, those of one tile while the other's softmax
 // runs, and before that zeroes the value rows behind a length (0 times NaN is NaN).
 // Every wait is bounded; after one that gave up the CTA records SSD_ERR_TIMEOUT, waits (bounded) for its
 // copies and products in flight and ends.
@@ -34,9 +34,10 @@ namespace shr {
 using namespace tc;
 
 constexpr int kTile = 128;                 // keys of a tile, packed rows of a row tile
-constexpr int kThreads = 384;
+constexpr int kThreads = 576;
 constexpr int kSlots = 5;                  // ring of K and V tiles
-constexpr int kSegs = 40;                  // segments a CTA has described at once
+constexpr int kBarBytes = 3072;
+constexpr int kSegs = 20;                  // segments a CTA has described at once
 constexpr int kMaxBatch = 4096;            // sequences: their offsets fit the ring before it is used
 constexpr unsigned long long kWaitClocks = 1ull << 32;
 
@@ -237,9 +238,10 @@ struct Bars {
   uint64_t last;
   uint32_t tmem_base;
   int failed, count, next;
+  float pair[2][256];                      // of each row tile: a number of every thread for the row's other one
   Seg segs[kSegs];
 };
-static_assert(sizeof(Bars) <= 2048, "barriers and segments");
+static_assert(sizeof(Bars) <= kBarBytes, "barriers and segments");
 
 template <int DH>
 struct Shape {
@@ -249,7 +251,7 @@ struct Shape {
   static constexpr uint32_t OFF_Q = 0;                      // two row tiles
   static constexpr uint32_t OFF_RING = 2 * kTileB;
   static constexpr uint32_t OFF_BAR = OFF_RING + kSlots * kTileB;
-  static constexpr uint32_t kSmem = OFF_BAR + 2048 + 1024;  // + slack to align the base to 1024
+  static constexpr uint32_t kSmem = OFF_BAR + kBarBytes;    // the base is 1024-byte aligned: there is no static shared memory  // + slack to align the base to 1024
 };
 static_assert(Shape<128>::kSmem <= 232448, "shared memory per CTA");
 static_assert(4 * (kMaxBatch + 1) * 4 <= kSlots * static_cast<int>(Shape<64>::kTileB), "offsets fit the ring");
@@ -283,44 +285,20 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// 2^x of a pair with x <= 2^6, on the FMA pipes: x = n + r, |r| <= 1/2, and a cubic for 2^r with a relative
-// error of 7.5e-5 (2^-13.7; the result is rounded to 8 bits). Below 2^-125: that. NaN becomes infinity or NaN.
-// The exponential unit makes 4 results a clock and scheduler, 1024 clocks for a row tile of 128 keys: as
-// long as one of its two products takes, twice a unit of work. With 3 of 8 pairs computed here neither waits
-// for the other.
-constexpr int kPolyOf8 = 3;
-__device__ __forceinline__ void exp2_pair(f32x2 x, float& e0, float& e1) {
-  constexpr float kMagic = 12582912.f;
-  float x0, x1, m0, m1, p0, p1;
-  apart(x, x0, x1);
-  x = two(max_nan(x0, -125.f), max_nan(x1, -125.f));
-  const f32x2 magic = two(kMagic, kMagic), m = add2(x, magic);
-  const f32x2 r = add2(x, fma2(m, two(-1.f, -1.f), magic));
-  f32x2 q = fma2(two(0.05517167f, 0.05517167f), r, two(0.24261113f, 0.24261113f));
-  q = fma2(q, r, two(0.69326099f, 0.69326099f));
-  q = fma2(q, r, two(0.99992807f, 0.99992807f));
-  apart(m, m0, m1);
-  apart(q, p0, p1);
-  e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(m0) << 23));
-  e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(m1) << 23));
-}
-
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1)
 k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUtensorMap map_vs, const __grid_constant__ CUtensorMap map_k,
         const __grid_constant__ CUtensorMap map_v, Params p) {
   using Sh = Shape<DH>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw;
   const uint32_t sbase = smem_u32(smem);
   Bars& bars = *reinterpret_cast<Bars*>(smem + Sh::OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  if ((sbase & 1023) != 0) {               // swizzled tiles need it
+    if (tid == 0) record_error(p.hdr, SSD_ERR_DEVICE, 604);
+    return;
+  }
 
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
@@ -329,16 +307,16 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars.s_full[t], 1);
-      mbar_init(&bars.p_full[t], 128);
+      mbar_init(&bars.p_full[t], 256);
       mbar_init(&bars.pv_done[t], 1);
-      mbar_init(&bars.q_full[t], 128);
-      mbar_init(&bars.o_free[t], 128);
+      mbar_init(&bars.q_full[t], 256);
+      mbar_init(&bars.o_free[t], 256);
     }
     mbar_init(&bars.last, 1);
     bars.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) {
+  if (warp == 16) {
     if (lane == 0) {
       prefetch_tmap(&map_ks);
       prefetch_tmap(&map_vs);
@@ -381,32 +359,34 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
     u = bars.next;
     const int nseg = bars.count;
 
-    if (warp < 8) {
-      // -------------------------------------------------------- softmax rows
-      const int t = warp >> 2;                              // row tile
-      const int wr = (warp & 3) * 32;                       // this warp's first row
-      const uint32_t lane_off = static_cast<uint32_t>(wr) << 16;
-      const uint32_t sc = tmem + TM_S + t * 128 + lane_off, oc = tmem + TM_O + t * 128 + lane_off;
-      // rows of tile t of a segment: G heads of each of its tokens
+    if (warp < 16) {
+      // -------------------------------------------------------- softmax rows: two threads a row
+      const int t = warp >> 3, half = (warp >> 2) & 1;      // row tile; keys 0-63 or 64-127 of a key tile
+      const int r = (warp & 3) * 32 + lane;                 // this thread's row
+      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t sc = tmem + TM_S + t * 128 + lane_off, oc = tmem + TM_O + t * 128 + half * (DH / 2) + lane_off;
+      float* pair_max = bars.pair[t];                       // [2][128]
+      auto tile_sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory"); };
+      // rows of tile t of a segment: G heads of each of its tokens; a warp brings sixteen
       auto load_q = [&](const Seg& s) {
         const int nrow = min(p.tokens, s.ntok - t * p.tokens) * p.G;
-        const int r = wr + lane;
-        const int token = r < nrow ? __ldcg(p.tok + s.tok0 + t * p.tokens + r / p.G) : -1;
+        const int w0 = (warp & 7) * 16, mine = w0 + (lane & 15);
+        const int token = mine < nrow ? __ldcg(p.tok + s.tok0 + t * p.tokens + mine / p.G) : -1;
         constexpr int CH = DH / 8;                          // 16-byte pieces of a row
         constexpr int RI = 32 / CH;                         // rows of one round
-        uint4 v[CH];
+        uint4 v[16 / RI];
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
+        for (int i = 0; i < 16 / RI; ++i) {
           const int rr = i * RI + lane / CH;
           const int tk = __shfl_sync(0xffffffffu, token, rr);
           v[i] = make_uint4(0, 0, 0, 0);
           if (tk >= 0)
             v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                        (static_cast<int64_t>(tk) * p.Hq + s.kvh * p.G + (wr + rr) % p.G) * DH) + lane % CH);
+                                                        (static_cast<int64_t>(tk) * p.Hq + s.kvh * p.G + (w0 + rr) % p.G) * DH) + lane % CH);
         }
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int rr = wr + i * RI + lane / CH, ch = lane % CH;
+        for (int i = 0; i < 16 / RI; ++i) {
+          const int rr = w0 + i * RI + lane / CH, ch = lane % CH;
           *reinterpret_cast<uint4*>(smem + Sh::OFF_Q + t * Sh::kTileB + (ch >> 3) * Sh::kHalf + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v[i];
         }
         fence_async_smem();
@@ -424,27 +404,25 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
         for (int j = s.j0; j < s.j1; ++j) {
           wait(bars, &bars.s_full[t], tiles & 1, p.hdr, 610);
           tc_fence_after();
-          // the scores are read twice, 64 at a time: all 128 at once leave the thread without registers
-          const int hi = s.len - j * kTile;
           uint32_t v[64];
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto read = [&](int h) {
-            tmem_ld32(sc + 64 * h, v);
-            tmem_ld32(sc + 64 * h + 32, v + 32);
-            tmem_wait_ld();
-            if (hi < 64 * h + 64) {
+          tmem_ld32(sc + 64 * half, v);
+          tmem_ld32(sc + 64 * half + 32, v + 32);
+          tmem_wait_ld();
+          const int hi = s.len - j * kTile - 64 * half;
+          if (hi < 64) {
 #pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (64 * h + c >= hi) v[c] = 0xff800000u;
-            }
-          };
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            read(h);
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) mx[(c >> 1) & 3] = fmaxf(mx[(c >> 1) & 3], fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+            for (int c = 0; c < 64; ++c)
+              if (c >= hi) v[c] = 0xff800000u;
           }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) mx[(c >> 1) & 3] = fmaxf(mx[(c >> 1) & 3], fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+          pair_max[half * 128 + r] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // both halves of the row have left TMEM: P may go over the scores
+          tc_fence_before();
+          tile_sync();
+          tc_fence_after();
+          const float top = fmaxf(pair_max[r], pair_max[128 + r]) * p.scale_log2;
           // the reference moves only when the maximum grows by more than 2^8
           const bool need = top > m + 8.f || m == -INFINITY;
           const float ref = need ? fmaxf(m, top) : m;
@@ -452,43 +430,25 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
           const float sub = ref > -INFINITY ? ref : 0.f;    // every key at -inf: all weights 0
           f32x2 rs[2] = {two(0.f, 0.f), two(0.f, 0.f)};
           const f32x2 slope = two(p.scale_log2, p.scale_log2), shift = two(-sub, -sub);
-          // P of keys 64 h .. goes over the scores 32 h .., which have been read for the last time
+          // P of keys 64 half .. + 63 as bf16 pairs over the scores' columns 32 half .. + 31
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            read(h);
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              const f32x2 x = fma2(two(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), slope, shift);
-              float e0, e1;
-              if ((c >> 1) % 8 < kPolyOf8) {
-                exp2_pair(x, e0, e1);
-              } else {
-                apart(x, e0, e1);
-                e0 = ex2_approx(e0);
-                e1 = ex2_approx(e1);
-              }
-              const uint32_t w = pack_bf16(e0, e1);
-              rs[(c >> 1) & 1] = add2(rs[(c >> 1) & 1], two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
-              v[c >> 1] = w;
-            }
-            if (ref == -INFINITY) {
-              // no key above -inf yet: weights 0, which the polynomial does not reach
-#pragma unroll
-              for (int c = 0; c < 32; ++c) v[c] = 0;
-            }
-            tmem_st32(sc + 32 * h, v);
+          for (int c = 0; c < 64; c += 2) {
+            float e0, e1;
+            apart(fma2(two(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), slope, shift), e0, e1);
+            const uint32_t w = pack_bf16(ex2_approx(e0), ex2_approx(e1));
+            rs[(c >> 1) & 1] = add2(rs[(c >> 1) & 1], two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
+            v[c >> 1] = w;
           }
+          tmem_st32(sc + 32 * half, v);
           float sum0, sum1;
           apart(add2(rs[0], rs[1]), sum0, sum1);
-          float sum = sum0 + sum1;
-          if (ref == -INFINITY) sum = sum < 1.f ? 0.f : NAN;           // scores that are no number stay so
           if (j > s.j0) {
             if (__any_sync(0xffffffffu, need)) {
               // O holds the sum up to the tile before: wait for that product, then rescale
               wait(bars, &bars.pv_done[t], (tiles - 1) & 1, p.hdr, 611);
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < DH / 32; ++c) {
+              for (int c = 0; c < DH / 64; ++c) {
                 uint32_t o[32];
                 tmem_ld32(oc + 32 * c, o);
                 tmem_wait_ld();
@@ -498,7 +458,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
               }
             }
           }
-          l = l * alpha + sum;
+          l = l * alpha + (sum0 + sum1);
           m = ref;
           tmem_wait_st();
           tc_fence_before();
@@ -507,29 +467,34 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
         }
         // the last scores are read: Q is free for the next segment, whose first product may start
         if (next < nseg) load_q(bars.segs[next]);
+        tile_sync();                                        // the last maxima are read
+        if (half == 1) pair_max[r] = l;
+        tile_sync();
+        const float l_other = pair_max[r];
         wait(bars, &bars.pv_done[t], (tiles - 1) & 1, p.hdr, 612);
         tc_fence_after();
         const int nrow = min(p.tokens, s.ntok - t * p.tokens) * p.G;
-        const int64_t row = static_cast<int64_t>(s.id) * 256 + t * 128 + wr + lane;
-        const bool keep = wr + lane < nrow && !bars.failed;
+        const int64_t row = static_cast<int64_t>(s.id) * 256 + t * 128 + r;
+        const bool keep = r < nrow && !bars.failed;
 #pragma unroll 1
-        for (int c = 0; c < DH / 32; ++c) {
+        for (int c = 0; c < DH / 64; ++c) {
           uint32_t o[32];
           tmem_ld32(oc + 32 * c, o);
           tmem_wait_ld();
           if (keep) {
-            float4* dst = reinterpret_cast<float4*>(p.o + row * DH + 32 * c);
+            float4* dst = reinterpret_cast<float4*>(p.o + row * DH + half * (DH / 2) + 32 * c);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
           }
         }
-        if (wr + lane < nrow) *reinterpret_cast<float2*>(p.ml + row * 2) = bars.failed ? make_float2(NAN, NAN) : make_float2(m, l);
+        if (half == 0 && r < nrow) *reinterpret_cast<float2*>(p.ml + row * 2) = bars.failed ? make_float2(NAN, NAN) : make_float2(m, l + l_other);
         tc_fence_before();
         mbar_arrive(&bars.o_free[t]);
+        tile_sync();                                        // pair_max is free
         i = next;
       }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
       // -------------------------------------------------------- TMA: K0 V0 K1 V1 ..
       if (lane == 0) {
         for (int i = 0; i < nseg && !bars.failed; ++i) {
@@ -550,7 +515,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
         }
       }
       __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 17) {
       // -------------------------------------------------------- products: the whole warp waits, one lane issues
       const uint32_t lead = elect_one();
       constexpr uint32_t idS = idesc_bf16(false, kTile), idPV = idesc_bf16(true, DH);
@@ -624,15 +589,15 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
   }
 
   // copies in flight end before the CTA does, also after a wait that gave up
-  if (warp == 8 && lane == 0)
+  if (warp == 16 && lane == 0)
     for (uint32_t e = it > kSlots ? it - kSlots : 0; e < it; ++e) wait_anyway(&bars.full[e % kSlots], (e / kSlots) & 1);
-  if (warp == 9 && used != 0) {
+  if (warp == 17 && used != 0) {
     mma_commit_warp(&bars.last, elect_one());
     wait_anyway(&bars.last, 0);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
