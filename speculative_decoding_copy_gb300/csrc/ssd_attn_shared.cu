@@ -14,7 +14,7 @@
 //   k_join    a warp a row: the segments of its shared and own keys, and its own block.
 // k_parts, 576 threads, all 512 columns of TMEM: warps 0-7 and 8-15 hold a row tile each (two threads a row,
 // 64 of a tile's 128 keys each): scores from TMEM into registers, the row's maximum between the two
-// threads, P as bf16 pairs over the scores' own columns, O rescaled in TMEM only when a maximum grew by
+// threads, P as bf16 pairs back into TMEM, O rescaled in TMEM only when a maximum grew by
 // more than 2^8; warp 16 fetches K and V tiles by TMA into a ring of five; warp 17 issues the products, those of one tile while the other's softmax
 // runs, and before that zeroes the value rows behind a length (0 times NaN is NaN).
 // Every wait is bounded; after one that gave up the CTA records SSD_ERR_TIMEOUT, waits (bounded) for its
@@ -234,11 +234,11 @@ __device__ __forceinline__ int64_t tile_row(const Params& p, const Seg& s, int j
 // ------------------------------------------------------------------ parts, tensor cores
 struct Bars {
   uint64_t full[kSlots], empty[kSlots];
-  uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], o_free[2];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full[2], o_free[2];
   uint64_t last;
   uint32_t tmem_base;
   int failed, count, next;
-  float pair[2][256];                      // of each row tile: a number of every thread for the row's other one
+  uint16_t pair[2][2][256];                // of each row tile, in turns: a maximum of every thread, for the row's other one
   Seg segs[kSegs];
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barriers and segments");
@@ -255,7 +255,9 @@ struct Shape {
 };
 static_assert(Shape<128>::kSmem <= 232448, "shared memory per CTA");
 static_assert(4 * (kMaxBatch + 1) * 4 <= kSlots * static_cast<int>(Shape<64>::kTileB), "offsets fit the ring");
-constexpr uint32_t TM_S = 0, TM_O = 256;   // scores of tile 0 and 1 (P over their first 64 columns), O of tile 0 and 1
+// TMEM columns: one buffer of scores, taken by the row tiles in turns (it is free as soon as the scores are in
+// registers, long before their P is made), P of tile 0 and 1 as bf16 pairs, O of tile 0 and 1
+constexpr uint32_t TM_S = 0, TM_P = 128, TM_O = 256;
 
 __device__ __forceinline__ bool wait(Bars& bars, uint64_t* bar, uint32_t parity, WsHeader* hdr, int where) {
   return mbar_wait_bounded(bar, parity, &bars.failed, hdr, where, kWaitClocks);
@@ -280,6 +282,11 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   f32x2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -294,7 +301,8 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
   uint8_t* smem = smem_raw;
   const uint32_t sbase = smem_u32(smem);
   Bars& bars = *reinterpret_cast<Bars*>(smem + Sh::OFF_BAR);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  // (by a shuffle: the compiler then knows it, and what follows from it, to be the same for the warp)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, cta = blockIdx.x;
   if ((sbase & 1023) != 0) {               // swizzled tiles need it
     if (tid == 0) record_error(p.hdr, SSD_ERR_DEVICE, 604);
     return;
@@ -307,6 +315,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars.s_full[t], 1);
+      mbar_init(&bars.s_free[t], 256);
       mbar_init(&bars.p_full[t], 256);
       mbar_init(&bars.pv_done[t], 1);
       mbar_init(&bars.q_full[t], 256);
@@ -329,7 +338,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the plan
   const int share = __ldcg(p.plan + kShare), units = __ldcg(p.plan + kUnits), tokens = __ldcg(p.plan + kTokens);
   const int shared_len = __ldcg(p.plan + kSharedLen);
@@ -339,7 +348,8 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
 
   // phases, each role its own: ring entries so far; of the softmax warps the tiles so far; of the
   // products one bit a row tile
-  uint32_t it = 0, tiles = 0, ph_p = 0, ph_q = 0, ph_o = 0, used = 0;
+  int last = -1;                                            // tile of the last scores
+  uint32_t it = 0, tiles = 0, ph_s = 0, ph_p = 0, ph_q = 0, ph_o = 0, used = 0;
 
   bool more = u < u1;
   while (more) {
@@ -364,8 +374,8 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
       const int t = warp >> 3, half = (warp >> 2) & 1;      // row tile; keys 0-63 or 64-127 of a key tile
       const int r = (warp & 3) * 32 + lane;                 // this thread's row
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t sc = tmem + TM_S + t * 128 + lane_off, oc = tmem + TM_O + t * 128 + half * (DH / 2) + lane_off;
-      float* pair_max = bars.pair[t];                       // [2][128]
+      const uint32_t sc = tmem + TM_S + 64 * half + lane_off, pc = tmem + TM_P + 64 * t + 32 * half + lane_off;
+      const uint32_t oc = tmem + TM_O + t * 128 + half * (DH / 2) + lane_off;
       auto tile_sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory"); };
       // rows of tile t of a segment: G heads of each of its tokens; a warp brings sixteen
       auto load_q = [&](const Seg& s) {
@@ -405,9 +415,11 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
           wait(bars, &bars.s_full[t], tiles & 1, p.hdr, 610);
           tc_fence_after();
           uint32_t v[64];
-          tmem_ld32(sc + 64 * half, v);
-          tmem_ld32(sc + 64 * half + 32, v + 32);
+          tmem_ld32(sc, v);
+          tmem_ld32(sc + 32, v + 32);
           tmem_wait_ld();
+          tc_fence_before();
+          mbar_arrive(&bars.s_free[t]);
           const int hi = s.len - j * kTile - 64 * half;
           if (hi < 64) {
 #pragma unroll
@@ -416,13 +428,12 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) mx[(c >> 1) & 3] = fmaxf(mx[(c >> 1) & 3], fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
-          pair_max[half * 128 + r] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // both halves of the row have left TMEM: P may go over the scores
-          tc_fence_before();
+          for (int c = 0; c < 64; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+          // (as bf16: any common reference near the maximum serves; two buffers, as a thread may be a tile ahead)
+          uint16_t* pair = bars.pair[t][tiles & 1];
+          pair[half * 128 + r] = static_cast<uint16_t>(__float_as_uint(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3])) >> 16);
           tile_sync();
-          tc_fence_after();
-          const float top = fmaxf(pair_max[r], pair_max[128 + r]) * p.scale_log2;
+          const float top = fmaxf(bf16_to_f32(pair[r]), bf16_to_f32(pair[128 + r])) * p.scale_log2;
           // the reference moves only when the maximum grows by more than 2^8
           const bool need = top > m + 8.f || m == -INFINITY;
           const float ref = need ? fmaxf(m, top) : m;
@@ -430,7 +441,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
           const float sub = ref > -INFINITY ? ref : 0.f;    // every key at -inf: all weights 0
           f32x2 rs[2] = {two(0.f, 0.f), two(0.f, 0.f)};
           const f32x2 slope = two(p.scale_log2, p.scale_log2), shift = two(-sub, -sub);
-          // P of keys 64 half .. + 63 as bf16 pairs over the scores' columns 32 half .. + 31
+          // P of keys 64 half .. + 63 as bf16 pairs
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
             float e0, e1;
@@ -439,14 +450,16 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
             rs[(c >> 1) & 1] = add2(rs[(c >> 1) & 1], two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
             v[c >> 1] = w;
           }
-          tmem_st32(sc + 32 * half, v);
+          // the product before has read the last P, and O holds the sum up to it
+          if (tiles > 0) {
+            wait(bars, &bars.pv_done[t], (tiles - 1) & 1, p.hdr, 611);
+            tc_fence_after();
+          }
+          tmem_st32(pc, v);
           float sum0, sum1;
           apart(add2(rs[0], rs[1]), sum0, sum1);
           if (j > s.j0) {
             if (__any_sync(0xffffffffu, need)) {
-              // O holds the sum up to the tile before: wait for that product, then rescale
-              wait(bars, &bars.pv_done[t], (tiles - 1) & 1, p.hdr, 611);
-              tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < DH / 64; ++c) {
                 uint32_t o[32];
@@ -468,9 +481,10 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
         // the last scores are read: Q is free for the next segment, whose first product may start
         if (next < nseg) load_q(bars.segs[next]);
         tile_sync();                                        // the last maxima are read
-        if (half == 1) pair_max[r] = l;
+        float* sums = reinterpret_cast<float*>(bars.pair[t]);
+        if (half == 1) sums[r] = l;
         tile_sync();
-        const float l_other = pair_max[r];
+        const float l_other = sums[r];
         wait(bars, &bars.pv_done[t], (tiles - 1) & 1, p.hdr, 612);
         tc_fence_after();
         const int nrow = min(p.tokens, s.ntok - t * p.tokens) * p.G;
@@ -491,7 +505,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
         if (half == 0 && r < nrow) *reinterpret_cast<float2*>(p.ml + row * 2) = bars.failed ? make_float2(NAN, NAN) : make_float2(m, l + l_other);
         tc_fence_before();
         mbar_arrive(&bars.o_free[t]);
-        tile_sync();                                        // pair_max is free
+        tile_sync();                                        // and the sums
         i = next;
       }
     } else if (warp == 16) {
@@ -501,16 +515,17 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
           const Seg s = bars.segs[i];
           const CUtensorMap* mk = s.b < 0 ? &map_ks : &map_k;
           const CUtensorMap* mv = s.b < 0 ? &map_vs : &map_v;
-          for (int j = s.j0; j < s.j1 && !bars.failed; ++j) {
-            const int y = static_cast<int>(tile_row(p, s, j));
-            for (int kv = 0; kv < 2; ++kv, ++it) {
-              const int slot = it % kSlots;
-              if (it >= kSlots && !wait(bars, &bars.empty[slot], ((it / kSlots) - 1) & 1, p.hdr, 620)) break;
-              const uint32_t dst = sbase + Sh::OFF_RING + slot * Sh::kTileB;
-              mbar_expect_tx(&bars.full[slot], Sh::kTileB);
+          const int nj = s.j1 - s.j0;
+          // in the order of use: K0 K1 V0 K2 V1 .. V of the last tile
+          for (int e = 0; e < 2 * nj && !bars.failed; ++e, ++it) {
+            const bool is_k = e == 0 || ((e & 1) && e < 2 * nj - 1);
+            const int j = s.j0 + (is_k ? (e + 1) / 2 : e == 2 * nj - 1 ? nj - 1 : e / 2 - 1);
+            const int y = static_cast<int>(tile_row(p, s, j)), slot = it % kSlots;
+            if (it >= kSlots && !wait(bars, &bars.empty[slot], ((it / kSlots) - 1) & 1, p.hdr, 620)) break;
+            const uint32_t dst = sbase + Sh::OFF_RING + slot * Sh::kTileB;
+            mbar_expect_tx(&bars.full[slot], Sh::kTileB);
 #pragma unroll
-              for (uint32_t h = 0; h < Sh::kHalves; ++h) tma_load_2d(dst + h * Sh::kHalf, kv == 0 ? mk : mv, 64 * h, y, &bars.full[slot]);
-            }
+            for (uint32_t h = 0; h < Sh::kHalves; ++h) tma_load_2d(dst + h * Sh::kHalf, is_k ? mk : mv, 64 * h, y, &bars.full[slot]);
           }
         }
       }
@@ -521,18 +536,23 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
       constexpr uint32_t idS = idesc_bf16(false, kTile), idPV = idesc_bf16(true, DH);
       for (int i = 0; i < nseg; ++i) {
         const Seg s = bars.segs[i];
-        const int nt = s.ntok > p.tokens ? 2 : 1, nj = s.j1 - s.j0;
-        // K of tile j is ring entry it + 2 (j - j0), V the one behind it
+        const int nt = __shfl_sync(0xffffffffu, s.ntok > p.tokens ? 2 : 1, 0), nj = __shfl_sync(0xffffffffu, s.j1 - s.j0, 0);
         auto scores = [&](int t, int jj) {
-          const uint32_t e = it + 2 * jj, slot = e % kSlots;
+          const uint32_t e = it + (jj == 0 ? 0 : 2 * jj - 1), slot = e % kSlots;
           wait(bars, &bars.full[slot], (e / kSlots) & 1, p.hdr, 630);
+          // the scores before, of whichever tile, are in registers
+          if (last >= 0) {
+            wait(bars, &bars.s_free[last], (ph_s >> last) & 1, p.hdr, 636);
+            ph_s ^= 1u << last;
+          }
+          last = t;
           tc_fence_after();
           const uint64_t kd = sw128_desc(sbase + Sh::OFF_RING + slot * Sh::kTileB, 16, 1024);
           const uint64_t qd = sw128_desc(sbase + Sh::OFF_Q + t * Sh::kTileB, 16, 1024);
 #pragma unroll
           for (int ks = 0; ks < DH / 16; ++ks) {
             const uint32_t step = ((ks >> 2) * Sh::kHalf + (ks & 3) * 32) >> 4;      // addresses in 16 bytes; no carry: all below 2^18
-            mma_bf16_warp(tmem + TM_S + t * 128, qd + step, kd + step, idS, ks > 0 ? 1u : 0u, lead);
+            mma_bf16_warp(tmem + TM_S, qd + step, kd + step, idS, ks > 0 ? 1u : 0u, lead);
           }
           mma_commit_warp(&bars.s_full[t], lead);
           if (t == nt - 1) mma_commit_warp(&bars.empty[slot], lead);
@@ -543,8 +563,10 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
           scores(t, 0);
         }
         for (int jj = 0; jj < nj; ++jj) {
-          const uint32_t e = it + 2 * jj + 1, slot = e % kSlots;
+          const uint32_t e = it + (jj == nj - 1 ? 2 * nj - 1 : 2 * jj + 2), slot = e % kSlots;
           for (int t = 0; t < nt; ++t) {
+            // the next scores first: they need nothing of this tile's softmax but its reading of the last ones
+            if (jj + 1 < nj) scores(t, jj + 1);
             if (t == 0) {
               wait(bars, &bars.full[slot], (e / kSlots) & 1, p.hdr, 634);
               const int r0 = s.len - (s.j0 + jj) * kTile;
@@ -570,14 +592,12 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
             }
             tc_fence_after();
             const uint64_t vd = sw128_desc(sbase + Sh::OFF_RING + slot * Sh::kTileB, Sh::kHalf, 1024);
-            const uint32_t pa = tmem + TM_S + t * 128;
+            const uint32_t pa = tmem + TM_P + 64 * t;
 #pragma unroll
             for (int ks = 0; ks < kTile / 16; ++ks)
               mma_bf16_ts_warp(tmem + TM_O + t * 128, pa + ks * 8, vd + ks * (16 * 128 >> 4), idPV, (jj > 0 || ks > 0) ? 1u : 0u, lead);
             mma_commit_warp(&bars.pv_done[t], lead);
             if (t == nt - 1) mma_commit_warp(&bars.empty[slot], lead);
-            // the scores of the next tile go over P: products of one thread run in the order issued
-            if (jj + 1 < nj) scores(t, jj + 1);
           }
         }
         it += 2 * nj;
