@@ -56,7 +56,7 @@ struct Params {
   int32_t* tok;                            // the present tokens b * NT + t
   int32_t *tok_first, *unit0, *ph0, *own_len;      // [B + 1] (own_len [B])
   float* ml;                               // [segments][256][2]
-  float* o;                                // [segments][256][dh]
+  float* o;                                // [segments][2 row tiles][dh / 4][128][4]
 };
 enum { kTokens = 0, kShare = 1, kUnits = 2, kSharedLen = 3, kPlan = 16 };
 
@@ -377,11 +377,14 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
       const uint32_t sc = tmem + TM_S + 64 * half + lane_off, pc = tmem + TM_P + 64 * t + 32 * half + lane_off;
       const uint32_t oc = tmem + TM_O + t * 128 + half * (DH / 2) + lane_off;
       auto tile_sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory"); };
-      // rows of tile t of a segment: G heads of each of its tokens; a warp brings sixteen
-      auto load_q = [&](const Seg& s) {
-        const int nrow = min(p.tokens, s.ntok - t * p.tokens) * p.G;
-        const int w0 = (warp & 7) * 16, mine = w0 + (lane & 15);
-        const int token = mine < nrow ? __ldcg(p.tok + s.tok0 + t * p.tokens + mine / p.G) : -1;
+      // rows of tile t of a segment: G heads of each of its tokens; a warp brings sixteen, whose token a
+      // lane knows (asked for a segment ahead)
+      const int w0 = (warp & 7) * 16;
+      auto token_of = [&](const Seg& s) {
+        const int nrow = min(p.tokens, s.ntok - t * p.tokens) * p.G, mine = w0 + (lane & 15);
+        return mine < nrow ? __ldcg(p.tok + s.tok0 + t * p.tokens + mine / p.G) : -1;
+      };
+      auto load_q = [&](const Seg& s, int token) {
         constexpr int CH = DH / 8;                          // 16-byte pieces of a row
         constexpr int RI = 32 / CH;                         // rows of one round
         uint4 v[16 / RI];
@@ -405,11 +408,12 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
       auto active = [&](const Seg& s) { return s.ntok > t * p.tokens; };
       int i = 0;
       while (i < nseg && !active(bars.segs[i])) ++i;
-      if (i < nseg) load_q(bars.segs[i]);
+      if (i < nseg) load_q(bars.segs[i], token_of(bars.segs[i]));
       while (i < nseg) {
         const Seg s = bars.segs[i];
         int next = i + 1;
         while (next < nseg && !active(bars.segs[next])) ++next;
+        const int token = next < nseg ? token_of(bars.segs[next]) : -1;
         float m = -INFINITY, l = 0.f;
         for (int j = s.j0; j < s.j1; ++j) {
           wait(bars, &bars.s_full[t], tiles & 1, p.hdr, 610);
@@ -479,7 +483,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
           ++tiles;
         }
         // the last scores are read: Q is free for the next segment, whose first product may start
-        if (next < nseg) load_q(bars.segs[next]);
+        if (next < nseg) load_q(bars.segs[next], token);
         tile_sync();                                        // the last maxima are read
         float* sums = reinterpret_cast<float*>(bars.pair[t]);
         if (half == 1) sums[r] = l;
@@ -490,16 +494,18 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
         const int nrow = min(p.tokens, s.ntok - t * p.tokens) * p.G;
         const int64_t row = static_cast<int64_t>(s.id) * 256 + t * 128 + r;
         const bool keep = r < nrow && !bars.failed;
+        // O of a tile as [dh / 4][128 rows][4]: a warp's 32 rows lie side by side
+        float4* dst = reinterpret_cast<float4*>(p.o) + (static_cast<int64_t>(s.id) * 2 + t) * (DH / 4) * 128 + half * (DH / 8) * 128 + r;
 #pragma unroll 1
         for (int c = 0; c < DH / 64; ++c) {
           uint32_t o[32];
           tmem_ld32(oc + 32 * c, o);
           tmem_wait_ld();
           if (keep) {
-            float4* dst = reinterpret_cast<float4*>(p.o + row * DH + half * (DH / 2) + 32 * c);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+              dst[(8 * c + e) * 128] =
+                  make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
           }
         }
         if (half == 0 && r < nrow) *reinterpret_cast<float2*>(p.ml + row * 2) = bars.failed ? make_float2(NAN, NAN) : make_float2(m, l + l_other);
@@ -718,7 +724,10 @@ __global__ void __launch_bounds__(kSimtThreads) k_parts_simt(Params p) {
           const int64_t row = static_cast<int64_t>(s.id) * 256 + tile * 128 + (tk - tile * p.tokens) * p.G + x % p.G;
           if (lane == 0) *reinterpret_cast<float2*>(p.ml + row * 2) = make_float2(m[r], l[r]);
 #pragma unroll
-          for (int e = 0; e < E; ++e) p.o[row * DH + lane + 32 * e] = o[r][e];
+          for (int e = 0; e < E; ++e) {
+            const int c = lane + 32 * e;
+            p.o[(((static_cast<int64_t>(s.id) * 2 + tile) * (DH / 4) + c / 4) * 128 + (row & 127)) * 4 + c % 4] = o[r][e];
+          }
         }
       }
     }
@@ -746,136 +755,154 @@ __device__ __forceinline__ void load_n(const T* p, float (&v)[N]) {
   }
 }
 
-// One warp a row: lane i holds dims i N .. i N + N - 1. Own-block keys are read here, one row after
-// another: a key of another block or of an absent token is never touched, whatever it holds.
+// One warp for up to four heads of a token that share their keys: grid (tokens, groups of heads / 4). Lane i
+// holds dims i N .. i N + N - 1 of each head; in a list of eight keys or segments it is also the one that
+// has the score, maximum or weight of number i / 4 for head i % 4. The own block's keys are read here, one
+// token after another: a key of another block or of an absent token is never touched, whatever it holds.
 template <typename T, int DH>
 __global__ void __launch_bounds__(128) k_join(Params p) {
-  constexpr int N = DH / 32;
-  constexpr int KG = 8;                    // keys, or segments, whose loads are issued together
+  constexpr int N = DH / 32, H = 4, L = 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int64_t R = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int i = static_cast<int>(R / p.Hq), h = static_cast<int>(R % p.Hq);
-  if (i >= __ldcg(p.plan + kTokens)) return;
-  const int share = __ldcg(p.plan + kShare), pair = 2 * p.tokens;
+  const int lane = threadIdx.x & 31, g_of = lane & 3, n_of = lane >> 2;
+  const int i = blockIdx.x, groups = ceil_div(p.G, H), unit = blockIdx.y * 4 + (threadIdx.x >> 5);
+  if (i >= __ldcg(p.plan + kTokens) || unit >= p.Hkv * groups) return;
+  const int share = __ldcg(p.plan + kShare), shared_len = __ldcg(p.plan + kSharedLen), pair = 2 * p.tokens;
   const int token = __ldcg(p.tok + i), NT = p.NB * p.Dmax;
-  const int b = token / NT, t = token % NT, pos = t % p.Dmax;
-  const int kvh = h / p.G, g = h % p.G;
-  float q[N];
-  load_n<T, N>(static_cast<const T*>(p.q) + (static_cast<int64_t>(token) * p.Hq + h) * DH + lane * N, q);
+  const int b = token / NT, pos = (token - b * NT) % p.Dmax;
+  const int own_i = i - __ldcg(p.tok_first + b), own_u = __ldcg(p.unit0 + b), own_ph = __ldcg(p.ph0 + b), own_len = __ldcg(p.own_len + b);
+  const int kvh = unit / groups, g0 = (unit - kvh * groups) * H, gn = min(H, p.G - g0);
+  float q[H][N], o[H][N];
 #pragma unroll
-  for (int e = 0; e < N; ++e) q[e] *= p.scale_log2;
-  float m = -INFINITY, l = 0.f, o[N];
+  for (int g = 0; g < H; ++g) {
+    load_n<T, N>(static_cast<const T*>(p.q) + (static_cast<int64_t>(token) * p.Hq + kvh * p.G + g0 + min(g, gn - 1)) * DH + lane * N, q[g]);
 #pragma unroll
-  for (int e = 0; e < N; ++e) o[e] = 0.f;
+    for (int e = 0; e < N; ++e) {
+      q[g][e] *= p.scale_log2;
+      o[g][e] = 0.f;
+    }
+  }
+  // of head g_of: reference maximum and sum so far
+  float m = -INFINITY, l = 0.f;
+  // takes in scores s with weights' factors a (of number n_of, head g_of); returns the weight
+  auto take = [&](float s, float a) {
+    float top = fmaxf(m, s);
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float ref = top > -INFINITY ? top : 0.f;
+    const float f = ex2_approx(m - ref), w = ex2_approx(s - ref);        // 0 for -inf, NaN where there is one
+    float sum = a * w;
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    l = l * f + sum;
+    m = top;
+#pragma unroll
+    for (int g = 0; g < H; ++g) {
+      const float fg = __shfl_sync(0xffffffffu, f, g);
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[g][e] *= fg;
+    }
+    return w;
+  };
 
   // own block: slots k Dmax .. t
   const int64_t kv0 = ((static_cast<int64_t>(token) - pos) * p.Hkv + kvh) * DH + lane * N;
   const int64_t step = static_cast<int64_t>(p.Hkv) * DH;
-  for (int c0 = 0; c0 <= pos; c0 += KG) {
-    float k[KG][N], v[KG][N], s[KG];
+  for (int c0 = 0; c0 <= pos; c0 += L) {
+    float k[L][N], v[L][N], s[L * H];
 #pragma unroll
-    for (int c = 0; c < KG; ++c) {
-      const int64_t at = kv0 + min(c0 + c, pos) * step;      // behind the last one: that again
+    for (int c = 0; c < L; ++c) {
+      const int64_t at = kv0 + min(c0 + c, pos) * step;      // behind the last one: that again, without weight
       load_n<T, N>(static_cast<const T*>(p.k_cand) + at, k[c]);
       load_n<T, N>(static_cast<const T*>(p.v_cand) + at, v[c]);
     }
 #pragma unroll
-    for (int c = 0; c < KG; ++c) {
-      s[c] = 0.f;
+    for (int c = 0; c < L; ++c)
 #pragma unroll
-      for (int e = 0; e < N; ++e) s[c] = fmaf(q[e], k[c][e], s[c]);
-    }
+      for (int g = 0; g < H; ++g) {
+        s[c * H + g] = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[c * H + g] = fmaf(q[g][e], k[c][e], s[c * H + g]);
+      }
+    // 32 sums over 32 lanes, one to each lane: halves change hands
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
-      for (int c = 0; c < KG; ++c) s[c] += __shfl_xor_sync(0xffffffffu, s[c], d);
-    float top = m;
+      for (int x = 0; x < d; ++x) {
+        const bool up = lane & d;
+        const float send = up ? s[x] : s[x + d];
+        s[x] = (up ? s[x + d] : s[x]) + __shfl_xor_sync(0xffffffffu, send, d);
+      }
+    const bool there = c0 + n_of <= pos;
+    const float w = take(there ? s[0] : -INFINITY, 1.f);
 #pragma unroll
-    for (int c = 0; c < KG; ++c) {
-      if (c0 + c > pos) s[c] = -INFINITY;
-      top = fmaxf(top, s[c]);
-    }
-    bool nan = false;                      // a score that is no number makes the row none
-#pragma unroll
-    for (int c = 0; c < KG; ++c) nan = nan || s[c] != s[c];
-    if (top == -INFINITY && !nan) continue;
-    const float f = m == -INFINITY ? 0.f : ex2_approx(m - top);
-    l *= f;
-#pragma unroll
-    for (int e = 0; e < N; ++e) o[e] *= f;
-#pragma unroll
-    for (int c = 0; c < KG; ++c) {
+    for (int c = 0; c < L; ++c) {
       if (c0 + c > pos) break;
-      const float w = ex2_approx(s[c] - top);
-      l += w;
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = fmaf(w, v[c][e], o[e]);
+      for (int g = 0; g < H; ++g) {
+        const float wg = __shfl_sync(0xffffffffu, w, c * H + g);
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[g][e] = fmaf(wg, v[c][e], o[g][e]);
+      }
     }
-    m = top;
   }
 
-  // segments: first and last of the shared prompt's, then of the own prefix's
+  // the segments of a pair's units u_base + at kt .. + kt - 1
   auto join = [&](int i0, int u_base, int ph_base, int len) {
     if (len <= 0) return;
-    const int kt = ceil_div(len, kTile), at = (i0 / pair) * p.Hkv + kvh, in = i0 % pair;
-    const int row = (in / p.tokens) * 128 + (in % p.tokens) * p.G + g;
+    const int kt = ceil_div(len, kTile), pr = i0 / pair, in = i0 - pr * pair, at = pr * p.Hkv + kvh;
+    const int tile = in / p.tokens, row = (in - tile * p.tokens) * p.G + g0;
     const int u = u_base + at * kt, c0 = u / share, n = (u + kt - 1) / share - c0 + 1;
-    const int64_t r0 = static_cast<int64_t>(ph_base + at + c0) * 256 + row;
-    for (int s0 = 0; s0 < n; s0 += 4) {
-      float2 ml[4];
-      float x[4][N];
+    const int64_t id0 = static_cast<int64_t>(ph_base) + at + c0;
+    for (int s0 = 0; s0 < n; s0 += L) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (s0 + n_of < n && g_of < gn) ml = __ldcg(reinterpret_cast<const float2*>(p.ml) + (id0 + s0 + n_of) * 256 + tile * 128 + row + g_of);
+      const float w = take(ml.x, ml.y);
+      for (int c = 0; c < min(L, n - s0); c += 2) {
+        float x[2][H][N];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int64_t r = r0 + static_cast<int64_t>(min(s0 + c, n - 1)) * 256;
-        ml[c] = __ldcg(reinterpret_cast<const float2*>(p.ml) + r);
+        for (int y = 0; y < 2; ++y) {
+          // (an odd last one twice, the second time without weight)
+          const float* src = p.o + ((((id0 + s0 + min(c + y, n - s0 - 1)) * 2 + tile) * (DH / 4) + lane * N / 4) * 128 + row) * 4 + lane * N % 4;
 #pragma unroll
-        for (int e = 0; e < N; e += 2) {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(p.o + r * DH + lane * N + e));
-          x[c][e] = y.x;
-          x[c][e + 1] = y.y;
+          for (int g = 0; g < H; ++g)
+#pragma unroll
+            for (int e = 0; e < N; e += 2) {
+              const float2 z = g < gn ? __ldcg(reinterpret_cast<const float2*>(src + 4 * g + e)) : make_float2(0.f, 0.f);
+              x[y][g][e] = z.x;
+              x[y][g][e + 1] = z.y;
+            }
         }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int g = 0; g < H; ++g) {
+            const float wg = __shfl_sync(0xffffffffu, w, ((c + y) & (L - 1)) * H + g);
+            if (c + y < n - s0) {
+#pragma unroll
+              for (int e = 0; e < N; ++e) o[g][e] = fmaf(wg, x[y][g][e], o[g][e]);
+            }
+          }
       }
-      float top = m;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (s0 + c >= n) ml[c].x = -INFINITY;
-        top = fmaxf(top, ml[c].x);
-      }
-      if (top == -INFINITY) {
-        // no weight so far; a sum that is no number stays one
-#pragma unroll
-        for (int c = 0; c < 4; ++c) l += s0 + c < n ? ml[c].y : 0.f;
-        continue;
-      }
-      const float f = m == -INFINITY ? 0.f : ex2_approx(m - top);
-      l *= f;
-#pragma unroll
-      for (int e = 0; e < N; ++e) o[e] *= f;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (s0 + c >= n) continue;
-        const float w = ex2_approx(ml[c].x - top);          // 0 for a segment of scores at -inf, whose O is 0
-        l = fmaf(ml[c].y, w, l);
-#pragma unroll
-        for (int e = 0; e < N; ++e) o[e] = fmaf(w, x[c][e], o[e]);
-      }
-      m = top;
     }
   };
-  join(i, 0, 0, __ldcg(p.plan + kSharedLen));
-  join(i - __ldcg(p.tok_first + b), __ldcg(p.unit0 + b), __ldcg(p.ph0 + b), __ldcg(p.own_len + b));
+  join(i, 0, 0, shared_len);
+  join(own_i, own_u, own_ph, own_len);
 
   const float inv = 1.f / l;
-  const int64_t at = (static_cast<int64_t>(token) * p.Hq + h) * DH + lane * N;
-  if (sizeof(T) == 4 || p.out_f32) {
-    float* out = static_cast<float*>(p.out) + at;
 #pragma unroll
-    for (int e = 0; e < N; e += 2) *reinterpret_cast<float2*>(out + e) = make_float2(o[e] * inv, o[e + 1] * inv);
-  } else {
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at);
+  for (int g = 0; g < H; ++g) {
+    const float f = __shfl_sync(0xffffffffu, inv, g);
+    if (g >= gn) continue;
+    const int64_t at = (static_cast<int64_t>(token) * p.Hq + kvh * p.G + g0 + g) * DH + lane * N;
+    if (sizeof(T) == 4 || p.out_f32) {
+      float* out = static_cast<float*>(p.out) + at;
 #pragma unroll
-    for (int e = 0; e < N; e += 2) out[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
+      for (int e = 0; e < N; e += 2) *reinterpret_cast<float2*>(out + e) = make_float2(o[g][e] * f, o[g][e + 1] * f);
+    } else {
+      uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at);
+#pragma unroll
+      for (int e = 0; e < N; e += 2) out[e / 2] = pack_bf16(o[g][e] * f, o[g][e + 1] * f);
+    }
   }
 }
 
@@ -990,8 +1017,9 @@ static int launch_parts(const Params& p, const ssd_attn_shared_args* a, cudaStre
 
 template <typename T, int DH>
 static cudaError_t launch_join(const Params& p, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(p.B) * p.NB * p.Dmax * p.Hq;
-  return launch_pdl(k_join<T, DH>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, p);
+  const int64_t tokens = static_cast<int64_t>(p.B) * p.NB * p.Dmax;
+  const int units = p.Hkv * ceil_div(p.G, 4);
+  return launch_pdl(k_join<T, DH>, dim3(static_cast<unsigned>(tokens), static_cast<unsigned>(ceil_div(units, 4))), dim3(128), 0, s, p);
 }
 
 }  // namespace shr
