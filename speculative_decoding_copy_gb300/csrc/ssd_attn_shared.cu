@@ -58,6 +58,9 @@ struct Params {
   float* ml;                               // [segments][256][2]
   float* o;                                // [segments][2 row tiles][dh / 4][128][4]
 };
+// units that a pair and head costs beside its key tiles: Q, and O out to the workspace (8000 clocks where a
+// unit is 3400)
+constexpr int kSetup = 2;
 enum { kTokens = 0, kShare = 1, kUnits = 2, kSharedLen = 3, kPlan = 16 };
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(Params p) {
   if (tid == 0) p.tok_first[p.B] = tokens;
   const int pair = 2 * p.tokens;
   int ph = S > 0 ? ceil_div(tokens, pair) * p.Hkv : 0;
-  int units = ph * ceil_div(S, kTile);
+  int units = ph * (ceil_div(S, kTile) + kSetup);
   __syncthreads();                          // tok_first is written
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(Params p) {
       }
       p.own_len[b] = P;
       h = P > 0 ? ceil_div(p.tok_first[b + 1] - p.tok_first[b], pair) * p.Hkv : 0;
-      u = h * ceil_div(P, kTile);
+      u = h * (ceil_div(P, kTile) + kSetup);
     }
     int total_u, total_h;
     const int fu = plan_scan(u, part, &total_u), fh = plan_scan(h, part, &total_h);
@@ -204,19 +207,36 @@ __device__ int describe(const Params& p, Seg* segs, int* count, int c, int u, in
       all = tok_first[b + 1] - first;
       ph = ph0[b];
     }
-    const int kt = ceil_div(s.len, kTile), at = (u - base) / kt;
+    const int kt = ceil_div(s.len, kTile) + kSetup, at = (u - base) / kt;
     s.kvh = at % p.Hkv;
     const int pr = at / p.Hkv;
     s.tok0 = first + pr * pair;
     s.ntok = min(pair, all - pr * pair);
-    s.j0 = (u - base) - at * kt;
-    s.j1 = min(kt, s.j0 + (u1 - u));
+    // units base + at kt .. are kSetup ones without keys, then a key tile each
+    const int from = u - base - at * kt, to = min(kt, from + (u1 - u));
+    s.j0 = max(from - kSetup, 0);
+    s.j1 = to - kSetup;
     s.id = ph + at + c;
-    segs[n++] = s;
-    u += s.j1 - s.j0;
+    if (s.j1 > s.j0) segs[n++] = s;
+    u += to - from;
   }
   *count = n;
   return u;
+}
+
+// Segments are worked through in groups: one of two row tiles, which share its keys, or up to two of one row
+// tile each, side by side, each with its own keys. Segment i begins one; returns how many it has.
+__device__ __forceinline__ int group_of(const Params& p, const Seg* segs, int i, int nseg) {
+  return segs[i].ntok <= p.tokens && i + 1 < nseg && segs[i + 1].ntok <= p.tokens ? 2 : 1;
+}
+// What row tile t of the CTA does in the group of segment i: a segment (or -1), and which of its row tiles
+struct Part {
+  int seg, tile;
+};
+__device__ __forceinline__ Part part_of(const Params& p, const Seg* segs, int i, int n, int t) {
+  if (n == 2) return {i + t, 0};
+  if (t == 0 || segs[i].ntok > p.tokens) return {i, t};
+  return {-1, 0};
 }
 
 // row of the K or V tensor (rows of dh elements) at which key tile j of a segment starts
@@ -234,11 +254,11 @@ __device__ __forceinline__ int64_t tile_row(const Params& p, const Seg& s, int j
 // ------------------------------------------------------------------ parts, tensor cores
 struct Bars {
   uint64_t full[kSlots], empty[kSlots];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full[2], o_free[2];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full[2], o_free[2], max_read[2];
   uint64_t last;
   uint32_t tmem_base;
   int failed, count, next;
-  uint16_t pair[2][2][256];                // of each row tile, in turns: a maximum of every thread, for the row's other one
+  float pair[2][256];                      // of each row tile: a maximum (at the end a sum) of every thread, for the row's other one
   Seg segs[kSegs];
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barriers and segments");
@@ -319,6 +339,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
       mbar_init(&bars.p_full[t], 256);
       mbar_init(&bars.pv_done[t], 1);
       mbar_init(&bars.q_full[t], 256);
+      mbar_init(&bars.max_read[t], 256);
       mbar_init(&bars.o_free[t], 256);
     }
     mbar_init(&bars.last, 1);
@@ -380,9 +401,21 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
       // rows of tile t of a segment: G heads of each of its tokens; a warp brings sixteen, whose token a
       // lane knows (asked for a segment ahead)
       const int w0 = (warp & 7) * 16;
-      auto token_of = [&](const Seg& s) {
-        const int nrow = min(p.tokens, s.ntok - t * p.tokens) * p.G, mine = w0 + (lane & 15);
-        return mine < nrow ? __ldcg(p.tok + s.tok0 + t * p.tokens + mine / p.G) : -1;
+      auto rows_of = [&](const Seg& s, int tile) { return min(p.tokens, s.ntok - tile * p.tokens) * p.G; };
+      auto token_of = [&](const Part& a) {
+        const Seg& s = bars.segs[a.seg];
+        const int mine = w0 + (lane & 15);
+        return mine < rows_of(s, a.tile) ? __ldcg(p.tok + s.tok0 + a.tile * p.tokens + mine / p.G) : -1;
+      };
+      // the next part of this row tile behind group i (moved on), seg < 0: none
+      auto next_part = [&](int& i) {
+        Part a = {-1, 0};
+        while (i < nseg && a.seg < 0) {
+          const int n = group_of(p, bars.segs, i, nseg);
+          a = part_of(p, bars.segs, i, n, t);
+          i += n;
+        }
+        return a;
       };
       auto load_q = [&](const Seg& s, int token) {
         constexpr int CH = DH / 8;                          // 16-byte pieces of a row
@@ -405,15 +438,13 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
         fence_async_smem();
         mbar_arrive(&bars.q_full[t]);
       };
-      auto active = [&](const Seg& s) { return s.ntok > t * p.tokens; };
       int i = 0;
-      while (i < nseg && !active(bars.segs[i])) ++i;
-      if (i < nseg) load_q(bars.segs[i], token_of(bars.segs[i]));
-      while (i < nseg) {
-        const Seg s = bars.segs[i];
-        int next = i + 1;
-        while (next < nseg && !active(bars.segs[next])) ++next;
-        const int token = next < nseg ? token_of(bars.segs[next]) : -1;
+      Part now = next_part(i);
+      if (now.seg >= 0) load_q(bars.segs[now.seg], token_of(now));
+      while (now.seg >= 0) {
+        const Seg s = bars.segs[now.seg];
+        const Part then = next_part(i);
+        const int token = then.seg >= 0 ? token_of(then) : -1;
         float m = -INFINITY, l = 0.f;
         for (int j = s.j0; j < s.j1; ++j) {
           wait(bars, &bars.s_full[t], tiles & 1, p.hdr, 610);
@@ -433,11 +464,13 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int c = 0; c < 64; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-          // (as bf16: any common reference near the maximum serves; two buffers, as a thread may be a tile ahead)
-          uint16_t* pair = bars.pair[t][tiles & 1];
-          pair[half * 128 + r] = static_cast<uint16_t>(__float_as_uint(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3])) >> 16);
+          // (the other threads have read the last tile's: long since, as a rule)
+          if (tiles > 0) wait(bars, &bars.max_read[t], (tiles - 1) & 1, p.hdr, 613);
+          float* pair = bars.pair[t];
+          pair[half * 128 + r] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           tile_sync();
-          const float top = fmaxf(bf16_to_f32(pair[r]), bf16_to_f32(pair[128 + r])) * p.scale_log2;
+          const float top = fmaxf(pair[r], pair[128 + r]) * p.scale_log2;
+          mbar_arrive(&bars.max_read[t]);
           // the reference moves only when the maximum grows by more than 2^8
           const bool need = top > m + 8.f || m == -INFINITY;
           const float ref = need ? fmaxf(m, top) : m;
@@ -483,19 +516,19 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
           ++tiles;
         }
         // the last scores are read: Q is free for the next segment, whose first product may start
-        if (next < nseg) load_q(bars.segs[next], token);
+        if (then.seg >= 0) load_q(bars.segs[then.seg], token);
         tile_sync();                                        // the last maxima are read
-        float* sums = reinterpret_cast<float*>(bars.pair[t]);
+        float* sums = bars.pair[t];
         if (half == 1) sums[r] = l;
         tile_sync();
         const float l_other = sums[r];
         wait(bars, &bars.pv_done[t], (tiles - 1) & 1, p.hdr, 612);
         tc_fence_after();
-        const int nrow = min(p.tokens, s.ntok - t * p.tokens) * p.G;
-        const int64_t row = static_cast<int64_t>(s.id) * 256 + t * 128 + r;
+        const int nrow = rows_of(s, now.tile);
+        const int64_t row = static_cast<int64_t>(s.id) * 256 + now.tile * 128 + r;
         const bool keep = r < nrow && !bars.failed;
         // O of a tile as [dh / 4][128 rows][4]: a warp's 32 rows lie side by side
-        float4* dst = reinterpret_cast<float4*>(p.o) + (static_cast<int64_t>(s.id) * 2 + t) * (DH / 4) * 128 + half * (DH / 8) * 128 + r;
+        float4* dst = reinterpret_cast<float4*>(p.o) + (static_cast<int64_t>(s.id) * 2 + now.tile) * (DH / 4) * 128 + half * (DH / 8) * 128 + r;
 #pragma unroll 1
         for (int c = 0; c < DH / 64; ++c) {
           uint32_t o[32];
@@ -512,27 +545,37 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
         tc_fence_before();
         mbar_arrive(&bars.o_free[t]);
         tile_sync();                                        // and the sums
-        i = next;
+        now = then;
       }
     } else if (warp == 16) {
       // -------------------------------------------------------- TMA: K0 V0 K1 V1 ..
       if (lane == 0) {
-        for (int i = 0; i < nseg && !bars.failed; ++i) {
-          const Seg s = bars.segs[i];
-          const CUtensorMap* mk = s.b < 0 ? &map_ks : &map_k;
-          const CUtensorMap* mv = s.b < 0 ? &map_vs : &map_v;
-          const int nj = s.j1 - s.j0;
-          // in the order of use: K0 K1 V0 K2 V1 .. V of the last tile
-          for (int e = 0; e < 2 * nj && !bars.failed; ++e, ++it) {
-            const bool is_k = e == 0 || ((e & 1) && e < 2 * nj - 1);
-            const int j = s.j0 + (is_k ? (e + 1) / 2 : e == 2 * nj - 1 ? nj - 1 : e / 2 - 1);
-            const int y = static_cast<int>(tile_row(p, s, j)), slot = it % kSlots;
-            if (it >= kSlots && !wait(bars, &bars.empty[slot], ((it / kSlots) - 1) & 1, p.hdr, 620)) break;
-            const uint32_t dst = sbase + Sh::OFF_RING + slot * Sh::kTileB;
-            mbar_expect_tx(&bars.full[slot], Sh::kTileB);
+        // tile j of a segment's keys or values into the next ring entry
+        auto fetch = [&](const Seg& s, int j, bool is_k) {
+          const int y = static_cast<int>(tile_row(p, s, j)), slot = it % kSlots;
+          if (bars.failed || (it >= kSlots && !wait(bars, &bars.empty[slot], ((it / kSlots) - 1) & 1, p.hdr, 620))) return;
+          const CUtensorMap* map = s.b < 0 ? (is_k ? &map_ks : &map_vs) : (is_k ? &map_k : &map_v);
+          const uint32_t dst = sbase + Sh::OFF_RING + slot * Sh::kTileB;
+          mbar_expect_tx(&bars.full[slot], Sh::kTileB);
 #pragma unroll
-            for (uint32_t h = 0; h < Sh::kHalves; ++h) tma_load_2d(dst + h * Sh::kHalf, is_k ? mk : mv, 64 * h, y, &bars.full[slot]);
+          for (uint32_t h = 0; h < Sh::kHalves; ++h) tma_load_2d(dst + h * Sh::kHalf, map, 64 * h, y, &bars.full[slot]);
+          ++it;
+        };
+        // in the order of use below: a tile's keys ahead of the values of the tile before
+        for (int i = 0; i < nseg && !bars.failed;) {
+          const int n = group_of(p, bars.segs, i, nseg);
+          int most = 0;
+          for (int k = 0; k < n; ++k) {
+            most = max(most, bars.segs[i + k].j1 - bars.segs[i + k].j0);
+            fetch(bars.segs[i + k], bars.segs[i + k].j0, true);
           }
+          for (int jj = 0; jj < most; ++jj)
+            for (int k = 0; k < n; ++k) {
+              const Seg& s = bars.segs[i + k];
+              if (s.j0 + jj + 1 < s.j1) fetch(s, s.j0 + jj + 1, true);
+              if (s.j0 + jj < s.j1) fetch(s, s.j0 + jj, false);
+            }
+          i += n;
         }
       }
       __syncwarp();
@@ -540,12 +583,18 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
       // -------------------------------------------------------- products: the whole warp waits, one lane issues
       const uint32_t lead = elect_one();
       constexpr uint32_t idS = idesc_bf16(false, kTile), idPV = idesc_bf16(true, DH);
-      for (int i = 0; i < nseg; ++i) {
-        const Seg s = bars.segs[i];
-        const int nt = __shfl_sync(0xffffffffu, s.ntok > p.tokens ? 2 : 1, 0), nj = __shfl_sync(0xffffffffu, s.j1 - s.j0, 0);
-        auto scores = [&](int t, int jj) {
-          const uint32_t e = it + (jj == 0 ? 0 : 2 * jj - 1), slot = e % kSlots;
-          wait(bars, &bars.full[slot], (e / kSlots) & 1, p.hdr, 630);
+      for (int i = 0; i < nseg;) {
+        // of each row tile: its key tiles (0: it has no part), and whether it has its own
+        const int n = __shfl_sync(0xffffffffu, group_of(p, bars.segs, i, nseg), 0);
+        const Part part1 = part_of(p, bars.segs, i, n, 1);
+        const int nj0 = __shfl_sync(0xffffffffu, bars.segs[i].j1 - bars.segs[i].j0, 0);
+        const int nj1 = __shfl_sync(0xffffffffu, part1.seg < 0 ? 0 : bars.segs[part1.seg].j1 - bars.segs[part1.seg].j0, 0);
+        const bool both = n == 1 && nj1 > 0;                // two row tiles of one segment: entries serve both
+        uint32_t ek = 0, ev = 0;                            // ring entries of the keys and values in use
+        auto scores = [&](int t) {
+          if (t == 0 || !both) ek = it++;
+          const uint32_t slot = ek % kSlots;
+          wait(bars, &bars.full[slot], (ek / kSlots) & 1, p.hdr, 630);
           // the scores before, of whichever tile, are in registers
           if (last >= 0) {
             wait(bars, &bars.s_free[last], (ph_s >> last) & 1, p.hdr, 636);
@@ -561,24 +610,30 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
             mma_bf16_warp(tmem + TM_S, qd + step, kd + step, idS, ks > 0 ? 1u : 0u, lead);
           }
           mma_commit_warp(&bars.s_full[t], lead);
-          if (t == nt - 1) mma_commit_warp(&bars.empty[slot], lead);
+          if (t == 1 || !both) mma_commit_warp(&bars.empty[slot], lead);
         };
-        for (int t = 0; t < nt; ++t) {
+        for (int t = 0; t < 2; ++t) {
+          const int nj = t == 0 ? nj0 : nj1;
+          if (nj == 0) continue;
           wait(bars, &bars.q_full[t], (ph_q >> t) & 1, p.hdr, 631);
           ph_q ^= 1u << t;
-          scores(t, 0);
+          scores(t);
         }
-        for (int jj = 0; jj < nj; ++jj) {
-          const uint32_t e = it + (jj == nj - 1 ? 2 * nj - 1 : 2 * jj + 2), slot = e % kSlots;
-          for (int t = 0; t < nt; ++t) {
+        const int most = max(nj0, nj1);
+        for (int jj = 0; jj < most; ++jj) {
+          for (int t = 0; t < 2; ++t) {
+            const int nj = t == 0 ? nj0 : nj1;
+            if (jj >= nj) continue;
             // the next scores first: they need nothing of this tile's softmax but its reading of the last ones
-            if (jj + 1 < nj) scores(t, jj + 1);
-            if (t == 0) {
-              wait(bars, &bars.full[slot], (e / kSlots) & 1, p.hdr, 634);
+            if (jj + 1 < nj) scores(t);
+            if (t == 0 || !both) {
+              ev = it++;
+              wait(bars, &bars.full[ev % kSlots], (ev / kSlots) & 1, p.hdr, 634);
+              const Seg& s = bars.segs[t == 0 || both ? i : i + 1];
               const int r0 = s.len - (s.j0 + jj) * kTile;
               if (r0 < kTile) {
                 // value rows behind the length: their weights are 0, and 0 times NaN would be NaN
-                uint8_t* v = smem + Sh::OFF_RING + slot * Sh::kTileB;
+                uint8_t* v = smem + Sh::OFF_RING + ev % kSlots * Sh::kTileB;
                 for (int x = r0 * 8 + lane; x < kTile * 8; x += 32)
 #pragma unroll
                   for (uint32_t h = 0; h < Sh::kHalves; ++h) *reinterpret_cast<uint4*>(v + h * Sh::kHalf + x * 16) = make_uint4(0, 0, 0, 0);
@@ -586,6 +641,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
                 __syncwarp();
               }
             }
+            const uint32_t slot = ev % kSlots;
             wait(bars, &bars.p_full[t], (ph_p >> t) & 1, p.hdr, 632);
             ph_p ^= 1u << t;
             if (jj == 0) {
@@ -603,10 +659,10 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
             for (int ks = 0; ks < kTile / 16; ++ks)
               mma_bf16_ts_warp(tmem + TM_O + t * 128, pa + ks * 8, vd + ks * (16 * 128 >> 4), idPV, (jj > 0 || ks > 0) ? 1u : 0u, lead);
             mma_commit_warp(&bars.pv_done[t], lead);
-            if (t == nt - 1) mma_commit_warp(&bars.empty[slot], lead);
+            if (t == 1 || !both) mma_commit_warp(&bars.empty[slot], lead);
           }
         }
-        it += 2 * nj;
+        i += n;
         if (__any_sync(0xffffffffu, bars.failed)) break;
       }
     }
@@ -851,7 +907,7 @@ __global__ void __launch_bounds__(128) k_join(Params p) {
     if (len <= 0) return;
     const int kt = ceil_div(len, kTile), pr = i0 / pair, in = i0 - pr * pair, at = pr * p.Hkv + kvh;
     const int tile = in / p.tokens, row = (in - tile * p.tokens) * p.G + g0;
-    const int u = u_base + at * kt, c0 = u / share, n = (u + kt - 1) / share - c0 + 1;
+    const int u = u_base + at * (kt + kSetup) + kSetup, c0 = u / share, n = (u + kt - 1) / share - c0 + 1;
     const int64_t id0 = static_cast<int64_t>(ph_base) + at + c0;
     for (int s0 = 0; s0 < n; s0 += L) {
       float2 ml = make_float2(-INFINITY, 0.f);
@@ -959,7 +1015,7 @@ static Layout layout(const ssd_attn_shared_args* a, int ctas) {
   const int64_t s_cap = a->shared_table != nullptr ? 128LL * a->shared_pages : a->S_max;
   const int64_t p_cap = a->block_table != nullptr ? 128LL * a->pages_per_seq : a->P_max;
   const int64_t ph_s = (all + pair - 1) / pair * a->Hkv, ph_o = (NT + pair - 1) / pair * a->Hkv * a->B;
-  L.units = ph_s * ((s_cap + kTile - 1) / kTile) + ph_o * ((p_cap + kTile - 1) / kTile);
+  L.units = ph_s * ((s_cap + kTile - 1) / kTile + kSetup) + ph_o * ((p_cap + kTile - 1) / kTile + kSetup);
   L.segments = (s_cap > 0 ? ph_s : 0) + (p_cap > 0 ? ph_o : 0) + ctas;
   size_t at = sizeof(WsHeader);
   auto take = [&](size_t bytes) {
