@@ -58,12 +58,14 @@ struct Params {
   float* ml;                               // [segments][256][2]
   float* o;                                // [segments][2 row tiles][dh / 4][128][4]
 };
-// units that a pair and head costs beside its key tiles: Q, and O out to the workspace (8000 clocks where a
-// unit is 3400)
+// Work is measured in units of 1700 clocks, what a key tile takes with one row tile beside another segment's;
+// with two row tiles (3400) it counts as two, and Q in and O out of a pair and head as two more tiles.
 constexpr int kSetup = 2;
 enum { kTokens = 0, kShare = 1, kUnits = 2, kSharedLen = 3, kPlan = 16 };
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// units of a key tile for rows of `tokens` tokens, of which a row tile holds `per`
+__device__ __forceinline__ int tile_units(int tokens, int per) { return tokens > per ? 2 : 1; }
 
 // ------------------------------------------------------------------ plan
 constexpr int kPlanThreads = 1024;
@@ -117,7 +119,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(Params p) {
   if (tid == 0) p.tok_first[p.B] = tokens;
   const int pair = 2 * p.tokens;
   int ph = S > 0 ? ceil_div(tokens, pair) * p.Hkv : 0;
-  int units = ph * (ceil_div(S, kTile) + kSetup);
+  int units = ph * (ceil_div(S, kTile) + kSetup) * tile_units(tokens, p.tokens);
+  int two = units > 0 && tokens > p.tokens;                 // whether tiles of two units occur
   __syncthreads();                          // tok_first is written
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
@@ -129,8 +132,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(Params p) {
         P = 0;
       }
       p.own_len[b] = P;
-      h = P > 0 ? ceil_div(p.tok_first[b + 1] - p.tok_first[b], pair) * p.Hkv : 0;
-      u = h * (ceil_div(P, kTile) + kSetup);
+      const int n = p.tok_first[b + 1] - p.tok_first[b];
+      h = P > 0 ? ceil_div(n, pair) * p.Hkv : 0;
+      u = h * (ceil_div(P, kTile) + kSetup) * tile_units(n, p.tokens);
+      if (u > 0 && n > p.tokens) two = 1;
     }
     int total_u, total_h;
     const int fu = plan_scan(u, part, &total_u), fh = plan_scan(h, part, &total_h);
@@ -141,11 +146,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(Params p) {
     units += total_u;
     ph += total_h;
   }
+  two = __syncthreads_or(two);
   if (tid == 0) {
     p.unit0[p.B] = units;
     p.ph0[p.B] = ph;
     p.plan[kTokens] = tokens;
-    p.plan[kShare] = max(1, ceil_div(units, p.ctas));
+    // (never less than a tile: a run in the middle of a pair then has one at least)
+    p.plan[kShare] = max(two ? 2 : 1, ceil_div(units, p.ctas));
     p.plan[kUnits] = units;
     p.plan[kSharedLen] = S;
   }
@@ -207,15 +214,15 @@ __device__ int describe(const Params& p, Seg* segs, int* count, int c, int u, in
       all = tok_first[b + 1] - first;
       ph = ph0[b];
     }
-    const int kt = ceil_div(s.len, kTile) + kSetup, at = (u - base) / kt;
+    const int w = tile_units(all, p.tokens), kt = (ceil_div(s.len, kTile) + kSetup) * w, at = (u - base) / kt;
     s.kvh = at % p.Hkv;
     const int pr = at / p.Hkv;
     s.tok0 = first + pr * pair;
     s.ntok = min(pair, all - pr * pair);
-    // units base + at kt .. are kSetup ones without keys, then a key tile each
+    // key tile j has the w units from base + at kt + (kSetup + j) w on, and belongs to the run that has the first
     const int from = u - base - at * kt, to = min(kt, from + (u1 - u));
-    s.j0 = max(from - kSetup, 0);
-    s.j1 = to - kSetup;
+    s.j0 = max(ceil_div(from, w) - kSetup, 0);
+    s.j1 = ceil_div(to, w) - kSetup;
     s.id = ph + at + c;
     if (s.j1 > s.j0) segs[n++] = s;
     u += to - from;
@@ -821,11 +828,12 @@ __global__ void __launch_bounds__(128) k_join(Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, g_of = lane & 3, n_of = lane >> 2;
   const int i = blockIdx.x, groups = ceil_div(p.G, H), unit = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (i >= __ldcg(p.plan + kTokens) || unit >= p.Hkv * groups) return;
+  const int all_tokens = __ldcg(p.plan + kTokens);
+  if (i >= all_tokens || unit >= p.Hkv * groups) return;
   const int share = __ldcg(p.plan + kShare), shared_len = __ldcg(p.plan + kSharedLen), pair = 2 * p.tokens;
   const int token = __ldcg(p.tok + i), NT = p.NB * p.Dmax;
   const int b = token / NT, pos = (token - b * NT) % p.Dmax;
-  const int own_i = i - __ldcg(p.tok_first + b), own_u = __ldcg(p.unit0 + b), own_ph = __ldcg(p.ph0 + b), own_len = __ldcg(p.own_len + b);
+  const int own_first = __ldcg(p.tok_first + b), own_tokens = __ldcg(p.tok_first + b + 1) - own_first, own_u = __ldcg(p.unit0 + b), own_ph = __ldcg(p.ph0 + b), own_len = __ldcg(p.own_len + b);
   const int kvh = unit / groups, g0 = (unit - kvh * groups) * H, gn = min(H, p.G - g0);
   float q[H][N], o[H][N];
 #pragma unroll
@@ -903,11 +911,11 @@ __global__ void __launch_bounds__(128) k_join(Params p) {
   }
 
   // the segments of a pair's units u_base + at kt .. + kt - 1
-  auto join = [&](int i0, int u_base, int ph_base, int len) {
+  auto join = [&](int i0, int all, int u_base, int ph_base, int len) {
     if (len <= 0) return;
     const int kt = ceil_div(len, kTile), pr = i0 / pair, in = i0 - pr * pair, at = pr * p.Hkv + kvh;
     const int tile = in / p.tokens, row = (in - tile * p.tokens) * p.G + g0;
-    const int u = u_base + at * (kt + kSetup) + kSetup, c0 = u / share, n = (u + kt - 1) / share - c0 + 1;
+    const int w1 = tile_units(all, p.tokens), u = u_base + (at * (kt + kSetup) + kSetup) * w1, c0 = u / share, n = (u + (kt - 1) * w1) / share - c0 + 1;
     const int64_t id0 = static_cast<int64_t>(ph_base) + at + c0;
     for (int s0 = 0; s0 < n; s0 += L) {
       float2 ml = make_float2(-INFINITY, 0.f);
@@ -941,8 +949,8 @@ __global__ void __launch_bounds__(128) k_join(Params p) {
       }
     }
   };
-  join(i, 0, 0, shared_len);
-  join(own_i, own_u, own_ph, own_len);
+  join(i, all_tokens, 0, 0, shared_len);
+  join(i - own_first, own_tokens, own_u, own_ph, own_len);
 
   const float inv = 1.f / l;
 #pragma unroll
@@ -1015,7 +1023,7 @@ static Layout layout(const ssd_attn_shared_args* a, int ctas) {
   const int64_t s_cap = a->shared_table != nullptr ? 128LL * a->shared_pages : a->S_max;
   const int64_t p_cap = a->block_table != nullptr ? 128LL * a->pages_per_seq : a->P_max;
   const int64_t ph_s = (all + pair - 1) / pair * a->Hkv, ph_o = (NT + pair - 1) / pair * a->Hkv * a->B;
-  L.units = ph_s * ((s_cap + kTile - 1) / kTile + kSetup) + ph_o * ((p_cap + kTile - 1) / kTile + kSetup);
+  L.units = 2 * (ph_s * ((s_cap + kTile - 1) / kTile + kSetup) + ph_o * ((p_cap + kTile - 1) / kTile + kSetup));
   L.segments = (s_cap > 0 ? ph_s : 0) + (p_cap > 0 ? ph_o : 0) + ctas;
   size_t at = sizeof(WsHeader);
   auto take = [&](size_t bytes) {
