@@ -61,7 +61,7 @@ struct Params {
 // Work is measured in units of 1700 clocks, what a key tile takes with one row tile beside another segment's;
 // with two row tiles (3400) it counts as two, and Q in and O out of a pair and head as two more tiles.
 constexpr int kSetup = 2;
-enum { kTokens = 0, kShare = 1, kUnits = 2, kSharedLen = 3, kPlan = 16 };
+enum { kTokens = 0, kShare = 1, kUnits = 2, kSharedLen = 3, kSharedUnits = 4, kSharedPairs = 5, kPlan = 16 };
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // units of a key tile for rows of `tokens` tokens, of which a row tile holds `per`
@@ -70,103 +70,110 @@ __device__ __forceinline__ int tile_units(int tokens, int per) { return tokens >
 // ------------------------------------------------------------------ plan
 constexpr int kPlanThreads = 1024;
 
-__device__ __forceinline__ int plan_scan(int v, int* part, int* total) {
+// exclusive sums of three numbers over the CTA, and the totals
+__device__ __forceinline__ void plan_scan(int (&v)[3], int (*part)[32], int (&total)[3]) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  int x = v;
+  int x[3] = {v[0], v[1], v[2]}, w[3];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) part[wid] = x;
-  __syncthreads();
-  int w = part[lane];
+  for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w += y;
+    for (int k = 0; k < 3; ++k) {
+      const int y = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] += y;
+    }
+  __syncthreads();
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) part[k][wid] = x[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) w[k] = part[k][lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int y = __shfl_up_sync(0xffffffffu, w[k], o);
+      if (lane >= o) w[k] += y;
+    }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    total[k] = __shfl_sync(0xffffffffu, w[k], 31);
+    const int before = __shfl_sync(0xffffffffu, w[k], max(wid - 1, 0));
+    v[k] = x[k] - v[k] + (wid > 0 ? before : 0);
   }
-  *total = __shfl_sync(0xffffffffu, w, 31);
-  const int before = __shfl_sync(0xffffffffu, w, max(wid - 1, 0));
-  return x - v + (wid > 0 ? before : 0);
 }
 
 // Segment (of pair-and-head ph, cut by CTA c's run) has the number ph + c: from one segment to the next
-// one of the two grows or both do. Pairs of the shared prompt come first, then those of each sequence.
+// one of the two grows or both do. Pairs of the shared prompt come first, then those of each sequence
+// (unit0 and ph0 count from the first of these).
 __global__ void __launch_bounds__(kPlanThreads) k_plan(Params p) {
-  __shared__ int part[32];
+  __shared__ int part[3][32];
+  __shared__ int first[kPlanThreads];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int S = __ldg(p.shared_len);
   const int64_t s_cap = p.shared_table != nullptr ? 128LL * p.shared_pages : p.S_max;
-  if (S < 0 || S > s_cap) {
-    if (tid == 0) record_error(p.hdr, SSD_ERR_DEVICE, 601);
-    S = 0;
-  }
   const int64_t p_cap = p.block_table != nullptr ? 128LL * p.pages_per_seq : p.P_max;
-  int tokens = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    int n = 0;
-    if (b < p.B)
-      for (int k = 0; k < p.NB; ++k) n += min(max(__ldg(p.blk_len + static_cast<int64_t>(b) * p.NB + k), 0), p.Dmax);
-    int total;
-    const int first = plan_scan(n, part, &total);
-    if (b < p.B) p.tok_first[b] = tokens + first;
-    tokens += total;
-  }
-  if (tid == 0) p.tok_first[p.B] = tokens;
   const int pair = 2 * p.tokens;
-  int ph = S > 0 ? ceil_div(tokens, pair) * p.Hkv : 0;
-  int units = ph * (ceil_div(S, kTile) + kSetup) * tile_units(tokens, p.tokens);
-  int two = units > 0 && tokens > p.tokens;                 // whether tiles of two units occur
-  __syncthreads();                          // tok_first is written
+  int tokens = 0, units = 0, ph = 0, two = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    int u = 0, h = 0;
+    int v[3] = {0, 0, 0}, total[3];
     if (b < p.B) {
       int P = __ldg(p.prefix_len + b);
+      for (int k = 0; k < p.NB; ++k) v[0] += min(max(__ldg(p.blk_len + static_cast<int64_t>(b) * p.NB + k), 0), p.Dmax);
       if (P < 0 || P > p_cap) {
         record_error(p.hdr, SSD_ERR_DEVICE, 602);
         P = 0;
       }
       p.own_len[b] = P;
-      const int n = p.tok_first[b + 1] - p.tok_first[b];
-      h = P > 0 ? ceil_div(n, pair) * p.Hkv : 0;
-      u = h * (ceil_div(P, kTile) + kSetup) * tile_units(n, p.tokens);
-      if (u > 0 && n > p.tokens) two = 1;
+      v[1] = P > 0 ? ceil_div(v[0], pair) * p.Hkv : 0;
+      v[2] = v[1] * (ceil_div(P, kTile) + kSetup) * tile_units(v[0], p.tokens);
+      if (v[2] > 0 && v[0] > p.tokens) two = 1;
     }
-    int total_u, total_h;
-    const int fu = plan_scan(u, part, &total_u), fh = plan_scan(h, part, &total_h);
+    plan_scan(v, part, total);
+    first[tid] = tokens + v[0];
     if (b < p.B) {
-      p.unit0[b] = units + fu;
-      p.ph0[b] = ph + fh;
+      p.tok_first[b] = tokens + v[0];
+      p.ph0[b] = ph + v[1];
+      p.unit0[b] = units + v[2];
     }
-    units += total_u;
-    ph += total_h;
+    tokens += total[0];
+    ph += total[1];
+    units += total[2];
+    __syncthreads();
+    // their tokens: a warp a sequence
+    for (int b = b0 + wid; b < min(p.B, b0 + kPlanThreads); b += kPlanThreads / 32) {
+      int at = first[b - b0];
+      for (int k0 = 0; k0 < p.NB; k0 += 32) {
+        const int len = k0 + lane < p.NB ? min(max(__ldg(p.blk_len + static_cast<int64_t>(b) * p.NB + k0 + lane), 0), p.Dmax) : 0;
+        for (int k = k0; k < min(p.NB, k0 + 32); ++k) {
+          const int n = __shfl_sync(0xffffffffu, len, k - k0);
+          for (int d = lane; d < n; d += 32) p.tok[at + d] = (b * p.NB + k) * p.Dmax + d;
+          at += n;
+        }
+      }
+    }
   }
   two = __syncthreads_or(two);
   if (tid == 0) {
+    if (S < 0 || S > s_cap) {
+      record_error(p.hdr, SSD_ERR_DEVICE, 601);
+      S = 0;
+    }
+    const int ph_s = S > 0 ? ceil_div(tokens, pair) * p.Hkv : 0;
+    const int units_s = ph_s * (ceil_div(S, kTile) + kSetup) * tile_units(tokens, p.tokens);
+    if (units_s > 0 && tokens > p.tokens) two = 1;
+    p.tok_first[p.B] = tokens;
     p.unit0[p.B] = units;
-    p.ph0[p.B] = ph;
     p.plan[kTokens] = tokens;
     // (never less than a tile: a run in the middle of a pair then has one at least)
-    p.plan[kShare] = max(two ? 2 : 1, ceil_div(units, p.ctas));
-    p.plan[kUnits] = units;
+    p.plan[kShare] = max(two ? 2 : 1, ceil_div(units_s + units, p.ctas));
+    p.plan[kUnits] = units_s + units;
     p.plan[kSharedLen] = S;
-  }
-  // the tokens: a warp a sequence
-  for (int b = wid; b < p.B; b += kPlanThreads / 32) {
-    int at = p.tok_first[b];
-    for (int k0 = 0; k0 < p.NB; k0 += 32) {
-      const int len = k0 + lane < p.NB ? min(max(__ldg(p.blk_len + static_cast<int64_t>(b) * p.NB + k0 + lane), 0), p.Dmax) : 0;
-      for (int k = k0; k < min(p.NB, k0 + 32); ++k) {
-        const int n = __shfl_sync(0xffffffffu, len, k - k0);
-        for (int d = lane; d < n; d += 32) p.tok[at + d] = (b * p.NB + k) * p.Dmax + d;
-        at += n;
-      }
-    }
+    p.plan[kSharedUnits] = units_s;
+    p.plan[kSharedPairs] = ph_s;
   }
 }
 
@@ -191,8 +198,8 @@ __device__ __forceinline__ int find_seq(const int* unit0, int B, int u) {
 // Segments of units [u, u1) for CTA c, as many as fit; returns the unit behind them. `b` is the sequence
 // that u lies in, where it is not in the shared part (-1: not looked for yet).
 __device__ int describe(const Params& p, Seg* segs, int* count, int c, int u, int u1, const int* unit0, const int* ph0, const int* tok_first,
-                        const int* own_len, int tokens, int shared_len) {
-  const int pair = 2 * p.tokens, own0 = unit0[0];
+                        const int* own_len, int tokens, int shared_len, int own0, int own_ph) {
+  const int pair = 2 * p.tokens;
   int n = 0, b = -1;
   while (u < u1 && n < kSegs) {
     Seg s;
@@ -205,14 +212,14 @@ __device__ int describe(const Params& p, Seg* segs, int* count, int c, int u, in
       all = tokens;
       ph = 0;
     } else {
-      if (b < 0) b = find_seq(unit0, p.B, u);
-      while (unit0[b + 1] <= u) ++b;
+      if (b < 0) b = find_seq(unit0, p.B, u - own0);
+      while (own0 + unit0[b + 1] <= u) ++b;
       s.b = b;
       s.len = own_len[b];
-      base = unit0[b];
+      base = own0 + unit0[b];
       first = tok_first[b];
       all = tok_first[b + 1] - first;
-      ph = ph0[b];
+      ph = own_ph + ph0[b];
     }
     const int w = tile_units(all, p.tokens), kt = (ceil_div(s.len, kTile) + kSetup) * w, at = (u - base) / kt;
     s.kvh = at % p.Hkv;
@@ -385,13 +392,14 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
     int* off = reinterpret_cast<int*>(smem + Sh::OFF_RING);
     for (int i = tid; i <= p.B; i += kThreads) {
       off[i] = __ldcg(p.unit0 + i);
-      off[(p.B + 1) + i] = __ldcg(p.ph0 + i);
+      off[(p.B + 1) + i] = i < p.B ? __ldcg(p.ph0 + i) : 0;
       off[2 * (p.B + 1) + i] = __ldcg(p.tok_first + i);
       off[3 * (p.B + 1) + i] = i < p.B ? __ldcg(p.own_len + i) : 0;
     }
     __syncthreads();
     if (tid == 0)
-      bars.next = describe(p, bars.segs, &bars.count, cta, u, u1, off, off + (p.B + 1), off + 2 * (p.B + 1), off + 3 * (p.B + 1), tokens, shared_len);
+      bars.next = describe(p, bars.segs, &bars.count, cta, u, u1, off, off + (p.B + 1), off + 2 * (p.B + 1), off + 3 * (p.B + 1), tokens, shared_len,
+                           __ldcg(p.plan + kSharedUnits), __ldcg(p.plan + kSharedPairs));
     fence_async_smem();                                     // TMA writes over what was just read
     __syncthreads();
     u = bars.next;
@@ -715,7 +723,8 @@ __global__ void __launch_bounds__(kSimtThreads) k_parts_simt(Params p) {
   while (u < u1) {
     __syncthreads();
     if (tid == 0)
-      next = describe(p, segs, &count, blockIdx.x, u, u1, p.unit0, p.ph0, p.tok_first, p.own_len, p.plan[kTokens], p.plan[kSharedLen]);
+      next = describe(p, segs, &count, blockIdx.x, u, u1, p.unit0, p.ph0, p.tok_first, p.own_len, p.plan[kTokens], p.plan[kSharedLen],
+                      p.plan[kSharedUnits], p.plan[kSharedPairs]);
     __syncthreads();
     u = next;
     for (int i = 0; i < count; ++i) {
@@ -825,6 +834,8 @@ __device__ __forceinline__ void load_n(const T* p, float (&v)[N]) {
 template <typename T, int DH>
 __global__ void __launch_bounds__(128) k_join(Params p) {
   constexpr int N = DH / 32, H = 4, L = 8;
+  // (Let in by k_parts once the plan is complete, to do the own block meanwhile, it made a call of two tokens
+  // 34 us instead of 18.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, g_of = lane & 3, n_of = lane >> 2;
   const int i = blockIdx.x, groups = ceil_div(p.G, H), unit = blockIdx.y * 4 + (threadIdx.x >> 5);
@@ -833,7 +844,7 @@ __global__ void __launch_bounds__(128) k_join(Params p) {
   const int share = __ldcg(p.plan + kShare), shared_len = __ldcg(p.plan + kSharedLen), pair = 2 * p.tokens;
   const int token = __ldcg(p.tok + i), NT = p.NB * p.Dmax;
   const int b = token / NT, pos = (token - b * NT) % p.Dmax;
-  const int own_first = __ldcg(p.tok_first + b), own_tokens = __ldcg(p.tok_first + b + 1) - own_first, own_u = __ldcg(p.unit0 + b), own_ph = __ldcg(p.ph0 + b), own_len = __ldcg(p.own_len + b);
+  const int own_first = __ldcg(p.tok_first + b), own_tokens = __ldcg(p.tok_first + b + 1) - own_first, own_u = __ldcg(p.plan + kSharedUnits) + __ldcg(p.unit0 + b), own_ph = __ldcg(p.plan + kSharedPairs) + __ldcg(p.ph0 + b), own_len = __ldcg(p.own_len + b);
   const int kvh = unit / groups, g0 = (unit - kvh * groups) * H, gn = min(H, p.G - g0);
   float q[H][N], o[H][N];
 #pragma unroll
