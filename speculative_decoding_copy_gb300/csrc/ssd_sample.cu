@@ -32,16 +32,16 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 512;                 // of one level of `select`
 constexpr int kBinBits = 9;
-constexpr int kLin = 256;                  // bins of a row's values, the first level of top-p
+constexpr int kLin = 512;                  // bins of a row's values, the first level of top-p
 constexpr int kMaxCluster = 8;
 constexpr int kIdxBits = 20;               // V <= 2^20: the weight sums then fit 64 bits
 constexpr int kTab = 64;
 constexpr uint64_t kAll = ~0ull;
-constexpr int kMaxShare = 4;                // top-k tokens a warp answers for, where its lanes' largest bound them
+constexpr int kTop = 4;                     // of each warp's lanes' largest, the ones that bound small top-k
+constexpr int kShortK = 256;                // up to this the tokens above the bound are sorted, beyond they are binned
 constexpr int kList = 1024;                // tokens near a border that one CTA may hold,
 constexpr int kFew = 256;                   // tokens from which one is drawn by sorting them once more
-constexpr int kCrowd = 256;                // entries of a bucket up to which they are counted against each other
-constexpr int kMerged = 4 * kThreads;       // and all CTAs of the cluster together, to be ordered
+constexpr int kMerged = 4 * kThreads;      // and all CTAs of the cluster together, to be sorted
 
 struct Params {
   const void* logits;
@@ -68,12 +68,7 @@ struct Shared {
   int2 tab[kTab];                          // powers of two of the row (make_table)
   union {
     uint32_t hist[2][4][kBins];            // count; bits 0-15, 16-31 and 32-43 of the weight; two levels in turns
-    struct {
-      uint64_t list[2048];                 // unsorted (kMerged of them at most), and
-      uint16_t order[kMerged];             // the places of its entries in ascending order
-      uint16_t slot[kMerged];
-      uint32_t bucket[kThreads + 1];
-    } m;
+    uint64_t sorted[kMerged];
   };
   uint64_t list[kList];                    // this CTA's tokens near a border
   uint64_t ex_sum[2][kMaxCluster];         // from every CTA of the cluster
@@ -82,9 +77,9 @@ struct Shared {
   uint64_t part[kWarps], part2[kWarps];
   uint64_t wsum[kWarps];
   float wmax[kWarps];
-  uint32_t wkey[kWarps];
+  uint32_t wkey[kWarps * kTop];
   uint64_t sel_e, sel_incl;                // of the bin chosen: weight before it, and with it
-  uint32_t sel_n, sel_cnt, sel_bin, list_n, kd_min, kd_max, fullest;
+  uint32_t sel_n, sel_cnt, sel_bin, list_n;
 };
 
 // the same variable in the CTA of rank `r`
@@ -503,6 +498,19 @@ struct Pick {
   __device__ __forceinline__ bool operator()(float x) const { return x >= cut && (per == 0.f || bin_of(x) == bin); }
 };
 
+// bins of the values from `cut` up to the row's largest: rounded, but never falling as the value falls
+__device__ __forceinline__ Pick bins_from(const Scale& sc, float cut) {
+  const float range = sc.zmax - cut, per = range > 0.f ? __fdiv_rd(kLin - 2.f, range) : 0.f;
+  return {cut, sc.zmax, per < kFltMax ? per : 0.f, 0.f, INFINITY, 0};
+}
+// `maybe` of the one bin chosen
+__device__ __forceinline__ void narrow(Pick& pick, const Scale& sc) {
+  if (!sc.plain) return;
+  const float range = sc.zmax - pick.cut, width = range * (1.f / (kLin - 2));
+  pick.mid = fmaf(-width, static_cast<float>(pick.bin), sc.zmax);
+  pick.half = fmaf(fabsf(sc.zmax) + range, 1e-6f, 0.501f * width) + 1.17549435e-38f;
+}
+
 // The bound of comp below which the tokens stay, COUNT: the first `target` of them, else those before
 // which the weight is below `target` (> 0). Looked at: the tokens of `pick`, before which lies the
 // weight e0. Returns the bound and the weight of those that stay. One level for each 9 bits of comp.
@@ -543,43 +551,58 @@ __device__ __noinline__ ulonglong2 select(const Row<T, RES>* shared_row, const S
   }
 }
 
-__device__ __forceinline__ uint64_t exchange(uint64_t v, int i, int k, int d) {
-  const uint64_t o = __shfl_xor_sync(0xffffffffu, v, d);
-  return (((i & k) == 0) == ((i & d) == 0)) == (o < v) ? o : v;
-}
-// sort the first P (a power of two, 32 <= P <= kMerged) entries of `list` ascending, in place
-__device__ void sort_list(uint64_t* list, int P) {
-  const int tid = threadIdx.x;
-  for (int i = tid; i < P; i += kThreads) {
-    uint64_t v = list[i];
+// Sort the first P (a power of two up to kMerged) entries of `list` ascending, a bitonic network: thread t
+// holds entries E t .. E t + E - 1 in registers (P <= E kThreads), neighbours up to 32 E apart meet by shuffles
+// and only wider steps pass through shared memory. 2048 entries take about 7000 clocks of a CTA, 512
+// about 4000 (with every step wider than 32 through shared memory the 2048 took 40000).
+template <int E>
+__device__ __forceinline__ void sort_entries(uint64_t* list, int P) {
+  const int tid = threadIdx.x, i0 = tid * E;
+  uint64_t v[E];
 #pragma unroll
-    for (int k = 2; k <= 32; k <<= 1)
+  for (int e = 0; e < E; ++e) v[e] = i0 + e < P ? list[i0 + e] : kAll;
+  auto pick = [](uint64_t a, uint64_t b, bool low) { return (b < a) == low ? b : a; };
+  for (int k = 2; k <= P; k <<= 1) {
+    for (int j = k >> 1; j >= 32 * E; j >>= 1) {
+      __syncthreads();
 #pragma unroll
-      for (int d = k >> 1; d > 0; d >>= 1) v = exchange(v, i, k, d);
-    list[i] = v;
+      for (int e = 0; e < E; ++e)
+        if (i0 + e < P) list[i0 + e] = v[e];
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (i0 + e < P) v[e] = pick(v[e], list[(i0 + e) ^ j], (((i0 + e) & k) == 0) == (((i0 + e) & j) == 0));
+    }
+#pragma unroll
+    for (int j = 16 * E; j >= E; j >>= 1) {
+      if (j >= k) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        v[e] = pick(v[e], __shfl_xor_sync(0xffffffffu, v[e], j / E), (((i0 + e) & k) == 0) == (((i0 + e) & j) == 0));
+    }
+#pragma unroll
+    for (int j = E >> 1; j > 0; j >>= 1) {
+      if (j >= k) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if ((e & j) == 0) {
+          const uint64_t a = v[e], b = v[e | j];
+          const bool up = ((i0 + e) & k) == 0;
+          v[e] = pick(a, b, up);
+          v[e | j] = pick(a, b, !up);
+        }
+    }
   }
   __syncthreads();
-  for (int k = 64; k <= P; k <<= 1) {
-    for (int j = k >> 1; j >= 32; j >>= 1) {
-      for (int t = tid; t < P / 2; t += kThreads) {
-        const int i = ((t & ~(j - 1)) << 1) | (t & (j - 1));
-        const uint64_t a = list[i], b = list[i + j];
-        if (((i & k) == 0) == (b < a)) {
-          list[i] = b;
-          list[i + j] = a;
-        }
-      }
-      __syncthreads();
-    }
-    // the rest of this merge stays within 32 neighbours
-    for (int i = tid; i < P; i += kThreads) {
-      uint64_t v = list[i];
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) v = exchange(v, i, k, d);
-      list[i] = v;
-    }
-    __syncthreads();
-  }
+  for (int e = 0; e < E; ++e)
+    if (i0 + e < P) list[i0 + e] = v[e];
+  __syncthreads();
+}
+__device__ __noinline__ void sort_list(uint64_t* list, int P) {
+  if (P <= kThreads) sort_entries<1>(list, P);
+  else if (P <= 2 * kThreads) sort_entries<2>(list, P);
+  else sort_entries<4>(list, P);
 }
 
 __device__ __forceinline__ int padded(int n) {
@@ -588,70 +611,10 @@ __device__ __forceinline__ int padded(int n) {
   return P;
 }
 
-// sh.m.order from the n entries of sh.m.list: each goes to one of 512 buckets by its value, and in there
-// to the place that the number of smaller ones gives it. Rows whose values crowd into one bucket
-// (ties) are sorted instead. bucket, kd_min and kd_max are set, `fullest` is 0.
-__device__ __forceinline__ void order_list(Shared& sh, const Scale& sc, int n) {
-  const int tid = threadIdx.x;
-  const float top = okey_value(sc.kmax - sh.kd_min), range = top - okey_value(sc.kmax - sh.kd_max);
-  const float per = range > 0.f ? fminf(__fdividef(kThreads - 2.f, range), kFltMax) : 0.f;
-  uint32_t at[kMerged / kThreads];         // bucket, and place in it above 16 bits
-#pragma unroll
-  for (int e = 0; e < kMerged / kThreads; ++e) {
-    const int j = tid + e * kThreads;
-    if (j < n) {
-      const float z = okey_value(sc.kmax - static_cast<uint32_t>(sh.m.list[j] >> kIdxBits));
-      const int b = min(__float_as_int(fmaf(top - z, per, kMagic)) - kMagicBits, kThreads - 1);
-      at[e] = static_cast<uint32_t>(b) | atomicAdd(&sh.m.bucket[b], 1u) << 16;
-    }
-  }
-  __syncthreads();
-  const uint32_t own = sh.m.bucket[tid];
-  const uint32_t most = __reduce_max_sync(0xffffffffu, own);
-  if ((tid & 31) == 0) atomicMax(&sh.fullest, most);
-  uint64_t total;
-  const uint32_t first = static_cast<uint32_t>(block_scan(own, sh.part, &total));
-  if (sh.fullest > kCrowd) {
-    const int P = padded(n);
-    for (int j = n + tid; j < P; j += kThreads) sh.m.list[j] = kAll;
-    __syncthreads();
-    sort_list(sh.m.list, P);
-    for (int j = tid; j < n; j += kThreads) sh.m.order[j] = static_cast<uint16_t>(j);
-    __syncthreads();
-    return;
-  }
-  sh.m.bucket[tid] = first;
-  if (tid == 0) sh.m.bucket[kThreads] = static_cast<uint32_t>(n);
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < kMerged / kThreads; ++e) {
-    const int j = tid + e * kThreads;
-    if (j < n) sh.m.slot[sh.m.bucket[at[e] & 0xffff] + (at[e] >> 16)] = static_cast<uint16_t>(j);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < kMerged / kThreads; ++e) {
-    const int j = tid + e * kThreads;
-    if (j < n) {
-      const uint32_t b = at[e] & 0xffff, b0 = sh.m.bucket[b], b1 = sh.m.bucket[b + 1];
-      const uint64_t v = sh.m.list[j];
-      uint32_t place = b0;
-      for (uint32_t i = b0; i < b1; ++i) place += sh.m.list[sh.m.slot[i]] < v ? 1 : 0;
-      sh.m.order[place] = static_cast<uint16_t>(j);
-    }
-  }
-  __syncthreads();
-}
-
-// The tokens of `pick`, as comp, of all CTAs in sh.m.list, ordered; returns their number, or -1 where they
-// are too many. Every CTA gets the same.
+// The tokens of `pick`, as comp, of all CTAs in sh.sorted; returns their number, or -1 where they are too many. Every CTA gets the same.
 template <typename R>
 __device__ __forceinline__ int gather(const R& row, const Scale& sc, Shared& sh, int C, const Pick& pick) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  if (tid == 0) {
-    sh.kd_min = ~0u;
-    sh.kd_max = sh.fullest = 0;
-  }
   row.each([&](const float (&x)[4], int i) {
     if (!(pick.maybe(x[0]) || pick.maybe(x[1]) || pick.maybe(x[2]) || pick.maybe(x[3]))) return;
 #pragma unroll
@@ -673,31 +636,21 @@ __device__ __forceinline__ int gather(const R& row, const Scale& sc, Shared& sh,
   }
   if (!fits || n > kMerged) return -1;
   k = __shfl_sync(0xffffffffu, k, wid & (kMaxCluster - 1));
-  sh.m.bucket[tid] = 0;
+  const int P = padded(static_cast<int>(n));
   if (wid < C) {
     const uint64_t* from = peer(sh.list, wid);
-    uint32_t lo = ~0u, hi = 0;
-    for (uint32_t i = lane; i < k; i += 32) {
-      const uint64_t v = from[i];
-      sh.m.list[before + i] = v;
-      lo = min(lo, static_cast<uint32_t>(v >> kIdxBits));
-      hi = max(hi, static_cast<uint32_t>(v >> kIdxBits));
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) {
-      atomicMin(&sh.kd_min, lo);
-      atomicMax(&sh.kd_max, hi);
-    }
+    for (uint32_t i = lane; i < k; i += 32) sh.sorted[before + i] = from[i];
+  } else if (wid >= kMaxCluster) {
+    for (int i = static_cast<int>(n) + tid - 32 * kMaxCluster; i < P; i += kThreads - 32 * kMaxCluster) sh.sorted[i] = kAll;
   }
   __syncthreads();
-  order_list(sh, sc, static_cast<int>(n));
+  sort_list(sh.sorted, P);
   return static_cast<int>(n);
 }
 
-// Of the n ordered tokens in sh.m, before which lies the weight e0: those that stay, in their order,
+// Of the n tokens in sh.sorted, before which lies the weight e0: those that stay, in their order,
 // under `k` tokens, the sum before a token below ceil(top_p * sum of the first k) (or below
-// `target`, where that is > 0) and min-p. *kept: e0 and their weight. At least one stays.
+// `target`, where that is not 0) and min-p. *kept: e0 and their weight. At least one stays.
 __device__ int cut_sorted(Shared& sh, const Scale& sc, int n, uint64_t e0, int k, float top_p, uint64_t target, float min_p, uint64_t* kept) {
   const int tid = threadIdx.x;
   const int per = (n + kThreads - 1) / kThreads;             // up to 4 neighbours a thread
@@ -710,7 +663,7 @@ __device__ int cut_sorted(Shared& sh, const Scale& sc, int n, uint64_t e0, int k
     W[e] = 0;
     mp[e] = true;
     if (e < per && j < n) {
-      const float z = okey_value(sc.kmax - static_cast<uint32_t>(sh.m.list[sh.m.order[j]] >> kIdxBits));
+      const float z = okey_value(sc.kmax - static_cast<uint32_t>(sh.sorted[j] >> kIdxBits));
       float wh, wl;
       weight(z, sc, sh.tab, sh.pow, wh, wl);
       W[e] = weight_int(wh, wl);
@@ -816,9 +769,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
   const Rate rate = make_rate(temp);
   // how far below the largest a token may lie whose weight is (1 - top_p) / V of it
   const float depth = top_p < 1.f ? __fmul_ru(-logf((1.f - fmaxf(top_p, 0.f)) / static_cast<float>(p.V) * 0.999f), temp) : 0.f;
-  // with top-k: the tokens that each warp that holds any, or each CTA, answers for
+  // with top-k: the tokens that each CTA that holds any answers for. A value that many of its tokens reach is
+  // found, and the least of these values is reached by k tokens of the row
   const int warps = (nvec + p.nvw - 1) / p.nvw, ctas = (warps + kWarps - 1) / kWarps;
-  const int share_w = static_cast<int>((k + warps - 1) / warps), share = static_cast<int>((k + ctas - 1) / ctas);
+  const int share = static_cast<int>((k + ctas - 1) / ctas);
   if (tid == 0) sh.list_n = 0;
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (!RES) __syncthreads();               // the ends
@@ -828,24 +782,36 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
   row.each([&](const float (&x)[4], int) { mx = fmaxf(fmaxf(mx, fmaxf(x[0], x[1])), fmaxf(x[2], x[3])); });
   uint32_t reach = 0;                      // as okey; 0: none found
   const uint32_t key = okey(fminf(mx, kFltMax) + 0.f);
-  if (k > 0 && share_w <= kMaxShare) {
-    // the least, over the warps, of the share_w-th largest of the lanes' largest
+  const bool few = k > 0 && share <= kWarps * kTop / 2;
+  if (few) {
     uint32_t left = key;
-    for (int j = 0; j < share_w; ++j) {
-      reach = __reduce_max_sync(0xffffffffu, left);
-      const uint32_t who = __ballot_sync(0xffffffffu, left == reach);
+#pragma unroll
+    for (int j = 0; j < kTop; ++j) {
+      const uint32_t most = __reduce_max_sync(0xffffffffu, left);
+      const uint32_t who = __ballot_sync(0xffffffffu, left == most);
       if (lane == __ffs(who) - 1) left = 0;
+      if (lane == 0) sh.wkey[wid * kTop + j] = row.nw > 0 ? most : 0;
     }
-    if (lane == 0) sh.wkey[wid] = row.nw > 0 ? reach : ~0u;
   }
   {
     const float m = warp_max(mx);
     if (lane == 0) sh.wmax[wid] = m;
   }
   __syncthreads();
-  if (k > 0 && share_w > kMaxShare && share <= 2 * kThreads) {
-    // the least, over the CTAs, of the share-th largest of the threads' largest (with more tokens
-    // than threads: half the share by their second largest, which two tokens reach), to 16 bits
+  if (few) {
+    // the share-th largest of the warps' kTop largest each: the largest that as many reach
+    if (wid == 0) {
+#pragma unroll
+      for (int j = 0; j < kWarps * kTop / 32; ++j) {
+        const uint32_t v = sh.wkey[32 * j + lane];
+        int n = 0;
+        for (int i = 0; i < kWarps * kTop; ++i) n += sh.wkey[i] >= v ? 1 : 0;
+        reach = max(reach, __reduce_max_sync(0xffffffffu, n >= share ? v : 0u));
+      }
+    }
+  } else if (k > 0 && share <= 2 * kThreads) {
+    // the share-th largest of the threads' largest (with more tokens than threads: half the share by
+    // their second largest, which two tokens reach), to 16 bits
     uint32_t own = key;
     int want = share;
     if (share > kThreads) {
@@ -860,23 +826,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
       own = okey(fminf(m2, kFltMax) + 0.f);
       want = (share + 1) / 2;
     }
-    reach = 0;
     for (int bit = 31; bit >= 16; --bit) {
       const uint32_t t = reach | (1u << bit);
       if (__syncthreads_count(own >= t) >= want) reach = t;
     }
-    if (rank >= ctas) reach = ~0u;
   }
+  if (rank >= ctas) reach = ~0u;           // a CTA without tokens does not count
   if (tid < C) {
     float t = -INFINITY;
-    uint32_t least = share_w <= kMaxShare ? ~0u : reach;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      t = fmaxf(t, sh.wmax[w]);
-      if (share_w <= kMaxShare) least = min(least, sh.wkey[w]);
-    }
+    for (int w = 0; w < kWarps; ++w) t = fmaxf(t, sh.wmax[w]);
     *peer(&sh.ex_max[rank], tid) = t;
-    *peer(&sh.ex_key[rank], tid) = least;
+    *peer(&sh.ex_key[rank], tid) = reach;
   }
   cluster_sync();
   float zmax = -INFINITY;
@@ -903,13 +864,46 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
       // from low to zmax, a little wider
       const float span = 0.5f * (sc.zmax - low);
       const Pick pick = {low, 0.f, 0.f, low + span, sc.plain ? fmaf(fabsf(sc.zmax) + fabsf(low), 1e-6f, span) + 1.17549435e-38f : INFINITY, 0};
-      const int n = gather(row, sc, sh, C, pick);
-      if (n >= 0) {
-        const int m = cut_sorted(sh, sc, n, 0, static_cast<int>(k), top_p, 0, min_p, &S);
-        bound = sh.m.list[sh.m.order[m - 1]] + 1;
-        stays = m;
-        all_cut = true;
-      } else {
+      int n = -1;
+      if (k <= kShortK) {
+        n = gather(row, sc, sh, C, pick);
+        if (n >= 0) {
+          const int m = cut_sorted(sh, sc, n, 0, static_cast<int>(k), top_p, 0, min_p, &S);
+          bound = sh.sorted[m - 1] + 1;
+          stays = m;
+          all_cut = true;
+        }
+      }
+      const float range = sc.zmax - low;
+      if (n < 0 && low > -kFltMax && range > 1e-30f && range < kFltMax) {
+        // many: bins of the values from low up, then the tokens of the bin in which the k-th lies
+        if (k <= kShortK) {                // another CTA may still read the list of before
+          cluster_sync();
+          if (tid == 0) sh.list_n = 0;
+        }
+        Pick bin = bins_from(sc, low);
+        clear_bins<kLin>(sh, 0);
+        row.each([&](const float (&x)[4], int) {
+          if (!(x[0] >= low || x[1] >= low || x[2] >= low || x[3] >= low)) return;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (x[e] >= low) {
+              float wh, wl;
+              weight(x[e], sc, sh.tab, sh.pow, wh, wl);
+              add_to_bin<true>(sh, 0, bin.bin_of(x[e]), weight_int(wh, wl));
+            }
+        });
+        cluster_sync();
+        uint64_t n0 = 0, e0 = 0, incl, cnt;
+        bin.bin = find_bin<true, kLin>(sh, 0, C, static_cast<uint64_t>(k), n0, e0, &incl, &cnt);
+        narrow(bin, sc);
+        n = gather(row, sc, sh, C, bin);
+        if (n >= 0) {
+          const int m = cut_sorted(sh, sc, n, e0, static_cast<int>(k - static_cast<int64_t>(n0)), 1.f, kAll, 0.f, &S);
+          bound = sh.sorted[m - 1] + 1;
+        }
+      }
+      if (n < 0) {
         if (tid == 0) shared_pick = pick;
         const ulonglong2 got = select<true>(&shared_row, &shared_scale, &shared_pick, static_cast<uint64_t>(k), 0, sh, C);
         bound = got.x;
@@ -920,10 +914,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
     if (top_p < 1.f && !all_cut) {
       // tokens of a weight below (1 - top_p) / V, together, are not more than the tail that is cut
       // (the sum is at least 1); binned by their value are the others, and all are summed
-      const float z_cut = fmaxf(__fadd_rd(sc.zmax, -depth), sc.zmin), range = sc.zmax - z_cut;
-      const float per = range > 0.f ? __fdiv_rd(kLin - 2.f, range) : 0.f;
-      // bins of values: rounded, but never falling as the value falls
-      Pick pick = {z_cut, sc.zmax, per < kFltMax ? per : 0.f, 0.f, INFINITY, 0};
+      const float z_cut = fmaxf(__fadd_rd(sc.zmax, -depth), sc.zmin);
+      Pick pick = bins_from(sc, z_cut);
       if (known) {                         // another CTA may still read the bins or the list of before
         cluster_sync();
         if (tid == 0) sh.list_n = 0;
@@ -931,6 +923,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
       clear_bins<kLin>(sh, 0);
       uint32_t sa = 0, sb = 0, count = 0;
       row.each([&](const float (&x)[4], int) {
+        // (the sum of the first k is known: only the bins are asked for)
+        if (known && !(x[0] >= z_cut || x[1] >= z_cut || x[2] >= z_cut || x[3] >= z_cut)) return;
         uint32_t a[4], b[4];
         f32x2 wh[2], wl[2];
         weights4(x, sc, sh.tab, sh.pow, wh, wl);
@@ -950,15 +944,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
       const uint64_t target = max(mul_fraction(known ? S : sum, fmaxf(top_p, 0.f), true), uint64_t{1});
       uint64_t n0 = 0, e0 = 0, incl, cnt;
       pick.bin = find_bin<false, kLin>(sh, 0, C, target, n0, e0, &incl, &cnt);
-      if (sc.plain) {
-        const float width = range * (1.f / (kLin - 2));
-        pick.mid = fmaf(-width, static_cast<float>(pick.bin), sc.zmax);
-        pick.half = fmaf(fabsf(sc.zmax) + range, 1e-6f, 0.501f * width) + 1.17549435e-38f;
-      }
+      narrow(pick, sc);
       const int n = gather(row, sc, sh, C, pick);
       if (n >= 0) {
         const int m = cut_sorted(sh, sc, n, e0, n, 1.f, target, 0.f, &S);
-        bound = sh.m.list[sh.m.order[m - 1]] + 1;
+        bound = sh.sorted[m - 1] + 1;
       } else {
         if (tid == 0) shared_pick = pick;
         const ulonglong2 got = select<false>(&shared_row, &shared_scale, &shared_pick, target, e0, sh, C);
@@ -1107,17 +1097,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
         const int P = padded(stays);
         uint64_t own = kAll;
         if (tid < stays) {
-          const uint64_t comp = sh.m.list[sh.m.order[tid]];
+          const uint64_t comp = sh.sorted[tid];
           float wh, wl;
           weight(okey_value(sc.kmax - static_cast<uint32_t>(comp >> kIdxBits)), sc, sh.tab, sh.pow, wh, wl);
           own = (comp & ((1u << kIdxBits) - 1)) << 44 | weight_int(wh, wl);
         }
-        const uint64_t comp = tid < stays ? sh.m.list[sh.m.order[tid]] : 0;
+        const uint64_t comp = tid < stays ? sh.sorted[tid] : 0;
         __syncthreads();
-        if (tid < P) sh.m.list[tid] = own;
+        if (tid < P) sh.sorted[tid] = own;
         __syncthreads();
-        sort_list(sh.m.list, P);
-        const uint64_t at = tid < stays ? sh.m.list[tid] : 0, W = at & ((1ull << 44) - 1);
+        sort_list(sh.sorted, P);
+        const uint64_t at = tid < stays ? sh.sorted[tid] : 0, W = at & ((1ull << 44) - 1);
         uint64_t all;
         const uint64_t pre = block_scan(W, sh.part, &all);
         if (thr >= pre && thr < pre + W) sh.sel_bin = static_cast<uint32_t>(at >> 44);
