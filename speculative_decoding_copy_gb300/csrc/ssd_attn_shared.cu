@@ -729,8 +729,9 @@ __global__ void __launch_bounds__(kSimtThreads) k_parts_simt(Params p) {
     u = next;
     for (int i = 0; i < count; ++i) {
       const Seg s = segs[i];
-      const float* kb = static_cast<const float*>(s.b < 0 ? p.k_shared : p.k_cache);
-      const float* vb = static_cast<const float*>(s.b < 0 ? p.v_shared : p.v_cache);
+      const bool apart = s.b < 0 && p.shared_table == nullptr;        // else in the caches' pages
+      const float* kb = static_cast<const float*>(apart ? p.k_shared : p.k_cache);
+      const float* vb = static_cast<const float*>(apart ? p.v_shared : p.v_cache);
       // the rows of both tiles one after another: row x is head x % G of token x / G
       const int rows = s.ntok * p.G;
       for (int x0 = 0; x0 < rows; x0 += 8 * kSimtRows) {

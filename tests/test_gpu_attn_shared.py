@@ -102,7 +102,8 @@ SHAPES = [
 
 
 @pytest.mark.parametrize("kw", SHAPES, ids=lambda k: "S%d own%s" % (k["S_len"], k["own"][:3]))
-@pytest.mark.parametrize("dh,paged,f32", [(128, False, False), (64, False, False), (128, True, False), (64, True, False), (128, False, True), (64, False, True)])
+@pytest.mark.parametrize("dh,paged,f32", [(128, False, False), (64, False, False), (128, True, False), (64, True, False), (128, False, True), (64, False, True),
+                                          (128, True, True), (64, True, True)])
 def test_against_oracle(kw, dh, paged, f32):
     c = Case(1, dh=dh, paged=paged, f32=f32, **kw)
     c.check(c.run())
