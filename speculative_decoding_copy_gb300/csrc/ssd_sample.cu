@@ -6,14 +6,34 @@
 // cut nor a token depends on the order in which threads add. The tokens that stay are the first
 // ones in the order (z descending, index ascending), so one composite number
 //   comp = (okey(z_max) - okey(z)) * 2^20 + index       (okey: the fp32 order as unsigned integers)
-// and one bound say which. A bound is found by histograms of 512 bins of comp (count and weight
-// of each), the next one over the bin in which the count passes top-k or the weight passes
-// top_p * sum, down to single tokens; ties at the border are thereby cut by their index.
+// and one bound say which; ties at the border are thereby cut by their index.
 //
-// A cluster of 1 to 8 CTAs holds a row in its shared memory: it is read from HBM once, and the
-// passes over it (sum, histograms, output) read shared memory. Partial results cross the
-// cluster through distributed shared memory. Rows beyond the cluster's shared memory are
-// read again from L2.
+// A cluster of 1 to 8 CTAs holds a row in its shared memory: it is read from HBM once, and every
+// further pass reads shared memory. Partial results cross the cluster through distributed shared
+// memory. Rows beyond the cluster's shared memory are read again from L2. The passes:
+//   1  the largest value; with top-k also a value that at least k tokens reach (the share-th largest of
+//      the warps' or the threads' own largest, the least of these over the CTAs);
+//   2a top-k up to 256: the tokens above that value, as a rule little more than k, are brought together
+//      and sorted in every CTA; top-k, top-p, min-p and the draw follow from that list alone;
+//   2b larger top-k: bins of the values from there up (count and weight), the tokens of the bin in
+//      which the k-th lies sorted;
+//   2c top-p alone, or behind 2b: all weights summed, those that can matter in 512 bins of their value;
+//      the tokens of the bin in which the sum passes top_p of the whole sorted. Tokens of a weight
+//      below (1 - top_p) / V cannot be the border and are not binned;
+//   3  the weight of what stays, where min-p or a draw needs it; the output rows; the token.
+// Lists too long to be sorted (thousands of equal values) go through `select`, nine bits of comp a level.
+//
+// What bounds it: not HBM. 81 rows of 128256 fp32 logits (nucleus) take 82 us, 1.0 TB/s of the 83 MB
+// that have to be moved (12 us): about 90 instructions a token (two evaluations of its weight of 25
+// each, the rest bins, tests and the output) and 2000 a warp for the fixed phases, barriers across a
+// cluster of six among them; issue slots are busy for half of the time with two CTAs an SM, which is
+// what registers (64 a thread) and shared memory allow. In steps (us, that case / 64 tokens of 151936
+// bf16 logits): every level of a radix search weighs every token 221 / 245; one fp64 division and
+// logarithm a thread taken out 219 / 163 (a single row 87 -> 17); bins of linear width 133 / 68; pairs
+// of fp32 in one instruction 93; the border's tokens sorted in registers and the row on six CTAs
+// instead of eight 85; top-k bounded from each warp's four largest (256 rows 66 -> 60) 82 / 69.
+// Tried without gain: 384 threads and no spilled registers; weights added to a bin by two additions
+// that wait for nothing instead of one that returns its carry.
 #include <math.h>
 
 #include <algorithm>
@@ -41,6 +61,7 @@ constexpr int kTop = 4;                     // of each warp's lanes' largest, th
 constexpr int kShortK = 256;                // up to this the tokens above the bound are sorted, beyond they are binned
 constexpr int kList = 1024;                // tokens near a border that one CTA may hold,
 constexpr int kFew = 256;                   // tokens from which one is drawn by sorting them once more
+constexpr int kThreadTokens = 512;         // a thread's part of a row, at most
 constexpr int kMerged = 4 * kThreads;      // and all CTAs of the cluster together, to be sorted
 
 struct Params {
@@ -67,7 +88,7 @@ struct Shared {
   float2 pow[kTab];                        // kPowers
   int2 tab[kTab];                          // powers of two of the row (make_table)
   union {
-    uint32_t hist[2][4][kBins];            // count; bits 0-15, 16-31 and 32-43 of the weight; two levels in turns
+    uint32_t hist[2][4][kBins];            // count; sums of bits 0-15 (or 0-31), 16-31 and 32-43 of the weight; two levels in turns
     uint64_t sorted[kMerged];
   };
   uint64_t list[kList];                    // this CTA's tokens near a border
@@ -430,14 +451,20 @@ __device__ __forceinline__ void clear_bins(Shared& sh, int buf) {
   __syncthreads();
 }
 
-// add one token to a bin: its weight in three parts, whose sums over a CTA's tokens (fewer than 2^16)
-// fit a word each, so that no addition has to wait for a carry; the last one is rare
-template <bool COUNT>
+// add one token to a bin. SMALL: of at most 2^16 a CTA, so that the sums of the weight's three parts fit a
+// word each and no addition has to wait for a carry (the last one is rare); else the low word's carry goes
+// into the high one, whose sum over 2^20 tokens is at most 2^31
+template <bool COUNT, bool SMALL>
 __device__ __forceinline__ void add_to_bin(Shared& sh, int buf, int bin, uint64_t W) {
   if (COUNT) atomicAdd(&sh.hist[buf][0][bin], 1u);
-  const uint32_t l = static_cast<uint32_t>(W), h = static_cast<uint32_t>(W >> 32);
-  atomicAdd(&sh.hist[buf][1][bin], l & 0xffffu);
-  atomicAdd(&sh.hist[buf][2][bin], l >> 16);
+  const uint32_t l = static_cast<uint32_t>(W);
+  uint32_t h = static_cast<uint32_t>(W >> 32);
+  if (SMALL) {
+    atomicAdd(&sh.hist[buf][1][bin], l & 0xffffu);
+    atomicAdd(&sh.hist[buf][2][bin], l >> 16);
+  } else {
+    h += atomicAdd(&sh.hist[buf][1][bin], l) > ~l ? 1u : 0u;
+  }
   if (h != 0) atomicAdd(&sh.hist[buf][3][bin], h);
 }
 
@@ -539,7 +566,7 @@ __device__ __noinline__ ulonglong2 select(const Row<T, RES>* shared_row, const S
         if (at >> width != 0) continue;
         float wh, wl;
         weight(x[e], sc, sh.tab, sh.pow, wh, wl);
-        add_to_bin<true>(sh, buf, static_cast<int>(at >> shift), weight_int(wh, wl));
+        add_to_bin<true, RES>(sh, buf, static_cast<int>(at >> shift), weight_int(wh, wl));
       }
     });
     cluster_sync();
@@ -890,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
             if (x[e] >= low) {
               float wh, wl;
               weight(x[e], sc, sh.tab, sh.pow, wh, wl);
-              add_to_bin<true>(sh, 0, bin.bin_of(x[e]), weight_int(wh, wl));
+              add_to_bin<true, RES>(sh, 0, bin.bin_of(x[e]), weight_int(wh, wl));
             }
         });
         cluster_sync();
@@ -935,9 +962,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
         count += 4;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (x[e] >= z_cut) add_to_bin<false>(sh, 0, pick.bin_of(x[e]), weight_of(a[e], b[e]));
+          if (x[e] >= z_cut) add_to_bin<false, RES>(sh, 0, pick.bin_of(x[e]), weight_of(a[e], b[e]));
       });
-      // the biases go out modulo 2^32: a thread holds at most 512 tokens, so the sums fit
+      // the biases go out modulo 2^32: a thread holds at most kThreadTokens, so the sums (2^21 each) fit
       sa -= count * kMagicBits;
       sb -= count * kMagicBits;
       const uint64_t sum = cluster_sum(static_cast<uint64_t>(static_cast<int64_t>(static_cast<int>(sa)) * 4194304 + static_cast<int>(sb)), sh, 0, rank, C, &before, &mine);
@@ -1156,11 +1183,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
 }
 
 constexpr int kMaxData = 160 * 1024;       // a CTA's part of a row in shared memory, at most
+// and no more than the 2^16 tokens whose sums in bins fit (add_to_bin)
+template <typename T>
+constexpr int max_data() {
+  return std::min(kMaxData, 65536 * static_cast<int>(sizeof(T)));
+}
 
 template <typename T>
 static void shape(int nvec, int C, Params& p) {
   p.nvw = (nvec + kWarps * C - 1) / (kWarps * C);
-  p.nres = std::min(p.nvw, kMaxData / 16 / kWarps);
+  p.nres = std::min(p.nvw, max_data<T>() / 16 / kWarps);
 }
 
 // CTAs of a row and clusters that run at once, for a row of nvec vectors: asked once for each C and
@@ -1213,6 +1245,7 @@ static int launch(const Params& in, int64_t rows, cudaStream_t s) {
   double least = 0.;
   for (int c = 1; c <= kMaxCluster; ++c) {
     shape<T>(nvec, c, p);
+    if ((p.nvw + 31) / 32 * VE > kThreadTokens) continue;
     const int active = active_clusters<T>(dev, c, static_cast<size_t>(p.nres) * kWarps * 16);
     if (active < 1) continue;
     double part = static_cast<double>(p.nvw) * kWarps * VE;
