@@ -15,10 +15,23 @@
 // k_parts, 576 threads, all 512 columns of TMEM: warps 0-7 and 8-15 hold a row tile each (two threads a row,
 // 64 of a tile's 128 keys each): scores from TMEM into registers, the row's maximum between the two
 // threads, P as bf16 pairs back into TMEM, O rescaled in TMEM only when a maximum grew by
-// more than 2^8; warp 16 fetches K and V tiles by TMA into a ring of five; warp 17 issues the products, those of one tile while the other's softmax
-// runs, and before that zeroes the value rows behind a length (0 times NaN is NaN).
+// more than 2^8; warp 16 fetches K and V tiles by TMA into a ring of five; warp 17 issues the products,
+// those of one tile while the other's softmax runs, and before that zeroes the value rows behind a
+// length (0 times NaN is NaN).
+// The order of a unit's products is S0 S1 | S0' PV0 S1' PV1 | ..: the next scores are issued before this
+// tile's probabilities are made, so neither the products nor the exponentials wait for the other's latency.
+// Segments of one row tile (few tokens) run two side by side, one in each row tile's place.
 // Every wait is bounded; after one that gave up the CTA records SSD_ERR_TIMEOUT, waits (bounded) for its
-// copies and products in flight and ends.
+// copies and products in flight and ends; rows it shares come out NaN.
+//
+// What bounds it (clocks of a unit of 128 keys x 256 rows, dh 128): 3350, of which the four products take
+// 2060 at their best and the exponentials 2050 (4 a clock and scheduler). In steps: 4450 with one thread
+// issuing in a diverged warp (170 clocks a product instead of 64); 3400 issued by a converged one; the same
+// with a cubic for 3 of 8 exponentials (its instructions cost what the unit saves) and with two threads a
+// row; 3350 with the scores ahead, now the products' own queue. A segment's end (O out, the next Q in)
+// costs 8000 clocks, 15000 before its rows were written side by side. 32 sequences, 9 blocks of 16 tokens
+// (30% there) behind 16384 shared and up to 2048 own keys: 402 us, 0.5 of the bf16 rate; 64 single
+// tokens behind 8192 and up to 500: 47 us for 103 MB.
 #include <cuda.h>
 #include <math.h>
 
@@ -36,7 +49,7 @@ using namespace tc;
 constexpr int kTile = 128;                 // keys of a tile, packed rows of a row tile
 constexpr int kThreads = 576;
 constexpr int kSlots = 5;                  // ring of K and V tiles
-constexpr int kBarBytes = 3072;
+constexpr int kBarBytes = 3 * 1024;
 constexpr int kSegs = 20;                  // segments a CTA has described at once
 constexpr int kMaxBatch = 4096;            // sequences: their offsets fit the ring before it is used
 constexpr unsigned long long kWaitClocks = 1ull << 32;
@@ -285,7 +298,7 @@ struct Shape {
   static constexpr uint32_t OFF_Q = 0;                      // two row tiles
   static constexpr uint32_t OFF_RING = 2 * kTileB;
   static constexpr uint32_t OFF_BAR = OFF_RING + kSlots * kTileB;
-  static constexpr uint32_t kSmem = OFF_BAR + kBarBytes;    // the base is 1024-byte aligned: there is no static shared memory  // + slack to align the base to 1024
+  static constexpr uint32_t kSmem = OFF_BAR + kBarBytes;    // the base is 1024-byte aligned: there is no static shared memory
 };
 static_assert(Shape<128>::kSmem <= 232448, "shared memory per CTA");
 static_assert(4 * (kMaxBatch + 1) * 4 <= kSlots * static_cast<int>(Shape<64>::kTileB), "offsets fit the ring");
@@ -386,11 +399,12 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
   int last = -1;                                            // tile of the last scores
   uint32_t it = 0, tiles = 0, ph_s = 0, ph_p = 0, ph_q = 0, ph_o = 0, used = 0;
 
-  bool more = u < u1;
-  while (more) {
-    // offsets of the sequences into the ring, then this CTA's segments from there
+  bool gave_up = false;
+  while (u < u1) {
+    // offsets of the sequences into the ring, then this CTA's segments from there (after a wait that gave up
+    // copies may still arrive in the ring)
     int* off = reinterpret_cast<int*>(smem + Sh::OFF_RING);
-    for (int i = tid; i <= p.B; i += kThreads) {
+    for (int i = tid; i <= p.B && !gave_up; i += kThreads) {
       off[i] = __ldcg(p.unit0 + i);
       off[(p.B + 1) + i] = i < p.B ? __ldcg(p.ph0 + i) : 0;
       off[2 * (p.B + 1) + i] = __ldcg(p.tok_first + i);
@@ -398,14 +412,19 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
     }
     __syncthreads();
     if (tid == 0)
-      bars.next = describe(p, bars.segs, &bars.count, cta, u, u1, off, off + (p.B + 1), off + 2 * (p.B + 1), off + 3 * (p.B + 1), tokens, shared_len,
+      bars.next = describe(p, bars.segs, &bars.count, cta, u, u1, gave_up ? p.unit0 : off, gave_up ? p.ph0 : off + (p.B + 1),
+                           gave_up ? p.tok_first : off + 2 * (p.B + 1), gave_up ? p.own_len : off + 3 * (p.B + 1), tokens, shared_len,
                            __ldcg(p.plan + kSharedUnits), __ldcg(p.plan + kSharedPairs));
     fence_async_smem();                                     // TMA writes over what was just read
     __syncthreads();
     u = bars.next;
     const int nseg = bars.count;
 
-    if (warp < 16) {
+    if (gave_up) {
+      // segments that nothing computes: their rows come out NaN, not as what the workspace held
+      for (int e = tid; e < 256 * nseg; e += kThreads)
+        *reinterpret_cast<float2*>(p.ml + (static_cast<int64_t>(bars.segs[e >> 8].id) * 256 + (e & 255)) * 2) = make_float2(NAN, NAN);
+    } else if (warp < 16) {
       // -------------------------------------------------------- softmax rows: two threads a row
       const int t = warp >> 3, half = (warp >> 2) & 1;      // row tile; keys 0-63 or 64-127 of a key tile
       const int r = (warp & 3) * 32 + lane;                 // this thread's row
@@ -682,7 +701,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
       }
     }
     // segments and ring are free; the CTA goes on, or ends, as one
-    more = !__syncthreads_or(bars.failed) && u < u1;
+    gave_up = __syncthreads_or(bars.failed);
   }
 
   // copies in flight end before the CTA does, also after a wait that gave up
