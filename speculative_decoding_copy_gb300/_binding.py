@@ -523,10 +523,10 @@ def _new(stream, shape, dtype, device, make=torch.empty):
 
 
 def _quant_call(fn, args, ws, device, stream, *named, more=()):
-    """Call entry point `fn` (`more`: what it takes between `args` and the workspace) on `stream` (the device's current one where none is given) with the
+    """Call entry point `fn` on `stream` (the device's current one where none is given) with the
     device current; a workspace whose header is clear is made where none is given. `named`:
     the (name, tensor) pairs that must not overlap, to name those for which the call was
-    refused."""
+    refused. `more`: what the entry point takes between `args` and the workspace."""
     if ws is None:
         ws = _new(stream, 256, torch.uint8, device, torch.zeros)
     elif ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
@@ -767,14 +767,10 @@ def ssd_verify_attn_shared(q, k_shared, v_shared, shared_len, k_cache, v_cache, 
         with torch.cuda.device(dev):
             need = ssd_verify_attn_shared_workspace_size(args)
         ws = _new(stream, max(need, 256), torch.uint8, dev)
-        ws[:256].zero_() if stream is None else _zero_on(stream, ws)
+        with torch.cuda.stream(stream):
+            ws[:256].zero_()
     _quant_call("ssd_verify_attn_shared", args, ws, dev, stream, ("out", out), ("q", q))
     return out
-
-
-def _zero_on(stream, ws):
-    with torch.cuda.stream(stream):
-        ws[:256].zero_()
 
 
 # ---------------------------------------------------------------------------
