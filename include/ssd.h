@@ -26,6 +26,9 @@
  * ssd_commit_kv (append the accepted candidates' keys and values to the cache),
  * the 8-bit cache (ssd_append_kv_quant, ssd_commit_kv_quant write it,
  * ssd_verify_attn_quant attends over it) and its pages (ssd_page_tables),
+ * sampled continuations of one prompt (ssd_verify_attn_shared reads its keys once for the
+ * batch, ssd_filter_probs makes the distributions that a temperature, top-k, top-p and
+ * min-p leave, ssd_sample draws the drafts from them),
  * ssd_copy_stats (copy attempts and speculation tax), ssd_lowrank_head (the
  * SlimSpec low-rank draft LM head), ssd_accept_static (ssd_accept without a
  * caller workspace) with ssd_read_static_error, and the diagnostics
@@ -711,8 +714,9 @@ int ssd_verify_attn_shared(const ssd_attn_shared_args* a, void* ws, size_t ws_by
  *     w >= min_p                                         (min_p <= 0 or NaN: all)
  *   or j = 0; p_i = w_i / sum of w of those that stay, 0 for the others.
  * T == 0 is greedy: the first of the largest stays alone. A T that is negative or NaN
- * records SSD_ERR_DEVICE and counts as 0; one above 2^100 counts as 2^100. A NaN logit counts as -inf and never stays, +inf as the
- * largest finite number; a row without a logit above -inf becomes all zeros.
+ * records SSD_ERR_DEVICE and counts as 0; one above 2^100 counts as 2^100, one between 0 and
+ * log2(e) 2^-120 as that. A NaN logit counts as -inf and never stays, +inf as the largest finite
+ * number; a row without a logit above -inf becomes all zeros.
  * Weights have a relative error under 2^-29 and sums are exact sums of round(w 2^43), so results
  * do not depend on the order of execution, and a token is cut otherwise than in exact
  * arithmetic only where the sum before it is within about 2^-29 of the border (relative).
