@@ -13,7 +13,7 @@
 // memory. Rows beyond the cluster's shared memory are read again from L2. The passes:
 //   1  the largest value; with top-k also a value that at least k tokens reach (the share-th largest of
 //      the warps' or the threads' own largest, the least of these over the CTAs);
-//   2a top-k up to 256: the tokens above that value, as a rule little more than k, are brought together
+//   2a top-k up to 1024: the tokens above that value, as a rule little more than k, are brought together
 //      and sorted in every CTA; top-k, top-p, min-p and the draw follow from that list alone;
 //   2b larger top-k: bins of the values from there up (count and weight), the tokens of the bin in
 //      which the k-th lies sorted;
@@ -58,9 +58,9 @@ constexpr int kIdxBits = 20;               // V <= 2^20: the weight sums then fi
 constexpr int kTab = 64;
 constexpr uint64_t kAll = ~0ull;
 constexpr int kTop = 4;                     // of each warp's lanes' largest, the ones that bound small top-k
-constexpr int kShortK = 256;                // up to this the tokens above the bound are sorted, beyond they are binned
+constexpr int kShortK = 1024;               // up to this the tokens above the bound are sorted, beyond they are binned
 constexpr int kList = 1024;                // tokens near a border that one CTA may hold,
-constexpr int kFew = 256;                   // tokens from which one is drawn by sorting them once more
+constexpr int kFew = kThreads;             // tokens from which one is drawn by sorting them once more
 constexpr int kThreadTokens = 512;         // a thread's part of a row, at most
 constexpr int kMerged = 4 * kThreads;      // and all CTAs of the cluster together, to be sorted
 
