@@ -31,7 +31,8 @@
 // bf16 logits): every level of a radix search weighs every token 221 / 245; one fp64 division and
 // logarithm a thread taken out 219 / 163 (a single row 87 -> 17); bins of linear width 133 / 68; pairs
 // of fp32 in one instruction 93; the border's tokens sorted in registers and the row on six CTAs
-// instead of eight 85; top-k bounded from each warp's four largest (256 rows 66 -> 60) 82 / 69.
+// instead of eight 85; top-k bounded from each warp's four largest (256 rows 66 -> 60) 82 / 69;
+// top-k up to 1024 from the list 82 / 63; lists of more than 1024 tokens sorted a CTA each and merged 82 / 61.
 // Tried without gain: 384 threads and no spilled registers; weights added to a bin by two additions
 // that wait for nothing instead of one that returns its carry.
 #include <math.h>
@@ -638,6 +639,36 @@ __device__ __forceinline__ int padded(int n) {
   return P;
 }
 
+// The sorted tokens of all CTAs' lists in every CTA's sh.sorted: each CTA sorts its own, finds how many of
+// each other's lie before each of its tokens, all lists in step, and puts the token there in every CTA.
+// 1400 tokens of four CTAs take 20000 to 35000 clocks; all sorted in each CTA they took 35000 to 55000.
+__device__ __noinline__ void merge_lists(Shared& sh, int C, int rank) {
+  const int tid = threadIdx.x, own = static_cast<int>(sh.list_n), P = padded(own);
+  for (int i = own + tid; i < P; i += kThreads) sh.list[i] = kAll;
+  __syncthreads();
+  sort_list(sh.list, P);
+  cluster_sync();
+  int n[kMaxCluster];
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c) n[c] = c < C && c != rank ? static_cast<int>(*peer(&sh.list_n, c)) : 0;
+  for (int i = tid; i < own; i += kThreads) {
+    const uint64_t comp = sh.list[i];
+    int at[kMaxCluster];
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) at[c] = 0;
+#pragma unroll 1
+    for (int step = kList; step > 0; step >>= 1)
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c)
+        if (at[c] + step <= n[c] && peer(sh.list, c)[at[c] + step - 1] < comp) at[c] += step;
+    int to = i;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) to += at[c];
+    for (int c = 0; c < C; ++c) peer(sh.sorted, c)[to] = comp;
+  }
+  cluster_sync();
+}
+
 // The tokens of `pick`, as comp, of all CTAs in sh.sorted; returns their number, or -1 where they are too many. Every CTA gets the same.
 template <typename R>
 __device__ __forceinline__ int gather(const R& row, const Scale& sc, Shared& sh, int C, const Pick& pick) {
@@ -662,6 +693,10 @@ __device__ __forceinline__ int gather(const R& row, const Scale& sc, Shared& sh,
     n += kc;
   }
   if (!fits || n > kMerged) return -1;
+  if (n > 2 * kThreads) {
+    merge_lists(sh, C, static_cast<int>(cluster_rank()));
+    return static_cast<int>(n);
+  }
   k = __shfl_sync(0xffffffffu, k, wid & (kMaxCluster - 1));
   const int P = padded(static_cast<int>(n));
   if (wid < C) {

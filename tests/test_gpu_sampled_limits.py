@@ -4,9 +4,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import sample_oracle as Q
 from speculative_decoding_copy_gb300 import _binding as S
 from test_gpu_attn_shared import DEV, Case
-from test_gpu_sample import _check_row, _rows, _settings
+from test_gpu_sample import NEAR, _check_row, _rows, _settings
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +91,32 @@ def test_logit_rows_beyond_32_bits():
             assert torch.equal(out[s], out[r])
         assert (got["token"][r::3] == got["token"][r]).all() and got["token"][r] >= 0
     assert ok >= 2
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("R,V", [(1, 50257), (8, 128256), (64, 20000), (300, 5003)])
+def test_top_k_of_hundreds(R, V, bf16):
+    """Sorted lists of one and of several CTAs, lists too long to be sorted, and the bins beyond; drawn from the
+    list and from the row."""
+    rng = np.random.default_rng(R)
+    rows = [(t, k, p, m) for k in (257, 512, 513, 700, 1000, 1024, 1025, 2100) for t, p, m in ((1.0, 1.0, 0.0), (1.5, 0.97, 0.0), (0.8, 0.9, 0.01))]
+    rows = [rows[(7 * r) % len(rows)] for r in range(R)]
+    kw, ora = _settings(rows)
+    z = _rows(rng, R, V)
+    z[::3] = np.round(z[::3] * 4) / 4                        # many ties, at the borders too
+    x = torch.from_numpy(z).to(DEV)
+    x = x.to(torch.bfloat16) if bf16 else x
+    u = (rng.integers(0, 1 << 24, R) / (1 << 24)).astype(np.float32)
+    full = torch.empty((R, V), device=DEV)
+    got = S.ssd_sample(x, torch.from_numpy(u).to(DEV), **kw, probs_out=full)
+    tok, prob, p, z = got["token"].cpu().numpy(), got["prob"].cpu().numpy(), full.cpu().double().numpy(), x.float().cpu().numpy()
+    compared = 0
+    for r in range(R):
+        if not _check_row(p[r], z[r], ora[r]):
+            continue
+        want, _, gap = Q.token(z[r], u[r], **ora[r])
+        if gap < NEAR:
+            continue
+        compared += 1
+        assert tok[r] == want and prob[r] == p[r, want]
+    assert compared >= R - max(1, R // 20)
