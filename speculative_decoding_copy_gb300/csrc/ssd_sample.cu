@@ -786,6 +786,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
     const int64_t b = r / (1 + n), t = r % (1 + n) - 1;
     if (t >= 0 && t % p.Dmax >= __ldg(p.blk_len + b * p.NB + t / p.Dmax)) return;
   }
+  // this CTA runs: the others of the cluster may write to its shared memory (they wait for that before they do)
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   const uint8_t* start = static_cast<const uint8_t*>(p.logits) + r * p.row_bytes;
   R row;
   row.off = static_cast<int>((reinterpret_cast<uintptr_t>(start) & 15) / sizeof(T));
@@ -894,6 +896,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
     }
   }
   if (rank >= ctas) reach = ~0u;           // a CTA without tokens does not count
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   if (tid < C) {
     float t = -INFINITY;
 #pragma unroll
