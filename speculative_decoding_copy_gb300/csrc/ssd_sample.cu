@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
     temp = 1.f;
     k = 1;
   }
-  min_p = fminf(min_p, 1.f);
+  min_p = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;             // NaN: all
   if (k < 0 || k >= p.V) k = 0;
   const Rate rate = make_rate(temp);
   // how far below the largest a token may lie whose weight is (1 - top_p) / V of it

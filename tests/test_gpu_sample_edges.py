@@ -30,3 +30,23 @@ def test_clusters_whose_ctas_start_at_different_times(R, V):
     torch.cuda.synchronize()
     for p, t in got:
         assert torch.equal(p, want) and torch.equal(t["token"], ref["token"]) and torch.equal(t["prob"], ref["prob"])
+
+
+@pytest.mark.parametrize("V", [1, 7, 1000, 40000])
+@pytest.mark.parametrize("k", [0, 5, 600, 3000])
+def test_settings_that_are_no_number_cut_nothing(V, k):
+    """NaN top-p and min-p (of either sign): as if they were not given; with top-k by the sorted list, by bins, and without it."""
+    rng = np.random.default_rng(V + k)
+    nan = float("nan")
+    given = [(0.8, k, nan, nan), (0.8, k, 1.0, nan), (0.8, k, nan, 0.0), (0.8, k, 0.9, nan), (0.8, k, nan, 0.01), (0.8, k, 1.0, -nan), (0.0, k, nan, nan)]
+    alike = [(t, k, 1.0 if p != p else p, 0.0 if m != m else m) for t, k, p, m in given]
+    kw, _ = _settings(given)
+    plain, ora = _settings(alike)
+    x = _dev(np.repeat(_rows(rng, 1, V), len(given), 0), False)
+    u = torch.full((len(given),), 0.6875, device="cuda")
+    got, want = S.ssd_filter_probs(x, **kw), S.ssd_filter_probs(x, **plain)
+    assert torch.equal(got, want)
+    a, b = S.ssd_sample(x, u, **kw), S.ssd_sample(x, u, **plain)
+    assert torch.equal(a["token"], b["token"]) and torch.equal(a["prob"], b["prob"])
+    z = x.cpu().numpy()
+    assert sum(_check_row(got[r].cpu().double().numpy(), z[r], ora[r]) for r in range(len(ora))) >= len(ora) - 1
