@@ -669,7 +669,8 @@ __device__ __noinline__ void merge_lists(Shared& sh, int C, int rank) {
   cluster_sync();
 }
 
-// The tokens of `pick`, as comp, of all CTAs in sh.sorted; returns their number, or -1 where they are too many. Every CTA gets the same.
+// The tokens of `pick` (one at least), as comp, of all CTAs in sh.sorted; returns their number, or -1 where they are too many. Every
+// CTA gets the same.
 template <typename R>
 __device__ __forceinline__ int gather(const R& row, const Scale& sc, Shared& sh, int C, const Pick& pick) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -926,9 +927,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
   if (!empty) {
     if (k > 0) {
       const float low = reach > okey(-INFINITY) ? okey_value(reach) : -kFltMax;
-      // from low to zmax, a little wider
-      const float span = 0.5f * (sc.zmax - low);
-      const Pick pick = {low, 0.f, 0.f, low + span, sc.plain ? fmaf(fabsf(sc.zmax) + fabsf(low), 1e-6f, span) + 1.17549435e-38f : INFINITY, 0};
+      // from low to zmax, a little wider; of rows that are not plain every number: there may be infinities
+      const float span = 0.5f * sc.zmax - 0.5f * low;
+      const Pick pick = {low, 0.f, 0.f, sc.plain ? low + span : 0.f,
+                         sc.plain ? fmaf(fabsf(sc.zmax) + fabsf(low), 1e-6f, span) + 1.17549435e-38f : INFINITY, 0};
       int n = -1;
       if (k <= kShortK) {
         n = gather(row, sc, sh, C, pick);

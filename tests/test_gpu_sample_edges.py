@@ -50,3 +50,50 @@ def test_settings_that_are_no_number_cut_nothing(V, k):
     assert torch.equal(a["token"], b["token"]) and torch.equal(a["prob"], b["prob"])
     z = x.cpu().numpy()
     assert sum(_check_row(got[r].cpu().double().numpy(), z[r], ora[r]) for r in range(len(ora))) >= len(ora) - 1
+
+
+def _runs_of_inf(V, n, at, rest, rng):
+    """A row with n infinities side by side from `at` on, and a NaN before and behind them."""
+    z = np.full(V, -np.inf, np.float32)
+    if rest == "some":
+        z[rng.integers(0, V, max(1, V // 50))] = 1.5
+    elif rest == "all":
+        z = rng.standard_normal(V).astype(np.float32)
+    z[at:at + n] = np.inf
+    z[max(at - 1, 0):at] = np.nan
+    z[at + n:at + n + 1] = np.nan
+    return z
+
+
+# top-k below, at and above the number of infinities, of live tokens, of lists and of tokens; greedy; the other cuts beside it
+INF_SETTINGS = [(1.0, 3, 1.0, 0.0), (1.0, 5, 1.0, 0.0), (0.7, 50, 0.9, 0.0), (1.0, 600, 1.0, 0.5), (1.3, 2000, 0.7, 0.0), (0.0, 0, 1.0, 0.0), (0.0, 7, 0.5, 0.1),
+                (1.0, 0, 0.6, 0.0), (1.0, 0, 1.0, 0.3), (1e-3, 5, 1.0, 0.0), (1e20, 9, 1.0, 0.0), (1.0, 0, 1.0, 0.0)]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("rest", ["none", "some", "all"])
+@pytest.mark.parametrize("V,n,at", [(8, 4, 0), (8, 8, 0), (9, 4, 4), (30, 8, 8), (30, 5, 3), (1000, 4, 512), (1000, 8, 41), (5003, 16, 4096), (40000, 8, 39992), (40000, 1200, 20000),
+                                    (600001, 4, 300000)])
+def test_runs_of_infinities(V, n, at, rest, bf16):
+    """+inf counts as the largest finite number wherever it stands: whole vectors of it, with NaN beside, too."""
+    rng = np.random.default_rng(V + n)
+    rows = [s for s in INF_SETTINGS if s[1] <= V]
+    z = np.stack([_runs_of_inf(V, n, at, rest, rng) for _ in rows])
+    kw, ora = _settings(rows)
+    x = _dev(z, bf16)
+    z = x.float().cpu().numpy()
+    u = ((np.arange(len(rows)) * 5 % 16 + 0.37) / 16).astype(np.float32)
+    full = torch.full((len(rows), V), 7.0, device="cuda")
+    out = dict(token=torch.full((len(rows),), -5, dtype=torch.int32, device="cuda"), prob=torch.full((len(rows),), -5.0, device="cuda"))
+    S.ssd_sample(x, torch.from_numpy(u).cuda(), **kw, out=out, probs_out=full)
+    assert torch.equal(full, S.ssd_filter_probs(x, **kw))
+    p, tok, prob = full.cpu().double().numpy(), out["token"].cpu().numpy(), out["prob"].cpu().numpy()
+    compared = 0
+    for r in range(len(rows)):
+        if not _check_row(p[r], z[r], ora[r]):
+            continue
+        want, _, gap = Q.token(z[r], u[r], **ora[r])
+        if gap >= NEAR:
+            compared += 1
+            assert tok[r] == want and prob[r] == p[r, want], (rows[r], tok[r], want)
+    assert compared >= len(rows) - 2
