@@ -824,11 +824,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(Params p) {
     if (tid == 0) record_error(p.hdr, SSD_ERR_DEVICE, 501);
     temp = 0.f;
   }
-  temp = fminf(temp, 0x1p100f);
   if (temp == 0.f) {                       // greedy: the first of the largest
     temp = 1.f;
     k = 1;
   }
+  temp = fminf(fmaxf(temp, 0x1.715476p-120f), 0x1p100f);     // from log2(e) 2^-120, whose rate is 2^120, on
   min_p = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;             // NaN: all
   if (k < 0 || k >= p.V) k = 0;
   const Rate rate = make_rate(temp);

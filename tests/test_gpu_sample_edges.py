@@ -97,3 +97,27 @@ def test_runs_of_infinities(V, n, at, rest, bf16):
             compared += 1
             assert tok[r] == want and prob[r] == p[r, want], (rows[r], tok[r], want)
     assert compared >= len(rows) - 2
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("V", [3, 64, 5000])
+def test_smallest_temperatures(V, bf16):
+    """A temperature between 0 and log2(e) 2^-120 counts as that in every cut, also in what top-p looks at."""
+    least = float(np.log2(np.e)) * 2.0 ** -120
+    rows = [(t, k, p, m) for t in (1e-45, 1e-40, 1e-37, 1.0853631e-36) for k, p, m in ((0, 0.9, 0.0), (0, 0.3, 0.0), (2, 0.9, 0.0), (2000, 0.8, 0.0), (0, 1.0, 0.2), (0, 0.999, 0.0))]
+    rng = np.random.default_rng(V)
+    z = -(np.arange(V) * 1e-37 * 64 / V) + rng.integers(0, 3, V) * 1e-38
+    x = _dev(np.repeat(rng.permutation(z)[None].astype(np.float32), len(rows), 0), bf16)
+    kw, ora = _settings(rows)
+    u = torch.full((len(rows),), 0.40625, device="cuda")
+    got, tok = S.ssd_filter_probs(x, **kw), S.ssd_sample(x, u, **kw)["token"].cpu().numpy()
+    z = x.float().cpu().numpy()
+    compared = 0
+    for r, o in enumerate(ora):
+        o["temperature"] = least
+        if not _check_row(got[r].cpu().double().numpy(), z[r], o):
+            continue
+        compared += 1
+        want, _, gap = Q.token(z[r], 0.40625, **o)
+        assert gap < NEAR or tok[r] == want
+    assert compared >= len(rows) - 2
