@@ -673,7 +673,11 @@ int ssd_lowrank_head(const ssd_head_args* a, void* ws, size_t ws_bytes, void* st
  * outside its cache or a page outside the pool records SSD_ERR_DEVICE (the length counts as 0,
  * the page as page 0); block lengths count as the nearest of 0 .. Dmax.
  * Workspace: ssd_verify_attn_shared_workspace_size(a) bytes for the current device, 256-byte
- * aligned; its contents need no initialisation but for the header (as for ssd_verify_attn). Calls
+ * aligned; its contents need no initialisation but for the header (as for ssd_verify_attn). With
+ * G = Hq / Hkv, per = 128 / G (whole), rows(n) = n G for n <= per tokens, else 256, parts(n) = Hkv
+ * ceil(n / (2 per)) and C the SMs (SSD_F32: four times them) it is about 4 (dh + 2) bytes times
+ *   (parts(B NB Dmax) + C) rows(B NB Dmax) + (B parts(NB Dmax) + C) rows(NB Dmax),
+ * the second term for the sequences' own keys (C = 152 SMs alone, 256 rows, dh 128: 20 MB). Calls
  * one after another on a stream may share it; calls that overlap on the GPU may not.
  */
 typedef struct {

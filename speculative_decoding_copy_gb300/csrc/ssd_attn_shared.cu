@@ -54,6 +54,15 @@ constexpr int kSegs = 20;                  // segments a CTA has described at on
 constexpr int kMaxBatch = 4096;            // sequences: their offsets fit the ring before it is used
 constexpr unsigned long long kWaitClocks = 1ull << 32;
 
+// Where the segments of the shared or of the own keys go: of each (reference maximum, sum) of its rows and O, for
+// `tiles` row tiles of `rows` rows, of which there are no more than the most tokens a segment can have need
+struct Slots {
+  float* ml;                               // [segments][tiles][rows][2]
+  float* o;                                // [segments][tiles][dh / 4][rows][4]
+  int tiles, rows;
+  __host__ __device__ int64_t first(int64_t id, int tile) const { return (id * tiles + tile) * rows; }     // row of all segments'
+};
+
 struct Params {
   const void *q, *k_shared, *v_shared, *k_cache, *v_cache, *k_cand, *v_cand;
   void* out;
@@ -68,13 +77,12 @@ struct Params {
   int32_t* plan;                           // kPlan numbers
   int32_t* tok;                            // the present tokens b * NT + t
   int32_t *tok_first, *unit0, *ph0, *own_len;      // [B + 1] (own_len [B])
-  float* ml;                               // [segments][256][2]
-  float* o;                                // [segments][2 row tiles][dh / 4][128][4]
+  Slots shared, own;
 };
 // Work is measured in units of 1700 clocks, what a key tile takes with one row tile beside another segment's;
 // with two row tiles (3400) it counts as two, and Q in and O out of a pair and head as two more tiles.
 constexpr int kSetup = 2;
-enum { kTokens = 0, kShare = 1, kUnits = 2, kSharedLen = 3, kSharedUnits = 4, kSharedPairs = 5, kPlan = 16 };
+enum { kTokens = 0, kShare = 1, kUnits = 2, kSharedLen = 3, kSharedUnits = 4, kPlan = 16 };
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // units of a key tile for rows of `tokens` tokens, of which a row tile holds `per`
@@ -118,7 +126,7 @@ __device__ __forceinline__ void plan_scan(int (&v)[3], int (*part)[32], int (&to
 
 // Segment (of pair-and-head ph, cut by CTA c's run) has the number ph + c: from one segment to the next
 // one of the two grows or both do. Pairs of the shared prompt come first, then those of each sequence
-// (unit0 and ph0 count from the first of these).
+// (unit0 and ph0 count from the first of these, and so do their segments).
 __global__ void __launch_bounds__(kPlanThreads) k_plan(Params p) {
   __shared__ int part[3][32];
   __shared__ int first[kPlanThreads];
@@ -186,7 +194,6 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(Params p) {
     p.plan[kUnits] = units_s + units;
     p.plan[kSharedLen] = S;
     p.plan[kSharedUnits] = units_s;
-    p.plan[kSharedPairs] = ph_s;
   }
 }
 
@@ -211,7 +218,7 @@ __device__ __forceinline__ int find_seq(const int* unit0, int B, int u) {
 // Segments of units [u, u1) for CTA c, as many as fit; returns the unit behind them. `b` is the sequence
 // that u lies in, where it is not in the shared part (-1: not looked for yet).
 __device__ int describe(const Params& p, Seg* segs, int* count, int c, int u, int u1, const int* unit0, const int* ph0, const int* tok_first,
-                        const int* own_len, int tokens, int shared_len, int own0, int own_ph) {
+                        const int* own_len, int tokens, int shared_len, int own0) {
   const int pair = 2 * p.tokens;
   int n = 0, b = -1;
   while (u < u1 && n < kSegs) {
@@ -232,7 +239,7 @@ __device__ int describe(const Params& p, Seg* segs, int* count, int c, int u, in
       base = own0 + unit0[b];
       first = tok_first[b];
       all = tok_first[b + 1] - first;
-      ph = own_ph + ph0[b];
+      ph = ph0[b];
     }
     const int w = tile_units(all, p.tokens), kt = (ceil_div(s.len, kTile) + kSetup) * w, at = (u - base) / kt;
     s.kvh = at % p.Hkv;
@@ -414,7 +421,7 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
     if (tid == 0)
       bars.next = describe(p, bars.segs, &bars.count, cta, u, u1, gave_up ? p.unit0 : off, gave_up ? p.ph0 : off + (p.B + 1),
                            gave_up ? p.tok_first : off + 2 * (p.B + 1), gave_up ? p.own_len : off + 3 * (p.B + 1), tokens, shared_len,
-                           __ldcg(p.plan + kSharedUnits), __ldcg(p.plan + kSharedPairs));
+                           __ldcg(p.plan + kSharedUnits));
     fence_async_smem();                                     // TMA writes over what was just read
     __syncthreads();
     u = bars.next;
@@ -422,8 +429,11 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
 
     if (gave_up) {
       // segments that nothing computes: their rows come out NaN, not as what the workspace held
-      for (int e = tid; e < 256 * nseg; e += kThreads)
-        *reinterpret_cast<float2*>(p.ml + (static_cast<int64_t>(bars.segs[e >> 8].id) * 256 + (e & 255)) * 2) = make_float2(NAN, NAN);
+      for (int i = 0; i < nseg; ++i) {
+        const Slots& w = bars.segs[i].b < 0 ? p.shared : p.own;
+        for (int e = tid; e < w.tiles * w.rows; e += kThreads)
+          *reinterpret_cast<float2*>(w.ml + (w.first(bars.segs[i].id, 0) + e) * 2) = make_float2(NAN, NAN);
+      }
     } else if (warp < 16) {
       // -------------------------------------------------------- softmax rows: two threads a row
       const int t = warp >> 3, half = (warp >> 2) & 1;      // row tile; keys 0-63 or 64-127 of a key tile
@@ -559,10 +569,12 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
         wait(bars, &bars.pv_done[t], (tiles - 1) & 1, p.hdr, 612);
         tc_fence_after();
         const int nrow = rows_of(s, now.tile);
-        const int64_t row = static_cast<int64_t>(s.id) * 256 + now.tile * 128 + r;
+        const Slots& w = s.b < 0 ? p.shared : p.own;
+        const int64_t first = w.first(s.id, now.tile);
+        const int rows = w.rows;
         const bool keep = r < nrow && !bars.failed;
-        // O of a tile as [dh / 4][128 rows][4]: a warp's 32 rows lie side by side
-        float4* dst = reinterpret_cast<float4*>(p.o) + (static_cast<int64_t>(s.id) * 2 + now.tile) * (DH / 4) * 128 + half * (DH / 8) * 128 + r;
+        // O of a tile as [dh / 4][rows][4]: a warp's rows lie side by side
+        float4* dst = reinterpret_cast<float4*>(w.o + first * DH) + half * (DH / 8) * rows + r;
 #pragma unroll 1
         for (int c = 0; c < DH / 64; ++c) {
           uint32_t o[32];
@@ -571,11 +583,11 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
           if (keep) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              dst[(8 * c + e) * 128] =
+              dst[(8 * c + e) * rows] =
                   make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
           }
         }
-        if (half == 0 && r < nrow) *reinterpret_cast<float2*>(p.ml + row * 2) = bars.failed ? make_float2(NAN, NAN) : make_float2(m, l + l_other);
+        if (half == 0 && r < nrow) *reinterpret_cast<float2*>(w.ml + (first + r) * 2) = bars.failed ? make_float2(NAN, NAN) : make_float2(m, l + l_other);
         tc_fence_before();
         mbar_arrive(&bars.o_free[t]);
         tile_sync();                                        // and the sums
@@ -743,7 +755,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_parts_simt(Params p) {
     __syncthreads();
     if (tid == 0)
       next = describe(p, segs, &count, blockIdx.x, u, u1, p.unit0, p.ph0, p.tok_first, p.own_len, p.plan[kTokens], p.plan[kSharedLen],
-                      p.plan[kSharedUnits], p.plan[kSharedPairs]);
+                      p.plan[kSharedUnits]);
     __syncthreads();
     u = next;
     for (int i = 0; i < count; ++i) {
@@ -813,12 +825,14 @@ __global__ void __launch_bounds__(kSimtThreads) k_parts_simt(Params p) {
           const int x = x0 + warp * kSimtRows + r;
           if (x >= rows) continue;
           const int tk = x / p.G, tile = tk / p.tokens;
-          const int64_t row = static_cast<int64_t>(s.id) * 256 + tile * 128 + (tk - tile * p.tokens) * p.G + x % p.G;
-          if (lane == 0) *reinterpret_cast<float2*>(p.ml + row * 2) = make_float2(m[r], l[r]);
+          const Slots& at = s.b < 0 ? p.shared : p.own;
+          const int64_t first = at.first(s.id, tile);
+          const int row = (tk - tile * p.tokens) * p.G + x % p.G;
+          if (lane == 0) *reinterpret_cast<float2*>(at.ml + (first + row) * 2) = make_float2(m[r], l[r]);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const int c = lane + 32 * e;
-            p.o[(((static_cast<int64_t>(s.id) * 2 + tile) * (DH / 4) + c / 4) * 128 + (row & 127)) * 4 + c % 4] = o[r][e];
+            at.o[first * DH + (c / 4 * at.rows + row) * 4 + c % 4] = o[r][e];
           }
         }
       }
@@ -864,7 +878,7 @@ __global__ void __launch_bounds__(128) k_join(Params p) {
   const int share = __ldcg(p.plan + kShare), shared_len = __ldcg(p.plan + kSharedLen), pair = 2 * p.tokens;
   const int token = __ldcg(p.tok + i), NT = p.NB * p.Dmax;
   const int b = token / NT, pos = (token - b * NT) % p.Dmax;
-  const int own_first = __ldcg(p.tok_first + b), own_tokens = __ldcg(p.tok_first + b + 1) - own_first, own_u = __ldcg(p.plan + kSharedUnits) + __ldcg(p.unit0 + b), own_ph = __ldcg(p.plan + kSharedPairs) + __ldcg(p.ph0 + b), own_len = __ldcg(p.own_len + b);
+  const int own_first = __ldcg(p.tok_first + b), own_tokens = __ldcg(p.tok_first + b + 1) - own_first, own_u = __ldcg(p.plan + kSharedUnits) + __ldcg(p.unit0 + b), own_ph = __ldcg(p.ph0 + b), own_len = __ldcg(p.own_len + b);
   const int kvh = unit / groups, g0 = (unit - kvh * groups) * H, gn = min(H, p.G - g0);
   float q[H][N], o[H][N];
 #pragma unroll
@@ -942,7 +956,7 @@ __global__ void __launch_bounds__(128) k_join(Params p) {
   }
 
   // the segments of a pair's units u_base + at kt .. + kt - 1
-  auto join = [&](int i0, int all, int u_base, int ph_base, int len) {
+  auto join = [&](const Slots& part, int i0, int all, int u_base, int ph_base, int len) {
     if (len <= 0) return;
     const int kt = ceil_div(len, kTile), pr = i0 / pair, in = i0 - pr * pair, at = pr * p.Hkv + kvh;
     const int tile = in / p.tokens, row = (in - tile * p.tokens) * p.G + g0;
@@ -950,14 +964,14 @@ __global__ void __launch_bounds__(128) k_join(Params p) {
     const int64_t id0 = static_cast<int64_t>(ph_base) + at + c0;
     for (int s0 = 0; s0 < n; s0 += L) {
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (s0 + n_of < n && g_of < gn) ml = __ldcg(reinterpret_cast<const float2*>(p.ml) + (id0 + s0 + n_of) * 256 + tile * 128 + row + g_of);
+      if (s0 + n_of < n && g_of < gn) ml = __ldcg(reinterpret_cast<const float2*>(part.ml) + part.first(id0 + s0 + n_of, tile) + row + g_of);
       const float w = take(ml.x, ml.y);
       for (int c = 0; c < min(L, n - s0); c += 2) {
         float x[2][H][N];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           // (an odd last one twice, the second time without weight)
-          const float* src = p.o + ((((id0 + s0 + min(c + y, n - s0 - 1)) * 2 + tile) * (DH / 4) + lane * N / 4) * 128 + row) * 4 + lane * N % 4;
+          const float* src = part.o + part.first(id0 + s0 + min(c + y, n - s0 - 1), tile) * DH + (lane * N / 4 * part.rows + row) * 4 + lane * N % 4;
 #pragma unroll
           for (int g = 0; g < H; ++g)
 #pragma unroll
@@ -980,8 +994,8 @@ __global__ void __launch_bounds__(128) k_join(Params p) {
       }
     }
   };
-  join(i, all_tokens, 0, 0, shared_len);
-  join(i - own_first, own_tokens, own_u, own_ph, own_len);
+  join(p.shared, i, all_tokens, 0, 0, shared_len);
+  join(p.own, i - own_first, own_tokens, own_u, own_ph, own_len);
 
   const float inv = 1.f / l;
 #pragma unroll
@@ -1032,8 +1046,13 @@ static int validate(const ssd_attn_shared_args* a) {
 }
 
 struct Layout {
-  size_t plan, tok, tok_first, unit0, ph0, own_len, ml, o, total;
-  int64_t units, segments;
+  struct Part {
+    size_t ml, o;
+    int tiles, rows;
+  };
+  size_t plan, tok, tok_first, unit0, ph0, own_len, total;
+  Part shared, own;
+  int64_t units;
 };
 
 static int sm_count(int dev) {
@@ -1055,7 +1074,6 @@ static Layout layout(const ssd_attn_shared_args* a, int ctas) {
   const int64_t p_cap = a->block_table != nullptr ? 128LL * a->pages_per_seq : a->P_max;
   const int64_t ph_s = (all + pair - 1) / pair * a->Hkv, ph_o = (NT + pair - 1) / pair * a->Hkv * a->B;
   L.units = 2 * (ph_s * ((s_cap + kTile - 1) / kTile + kSetup) + ph_o * ((p_cap + kTile - 1) / kTile + kSetup));
-  L.segments = (s_cap > 0 ? ph_s : 0) + (p_cap > 0 ? ph_o : 0) + ctas;
   size_t at = sizeof(WsHeader);
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -1068,8 +1086,17 @@ static Layout layout(const ssd_attn_shared_args* a, int ctas) {
   L.unit0 = take(4 * (static_cast<size_t>(a->B) + 1));
   L.ph0 = take(4 * (static_cast<size_t>(a->B) + 1));
   L.own_len = take(4 * static_cast<size_t>(a->B));
-  L.ml = take(static_cast<size_t>(L.segments) * 256 * 8);
-  L.o = take(static_cast<size_t>(L.segments) * 256 * a->dh * 4);
+  // every pair and head may be a segment, and every CTA but one may cut one more; its rows are those of `tokens` or, if
+  // they are more than a row tile, of two row tiles
+  auto part = [&](int64_t cap, int64_t ph, int64_t tokens) {
+    Layout::Part x = {0, 0, tokens > pair / 2 ? 2 : 1, tokens > pair / 2 ? kTile : static_cast<int>(tokens) * (a->Hq / a->Hkv)};
+    const size_t rows = cap > 0 ? static_cast<size_t>(ph + ctas) * x.tiles * x.rows : 0;
+    x.ml = take(rows * 8);
+    x.o = take(rows * a->dh * 4);
+    return x;
+  };
+  L.shared = part(s_cap, ph_s, all);
+  L.own = part(p_cap, ph_o, NT);
   L.total = at;
   return L;
 }
@@ -1185,8 +1212,8 @@ extern "C" int ssd_verify_attn_shared(const ssd_attn_shared_args* a, void* ws, s
   p.unit0 = reinterpret_cast<int32_t*>(w + L.unit0);
   p.ph0 = reinterpret_cast<int32_t*>(w + L.ph0);
   p.own_len = reinterpret_cast<int32_t*>(w + L.own_len);
-  p.ml = reinterpret_cast<float*>(w + L.ml);
-  p.o = reinterpret_cast<float*>(w + L.o);
+  p.shared = {reinterpret_cast<float*>(w + L.shared.ml), reinterpret_cast<float*>(w + L.shared.o), L.shared.tiles, L.shared.rows};
+  p.own = {reinterpret_cast<float*>(w + L.own.ml), reinterpret_cast<float*>(w + L.own.o), L.own.tiles, L.own.rows};
   if (launch_pdl(shr::k_plan, dim3(1), dim3(shr::kPlanThreads), 0, s, p) != cudaSuccess) return SSD_ERR_CUDA;
   if (a->dtype == SSD_BF16) {
     const int e = a->dh == 64 ? shr::launch_parts<64>(p, a, s) : shr::launch_parts<128>(p, a, s);
