@@ -668,7 +668,10 @@ int ssd_lowrank_head(const ssd_head_args* a, void* ws, size_t ws_bytes, void* st
  * depend on the order of execution: a call repeats bit for bit.
  * Supported: dh 64 or 128; Hq % Hkv == 0, Hq / Hkv <= 64; Dmax <= 256, NB * Dmax <= 8192;
  * B <= 4096; Hkv <= 1024; 16-byte aligned tensors; fewer than 2^31 rows of keys and rows of out,
- * fewer than 2^30 units of work (128 keys x 256 rows of a kv head); else SSD_ERR_UNSUPPORTED.
+ * fewer than 2^30 units of work (128 keys x up to 128 rows of a kv head, and two more for each such
+ * rows' queries and output; with parts() as below and S, P the keys that k_shared, k_cache or the tables hold)
+ *   2 parts(B NB Dmax) (ceil(S / 128) + 2) + 2 B parts(NB Dmax) (ceil(P / 128) + 2);
+ * else SSD_ERR_UNSUPPORTED, and a workspace size of 0.
  * scale == 0 selects 1/sqrt(dh). out must not overlap an input (SSD_ERR_INVALID). A length
  * outside its cache or a page outside the pool records SSD_ERR_DEVICE (the length counts as 0,
  * the page as page 0); block lengths count as the nearest of 0 .. Dmax.

@@ -7,7 +7,7 @@
 // all sequences as the rows of one product, a sequence's own prefix with its tokens, the own block
 // (at most 256 keys) row by row. Three kernels:
 //   k_plan    one CTA: list of the present tokens, offsets of the sequences, and the work in units of
-//             128 keys x 256 packed rows ("pairs" of two row tiles) x one kv head;
+//             128 keys x 128 packed rows (a row tile; two of the same keys are a "pair") x one kv head;
 //   k_parts   one CTA an SM: an equal run of units each, so that a long prompt, many short prefixes or
 //             both fill the GPU whatever their sizes. Where a run crosses from one pair (and head) to
 //             the next, a segment ends and its (m, l, O) go to the workspace;
@@ -1016,6 +1016,20 @@ __global__ void __launch_bounds__(128) k_join(Params p) {
 }
 
 // ------------------------------------------------------------------ host
+// the most keys of the shared prompt and of a sequence, tokens of a pair, and pairs (x kv heads) of both
+struct Extent {
+  int64_t s_cap, p_cap, pair, ph_s, ph_o;
+  explicit Extent(const ssd_attn_shared_args* a) {
+    const int64_t NT = static_cast<int64_t>(a->NB) * a->Dmax;
+    s_cap = a->shared_table != nullptr ? 128LL * a->shared_pages : a->S_max;
+    p_cap = a->block_table != nullptr ? 128LL * a->pages_per_seq : a->P_max;
+    pair = 2 * (kTile / (a->Hq / a->Hkv));
+    ph_s = (a->B * NT + pair - 1) / pair * a->Hkv;
+    ph_o = (NT + pair - 1) / pair * a->Hkv * a->B;
+  }
+  int64_t units() const { return 2 * (ph_s * ((s_cap + kTile - 1) / kTile + kSetup) + ph_o * ((p_cap + kTile - 1) / kTile + kSetup)); }
+};
+
 static int validate(const ssd_attn_shared_args* a) {
   if (a == nullptr) return SSD_ERR_INVALID;
   if (a->B < 0 || a->NB < 1 || a->Dmax < 1 || a->Hq < 1 || a->Hkv < 1 || a->P_max < 0 || a->S_max < 0) return SSD_ERR_INVALID;
@@ -1042,6 +1056,8 @@ static int validate(const ssd_attn_shared_args* a) {
   if (a->shared_table == nullptr && a->S_max > 0 && (!a->k_shared || !a->v_shared)) return SSD_ERR_INVALID;
   for (const void* x : {a->q, a->k_shared, a->v_shared, a->k_cache, a->v_cache, a->k_cand, a->v_cand, static_cast<const void*>(a->out)})
     if (!aligned(x, 16)) return SSD_ERR_UNSUPPORTED;
+  // units of work are counted in 32 bits
+  if (Extent(a).units() >= (1LL << 30) || static_cast<int64_t>(a->B) * a->NB * a->Dmax * a->Hq >= (1LL << 31)) return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
 }
 
@@ -1052,7 +1068,6 @@ struct Layout {
   };
   size_t plan, tok, tok_first, unit0, ph0, own_len, total;
   Part shared, own;
-  int64_t units;
 };
 
 static int sm_count(int dev) {
@@ -1069,11 +1084,7 @@ static int grid_of(const ssd_attn_shared_args* a, int sms) { return a->dtype == 
 static Layout layout(const ssd_attn_shared_args* a, int ctas) {
   Layout L{};
   const int64_t NT = static_cast<int64_t>(a->NB) * a->Dmax, all = a->B * NT;
-  const int pair = 2 * (kTile / (a->Hq / a->Hkv));
-  const int64_t s_cap = a->shared_table != nullptr ? 128LL * a->shared_pages : a->S_max;
-  const int64_t p_cap = a->block_table != nullptr ? 128LL * a->pages_per_seq : a->P_max;
-  const int64_t ph_s = (all + pair - 1) / pair * a->Hkv, ph_o = (NT + pair - 1) / pair * a->Hkv * a->B;
-  L.units = 2 * (ph_s * ((s_cap + kTile - 1) / kTile + kSetup) + ph_o * ((p_cap + kTile - 1) / kTile + kSetup));
+  const Extent x(a);
   size_t at = sizeof(WsHeader);
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -1089,14 +1100,15 @@ static Layout layout(const ssd_attn_shared_args* a, int ctas) {
   // every pair and head may be a segment, and every CTA but one may cut one more; its rows are those of `tokens` or, if
   // they are more than a row tile, of two row tiles
   auto part = [&](int64_t cap, int64_t ph, int64_t tokens) {
-    Layout::Part x = {0, 0, tokens > pair / 2 ? 2 : 1, tokens > pair / 2 ? kTile : static_cast<int>(tokens) * (a->Hq / a->Hkv)};
-    const size_t rows = cap > 0 ? static_cast<size_t>(ph + ctas) * x.tiles * x.rows : 0;
-    x.ml = take(rows * 8);
-    x.o = take(rows * a->dh * 4);
-    return x;
+    const bool two = tokens > x.pair / 2;
+    Layout::Part y = {0, 0, two ? 2 : 1, two ? kTile : static_cast<int>(tokens) * (a->Hq / a->Hkv)};
+    const size_t rows = cap > 0 ? static_cast<size_t>(ph + ctas) * y.tiles * y.rows : 0;
+    y.ml = take(rows * 8);
+    y.o = take(rows * a->dh * 4);
+    return y;
   };
-  L.shared = part(s_cap, ph_s, all);
-  L.own = part(p_cap, ph_o, NT);
+  L.shared = part(x.s_cap, x.ph_s, all);
+  L.own = part(x.p_cap, x.ph_o, NT);
   L.total = at;
   return L;
 }
@@ -1172,7 +1184,6 @@ extern "C" int ssd_verify_attn_shared(const ssd_attn_shared_args* a, void* ws, s
   const int ctas = shr::grid_of(a, shr::sm_count(dev));
   if (ctas < 1) return SSD_ERR_CUDA;
   const shr::Layout L = shr::layout(a, ctas);
-  if (L.units >= (1LL << 30) || rows / a->dh >= (1LL << 31)) return SSD_ERR_UNSUPPORTED;
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < L.total) return SSD_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* w = static_cast<char*>(ws);
