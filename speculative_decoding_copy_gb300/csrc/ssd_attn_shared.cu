@@ -1032,7 +1032,9 @@ struct Extent {
 
 static int validate(const ssd_attn_shared_args* a) {
   if (a == nullptr) return SSD_ERR_INVALID;
-  if (a->B < 0 || a->NB < 1 || a->Dmax < 1 || a->Hq < 1 || a->Hkv < 1 || a->P_max < 0 || a->S_max < 0) return SSD_ERR_INVALID;
+  if (a->B < 0 || a->NB < 1 || a->Dmax < 1 || a->Hq < 1 || a->Hkv < 1 || a->P_max < 0) return SSD_ERR_INVALID;
+  const bool apart = a->shared_table == nullptr;            // else k_shared, v_shared and S_max are not used
+  if (apart && a->S_max < 0) return SSD_ERR_INVALID;
   if (a->dtype != SSD_F32 && a->dtype != SSD_BF16) return SSD_ERR_INVALID;
   if (a->out_dtype != a->dtype && a->out_dtype != SSD_F32) return SSD_ERR_INVALID;
   if (a->Hq % a->Hkv != 0 || !(a->scale >= 0.f)) return SSD_ERR_INVALID;
@@ -1047,15 +1049,16 @@ static int validate(const ssd_attn_shared_args* a) {
   if (a->shared_table != nullptr && a->shared_pages < 1) return SSD_ERR_INVALID;
   // a shared prompt in pages lies in the pool of the sequences' pages
   if (a->shared_table != nullptr && a->block_table == nullptr) return SSD_ERR_INVALID;
-  if (a->pages_per_seq > (1 << 20) || a->shared_pages > (1 << 20) || a->P_max > (1LL << 27) || a->S_max > (1LL << 27)) return SSD_ERR_UNSUPPORTED;
+  if (a->pages_per_seq > (1 << 20) || a->shared_pages > (1 << 20) || a->P_max > (1LL << 27) || (apart && a->S_max > (1LL << 27))) return SSD_ERR_UNSUPPORTED;
   if (a->block_table == nullptr && static_cast<double>(a->B) * a->Hkv * a->P_max >= 0x1p31) return SSD_ERR_UNSUPPORTED;
-  if (a->shared_table == nullptr && static_cast<double>(a->Hkv) * a->S_max >= 0x1p31) return SSD_ERR_UNSUPPORTED;
+  if (apart && static_cast<double>(a->Hkv) * a->S_max >= 0x1p31) return SSD_ERR_UNSUPPORTED;
   if (a->B == 0) return SSD_OK;
   if (!a->q || !a->k_cand || !a->v_cand || !a->out || !a->shared_len || !a->prefix_len || !a->blk_len) return SSD_ERR_INVALID;
   if ((a->block_table != nullptr || a->P_max > 0) && (!a->k_cache || !a->v_cache)) return SSD_ERR_INVALID;
-  if (a->shared_table == nullptr && a->S_max > 0 && (!a->k_shared || !a->v_shared)) return SSD_ERR_INVALID;
-  for (const void* x : {a->q, a->k_shared, a->v_shared, a->k_cache, a->v_cache, a->k_cand, a->v_cand, static_cast<const void*>(a->out)})
+  if (apart && a->S_max > 0 && (!a->k_shared || !a->v_shared)) return SSD_ERR_INVALID;
+  for (const void* x : {a->q, a->k_cache, a->v_cache, a->k_cand, a->v_cand, static_cast<const void*>(a->out)})
     if (!aligned(x, 16)) return SSD_ERR_UNSUPPORTED;
+  if (apart && (!aligned(a->k_shared, 16) || !aligned(a->v_shared, 16))) return SSD_ERR_UNSUPPORTED;
   // units of work are counted in 32 bits
   if (Extent(a).units() >= (1LL << 30) || static_cast<int64_t>(a->B) * a->NB * a->Dmax * a->Hq >= (1LL << 31)) return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
@@ -1175,7 +1178,8 @@ extern "C" int ssd_verify_attn_shared(const ssd_attn_shared_args* a, void* ws, s
   const int64_t es = a->dtype == SSD_BF16 ? 2 : 4, NT = static_cast<int64_t>(a->NB) * a->Dmax;
   const int64_t rows = a->B * NT * a->Hq * a->dh, cand = a->B * NT * a->Hkv * a->dh * es, row = static_cast<int64_t>(a->Hkv) * a->dh * es;
   const int64_t own = a->block_table != nullptr ? a->num_pages * 128 * row : a->B * a->P_max * row;
-  const Span spans[] = {{a->out, rows * (a->out_dtype == SSD_F32 ? 4 : 2)}, {a->q, rows * es}, {a->k_shared, a->S_max * row}, {a->v_shared, a->S_max * row},
+  const int64_t prompt = a->shared_table != nullptr ? 0 : a->S_max * row;
+  const Span spans[] = {{a->out, rows * (a->out_dtype == SSD_F32 ? 4 : 2)}, {a->q, rows * es}, {a->k_shared, prompt}, {a->v_shared, prompt},
                         {a->k_cache, own}, {a->v_cache, own}, {a->k_cand, cand}, {a->v_cand, cand}, {a->shared_len, 4}, {a->prefix_len, 4LL * a->B},
                         {a->blk_len, 4LL * a->B * a->NB}, {a->shared_table, 4LL * a->shared_pages}, {a->block_table, 4LL * a->B * a->pages_per_seq}};
   if (overlap(spans, 1, 13)) return SSD_ERR_INVALID;

@@ -43,3 +43,13 @@ def test_most_rows_of_out(L):  # noqa: F811
     kw = dict(NB=32, Dmax=256, Hq=1024, Hkv=16, S_max=0, P_max=0)
     for B, ok in ((255, True), (256, False)):
         assert (L.ssd_verify_attn_shared_workspace_size(ctypes.byref(_attn(B=B, **kw))) > 0) == ok
+
+
+@pytest.mark.parametrize("kw", [dict(k_shared=(1 << 40) + 2), dict(v_shared=1 << 48), dict(S_max=1 << 40), dict(S_max=-1), dict(k_shared=None, v_shared=None, S_max=300)],
+                         ids=str)
+def test_prompt_in_pages_leaves_its_own_buffers_unused(L, kw):  # noqa: F811
+    """With a shared_table the shared keys come from the pool: k_shared, v_shared and S_max may hold anything."""
+    a = _attn(block_table=1 << 41, pages_per_seq=2, shared_table=1 << 42, shared_pages=3, num_pages=9)
+    _set(a, out=1 << 48, **kw)
+    assert L.ssd_verify_attn_shared_workspace_size(ctypes.byref(a)) > 0
+    assert L.ssd_verify_attn_shared(ctypes.byref(a), None, 0, None) in (S.SSD_ERR_WORKSPACE, S.SSD_ERR_CUDA)
