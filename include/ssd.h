@@ -718,15 +718,17 @@ int ssd_verify_attn_shared(const ssd_attn_shared_args* a, void* ws, size_t ws_by
  *   a token at place j (from 0) of that order stays iff
  *     j < top_k                                          (top_k <= 0 or >= V: all)
  *     sum of w before it < top_p * sum of w of the first top_k   (top_p >= 1 or NaN: all)
- *     w >= min_p                                         (min_p <= 0 or NaN: all)
+ *     w >= min_p                                         (min_p <= 0 or NaN: all; above 1: as 1)
  *   or j = 0; p_i = w_i / sum of w of those that stay, 0 for the others.
  * T == 0 is greedy: the first of the largest stays alone. A T that is negative or NaN
  * records SSD_ERR_DEVICE and counts as 0; one above 2^100 counts as 2^100, one between 0 and
  * log2(e) 2^-120 as that. A NaN logit counts as -inf and never stays, +inf as the largest finite
  * number; a row without a logit above -inf becomes all zeros.
- * Weights have a relative error under 2^-29 and sums are exact sums of round(w 2^43), so results
- * do not depend on the order of execution, and a token is cut otherwise than in exact
- * arithmetic only where the sum before it is within about 2^-29 of the border (relative).
+ * Weights have a relative error under 2^-29 (those below 2^-125 are 0) and sums are exact sums of
+ * round(w 2^43), each within 2^-44 of its w: results do not depend on the order of execution. A
+ * token is cut otherwise than in exact arithmetic only where the sum before it is within
+ * 2^-28 top_p sum + V 2^-43 of top_p sum (the largest w is 1), or its w within 2^-29 of min_p (relative),
+ * and p_i is within 2^-23.9 + V 2^-44 (relative, numbers below 2^-126 2^-126) of w_i / sum.
  * Rows and settings (ssd_rows_args): logits R rows of V elements of dtype (SSD_F32 or SSD_BF16),
  * row_stride elements apart (any alignment of the element); row r takes its setting from entry
  * r / rows_per of temperature, top_k, top_p, min_p (each may be NULL: 1, all, all, all).

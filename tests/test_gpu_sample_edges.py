@@ -121,3 +121,39 @@ def test_smallest_temperatures(V, bf16):
         want, _, gap = Q.token(z[r], 0.40625, **o)
         assert gap < NEAR or tok[r] == want
     assert compared >= len(rows) - 2
+
+
+@pytest.mark.parametrize("V", [1 << 20, 128256, 5003])
+@pytest.mark.parametrize("units", [0.3, 0.55, 1.1, 1.45, 2.6, 700.0])
+def test_cuts_in_a_long_tail_of_small_weights(V, units):
+    """One token and V - 1 equal ones whose weight is `units` of 2^-43, to which sums round it: what stays ends
+    within the documented distance of the border, 2^-28 top_p sum + V 2^-43, and no further."""
+    ps = [1 - 2.0 ** -24, 1 - 2.0 ** -22, 1 - 2.0 ** -18, 0.999, 0.5]
+    z = np.full((len(ps), V), np.log(units * 2.0 ** -43), np.float32)
+    z[:, V // 3] = 0.0
+    kw, _ = _settings([(1.0, 0, p, 0.0) for p in ps])
+    got = S.ssd_filter_probs(torch.from_numpy(z).cuda(), **kw).cpu().double().numpy()
+    w = float(np.exp(np.float64(z[0, 0])))
+    total = 1 + (V - 1) * w
+    for r, p in enumerate(ps):
+        n = int((got[r] > 0).sum())
+        target, off = p * total, 2.0 ** -28 * p * total + V * 2.0 ** -43
+        before = lambda j: 0.0 if j == 0 else 1 + (j - 1) * w  # noqa: B023  (of the token at place j)
+        assert n >= 1 and got[r, V // 3] > 0
+        assert n == 1 or before(n - 1) < target + off
+        assert n == V or before(n) >= target - off
+        # equal tokens by their index, and the probabilities those of what stays
+        first = np.flatnonzero(got[r] > 0)
+        assert (np.delete(np.arange(V), V // 3)[:n - 1] == first[first != V // 3]).all()
+        sum_ = 1 + (n - 1) * w
+        np.testing.assert_allclose(got[r, first], np.where(first == V // 3, 1.0, w) / sum_, rtol=RTOL + V * 2.0 ** -44)
+
+
+@pytest.mark.parametrize("k", [0, 3, 5000])
+def test_min_p_above_one_counts_as_one(k):
+    z = torch.randn((3, 6000), device="cuda").clamp_(max=2.0)
+    z[:, [7, 100, 4444, 5999]] = 2.5
+    m = torch.tensor([1.0, 2.0, float("inf")], device="cuda")
+    got = S.ssd_filter_probs(z, top_k=torch.full((3,), k, dtype=torch.int32, device="cuda"), min_p=m)
+    for r in range(3):
+        assert (got[r] > 0).nonzero()[:, 0].tolist() == [7, 100, 4444, 5999][:k or None]
