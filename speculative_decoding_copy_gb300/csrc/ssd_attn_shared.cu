@@ -24,14 +24,16 @@
 // Every wait is bounded; after one that gave up the CTA records SSD_ERR_TIMEOUT, waits (bounded) for its
 // copies and products in flight and ends; rows it shares come out NaN.
 //
-// What bounds it (clocks of a unit of 128 keys x 256 rows, dh 128): 3350, of which the four products take
-// 2060 at their best and the exponentials 2050 (4 a clock and scheduler). In steps: 4450 with one thread
-// issuing in a diverged warp (170 clocks a product instead of 64); 3400 issued by a converged one; the same
-// with a cubic for 3 of 8 exponentials (its instructions cost what the unit saves) and with two threads a
-// row; 3350 with the scores ahead, now the products' own queue. A segment's end (O out, the next Q in)
-// costs 8000 clocks, 15000 before its rows were written side by side. 32 sequences, 9 blocks of 16 tokens
-// (30% there) behind 16384 shared and up to 2048 own keys: 402 us, 0.5 of the bf16 rate; 64 single
-// tokens behind 8192 and up to 500: 47 us for 103 MB.
+// What bounds it (clocks of 128 keys x 256 rows, dh 128): 3350, of which the four products take 2060 at their
+// best and the exponentials 1030 (8 a clock and scheduler), so it waits: in the serving batch below a CTA
+// takes 657 thousand clocks for 165 such units and its segments' ends; the products are 341 thousand of
+// them (tensor pipe 50% busy), their warp waits 42 for keys, 39 for scores to be read, 34 for P, 19 for
+// values, 12 for Q, and a softmax warp 320 for scores. In steps: 4450 with one thread issuing in a diverged
+// warp (170 clocks a product instead of 64); 3400 issued by a converged one; the same with a cubic for 3 of 8
+// exponentials and with two threads a row; 3350 with the scores ahead. A segment's end (O out, the
+// next Q in) costs 8000 clocks, 15000 before its rows were written side by side. 32 sequences, 9 blocks of
+// 16 tokens (30% there) behind 16384 shared and up to 2048 own keys: 403-426 us, 0.5 of the bf16 rate;
+// 64 single tokens behind 8192 and up to 500: 46 us for 103 MB. Head dim 64: 329 and 36 us.
 #include <cuda.h>
 #include <math.h>
 
@@ -311,6 +313,7 @@ static_assert(Shape<128>::kSmem <= 232448, "shared memory per CTA");
 static_assert(4 * (kMaxBatch + 1) * 4 <= kSlots * static_cast<int>(Shape<64>::kTileB), "offsets fit the ring");
 // TMEM columns: one buffer of scores, taken by the row tiles in turns (it is free as soon as the scores are in
 // registers, long before their P is made), P of tile 0 and 1 as bf16 pairs, O of tile 0 and 1
+// (P in the first half of its own S, with a buffer of scores for each row tile, would fill the 512 columns too: not tried)
 constexpr uint32_t TM_S = 0, TM_P = 128, TM_O = 256;
 
 __device__ __forceinline__ bool wait(Bars& bars, uint64_t* bar, uint32_t parity, WsHeader* hdr, int where) {
@@ -733,7 +736,10 @@ k_parts(const __grid_constant__ CUtensorMap map_ks, const __grid_constant__ CUte
 
 // ------------------------------------------------------------------ parts, fp32
 // The same runs and segments without tensor cores: 8 warps, four rows a warp at a time over tiles of 32
-// keys in shared memory. Bound by its fp32 products; fp32 inputs are for small models and tests.
+// keys in shared memory. Bound by shared memory: a product of the scores takes two words from there, each key
+// is read again for each of a warp's rows, and four barriers stand between 32 keys and the next (8 sequences of
+// 80 tokens, 32 heads, behind 4096 keys and up to 1500: 4340 us, 12 TFLOP/s). fp32 inputs are for small
+// models and tests.
 constexpr int kSimtThreads = 256;
 constexpr int kSimtRows = 4;               // of a warp
 constexpr int kSimtKeys = 32;

@@ -23,11 +23,13 @@
 //   3  the weight of what stays, where min-p or a draw needs it; the output rows; the token.
 // Lists too long to be sorted (thousands of equal values) go through `select`, nine bits of comp a level.
 //
-// What bounds it: not HBM. 81 rows of 128256 fp32 logits (nucleus) take 82 us, 1.0 TB/s of the 83 MB
+// What bounds it: not HBM. 81 rows of 128256 fp32 logits (nucleus) take 82-92 us, 0.9-1.0 TB/s of the 83 MB
 // that have to be moved (12 us): about 90 instructions a token (two evaluations of its weight of 25
 // each, the rest bins, tests and the output) and 2000 a warp for the fixed phases, barriers across a
 // cluster of six among them; issue slots are busy for half of the time with two CTAs an SM, which is
-// what registers (64 a thread) and shared memory allow. In steps (us, that case / 64 tokens of 151936
+// what registers (64 a thread) and shared memory allow. Clocks of a CTA's 88 thousand there: load 6, largest
+// value 5, weights and bins 20, their sums and bin 9, the bin's tokens brought together and sorted 30 (other
+// CTAs of the cluster waited for in that), cut 3, output 10. In steps (us, that case / 64 tokens of 151936
 // bf16 logits): every level of a radix search weighs every token 221 / 245; one fp64 division and
 // logarithm a thread taken out 219 / 163 (a single row 87 -> 17); bins of linear width 133 / 68; pairs
 // of fp32 in one instruction 93; the border's tokens sorted in registers and the row on six CTAs
@@ -59,7 +61,12 @@ constexpr int kIdxBits = 20;               // V <= 2^20: the weight sums then fi
 constexpr int kTab = 64;
 constexpr uint64_t kAll = ~0ull;
 constexpr int kTop = 4;                     // of each warp's lanes' largest, the ones that bound small top-k
-constexpr int kShortK = 1024;               // up to this the tokens above the bound are sorted, beyond they are binned
+// Up to kShortK the tokens above the bound are sorted, beyond they are binned. us by the list / by bins, top-k alone and with
+// top-p 0.95: 64 rows of 151936 bf16 logits k 50 22 / 29, 22 / 59; 400 33 / 34, 34 / 64; 1000 46 / 41, 46 / 71; 1300 54 / 44,
+// 84 / 73. 8 rows of 128256: 400 21 / 23, 22 / 39; 1000 26 / 24, 26 / 41. Where a CTA holds a whole row its list is too
+// short from about 500 on, and what was brought together is binned after all: 300 rows of 32000 400 37 / 41, 37 / 66; 1000 62 / 51,
+// 89 / 78.
+constexpr int kShortK = 1024;
 constexpr int kList = 1024;                // tokens near a border that one CTA may hold,
 constexpr int kFew = kThreads;             // tokens from which one is drawn by sorting them once more
 constexpr int kThreadTokens = 512;         // a thread's part of a row, at most
@@ -1280,7 +1287,10 @@ static int launch(const Params& in, int64_t rows, cudaStream_t s) {
   Params p = in;
   const int nvec = (p.V + 2 * VE - 2) / VE;                  // at most, whatever the row's first element's place
   // CTAs a row: the least of (waves of clusters) x (a fixed part, the cluster's barriers, and the CTA's
-  // share of the row), both in tokens: 512 threads pass over 12500 of them in the fixed part's time
+  // share of the row), both in tokens: 512 threads pass over 12500 of them in the fixed part's time.
+  // us with 1 .. 8 CTAs, top-p 0.95 (* the rule's): a row of 128256 fp32 logits 123 65 43 32 29 28 26 25*; 81 of them 132 137
+  // 95 102 93 82* 102 97; 64 rows of 151936 bf16 132 73 92 63* 90 86 86 84; 300 of them 283 283 317 252* 274 296 335 330; 648
+  // rows of 32000 113* 132 177 197 258 319 394 377; 40 of them 32 23 21 24 24 25* 40 39
   int C = 0;
   double least = 0.;
   for (int c = 1; c <= kMaxCluster; ++c) {
